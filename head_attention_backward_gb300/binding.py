@@ -9,6 +9,7 @@ not been built: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import dataclasses
 import math
 import os
 from typing import Optional
@@ -24,7 +25,8 @@ BIAS_NONE, BIAS_11SS, BIAS_1HSS, BIAS_BHSS, BIAS_B1SS = 0, 1, 2, 3, 4   # attn_b
 DET_ATOMIC, DET_ORDERED, DET_SPLIT = 0, 1, 2   # attn_det_t
 STATUS = {0: "ATTN_OK", -1: "ATTN_ERR_INVALID_ARG", -2: "ATTN_ERR_UNSUPPORTED_HEADDIM",
           -3: "ATTN_ERR_WORKSPACE_TOO_SMALL", -4: "ATTN_ERR_CUDA", -5: "ATTN_ERR_DEVICE_FLAG",
-          -6: "ATTN_ERR_TIMEOUT", -7: "ATTN_ERR_BAD_SEQLENS"}
+          -6: "ATTN_ERR_TIMEOUT", -7: "ATTN_ERR_BAD_SEQLENS", -8: "ATTN_ERR_BAD_PAGE",
+          -9: "ATTN_ERR_OUT_OF_PAGES"}
 # attn_status_t codes by name (ATTN_OK, ATTN_ERR_INVALID_ARG, ...)
 globals().update({name: code for code, name in STATUS.items()})
 
@@ -63,8 +65,45 @@ class AttnHostTensors(ctypes.Structure):
                 ("dq", _vp), ("dk", _vp), ("dv", _vp)]
 
 
+class AttnRopeParams(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("batch", _i32), ("seqlen", _i32), ("nhead_q", _i32), ("nhead_kv", _i32),
+                ("head_dim", _i32), ("rot_dim", _i32), ("n_axes", _i32), ("interleaved", _i32), ("inverse", _i32),
+                ("positions", _vp), ("stride_pos", _i64x3), ("inv_freq", _vp), ("pair_axis", _vp),
+                ("q", _vp), ("k", _vp), ("q_out", _vp), ("k_out", _vp),
+                ("stride_q", _i64x3), ("stride_k", _i64x3), ("stride_q_out", _i64x3), ("stride_k_out", _i64x3)]
+
+
+class AttnKvCache(ctypes.Structure):
+    _fields_ = [("num_pages", _i32), ("page_size", _i32), ("nhead_kv", _i32), ("d_qk", _i32), ("d_v", _i32),
+                ("reserved", _i32), ("k", _vp), ("v", _vp), ("k_exp", _vp), ("v_exp", _vp),
+                ("stride_k", _i64x3), ("stride_v", _i64x3)]
+
+
+class AttnKvPlanParams(ctypes.Structure):
+    _fields_ = [("batch", _i32), ("page_size", _i32), ("num_pages", _i32), ("max_blocks", _i32),
+                ("max_tokens", _i32), ("reserved", _i32), ("new_lens", _vp), ("seqlens", _vp), ("seqlens_out", _vp),
+                ("block_table", _vp), ("table_stride", ctypes.c_int64), ("free_pages", _vp), ("free_count", _vp),
+                ("free_count_out", _vp), ("cu_seqlens", _vp), ("positions", _vp), ("slots", _vp), ("status", _vp)]
+
+
+class AttnKvAppendParams(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("tokens", _i32), ("k", _vp), ("v", _vp), ("stride_k", _i64x3),
+                ("stride_v", _i64x3), ("slots", _vp), ("cache", AttnKvCache)]
+
+
+class AttnKvFwdParams(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("batch", _i32), ("nhead_q", _i32), ("total_q", _i32), ("max_seqlen_q", _i32),
+                ("max_seqlen_k", _i32), ("max_blocks", _i32), ("mask", _i32), ("window_left", _i32),
+                ("window_right", _i32), ("softmax_scale", _f32), ("reserved", _i32), ("cu_seqlens_q", _vp),
+                ("cu_seqlens_q_padded", _vp), ("seqlens_k", _vp), ("block_table", _vp),
+                ("table_stride", ctypes.c_int64), ("q", _vp), ("o", _vp), ("lse", _vp), ("stride_q", _i64x3),
+                ("stride_o", _i64x3), ("cache", AttnKvCache)]
+
+
 EXPORTS = ["attn_bwd_workspace_size", "attn_bwd", "attn_bwd_timed", "attn_bwd_read_status",
-           "attn_fwd", "attn_status_string", "attn_bwd_static_ws", "attn_selftest_waits", "attn_bwd_host"]
+           "attn_fwd", "attn_status_string", "attn_bwd_static_ws", "attn_selftest_waits", "attn_bwd_host",
+           "attn_rope", "attn_kv_plan", "attn_kv_append", "attn_kv_fwd_workspace_size", "attn_kv_fwd",
+           "attn_kv_fwd_read_status"]
 
 _lib = None
 
@@ -88,6 +127,18 @@ def load(path: str = LIB_PATH):
     lib.attn_bwd_read_status.restype = ctypes.c_int
     lib.attn_fwd.argtypes = [P(AttnFwdParams), _vp]
     lib.attn_fwd.restype = ctypes.c_int
+    lib.attn_rope.argtypes = [P(AttnRopeParams), _vp]
+    lib.attn_rope.restype = ctypes.c_int
+    lib.attn_kv_plan.argtypes = [P(AttnKvPlanParams), _vp]
+    lib.attn_kv_plan.restype = ctypes.c_int
+    lib.attn_kv_append.argtypes = [P(AttnKvAppendParams), _vp]
+    lib.attn_kv_append.restype = ctypes.c_int
+    lib.attn_kv_fwd_workspace_size.argtypes = [P(AttnKvFwdParams), P(ctypes.c_size_t)]
+    lib.attn_kv_fwd_workspace_size.restype = ctypes.c_int
+    lib.attn_kv_fwd.argtypes = [P(AttnKvFwdParams), _vp, ctypes.c_size_t, _vp]
+    lib.attn_kv_fwd.restype = ctypes.c_int
+    lib.attn_kv_fwd_read_status.argtypes = [P(AttnKvFwdParams), _vp, ctypes.c_size_t, _vp, P(ctypes.c_int)]
+    lib.attn_kv_fwd_read_status.restype = ctypes.c_int
     lib.attn_status_string.argtypes = [ctypes.c_int]
     lib.attn_status_string.restype = ctypes.c_char_p
     lib.attn_bwd_host.argtypes = [P(AttnBwdParams), P(AttnHostTensors), _vp, ctypes.c_size_t, _vp, _vp, _vp,
@@ -129,6 +180,34 @@ def attn_bwd_read_status(workspace: int, stream: int = 0):
 
 def attn_fwd(p: AttnFwdParams, stream: int = 0) -> int:
     return load().attn_fwd(ctypes.byref(p), stream)
+
+
+def attn_rope(p: AttnRopeParams, stream: int = 0) -> int:
+    return load().attn_rope(ctypes.byref(p), stream)
+
+
+def attn_kv_plan(p: AttnKvPlanParams, stream: int = 0) -> int:
+    return load().attn_kv_plan(ctypes.byref(p), stream)
+
+
+def attn_kv_append(p: AttnKvAppendParams, stream: int = 0) -> int:
+    return load().attn_kv_append(ctypes.byref(p), stream)
+
+
+def attn_kv_fwd_workspace_size(p: AttnKvFwdParams):
+    n = ctypes.c_size_t(0)
+    st = load().attn_kv_fwd_workspace_size(ctypes.byref(p), ctypes.byref(n))
+    return st, n.value
+
+
+def attn_kv_fwd(p: AttnKvFwdParams, workspace: int, workspace_bytes: int, stream: int = 0) -> int:
+    return load().attn_kv_fwd(ctypes.byref(p), workspace, workspace_bytes, stream)
+
+
+def attn_kv_fwd_read_status(p: AttnKvFwdParams, workspace: int, workspace_bytes: int, stream: int = 0):
+    s = ctypes.c_int(0)
+    st = load().attn_kv_fwd_read_status(ctypes.byref(p), workspace, workspace_bytes, stream, ctypes.byref(s))
+    return st, s.value
 
 
 def attn_bwd_host(p: AttnBwdParams, host: AttnHostTensors, workspace: int, workspace_bytes: int, stream: int,
@@ -367,3 +446,278 @@ def attn_backward(q, k, v, o, do, lse, *, scale, mask=MASK_NONE, left=-1, right=
     if return_dbias:
         return dq, dk, dv, dbias
     return dq, dk, dv
+
+
+# ------------------------------------------- rotary positions and the cache
+#
+# These run once per layer or step of a serving loop, so they check shapes,
+# types and devices (an AttnError or ValueError before any launch) and fill
+# their struct in one go; nothing synchronises unless asked to.
+
+def _need(t: torch.Tensor, what: str, dtypes, shape=None, device=None):
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what}: dtype {t.dtype} is not one of {tuple(dtypes)}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{what} must be on {device or 'a CUDA device'}, not on {t.device}")
+
+
+def _ints(t: torch.Tensor, what: str, n: int, device, dtype=torch.int32) -> int:
+    """Address of a contiguous vector of n whole numbers on `device`."""
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1) or t.device != device:
+        raise ValueError(f"{what} must be a contiguous {dtype} vector of {n} on {device}")
+    return t.data_ptr()
+
+
+_F16 = (torch.bfloat16, torch.float16)
+_FLOATS = tuple(_DTYPES)
+
+
+class _Launch:
+    """The stream of a call and its outputs: with an explicit stream the
+    outputs are allocated on it, so the allocator does not hand their memory to
+    other work while the kernels may still write it."""
+
+    __slots__ = ("device", "stream", "guard")
+
+    def __init__(self, device: torch.device, stream):
+        if device.index != torch.cuda.current_device():
+            raise ValueError(f"tensors on {device}, but the current device is {torch.cuda.current_device()}")
+        self.device, self.guard = device, None
+        if stream is None:
+            self.stream = torch.cuda.current_stream().cuda_stream
+        else:
+            self.stream = _stream(stream)
+            if self.stream != torch.cuda.current_stream().cuda_stream:
+                self.guard = torch.cuda.stream(torch.cuda.ExternalStream(self.stream, device=device)
+                                               if not hasattr(stream, "cuda_stream") else stream)
+
+    def empty(self, shape, dtype):
+        if self.guard is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with self.guard:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0) -> torch.Tensor:
+    """The usual ladder base^(-2 i / rot_dim), i < rot_dim / 2, in 64 bits on
+    the host: the inv_freq of rope()."""
+    return base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)
+
+
+def rope(q, k, positions, inv_freq, *, pair_axis=None, interleaved=False, inverse=False, out=None, stream=None):
+    """q and k (or None) with their rotary positions applied (attn_rope), as
+    new tensors or into `out` = (q_out, k_out), which may be (q, k).
+
+    q [T, H, D] or [B, S, H, D], k likewise with its own heads; positions int32
+    [T] / [B, S], or with a leading axis dimension [n_axes, ...] for several
+    axes; inv_freq and pair_axis are host tensors (float64 and uint8,
+    rot_dim / 2 entries).  inverse=True is the gradient: rope(dq, dk, ...,
+    inverse=True) after attn_backward."""
+    _need(q, "q", _FLOATS)
+    dev = q.device
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [T, H, D] or [B, S, H, D]")
+    rows = q.shape[:-2]
+    if k is not None:
+        _need(k, "k", (q.dtype,), (*rows, k.shape[-2], q.shape[-1]), dev)
+    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 vector on the host")
+    half = inv_freq.shape[0]
+    if pair_axis is not None and (pair_axis.dtype != torch.uint8 or pair_axis.is_cuda or pair_axis.shape != (half,)
+                                  or not pair_axis.is_contiguous()):
+        raise ValueError("pair_axis must be a contiguous uint8 vector on the host, as long as inv_freq")
+    if positions.shape == rows:
+        n_axes, sp = 1, (0, *positions.stride())
+    elif positions.shape[1:] == rows:
+        n_axes, sp = positions.shape[0], positions.stride()
+    else:
+        raise ValueError(f"positions {tuple(positions.shape)} do not fit rows {tuple(rows)}")
+    _need(positions, "positions", (torch.int32,), None, dev)
+    L = _Launch(dev, stream)
+    if out is None:
+        qo = L.empty(q.shape, q.dtype)
+        ko = None if k is None else L.empty(k.shape, k.dtype)
+    else:
+        qo, ko = out
+        _need(qo, "out[0]", (q.dtype,), q.shape, dev)
+        if k is not None:
+            _need(ko, "out[1]", (q.dtype,), k.shape, dev)
+    group = len(rows) == 1
+    if group:
+        sp = (sp[0], 0, sp[1])
+    zero = (0, 0, 0)
+    p = AttnRopeParams(
+        _DTYPES[q.dtype], 1 if group else rows[0], rows[-1], q.shape[-2], 0 if k is None else k.shape[-2],
+        q.shape[-1], 2 * half, n_axes, 1 if interleaved else 0, 1 if inverse else 0, positions.data_ptr(),
+        _i64x3(*sp), inv_freq.data_ptr(), None if pair_axis is None else pair_axis.data_ptr(),
+        q.data_ptr(), None if k is None else k.data_ptr(), qo.data_ptr(), None if k is None else ko.data_ptr(),
+        _i64x3(*_strides(q, group)), _i64x3(*(zero if k is None else _strides(k, group))),
+        _i64x3(*_strides(qo, group)), _i64x3(*(zero if k is None else _strides(ko, group))))
+    st = attn_rope(p, L.stream)
+    if st != 0:
+        raise AttnError(st, "attn_rope")
+    return qo, (None if k is None else ko)
+
+
+class KvCache:
+    """Handle of a paged 8-bit cache (attn_kv_cache): k [pages, page_size,
+    kv heads, d_qk] and v [..., d_v] as torch.float8_e4m3fn (or uint8), any
+    strides with a contiguous head dimension, and the scale exponents k_exp,
+    v_exp uint8 [pages, kv heads].  Keep it next to the tensors it holds."""
+
+    def __init__(self, k, v, k_exp, v_exp):
+        pages, size, heads, dqk = k.shape
+        _need(k, "k", (torch.float8_e4m3fn, torch.uint8))
+        _need(v, "v", (k.dtype,), (pages, size, heads, v.shape[-1]), k.device)
+        for name, e in (("k_exp", k_exp), ("v_exp", v_exp)):
+            _need(e, name, (torch.uint8,), (pages, heads), k.device)
+            if not e.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        if k.stride(3) != 1 or v.stride(3) != 1:
+            raise ValueError("the head dimension must be contiguous (stride 1)")
+        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        self.num_pages, self.page_size, self.nhead_kv, self.d_qk, self.d_v = pages, size, heads, dqk, v.shape[-1]
+        self.device = k.device
+        self.params = AttnKvCache(pages, size, heads, dqk, self.d_v, 0, k.data_ptr(), v.data_ptr(), k_exp.data_ptr(),
+                                  v_exp.data_ptr(), _i64x3(*k.stride()[:3]), _i64x3(*v.stride()[:3]))
+
+    @classmethod
+    def empty(cls, num_pages, page_size, nhead_kv, d_qk, d_v, device="cuda"):
+        """A new cache, zero everywhere."""
+        k, v = (torch.zeros((num_pages, page_size, nhead_kv, d), dtype=torch.uint8, device=device)
+                .view(torch.float8_e4m3fn) for d in (d_qk, d_v))
+        e = [torch.full((num_pages, nhead_kv), 127, dtype=torch.uint8, device=device) for _ in range(2)]
+        return cls(k, v, *e)
+
+
+@dataclasses.dataclass
+class KvPlan:
+    """What attn_kv_plan computes: packed segment offsets, the requests' new
+    lengths, one position and slot per token, the free pages left, the status
+    word (0 = ATTN_OK), all on the device."""
+    cu_seqlens: torch.Tensor
+    seqlens: torch.Tensor
+    positions: torch.Tensor
+    slots: torch.Tensor
+    free_count: torch.Tensor
+    status: torch.Tensor
+
+    def check(self):
+        """Synchronises; raises AttnError if the step was refused."""
+        s = int(self.status)
+        if s != 0:
+            raise AttnError(s, "attn_kv_plan (device status)")
+
+
+def kv_plan(new_lens, seqlens, block_table, free_pages, free_count, *, page_size, max_tokens, out=None, stream=None):
+    """Pages, positions and slots for one step (attn_kv_plan).  new_lens and
+    seqlens int32 [B] (KV_RELEASE ends a request), block_table int32
+    [B, max_blocks] and free_pages int32 [num_pages] are updated in place,
+    free_count int32 [1].  Returns a KvPlan, `out` itself when given: its
+    seqlens and free_count may be the inputs', so that a captured call
+    advances its state at every replay."""
+    dev, n = new_lens.device, new_lens.shape[0]
+    _need(block_table, "block_table", (torch.int32,), (n, block_table.shape[-1]), dev)
+    if block_table.stride(1) != 1:
+        raise ValueError("block_table rows must be contiguous")
+    L = _Launch(dev, stream)
+    if out is None:
+        # two blocks for six vectors: the positions and other words, the slots
+        ints = L.empty((2 * n + 3 + max_tokens,), torch.int32)
+        a, b, c, d, e = ints.split((n + 1, n, 1, 1, max_tokens))
+        out = KvPlan(a, b, e, L.empty((max_tokens,), torch.int64), c, d)
+    p = AttnKvPlanParams(
+        n, page_size, free_pages.shape[0], block_table.shape[1], max_tokens, 0,
+        _ints(new_lens, "new_lens", n, dev), _ints(seqlens, "seqlens", n, dev),
+        _ints(out.seqlens, "out.seqlens", n, dev), block_table.data_ptr(),
+        block_table.stride(0) if n > 1 else block_table.shape[1],
+        _ints(free_pages, "free_pages", free_pages.shape[0], dev), _ints(free_count, "free_count", 1, dev),
+        _ints(out.free_count, "out.free_count", 1, dev), _ints(out.cu_seqlens, "out.cu_seqlens", n + 1, dev),
+        _ints(out.positions, "out.positions", max_tokens, dev),
+        _ints(out.slots, "out.slots", max_tokens, dev, torch.int64), _ints(out.status, "out.status", 1, dev))
+    st = attn_kv_plan(p, L.stream)
+    if st != 0:
+        raise AttnError(st, "attn_kv_plan")
+    return out
+
+
+def kv_append(k, v, slots, cache: KvCache, *, stream=None):
+    """New keys and values into the cache (attn_kv_append): k [T, kv heads,
+    d_qk] and v [T, kv heads, d_v] in bf16 or fp16, slots int64 [T] as from
+    kv_plan (-1: skipped)."""
+    n = k.shape[0]
+    _need(k, "k", _F16, (n, cache.nhead_kv, cache.d_qk), cache.device)
+    _need(v, "v", (k.dtype,), (n, cache.nhead_kv, cache.d_v), cache.device)
+    L = _Launch(cache.device, stream)
+    p = AttnKvAppendParams(_DTYPES[k.dtype], n, k.data_ptr(), v.data_ptr(), _i64x3(*_packed(k)), _i64x3(*_packed(v)),
+                           _ints(slots, "slots", n, cache.device, torch.int64), cache.params)
+    st = attn_kv_append(p, L.stream)
+    if st != 0:
+        raise AttnError(st, "attn_kv_append")
+
+
+def _packed(t):
+    """{0, row, head} strides of a [T, H, D] tensor; a dimension of one entry
+    may carry any stride, so it is given the contiguous one."""
+    s = t.stride()
+    if s[2] != 1:
+        raise ValueError("the head dimension must be contiguous (stride 1)")
+    n, h, d = t.shape
+    head = s[1] if h > 1 else d
+    return 0, (s[0] if n > 1 else h * head), head
+
+
+def attn_kv_forward(q, cache: KvCache, block_table, seqlens_k, cu_seqlens_q, *, scale, mask=MASK_CAUSAL_BOTTOM_RIGHT,
+                    left=-1, right=-1, max_seqlen_q, max_seqlen_k, cu_seqlens_q_padded=None, out=None, workspace=None,
+                    stream=None, check_status=False):
+    """O [T, Hq, d_v] and LSE [Hq, T] of packed queries q [T, Hq, d_qk] over the
+    cache (attn_kv_fwd).  block_table int32 [B, max_blocks], seqlens_k int32
+    [B], cu_seqlens_q int32 [B + 1] as from kv_plan.  Rows of no segment are
+    not written: pass `out` = (o, lse) to choose what they hold, in outputs
+    allocated here they are undefined.  check_status=True synchronises and
+    raises what the kernels found (lengths beyond their bounds, pages outside
+    the cache)."""
+    dev, n = cache.device, seqlens_k.shape[0]
+    t, hq = q.shape[0], q.shape[1]
+    _need(q, "q", _F16, (t, hq, cache.d_qk), dev)
+    _need(block_table, "block_table", (torch.int32,), (n, block_table.shape[-1]), dev)
+    if block_table.stride(1) != 1:
+        raise ValueError("block_table rows must be contiguous")
+    L = _Launch(dev, stream)
+    if out is None:
+        o, lse = L.empty((t, hq, cache.d_v), q.dtype), L.empty((hq, t), torch.float32)
+    else:
+        o, lse = out
+        _need(o, "out[0]", (q.dtype,), (t, hq, cache.d_v), dev)
+        _need(lse, "out[1]", (torch.float32,), (hq, t), dev)
+        if not lse.is_contiguous():
+            raise ValueError("out[1] must be contiguous")
+    p = AttnKvFwdParams(
+        _DTYPES[q.dtype], n, hq, t, max_seqlen_q, max_seqlen_k, block_table.shape[1], mask, left, right, scale, 0,
+        _ints(cu_seqlens_q, "cu_seqlens_q", n + 1, dev),
+        None if cu_seqlens_q_padded is None else _ints(cu_seqlens_q_padded, "cu_seqlens_q_padded", n + 1, dev),
+        _ints(seqlens_k, "seqlens_k", n, dev), block_table.data_ptr(),
+        block_table.stride(0) if n > 1 else block_table.shape[1], q.data_ptr(), o.data_ptr(), lse.data_ptr(),
+        _i64x3(*_packed(q)), _i64x3(*_packed(o)), cache.params)
+    st, need = attn_kv_fwd_workspace_size(p)
+    if st != 0:
+        raise AttnError(st, "attn_kv_fwd_workspace_size")
+    if workspace is None:
+        workspace = L.empty((need,), torch.uint8)
+    elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    st = attn_kv_fwd(p, workspace.data_ptr(), workspace.numel(), L.stream)
+    if st != 0:
+        raise AttnError(st, "attn_kv_fwd")
+    if check_status:
+        st, found = attn_kv_fwd_read_status(p, workspace.data_ptr(), workspace.numel(), L.stream)
+        if st != 0:
+            raise AttnError(st, "attn_kv_fwd_read_status")
+        if found != 0:
+            raise AttnError(found, "attn_kv_fwd (device status)")
+    return o, lse
+
+
+KV_RELEASE = -1   # ATTN_KV_RELEASE

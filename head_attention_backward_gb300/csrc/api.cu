@@ -632,6 +632,8 @@ extern "C" const char* attn_status_string(int status) {
     case ATTN_ERR_DEVICE_FLAG: return "device reported an error";
     case ATTN_ERR_TIMEOUT: return "bounded device wait expired";
     case ATTN_ERR_BAD_SEQLENS: return "cu_seqlens inconsistent with declared bounds";
+    case ATTN_ERR_BAD_PAGE: return "page number outside the cache";
+    case ATTN_ERR_OUT_OF_PAGES: return "not enough free pages";
     default: return "unknown status";
   }
 }

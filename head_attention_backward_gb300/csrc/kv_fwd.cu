@@ -1,0 +1,715 @@
+// Attention of packed query segments over the paged 8-bit cache (attn_kv_fwd).
+//
+//   O = softmax(s Q K^T) V,  K = 2^ek Kq, V = 2^ev Vq per page and kv head.
+//
+// Decoding reads every visible cache byte once and does 4 Hq / Hkv flops per
+// byte: bound by memory, far from the tensor cores' rate.  So the query rows
+// that share a kv head (tokens x Hq / Hkv, in tiles of 16) meet the cache in
+// warp-level m16n8k16 products, and the work is laid out for the loads:
+//
+// * A CTA owns one tile of 16 rows, one kv head and one split of the keys; its
+//   four warps take 16-key tiles in turn, each with a ring of its own that
+//   16-byte asynchronous copies keep full.  No barrier joins the warps until
+//   the end.  A tile lies in one page, so its scales are uniform.
+// * e4m3 is exact in fp16.  The contraction's order is free, so a lane takes
+//   16 consecutive bytes of a K row as its share of four k-steps and 16
+//   consecutive bytes of four V rows as its share of 16 column tiles: wide
+//   conflict-free shared loads, no transposition, one conversion per two
+//   values.
+// * q goes to fp16 under a power-of-two scale per row (largest magnitude in
+//   [2^14, 2^15)), which is exact for bf16 too unless an element is 2^-28 of
+//   its row's largest.  P is fp16 with its running maximum at 2^8: 11 bits down
+//   to 2^-22 of the row's maximum, 2^-32 reached.  Scores, maxima, sums and O
+//   are fp32.
+// * The accumulator is held in units of the current page's V scale and
+//   multiplied by the exact ratio where the scale changes.
+//
+// Splits leave (O, max, sum) in the workspace; a second small kernel joins
+// them in a fixed order.
+#include <cmath>
+
+#include "common.cuh"
+#include "kv_common.cuh"
+#include "sm100_ptx.cuh"
+
+namespace attn {
+namespace kvfwd {
+
+constexpr int NWARPS = 4;
+constexpr int NTHREADS = 32 * NWARPS;
+constexpr int ROWS = 16;            // query rows of a CTA
+constexpr int TILE = 16;            // keys of a warp's step
+constexpr int MAX_TILES = 256;      // tiles of a split: its page table fits shared memory
+constexpr int MIN_TILES = 16;       // a split is worth at least this many
+constexpr int SMS = 152;
+constexpr float P_LOG2 = 8.f;       // P = 2^8 at the running maximum
+constexpr float SLACK_LOG2 = 7.f;   // growth of the maximum that is let pass: P <= 2^15
+
+template <int DQK, int DV>
+struct Cfg {
+  static constexpr int KB = TILE * DQK, VB = TILE * DV;
+  static constexpr int STAGE = KB + VB;
+  static constexpr int NST = STAGE <= 2048 ? 6 : STAGE <= 5120 ? 4 : 3;
+  static constexpr int RING = NST * STAGE;
+  static constexpr int OFF_META = NWARPS * RING;                       // int2[MAX_TILES + 1]: page, exponents
+  static constexpr int OFF_ML = OFF_META + (MAX_TILES + 1) * 8;        // float[2][NWARPS][ROWS]
+  static constexpr int SMEM = OFF_ML + 2 * NWARPS * ROWS * 4 + 8;
+  static_assert(NWARPS * ROWS * DV * 4 <= NWARPS * RING, "the join of the warps reuses the rings");
+};
+
+struct Args {
+  const void* q;
+  void* o;
+  float* lse;
+  Strides sq, so;
+  const int* cu_q;
+  const int* st_q;
+  const int* len_k;
+  const int* table;
+  long long table_stride;
+  int max_k;             // min(max_seqlen_k, max_blocks pages)
+  int total_q, max_q;
+  int hq, g;             // query heads, per kv head
+  int mask, left, right;
+  float scale_log2;
+  int nsplit, split_tiles, mtiles;
+  float* part_o;         // [job][nsplit][ROWS][DV]
+  float2* part_ml;       // [job][nsplit][ROWS]
+  int* status;           // [batch][nsplit]
+  KvCacheView c;
+};
+
+// What a request's row tile and the keys it sees come to.
+struct Job {
+  int lq, lk, q0;        // segment
+  int row0, nrow;        // rows of the tile (row = token * g + head of the group)
+  int klo, khi;          // keys that any of its rows sees, khi < klo: none
+  int kbeg;              // klo rounded down to a tile
+  int ntile;
+  bool bad;              // lengths outside the declared bounds
+};
+
+__device__ __forceinline__ Job make_job(const Args& A, int b, int m, MaskArgs& mk) {
+  Job j;
+  const int a = __ldg(A.cu_q + b);
+  j.lq = __ldg(A.cu_q + b + 1) - a;
+  j.q0 = __ldg(A.st_q + b);
+  j.lk = __ldg(A.len_k + b);
+  j.bad = j.lq < 0 || j.lq > A.max_q || j.q0 < 0 || (long long)j.q0 + j.lq > A.total_q;
+  if (j.bad) j.lq = 0;
+  if (j.lk < 0 || j.lk > A.max_k) {
+    j.bad = true;
+    j.lk = j.lk < 0 ? 0 : A.max_k;
+  }
+  mk = mask_args(A.mask, A.left, A.right, j.lq, j.lk);
+  j.row0 = m * ROWS;
+  j.nrow = min(ROWS, j.lq * A.g - j.row0);
+  j.klo = 0;
+  j.khi = j.lk - 1;
+  if (j.nrow > 0) {
+    const int i0 = j.row0 / A.g, i1 = (j.row0 + j.nrow - 1) / A.g;
+    if (mk.left >= 0) j.klo = (int)max(0ll, (long long)i0 + mk.off - mk.left);
+    if (mk.right >= 0) j.khi = (int)min((long long)j.khi, (long long)i1 + mk.off + mk.right);
+  }
+  j.kbeg = j.klo & ~(TILE - 1);
+  j.ntile = j.khi >= j.klo ? (j.khi - j.kbeg) / TILE + 1 : 0;
+  return j;
+}
+
+__device__ __forceinline__ bool sees(const MaskArgs& m, int i, int j) {
+  const long long c = (long long)i + m.off;
+  return (m.left < 0 || j >= c - m.left) && (m.right < 0 || j <= c + m.right);
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 16-byte asynchronous copy past L1; bytes = 0 writes zeros.
+__device__ __forceinline__ void cp_async16(uint32_t sdst, const void* gsrc, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sdst), "l"(gsrc), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// Byte offset of 16-byte piece c of row r in a warp's K or V tile.  The lanes
+// of one shared load phase read, of K, rows 2p and 2p + 1 at pieces t (mod 4)
+// and, of V, rows 2t at pieces 2p and 2p + 1 (t = 0..3): the piece is moved
+// within its 128-byte line so that the eight fall on different banks.
+template <int D>
+__device__ __forceinline__ int k_off(int r, int c) {
+  return r * D + ((D % 128 == 0 ? c ^ ((r & 1) << 2) : c) << 4);
+}
+template <int D>
+__device__ __forceinline__ int v_off(int r, int c) {
+  const int x = ((r >> 1) & 3) << 1;
+  if (D == 64) return (r >> 1) * 128 + ((((r & 1) << 2 | c) ^ x) << 4);
+  return r * D + ((c ^ x) << 4);
+}
+
+template <typename T> __device__ __forceinline__ float2 up2(uint32_t x);
+template <> __device__ __forceinline__ float2 up2<__nv_bfloat16>(uint32_t x) {
+  return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&x));
+}
+template <> __device__ __forceinline__ float2 up2<__half>(uint32_t x) {
+  return __half22float2(*reinterpret_cast<__half2*>(&x));
+}
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T> __device__ __forceinline__ uint32_t pack_t2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack_t2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack_t2<__half>(float a, float b) { return pack_h2(a, b); }
+
+template <int DQK, int DV, typename T>
+__global__ void __launch_bounds__(NTHREADS) kv_fwd_kernel(const Args A) {
+  using C = Cfg<DQK, DV>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  int2* meta = reinterpret_cast<int2*>(smem + C::OFF_META);
+  float* s_m = reinterpret_cast<float*>(smem + C::OFF_ML);
+  float* s_l = s_m + NWARPS * ROWS;
+  int* s_bad = reinterpret_cast<int*>(s_l + NWARPS * ROWS);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+
+  // block -> (request, kv head, split, row tile), row tiles next to each other
+  int x = blockIdx.x;
+  const int m = x % A.mtiles;
+  x /= A.mtiles;
+  const int split = x % A.nsplit;
+  x /= A.nsplit;
+  const int hk = x % A.c.hkv, b = x / A.c.hkv;
+  MaskArgs mk;
+  const Job J = make_job(A, b, m, mk);
+  const bool reports = hk == 0 && m == 0;   // one CTA per (request, split) says what it found
+  if (tid == 0) *s_bad = 0;
+  const int tile0 = split * A.split_tiles;
+  if (J.nrow <= 0 || (split > 0 && tile0 >= J.ntile)) {
+    if (reports && tid == 0) A.status[b * A.nsplit + split] = J.bad ? ATTN_ERR_BAD_SEQLENS : ATTN_OK;
+    return;
+  }
+  const int ntile = min(A.split_tiles, J.ntile - tile0);      // may be <= 0 for split 0
+  const int key0 = J.kbeg + tile0 * TILE;
+  const int page0 = key0 >> A.c.page_shift;
+  __syncthreads();
+
+  // pages and scales of this split
+  if (ntile > 0) {
+    const int npage = ((key0 + ntile * TILE - 1) >> A.c.page_shift) - page0 + 1;
+    for (int i = tid; i < npage; i += NTHREADS) {
+      const int page = __ldg(A.table + b * A.table_stride + page0 + i);
+      int e = 0;
+      if (page >= 0 && page < A.c.num_pages) {
+        const long long at = (long long)page * A.c.hkv + hk;
+        e = (kv_exp_of(__ldg(A.c.k_exp + at)) & 0xffff) | (kv_exp_of(__ldg(A.c.v_exp + at)) << 16);
+        meta[i] = make_int2(page, e);
+      } else {
+        *s_bad = 1;
+        meta[i] = make_int2(-1, 0);
+      }
+    }
+  }
+
+  // this lane's rows g and g + 8 of q, as fp16 under a power of two per row
+  uint32_t qa[DQK / 16][4];
+  float rs[2];
+  int tok[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int row = min(J.row0 + g + 8 * r, J.row0 + J.nrow - 1);   // rows past the end repeat the last
+    tok[r] = row / A.g;
+    const T* qp = static_cast<const T*>(A.q) + elem_off(A.sq, (long long)J.q0 + tok[r], hk * A.g + row - tok[r] * A.g);
+    uint4 raw[DQK / 32];
+    float mx = 0.f;
+#pragma unroll
+    for (int c = 0; c < DQK / 64; ++c) {
+      const uint4* p = reinterpret_cast<const uint4*>(qp + (t + 4 * c) * 16);
+      raw[2 * c] = __ldg(p);
+      raw[2 * c + 1] = __ldg(p + 1);
+    }
+#pragma unroll
+    for (int i = 0; i < DQK / 32; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = up2<T>(w[k]);
+        mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+      }
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    int e = (int)(__float_as_uint(mx) >> 23) - 127;
+    e = e == 128 ? 14 : max(e, -100);      // infinities stay what they are
+    const float up = exp2_int(14 - e);
+    rs[r] = A.scale_log2 * exp2_int(e - 14);
+#pragma unroll
+    for (int i = 0; i < DQK / 32; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {        // 16 elements of two pieces: k-step 4 (i / 2) + 2 (i & 1) + k / 2
+        const float2 f = up2<T>(w[k]);
+        qa[(i >> 1) * 4 + (i & 1) * 2 + (k >> 1)][(k & 1) * 2 + r] = pack_h2(f.x * up, f.y * up);
+      }
+    }
+  }
+  __syncthreads();
+
+  const uint32_t ring = ptx::smem_u32(smem) + warp * C::RING;
+  const int shift = A.c.page_shift, in_page = (1 << shift) - 1;
+  auto fetch = [&](int i) {   // tile i of the split into its stage; always one group
+    if (i < ntile) {
+      const int key = key0 + i * TILE;
+      const int page = meta[(key >> shift) - page0].x;
+      if (page >= 0) {
+        const uint32_t st = ring + ((i / NWARPS) % C::NST) * C::STAGE;
+        const uint8_t* ks = A.c.k + page * A.c.sk.p + hk * A.c.sk.h + (key & in_page) * A.c.sk.r;
+        const uint8_t* vs = A.c.v + page * A.c.sv.p + hk * A.c.sv.h + (key & in_page) * A.c.sv.r;
+#pragma unroll
+        for (int k = 0; k < DQK / 32; ++k) {
+          const int n = lane + 32 * k, r = n / (DQK / 16), c = n % (DQK / 16);
+          const bool in = key + r >= J.klo && key + r <= J.khi;   // the rest reads as zero
+          cp_async16(st + k_off<DQK>(r, c), in ? ks + r * A.c.sk.r + c * 16 : ks, in ? 16 : 0);
+        }
+#pragma unroll
+        for (int k = 0; k < DV / 32; ++k) {
+          const int n = lane + 32 * k, r = n / (DV / 16), c = n % (DV / 16);
+          const bool in = key + r >= J.klo && key + r <= J.khi;
+          cp_async16(st + C::KB + v_off<DV>(r, c), in ? vs + r * A.c.sv.r + c * 16 : vs, in ? 16 : 0);
+        }
+      }
+    }
+    cp_commit();
+  };
+
+  float o[DV / 8][4];
+#pragma unroll
+  for (int j = 0; j < DV / 8; ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
+  float mrow[2] = {-INFINITY, -INFINITY}, lrow[2] = {0.f, 0.f};
+  int ev = 0;
+  const int itok0 = J.row0 / A.g, itok1 = (J.row0 + J.nrow - 1) / A.g;
+
+#pragma unroll
+  for (int s = 0; s < C::NST - 1; ++s) fetch(warp + s * NWARPS);
+  for (int i = warp; i < ntile; i += NWARPS) {
+    fetch(i + (C::NST - 1) * NWARPS);
+    cp_wait<C::NST - 1>();
+    __syncwarp();
+    const int key = key0 + i * TILE;
+    const int2 mt = meta[(key >> shift) - page0];
+    if (mt.x >= 0) {
+      const uint32_t st = ring + ((i / NWARPS) % C::NST) * C::STAGE;
+      // S = Q K^T: column n of tile j is key 8 j + n
+      float s[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[j][k] = 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < DQK / 64; ++c) {
+        const uint4 w0 = lds128(st + k_off<DQK>(g, t + 4 * c)), w1 = lds128(st + k_off<DQK>(8 + g, t + 4 * c));
+        const uint32_t a0[4] = {w0.x, w0.y, w0.z, w0.w}, a1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          mma16816(s[0], qa[4 * c + k], e4m3x2_to_h2((uint16_t)a0[k]), e4m3x2_to_h2((uint16_t)(a0[k] >> 16)));
+          mma16816(s[1], qa[4 * c + k], e4m3x2_to_h2((uint16_t)a1[k]), e4m3x2_to_h2((uint16_t)(a1[k] >> 16)));
+        }
+      }
+      // scores in log2 units, masked ones -inf
+      const float ks = exp2_int((int)(short)(mt.y & 0xffff));
+      const float f[2] = {rs[0] * ks, rs[1] * ks};
+      const bool full = key >= J.klo && key + TILE - 1 <= J.khi &&
+                        (mk.right < 0 || key + TILE - 1 <= (long long)itok0 + mk.off + mk.right) &&
+                        (mk.left < 0 || key >= (long long)itok1 + mk.off - mk.left);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          s[j][k] *= f[k >> 1];
+          if (!full) {
+            const int kk = key + 8 * j + 2 * t + (k & 1);
+            if (kk < J.klo || kk > J.khi || !sees(mk, tok[k >> 1], kk)) s[j][k] = -INFINITY;
+          }
+        }
+      bool grow = false;
+      float top[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        top[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+        grow |= top[r] > mrow[r] + SLACK_LOG2;
+      }
+      const int ev_new = mt.y >> 16;
+      grow = __any_sync(0xffffffffu, grow);
+      if (grow || ev_new != ev) {
+        float a[2];
+        const float de = exp2_int(ev - ev_new);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          a[r] = 1.f;
+          if (grow) {
+            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+            if (top[r] > mrow[r]) {
+              a[r] = fast_exp2(mrow[r] - top[r]);   // 0 from -inf
+              mrow[r] = top[r];
+            }
+          }
+          lrow[r] *= a[r];
+          a[r] *= de;
+        }
+        ev = ev_new;
+#pragma unroll
+        for (int j = 0; j < DV / 8; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[j][k] *= a[k >> 1];
+      }
+      uint32_t pa[4];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float ref = mrow[r] == -INFINITY ? 0.f : mrow[r] - P_LOG2;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float p0 = fast_exp2(s[j][2 * r] - ref), p1 = fast_exp2(s[j][2 * r + 1] - ref);
+          lrow[r] += p0 + p1;
+          pa[2 * j + r] = pack_h2(p0, p1);
+        }
+      }
+      // O += P V: keys 2t, 2t + 1 and 8 more are this lane's rows of V, column
+      // n of tile j is element j of 8-lane group n's consecutive elements
+      const uint32_t vt = st + C::KB;
+      if (DV == 64) {
+        const int c = g >> 1, h8 = (g & 1) * 8;
+        const uint2 w0 = lds64(vt + v_off<DV>(2 * t, c) + h8), w1 = lds64(vt + v_off<DV>(2 * t + 1, c) + h8);
+        const uint2 w2 = lds64(vt + v_off<DV>(2 * t + 8, c) + h8), w3 = lds64(vt + v_off<DV>(2 * t + 9, c) + h8);
+        const uint32_t a[4][2] = {{w0.x, w0.y}, {w1.x, w1.y}, {w2.x, w2.y}, {w3.x, w3.y}};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t lo0 = __byte_perm(a[0][q], a[1][q], 0x5140), hi0 = __byte_perm(a[0][q], a[1][q], 0x7362);
+          const uint32_t lo1 = __byte_perm(a[2][q], a[3][q], 0x5140), hi1 = __byte_perm(a[2][q], a[3][q], 0x7362);
+          mma16816(o[4 * q], pa, e4m3x2_to_h2((uint16_t)lo0), e4m3x2_to_h2((uint16_t)lo1));
+          mma16816(o[4 * q + 1], pa, e4m3x2_to_h2((uint16_t)(lo0 >> 16)), e4m3x2_to_h2((uint16_t)(lo1 >> 16)));
+          mma16816(o[4 * q + 2], pa, e4m3x2_to_h2((uint16_t)hi0), e4m3x2_to_h2((uint16_t)hi1));
+          mma16816(o[4 * q + 3], pa, e4m3x2_to_h2((uint16_t)(hi0 >> 16)), e4m3x2_to_h2((uint16_t)(hi1 >> 16)));
+        }
+      } else {
+#pragma unroll
+        for (int half = 0; half < DV / 128; ++half) {
+          const int c = g + 8 * half;
+          const uint4 w0 = lds128(vt + v_off<DV>(2 * t, c)), w1 = lds128(vt + v_off<DV>(2 * t + 1, c));
+          const uint4 w2 = lds128(vt + v_off<DV>(2 * t + 8, c)), w3 = lds128(vt + v_off<DV>(2 * t + 9, c));
+          const uint32_t a[4][4] = {{w0.x, w0.y, w0.z, w0.w}, {w1.x, w1.y, w1.z, w1.w},
+                                    {w2.x, w2.y, w2.z, w2.w}, {w3.x, w3.y, w3.z, w3.w}};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t lo0 = __byte_perm(a[0][q], a[1][q], 0x5140), hi0 = __byte_perm(a[0][q], a[1][q], 0x7362);
+            const uint32_t lo1 = __byte_perm(a[2][q], a[3][q], 0x5140), hi1 = __byte_perm(a[2][q], a[3][q], 0x7362);
+            const int j = half * 16 + 4 * q;
+            mma16816(o[j], pa, e4m3x2_to_h2((uint16_t)lo0), e4m3x2_to_h2((uint16_t)lo1));
+            mma16816(o[j + 1], pa, e4m3x2_to_h2((uint16_t)(lo0 >> 16)), e4m3x2_to_h2((uint16_t)(lo1 >> 16)));
+            mma16816(o[j + 2], pa, e4m3x2_to_h2((uint16_t)hi0), e4m3x2_to_h2((uint16_t)hi1));
+            mma16816(o[j + 3], pa, e4m3x2_to_h2((uint16_t)(hi0 >> 16)), e4m3x2_to_h2((uint16_t)(hi1 >> 16)));
+          }
+        }
+      }
+    }
+    __syncwarp();   // the stage may be refilled
+  }
+  cp_wait<0>();
+
+  // join the warps: maxima and sums, then each warp's O under the common maximum
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    lrow[r] += __shfl_xor_sync(0xffffffffu, lrow[r], 1);
+    lrow[r] += __shfl_xor_sync(0xffffffffu, lrow[r], 2);
+    if (t == 0) {
+      s_m[warp * ROWS + g + 8 * r] = mrow[r];
+      s_l[warp * ROWS + g + 8 * r] = lrow[r];
+    }
+  }
+  __syncthreads();   // also: every ring has been read
+  float* so = reinterpret_cast<float*>(smem);   // [NWARPS][ROWS][DV]
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int row = g + 8 * r;
+    float top = s_m[row];
+#pragma unroll
+    for (int w = 1; w < NWARPS; ++w) top = fmaxf(top, s_m[w * ROWS + row]);
+    const float a = (mrow[r] == -INFINITY ? 0.f : fast_exp2(mrow[r] - top)) * exp2_int(ev);
+    float* dst = so + (warp * ROWS + row) * DV;
+    if (mrow[r] == -INFINITY && !(lrow[r] != lrow[r])) {
+#pragma unroll
+      for (int j = 0; j < DV / 8; ++j) o[j][2 * r] = o[j][2 * r + 1] = 0.f;   // nothing seen
+    }
+    constexpr int NJ = DV == 64 ? 8 : 16;   // consecutive elements of a lane group
+#pragma unroll
+    for (int j = 0; j < DV / 8; j += 4) {
+      const int at = (j / NJ) * 128 + j % NJ + 2 * t * NJ;
+      *reinterpret_cast<float4*>(dst + at) =
+          make_float4(o[j][2 * r] * a, o[j + 1][2 * r] * a, o[j + 2][2 * r] * a, o[j + 3][2 * r] * a);
+      *reinterpret_cast<float4*>(dst + at + NJ) =
+          make_float4(o[j][2 * r + 1] * a, o[j + 1][2 * r + 1] * a, o[j + 2][2 * r + 1] * a, o[j + 3][2 * r + 1] * a);
+    }
+  }
+  __syncthreads();
+  const bool whole = J.ntile <= A.split_tiles;   // no other split holds keys of these rows
+  const long long part = ((long long)(b * A.c.hkv + hk) * A.mtiles + m) * A.nsplit + split;
+  for (int i = tid; i < J.nrow * (DV / 4); i += NTHREADS) {
+    const int row = i / (DV / 4), c = (i % (DV / 4)) * 4;
+    float top = s_m[row];
+#pragma unroll
+    for (int w = 1; w < NWARPS; ++w) top = fmaxf(top, s_m[w * ROWS + row]);
+    float l = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < NWARPS; ++w) {
+      const float mw = s_m[w * ROWS + row], lw = s_l[w * ROWS + row];
+      l += mw == -INFINITY ? lw : lw * fast_exp2(mw - top);   // lw is 0 there, or NaN
+      const float4 y = *reinterpret_cast<const float4*>(so + (w * ROWS + row) * DV + c);
+      v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+    }
+    if (whole) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int tk = (J.row0 + row) / A.g, h = hk * A.g + J.row0 + row - tk * A.g;
+      T* dst = static_cast<T*>(A.o) + elem_off(A.so, (long long)J.q0 + tk, h) + c;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_t2<T>(v.x * inv, v.y * inv), pack_t2<T>(v.z * inv, v.w * inv));
+      if (c == 0)
+        A.lse[(long long)h * A.total_q + J.q0 + tk] =
+            l == 0.f ? -INFINITY : (top - P_LOG2 + log2f(l)) * 0.6931471805599453f;
+    } else {
+      *reinterpret_cast<float4*>(A.part_o + (part * ROWS + row) * DV + c) = v;
+      if (c == 0) A.part_ml[part * ROWS + row] = make_float2(top, l);
+    }
+  }
+  if (reports && tid == 0)
+    A.status[b * A.nsplit + split] = J.bad ? ATTN_ERR_BAD_SEQLENS : *s_bad ? ATTN_ERR_BAD_PAGE : ATTN_OK;
+}
+
+// Joins the splits of a row in ascending order: O = sum 2^(m_s - m) O_s / sum
+// 2^(m_s - m) l_s.  A CTA takes NTHREADS / (DV / 4) rows of one job.
+template <int DV, typename T>
+__global__ void __launch_bounds__(NTHREADS) join_kernel(const Args A) {
+  constexpr int PER = NTHREADS / (DV / 4);
+  constexpr int GROUPS = ROWS / PER;
+  const int job = blockIdx.x / GROUPS, row = (blockIdx.x % GROUPS) * PER + threadIdx.x / (DV / 4);
+  const int c = (threadIdx.x % (DV / 4)) * 4;
+  const int m = job % A.mtiles, bh = job / A.mtiles, hk = bh % A.c.hkv, b = bh / A.c.hkv;
+  MaskArgs mk;
+  const Job J = make_job(A, b, m, mk);
+  if (row >= J.nrow || J.ntile <= A.split_tiles) return;
+  const int n = cdiv(J.ntile, A.split_tiles);
+  const float2* ml = A.part_ml + (long long)job * A.nsplit * ROWS + row;
+  const float* po = A.part_o + ((long long)job * A.nsplit * ROWS + row) * DV + c;
+  float top = -INFINITY;
+  for (int s = 0; s < n; ++s) top = fmaxf(top, ml[s * ROWS].x);
+  float l = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) {
+    const float2 x = ml[s * ROWS];
+    const float4 y = *reinterpret_cast<const float4*>(po + (long long)s * ROWS * DV);
+    const float w = x.x == -INFINITY ? (x.y != x.y ? x.y : 0.f) : fast_exp2(x.x - top);
+    l += w * x.y;
+    v.x += w * y.x; v.y += w * y.y; v.z += w * y.z; v.w += w * y.w;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int tk = (J.row0 + row) / A.g, h = hk * A.g + J.row0 + row - tk * A.g;
+  T* dst = static_cast<T*>(A.o) + elem_off(A.so, (long long)J.q0 + tk, h) + c;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_t2<T>(v.x * inv, v.y * inv), pack_t2<T>(v.z * inv, v.w * inv));
+  if (c == 0)
+    A.lse[(long long)h * A.total_q + J.q0 + tk] =
+        l == 0.f ? -INFINITY : (top - P_LOG2 + log2f(l)) * 0.6931471805599453f;
+}
+
+// ---------------------------------------------------------------- host side
+
+struct Layout {
+  int mtiles, nsplit, split_tiles;
+  long long jobs;
+  size_t off_status, off_ml, off_o, total;
+};
+
+static int max_keys(const attn_kv_fwd_params& p) {
+  const long long cap = (long long)p.max_blocks * p.cache.page_size;
+  return (int)(cap < p.max_seqlen_k ? cap : p.max_seqlen_k);
+}
+
+// Splits: enough CTAs to fill the GPU a few times over, none shorter than
+// MIN_TILES tiles.
+static Layout layout(const attn_kv_fwd_params& p) {
+  Layout L{};
+  const int g = p.nhead_q / p.cache.nhead_kv;
+  L.mtiles = (int)cdiv_ll((long long)(p.max_seqlen_q > 0 ? p.max_seqlen_q : 1) * g, ROWS);
+  L.jobs = (long long)p.batch * p.cache.nhead_kv * L.mtiles;
+  const int tiles = max_keys(p) / TILE + 2;
+  const long long want = SMS * 12;
+  long long n = cdiv_ll(want, L.jobs);
+  if (n > cdiv(tiles, MIN_TILES)) n = cdiv(tiles, MIN_TILES);
+  if (n < cdiv(tiles, MAX_TILES)) n = cdiv(tiles, MAX_TILES);
+  L.split_tiles = cdiv(cdiv(tiles, (int)n), NWARPS) * NWARPS;
+  if (L.split_tiles > MAX_TILES) L.split_tiles = MAX_TILES;
+  L.nsplit = cdiv(tiles, L.split_tiles);
+  auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
+  size_t o = 0;
+  L.off_status = o;
+  o = up(o + (size_t)p.batch * L.nsplit * sizeof(int));
+  const size_t parts = L.nsplit > 1 ? (size_t)L.jobs * L.nsplit : 0;
+  L.off_ml = o;
+  o = up(o + parts * ROWS * sizeof(float2));
+  L.off_o = o;
+  o = up(o + parts * ROWS * p.cache.d_v * sizeof(float));
+  L.total = o;
+  return L;
+}
+
+// The checks that need no pointers (the sizing call's).
+static int validate_sizes(const attn_kv_fwd_params* p) {
+  if (!p || p->reserved != 0 || (p->dtype != ATTN_BF16 && p->dtype != ATTN_FP16)) return ATTN_ERR_INVALID_ARG;
+  const attn_kv_cache& c = p->cache;
+  if (c.num_pages < 1 || c.nhead_kv < 1 || c.reserved != 0 || kv_page_shift(c.page_size) < 0) return ATTN_ERR_INVALID_ARG;
+  if (!kv_headdims(c.d_qk, c.d_v)) return ATTN_ERR_UNSUPPORTED_HEADDIM;
+  if (p->batch < 1 || p->batch > (1 << 20) || p->nhead_q < 1 || p->nhead_q > (1 << 16) || p->nhead_q % c.nhead_kv)
+    return ATTN_ERR_INVALID_ARG;
+  if (p->total_q < 0 || p->total_q > (1 << 30) || p->max_seqlen_q < 0 || p->max_seqlen_q > (1 << 30) ||
+      p->max_seqlen_k < 0 || p->max_seqlen_k > (1 << 30) || p->max_blocks < 1 ||
+      (long long)p->max_blocks * c.page_size > (1LL << 30))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->mask < ATTN_MASK_NONE || p->mask > ATTN_MASK_WINDOW) return ATTN_ERR_INVALID_ARG;
+  if (p->mask == ATTN_MASK_WINDOW && (p->window_left < -1 || p->window_right < -1)) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(p->softmax_scale) || p->softmax_scale == 0.f) return ATTN_ERR_INVALID_ARG;
+  // rows of a group and the grid fit 32 bits
+  const long long rows = (long long)p->max_seqlen_q * (p->nhead_q / c.nhead_kv);
+  if (rows > (1LL << 30)) return ATTN_ERR_INVALID_ARG;
+  const Layout L = layout(*p);
+  if (L.jobs * L.nsplit > (1LL << 30) || L.jobs > (1LL << 26)) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+template <int DQK, int DV, typename T>
+static int launch(const Args& a, long long jobs, cudaStream_t st) {
+  using C = Cfg<DQK, DV>;
+  auto kern = kv_fwd_kernel<DQK, DV, T>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  kern<<<(unsigned)(jobs * a.nsplit), NTHREADS, C::SMEM, st>>>(a);
+  if (a.nsplit > 1) {
+    constexpr int GROUPS = ROWS / (NTHREADS / (DV / 4));
+    join_kernel<DV, T><<<(unsigned)(jobs * GROUPS), NTHREADS, 0, st>>>(a);
+  }
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+template <typename T>
+static int launch_dims(const Args& a, int dqk, int dv, long long jobs, cudaStream_t st) {
+  if (dqk == 64) return launch<64, 64, T>(a, jobs, st);
+  if (dqk == 128) return launch<128, 128, T>(a, jobs, st);
+  if (dqk == 192) return launch<192, 128, T>(a, jobs, st);
+  return launch<256, 256, T>(a, jobs, st);
+}
+
+static int run(const attn_kv_fwd_params* p, void* ws, size_t ws_bytes, cudaStream_t st) {
+  int s = validate_sizes(p);
+  if (s != ATTN_OK) return s;
+  Args a{};
+  if ((s = kv_resolve(p->cache, &a.c)) != ATTN_OK) return s;
+  const int dqk = p->cache.d_qk, dv = p->cache.d_v;
+  if (!packed_strides(p->stride_q, p->nhead_q, dqk, &a.sq) || !packed_strides(p->stride_o, p->nhead_q, dv, &a.so))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->table_stride < p->max_blocks || p->table_stride >= (1LL << 36)) return ATTN_ERR_INVALID_ARG;
+  const void* ints[] = {p->cu_seqlens_q, p->seqlens_k, p->block_table};
+  for (const void* x : ints)
+    if (!x || !aligned_to(x, 4)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned_to(p->cu_seqlens_q_padded, 4)) return ATTN_ERR_INVALID_ARG;
+  const bool rows = p->total_q > 0;
+  if ((rows && (!p->q || !p->o || !p->lse)) || !aligned_to(p->q, 16) || !aligned_to(p->o, 16) || !aligned_to(p->lse, 4))
+    return ATTN_ERR_INVALID_ARG;
+  if (!ws || !aligned_to(ws, 256)) return ATTN_ERR_INVALID_ARG;
+  const Layout L = layout(*p);
+  if (ws_bytes < L.total) return ATTN_ERR_WORKSPACE_TOO_SMALL;
+  char* w = static_cast<char*>(ws);
+  a.q = p->q;
+  a.o = p->o;
+  a.lse = p->lse;
+  a.cu_q = p->cu_seqlens_q;
+  a.st_q = p->cu_seqlens_q_padded ? p->cu_seqlens_q_padded : p->cu_seqlens_q;
+  a.len_k = p->seqlens_k;
+  a.table = p->block_table;
+  a.table_stride = p->table_stride;
+  a.max_k = max_keys(*p);
+  a.total_q = p->total_q;
+  a.max_q = p->max_seqlen_q;
+  a.hq = p->nhead_q;
+  a.g = p->nhead_q / p->cache.nhead_kv;
+  a.mask = p->mask;
+  a.left = p->mask == ATTN_MASK_WINDOW ? p->window_left : -1;
+  a.right = p->mask == ATTN_MASK_WINDOW ? p->window_right : -1;
+  a.scale_log2 = p->softmax_scale * 1.4426950408889634f;
+  a.nsplit = L.nsplit;
+  a.split_tiles = L.split_tiles;
+  a.mtiles = L.mtiles;
+  a.status = reinterpret_cast<int*>(w + L.off_status);
+  a.part_ml = reinterpret_cast<float2*>(w + L.off_ml);
+  a.part_o = reinterpret_cast<float*>(w + L.off_o);
+  if (p->dtype == ATTN_BF16) return launch_dims<__nv_bfloat16>(a, dqk, dv, L.jobs, st);
+  return launch_dims<__half>(a, dqk, dv, L.jobs, st);
+}
+
+}  // namespace kvfwd
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" int attn_kv_fwd_workspace_size(const attn_kv_fwd_params* p, size_t* bytes) {
+  if (!bytes) return ATTN_ERR_INVALID_ARG;
+  *bytes = 0;
+  const int s = kvfwd::validate_sizes(p);
+  if (s != ATTN_OK) return s;
+  *bytes = kvfwd::layout(*p).total;
+  return ATTN_OK;
+}
+
+extern "C" int attn_kv_fwd(const attn_kv_fwd_params* p, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return kvfwd::run(p, workspace, workspace_bytes, stream);
+}
+
+extern "C" int attn_kv_fwd_read_status(const attn_kv_fwd_params* p, const void* workspace, size_t workspace_bytes,
+                                       cudaStream_t stream, int* status) {
+  if (!workspace || !status) return ATTN_ERR_INVALID_ARG;
+  const int s = kvfwd::validate_sizes(p);
+  if (s != ATTN_OK) return s;
+  const kvfwd::Layout L = kvfwd::layout(*p);
+  if (workspace_bytes < L.total) return ATTN_ERR_WORKSPACE_TOO_SMALL;
+  *status = ATTN_OK;
+  if (cudaStreamSynchronize(stream) != cudaSuccess) return ATTN_ERR_CUDA;
+  // request by request in pieces that fit the stack (no allocation in this library)
+  int part[1024];
+  const long long n = (long long)p->batch * L.nsplit;
+  for (long long i = 0; i < n; i += 1024) {
+    const size_t k = (size_t)(n - i < 1024 ? n - i : 1024);
+    if (cudaMemcpy(part, static_cast<const char*>(workspace) + L.off_status + i * sizeof(int), k * sizeof(int),
+                   cudaMemcpyDeviceToHost) != cudaSuccess)
+      return ATTN_ERR_CUDA;
+    for (size_t j = 0; j < k; ++j)
+      if (part[j] != ATTN_OK && *status == ATTN_OK) *status = part[j];
+  }
+  return ATTN_OK;
+}

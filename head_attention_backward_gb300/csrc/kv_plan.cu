@@ -1,0 +1,193 @@
+// Bookkeeping of a serving step (attn_kv_plan): prefix sums over the requests,
+// a stack of free pages, one slot and position per new token.
+//
+// A few kilobytes move, so the call is its launch and three dependent trips to
+// memory.  One CTA does it all: the sums of a batch of 8192 requests are eight
+// requests per thread, and nothing has to wait for another CTA.
+#include "common.cuh"
+#include "kv_common.cuh"
+
+namespace attn {
+namespace kvplan {
+
+constexpr int NTHREADS = 1024;
+
+struct Sums {
+  long long tok, take, back;
+};
+
+__device__ __forceinline__ Sums add(Sums a, Sums b) { return {a.tok + b.tok, a.take + b.take, a.back + b.back}; }
+
+// Largest b with prefix[b] <= x, for prefix[0] = 0 <= x < prefix[n].
+__device__ __forceinline__ int find(const int* prefix, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int pages_of(int tokens, int shift) { return (int)(((long long)tokens + (1 << shift) - 1) >> shift); }
+
+__global__ void __launch_bounds__(NTHREADS) plan_kernel(const attn_kv_plan_params P, const int shift) {
+  extern __shared__ int sm[];
+  const int n = P.batch;
+  int* cu = sm;                   // [n + 1] new tokens before request b
+  int* take = cu + n + 1;         // [n + 1] pages popped before it
+  int* back = take + n + 1;       // [n + 1] pages given back before it
+  int* len0 = back + n + 1;       // [n]     tokens it keeps
+  __shared__ Sums part[NTHREADS / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = cdiv(n, NTHREADS);
+  const int b0 = min(tid * per, n), b1 = min(b0 + per, n);
+  const int free_n = *P.free_count;   // the output may be the same word: read by all before the first barrier
+  const long long cap = (long long)P.max_blocks << shift;
+  bool bad = free_n < 0 || free_n > P.num_pages;
+  Sums mine{0, 0, 0};
+  for (int b = b0; b < b1; ++b) {
+    const int add_n = P.new_lens[b], len = P.seqlens[b];
+    if (add_n < ATTN_KV_RELEASE || len < 0 || len > cap || (add_n > 0 && (long long)len + add_n > cap)) {
+      bad = true;
+      continue;
+    }
+    const int held = pages_of(len, shift);
+    if (add_n == ATTN_KV_RELEASE) {
+      mine.back += held;
+    } else {
+      mine.tok += add_n;
+      mine.take += pages_of(len + add_n, shift) - held;
+    }
+  }
+  // exclusive prefix over the threads
+  Sums s = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    Sums o;
+    o.tok = __shfl_up_sync(0xffffffffu, s.tok, d);
+    o.take = __shfl_up_sync(0xffffffffu, s.take, d);
+    o.back = __shfl_up_sync(0xffffffffu, s.back, d);
+    if (lane >= d) s = add(s, o);
+  }
+  if (lane == 31) part[warp] = s;
+  const bool any_bad = __syncthreads_or(bad);
+  Sums before{0, 0, 0}, total{0, 0, 0};
+  for (int w = 0; w < NTHREADS / 32; ++w) {
+    if (w == warp) before = total;
+    total = add(total, part[w]);
+  }
+  before = add(before, Sums{s.tok - mine.tok, s.take - mine.take, s.back - mine.back});
+  int why = any_bad || total.tok > P.max_tokens || total.back > P.num_pages - free_n ? ATTN_ERR_BAD_SEQLENS
+            : total.take > free_n + total.back                                       ? ATTN_ERR_OUT_OF_PAGES
+                                                                                     : ATTN_OK;
+  if (why == ATTN_OK) {
+    // the sums fit 32 bits from here on
+    for (int b = b0; b < b1; ++b) {
+      const int add_n = P.new_lens[b], len = P.seqlens[b];
+      cu[b] = (int)before.tok;
+      take[b] = (int)before.take;
+      back[b] = (int)before.back;
+      const int held = pages_of(len, shift);
+      if (add_n == ATTN_KV_RELEASE) {
+        len0[b] = 0;
+        before.back += held;
+      } else {
+        len0[b] = len;
+        before.tok += add_n;
+        before.take += pages_of(len + add_n, shift) - held;
+      }
+    }
+    if (tid == 0) {
+      cu[n] = (int)total.tok;
+      take[n] = (int)total.take;
+      back[n] = (int)total.back;
+    }
+  }
+  __syncthreads();
+  const int nback = why == ATTN_OK ? back[n] : 0, ntake = why == ATTN_OK ? take[n] : 0;
+  const int top = free_n + nback;
+  // page number i given back / popped i-th (before anything is written)
+  auto given = [&](int i) {
+    const int b = find(back, n, i);
+    return __ldcg(P.block_table + b * P.table_stride + (i - back[b]));
+  };
+  auto outside = [&](int page) { return page < 0 || page >= P.num_pages; };
+  bool off = false;
+  for (int i = tid; i < nback; i += NTHREADS) off |= outside(given(i));
+  for (int i = tid; i < ntake; i += NTHREADS) {
+    const int at = top - 1 - i;
+    if (at < free_n) off |= outside(__ldcg(P.free_pages + at));
+  }
+  if (__syncthreads_or(off)) why = ATTN_ERR_BAD_PAGE;
+  if (why != ATTN_OK) {
+    for (int b = tid; b <= n; b += NTHREADS) {
+      P.cu_seqlens[b] = 0;
+      if (b < n) P.seqlens_out[b] = P.seqlens[b];
+    }
+    for (int t = tid; t < P.max_tokens; t += NTHREADS) {
+      P.positions[t] = 0;
+      P.slots[t] = -1;
+    }
+    if (tid == 0) {
+      *P.free_count_out = free_n;
+      *P.status = why;
+    }
+    return;
+  }
+  for (int i = tid; i < nback; i += NTHREADS) P.free_pages[free_n + i] = given(i);
+  __syncthreads();
+  for (int i = tid; i < ntake; i += NTHREADS) {
+    const int b = find(take, n, i);
+    P.block_table[b * P.table_stride + pages_of(len0[b], shift) + (i - take[b])] = __ldcg(P.free_pages + top - 1 - i);
+  }
+  for (int b = tid; b <= n; b += NTHREADS) {
+    P.cu_seqlens[b] = cu[b];
+    if (b < n) P.seqlens_out[b] = len0[b] + cu[b + 1] - cu[b];
+  }
+  if (tid == 0) {
+    *P.free_count_out = top - ntake;
+    *P.status = ATTN_OK;
+  }
+  __syncthreads();
+  const int total_tok = cu[n];
+  for (int t = tid; t < P.max_tokens; t += NTHREADS) {
+    int pos = 0;
+    long long slot = -1;
+    if (t < total_tok) {
+      const int b = find(cu, n, t);
+      pos = len0[b] + t - cu[b];
+      const int page = __ldcg(P.block_table + b * P.table_stride + (pos >> shift));
+      slot = ((long long)page << shift) + (pos & ((1 << shift) - 1));
+    }
+    P.positions[t] = pos;
+    P.slots[t] = slot;
+  }
+}
+
+static int run(const attn_kv_plan_params* p, cudaStream_t st) {
+  if (!p || p->reserved != 0) return ATTN_ERR_INVALID_ARG;
+  const int shift = kv_page_shift(p->page_size);
+  if (shift < 0 || p->batch < 1 || p->batch > ATTN_KV_MAX_BATCH || p->num_pages < 1 || p->max_blocks < 1 ||
+      p->max_tokens < 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (((long long)p->max_blocks << shift) > (1LL << 30) || p->table_stride < p->max_blocks ||
+      p->table_stride >= (1LL << 36))
+    return ATTN_ERR_INVALID_ARG;
+  const void* need[] = {p->new_lens, p->seqlens, p->seqlens_out, p->block_table, p->free_pages, p->free_count,
+                        p->free_count_out, p->cu_seqlens, p->status};
+  for (const void* x : need)
+    if (!x || !aligned_to(x, 4)) return ATTN_ERR_INVALID_ARG;
+  if (p->max_tokens > 0 && (!p->positions || !p->slots)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned_to(p->positions, 4) || !aligned_to(p->slots, 8)) return ATTN_ERR_INVALID_ARG;
+  const size_t smem = (4 * (size_t)p->batch + 3) * sizeof(int);
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  plan_kernel<<<1, NTHREADS, smem, st>>>(*p, shift);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace kvplan
+}  // namespace attn
+
+extern "C" int attn_kv_plan(const attn_kv_plan_params* p, cudaStream_t stream) { return attn::kvplan::run(p, stream); }

@@ -1,0 +1,236 @@
+// Rotary positions of q and k (attn_rope): pair (a, b) of a row becomes
+//   (a cos t - b sin t, b cos t + a sin t),  t = position * inv_freq.
+//
+// Memory bound: every element is read once and written once, the cosines are
+// computed once per (row, pair) and shared by the row's heads through shared
+// memory.
+#include <cmath>
+
+#include "common.cuh"
+#include "kv_common.cuh"
+
+namespace attn {
+namespace rope {
+
+constexpr int MAX_PAIRS = ATTN_ROPE_MAX_DIM / 2;
+constexpr int NTHREADS = 256;
+
+// Turns per position as a fraction of 2^64: position * step wraps exactly like
+// the angle does, so no reduction error grows with the position.
+struct Table {
+  unsigned long long step[MAX_PAIRS];
+  uint8_t axis[MAX_PAIRS];
+};
+
+struct Side {
+  const void* in;
+  void* out;
+  long long ib, ir, ih, ob, orow, oh;   // element strides {batch, row, head}
+};
+
+struct Args {
+  Side q, k;
+  const int* pos;
+  long long pa, pb, pr;
+  int rows, seqlen, hq, heads, dim, half, inverse, tok;
+};
+
+// cos and sin of 2 pi x / 2^64.  The nearest quarter turn is split off in
+// integers; the rest, at most an eighth of a turn, goes through the Taylor
+// series of sine and cosine (remainders below (pi/4)^11 / 11! = 1.8e-9 and
+// (pi/4)^12 / 12! = 1.2e-10).
+__device__ __forceinline__ float2 cos_sin_turns(unsigned long long x) {
+  const uint32_t u = (uint32_t)(x >> 32);
+  const uint32_t quarter = (u + 0x20000000u) >> 30;
+  const float r = (float)(int32_t)(u - (quarter << 30)) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+  const float z = r * r;
+  float s = fmaf(z, 2.7557319224e-6f, -1.9841269841e-4f);
+  s = fmaf(z, s, 8.3333333333e-3f);
+  s = fmaf(z, s, -1.6666666667e-1f);
+  s = fmaf(r * z, s, r);
+  float c = fmaf(z, -2.7557319224e-7f, 2.4801587302e-5f);
+  c = fmaf(z, c, -1.3888888889e-3f);
+  c = fmaf(z, c, 4.1666666667e-2f);
+  c = fmaf(z, c, -0.5f);
+  c = fmaf(z, c, 1.f);
+  if (quarter & 1) {
+    const float t = s;
+    s = c;
+    c = -t;
+  }
+  if (quarter & 2) {
+    s = -s;
+    c = -c;
+  }
+  return make_float2(c, s);
+}
+
+template <typename T, int N>
+struct alignas(sizeof(T) * N) Vec {
+  T v[N];
+};
+
+// One chunk: VP pairs, the a's and b's of which lie in two vectors of VP
+// elements (lo and hi half of the rotated columns, or one run of 2 VP elements
+// when interleaved).  VP = 8 (16-bit) or 4 (fp32) is one 16-byte access per
+// vector; VP = 1 takes any rot_dim and fp32 alignment.  Columns past the
+// rotated ones are copied in chunks of VP.
+template <typename T, int VP, bool INTER>
+__global__ void __launch_bounds__(NTHREADS) rope_kernel(const Args A, const __grid_constant__ Table table) {
+  using V = Vec<T, VP>;
+  extern __shared__ float2 cs[];   // [tok][half]
+  const int row0 = blockIdx.x * A.tok;
+  const int nrow = min(A.tok, A.rows - row0);
+  for (int i = threadIdx.x; i < nrow * A.half; i += NTHREADS) {
+    const int r = i / A.half, pair = i - r * A.half;
+    const int row = row0 + r, b = row / A.seqlen, s = row - b * A.seqlen;
+    const int pos = __ldg(A.pos + table.axis[pair] * A.pa + b * A.pb + s * A.pr);
+    float2 x = cos_sin_turns((unsigned long long)(long long)pos * table.step[pair]);
+    if (A.inverse) x.y = -x.y;
+    cs[i] = x;
+  }
+  __syncthreads();
+  const int rot_chunks = A.half / VP;
+  const int chunks = rot_chunks + (A.dim - 2 * A.half) / VP;
+  for (int i = threadIdx.x; i < nrow * A.heads * chunks; i += NTHREADS) {
+    const int c = i % chunks, rh = i / chunks;
+    const int h = rh % A.heads, r = rh / A.heads;
+    const int row = row0 + r, b = row / A.seqlen, s = row - b * A.seqlen;
+    const bool is_q = h < A.hq;
+    const Side& x = is_q ? A.q : A.k;
+    const int hh = is_q ? h : h - A.hq;
+    const T* in = static_cast<const T*>(x.in) + b * x.ib + s * x.ir + hh * x.ih;
+    T* out = static_cast<T*>(x.out) + b * x.ob + s * x.orow + hh * x.oh;
+    if (c >= rot_chunks) {
+      const int at = 2 * A.half + (c - rot_chunks) * VP;
+      *reinterpret_cast<V*>(out + at) = *reinterpret_cast<const V*>(in + at);
+      continue;
+    }
+    const int at0 = INTER ? c * 2 * VP : c * VP;
+    const int at1 = INTER ? at0 + VP : at0 + A.half;
+    V v0 = *reinterpret_cast<const V*>(in + at0);
+    V v1 = *reinterpret_cast<const V*>(in + at1);
+    const float2* t = cs + r * A.half + c * VP;
+#pragma unroll
+    for (int p = 0; p < VP; ++p) {
+      // element of a and b of pair p among the 2 VP loaded ones
+      const int ea = INTER ? 2 * p : p, eb = INTER ? 2 * p + 1 : p + VP;
+      T& ra = ea < VP ? v0.v[ea] : v1.v[ea - VP];
+      T& rb = eb < VP ? v0.v[eb] : v1.v[eb - VP];
+      const float a = TypeOps<T>::to_f(ra), bb = TypeOps<T>::to_f(rb);
+      const float2 k = t[p];
+      ra = TypeOps<T>::from_f(a * k.x - bb * k.y);
+      rb = TypeOps<T>::from_f(bb * k.x + a * k.y);
+    }
+    *reinterpret_cast<V*>(out + at0) = v0;
+    *reinterpret_cast<V*>(out + at1) = v1;
+  }
+}
+
+template <typename T, int VP>
+static void launch(const Args& a, const Table& t, bool inter, cudaStream_t st) {
+  const int grid = cdiv(a.rows, a.tok);
+  const size_t smem = (size_t)a.tok * a.half * sizeof(float2);
+  if (inter)
+    rope_kernel<T, VP, true><<<grid, NTHREADS, smem, st>>>(a, t);
+  else
+    rope_kernel<T, VP, false><<<grid, NTHREADS, smem, st>>>(a, t);
+}
+
+// {batch, row, head} strides: contiguous when all are zero, otherwise positive
+// wherever the dimension has more than one entry and, for 16-bit types, whole
+// 16-byte units.
+static bool strides3(const int64_t in[3], int batch, int seqlen, int heads, int dim, bool vec16, long long out[3]) {
+  if (in[0] == 0 && in[1] == 0 && in[2] == 0) {
+    out[2] = dim;
+    out[1] = (long long)heads * dim;
+    out[0] = (long long)seqlen * out[1];
+    return true;
+  }
+  const int n[3] = {batch, seqlen, heads};
+  for (int i = 0; i < 3; ++i) {
+    out[i] = n[i] > 1 ? in[i] : 0;
+    if (n[i] > 1 && (in[i] <= 0 || in[i] >= (1LL << 36) || (vec16 && in[i] % 8))) return false;
+  }
+  return true;
+}
+
+static int run(const attn_rope_params* p, cudaStream_t st) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  if (p->dtype < ATTN_BF16 || p->dtype > ATTN_FP32) return ATTN_ERR_INVALID_ARG;
+  const bool f32 = p->dtype == ATTN_FP32;
+  if (p->batch < 0 || p->seqlen < 0 || p->nhead_q < 1 || p->nhead_kv < 0) return ATTN_ERR_INVALID_ARG;
+  if ((long long)p->batch * p->seqlen > (1LL << 30) || p->nhead_q > (1 << 20) || p->nhead_kv > (1 << 20))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->head_dim < 2 || p->head_dim > ATTN_ROPE_MAX_DIM || (!f32 && p->head_dim % 8))
+    return ATTN_ERR_UNSUPPORTED_HEADDIM;
+  if (p->rot_dim < 2 || p->rot_dim > p->head_dim || p->rot_dim % 2) return ATTN_ERR_INVALID_ARG;
+  if (p->n_axes < 1 || p->n_axes > ATTN_ROPE_MAX_AXES) return ATTN_ERR_INVALID_ARG;
+  const int half = p->rot_dim / 2;
+  if (!p->inv_freq) return ATTN_ERR_INVALID_ARG;
+  Table t{};
+  for (int i = 0; i < half; ++i) {
+    const double f = p->inv_freq[i];
+    if (!std::isfinite(f)) return ATTN_ERR_INVALID_ARG;
+    t.axis[i] = p->pair_axis ? p->pair_axis[i] : 0;
+    if (t.axis[i] >= p->n_axes) return ATTN_ERR_INVALID_ARG;
+    // turns per position, whole turns dropped, in units of 2^-64
+    double turns = f * 0.15915494309189533577;
+    turns -= std::floor(turns);
+    const double hi = std::floor(turns * 4294967296.0);            // exact: a shift, then 32 whole bits
+    const double lo = (turns * 4294967296.0 - hi) * 4294967296.0;   // exact, below 2^32
+    t.step[i] = ((unsigned long long)hi << 32) + (unsigned long long)lo;   // turns = 1.0 wraps to 0
+  }
+  const bool has_k = p->nhead_kv > 0;
+  Args a{};
+  long long s[3];
+  auto side = [&](const void* in, void* out, const int64_t si[3], const int64_t so[3], int heads, Side* x) {
+    const unsigned al = f32 ? 4 : 16;
+    if (!in || !out || !aligned_to(in, al) || !aligned_to(out, al)) return false;
+    if (!strides3(si, p->batch, p->seqlen, heads, p->head_dim, !f32, s)) return false;
+    x->in = in; x->ib = s[0]; x->ir = s[1]; x->ih = s[2];
+    if (!strides3(so, p->batch, p->seqlen, heads, p->head_dim, !f32, s)) return false;
+    x->out = out; x->ob = s[0]; x->orow = s[1]; x->oh = s[2];
+    // in place only element by element
+    return in != out || (x->ib == x->ob && x->ir == x->orow && x->ih == x->oh) ||
+           (long long)p->batch * p->seqlen == 0;
+  };
+  const long long rows = (long long)p->batch * p->seqlen;
+  if (rows == 0) return ATTN_OK;
+  if (!side(p->q, p->q_out, p->stride_q, p->stride_q_out, p->nhead_q, &a.q)) return ATTN_ERR_INVALID_ARG;
+  if (has_k && !side(p->k, p->k_out, p->stride_k, p->stride_k_out, p->nhead_kv, &a.k)) return ATTN_ERR_INVALID_ARG;
+  if (!p->positions || !aligned_to(p->positions, 4)) return ATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (p->stride_pos[i] < 0 || p->stride_pos[i] >= (1LL << 36)) return ATTN_ERR_INVALID_ARG;
+  a.pos = p->positions;
+  a.pa = p->stride_pos[0]; a.pb = p->stride_pos[1]; a.pr = p->stride_pos[2];
+  a.rows = (int)rows;
+  a.seqlen = p->seqlen;
+  a.hq = p->nhead_q;
+  a.heads = p->nhead_q + p->nhead_kv;
+  a.dim = p->head_dim;
+  a.half = half;
+  a.inverse = p->inverse != 0;
+  a.tok = 1;
+  const int vp = f32 ? 4 : 8;
+  bool vec = p->interleaved ? p->rot_dim % (2 * vp) == 0 : half % vp == 0;
+  vec = vec && p->head_dim % vp == 0;
+  if (f32)
+    for (const Side* x : {&a.q, &a.k}) {
+      if (x == &a.k && !has_k) continue;
+      vec = vec && aligned_to(x->in, 16) && aligned_to(x->out, 16) && x->ib % 4 == 0 && x->ir % 4 == 0 &&
+            x->ih % 4 == 0 && x->ob % 4 == 0 && x->orow % 4 == 0 && x->oh % 4 == 0;
+    }
+  const bool inter = p->interleaved != 0;
+  switch (p->dtype) {
+    case ATTN_BF16: vec ? launch<__nv_bfloat16, 8>(a, t, inter, st) : launch<__nv_bfloat16, 1>(a, t, inter, st); break;
+    case ATTN_FP16: vec ? launch<__half, 8>(a, t, inter, st) : launch<__half, 1>(a, t, inter, st); break;
+    default: vec ? launch<float, 4>(a, t, inter, st) : launch<float, 1>(a, t, inter, st); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace rope
+}  // namespace attn
+
+extern "C" int attn_rope(const attn_rope_params* p, cudaStream_t stream) { return attn::rope::run(p, stream); }

@@ -69,8 +69,10 @@ typedef enum {
   ATTN_ERR_CUDA = -4,                /* a CUDA runtime/driver call failed           */
   ATTN_ERR_DEVICE_FLAG = -5,         /* kernels reported an error (see read_status) */
   ATTN_ERR_TIMEOUT = -6,             /* a bounded in-kernel wait expired            */
-  ATTN_ERR_BAD_SEQLENS = -7          /* cu_seqlens (or the padded starts) not
+  ATTN_ERR_BAD_SEQLENS = -7,         /* cu_seqlens (or the padded starts) not
                                         monotone, overlapping or beyond the bounds */
+  ATTN_ERR_BAD_PAGE = -8,            /* a page number outside the cache           */
+  ATTN_ERR_OUT_OF_PAGES = -9         /* more pages wanted than are free           */
 } attn_status_t;
 
 /* Mask kinds: the AITER mask enum reviewed in TransformerEngine PR #446
@@ -385,6 +387,227 @@ int attn_bwd_static_ws(const attn_bwd_params* p, cudaStream_t stream);
  * caller; its contents are overwritten.  Synchronises `stream`.  Returns
  * ATTN_OK when the test ran (the results are in status), an error otherwise. */
 int attn_selftest_waits(void* scratch, size_t scratch_bytes, cudaStream_t stream, int status[3]);
+
+/* ===================================================================== *
+ * Serving operators: rotary positions, a paged 8-bit key / value cache,
+ * its bookkeeping, and attention over it.  One serving step runs
+ *   attn_kv_plan -> attn_rope -> attn_kv_append -> attn_kv_fwd
+ * on one stream without a host synchronisation, and can be captured into a
+ * CUDA graph (attn_kv_plan may update its lengths in place, so a replay is
+ * the next step).  attn_rope also serves training: forward before attn_fwd,
+ * inverse on attn_bwd's dq and dk.  The pages cited above have no
+ * counterpart of these: they are additions of this library, under its
+ * conventions (caller's buffers and stream, checks before any launch).
+ * ===================================================================== */
+
+#define ATTN_ROPE_MAX_AXES 4
+#define ATTN_ROPE_MAX_DIM 256
+
+/* Rotary positions of q and k in one call.  Pair i (0 <= i < rot_dim / 2) of
+ * every head of a row is turned by the angle
+ *   t = positions[pair_axis[i]][row] * inv_freq[i]   (radians):
+ *   y_a = x_a cos t - x_b sin t,   y_b = x_b cos t + x_a sin t,
+ * where (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved.
+ * Columns from rot_dim on are copied bit by bit.  With several axes (time,
+ * height, width of an image or video token) each pair follows the axis that
+ * pair_axis names.  inverse != 0 turns by -t: the gradient with respect to x
+ * of the forward call, applied to the gradient of y.
+ * The angle is reduced to a fraction of a turn in 64-bit fixed point, so it
+ * is as exact at position 2^20 as at 0 (the table holds inv_freq / 2 pi to 53
+ * bits); products and sums are fp32 and each output is rounded once. */
+typedef struct {
+  int32_t dtype;          /* attn_dtype_t of q, k and the outputs                  */
+  int32_t batch;          /* rows are [batch, seqlen]; packed tokens: batch = 1    */
+  int32_t seqlen;
+  int32_t nhead_q;        /* >= 1                                                  */
+  int32_t nhead_kv;       /* 0: no k                                               */
+  int32_t head_dim;       /* 2 .. 256; a multiple of 8 for BF16/FP16               */
+  int32_t rot_dim;        /* even, 2 .. head_dim                                   */
+  int32_t n_axes;         /* 1 .. ATTN_ROPE_MAX_AXES                               */
+  int32_t interleaved;    /* pairing, see above                                    */
+  int32_t inverse;
+  const int32_t* positions; /* device, 4-byte aligned; any int32 value             */
+  int64_t stride_pos[3];  /* elements from one {axis, batch entry, row} to the next;
+                             0 shares positions along that dimension (no default) */
+  const double* inv_freq; /* HOST, [rot_dim / 2], finite; read during the call     */
+  const uint8_t* pair_axis; /* HOST, [rot_dim / 2], each < n_axes; NULL: all axis 0 */
+  const void* q;          /* device, 16-byte aligned (4-byte for FP32)             */
+  const void* k;
+  void* q_out;            /* device; may be q itself with q's strides (in place),
+                             otherwise the outputs overlap nothing               */
+  void* k_out;
+  int64_t stride_q[3];    /* {batch, row, head} element strides as in
+                             attn_bwd_params (all three 0: contiguous), but any
+                             batch stride                                        */
+  int64_t stride_k[3];
+  int64_t stride_q_out[3];
+  int64_t stride_k_out[3];
+} attn_rope_params;
+
+/* Enqueue the rotation on `stream` (one kernel).  No rows: nothing runs. */
+int attn_rope(const attn_rope_params* p, cudaStream_t stream);
+
+/* A paged cache of keys and values in 8 bits.  Page p holds page_size
+ * consecutive tokens of one request.  Element (p, row, head, c) of k is the
+ * e4m3 value (4 exponent bits, 3 mantissa bits, largest 448) at byte
+ * p * stride_k[0] + row * stride_k[1] + head * stride_k[2] + c of k, times the
+ * scale of its page and head, 2^(k_exp[p * nhead_kv + head] - 127); likewise
+ * v.  A power of two costs an e4m3 value no precision and makes the scale
+ * exact to apply and to change.  Exponent bytes are read clamped to
+ * [97, 157], the scales 2^-30 .. 2^30. */
+typedef struct {
+  int32_t num_pages;      /* >= 1                                                  */
+  int32_t page_size;      /* 16, 32, 64, 128 or 256                                */
+  int32_t nhead_kv;
+  int32_t d_qk;           /* (64, 64), (128, 128), (192, 128) or (256, 256)        */
+  int32_t d_v;
+  int32_t reserved;       /* 0                                                     */
+  void* k;                /* device, 16-byte aligned                               */
+  void* v;
+  uint8_t* k_exp;         /* device, [num_pages, nhead_kv]                         */
+  uint8_t* v_exp;
+  int64_t stride_k[3];    /* {page, row, head} byte strides, positive multiples of
+                             16; all three 0 = [page, row, head, d] contiguous.
+                             A layout with the heads outside the rows works too */
+  int64_t stride_v[3];
+} attn_kv_cache;
+
+/* Requests of one attn_kv_plan call, and the new_lens entry of a request that
+ * has ended. */
+#define ATTN_KV_MAX_BATCH 8192
+#define ATTN_KV_RELEASE (-1)
+
+/* Bookkeeping of one serving step, from request lengths on the device: pages
+ * for the new tokens, their positions and cache slots, the segment offsets.
+ * The free pages are a stack: free_pages[0 .. free_count - 1].  In this order
+ *   1. a request b with new_lens[b] = ATTN_KV_RELEASE gives back its
+ *      ceil(seqlens[b] / page_size) pages (pushed request by request, in
+ *      block-table order) and its length becomes 0;
+ *   2. the others grow to seqlens[b] + new_lens[b] tokens; pages they lack are
+ *      popped, request by request in order, and entered in block_table.
+ * Token t of request b's new ones (row cu_seqlens[b] + t of the packed step)
+ * gets position x = seqlens[b] + t and slot block_table[b][x / page_size] *
+ * page_size + x % page_size.  Everything is a function of the inputs alone.
+ * If anything is wrong, nothing changes: seqlens_out and free_count_out
+ * repeat the inputs, cu_seqlens is 0 and every slot -1 (a step without
+ * tokens for the other operators), and *status says why:
+ * ATTN_ERR_BAD_SEQLENS (a length below 0, past max_blocks pages or with
+ * more new tokens than max_tokens in all; a free_count outside 0..num_pages,
+ * or more pages given back than the stack holds), ATTN_ERR_OUT_OF_PAGES, or
+ * ATTN_ERR_BAD_PAGE (a page to be pushed or popped outside 0..num_pages - 1). */
+typedef struct {
+  int32_t batch;          /* 1 .. ATTN_KV_MAX_BATCH                                */
+  int32_t page_size;      /* as in attn_kv_cache                                   */
+  int32_t num_pages;
+  int32_t max_blocks;     /* columns of block_table, max_blocks * page_size <= 2^30 */
+  int32_t max_tokens;     /* entries of positions and slots                        */
+  int32_t reserved;       /* 0                                                     */
+  const int32_t* new_lens;   /* device, [batch]                                    */
+  const int32_t* seqlens;    /* device, [batch], tokens in the cache               */
+  int32_t* seqlens_out;      /* device, [batch]; may be seqlens                    */
+  int32_t* block_table;      /* device, [batch] rows of max_blocks, updated        */
+  int64_t table_stride;      /* elements from row to row, >= max_blocks            */
+  int32_t* free_pages;       /* device, [num_pages], updated                       */
+  const int32_t* free_count; /* device, [1]                                        */
+  int32_t* free_count_out;   /* device, [1]; may be free_count                     */
+  int32_t* cu_seqlens;       /* device output, [batch + 1]                         */
+  int32_t* positions;        /* device output, [max_tokens], 0 past the last token */
+  int64_t* slots;            /* device output, [max_tokens], 8-byte aligned, -1
+                                past the last token                              */
+  int32_t* status;           /* device output, [1], attn_status_t                  */
+} attn_kv_plan_params;
+
+/* Enqueue the bookkeeping on `stream`. */
+int attn_kv_plan(const attn_kv_plan_params* p, cudaStream_t stream);
+
+/* Quantise new keys and values into the cache.  Token t goes to row
+ * slots[t] % page_size of page slots[t] / page_size; slots outside the cache
+ * (-1) are skipped.  The tokens of a call that go to one page form a run; the
+ * page's rows in front of the run's first row are live, other rows that the
+ * run does not name are not (their values become unspecified).  For each run,
+ * head and side, with amax = the largest |x| of the run and e(amax) the least
+ * e with amax <= 448 * 2^e, limited to [-30, 30]:
+ *   - the run holds row 0: the scale becomes 2^e(amax);
+ *   - otherwise it becomes the larger of that and the old scale, and if it
+ *     grew the live rows are rounded again to it;
+ *   - the new values are rounded (to nearest even) to e4m3 multiples of it;
+ *     beyond 448 scales they are clamped, NaN stays NaN (and is ignored by
+ *     amax).
+ * A run is found as long as fewer than page_size tokens of other pages (or
+ * skipped ones) lie between two of its tokens.  A page named again farther
+ * off, or a slot named twice, leaves that page's values unspecified, and
+ * nothing else. */
+typedef struct {
+  int32_t dtype;          /* ATTN_BF16 or ATTN_FP16: type of k and v               */
+  int32_t tokens;         /* rows of k, v and slots                                */
+  const void* k;          /* device, [tokens, nhead_kv, d_qk], 16-byte aligned     */
+  const void* v;          /* device, [tokens, nhead_kv, d_v]                       */
+  int64_t stride_k[3];    /* {ignored, row, head} element strides, as the group
+                             mode of attn_bwd_params (all three 0: contiguous)   */
+  int64_t stride_v[3];
+  const int64_t* slots;   /* device, [tokens], 8-byte aligned                      */
+  attn_kv_cache cache;
+} attn_kv_append_params;
+
+/* Enqueue the append on `stream` (one kernel). */
+int attn_kv_append(const attn_kv_append_params* p, cudaStream_t stream);
+
+/* Attention of packed query segments over the cache: segment b's queries are
+ * rows cu_seqlens_q[b] .. of q (the physical start comes from
+ * cu_seqlens_q_padded when given, as in attn_bwd_params), its keys the first
+ * seqlens_k[b] tokens of the pages in block_table row b.  Masks are those of
+ * attn_mask_t with Lk = seqlens_k[b]; ATTN_MASK_CAUSAL_BOTTOM_RIGHT is the one
+ * of generation (the new tokens are the last ones), ATTN_MASK_NONE that of
+ * cross attention to an encoder's cached states.  A row that sees no key gets
+ * O = 0 and LSE = -inf; rows of no segment are left as they were.
+ * Lengths and pages are checked on the device: a segment outside q counts as
+ * empty, seqlens_k is limited to 0 .. min(max_seqlen_k, max_blocks pages), the
+ * tokens of a page outside the cache are masked, and attn_kv_fwd_read_status
+ * reports it.  Cache rows past seqlens_k (or, for single-token segments,
+ * outside the mask) never reach a result, whatever they hold; other masked
+ * values must be finite. */
+typedef struct {
+  int32_t dtype;          /* ATTN_BF16 or ATTN_FP16: type of q and o               */
+  int32_t batch;          /* segments, >= 1                                        */
+  int32_t nhead_q;        /* a multiple of cache.nhead_kv                          */
+  int32_t total_q;        /* rows of q and o                                       */
+  int32_t max_seqlen_q;   /* upper bound on every query segment: longer ones count
+                             as empty (reported)                                 */
+  int32_t max_seqlen_k;   /* upper bound on seqlens_k; splits and workspace follow
+                             it, so a tight bound is a fast one                  */
+  int32_t max_blocks;     /* columns of block_table                                */
+  int32_t mask;           /* attn_mask_t                                           */
+  int32_t window_left;    /* ATTN_MASK_WINDOW only; -1 = unbounded                 */
+  int32_t window_right;
+  float softmax_scale;    /* finite, not 0                                         */
+  int32_t reserved;       /* 0                                                     */
+  const int32_t* cu_seqlens_q; /* device, [batch + 1]                              */
+  const int32_t* cu_seqlens_q_padded; /* device, [batch + 1], or NULL              */
+  const int32_t* seqlens_k;    /* device, [batch]                                  */
+  const int32_t* block_table;  /* device, [batch] rows of max_blocks               */
+  int64_t table_stride;        /* elements from row to row, >= max_blocks          */
+  const void* q;          /* device, [total_q, nhead_q, d_qk], 16-byte aligned     */
+  void* o;                /* device output, [total_q, nhead_q, d_v]                */
+  float* lse;             /* device output, [nhead_q, total_q], fp32 natural log   */
+  int64_t stride_q[3];    /* {ignored, row, head} element strides, as the group
+                             mode of attn_bwd_params (all three 0: contiguous)   */
+  int64_t stride_o[3];
+  attn_kv_cache cache;
+} attn_kv_fwd_params;
+
+/* Workspace bytes attn_kv_fwd needs for *p: host arithmetic on the scalar
+ * fields alone, as attn_bwd_workspace_size. */
+int attn_kv_fwd_workspace_size(const attn_kv_fwd_params* p, size_t* bytes);
+
+/* Enqueue the attention on `stream`.  `workspace`: device, 256-byte aligned,
+ * contents irrelevant on entry, not shared with another call in flight. */
+int attn_kv_fwd(const attn_kv_fwd_params* p, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Synchronise `stream` and return what the last attn_kv_fwd of *p on
+ * `workspace` found on the device (ATTN_OK, ATTN_ERR_BAD_SEQLENS,
+ * ATTN_ERR_BAD_PAGE) in *status. */
+int attn_kv_fwd_read_status(const attn_kv_fwd_params* p, const void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream, int* status);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,515 @@
+"""The paged 8-bit cache on the GPU: bookkeeping, append and attention against
+the fp64 oracle, alone and as the serving step they make up."""
+import math
+
+import pytest
+import torch
+
+from oracle import kv_ref
+from tests.kv_cases import block_table, check_attend, random_cache
+from tests.test_gpu_parity import B  # noqa: F401  (fixture)
+
+pytestmark = pytest.mark.gpu
+
+I32 = torch.int32
+DIMS = [(64, 64), (128, 128), (192, 128), (256, 256)]
+
+
+def dev(x, dtype=I32):
+    return torch.tensor(x, dtype=dtype, device="cuda")
+
+
+def handle(B, kc, vc, ke, ve):
+    f8 = torch.float8_e4m3fn
+    return B.KvCache(kc.cuda().view(f8), vc.cuda().view(f8), ke.cuda(), ve.cuda())
+
+
+# ---------------------------------------------------------------------- plan
+
+PLANS = [
+    # page, new_lens, seqlens, extra free pages, extra token capacity
+    (16, [1], [0], 0, 0),
+    (16, [0], [0], 1, 3),
+    (16, [1, 1, 1], [15, 16, 17], 0, 0),
+    (32, [0, 5, -1, 100, 1, -1, 0], [0, 0, 70, 3, 32, 0, 64], 0, 7),
+    (64, [-1, -1], [64, 1], 0, 0),
+    (16, [-1, 40], [33, 0], -2, 1),          # the new request needs the pages given back
+    (256, [1000, 1], [1000, 255], 5, 0),
+    (16, [7000, 3, 1], [0, 10, 5000], 3, 11),
+]
+
+
+@pytest.mark.parametrize("page,new,lens,spare,more", PLANS)
+@pytest.mark.parametrize("in_place", [False, True])
+def test_plan(B, page, new, lens, spare, more, in_place):
+    g = torch.Generator().manual_seed(len(new))
+    held = [(n + page - 1) // page for n in lens]
+    grown = [(max(0, n) + (0 if n < 0 else x) + page - 1) // page for n, x in zip(new, lens)]
+    need = sum(max(0, a - h) for a, h in zip(grown, held))
+    pool = sum(held) + need + max(spare, 0)
+    order = torch.randperm(pool, generator=g).tolist()
+    cols = max(grown + held) + 2
+    table, at = [], 0
+    for h in held:
+        table.append(order[at:at + h] + [-1] * (cols - h))
+        at += h
+    free = order[at:]
+    if spare < 0:
+        free = free[:spare]
+    count = len(free)
+    free = free + [-7] * (pool - count)
+    cap = sum(max(n, 0) for n in new) + more
+    td = dev(table)
+    wide = torch.full((len(new), cols + 5), -3, dtype=I32, device="cuda")   # rows further apart than they are long
+    wide[:, :cols] = td
+    td = wide[:, :cols]
+    fd, nd, ld, cd = dev(free), dev(new), dev(lens), dev([count])
+    out = None
+    if in_place:
+        out = B.KvPlan(torch.empty(len(new) + 1, dtype=I32, device="cuda"), ld, torch.empty(cap, dtype=I32, device="cuda"),
+                       torch.empty(cap, dtype=torch.int64, device="cuda"), cd, dev([5]))
+    p = B.kv_plan(nd, ld, td, fd, cd, page_size=page, max_tokens=cap, out=out)
+    p.check()
+    cu, after, pos, slots, left = kv_ref.plan(new, lens, table, free, count, page, cap)
+    assert p.cu_seqlens.tolist() == cu and p.seqlens.tolist() == after
+    assert p.positions.tolist() == pos and p.slots.tolist() == slots
+    assert p.free_count.tolist() == [left] and td.tolist() == table and fd.tolist() == free
+    assert bool((wide[:, cols:] == -3).all())
+    if not in_place:
+        assert ld.tolist() == lens and cd.tolist() == [count]
+
+
+@pytest.mark.parametrize("batch", [1000, 1025, 8192])
+def test_plan_many_requests(B, batch):
+    g = torch.Generator().manual_seed(batch)
+    lens = torch.randint(0, 60, (batch,), generator=g).tolist()
+    new = torch.randint(-1, 5, (batch,), generator=g).tolist()
+    table, pool = block_table(lens, 16, g, extra_pages=batch, extra_cols=2)
+    used = {p for row in table for p in row if p >= 0}
+    free = [p for p in range(pool) if p not in used]
+    count = len(free)
+    free += [0] * (pool - count)
+    cap = sum(max(n, 0) for n in new) + 100
+    td, fd = dev(table), dev(free)
+    p = B.kv_plan(dev(new), dev(lens), td, fd, dev([count]), page_size=16, max_tokens=cap)
+    p.check()
+    cu, after, pos, slots, left = kv_ref.plan(new, lens, table, free, count, 16, cap)
+    assert p.cu_seqlens.tolist() == cu and p.seqlens.tolist() == after
+    assert p.positions.tolist() == pos and p.slots.tolist() == slots
+    assert p.free_count.tolist() == [left] and td.tolist() == table and fd.tolist() == free
+
+
+@pytest.mark.parametrize("what,status", [
+    ("len below zero", -7), ("len past the table", -7), ("grows past the table", -7), ("new below -1", -7),
+    ("too many tokens", -7), ("free_count negative", -7), ("free_count past the pool", -7), ("gives back too many", -7),
+    ("out of pages", -9), ("pops a bad page", -8), ("gives back a bad page", -8)])
+def test_plan_refused_step_changes_nothing(B, what, status):
+    page, cols, pool = 16, 4, 12
+    new, lens, count, cap = [3, -1, 20], [10, 33, 0], 8, 40
+    table = [[0, -1, -1, -1], [1, 2, 3, -1], [-1, -1, -1, -1]]
+    free = [4, 5, 6, 7, 8, 9, 10, 11] + [0] * 4
+    if what == "len below zero":
+        lens[0] = -1
+    elif what == "len past the table":
+        lens[1] = page * cols + 1
+    elif what == "grows past the table":
+        new[2] = page * cols + 1
+        cap = 100
+    elif what == "new below -1":
+        new[2] = -2
+    elif what == "too many tokens":
+        cap = 22
+    elif what == "free_count negative":
+        count = -1
+    elif what == "free_count past the pool":
+        count = pool + 1
+    elif what == "gives back too many":
+        count = pool - 2
+    elif what == "out of pages":
+        count, new, cap = 1, [3, 0, 40], 43
+    elif what == "pops a bad page":
+        free[7], new = pool, [3, 0, 20]
+    elif what == "gives back a bad page":
+        table[1][1] = -1
+    td, fd, ld, cd = dev(table), dev(free), dev(lens), dev([count])
+    p = B.kv_plan(dev(new), ld, td, fd, cd, page_size=page, max_tokens=cap)
+    assert int(p.status) == status
+    with pytest.raises(B.AttnError):
+        p.check()
+    assert td.tolist() == table and fd.tolist() == free
+    assert p.seqlens.tolist() == lens and p.free_count.tolist() == [count]
+    assert p.cu_seqlens.tolist() == [0, 0, 0, 0] and p.slots.tolist() == [-1] * cap
+
+
+# -------------------------------------------------------------------- append
+
+def runs(spec, page):
+    """Slots of (page number, first row, count) runs; None: a skipped token."""
+    out = []
+    for r in spec:
+        out += [-1] if r is None else list(range(r[0] * page + r[1], r[0] * page + r[1] + r[2]))
+    return out
+
+
+@pytest.mark.parametrize("dqk,dv", DIMS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("page,spec", [
+    (16, [(3, 0, 1)]),
+    (16, [(3, 15, 1), None, (0, 0, 16), (1, 0, 16), (2, 0, 5)]),
+    (16, [(i, 5, 1) for i in range(20)] + [None] * 14),
+    (32, [(0, 31, 1), (1, 0, 32), (5, 0, 32), (4, 7, 20), None, (2, 3, 1)]),
+    (256, [(1, 100, 156), (2, 0, 256), (0, 0, 3)]),
+])
+def test_append(B, dqk, dv, dtype, page, spec):
+    heads, pages = 3, 22
+    g = torch.Generator().manual_seed(dqk + page)
+    kc, ke = random_cache(pages, page, heads, dqk, g, 12)
+    vc, ve = random_cache(pages, page, heads, dv, g, 12)
+    slots = runs(spec, page)
+    n = len(slots)
+    k = torch.randn((n, heads, dqk), generator=g)
+    v = torch.randn((n, heads, dv), generator=g)
+    k = (k * 2.0 ** torch.randint(-12, 12, (n, 1, 1), generator=g)).to(dtype)
+    v = (v * 2.0 ** torch.randint(-3, 3, (n, heads, 1), generator=g)).to(dtype)
+    k[n // 2] = 0
+    v[0, 0] = 448.0                                   # exactly a scale's largest value
+    c = handle(B, kc, vc, ke, ve)
+    B.kv_append(k.cuda(), v.cuda(), dev(slots, torch.int64), c)
+    kv_ref.append(kc, ke, k, slots)
+    kv_ref.append(vc, ve, v, slots)
+    for name, got, ref in (("k", c.k, kc), ("v", c.v, vc), ("k_exp", c.k_exp, ke), ("v_exp", c.v_exp, ve)):
+        assert torch.equal(got.view(torch.uint8).cpu(), ref), name
+
+
+def test_append_odd_values(B):
+    """Zeros, NaN, infinities, subnormals, magnitudes past the scale range, and
+    scale bytes outside the format's range."""
+    g = torch.Generator().manual_seed(9)
+    kc, ke = random_cache(6, 16, 2, 64, g)
+    vc, ve = random_cache(6, 16, 2, 64, g)
+    ke[3], ve[3], ke[4] = 255, 0, 180
+    slots = runs([(0, 0, 2), (1, 4, 3), (2, 0, 1), (3, 2, 2), (4, 1, 1), (5, 0, 1)], 16)
+    n = len(slots)
+    k, v = torch.randn((n, 2, 64), generator=g), torch.randn((n, 2, 64), generator=g)
+    k[0], k[1] = 0.0, -0.0
+    k[2, 0, 5], k[3, 1, 7], v[2, :, :3] = math.nan, math.inf, -math.inf
+    k[5] = math.nan
+    k[6] *= 1e-38
+    v[6] *= 3e38
+    v[9] *= 1e-30
+    k, v = k.to(torch.bfloat16), v.to(torch.bfloat16)
+    c = handle(B, kc, vc, ke, ve)
+    B.kv_append(k.cuda(), v.cuda(), dev(slots, torch.int64), c)
+    kv_ref.append(kc, ke, k, slots)
+    kv_ref.append(vc, ve, v, slots)
+    nan = lambda x: (x & 127) == 127   # noqa: E731
+    for got, ref in ((c.k, kc), (c.v, vc)):
+        got = got.view(torch.uint8).cpu()
+        assert torch.equal(nan(got), nan(ref)) and torch.equal(got[~nan(ref)], ref[~nan(ref)])
+    assert torch.equal(c.k_exp.cpu(), ke) and torch.equal(c.v_exp.cpu(), ve)
+
+
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_append_runs_out_of_order(B, page):
+    """Tokens of several pages interleaved, a page filled backwards, gaps of up
+    to page_size - 1 skipped tokens inside a run, a run across CTA tiles."""
+    heads, d = 2, 64
+    g = torch.Generator().manual_seed(page)
+    slots = []
+    for i in range(8):                                    # pages 0 and 1 in turn, from rows 3 and 0
+        slots += [3 + i, page + i]
+    slots += list(range(3 * page - 1, 2 * page - 1, -1))   # page 2 backwards
+    for i in range(4):                                    # page 3 from row 2, as far apart as allowed
+        slots += [3 * page + 2 + i] + [-1] * (page - 1)
+    slots += list(range(4 * page + 1, 5 * page)) + [-1] * 40 + [5 * page + 7, 6 * page, 1 << 40, -5]
+    kc, ke = random_cache(7, page, heads, d, g, 10)
+    vc, ve = random_cache(7, page, heads, d, g, 10)
+    k, v = (torch.randn((len(slots), heads, d), generator=g).to(torch.bfloat16) for _ in range(2))
+    c = handle(B, kc, vc, ke, ve)
+    B.kv_append(k.cuda(), v.cuda(), dev(slots, torch.int64), c)
+    kv_ref.append(kc, ke, k, slots)
+    kv_ref.append(vc, ve, v, slots)
+    for got, ref in ((c.k, kc), (c.v, vc), (c.k_exp, ke), (c.v_exp, ve)):
+        assert torch.equal(got.view(torch.uint8).cpu(), ref)
+
+
+@pytest.mark.parametrize("tokens", [1, 300, 5000])
+def test_append_many_tokens_strided(B, tokens):
+    """A long prompt into pages in any order, k and v as slices of a packed
+    projection, the cache with its heads outside the rows, some tokens padded."""
+    page, heads, d = 64, 2, 128
+    g = torch.Generator().manual_seed(tokens)
+    pages = (tokens + page - 1) // page + 2
+    order = torch.randperm(pages, generator=g).tolist()
+    first = 37
+    slots = [order[(first + t) // page] * page + (first + t) % page for t in range(tokens)]
+    if tokens > 10:
+        for t in (3, 4, tokens - 1):
+            slots[t] = -1
+    kc, ke = random_cache(pages, page, heads, d, g)
+    vc, ve = random_cache(pages, page, heads, d, g)
+    kv = torch.randn((tokens, 2 * heads + 1, d), generator=g).to(torch.float16)
+    kvd = kv.cuda()
+    f8 = torch.float8_e4m3fn
+    kd, vd = (x.cuda().transpose(1, 2).contiguous().transpose(1, 2) for x in (kc, vc))
+    c = B.KvCache(kd.view(f8), vd.view(f8), ke.cuda(), ve.cuda())
+    B.kv_append(kvd[:, :heads], kvd[:, heads + 1:], dev(slots, torch.int64), c)
+    kv_ref.append(kc, ke, kv[:, :heads], slots)
+    kv_ref.append(vc, ve, kv[:, heads + 1:], slots)
+    for got, ref in ((kd, kc), (vd, vc), (c.k_exp, ke), (c.v_exp, ve)):
+        assert torch.equal(got.cpu(), ref)
+
+
+# -------------------------------------------------------------------- attend
+
+ATTEND = [
+    # page, lens (cached incl. new), new, heads (kv, per kv), mask, left, right
+    (16, [1], [1], 1, 1, 2, -1, -1),
+    (16, [0, 5, 16, 17], [1, 1, 1, 1], 2, 4, 2, -1, -1),
+    (32, [100, 0, 33, 700], [1, 0, 1, 1], 2, 1, 0, -1, -1),
+    (16, [1000, 257, 64], [1, 1, 1], 1, 16, 3, 100, 0),
+    (64, [300, 40], [7, 40], 2, 3, 2, -1, -1),
+    (16, [50, 3, 90], [5, 6, 33], 1, 5, 2, -1, -1),          # more queries than keys: rows that see nothing
+    (16, [50, 200, 90], [5, 16, 33], 2, 2, 3, 9, 2),
+    (16, [80, 70], [9, 4], 1, 2, 3, 0, 0),
+    (32, [60, 90], [60, 33], 2, 2, 1, -1, -1),               # top-left
+    (128, [500, 129], [3, 17], 1, 8, 0, -1, -1),             # cross attention
+    (16, [400, 200], [1, 1], 1, 33, 2, -1, -1),              # more heads in a group than one row tile
+    (256, [5000], [1], 2, 8, 2, -1, -1),
+    (16, [9000, 100], [1, 2], 1, 4, 2, -1, -1),              # many splits, and one
+]
+
+
+def attend_case(dqk, dv, dtype, page, lens, new, hkv, group, seed=0, q_scale=1.0):
+    g = torch.Generator().manual_seed(seed + dqk + page)
+    table, pool = block_table(lens, page, g)
+    kc, ke = random_cache(pool, page, hkv, dqk, g)
+    vc, ve = random_cache(pool, page, hkv, dv, g)
+    q = (torch.randn((sum(new), hkv * group, dqk), generator=g) * q_scale).to(dtype)
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    return q, table, kc, vc, ke, ve, cu
+
+
+@pytest.mark.parametrize("dqk,dv", DIMS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("page,lens,new,hkv,group,mask,left,right", ATTEND)
+def test_attend(B, dqk, dv, dtype, page, lens, new, hkv, group, mask, left, right):
+    q, table, kc, vc, ke, ve, cu = attend_case(dqk, dv, dtype, page, lens, new, hkv, group)
+    scale = dqk ** -0.5
+    o, lse = B.attn_kv_forward(q.cuda(), handle(B, kc, vc, ke, ve), dev(table), dev(lens), dev(cu), scale=scale,
+                               mask=mask, left=left, right=right, max_seqlen_q=max(new), max_seqlen_k=max(lens),
+                               check_status=True)
+    ref = kv_ref.attend(q, cu, lens, table, kc, vc, ke, ve, scale, mask, left, right)
+    check_attend(o, lse, ref, dtype, dqk, max(lens), what=f"{page} {lens} {new}")
+
+
+@pytest.mark.parametrize("scale", [-0.1, 3.0, 1e-6])
+def test_attend_scales(B, scale):
+    """Negative, large (one key takes all) and tiny softmax scales; q rows of
+    very different magnitudes, one of them zero."""
+    q, table, kc, vc, ke, ve, cu = attend_case(128, 128, torch.bfloat16, 16, [333, 50], [1, 3], 2, 4)
+    q = (q.float() * (2.0 ** torch.tensor([-40, 0, 3, -120])).view(4, 1, 1)).to(torch.bfloat16)
+    q[1, 3] = 0
+    o, lse = B.attn_kv_forward(q.cuda(), handle(B, kc, vc, ke, ve), dev(table), dev([333, 50]), dev(cu), scale=scale,
+                               max_seqlen_q=3, max_seqlen_k=400, check_status=True)
+    ref = kv_ref.attend(q, cu, [333, 50], table, kc, vc, ke, ve, scale, 2)
+    check_attend(o, lse, ref, torch.bfloat16, 128, 333)
+
+
+def test_attend_scale_extremes(B):
+    """Pages at both ends of the scale range next to each other, and a page of
+    tiny values that takes nearly all the weight."""
+    lens, new = [16 * 12], [1]
+    q, table, kc, vc, ke, ve, cu = attend_case(64, 64, torch.float16, 16, lens, new, 1, 2)
+    ve[table[0][3]], ve[table[0][4]], ve[table[0][5]], ve[table[0][9]] = 157, 97, 255, 0
+    ke[table[0][4]], ke[table[0][7]] = 127 - 5, 97
+    o, lse = B.attn_kv_forward(q.cuda(), handle(B, kc, vc, ke, ve), dev(table), dev(lens), dev(cu), scale=0.125,
+                               max_seqlen_q=1, max_seqlen_k=192)
+    ref = kv_ref.attend(q, cu, lens, table, kc, vc, ke, ve, 0.125, 2)
+    huge = ref[0].abs() > 65504 * (1 + 2.0 ** -11)
+    assert bool(huge.any())                      # fp16 outputs overflow there, as they should
+    assert bool(torch.isinf(o.cpu()[huge]).all())
+    ve[table[0][3]], ve[table[0][5]] = 127, 120
+    o, lse = B.attn_kv_forward(q.cuda(), handle(B, kc, vc, ke, ve), dev(table), dev(lens), dev(cu), scale=0.125,
+                               max_seqlen_q=1, max_seqlen_k=192)
+    check_attend(o, lse, kv_ref.attend(q, cu, lens, table, kc, vc, ke, ve, 0.125, 2), torch.float16, 64, 192)
+
+
+@pytest.mark.parametrize("dqk,dv", DIMS)
+def test_attend_ignores_what_it_must_not_see(B, dqk, dv):
+    """NaN bytes in cache rows past the length, outside a single token's window
+    and in other pages; block-table entries past the length point anywhere."""
+    lens, new, page = [37, 100, 64], [1, 1, 1], 32
+    q, table, kc, vc, ke, ve, cu = attend_case(dqk, dv, torch.bfloat16, page, lens, new, 2, 2)
+    ref = kv_ref.attend(q, cu, lens, table, kc, vc, ke, ve, 0.1, 3, 20, 0)
+    for b, n in enumerate(lens):
+        for j in range(n):
+            if j < n - 21:
+                kc[table[b][j // page], j % page] = 127
+                vc[table[b][j // page], j % page] = 255
+        last = table[b][(n - 1) // page]
+        if n % page:
+            kc[last, n % page:], vc[last, n % page:] = 255, 127
+        for j in range((n + page - 1) // page, len(table[b])):
+            table[b][j] = 10 ** 9 if j % 2 else -5
+    used = {p for b, n in enumerate(lens) for p in table[b][: (n + page - 1) // page]}
+    for p in range(kc.shape[0]):
+        if p not in used:
+            kc[p], vc[p] = 127, 127
+    o, lse = B.attn_kv_forward(q.cuda(), handle(B, kc, vc, ke, ve), dev(table), dev(lens), dev(cu), scale=0.1, mask=3,
+                               left=20, right=0, max_seqlen_q=1, max_seqlen_k=128, check_status=True)
+    check_attend(o, lse, ref, torch.bfloat16, dqk, 100)
+
+
+def test_attend_layouts_and_padding(B):
+    """q and o as slices of wider tensors, the cache with heads outside the
+    rows, padded segment starts; rows of no segment stay as they were."""
+    lens, new, page, hkv, group, d = [90, 30, 200], [2, 5, 1], 16, 2, 4, 128
+    q, table, kc, vc, ke, ve, cu = attend_case(d, d, torch.bfloat16, page, lens, new, hkv, group)
+    starts, total = [3, 6, 20, 25], 25
+    wide = torch.randn((total, hkv * group + 3, d), dtype=torch.bfloat16, device="cuda")
+    for b in range(3):
+        wide[starts[b]:starts[b] + new[b], 1:1 + hkv * group] = q[cu[b]:cu[b + 1]].cuda()
+    f8 = torch.float8_e4m3fn
+    kd, vd = (x.cuda().transpose(1, 2).contiguous().transpose(1, 2).view(f8) for x in (kc, vc))
+    ow = torch.full((total, hkv * group + 2, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((hkv * group, total), 5.0, device="cuda")
+    B.attn_kv_forward(wide[:, 1:1 + hkv * group], B.KvCache(kd, vd, ke.cuda(), ve.cuda()), dev(table), dev(lens), dev(cu),
+                      scale=0.1, max_seqlen_q=5, max_seqlen_k=200, cu_seqlens_q_padded=dev(starts),
+                      out=(ow[:, 1:-1], lse), check_status=True)
+    ref = kv_ref.attend(q, cu, lens, table, kc, vc, ke, ve, 0.1, 2)
+    rows = [starts[b] + i for b in range(3) for i in range(new[b])]
+    check_attend(ow[rows][:, 1:-1], lse[:, rows], ref, torch.bfloat16, d, 200)
+    others = [r for r in range(total) if r not in rows]
+    assert bool((ow[others] == 7).all()) and bool((lse[:, others] == 5).all())
+    assert bool((ow[:, 0] == 7).all()) and bool((ow[:, -1] == 7).all())
+
+
+def test_attend_reports_bad_lengths_and_pages(B):
+    lens, new, page = [90, 30], [1, 1], 16
+    q, table, kc, vc, ke, ve, cu = attend_case(64, 64, torch.bfloat16, page, lens, new, 1, 2)
+    c, qd = handle(B, kc, vc, ke, ve), q.cuda()
+    kw = dict(scale=0.1, max_seqlen_q=1, max_seqlen_k=96, check_status=True)
+    B.attn_kv_forward(qd, c, dev(table), dev(lens), dev(cu), **kw)
+    for bad_cu in ([0, 1, 3], [0, -1, 0], [-1, 0, 1]):
+        with pytest.raises(B.AttnError) as e:
+            B.attn_kv_forward(qd, c, dev(table), dev(lens), dev(bad_cu), **kw)
+        assert e.value.status == B.ATTN_ERR_BAD_SEQLENS
+    for bad in ([97, 30], [90, -1], [2 ** 31 - 1, 30]):
+        with pytest.raises(B.AttnError) as e:
+            B.attn_kv_forward(qd, c, dev(table), dev(bad), dev(cu), **kw)
+        assert e.value.status == B.ATTN_ERR_BAD_SEQLENS
+    # tokens of a page outside the cache are masked, the other request is untouched
+    hole = [list(r) for r in table]
+    hole[0][2] = kc.shape[0]
+    with pytest.raises(B.AttnError) as e:
+        B.attn_kv_forward(qd, c, dev(hole), dev(lens), dev(cu), **kw)
+    assert e.value.status == B.ATTN_ERR_BAD_PAGE
+    kw["check_status"] = False
+    o, lse = B.attn_kv_forward(qd, c, dev(hole), dev(lens), dev(cu), **kw)
+    k2, v2 = kc.clone(), vc.clone()
+    ref = kv_ref.attend(q, cu, [0, 30], table, k2, v2, ke, ve, 0.1, 2)
+    check_attend(o[1:], lse[:, 1:], tuple(x[1:] if i in (0, 2) else x[:, 1:] for i, x in enumerate(ref)),
+                 torch.bfloat16, 64, 90)
+    short = [table[0][:2] + table[0][3:], table[1]]
+    ref = kv_ref.attend(q, cu, [74, 30], short, kc, vc, ke, ve, 0.1, 2)
+    check_attend(o, lse, ref, torch.bfloat16, 64, 90)
+
+
+def test_attend_repeats_and_streams(B):
+    """The same bits on every run, from two calls in flight on two streams, and
+    from a captured graph replayed on new lengths."""
+    lens, new = [3000, 1500, 7], [1, 1, 1]
+    q, table, kc, vc, ke, ve, cu = attend_case(128, 128, torch.bfloat16, 16, lens, new, 2, 4)
+    c, qd, td, ld, cud = handle(B, kc, vc, ke, ve), q.cuda(), dev(table), dev(lens), dev(cu)
+    kw = dict(scale=0.1, max_seqlen_q=1, max_seqlen_k=3008)
+    want = B.attn_kv_forward(qd, c, td, ld, cud, **kw)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (s1, s2):
+        s.wait_stream(torch.cuda.current_stream())
+    got = [B.attn_kv_forward(qd, c, td, ld, cud, stream=s, **kw) for _ in range(4) for s in (s1, s2)]
+    torch.cuda.synchronize()
+    for o, lse in got:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    out = (torch.zeros_like(want[0]), torch.zeros_like(want[1]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.attn_kv_forward(qd, c, td, ld, cud, out=out, **kw)
+    graph.replay()
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+    ld.copy_(dev([100, 900, 0]))
+    graph.replay()
+    ref = kv_ref.attend(q, cu, [100, 900, 0], table, kc, vc, ke, ve, 0.1, 2)
+    check_attend(*out, ref, torch.bfloat16, 128, 900)
+
+
+# ------------------------------------------------------- the step they make up
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_serving_steps(B, graph):
+    """plan -> rope -> append -> attend over several steps: prompts, decoding,
+    a request that leaves and one that takes its pages; every step's cache
+    bytes, bookkeeping and attention against the oracle's.  Captured, the same
+    graph replays each step on new inputs."""
+    page, hkv, group, d, batch, pool, cols, cap = 16, 2, 4, 64, 3, 14, 8, 64
+    dtype, scale = torch.bfloat16, 64 ** -0.5
+    g = torch.Generator().manual_seed(11)
+    steps = [[20, 0, 33], [1, 17, 1], [1, 1, 1], [-1, 2, 1], [40, 1, 0], [1, 1, -1], [0, 1, 0]]
+    f, axis = B.rope_frequencies(d), (torch.arange(d // 2) % 2).to(torch.uint8)
+    # the oracle's state and the device's
+    lens, table, free, count = [0] * batch, [[-1] * cols for _ in range(batch)], list(range(pool)), pool
+    kc, vc = (torch.zeros((pool, page, hkv, d), dtype=torch.uint8) for _ in range(2))
+    ke, ve = (torch.full((pool, hkv), 127, dtype=torch.uint8) for _ in range(2))
+    c = handle(B, kc, vc, ke, ve)
+    td, fd, ld, cd, nd = dev(table), dev(free), dev(lens), dev([count]), dev([0] * batch)
+    qd = torch.zeros((cap, hkv * group, d), dtype=dtype, device="cuda")
+    kd, vd = (torch.zeros((cap, hkv, d), dtype=dtype, device="cuda") for _ in range(2))
+    hd = torch.zeros(cap, dtype=I32, device="cuda")          # a second axis, from the program
+    out = B.KvPlan(torch.empty(batch + 1, dtype=I32, device="cuda"), ld, torch.empty(cap, dtype=I32, device="cuda"),
+                   torch.empty(cap, dtype=torch.int64, device="cuda"), cd, dev([0]))
+    both = torch.empty((2, cap), dtype=I32, device="cuda")
+
+    def step():
+        p = B.kv_plan(nd, ld, td, fd, cd, page_size=page, max_tokens=cap, out=out)
+        both[0].copy_(p.positions)
+        both[1].copy_(hd)
+        rq, rk = B.rope(qd, kd, both, f, pair_axis=axis)
+        B.kv_append(rk, vd, p.slots, c)
+        o, lse = B.attn_kv_forward(rq, c, td, p.seqlens, p.cu_seqlens, scale=scale, max_seqlen_q=48,
+                                   max_seqlen_k=cols * page)
+        return rq, rk, o, lse
+
+    if graph:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            held = step()
+    for new in steps:
+        n = sum(max(x, 0) for x in new)
+        q = torch.randn((cap, hkv * group, d), generator=g).to(dtype)
+        k, v = (torch.randn((cap, hkv, d), generator=g).to(dtype) for _ in range(2))
+        h2 = torch.randint(0, 9, (cap,), generator=g, dtype=I32)
+        for dst, src in ((qd, q), (kd, k), (vd, v), (hd, h2), (nd, torch.tensor(new, dtype=I32))):
+            dst.copy_(src)
+        if graph:
+            gr.replay()
+            rq, rk, o, lse = held
+        else:
+            rq, rk, o, lse = step()
+        torch.cuda.synchronize()
+        out.check()
+        cu, lens, pos, slots, count = kv_ref.plan(new, lens, table, free, count, page, cap)
+        assert ld.tolist() == lens and cd.tolist() == [count] and td.tolist() == table and out.slots.tolist() == slots
+        pp = torch.stack([torch.tensor(pos, dtype=I32), h2])
+        for x, got in ((q, rq), (k, rk)):
+            ref = kv_ref.rope(x, pp, f, axis)
+            assert float((got.cpu().to(torch.float64) - ref).abs().max()) <= 2.0 ** -8 * 6   # half a step below 6
+        # from the device's own rounded keys and queries on, so that both sides store the same bytes
+        kv_ref.append(kc, ke, rk.cpu(), slots)
+        kv_ref.append(vc, ve, v, slots)
+        for got, ref in ((c.k, kc), (c.v, vc), (c.k_exp, ke), (c.v_exp, ve)):
+            assert torch.equal(got.view(torch.uint8).cpu(), ref)
+        if n:
+            ref = kv_ref.attend(rq.cpu()[:n], cu, lens, table, kc, vc, ke, ve, scale, 2)
+            check_attend(o[:n], lse[:, :n], ref, dtype, d, max(lens))
