@@ -122,8 +122,8 @@ __device__ __forceinline__ void append_run(const Run& r, const T* x, long long x
 
 // A CTA takes the runs that start in its tile of tokens (at most 32), all
 // heads and both sides of each, one (run, head, side) per warp at a time.  A
-// run is found by its page: it starts at a token whose page no token among the
-// page_size - 1 before it has, and ends where page_size tokens in a row have
+// run is found by its page: it starts at a token whose page none of the
+// page_size tokens before it has, and ends where page_size tokens in a row have
 // another.
 template <typename T, int DQK, int DV>
 __global__ void __launch_bounds__(NTHREADS) append_kernel(const Args A) {
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(NTHREADS) append_kernel(const Args A) {
   for (; maybe; maybe &= maybe - 1) {
     const int l = __ffs(maybe) - 1, page = __shfl_sync(0xffffffffu, mine, l);
     bool seen = false;
-    for (int j = 2 + lane; j < size; j += 32) seen |= page_at(t0 + l - j) == page;
+    for (int j = 2 + lane; j <= size; j += 32) seen |= page_at(t0 + l - j) == page;
     if (!__any_sync(0xffffffffu, seen)) starts |= 1u << l;
   }
   const int per_run = A.c.hkv * 2;
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(NTHREADS) append_kernel(const Args A) {
       page = page_at(t);
       int n = 0, first = size, last = t;
       __syncwarp();
-      for (int base = t; n < size && base < A.tokens && base - last < size; base += 32) {
+      for (int base = t; n < size && base < A.tokens && base - last <= size; base += 32) {
         const long long s = slot_at(base + lane);
         const bool same = s >= 0 && (int)(s >> shift) == page;
         const uint32_t all = __ballot_sync(0xffffffffu, same);
@@ -214,7 +214,7 @@ static int run(const attn_kv_append_params* p, cudaStream_t st) {
   a.v = p->v;
   a.slots = p->slots;
   a.tokens = p->tokens;
-  a.tile = 16;
+  a.tile = p->tokens <= 4096 ? 1 : 16;
   const int grid = cdiv(p->tokens, a.tile);
   if (p->dtype == ATTN_BF16) launch<__nv_bfloat16>(a, p->cache.d_qk, p->cache.d_v, grid, st);
   else launch<__half>(a, p->cache.d_qk, p->cache.d_v, grid, st);

@@ -4,25 +4,28 @@
 //
 // Decoding reads every visible cache byte once and does 4 Hq / Hkv flops per
 // byte: bound by memory, far from the tensor cores' rate.  So the query rows
-// that share a kv head (tokens x Hq / Hkv, in tiles of 16) meet the cache in
-// warp-level m16n8k16 products, and the work is laid out for the loads:
+// that share a kv head (tokens x Hq / Hkv, in tiles of 8 or 16) meet the cache
+// in warp-level m16n8k16 products, and the work is laid out for the loads:
 //
-// * A CTA owns one tile of 16 rows, one kv head and one split of the keys; its
-//   four warps take 16-key tiles in turn, each with a ring of its own that
-//   16-byte asynchronous copies keep full.  No barrier joins the warps until
-//   the end.  A tile lies in one page, so its scales are uniform.
+// * A CTA owns one row tile, one kv head and one split of the keys; its four
+//   warps take 16-key tiles in turn, each with a ring of its own that 16-byte
+//   asynchronous copies keep full.  No barrier joins the warps until the end.
+//   A tile lies in one page, so its scales are uniform.
+// * The products are transposed, S^T = K Q^T and O^T = V^T P^T: the 16-row side
+//   of the instruction holds keys and value columns, the 8-column side the few
+//   query rows.  S^T becomes the operand P^T by one 8 x 8 transposition per
+//   eight keys inside the warp.
 // * e4m3 is exact in fp16.  The contraction's order is free, so a lane takes
 //   16 consecutive bytes of a K row as its share of four k-steps and 16
-//   consecutive bytes of four V rows as its share of 16 column tiles: wide
-//   conflict-free shared loads, no transposition, one conversion per two
-//   values.
+//   consecutive bytes of four V rows as its share of eight column tiles: wide
+//   conflict-free shared loads, one conversion per two values.
 // * q goes to fp16 under a power-of-two scale per row (largest magnitude in
 //   [2^14, 2^15)), which is exact for bf16 too unless an element is 2^-28 of
-//   its row's largest.  P is fp16 with its running maximum at 2^8: 11 bits down
-//   to 2^-22 of the row's maximum, 2^-32 reached.  Scores, maxima, sums and O
+//   its row's largest.  P is fp16 with its running maximum at 2^4: 11 bits down
+//   to 2^-18 of the row's maximum, 2^-28 reached.  Scores, maxima, sums and O
 //   are fp32.
-// * The accumulator is held in units of the current page's V scale and
-//   multiplied by the exact ratio where the scale changes.
+// * The accumulator is held in units of one V scale; a page whose scale is
+//   within 2^4 of it has its ratio put on P (exact), others move the unit.
 //
 // Splits leave (O, max, sum) in the workspace; a second small kernel joins
 // them in a fixed order.
@@ -37,23 +40,27 @@ namespace kvfwd {
 
 constexpr int NWARPS = 4;
 constexpr int NTHREADS = 32 * NWARPS;
-constexpr int ROWS = 16;            // query rows of a CTA
 constexpr int TILE = 16;            // keys of a warp's step
 constexpr int MAX_TILES = 256;      // tiles of a split: its page table fits shared memory
 constexpr int MIN_TILES = 16;       // a split is worth at least this many
 constexpr int SMS = 152;
-constexpr float P_LOG2 = 8.f;       // P = 2^8 at the running maximum
-constexpr float SLACK_LOG2 = 7.f;   // growth of the maximum that is let pass: P <= 2^15
+constexpr int EV_SLACK = 4;         // V scales within 2^4 of the accumulator's unit go on P
+constexpr float P_LOG2 = 4.f;       // P = 2^4 at the running maximum
+constexpr float SLACK_LOG2 = 7.f;   // growth of the maximum that is let pass: P <= 2^(4 + 7 + 4)
 
-template <int DQK, int DV>
+// NT: query rows of a CTA in units of 8.
+template <int DQK, int DV, int NT>
 struct Cfg {
+  static constexpr int ROWS = 8 * NT;
   static constexpr int KB = TILE * DQK, VB = TILE * DV;
   static constexpr int STAGE = KB + VB;
-  static constexpr int NST = STAGE <= 2048 ? 6 : STAGE <= 5120 ? 4 : 3;
+  static constexpr int NST = STAGE <= 2048 ? 6 : 3;
   static constexpr int RING = NST * STAGE;
   static constexpr int OFF_META = NWARPS * RING;                       // int2[MAX_TILES + 1]: page, exponents
   static constexpr int OFF_ML = OFF_META + (MAX_TILES + 1) * 8;        // float[2][NWARPS][ROWS]
   static constexpr int SMEM = OFF_ML + 2 * NWARPS * ROWS * 4 + 8;
+  // CTAs per SM that the registers have to allow (shared memory allows them too)
+  static constexpr int RESIDENT = NT == 1 ? (DQK == 256 ? 2 : DQK == 192 ? 3 : 4) : (DQK == 256 ? 1 : DQK == 192 ? 2 : 3);
   static_assert(NWARPS * ROWS * DV * 4 <= NWARPS * RING, "the join of the warps reuses the rings");
 };
 
@@ -73,8 +80,8 @@ struct Args {
   int mask, left, right;
   float scale_log2;
   int nsplit, split_tiles, mtiles;
-  float* part_o;         // [job][nsplit][ROWS][DV]
-  float2* part_ml;       // [job][nsplit][ROWS]
+  float* part_o;         // [job][nsplit][rows][DV]
+  float2* part_ml;       // [job][nsplit][rows]
   int* status;           // [batch][nsplit]
   KvCacheView c;
 };
@@ -89,6 +96,7 @@ struct Job {
   bool bad;              // lengths outside the declared bounds
 };
 
+template <int ROWS>
 __device__ __forceinline__ Job make_job(const Args& A, int b, int m, MaskArgs& mk) {
   Job j;
   const int a = __ldg(A.cu_q + b);
@@ -179,9 +187,35 @@ template <> __device__ __forceinline__ uint32_t pack_t2<__nv_bfloat16>(float a, 
 }
 template <> __device__ __forceinline__ uint32_t pack_t2<__half>(float a, float b) { return pack_h2(a, b); }
 
-template <int DQK, int DV, typename T>
-__global__ void __launch_bounds__(NTHREADS) kv_fwd_kernel(const Args A) {
-  using C = Cfg<DQK, DV>;
+// Four columns of a finished row: O / l, and with the first ones the LSE.
+template <typename T>
+__device__ __forceinline__ void store_row(const Args& A, const Job& J, int hk, int row, int c, const float4& v, float top,
+                                          float l) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int tk = (J.row0 + row) / A.g, h = hk * A.g + J.row0 + row - tk * A.g;
+  T* dst = static_cast<T*>(A.o) + elem_off(A.so, (long long)J.q0 + tk, h) + c;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_t2<T>(v.x * inv, v.y * inv), pack_t2<T>(v.z * inv, v.w * inv));
+  if (c == 0)
+    A.lse[(long long)h * A.total_q + J.q0 + tk] =
+        l == 0.f ? -INFINITY : (top - P_LOG2 + log2f(l)) * 0.6931471805599453f;
+}
+
+// An 8 x 8 matrix of 16-bit values, a row over four lanes, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
+  const __half2 h = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int DQK, int DV, int NT, typename T>
+__global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_kernel(const Args A) {
+  using C = Cfg<DQK, DV, NT>;
+  constexpr int ROWS = C::ROWS;
   extern __shared__ __align__(128) uint8_t smem[];
   int2* meta = reinterpret_cast<int2*>(smem + C::OFF_META);
   float* s_m = reinterpret_cast<float*>(smem + C::OFF_ML);
@@ -198,7 +232,7 @@ __global__ void __launch_bounds__(NTHREADS) kv_fwd_kernel(const Args A) {
   x /= A.nsplit;
   const int hk = x % A.c.hkv, b = x / A.c.hkv;
   MaskArgs mk;
-  const Job J = make_job(A, b, m, mk);
+  const Job J = make_job<ROWS>(A, b, m, mk);
   const bool reports = hk == 0 && m == 0;   // one CTA per (request, split) says what it found
   if (tid == 0) *s_bad = 0;
   const int tile0 = split * A.split_tiles;
@@ -228,15 +262,17 @@ __global__ void __launch_bounds__(NTHREADS) kv_fwd_kernel(const Args A) {
     }
   }
 
-  // this lane's rows g and g + 8 of q, as fp16 under a power of two per row
-  uint32_t qa[DQK / 16][4];
-  float rs[2];
-  int tok[2];
+  // row g of each row group of q, as fp16 under a power of two; a negative
+  // softmax scale goes into its sign, so scores and their factors order alike
+  uint32_t qb[NT][DQK / 16][2];
+  float rs[NT][2];                       // log2 units per raw score of rows 2t, 2t + 1
+  int tok[NT][2];
+  const float sign = A.scale_log2 < 0.f ? -1.f : 1.f;
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int row = min(J.row0 + g + 8 * r, J.row0 + J.nrow - 1);   // rows past the end repeat the last
-    tok[r] = row / A.g;
-    const T* qp = static_cast<const T*>(A.q) + elem_off(A.sq, (long long)J.q0 + tok[r], hk * A.g + row - tok[r] * A.g);
+  for (int n = 0; n < NT; ++n) {
+    const int row = min(J.row0 + 8 * n + g, J.row0 + J.nrow - 1);   // rows past the end repeat the last
+    const int i = row / A.g;
+    const T* qp = static_cast<const T*>(A.q) + elem_off(A.sq, (long long)J.q0 + i, hk * A.g + row - i * A.g);
     uint4 raw[DQK / 32];
     float mx = 0.f;
 #pragma unroll
@@ -258,177 +294,209 @@ __global__ void __launch_bounds__(NTHREADS) kv_fwd_kernel(const Args A) {
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     int e = (int)(__float_as_uint(mx) >> 23) - 127;
     e = e == 128 ? 14 : max(e, -100);      // infinities stay what they are
-    const float up = exp2_int(14 - e);
-    rs[r] = A.scale_log2 * exp2_int(e - 14);
+    const float up = sign * exp2_int(14 - e);
+    const float unit = fabsf(A.scale_log2) * exp2_int(e - 14);
 #pragma unroll
     for (int i = 0; i < DQK / 32; ++i) {
       const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {        // 16 elements of two pieces: k-step 4 (i / 2) + 2 (i & 1) + k / 2
+      for (int k = 0; k < 4; ++k) {        // 16 elements in two pieces: k-step 4 (i / 2) + 2 (i & 1) + k / 2
         const float2 f = up2<T>(w[k]);
-        qa[(i >> 1) * 4 + (i & 1) * 2 + (k >> 1)][(k & 1) * 2 + r] = pack_h2(f.x * up, f.y * up);
+        qb[n][(i >> 1) * 4 + (i & 1) * 2 + (k >> 1)][k & 1] = pack_h2(f.x * up, f.y * up);
       }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {          // row 2t + r is lane group 2t + r's
+      rs[n][r] = __shfl_sync(0xffffffffu, unit, (2 * t + r) * 4);
+      tok[n][r] = min(J.row0 + 8 * n + 2 * t + r, J.row0 + J.nrow - 1) / A.g;
     }
   }
   __syncthreads();
 
   const uint32_t ring = ptx::smem_u32(smem) + warp * C::RING;
   const int shift = A.c.page_shift, in_page = (1 << shift) - 1;
-  auto fetch = [&](int i) {   // tile i of the split into its stage; always one group
+  const uint8_t* kbase = A.c.k + hk * A.c.sk.h;
+  const uint8_t* vbase = A.c.v + hk * A.c.sv.h;
+  // the rows of a tile in 16-byte pieces, piece lane + 32 k for the k-th copy of
+  // a lane: with whole rows per 32 pieces only the row moves, by a fixed step
+  const long long klane = (lane / (DQK / 16)) * A.c.sk.r + lane % (DQK / 16) * 16;
+  const long long vlane = (lane / (DV / 16)) * A.c.sv.r + lane % (DV / 16) * 16;
+  auto fetch = [&](int i, uint32_t st) {   // tile i of the split into the stage at st; always one group
     if (i < ntile) {
       const int key = key0 + i * TILE;
       const int page = meta[(key >> shift) - page0].x;
       if (page >= 0) {
-        const uint32_t st = ring + ((i / NWARPS) % C::NST) * C::STAGE;
-        const uint8_t* ks = A.c.k + page * A.c.sk.p + hk * A.c.sk.h + (key & in_page) * A.c.sk.r;
-        const uint8_t* vs = A.c.v + page * A.c.sv.p + hk * A.c.sv.h + (key & in_page) * A.c.sv.r;
+        const uint8_t* ks = kbase + page * A.c.sk.p + (key & in_page) * A.c.sk.r;
+        const uint8_t* vs = vbase + page * A.c.sv.p + (key & in_page) * A.c.sv.r;
+        const bool inside = key >= J.klo && key + TILE - 1 <= J.khi;
 #pragma unroll
         for (int k = 0; k < DQK / 32; ++k) {
           const int n = lane + 32 * k, r = n / (DQK / 16), c = n % (DQK / 16);
-          const bool in = key + r >= J.klo && key + r <= J.khi;   // the rest reads as zero
-          cp_async16(st + k_off<DQK>(r, c), in ? ks + r * A.c.sk.r + c * 16 : ks, in ? 16 : 0);
+          const uint8_t* src = 32 % (DQK / 16) == 0 ? ks + klane + (32 / (DQK / 16)) * k * A.c.sk.r
+                                                    : ks + r * A.c.sk.r + c * 16;
+          const bool in = inside || (key + r >= J.klo && key + r <= J.khi);   // the rest reads as zero
+          cp_async16(st + k_off<DQK>(r, c), in ? src : ks, in ? 16 : 0);
         }
 #pragma unroll
         for (int k = 0; k < DV / 32; ++k) {
           const int n = lane + 32 * k, r = n / (DV / 16), c = n % (DV / 16);
-          const bool in = key + r >= J.klo && key + r <= J.khi;
-          cp_async16(st + C::KB + v_off<DV>(r, c), in ? vs + r * A.c.sv.r + c * 16 : vs, in ? 16 : 0);
+          const bool in = inside || (key + r >= J.klo && key + r <= J.khi);
+          cp_async16(st + C::KB + v_off<DV>(r, c), in ? vs + vlane + (32 / (DV / 16)) * k * A.c.sv.r : vs, in ? 16 : 0);
         }
       }
     }
     cp_commit();
   };
 
-  float o[DV / 8][4];
+  constexpr int MT = DV / 16;     // tiles of 16 value columns
+  float o[NT][MT][4];
+  float mrow[NT][2], lrow[NT][2];
 #pragma unroll
-  for (int j = 0; j < DV / 8; ++j)
+  for (int n = 0; n < NT; ++n) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
-  float mrow[2] = {-INFINITY, -INFINITY}, lrow[2] = {0.f, 0.f};
-  int ev = 0;
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[n][j][k] = 0.f;
+    mrow[n][0] = mrow[n][1] = -INFINITY;
+    lrow[n][0] = lrow[n][1] = 0.f;
+  }
+  int unit = 0;                   // the accumulator counts in 2^unit
   const int itok0 = J.row0 / A.g, itok1 = (J.row0 + J.nrow - 1) / A.g;
 
+  uint32_t st_in = ring, st_out = ring;
+  auto next = [&](uint32_t st) { return st + C::STAGE == ring + C::RING ? ring : st + C::STAGE; };
 #pragma unroll
-  for (int s = 0; s < C::NST - 1; ++s) fetch(warp + s * NWARPS);
+  for (int s = 0; s < C::NST - 1; ++s) {
+    fetch(warp + s * NWARPS, st_in);
+    st_in = next(st_in);
+  }
   for (int i = warp; i < ntile; i += NWARPS) {
-    fetch(i + (C::NST - 1) * NWARPS);
+    fetch(i + (C::NST - 1) * NWARPS, st_in);
+    st_in = next(st_in);
     cp_wait<C::NST - 1>();
     __syncwarp();
     const int key = key0 + i * TILE;
     const int2 mt = meta[(key >> shift) - page0];
+    const uint32_t st = st_out;
+    st_out = next(st_out);
     if (mt.x >= 0) {
-      const uint32_t st = ring + ((i / NWARPS) % C::NST) * C::STAGE;
-      // S = Q K^T: column n of tile j is key 8 j + n
-      float s[2][4];
+      // S^T = K Q^T: keys g and g + 8, rows 2t and 2t + 1
+      float s[NT][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s[j][k] = 0.f;
-      }
+        for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
 #pragma unroll
       for (int c = 0; c < DQK / 64; ++c) {
         const uint4 w0 = lds128(st + k_off<DQK>(g, t + 4 * c)), w1 = lds128(st + k_off<DQK>(8 + g, t + 4 * c));
         const uint32_t a0[4] = {w0.x, w0.y, w0.z, w0.w}, a1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          mma16816(s[0], qa[4 * c + k], e4m3x2_to_h2((uint16_t)a0[k]), e4m3x2_to_h2((uint16_t)(a0[k] >> 16)));
-          mma16816(s[1], qa[4 * c + k], e4m3x2_to_h2((uint16_t)a1[k]), e4m3x2_to_h2((uint16_t)(a1[k] >> 16)));
+          const uint32_t a[4] = {e4m3x2_to_h2((uint16_t)a0[k]), e4m3x2_to_h2((uint16_t)a1[k]),
+                                 e4m3x2_to_h2((uint16_t)(a0[k] >> 16)), e4m3x2_to_h2((uint16_t)(a1[k] >> 16))};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816(s[n], a, qb[n][4 * c + k][0], qb[n][4 * c + k][1]);
         }
       }
-      // scores in log2 units, masked ones -inf
       const float ks = exp2_int((int)(short)(mt.y & 0xffff));
-      const float f[2] = {rs[0] * ks, rs[1] * ks};
       const bool full = key >= J.klo && key + TILE - 1 <= J.khi &&
                         (mk.right < 0 || key + TILE - 1 <= (long long)itok0 + mk.off + mk.right) &&
                         (mk.left < 0 || key >= (long long)itok1 + mk.off - mk.left);
+      if (!full) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          s[j][k] *= f[k >> 1];
-          if (!full) {
-            const int kk = key + 8 * j + 2 * t + (k & 1);
-            if (kk < J.klo || kk > J.khi || !sees(mk, tok[k >> 1], kk)) s[j][k] = -INFINITY;
+          for (int k = 0; k < 4; ++k) {
+            const int kk = key + g + 8 * (k >> 1);
+            if (kk < J.klo || kk > J.khi || !sees(mk, tok[n][k & 1], kk)) s[n][k] = -INFINITY;
           }
-        }
-      bool grow = false;
-      float top[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        top[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-        grow |= top[r] > mrow[r] + SLACK_LOG2;
       }
-      const int ev_new = mt.y >> 16;
-      grow = __any_sync(0xffffffffu, grow);
-      if (grow || ev_new != ev) {
-        float a[2];
-        const float de = exp2_int(ev - ev_new);
+      bool grow = false;
+      float f[NT][2], top[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          a[r] = 1.f;
-          if (grow) {
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-            if (top[r] > mrow[r]) {
-              a[r] = fast_exp2(mrow[r] - top[r]);   // 0 from -inf
-              mrow[r] = top[r];
-            }
-          }
-          lrow[r] *= a[r];
-          a[r] *= de;
+          f[n][r] = fmaxf(rs[n][r] * ks, 1.17549435e-38f);   // never 0: a masked score stays -inf
+          top[n][r] = fmaxf(s[n][r], s[n][2 + r]) * f[n][r];
+          grow |= top[n][r] > mrow[n][r] + SLACK_LOG2;
         }
-        ev = ev_new;
+      const int ev = mt.y >> 16;
+      grow = __any_sync(0xffffffffu, grow);
+      if (grow || ev > unit + EV_SLACK || ev < unit - EV_SLACK) {
+        const float de = exp2_int(unit - ev);
+        unit = ev;
 #pragma unroll
-        for (int j = 0; j < DV / 8; ++j)
+        for (int n = 0; n < NT; ++n) {
+          float a[2];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[j][k] *= a[k >> 1];
+          for (int r = 0; r < 2; ++r) {
+            float x = top[n][r];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            a[r] = 1.f;
+            if (x > mrow[n][r]) {
+              a[r] = fast_exp2(mrow[n][r] - x);   // 0 from -inf
+              mrow[n][r] = x;
+            }
+            lrow[n][r] *= a[r];
+            a[r] *= de;
+          }
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[n][j][k] *= a[k & 1];
+        }
       }
-      uint32_t pa[4];
+      const __half2 ratio = __float2half2_rn(exp2_int(ev - unit));
+      const uint32_t ratio_bits = *reinterpret_cast<const uint32_t*>(&ratio);
+      uint32_t pb[NT][2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float ref = mrow[r] == -INFINITY ? 0.f : mrow[r] - P_LOG2;
+      for (int n = 0; n < NT; ++n) {
+        const float r0 = mrow[n][0] == -INFINITY ? 0.f : P_LOG2 - mrow[n][0];
+        const float r1 = mrow[n][1] == -INFINITY ? 0.f : P_LOG2 - mrow[n][1];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float p0 = fast_exp2(s[j][2 * r] - ref), p1 = fast_exp2(s[j][2 * r + 1] - ref);
-          lrow[r] += p0 + p1;
-          pa[2 * j + r] = pack_h2(p0, p1);
+          const float p0 = fast_exp2(fmaf(s[n][2 * j], f[n][0], r0)), p1 = fast_exp2(fmaf(s[n][2 * j + 1], f[n][1], r1));
+          lrow[n][0] += p0;
+          lrow[n][1] += p1;
+          pb[n][j] = transpose8x8(mul_h2(pack_h2(p0, p1), ratio_bits));
         }
       }
-      // O += P V: keys 2t, 2t + 1 and 8 more are this lane's rows of V, column
-      // n of tile j is element j of 8-lane group n's consecutive elements
+      // O^T += V^T P^T: keys 2t, 2t + 1 and 8 more are this lane's rows of V;
+      // column tile j holds elements 2j (its rows 0-7) and 2j + 1 of each lane
+      // group's consecutive columns
       const uint32_t vt = st + C::KB;
+      auto columns = [&](int j, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+        const uint32_t lo0 = __byte_perm(w0, w1, 0x5140), hi0 = __byte_perm(w0, w1, 0x7362);
+        const uint32_t lo1 = __byte_perm(w2, w3, 0x5140), hi1 = __byte_perm(w2, w3, 0x7362);
+        const uint32_t a[4] = {e4m3x2_to_h2((uint16_t)lo0), e4m3x2_to_h2((uint16_t)(lo0 >> 16)),
+                               e4m3x2_to_h2((uint16_t)lo1), e4m3x2_to_h2((uint16_t)(lo1 >> 16))};
+        const uint32_t c[4] = {e4m3x2_to_h2((uint16_t)hi0), e4m3x2_to_h2((uint16_t)(hi0 >> 16)),
+                               e4m3x2_to_h2((uint16_t)hi1), e4m3x2_to_h2((uint16_t)(hi1 >> 16))};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma16816(o[n][j], a, pb[n][0], pb[n][1]);
+          mma16816(o[n][j + 1], c, pb[n][0], pb[n][1]);
+        }
+      };
       if (DV == 64) {
         const int c = g >> 1, h8 = (g & 1) * 8;
         const uint2 w0 = lds64(vt + v_off<DV>(2 * t, c) + h8), w1 = lds64(vt + v_off<DV>(2 * t + 1, c) + h8);
         const uint2 w2 = lds64(vt + v_off<DV>(2 * t + 8, c) + h8), w3 = lds64(vt + v_off<DV>(2 * t + 9, c) + h8);
-        const uint32_t a[4][2] = {{w0.x, w0.y}, {w1.x, w1.y}, {w2.x, w2.y}, {w3.x, w3.y}};
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint32_t lo0 = __byte_perm(a[0][q], a[1][q], 0x5140), hi0 = __byte_perm(a[0][q], a[1][q], 0x7362);
-          const uint32_t lo1 = __byte_perm(a[2][q], a[3][q], 0x5140), hi1 = __byte_perm(a[2][q], a[3][q], 0x7362);
-          mma16816(o[4 * q], pa, e4m3x2_to_h2((uint16_t)lo0), e4m3x2_to_h2((uint16_t)lo1));
-          mma16816(o[4 * q + 1], pa, e4m3x2_to_h2((uint16_t)(lo0 >> 16)), e4m3x2_to_h2((uint16_t)(lo1 >> 16)));
-          mma16816(o[4 * q + 2], pa, e4m3x2_to_h2((uint16_t)hi0), e4m3x2_to_h2((uint16_t)hi1));
-          mma16816(o[4 * q + 3], pa, e4m3x2_to_h2((uint16_t)(hi0 >> 16)), e4m3x2_to_h2((uint16_t)(hi1 >> 16)));
-        }
+        columns(0, w0.x, w1.x, w2.x, w3.x);
+        columns(2, w0.y, w1.y, w2.y, w3.y);
       } else {
 #pragma unroll
         for (int half = 0; half < DV / 128; ++half) {
           const int c = g + 8 * half;
           const uint4 w0 = lds128(vt + v_off<DV>(2 * t, c)), w1 = lds128(vt + v_off<DV>(2 * t + 1, c));
           const uint4 w2 = lds128(vt + v_off<DV>(2 * t + 8, c)), w3 = lds128(vt + v_off<DV>(2 * t + 9, c));
-          const uint32_t a[4][4] = {{w0.x, w0.y, w0.z, w0.w}, {w1.x, w1.y, w1.z, w1.w},
-                                    {w2.x, w2.y, w2.z, w2.w}, {w3.x, w3.y, w3.z, w3.w}};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t lo0 = __byte_perm(a[0][q], a[1][q], 0x5140), hi0 = __byte_perm(a[0][q], a[1][q], 0x7362);
-            const uint32_t lo1 = __byte_perm(a[2][q], a[3][q], 0x5140), hi1 = __byte_perm(a[2][q], a[3][q], 0x7362);
-            const int j = half * 16 + 4 * q;
-            mma16816(o[j], pa, e4m3x2_to_h2((uint16_t)lo0), e4m3x2_to_h2((uint16_t)lo1));
-            mma16816(o[j + 1], pa, e4m3x2_to_h2((uint16_t)(lo0 >> 16)), e4m3x2_to_h2((uint16_t)(lo1 >> 16)));
-            mma16816(o[j + 2], pa, e4m3x2_to_h2((uint16_t)hi0), e4m3x2_to_h2((uint16_t)hi1));
-            mma16816(o[j + 3], pa, e4m3x2_to_h2((uint16_t)(hi0 >> 16)), e4m3x2_to_h2((uint16_t)(hi1 >> 16)));
-          }
+          columns(8 * half, w0.x, w1.x, w2.x, w3.x);
+          columns(8 * half + 2, w0.y, w1.y, w2.y, w3.y);
+          columns(8 * half + 4, w0.z, w1.z, w2.z, w3.z);
+          columns(8 * half + 6, w0.w, w1.w, w2.w, w3.w);
         }
       }
     }
@@ -438,38 +506,37 @@ __global__ void __launch_bounds__(NTHREADS) kv_fwd_kernel(const Args A) {
 
   // join the warps: maxima and sums, then each warp's O under the common maximum
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    lrow[r] += __shfl_xor_sync(0xffffffffu, lrow[r], 1);
-    lrow[r] += __shfl_xor_sync(0xffffffffu, lrow[r], 2);
-    if (t == 0) {
-      s_m[warp * ROWS + g + 8 * r] = mrow[r];
-      s_l[warp * ROWS + g + 8 * r] = lrow[r];
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float l = lrow[n][r];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      if (g == 0) {
+        s_m[warp * ROWS + 8 * n + 2 * t + r] = mrow[n][r];
+        s_l[warp * ROWS + 8 * n + 2 * t + r] = l;
+      }
     }
-  }
   __syncthreads();   // also: every ring has been read
   float* so = reinterpret_cast<float*>(smem);   // [NWARPS][ROWS][DV]
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int row = g + 8 * r;
-    float top = s_m[row];
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int w = 1; w < NWARPS; ++w) top = fmaxf(top, s_m[w * ROWS + row]);
-    const float a = (mrow[r] == -INFINITY ? 0.f : fast_exp2(mrow[r] - top)) * exp2_int(ev);
-    float* dst = so + (warp * ROWS + row) * DV;
-    if (mrow[r] == -INFINITY && !(lrow[r] != lrow[r])) {
+    for (int r = 0; r < 2; ++r) {
+      const int row = 8 * n + 2 * t + r;
+      float top = s_m[row];
 #pragma unroll
-      for (int j = 0; j < DV / 8; ++j) o[j][2 * r] = o[j][2 * r + 1] = 0.f;   // nothing seen
+      for (int w = 1; w < NWARPS; ++w) top = fmaxf(top, s_m[w * ROWS + row]);
+      // a warp that saw no key of the row holds zeros (or NaN, which stays)
+      const float a = (mrow[n][r] == -INFINITY ? 1.f : fast_exp2(mrow[n][r] - top)) * exp2_int(unit);
+      float* dst = so + (warp * ROWS + row) * DV;
+      constexpr int RUN = DV == 64 ? 8 : 16;    // consecutive columns of a lane group
+#pragma unroll
+      for (int j = 0; j < MT; j += 2)
+        *reinterpret_cast<float4*>(dst + (2 * j / RUN) * 128 + g * RUN + 2 * j % RUN) =
+            make_float4(o[n][j][r] * a, o[n][j][2 + r] * a, o[n][j + 1][r] * a, o[n][j + 1][2 + r] * a);
     }
-    constexpr int NJ = DV == 64 ? 8 : 16;   // consecutive elements of a lane group
-#pragma unroll
-    for (int j = 0; j < DV / 8; j += 4) {
-      const int at = (j / NJ) * 128 + j % NJ + 2 * t * NJ;
-      *reinterpret_cast<float4*>(dst + at) =
-          make_float4(o[j][2 * r] * a, o[j + 1][2 * r] * a, o[j + 2][2 * r] * a, o[j + 3][2 * r] * a);
-      *reinterpret_cast<float4*>(dst + at + NJ) =
-          make_float4(o[j][2 * r + 1] * a, o[j + 1][2 * r + 1] * a, o[j + 2][2 * r + 1] * a, o[j + 3][2 * r + 1] * a);
-    }
-  }
   __syncthreads();
   const bool whole = J.ntile <= A.split_tiles;   // no other split holds keys of these rows
   const long long part = ((long long)(b * A.c.hkv + hk) * A.mtiles + m) * A.nsplit + split;
@@ -488,13 +555,7 @@ __global__ void __launch_bounds__(NTHREADS) kv_fwd_kernel(const Args A) {
       v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
     }
     if (whole) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int tk = (J.row0 + row) / A.g, h = hk * A.g + J.row0 + row - tk * A.g;
-      T* dst = static_cast<T*>(A.o) + elem_off(A.so, (long long)J.q0 + tk, h) + c;
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_t2<T>(v.x * inv, v.y * inv), pack_t2<T>(v.z * inv, v.w * inv));
-      if (c == 0)
-        A.lse[(long long)h * A.total_q + J.q0 + tk] =
-            l == 0.f ? -INFINITY : (top - P_LOG2 + log2f(l)) * 0.6931471805599453f;
+      store_row<T>(A, J, hk, row, c, v, top, l);
     } else {
       *reinterpret_cast<float4*>(A.part_o + (part * ROWS + row) * DV + c) = v;
       if (c == 0) A.part_ml[part * ROWS + row] = make_float2(top, l);
@@ -504,46 +565,62 @@ __global__ void __launch_bounds__(NTHREADS) kv_fwd_kernel(const Args A) {
     A.status[b * A.nsplit + split] = J.bad ? ATTN_ERR_BAD_SEQLENS : *s_bad ? ATTN_ERR_BAD_PAGE : ATTN_OK;
 }
 
-// Joins the splits of a row in ascending order: O = sum 2^(m_s - m) O_s / sum
-// 2^(m_s - m) l_s.  A CTA takes NTHREADS / (DV / 4) rows of one job.
-template <int DV, typename T>
+// Joins the splits of a row in a fixed order: O = sum 2^(m_s - m) O_s / sum
+// 2^(m_s - m) l_s.  A CTA takes one row; DV / 4 threads cover its columns, and
+// the thread groups take the splits in turn.
+template <int DV, int NT, typename T>
 __global__ void __launch_bounds__(NTHREADS) join_kernel(const Args A) {
-  constexpr int PER = NTHREADS / (DV / 4);
-  constexpr int GROUPS = ROWS / PER;
-  const int job = blockIdx.x / GROUPS, row = (blockIdx.x % GROUPS) * PER + threadIdx.x / (DV / 4);
-  const int c = (threadIdx.x % (DV / 4)) * 4;
+  constexpr int ROWS = 8 * NT;
+  constexpr int COLS = DV / 4, GROUPS = NTHREADS / COLS;
+  __shared__ float4 s_v[GROUPS][COLS];
+  __shared__ float s_l[GROUPS];
+  __shared__ float s_top[NTHREADS / 32];
+  const int job = blockIdx.x / ROWS, row = blockIdx.x % ROWS;
+  const int grp = threadIdx.x / COLS, col = threadIdx.x % COLS, c = col * 4;
   const int m = job % A.mtiles, bh = job / A.mtiles, hk = bh % A.c.hkv, b = bh / A.c.hkv;
   MaskArgs mk;
-  const Job J = make_job(A, b, m, mk);
+  const Job J = make_job<ROWS>(A, b, m, mk);
   if (row >= J.nrow || J.ntile <= A.split_tiles) return;
   const int n = cdiv(J.ntile, A.split_tiles);
   const float2* ml = A.part_ml + (long long)job * A.nsplit * ROWS + row;
   const float* po = A.part_o + ((long long)job * A.nsplit * ROWS + row) * DV + c;
   float top = -INFINITY;
-  for (int s = 0; s < n; ++s) top = fmaxf(top, ml[s * ROWS].x);
+  for (int s = threadIdx.x; s < n; s += NTHREADS) top = fmaxf(top, ml[s * ROWS].x);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < NTHREADS / 32; ++w) top = fmaxf(top, s_top[w]);
   float l = 0.f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int s = 0; s < n; ++s) {
+  for (int s = grp; s < n; s += GROUPS) {
     const float2 x = ml[s * ROWS];
     const float4 y = *reinterpret_cast<const float4*>(po + (long long)s * ROWS * DV);
-    const float w = x.x == -INFINITY ? (x.y != x.y ? x.y : 0.f) : fast_exp2(x.x - top);
+    // a split that saw no key of the row holds zeros (or NaN, which stays)
+    const float w = x.x == -INFINITY ? 1.f : fast_exp2(x.x - top);
     l += w * x.y;
     v.x += w * y.x; v.y += w * y.y; v.z += w * y.z; v.w += w * y.w;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int tk = (J.row0 + row) / A.g, h = hk * A.g + J.row0 + row - tk * A.g;
-  T* dst = static_cast<T*>(A.o) + elem_off(A.so, (long long)J.q0 + tk, h) + c;
-  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_t2<T>(v.x * inv, v.y * inv), pack_t2<T>(v.z * inv, v.w * inv));
-  if (c == 0)
-    A.lse[(long long)h * A.total_q + J.q0 + tk] =
-        l == 0.f ? -INFINITY : (top - P_LOG2 + log2f(l)) * 0.6931471805599453f;
+  s_v[grp][col] = v;
+  if (col == 0) s_l[grp] = l;
+  __syncthreads();
+  if (grp == 0) {
+#pragma unroll
+    for (int w = 1; w < GROUPS; ++w) {
+      const float4 y = s_v[w][col];
+      v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+      l += s_l[w];
+    }
+    store_row<T>(A, J, hk, row, c, v, top, l);
+  }
 }
 
 // ---------------------------------------------------------------- host side
 
 struct Layout {
-  int mtiles, nsplit, split_tiles;
+  int nt, mtiles, nsplit, split_tiles;
   long long jobs;
   size_t off_status, off_ml, off_o, total;
 };
@@ -558,10 +635,12 @@ static int max_keys(const attn_kv_fwd_params& p) {
 static Layout layout(const attn_kv_fwd_params& p) {
   Layout L{};
   const int g = p.nhead_q / p.cache.nhead_kv;
-  L.mtiles = (int)cdiv_ll((long long)(p.max_seqlen_q > 0 ? p.max_seqlen_q : 1) * g, ROWS);
+  const long long rows = (long long)(p.max_seqlen_q > 0 ? p.max_seqlen_q : 1) * g;
+  L.nt = rows <= 8 ? 1 : 2;
+  L.mtiles = (int)cdiv_ll(rows, 8 * L.nt);
   L.jobs = (long long)p.batch * p.cache.nhead_kv * L.mtiles;
   const int tiles = max_keys(p) / TILE + 2;
-  const long long want = SMS * 12;
+  const long long want = SMS * 6;
   long long n = cdiv_ll(want, L.jobs);
   if (n > cdiv(tiles, MIN_TILES)) n = cdiv(tiles, MIN_TILES);
   if (n < cdiv(tiles, MAX_TILES)) n = cdiv(tiles, MAX_TILES);
@@ -574,9 +653,9 @@ static Layout layout(const attn_kv_fwd_params& p) {
   o = up(o + (size_t)p.batch * L.nsplit * sizeof(int));
   const size_t parts = L.nsplit > 1 ? (size_t)L.jobs * L.nsplit : 0;
   L.off_ml = o;
-  o = up(o + parts * ROWS * sizeof(float2));
+  o = up(o + parts * 8 * L.nt * sizeof(float2));
   L.off_o = o;
-  o = up(o + parts * ROWS * p.cache.d_v * sizeof(float));
+  o = up(o + parts * 8 * L.nt * p.cache.d_v * sizeof(float));
   L.total = o;
   return L;
 }
@@ -604,26 +683,28 @@ static int validate_sizes(const attn_kv_fwd_params* p) {
   return ATTN_OK;
 }
 
-template <int DQK, int DV, typename T>
+template <int DQK, int DV, int NT, typename T>
 static int launch(const Args& a, long long jobs, cudaStream_t st) {
-  using C = Cfg<DQK, DV>;
-  auto kern = kv_fwd_kernel<DQK, DV, T>;
+  using C = Cfg<DQK, DV, NT>;
+  auto kern = kv_fwd_kernel<DQK, DV, NT, T>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return ATTN_ERR_CUDA;
   kern<<<(unsigned)(jobs * a.nsplit), NTHREADS, C::SMEM, st>>>(a);
-  if (a.nsplit > 1) {
-    constexpr int GROUPS = ROWS / (NTHREADS / (DV / 4));
-    join_kernel<DV, T><<<(unsigned)(jobs * GROUPS), NTHREADS, 0, st>>>(a);
-  }
+  if (a.nsplit > 1) join_kernel<DV, NT, T><<<(unsigned)(jobs * C::ROWS), NTHREADS, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+template <int DQK, int DV, typename T>
+static int launch_rows(const Args& a, const Layout& L, cudaStream_t st) {
+  return L.nt == 1 ? launch<DQK, DV, 1, T>(a, L.jobs, st) : launch<DQK, DV, 2, T>(a, L.jobs, st);
+}
+
 template <typename T>
-static int launch_dims(const Args& a, int dqk, int dv, long long jobs, cudaStream_t st) {
-  if (dqk == 64) return launch<64, 64, T>(a, jobs, st);
-  if (dqk == 128) return launch<128, 128, T>(a, jobs, st);
-  if (dqk == 192) return launch<192, 128, T>(a, jobs, st);
-  return launch<256, 256, T>(a, jobs, st);
+static int launch_dims(const Args& a, const Layout& L, int dqk, int dv, cudaStream_t st) {
+  if (dqk == 64) return launch_rows<64, 64, T>(a, L, st);
+  if (dqk == 128) return launch_rows<128, 128, T>(a, L, st);
+  if (dqk == 192) return launch_rows<192, 128, T>(a, L, st);
+  return launch_rows<256, 256, T>(a, L, st);
 }
 
 static int run(const attn_kv_fwd_params* p, void* ws, size_t ws_bytes, cudaStream_t st) {
@@ -669,8 +750,8 @@ static int run(const attn_kv_fwd_params* p, void* ws, size_t ws_bytes, cudaStrea
   a.status = reinterpret_cast<int*>(w + L.off_status);
   a.part_ml = reinterpret_cast<float2*>(w + L.off_ml);
   a.part_o = reinterpret_cast<float*>(w + L.off_o);
-  if (p->dtype == ATTN_BF16) return launch_dims<__nv_bfloat16>(a, dqk, dv, L.jobs, st);
-  return launch_dims<__half>(a, dqk, dv, L.jobs, st);
+  if (p->dtype == ATTN_BF16) return launch_dims<__nv_bfloat16>(a, L, dqk, dv, st);
+  return launch_dims<__half>(a, L, dqk, dv, st);
 }
 
 }  // namespace kvfwd
