@@ -307,10 +307,6 @@ static void log_config(const attn_bwd_params& p, const WsLayout& L) {
                p.softmax_scale, p.deterministic, L.nsplits, L.max_items, L.total);
 }
 
-// Tensor-core forward (fwd_tc.cu); ATTN_ERR_UNSUPPORTED_HEADDIM for the
-// dtypes and head dims it is not built for.
-int launch_fwd_tc(const attn_fwd_params& p, const FwdLayout& L, cudaStream_t st);
-
 // Schedule and preprocess launches of one call, or of one part of a call
 // split into parts (attn_bwd_host: parts after the first keep the status the
 // earlier parts left).

@@ -391,6 +391,18 @@ struct FwdLayout {
   long long bias_sb, bias_sh; // bias element strides of batch entry and head
 };
 void launch_fwd(const attn_fwd_params& p, const FwdLayout& L, cudaStream_t st);
+// Segments given by first row and length instead of offsets (group mode): row
+// arrays of `batch` entries on the device.
+struct FwdSegments {
+  const int* zeros;
+  const int* len_q;
+  const int* start_q;
+  const int* len_k;
+  const int* start_k;
+};
+// Tensor-core forward (fwd_tc.cu); ATTN_ERR_UNSUPPORTED_HEADDIM for the
+// dtypes, head dims and scales it is not built for.  `seg` replaces the cu_seqlens of p.
+int launch_fwd_tc(const attn_fwd_params& p, const FwdLayout& L, cudaStream_t st, const FwdSegments* seg = nullptr);
 // Forward of a problem with no key rows at all (O = 0, LSE = -inf).
 void launch_fwd_no_keys(const attn_fwd_params& p, const FwdLayout& L, cudaStream_t st);
 

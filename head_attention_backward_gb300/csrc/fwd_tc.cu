@@ -101,8 +101,10 @@ struct Maps {
 
 struct Args {
   int group, hq, g, sq, sk;
-  const int* cu_q;
+  const int* cu_q;        // a segment's length is the difference of its end and its begin
+  const int* cu_q_end;
   const int* cu_k;
+  const int* cu_k_end;
   const int* st_q;
   const int* st_k;
   int mask, left, right;
@@ -162,8 +164,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) fwd_tc_kernel(const __grid_consta
   const int h = blockIdx.y, b = blockIdx.z, hk = h / A.g;
   int q0, lq, k0, lk;
   if (A.group) {
-    lq = __ldg(A.cu_q + b + 1) - __ldg(A.cu_q + b);
-    lk = __ldg(A.cu_k + b + 1) - __ldg(A.cu_k + b);
+    lq = __ldg(A.cu_q_end + b) - __ldg(A.cu_q + b);
+    lk = __ldg(A.cu_k_end + b) - __ldg(A.cu_k + b);
     q0 = __ldg(A.st_q + b);
     k0 = __ldg(A.st_k + b);
   } else {
@@ -516,9 +518,9 @@ static bool make_map(CUtensorMap* m, const void* base, bool fp16, int dim, int h
 }
 
 template <int DQK, int DV, typename T>
-static int launch_typed(const attn_fwd_params& p, const FwdLayout& L, cudaStream_t st) {
+static int launch_typed(const attn_fwd_params& p, const FwdLayout& L, cudaStream_t st, const FwdSegments* seg) {
   using C = FCfg<DQK, DV>;
-  const bool group = p.cu_seqlens_q != nullptr;
+  const bool group = p.cu_seqlens_q != nullptr || seg;
   const bool fp16 = IsHalf<T>::value;
   const long long rq = group ? p.total_q : (long long)p.batch * p.seqlen_q;
   const long long rk = group ? p.total_k : (long long)p.batch * p.seqlen_k;
@@ -532,10 +534,12 @@ static int launch_typed(const attn_fwd_params& p, const FwdLayout& L, cudaStream
   a.g = p.nhead_q / p.nhead_kv;
   a.sq = p.seqlen_q;
   a.sk = p.seqlen_k;
-  a.cu_q = p.cu_seqlens_q;
-  a.cu_k = p.cu_seqlens_k;
-  a.st_q = p.cu_seqlens_q_padded ? p.cu_seqlens_q_padded : p.cu_seqlens_q;
-  a.st_k = p.cu_seqlens_k_padded ? p.cu_seqlens_k_padded : p.cu_seqlens_k;
+  a.cu_q = seg ? seg->zeros : p.cu_seqlens_q;
+  a.cu_q_end = seg ? seg->len_q : p.cu_seqlens_q + 1;
+  a.cu_k = seg ? seg->zeros : p.cu_seqlens_k;
+  a.cu_k_end = seg ? seg->len_k : p.cu_seqlens_k + 1;
+  a.st_q = seg ? seg->start_q : p.cu_seqlens_q_padded ? p.cu_seqlens_q_padded : p.cu_seqlens_q;
+  a.st_k = seg ? seg->start_k : p.cu_seqlens_k_padded ? p.cu_seqlens_k_padded : p.cu_seqlens_k;
   a.mask = p.mask;
   a.left = p.mask == ATTN_MASK_WINDOW ? p.window_left : -1;
   a.right = p.mask == ATTN_MASK_WINDOW ? p.window_right : -1;
@@ -556,10 +560,10 @@ static int launch_typed(const attn_fwd_params& p, const FwdLayout& L, cudaStream
 }
 
 template <typename T>
-static int launch_dims(const attn_fwd_params& p, const FwdLayout& L, cudaStream_t st) {
-  if (p.d_qk == 128 && p.d_v == 128) return launch_typed<128, 128, T>(p, L, st);
-  if (p.d_qk == 64 && p.d_v == 64) return launch_typed<64, 64, T>(p, L, st);
-  if (p.d_qk == 192 && p.d_v == 128) return launch_typed<192, 128, T>(p, L, st);
+static int launch_dims(const attn_fwd_params& p, const FwdLayout& L, cudaStream_t st, const FwdSegments* seg) {
+  if (p.d_qk == 128 && p.d_v == 128) return launch_typed<128, 128, T>(p, L, st, seg);
+  if (p.d_qk == 64 && p.d_v == 64) return launch_typed<64, 64, T>(p, L, st, seg);
+  if (p.d_qk == 192 && p.d_v == 128) return launch_typed<192, 128, T>(p, L, st, seg);
   return ATTN_ERR_UNSUPPORTED_HEADDIM;
 }
 
@@ -568,11 +572,11 @@ static int launch_dims(const attn_fwd_params& p, const FwdLayout& L, cudaStream_
 // Tensor-core forward for the 16-bit head-dim pairs it is built for and a
 // positive softmax scale; ATTN_ERR_UNSUPPORTED_HEADDIM otherwise (the caller
 // then runs the CUDA-core forward).
-int launch_fwd_tc(const attn_fwd_params& p, const FwdLayout& L, cudaStream_t st) {
+int launch_fwd_tc(const attn_fwd_params& p, const FwdLayout& L, cudaStream_t st, const FwdSegments* seg) {
   // the row max is taken on the raw scores, which needs a positive scale
   if (!(p.softmax_scale > 0.f)) return ATTN_ERR_UNSUPPORTED_HEADDIM;
-  if (p.dtype == ATTN_BF16) return fwdtc::launch_dims<__nv_bfloat16>(p, L, st);
-  if (p.dtype == ATTN_FP16) return fwdtc::launch_dims<__half>(p, L, st);
+  if (p.dtype == ATTN_BF16) return fwdtc::launch_dims<__nv_bfloat16>(p, L, st, seg);
+  if (p.dtype == ATTN_FP16) return fwdtc::launch_dims<__half>(p, L, st, seg);
   return ATTN_ERR_UNSUPPORTED_HEADDIM;
 }
 

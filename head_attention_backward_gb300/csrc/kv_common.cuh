@@ -2,6 +2,8 @@
 // of its arguments, and the e4m3 conversions (one PTX instruction each).
 #pragma once
 
+#include <initializer_list>
+
 #include "common.cuh"
 
 namespace attn {
@@ -36,15 +38,16 @@ inline int kv_page_shift(int page_size) {
 
 inline bool aligned_to(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
-inline bool kv_strides(const int64_t in[3], long long rows, long long heads, long long d, KvStrides* s) {
+// A dimension with one entry never uses its stride; it gets a valid one.
+inline bool kv_strides(const int64_t in[3], long long pages, long long rows, long long heads, long long d, KvStrides* s) {
   if (in[0] == 0 && in[1] == 0 && in[2] == 0) {
     *s = {rows * heads * d, heads * d, d};
     return true;
   }
-  *s = {in[0], in[1], in[2]};
+  *s = {pages > 1 ? in[0] : 16, in[1], heads > 1 ? in[2] : 16};
   const long long lim = 1LL << 40;
-  for (int i = 0; i < 3; ++i)
-    if (in[i] <= 0 || in[i] >= lim || in[i] % 16 != 0) return false;
+  for (long long x : {s->p, s->r, s->h})
+    if (x <= 0 || x >= lim || x % 16 != 0) return false;
   return true;
 }
 
@@ -54,8 +57,8 @@ inline int kv_resolve(const attn_kv_cache& c, KvCacheView* out) {
   if (shift < 0) return ATTN_ERR_INVALID_ARG;
   if (!kv_headdims(c.d_qk, c.d_v)) return ATTN_ERR_UNSUPPORTED_HEADDIM;
   if (!c.k || !c.v || !c.k_exp || !c.v_exp || !aligned_to(c.k, 16) || !aligned_to(c.v, 16)) return ATTN_ERR_INVALID_ARG;
-  if (!kv_strides(c.stride_k, c.page_size, c.nhead_kv, c.d_qk, &out->sk) ||
-      !kv_strides(c.stride_v, c.page_size, c.nhead_kv, c.d_v, &out->sv))
+  if (!kv_strides(c.stride_k, c.num_pages, c.page_size, c.nhead_kv, c.d_qk, &out->sk) ||
+      !kv_strides(c.stride_v, c.num_pages, c.page_size, c.nhead_kv, c.d_v, &out->sv))
     return ATTN_ERR_INVALID_ARG;
   out->k = static_cast<uint8_t*>(c.k);
   out->v = static_cast<uint8_t*>(c.v);
@@ -77,6 +80,20 @@ inline bool packed_strides(const int64_t in[3], int heads, int dim, Strides* s) 
   const long long lim = 1LL << 36;
   return in[1] > 0 && in[2] > 0 && in[1] < lim && in[2] < lim && in[1] % 8 == 0 && in[2] % 8 == 0;
 }
+
+// Long query segments over the cache (kv_long.cu).
+struct KvLong {
+  int from;               // segments of more query tokens than this
+  int slots;              // most of them that q can hold; 0: the path is not used
+  int group, groups;      // slots whose keys are expanded at a time, and times
+  long long kpad;         // rows of a slot's keys and values
+  size_t off_list, off_k, off_v, total;   // workspace; total is 0 without slots
+};
+KvLong kv_long_layout(const attn_kv_fwd_params& p, int max_k);
+int launch_kv_long(const attn_kv_fwd_params& p, const KvCacheView& c, const Strides& sq, const Strides& so, int max_k,
+                   const KvLong& L, char* ws, cudaStream_t st);
+// Status words of the long path in its part of the workspace: [slots].
+inline size_t kv_long_status_offset(const KvLong& L) { return L.off_list; }
 
 // ------------------------------------------------------------------ e4m3
 

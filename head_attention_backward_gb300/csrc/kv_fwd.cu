@@ -8,9 +8,10 @@
 // in warp-level m16n8k16 products, and the work is laid out for the loads:
 //
 // * A CTA owns one row tile, one kv head and one split of the keys; its four
-//   warps take 16-key tiles in turn, each with a ring of its own that 16-byte
-//   asynchronous copies keep full.  No barrier joins the warps until the end.
-//   A tile lies in one page, so its scales are uniform.
+//   warps take 16-key tiles in turn, each with a ring of its own that its lane
+//   0 keeps full by TMA (a 16-row box of a page and head, swizzled).  No
+//   barrier joins the warps until the end.  A tile lies in one page, so its
+//   scales are uniform.
 // * The products are transposed, S^T = K Q^T and O^T = V^T P^T: the 16-row side
 //   of the instruction holds keys and value columns, the 8-column side the few
 //   query rows.  S^T becomes the operand P^T by one 8 x 8 transposition per
@@ -18,7 +19,9 @@
 // * e4m3 is exact in fp16.  The contraction's order is free, so a lane takes
 //   16 consecutive bytes of a K row as its share of four k-steps and 16
 //   consecutive bytes of four V rows as its share of eight column tiles: wide
-//   conflict-free shared loads, one conversion per two values.
+//   shared loads, one conversion per two values.  So is the order of the keys:
+//   key_of() pairs rows so that the swizzle keeps both kinds of load free of
+//   bank conflicts (of V at head dim 64, two-way).
 // * q goes to fp16 under a power-of-two scale per row (largest magnitude in
 //   [2^14, 2^15)), which is exact for bf16 too unless an element is 2^-28 of
 //   its row's largest.  P is fp16 with its running maximum at 2^4: 11 bits down
@@ -29,7 +32,11 @@
 //
 // Splits leave (O, max, sum) in the workspace; a second small kernel joins
 // them in a fixed order.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <cmath>
+#include <mutex>
 
 #include "common.cuh"
 #include "kv_common.cuh"
@@ -42,8 +49,15 @@ constexpr int NWARPS = 4;
 constexpr int NTHREADS = 32 * NWARPS;
 constexpr int TILE = 16;            // keys of a warp's step
 constexpr int MAX_TILES = 256;      // tiles of a split: its page table fits shared memory
-constexpr int MIN_TILES = 16;       // a split is worth at least this many
-constexpr int SMS = 152;
+// Splits.  Few jobs: as many CTAs as fill one wave of two per SM (one request of
+// 131,072 tokens, 8 kv heads: 50.5 us with 304 CTAs, 55.3 with 152, 56.3 with
+// 608: more parts to join and an uneven second wave).  Many jobs: splits short
+// enough to even out ragged lengths (64 requests of up to 8,192 tokens: 108.4 us
+// at 64 tiles, 114.2 at 256, 114.0 at 32).  None so short that its prologue
+// outweighs it (4 requests of 1,000 tokens: 8.8 us at 8 tiles, 9.7 at 16).
+constexpr int WAVE = 304;
+constexpr int EVEN_TILES = 64;
+constexpr int MIN_TILES = 8;
 constexpr int EV_SLACK = 4;         // V scales within 2^4 of the accumulator's unit go on P
 constexpr float P_LOG2 = 4.f;       // P = 2^4 at the running maximum
 constexpr float SLACK_LOG2 = 7.f;   // growth of the maximum that is let pass: P <= 2^(4 + 7 + 4)
@@ -54,14 +68,19 @@ struct Cfg {
   static constexpr int ROWS = 8 * NT;
   static constexpr int KB = TILE * DQK, VB = TILE * DV;
   static constexpr int STAGE = KB + VB;
-  static constexpr int NST = STAGE <= 2048 ? 6 : 3;
+    static constexpr int NST = STAGE <= 2048 ? 6 : 3;
   static constexpr int RING = NST * STAGE;
-  static constexpr int OFF_META = NWARPS * RING;                       // int2[MAX_TILES + 1]: page, exponents
+  static constexpr int OFF_BAR = NWARPS * RING;                        // uint64_t[NWARPS][NST]
+  static constexpr int OFF_META = OFF_BAR + NWARPS * NST * 8;          // int2[MAX_TILES + 1]: page, exponents
   static constexpr int OFF_ML = OFF_META + (MAX_TILES + 1) * 8;        // float[2][NWARPS][ROWS]
-  static constexpr int SMEM = OFF_ML + 2 * NWARPS * ROWS * 4 + 8;
+  static constexpr int SMEM = OFF_ML + 2 * NWARPS * ROWS * 4 + 8 + 1024;   // + alignment slack
   // CTAs per SM that the registers have to allow (shared memory allows them too)
   static constexpr int RESIDENT = NT == 1 ? (DQK == 256 ? 2 : DQK == 192 ? 3 : 4) : (DQK == 256 ? 1 : DQK == 192 ? 2 : 3);
   static_assert(NWARPS * ROWS * DV * 4 <= NWARPS * RING, "the join of the warps reuses the rings");
+};
+
+struct Maps {
+  CUtensorMap k, v;      // (d, heads, rows of a page, pages)
 };
 
 struct Args {
@@ -76,10 +95,12 @@ struct Args {
   long long table_stride;
   int max_k;             // min(max_seqlen_k, max_blocks pages)
   int total_q, max_q;
+  int long_from;         // segments of more tokens are left to the long path
   int hq, g;             // query heads, per kv head
   int mask, left, right;
   float scale_log2;
   int nsplit, split_tiles, mtiles;
+  int job_rows;          // most rows that a row tile can have
   float* part_o;         // [job][nsplit][rows][DV]
   float2* part_ml;       // [job][nsplit][rows]
   int* status;           // [batch][nsplit]
@@ -104,7 +125,7 @@ __device__ __forceinline__ Job make_job(const Args& A, int b, int m, MaskArgs& m
   j.q0 = __ldg(A.st_q + b);
   j.lk = __ldg(A.len_k + b);
   j.bad = j.lq < 0 || j.lq > A.max_q || j.q0 < 0 || (long long)j.q0 + j.lq > A.total_q;
-  if (j.bad) j.lq = 0;
+  if (j.bad || j.lq > A.long_from) j.lq = 0;
   if (j.lk < 0 || j.lk > A.max_k) {
     j.bad = true;
     j.lk = j.lk < 0 ? 0 : A.max_k;
@@ -135,13 +156,26 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// 16-byte asynchronous copy past L1; bytes = 0 writes zeros.
-__device__ __forceinline__ void cp_async16(uint32_t sdst, const void* gsrc, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sdst), "l"(gsrc), "r"(bytes) : "memory");
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* desc, uint64_t* bar, int x, int y, int z,
+                                            int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(desc)), "r"(ptx::smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Bounded wait; a tile that does not arrive within the limit ends the loop.
+constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = ptx::globaltimer();
+  while (!ptx::mbar_try_wait_sleep(bar, parity, 20000))
+    if (ptx::globaltimer() - t0 > WAIT_LIMIT_NS) return false;
+  return true;
+}
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
+  return ptx::mbar_try_wait(bar, parity) || wait_slow(bar, parity);
+}
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -154,20 +188,26 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   return v;
 }
 
-// Byte offset of 16-byte piece c of row r in a warp's K or V tile.  The lanes
-// of one shared load phase read, of K, rows 2p and 2p + 1 at pieces t (mod 4)
-// and, of V, rows 2t at pieces 2p and 2p + 1 (t = 0..3): the piece is moved
-// within its 128-byte line so that the eight fall on different banks.
+// Byte offset of 16-byte piece c of row r in a warp's K or V tile: boxes of 16
+// rows of 128 bytes (64 where D is no multiple of 128), with the swizzle of
+// that width as TMA writes it.
 template <int D>
-__device__ __forceinline__ int k_off(int r, int c) {
-  return r * D + ((D % 128 == 0 ? c ^ ((r & 1) << 2) : c) << 4);
-}
+struct Box {
+  static constexpr int W = D % 128 == 0 ? 128 : 64;
+  static constexpr int N = D / W;
+};
 template <int D>
-__device__ __forceinline__ int v_off(int r, int c) {
-  const int x = ((r >> 1) & 3) << 1;
-  if (D == 64) return (r >> 1) * 128 + ((((r & 1) << 2 | c) ^ x) << 4);
-  return r * D + ((c ^ x) << 4);
+__device__ __forceinline__ int off(int r, int c) {
+  if (Box<D>::W == 128) return (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+  return (c >> 2) * 1024 + r * 64 + (((c & 3) ^ ((r >> 1) & 3)) << 4);
 }
+
+// Key of index g within eight: 0 5 2 7 4 1 6 3.  A K load's phase takes keys
+// key_of(2p), key_of(2p + 1) at pieces t (mod 4), a V load's the keys
+// key_of(2t) or key_of(2t + 1) at pieces 2p, 2p + 1 (t = 0..3): the first two
+// differ in bit 2, the other four in bits 1 and 2, so the swizzle sends the
+// eight pieces to different banks.
+__device__ __forceinline__ int key_of(int g) { return g ^ ((g & 1) << 2); }
 
 template <typename T> __device__ __forceinline__ float2 up2(uint32_t x);
 template <> __device__ __forceinline__ float2 up2<__nv_bfloat16>(uint32_t x) {
@@ -213,10 +253,11 @@ __device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
 }
 
 template <int DQK, int DV, int NT, typename T>
-__global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_kernel(const Args A) {
+__global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_kernel(const __grid_constant__ Maps maps, const Args A) {
   using C = Cfg<DQK, DV, NT>;
   constexpr int ROWS = C::ROWS;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (ptx::smem_u32(smem_raw) & 1023)) & 1023);   // the swizzle counts from 1024
   int2* meta = reinterpret_cast<int2*>(smem + C::OFF_META);
   float* s_m = reinterpret_cast<float*>(smem + C::OFF_ML);
   float* s_l = s_m + NWARPS * ROWS;
@@ -234,7 +275,14 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
   MaskArgs mk;
   const Job J = make_job<ROWS>(A, b, m, mk);
   const bool reports = hk == 0 && m == 0;   // one CTA per (request, split) says what it found
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * C::NST;
   if (tid == 0) *s_bad = 0;
+  if (lane == 0) {
+    for (int i = 0; i < C::NST; ++i) ptx::mbar_init(bars + i, 1);
+    ptx::fence_mbar_init();
+    ptx::tma_prefetch_desc(&maps.k);
+    ptx::tma_prefetch_desc(&maps.v);
+  }
   const int tile0 = split * A.split_tiles;
   if (J.nrow <= 0 || (split > 0 && tile0 >= J.ntile)) {
     if (reports && tid == 0) A.status[b * A.nsplit + split] = J.bad ? ATTN_ERR_BAD_SEQLENS : ATTN_OK;
@@ -243,13 +291,45 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
   const int ntile = min(A.split_tiles, J.ntile - tile0);      // may be <= 0 for split 0
   const int key0 = J.kbeg + tile0 * TILE;
   const int page0 = key0 >> A.c.page_shift;
+  const int shift = A.c.page_shift, in_page = (1 << shift) - 1;
+  const uint32_t ring = ptx::smem_u32(smem) + warp * C::RING;
+  const int* table = A.table + b * A.table_stride + page0;
+  // tile i of the split, of this page, into stage `at` (lane 0): every tile
+  // completes its barrier once
+  auto load = [&](int i, int at, int page) {
+    const int row = (key0 + i * TILE) & in_page;
+    const uint32_t st = ring + at * C::STAGE;
+    if (page >= 0 && page < A.c.num_pages) {
+      ptx::mbar_arrive_expect_tx(bars + at, C::STAGE);
+#pragma unroll
+      for (int c = 0; c < Box<DQK>::N; ++c)
+        tma_load_4d(st + c * TILE * Box<DQK>::W, &maps.k, bars + at, c * Box<DQK>::W, hk, row, page);
+#pragma unroll
+      for (int c = 0; c < Box<DV>::N; ++c)
+        tma_load_4d(st + C::KB + c * TILE * Box<DV>::W, &maps.v, bars + at, c * Box<DV>::W, hk, row, page);
+    } else {
+      ptx::mbar_arrive(bars + at);
+    }
+  };
+  // the first tiles leave before anything else is known
+  if (lane == 0) {
+    int first[C::NST - 1];
+#pragma unroll
+    for (int s = 0; s < C::NST - 1; ++s) {
+      const int i = warp + s * NWARPS;
+      first[s] = i < ntile ? __ldg(table + (((key0 + i * TILE) >> shift) - page0)) : -1;
+    }
+#pragma unroll
+    for (int s = 0; s < C::NST - 1; ++s)
+      if (warp + s * NWARPS < ntile) load(warp + s * NWARPS, s, first[s]);
+  }
   __syncthreads();
 
   // pages and scales of this split
   if (ntile > 0) {
     const int npage = ((key0 + ntile * TILE - 1) >> A.c.page_shift) - page0 + 1;
     for (int i = tid; i < npage; i += NTHREADS) {
-      const int page = __ldg(A.table + b * A.table_stride + page0 + i);
+      const int page = __ldg(table + i);
       int e = 0;
       if (page >= 0 && page < A.c.num_pages) {
         const long long at = (long long)page * A.c.hkv + hk;
@@ -313,41 +393,6 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
   }
   __syncthreads();
 
-  const uint32_t ring = ptx::smem_u32(smem) + warp * C::RING;
-  const int shift = A.c.page_shift, in_page = (1 << shift) - 1;
-  const uint8_t* kbase = A.c.k + hk * A.c.sk.h;
-  const uint8_t* vbase = A.c.v + hk * A.c.sv.h;
-  // the rows of a tile in 16-byte pieces, piece lane + 32 k for the k-th copy of
-  // a lane: with whole rows per 32 pieces only the row moves, by a fixed step
-  const long long klane = (lane / (DQK / 16)) * A.c.sk.r + lane % (DQK / 16) * 16;
-  const long long vlane = (lane / (DV / 16)) * A.c.sv.r + lane % (DV / 16) * 16;
-  auto fetch = [&](int i, uint32_t st) {   // tile i of the split into the stage at st; always one group
-    if (i < ntile) {
-      const int key = key0 + i * TILE;
-      const int page = meta[(key >> shift) - page0].x;
-      if (page >= 0) {
-        const uint8_t* ks = kbase + page * A.c.sk.p + (key & in_page) * A.c.sk.r;
-        const uint8_t* vs = vbase + page * A.c.sv.p + (key & in_page) * A.c.sv.r;
-        const bool inside = key >= J.klo && key + TILE - 1 <= J.khi;
-#pragma unroll
-        for (int k = 0; k < DQK / 32; ++k) {
-          const int n = lane + 32 * k, r = n / (DQK / 16), c = n % (DQK / 16);
-          const uint8_t* src = 32 % (DQK / 16) == 0 ? ks + klane + (32 / (DQK / 16)) * k * A.c.sk.r
-                                                    : ks + r * A.c.sk.r + c * 16;
-          const bool in = inside || (key + r >= J.klo && key + r <= J.khi);   // the rest reads as zero
-          cp_async16(st + k_off<DQK>(r, c), in ? src : ks, in ? 16 : 0);
-        }
-#pragma unroll
-        for (int k = 0; k < DV / 32; ++k) {
-          const int n = lane + 32 * k, r = n / (DV / 16), c = n % (DV / 16);
-          const bool in = inside || (key + r >= J.klo && key + r <= J.khi);
-          cp_async16(st + C::KB + v_off<DV>(r, c), in ? vs + vlane + (32 / (DV / 16)) * k * A.c.sv.r : vs, in ? 16 : 0);
-        }
-      }
-    }
-    cp_commit();
-  };
-
   constexpr int MT = DV / 16;     // tiles of 16 value columns
   float o[NT][MT][4];
   float mrow[NT][2], lrow[NT][2];
@@ -363,24 +408,46 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
   int unit = 0;                   // the accumulator counts in 2^unit
   const int itok0 = J.row0 / A.g, itok1 = (J.row0 + J.nrow - 1) / A.g;
 
-  uint32_t st_in = ring, st_out = ring;
-  auto next = [&](uint32_t st) { return st + C::STAGE == ring + C::RING ? ring : st + C::STAGE; };
-#pragma unroll
-  for (int s = 0; s < C::NST - 1; ++s) {
-    fetch(warp + s * NWARPS, st_in);
-    st_in = next(st_in);
-  }
+  int at_in = C::NST - 1, at_out = 0;
+  uint32_t parity = 0;
+  bool arrived = true;
   for (int i = warp; i < ntile; i += NWARPS) {
-    fetch(i + (C::NST - 1) * NWARPS, st_in);
-    st_in = next(st_in);
-    cp_wait<C::NST - 1>();
-    __syncwarp();
+    const int ahead = i + (C::NST - 1) * NWARPS;
+    if (lane == 0 && ahead < ntile) load(ahead, at_in, meta[((key0 + ahead * TILE) >> shift) - page0].x);
+    at_in = at_in + 1 == C::NST ? 0 : at_in + 1;
     const int key = key0 + i * TILE;
     const int2 mt = meta[(key >> shift) - page0];
-    const uint32_t st = st_out;
-    st_out = next(st_out);
+    const uint32_t st = ring + at_out * C::STAGE;
+    arrived = __all_sync(0xffffffffu, wait_bar(ptx::smem_u32(bars + at_out), parity));
+    if (!arrived) {
+      // give the copies still in flight as long again before the memory is used
+      for (int j = 0; j < C::NST && i + j * NWARPS < ntile; ++j) {
+        wait_bar(ptx::smem_u32(bars + at_out), parity);
+        if (++at_out == C::NST) {
+          at_out = 0;
+          parity ^= 1;
+        }
+      }
+      break;
+    }
+    if (++at_out == C::NST) {
+      at_out = 0;
+      parity ^= 1;
+    }
     if (mt.x >= 0) {
-      // S^T = K Q^T: keys g and g + 8, rows 2t and 2t + 1
+      const bool inside = key >= J.klo && key + TILE - 1 <= J.khi;
+      if (!inside) {
+        // rows that no query sees may hold anything: zero V there (masked
+        // scores make their weights 0, but 0 NaN is NaN)
+        for (int n = lane; n < TILE * (DV / 16); n += 32) {
+          const int r = n / (DV / 16), c = n % (DV / 16);
+          if (key + r < J.klo || key + r > J.khi)
+            *reinterpret_cast<uint4*>(smem + warp * C::RING + (st - ring) + C::KB + off<DV>(r, c)) = make_uint4(0, 0, 0, 0);
+        }
+        ptx::fence_proxy_async_smem();   // before the stage is refilled by TMA
+        __syncwarp();
+      }
+      // S^T = K Q^T: keys key_of(g) and 8 more, rows 2t and 2t + 1
       float s[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -388,7 +455,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
         for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
 #pragma unroll
       for (int c = 0; c < DQK / 64; ++c) {
-        const uint4 w0 = lds128(st + k_off<DQK>(g, t + 4 * c)), w1 = lds128(st + k_off<DQK>(8 + g, t + 4 * c));
+        const uint4 w0 = lds128(st + off<DQK>(key_of(g), t + 4 * c)), w1 = lds128(st + off<DQK>(8 + key_of(g), t + 4 * c));
         const uint32_t a0[4] = {w0.x, w0.y, w0.z, w0.w}, a1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -399,7 +466,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
         }
       }
       const float ks = exp2_int((int)(short)(mt.y & 0xffff));
-      const bool full = key >= J.klo && key + TILE - 1 <= J.khi &&
+      const bool full = inside &&
                         (mk.right < 0 || key + TILE - 1 <= (long long)itok0 + mk.off + mk.right) &&
                         (mk.left < 0 || key >= (long long)itok1 + mk.off - mk.left);
       if (!full) {
@@ -407,7 +474,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int kk = key + g + 8 * (k >> 1);
+            const int kk = key + key_of(g) + 8 * (k >> 1);
             if (kk < J.klo || kk > J.khi || !sees(mk, tok[n][k & 1], kk)) s[n][k] = -INFINITY;
           }
       }
@@ -464,8 +531,8 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
           pb[n][j] = transpose8x8(mul_h2(pack_h2(p0, p1), ratio_bits));
         }
       }
-      // O^T += V^T P^T: keys 2t, 2t + 1 and 8 more are this lane's rows of V;
-      // column tile j holds elements 2j (its rows 0-7) and 2j + 1 of each lane
+      // O^T += V^T P^T: keys key_of(2t), key_of(2t + 1) and 8 more are this lane's
+      // rows of V; column tile j holds elements 2j (its rows 0-7) and 2j + 1 of each lane
       // group's consecutive columns
       const uint32_t vt = st + C::KB;
       auto columns = [&](int j, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
@@ -481,18 +548,19 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
           mma16816(o[n][j + 1], c, pb[n][0], pb[n][1]);
         }
       };
+      const int v0 = key_of(2 * t), v1 = key_of(2 * t + 1);
       if (DV == 64) {
         const int c = g >> 1, h8 = (g & 1) * 8;
-        const uint2 w0 = lds64(vt + v_off<DV>(2 * t, c) + h8), w1 = lds64(vt + v_off<DV>(2 * t + 1, c) + h8);
-        const uint2 w2 = lds64(vt + v_off<DV>(2 * t + 8, c) + h8), w3 = lds64(vt + v_off<DV>(2 * t + 9, c) + h8);
+        const uint2 w0 = lds64(vt + off<DV>(v0, c) + h8), w1 = lds64(vt + off<DV>(v1, c) + h8);
+        const uint2 w2 = lds64(vt + off<DV>(v0 + 8, c) + h8), w3 = lds64(vt + off<DV>(v1 + 8, c) + h8);
         columns(0, w0.x, w1.x, w2.x, w3.x);
         columns(2, w0.y, w1.y, w2.y, w3.y);
       } else {
 #pragma unroll
         for (int half = 0; half < DV / 128; ++half) {
           const int c = g + 8 * half;
-          const uint4 w0 = lds128(vt + v_off<DV>(2 * t, c)), w1 = lds128(vt + v_off<DV>(2 * t + 1, c));
-          const uint4 w2 = lds128(vt + v_off<DV>(2 * t + 8, c)), w3 = lds128(vt + v_off<DV>(2 * t + 9, c));
+          const uint4 w0 = lds128(vt + off<DV>(v0, c)), w1 = lds128(vt + off<DV>(v1, c));
+          const uint4 w2 = lds128(vt + off<DV>(v0 + 8, c)), w3 = lds128(vt + off<DV>(v1 + 8, c));
           columns(8 * half, w0.x, w1.x, w2.x, w3.x);
           columns(8 * half + 2, w0.y, w1.y, w2.y, w3.y);
           columns(8 * half + 4, w0.z, w1.z, w2.z, w3.z);
@@ -502,7 +570,11 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
     }
     __syncwarp();   // the stage may be refilled
   }
-  cp_wait<0>();
+  if (!arrived) {   // a load did not arrive: no result instead of a wrong one
+    *s_bad = 2;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) lrow[n][0] = lrow[n][1] = __int_as_float(0x7fc00000);
+  }
 
   // join the warps: maxima and sums, then each warp's O under the common maximum
 #pragma unroll
@@ -538,6 +610,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
             make_float4(o[n][j][r] * a, o[n][j][2 + r] * a, o[n][j + 1][r] * a, o[n][j + 1][2 + r] * a);
     }
   __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const bool whole = J.ntile <= A.split_tiles;   // no other split holds keys of these rows
   const long long part = ((long long)(b * A.c.hkv + hk) * A.mtiles + m) * A.nsplit + split;
   for (int i = tid; i < J.nrow * (DV / 4); i += NTHREADS) {
@@ -562,40 +635,43 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
     }
   }
   if (reports && tid == 0)
-    A.status[b * A.nsplit + split] = J.bad ? ATTN_ERR_BAD_SEQLENS : *s_bad ? ATTN_ERR_BAD_PAGE : ATTN_OK;
+    A.status[b * A.nsplit + split] = *s_bad == 2 ? ATTN_ERR_TIMEOUT : J.bad ? ATTN_ERR_BAD_SEQLENS : *s_bad ? ATTN_ERR_BAD_PAGE : ATTN_OK;
 }
 
 // Joins the splits of a row in a fixed order: O = sum 2^(m_s - m) O_s / sum
 // 2^(m_s - m) l_s.  A CTA takes one row; DV / 4 threads cover its columns, and
-// the thread groups take the splits in turn.
+// the thread groups take the splits in turn: blockDim.x follows their number.
+constexpr int JOIN_THREADS = 512;   // at most
+
 template <int DV, int NT, typename T>
-__global__ void __launch_bounds__(NTHREADS) join_kernel(const Args A) {
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Args A) {
   constexpr int ROWS = 8 * NT;
-  constexpr int COLS = DV / 4, GROUPS = NTHREADS / COLS;
-  __shared__ float4 s_v[GROUPS][COLS];
-  __shared__ float s_l[GROUPS];
-  __shared__ float s_top[NTHREADS / 32];
-  const int job = blockIdx.x / ROWS, row = blockIdx.x % ROWS;
+  constexpr int COLS = DV / 4;
+  __shared__ float4 s_v[JOIN_THREADS / COLS][COLS];
+  __shared__ float s_l[JOIN_THREADS / COLS];
+  __shared__ float s_top[JOIN_THREADS / 32];
+  const int groups = blockDim.x / COLS, nw = blockDim.x / 32;
+  const int job = blockIdx.x / A.job_rows, row = blockIdx.x % A.job_rows;
   const int grp = threadIdx.x / COLS, col = threadIdx.x % COLS, c = col * 4;
   const int m = job % A.mtiles, bh = job / A.mtiles, hk = bh % A.c.hkv, b = bh / A.c.hkv;
   MaskArgs mk;
   const Job J = make_job<ROWS>(A, b, m, mk);
   if (row >= J.nrow || J.ntile <= A.split_tiles) return;
   const int n = cdiv(J.ntile, A.split_tiles);
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // launched early: the splits' kernel ends here
   const float2* ml = A.part_ml + (long long)job * A.nsplit * ROWS + row;
   const float* po = A.part_o + ((long long)job * A.nsplit * ROWS + row) * DV + c;
   float top = -INFINITY;
-  for (int s = threadIdx.x; s < n; s += NTHREADS) top = fmaxf(top, ml[s * ROWS].x);
+  for (int s = threadIdx.x; s < n; s += blockDim.x) top = fmaxf(top, ml[s * ROWS].x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < NTHREADS / 32; ++w) top = fmaxf(top, s_top[w]);
+  for (int w = 0; w < nw; ++w) top = fmaxf(top, s_top[w]);
   float l = 0.f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int s = grp; s < n; s += GROUPS) {
+  for (int s = grp; s < n; s += groups) {
     const float2 x = ml[s * ROWS];
     const float4 y = *reinterpret_cast<const float4*>(po + (long long)s * ROWS * DV);
     // a split that saw no key of the row holds zeros (or NaN, which stays)
@@ -607,8 +683,8 @@ __global__ void __launch_bounds__(NTHREADS) join_kernel(const Args A) {
   if (col == 0) s_l[grp] = l;
   __syncthreads();
   if (grp == 0) {
-#pragma unroll
-    for (int w = 1; w < GROUPS; ++w) {
+    const int used = min(groups, n);
+    for (int w = 1; w < used; ++w) {
       const float4 y = s_v[w][col];
       v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
       l += s_l[w];
@@ -620,9 +696,10 @@ __global__ void __launch_bounds__(NTHREADS) join_kernel(const Args A) {
 // ---------------------------------------------------------------- host side
 
 struct Layout {
-  int nt, mtiles, nsplit, split_tiles;
+  int nt, mtiles, job_rows, nsplit, split_tiles;
   long long jobs;
-  size_t off_status, off_ml, off_o, total;
+  size_t off_status, off_ml, off_o, off_long, total;
+  KvLong lng;
 };
 
 static int max_keys(const attn_kv_fwd_params& p) {
@@ -630,18 +707,18 @@ static int max_keys(const attn_kv_fwd_params& p) {
   return (int)(cap < p.max_seqlen_k ? cap : p.max_seqlen_k);
 }
 
-// Splits: enough CTAs to fill the GPU a few times over, none shorter than
-// MIN_TILES tiles.
 static Layout layout(const attn_kv_fwd_params& p) {
   Layout L{};
   const int g = p.nhead_q / p.cache.nhead_kv;
-  const long long rows = (long long)(p.max_seqlen_q > 0 ? p.max_seqlen_q : 1) * g;
+  L.lng = kv_long_layout(p, max_keys(p));
+  const int most = p.max_seqlen_q < L.lng.from ? p.max_seqlen_q : L.lng.from;   // query tokens of this path
+  const long long rows = (long long)(most > 0 ? most : 1) * g;
   L.nt = rows <= 8 ? 1 : 2;
   L.mtiles = (int)cdiv_ll(rows, 8 * L.nt);
+  L.job_rows = (int)(rows < 8 * L.nt ? rows : 8 * L.nt);
   L.jobs = (long long)p.batch * p.cache.nhead_kv * L.mtiles;
   const int tiles = max_keys(p) / TILE + 2;
-  const long long want = SMS * 6;
-  long long n = cdiv_ll(want, L.jobs);
+  long long n = L.jobs >= WAVE ? cdiv(tiles, EVEN_TILES) : WAVE / L.jobs;
   if (n > cdiv(tiles, MIN_TILES)) n = cdiv(tiles, MIN_TILES);
   if (n < cdiv(tiles, MAX_TILES)) n = cdiv(tiles, MAX_TILES);
   L.split_tiles = cdiv(cdiv(tiles, (int)n), NWARPS) * NWARPS;
@@ -656,7 +733,8 @@ static Layout layout(const attn_kv_fwd_params& p) {
   o = up(o + parts * 8 * L.nt * sizeof(float2));
   L.off_o = o;
   o = up(o + parts * 8 * L.nt * p.cache.d_v * sizeof(float));
-  L.total = o;
+  L.off_long = o;
+  L.total = o + L.lng.total;
   return L;
 }
 
@@ -683,14 +761,56 @@ static int validate_sizes(const attn_kv_fwd_params* p) {
   return ATTN_OK;
 }
 
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// The cache as (d, heads, rows of a page, pages), boxes of one head's 16 rows.
+template <int D>
+static bool make_map(CUtensorMap* m, const void* base, const KvCacheView& c, const KvStrides& s) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {D, (cuuint64_t)c.hkv, (cuuint64_t)1 << c.page_shift, (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)s.h, (cuuint64_t)s.r, (cuuint64_t)s.p};
+  const cuuint32_t box[4] = {Box<D>::W, 1, TILE, 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, Box<D>::W == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DQK, int DV, int NT, typename T>
 static int launch(const Args& a, long long jobs, cudaStream_t st) {
   using C = Cfg<DQK, DV, NT>;
+  Maps maps;
+  if (!make_map<DQK>(&maps.k, a.c.k, a.c, a.c.sk) || !make_map<DV>(&maps.v, a.c.v, a.c, a.c.sv)) return ATTN_ERR_CUDA;
   auto kern = kv_fwd_kernel<DQK, DV, NT, T>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return ATTN_ERR_CUDA;
-  kern<<<(unsigned)(jobs * a.nsplit), NTHREADS, C::SMEM, st>>>(a);
-  if (a.nsplit > 1) join_kernel<DV, NT, T><<<(unsigned)(jobs * C::ROWS), NTHREADS, 0, st>>>(a);
+  kern<<<(unsigned)(jobs * a.nsplit), NTHREADS, C::SMEM, st>>>(maps, a);
+  if (a.nsplit > 1) {
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(jobs * a.job_rows));
+    int threads = NTHREADS;   // about four splits to a thread group
+    while (threads < JOIN_THREADS && threads / (DV / 4) * 4 < a.nsplit) threads *= 2;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, join_kernel<DV, NT, T>, a) != cudaSuccess) return ATTN_ERR_CUDA;
+  }
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -747,9 +867,12 @@ static int run(const attn_kv_fwd_params* p, void* ws, size_t ws_bytes, cudaStrea
   a.nsplit = L.nsplit;
   a.split_tiles = L.split_tiles;
   a.mtiles = L.mtiles;
+  a.long_from = L.lng.from;
+  a.job_rows = L.job_rows;
   a.status = reinterpret_cast<int*>(w + L.off_status);
   a.part_ml = reinterpret_cast<float2*>(w + L.off_ml);
   a.part_o = reinterpret_cast<float*>(w + L.off_o);
+  if (L.lng.slots > 0 && (s = launch_kv_long(*p, a.c, a.sq, a.so, a.max_k, L.lng, w + L.off_long, st)) != ATTN_OK) return s;
   if (p->dtype == ATTN_BF16) return launch_dims<__nv_bfloat16>(a, L, dqk, dv, st);
   return launch_dims<__half>(a, L, dqk, dv, st);
 }
@@ -781,16 +904,18 @@ extern "C" int attn_kv_fwd_read_status(const attn_kv_fwd_params* p, const void* 
   if (workspace_bytes < L.total) return ATTN_ERR_WORKSPACE_TOO_SMALL;
   *status = ATTN_OK;
   if (cudaStreamSynchronize(stream) != cudaSuccess) return ATTN_ERR_CUDA;
-  // request by request in pieces that fit the stack (no allocation in this library)
+  // in pieces that fit the stack (this library allocates nothing)
   int part[1024];
-  const long long n = (long long)p->batch * L.nsplit;
-  for (long long i = 0; i < n; i += 1024) {
-    const size_t k = (size_t)(n - i < 1024 ? n - i : 1024);
-    if (cudaMemcpy(part, static_cast<const char*>(workspace) + L.off_status + i * sizeof(int), k * sizeof(int),
-                   cudaMemcpyDeviceToHost) != cudaSuccess)
-      return ATTN_ERR_CUDA;
-    for (size_t j = 0; j < k; ++j)
-      if (part[j] != ATTN_OK && *status == ATTN_OK) *status = part[j];
-  }
+  const char* words[2] = {static_cast<const char*>(workspace) + L.off_status,
+                          static_cast<const char*>(workspace) + L.off_long + kv_long_status_offset(L.lng)};
+  const long long count[2] = {(long long)p->batch * L.nsplit, L.lng.slots};
+  for (int a = 0; a < 2; ++a)
+    for (long long i = 0; i < count[a]; i += 1024) {
+      const size_t k = (size_t)(count[a] - i < 1024 ? count[a] - i : 1024);
+      if (cudaMemcpy(part, words[a] + i * sizeof(int), k * sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
+        return ATTN_ERR_CUDA;
+      for (size_t j = 0; j < k; ++j)
+        if (part[j] != ATTN_OK && *status == ATTN_OK) *status = part[j];
+    }
   return ATTN_OK;
 }

@@ -562,10 +562,16 @@ int attn_kv_append(const attn_kv_append_params* p, cudaStream_t stream);
  * O = 0 and LSE = -inf; rows of no segment are left as they were.
  * Lengths and pages are checked on the device: a segment outside q counts as
  * empty, seqlens_k is limited to 0 .. min(max_seqlen_k, max_blocks pages), the
- * tokens of a page outside the cache are masked, and attn_kv_fwd_read_status
- * reports it.  Cache rows past seqlens_k (or, for single-token segments,
- * outside the mask) never reach a result, whatever they hold; other masked
- * values must be finite. */
+ * tokens of a page outside the cache are masked (in a long segment, below, all
+ * tokens are), and attn_kv_fwd_read_status reports it.  Cache rows past
+ * seqlens_k (or, for single-token segments, outside the mask) never reach a
+ * result, whatever they hold; other masked values must be finite.
+ * Segments of more than 24 + 96 / (nhead_q / nhead_kv) query tokens (d_qk below
+ * 256, positive softmax_scale) are long: their keys and values are expanded to
+ * the type of q in the workspace and attn_fwd's tensor-core kernel runs on
+ * them, its softmax weights rounded to that type (with FP16, cache values past
+ * 65504 are clamped to it); other weights are rounded to 11 bits.  One call may
+ * mix both kinds.  Long segments must not overlap one another in q. */
 typedef struct {
   int32_t dtype;          /* ATTN_BF16 or ATTN_FP16: type of q and o               */
   int32_t batch;          /* segments, >= 1                                        */

@@ -277,7 +277,17 @@ ATTEND = [
     (16, [400, 200], [1, 1], 1, 33, 2, -1, -1),              # more heads in a group than one row tile
     (256, [5000], [1], 2, 8, 2, -1, -1),
     (16, [9000, 100], [1, 2], 1, 4, 2, -1, -1),              # many splits, and one
+    (16, [300, 1000, 40, 0, 129], [130, 1, 32, 50, 129], 2, 4, 2, -1, -1),   # long and short segments together
+    (32, [700, 33], [200, 33], 1, 2, 3, 150, 3),
+    (64, [128, 600], [300, 129], 2, 1, 0, -1, -1),           # cross attention of a prompt
 ]
+
+
+def weights(dtype, longest):
+    """Type that the softmax weights are rounded to: fp16, and for long segments
+    (from 25 tokens on at the earliest: 16-bit products on expanded keys) the
+    type of q."""
+    return dtype if longest > 24 else torch.float16
 
 
 def attend_case(dqk, dv, dtype, page, lens, new, hkv, group, seed=0, q_scale=1.0):
@@ -302,7 +312,7 @@ def test_attend(B, dqk, dv, dtype, page, lens, new, hkv, group, mask, left, righ
                                mask=mask, left=left, right=right, max_seqlen_q=max(new), max_seqlen_k=max(lens),
                                check_status=True)
     ref = kv_ref.attend(q, cu, lens, table, kc, vc, ke, ve, scale, mask, left, right)
-    check_attend(o, lse, ref, dtype, dqk, max(lens), what=f"{page} {lens} {new}")
+    check_attend(o, lse, ref, dtype, dqk, max(lens), weights(dtype, max(new)), what=f"{page} {lens} {new}")
 
 
 @pytest.mark.parametrize("scale", [-0.1, 3.0, 1e-6])
@@ -418,6 +428,42 @@ def test_attend_reports_bad_lengths_and_pages(B):
     check_attend(o, lse, ref, torch.bfloat16, 64, 90)
 
 
+def test_attend_long_segments_in_groups(B):
+    """Expanded keys that do not fit the workspace's limit at once: max_seqlen_k
+    of 2^18 at 8 heads of 128 + 128 columns is 1 GiB for each of three segments.
+    A page outside the cache empties the keys of its (long) segment only."""
+    lens, new, page, d = [200, 190, 1, 333], [164, 190, 1, 140], 16, 128
+    q, table, kc, vc, ke, ve, cu = attend_case(d, d, torch.bfloat16, page, lens, new, 8, 1)
+    cols = 2 ** 18 // page
+    wide = torch.full((4, cols), -1, dtype=I32)
+    wide[:, : len(table[0])] = torch.tensor(table, dtype=I32)
+    c = handle(B, kc, vc, ke, ve)
+    kw = dict(scale=0.1, max_seqlen_q=190, max_seqlen_k=2 ** 18)
+    o, lse = B.attn_kv_forward(q.cuda(), c, wide.cuda(), dev(lens), dev(cu), check_status=True, **kw)
+    ref = kv_ref.attend(q, cu, lens, table, kc, vc, ke, ve, 0.1, 2)
+    check_attend(o, lse, ref, torch.bfloat16, d, 333, torch.bfloat16)
+    wide[1, 2] = kc.shape[0] + 5
+    with pytest.raises(B.AttnError) as e:
+        B.attn_kv_forward(q.cuda(), c, wide.cuda(), dev(lens), dev(cu), check_status=True, **kw)
+    assert e.value.status == B.ATTN_ERR_BAD_PAGE
+    o, lse = B.attn_kv_forward(q.cuda(), c, wide.cuda(), dev(lens), dev(cu), **kw)
+    ref = kv_ref.attend(q, cu, [200, 0, 1, 333], table, kc, vc, ke, ve, 0.1, 2)
+    check_attend(o, lse, ref, torch.bfloat16, d, 333, torch.bfloat16)
+
+
+def test_attend_long_segments_overlapping(B):
+    """Padded starts that make long segments overlap: reported, nothing outside
+    the declared rows touched."""
+    lens, new = [80, 80, 80], [80, 80, 80]
+    q, table, kc, vc, ke, ve, cu = attend_case(64, 64, torch.bfloat16, 16, lens, new, 1, 2)
+    starts = dev([0, 5, 10, 90])
+    out = torch.full((90, 2, 64), 3.0, dtype=torch.bfloat16, device="cuda"), torch.zeros((2, 90), device="cuda")
+    with pytest.raises(B.AttnError) as e:
+        B.attn_kv_forward(q[:90].cuda(), handle(B, kc, vc, ke, ve), dev(table), dev(lens), dev(cu), scale=0.1,
+                          max_seqlen_q=80, max_seqlen_k=80, cu_seqlens_q_padded=starts, out=out, check_status=True)
+    assert e.value.status == B.ATTN_ERR_BAD_SEQLENS
+
+
 def test_attend_repeats_and_streams(B):
     """The same bits on every run, from two calls in flight on two streams, and
     from a captured graph replayed on new lengths."""
@@ -512,4 +558,4 @@ def test_serving_steps(B, graph):
             assert torch.equal(got.view(torch.uint8).cpu(), ref)
         if n:
             ref = kv_ref.attend(rq.cpu()[:n], cu, lens, table, kc, vc, ke, ve, scale, 2)
-            check_attend(o[:n], lse[:, :n], ref, dtype, d, max(lens))
+            check_attend(o[:n], lse[:, :n], ref, dtype, d, max(lens), weights(dtype, max(new)))
