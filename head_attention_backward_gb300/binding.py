@@ -9,10 +9,10 @@ not been built: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
-import dataclasses
 import math
 import os
-from typing import Optional
+import struct
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -450,54 +450,93 @@ def attn_backward(q, k, v, o, do, lse, *, scale, mask=MASK_NONE, left=-1, right=
 
 # ------------------------------------------- rotary positions and the cache
 #
-# These run once per layer or step of a serving loop, so they check shapes,
-# types and devices (an AttnError or ValueError before any launch) and fill
-# their struct in one go; nothing synchronises unless asked to.
+# These run once per layer or step of a serving loop, often for a few
+# microseconds of device time, so the marshalling is kept short: each tensor's
+# attributes are read once, the whole argument struct is packed in one go (the
+# layouts below are those of the ctypes mirrors above), and what is wrong is
+# only worked out once something is.
 
-def _need(t: torch.Tensor, what: str, dtypes, shape=None, device=None):
+_F16 = (torch.bfloat16, torch.float16)
+_FLOATS = tuple(_DTYPES)
+_BYTES = (torch.float8_e4m3fn, torch.uint8)
+_I32, _I64 = torch.int32, torch.int64
+_current_device = torch._C._cuda_getDevice
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+
+_ROPE = struct.Struct("<10i Q 3q 2Q 4Q 12q")
+_CACHE = struct.Struct("<6i 4Q 6q")
+_PLAN = struct.Struct("<6i 4Q q 7Q")
+_APPEND = struct.Struct("<2i 2Q 6q Q")
+_FWD = struct.Struct("<10i f i 4Q q 3Q 6q")
+for _s, _c, _tail in ((_ROPE, AttnRopeParams, 0), (_CACHE, AttnKvCache, 0), (_PLAN, AttnKvPlanParams, 0),
+                      (_APPEND, AttnKvAppendParams, 1), (_FWD, AttnKvFwdParams, 1)):
+    assert _s.size + (_tail and _CACHE.size) == ctypes.sizeof(_c), _c
+
+
+def _entry(name: str, nargs: int):
+    """The library's function `name` for packed structs (bytes)."""
+    global _entries
+    f = load()[name]
+    f.argtypes = [_vp] * nargs
+    f.restype = ctypes.c_int
+    _entries[name] = f
+    return f
+
+
+_entries = {}
+
+
+def _check(t: torch.Tensor, what: str, dtypes, shape=None, device=None):
+    """Raises ValueError if t is not of these types, shape and device."""
     if t.dtype not in dtypes:
         raise ValueError(f"{what}: dtype {t.dtype} is not one of {tuple(dtypes)}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{what} must be on {device or 'a CUDA device'}, not on {t.device}")
+    if not t.is_cuda or (device is not None and t.get_device() != device):
+        raise ValueError(f"{what} must be on cuda:{device if device is not None else '?'}, not on {t.device}")
 
 
-def _ints(t: torch.Tensor, what: str, n: int, device, dtype=torch.int32) -> int:
-    """Address of a contiguous vector of n whole numbers on `device`."""
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1) or t.device != device:
-        raise ValueError(f"{what} must be a contiguous {dtype} vector of {n} on {device}")
+def _vector(t: torch.Tensor, what: str, n: int, index: int, dtype=_I32) -> int:
+    """Address of a contiguous vector of n whole numbers on device `index`."""
+    if t.dtype is not dtype or t.get_device() != index or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous {dtype} vector of {n} on cuda:{index}; "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-_F16 = (torch.bfloat16, torch.float16)
-_FLOATS = tuple(_DTYPES)
+def _rows3(t: torch.Tensor, what: str):
+    """{0, row, head} strides of a [T, H, D] tensor; a dimension of one entry
+    may carry any stride, so it is given the contiguous one."""
+    row, head, one = t.stride()
+    n, h, d = t.shape
+    if one != 1 and d > 1:
+        raise ValueError(f"{what}: the head dimension must be contiguous (stride 1)")
+    if h == 1:
+        head = d
+    return 0, (row if n > 1 else h * head), head
 
 
-class _Launch:
-    """The stream of a call and its outputs: with an explicit stream the
-    outputs are allocated on it, so the allocator does not hand their memory to
-    other work while the kernels may still write it."""
+def _on(index: int, stream):
+    """(raw stream, context for allocations) of a call on device `index`.  With
+    an explicit stream the outputs are allocated on it, so that the allocator
+    does not hand their memory to other work while the kernels may still write
+    it."""
+    if index != _current_device():
+        raise ValueError(f"tensors on device {index}, but the current device is {_current_device()}")
+    raw = _current_raw_stream(index)
+    if stream is None:
+        return raw, None
+    want = _stream(stream)
+    if want == raw:
+        return raw, None
+    return want, torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(want))
 
-    __slots__ = ("device", "stream", "guard")
 
-    def __init__(self, device: torch.device, stream):
-        if device.index != torch.cuda.current_device():
-            raise ValueError(f"tensors on {device}, but the current device is {torch.cuda.current_device()}")
-        self.device, self.guard = device, None
-        if stream is None:
-            self.stream = torch.cuda.current_stream().cuda_stream
-        else:
-            self.stream = _stream(stream)
-            if self.stream != torch.cuda.current_stream().cuda_stream:
-                self.guard = torch.cuda.stream(torch.cuda.ExternalStream(self.stream, device=device)
-                                               if not hasattr(stream, "cuda_stream") else stream)
-
-    def empty(self, shape, dtype):
-        if self.guard is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with self.guard:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+def _empty(shape, dtype, device, ctx):
+    if ctx is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with ctx:
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0) -> torch.Tensor:
@@ -515,47 +554,70 @@ def rope(q, k, positions, inv_freq, *, pair_axis=None, interleaved=False, invers
     axes; inv_freq and pair_axis are host tensors (float64 and uint8,
     rot_dim / 2 entries).  inverse=True is the gradient: rope(dq, dk, ...,
     inverse=True) after attn_backward."""
-    _need(q, "q", _FLOATS)
-    dev = q.device
-    if q.dim() not in (3, 4):
+    dtype, index, qs = q.dtype, q.get_device(), q.shape
+    code, packed = _DTYPES.get(dtype), len(qs) == 3
+    if code is None or index < 0 or not (packed or len(qs) == 4):
+        _check(q, "q", _FLOATS)
         raise ValueError("q must be [T, H, D] or [B, S, H, D]")
-    rows = q.shape[:-2]
-    if k is not None:
-        _need(k, "k", (q.dtype,), (*rows, k.shape[-2], q.shape[-1]), dev)
-    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    if packed:
+        batch, (seqlen, heads, dim) = 1, qs
+    else:
+        batch, seqlen, heads, dim = qs
+    if (inv_freq.dtype is not torch.float64 or inv_freq.get_device() >= 0 or inv_freq.dim() != 1
+            or not inv_freq.is_contiguous()):
         raise ValueError("inv_freq must be a contiguous float64 vector on the host")
     half = inv_freq.shape[0]
-    if pair_axis is not None and (pair_axis.dtype != torch.uint8 or pair_axis.is_cuda or pair_axis.shape != (half,)
-                                  or not pair_axis.is_contiguous()):
-        raise ValueError("pair_axis must be a contiguous uint8 vector on the host, as long as inv_freq")
-    if positions.shape == rows:
-        n_axes, sp = 1, (0, *positions.stride())
-    elif positions.shape[1:] == rows:
-        n_axes, sp = positions.shape[0], positions.stride()
+    axis_ptr = 0
+    if pair_axis is not None:
+        if (pair_axis.dtype is not torch.uint8 or pair_axis.get_device() >= 0 or pair_axis.shape != (half,)
+                or not pair_axis.is_contiguous()):
+            raise ValueError("pair_axis must be a contiguous uint8 vector on the host, as long as inv_freq")
+        axis_ptr = pair_axis.data_ptr()
+    # strides {axis, batch entry, row}
+    ps, sp = positions.shape, positions.stride()
+    n_axes = 1
+    if ps == qs[:-2]:
+        sp = (0, 0, *sp) if packed else (0, *sp)
+    elif ps[1:] == qs[:-2]:
+        n_axes = ps[0]
+        if packed:
+            sp = (sp[0], 0, sp[1])
     else:
-        raise ValueError(f"positions {tuple(positions.shape)} do not fit rows {tuple(rows)}")
-    _need(positions, "positions", (torch.int32,), None, dev)
-    L = _Launch(dev, stream)
-    if out is None:
-        qo = L.empty(q.shape, q.dtype)
-        ko = None if k is None else L.empty(k.shape, k.dtype)
-    else:
+        raise ValueError(f"positions {tuple(ps)} do not fit rows {tuple(qs[:-2])}")
+    if positions.dtype is not _I32 or positions.get_device() != index:
+        _check(positions, "positions", (_I32,), None, index)
+    raw, ctx = _on(index, stream)
+    if out is not None:
         qo, ko = out
-        _need(qo, "out[0]", (q.dtype,), q.shape, dev)
+        _check(qo, "out[0]", (dtype,), qs, index)
         if k is not None:
-            _need(ko, "out[1]", (q.dtype,), k.shape, dev)
-    group = len(rows) == 1
-    if group:
-        sp = (sp[0], 0, sp[1])
-    zero = (0, 0, 0)
-    p = AttnRopeParams(
-        _DTYPES[q.dtype], 1 if group else rows[0], rows[-1], q.shape[-2], 0 if k is None else k.shape[-2],
-        q.shape[-1], 2 * half, n_axes, 1 if interleaved else 0, 1 if inverse else 0, positions.data_ptr(),
-        _i64x3(*sp), inv_freq.data_ptr(), None if pair_axis is None else pair_axis.data_ptr(),
-        q.data_ptr(), None if k is None else k.data_ptr(), qo.data_ptr(), None if k is None else ko.data_ptr(),
-        _i64x3(*_strides(q, group)), _i64x3(*(zero if k is None else _strides(k, group))),
-        _i64x3(*_strides(qo, group)), _i64x3(*(zero if k is None else _strides(ko, group))))
-    st = attn_rope(p, L.stream)
+            _check(ko, "out[1]", (dtype,), k.shape, index)
+    elif ctx is None:
+        qo, ko = torch.empty_like(q), None if k is None else torch.empty_like(k)
+    else:
+        with ctx:
+            qo, ko = torch.empty_like(q), None if k is None else torch.empty_like(k)
+    sq, so = q.stride(), qo.stride()
+    if sq[-1] != 1 or so[-1] != 1:
+        raise ValueError("the head dimension must be contiguous (stride 1)")
+    nk, kp, kop, sk, sko = 0, 0, 0, (0, 0, 0, 1), (0, 0, 0, 1)
+    if k is not None:
+        ks = k.shape
+        nk = ks[-2]
+        if k.dtype is not dtype or k.get_device() != index or ks[-1] != dim or ks[:-2] != qs[:-2]:
+            _check(k, "k", (dtype,), (*qs[:-2], nk, dim), index)
+        kp, kop, sk, sko = k.data_ptr(), ko.data_ptr(), k.stride(), ko.stride()
+        if sk[-1] != 1 or sko[-1] != 1:
+            raise ValueError("the head dimension must be contiguous (stride 1)")
+        if packed:
+            sk, sko = (0, *sk), (0, *sko)
+    if packed:
+        sq, so = (0, *sq), (0, *so)
+    p = _ROPE.pack(code, batch, seqlen, heads, nk, dim, 2 * half, n_axes, 1 if interleaved else 0,
+                   1 if inverse else 0, positions.data_ptr(), *sp, inv_freq.data_ptr(), axis_ptr, q.data_ptr(), kp,
+                   qo.data_ptr(), kop, sq[0], sq[1], sq[2], sk[0], sk[1], sk[2], so[0], so[1], so[2], sko[0], sko[1],
+                   sko[2])
+    st = (_entries.get("attn_rope") or _entry("attn_rope", 2))(p, raw)
     if st != 0:
         raise AttnError(st, "attn_rope")
     return qo, (None if k is None else ko)
@@ -565,23 +627,30 @@ class KvCache:
     """Handle of a paged 8-bit cache (attn_kv_cache): k [pages, page_size,
     kv heads, d_qk] and v [..., d_v] as torch.float8_e4m3fn (or uint8), any
     strides with a contiguous head dimension, and the scale exponents k_exp,
-    v_exp uint8 [pages, kv heads].  Keep it next to the tensors it holds."""
+    v_exp uint8 [pages, kv heads].  It keeps the tensors and their packed
+    description; make it once per cache."""
+
+    __slots__ = ("k", "v", "k_exp", "v_exp", "num_pages", "page_size", "nhead_kv", "d_qk", "d_v", "index", "packed")
 
     def __init__(self, k, v, k_exp, v_exp):
-        pages, size, heads, dqk = k.shape
-        _need(k, "k", (torch.float8_e4m3fn, torch.uint8))
-        _need(v, "v", (k.dtype,), (pages, size, heads, v.shape[-1]), k.device)
-        for name, e in (("k_exp", k_exp), ("v_exp", v_exp)):
-            _need(e, name, (torch.uint8,), (pages, heads), k.device)
-            if not e.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-        if k.stride(3) != 1 or v.stride(3) != 1:
+        index, ks, vs = k.get_device(), k.shape, v.shape
+        pages, size, heads, dqk = ks
+        dv = vs[3]
+        sk, sv = k.stride(), v.stride()
+        if (index < 0 or k.dtype not in _BYTES or v.dtype is not k.dtype or vs != (pages, size, heads, dv)
+                or v.get_device() != index or sk[3] != 1 or sv[3] != 1):
+            _check(k, "k", _BYTES)
+            _check(v, "v", (k.dtype,), (pages, size, heads, dv), index)
             raise ValueError("the head dimension must be contiguous (stride 1)")
+        es = (pages, heads)
+        for name, e in (("k_exp", k_exp), ("v_exp", v_exp)):
+            if e.dtype is not torch.uint8 or e.get_device() != index or e.shape != es or not e.is_contiguous():
+                _check(e, name, (torch.uint8,), es, index)
+                raise ValueError(f"{name} must be contiguous")
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
-        self.num_pages, self.page_size, self.nhead_kv, self.d_qk, self.d_v = pages, size, heads, dqk, v.shape[-1]
-        self.device = k.device
-        self.params = AttnKvCache(pages, size, heads, dqk, self.d_v, 0, k.data_ptr(), v.data_ptr(), k_exp.data_ptr(),
-                                  v_exp.data_ptr(), _i64x3(*k.stride()[:3]), _i64x3(*v.stride()[:3]))
+        self.num_pages, self.page_size, self.nhead_kv, self.d_qk, self.d_v, self.index = pages, size, heads, dqk, dv, index
+        self.packed = _CACHE.pack(pages, size, heads, dqk, dv, 0, k.data_ptr(), v.data_ptr(), k_exp.data_ptr(),
+                                  v_exp.data_ptr(), sk[0], sk[1], sk[2], sv[0], sv[1], sv[2])
 
     @classmethod
     def empty(cls, num_pages, page_size, nhead_kv, d_qk, d_v, device="cuda"):
@@ -592,8 +661,7 @@ class KvCache:
         return cls(k, v, *e)
 
 
-@dataclasses.dataclass
-class KvPlan:
+class KvPlan(NamedTuple):
     """What attn_kv_plan computes: packed segment offsets, the requests' new
     lengths, one position and slot per token, the free pages left, the status
     word (0 = ATTN_OK), all on the device."""
@@ -611,6 +679,15 @@ class KvPlan:
             raise AttnError(s, "attn_kv_plan (device status)")
 
 
+def _table(t: torch.Tensor, n: int, index: int):
+    """(columns, row stride) of an int32 [n, columns] block table."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not _I32 or t.get_device() != index or len(shape) != 2 or shape[0] != n or stride[1] != 1:
+        _check(t, "block_table", (_I32,), (n, shape[-1]), index)
+        raise ValueError("block_table rows must be contiguous")
+    return shape[1], (stride[0] if n > 1 else shape[1])
+
+
 def kv_plan(new_lens, seqlens, block_table, free_pages, free_count, *, page_size, max_tokens, out=None, stream=None):
     """Pages, positions and slots for one step (attn_kv_plan).  new_lens and
     seqlens int32 [B] (KV_RELEASE ends a request), block_table int32
@@ -618,26 +695,29 @@ def kv_plan(new_lens, seqlens, block_table, free_pages, free_count, *, page_size
     free_count int32 [1].  Returns a KvPlan, `out` itself when given: its
     seqlens and free_count may be the inputs', so that a captured call
     advances its state at every replay."""
-    dev, n = new_lens.device, new_lens.shape[0]
-    _need(block_table, "block_table", (torch.int32,), (n, block_table.shape[-1]), dev)
-    if block_table.stride(1) != 1:
-        raise ValueError("block_table rows must be contiguous")
-    L = _Launch(dev, stream)
+    index, n = new_lens.get_device(), new_lens.shape[0]
+    pages = free_pages.shape[0]
+    cols, row = _table(block_table, n, index)
+    new_p, len_p = _vector(new_lens, "new_lens", n, index), _vector(seqlens, "seqlens", n, index)
+    free_p, count_p = _vector(free_pages, "free_pages", pages, index), _vector(free_count, "free_count", 1, index)
+    raw, ctx = _on(index, stream)
     if out is None:
-        # two blocks for six vectors: the positions and other words, the slots
-        ints = L.empty((2 * n + 3 + max_tokens,), torch.int32)
-        a, b, c, d, e = ints.split((n + 1, n, 1, 1, max_tokens))
-        out = KvPlan(a, b, e, L.empty((max_tokens,), torch.int64), c, d)
-    p = AttnKvPlanParams(
-        n, page_size, free_pages.shape[0], block_table.shape[1], max_tokens, 0,
-        _ints(new_lens, "new_lens", n, dev), _ints(seqlens, "seqlens", n, dev),
-        _ints(out.seqlens, "out.seqlens", n, dev), block_table.data_ptr(),
-        block_table.stride(0) if n > 1 else block_table.shape[1],
-        _ints(free_pages, "free_pages", free_pages.shape[0], dev), _ints(free_count, "free_count", 1, dev),
-        _ints(out.free_count, "out.free_count", 1, dev), _ints(out.cu_seqlens, "out.cu_seqlens", n + 1, dev),
-        _ints(out.positions, "out.positions", max_tokens, dev),
-        _ints(out.slots, "out.slots", max_tokens, dev, torch.int64), _ints(out.status, "out.status", 1, dev))
-    st = attn_kv_plan(p, L.stream)
+        # two blocks for six vectors: the words, the slots
+        device = new_lens.device
+        words, slots = _empty((2 * n + 3 + max_tokens,), _I32, device, ctx), _empty((max_tokens,), _I64, device, ctx)
+        cu, lens, count, status, pos = words.split((n + 1, n, 1, 1, max_tokens))
+        out = KvPlan(cu, lens, pos, slots, count, status)
+        w = words.data_ptr()
+        cu_p, out_p, left_p, status_p, pos_p = w, w + 4 * (n + 1), w + 4 * (2 * n + 1), w + 4 * (2 * n + 2), w + 4 * (2 * n + 3)
+        slots_p = slots.data_ptr()
+    else:
+        cu_p, out_p = _vector(out.cu_seqlens, "out.cu_seqlens", n + 1, index), _vector(out.seqlens, "out.seqlens", n, index)
+        left_p, status_p = _vector(out.free_count, "out.free_count", 1, index), _vector(out.status, "out.status", 1, index)
+        pos_p = _vector(out.positions, "out.positions", max_tokens, index)
+        slots_p = _vector(out.slots, "out.slots", max_tokens, index, _I64)
+    p = _PLAN.pack(n, page_size, pages, cols, max_tokens, 0, new_p, len_p, out_p, block_table.data_ptr(), row, free_p,
+                   count_p, left_p, cu_p, pos_p, slots_p, status_p)
+    st = (_entries.get("attn_kv_plan") or _entry("attn_kv_plan", 2))(p, raw)
     if st != 0:
         raise AttnError(st, "attn_kv_plan")
     return out
@@ -647,26 +727,18 @@ def kv_append(k, v, slots, cache: KvCache, *, stream=None):
     """New keys and values into the cache (attn_kv_append): k [T, kv heads,
     d_qk] and v [T, kv heads, d_v] in bf16 or fp16, slots int64 [T] as from
     kv_plan (-1: skipped)."""
-    n = k.shape[0]
-    _need(k, "k", _F16, (n, cache.nhead_kv, cache.d_qk), cache.device)
-    _need(v, "v", (k.dtype,), (n, cache.nhead_kv, cache.d_v), cache.device)
-    L = _Launch(cache.device, stream)
-    p = AttnKvAppendParams(_DTYPES[k.dtype], n, k.data_ptr(), v.data_ptr(), _i64x3(*_packed(k)), _i64x3(*_packed(v)),
-                           _ints(slots, "slots", n, cache.device, torch.int64), cache.params)
-    st = attn_kv_append(p, L.stream)
+    index, ks, dtype = cache.index, k.shape, k.dtype
+    n, heads = ks[0], cache.nhead_kv
+    if (dtype not in _F16 or v.dtype is not dtype or ks != (n, heads, cache.d_qk) or v.shape != (n, heads, cache.d_v)
+            or k.get_device() != index or v.get_device() != index):
+        _check(k, "k", _F16, (n, heads, cache.d_qk), index)
+        _check(v, "v", (dtype,), (n, heads, cache.d_v), index)
+    raw, _ = _on(index, stream)
+    p = _APPEND.pack(_DTYPES[dtype], n, k.data_ptr(), v.data_ptr(), *_rows3(k, "k"), *_rows3(v, "v"),
+                     _vector(slots, "slots", n, index, _I64)) + cache.packed
+    st = (_entries.get("attn_kv_append") or _entry("attn_kv_append", 2))(p, raw)
     if st != 0:
         raise AttnError(st, "attn_kv_append")
-
-
-def _packed(t):
-    """{0, row, head} strides of a [T, H, D] tensor; a dimension of one entry
-    may carry any stride, so it is given the contiguous one."""
-    s = t.stride()
-    if s[2] != 1:
-        raise ValueError("the head dimension must be contiguous (stride 1)")
-    n, h, d = t.shape
-    head = s[1] if h > 1 else d
-    return 0, (s[0] if n > 1 else h * head), head
 
 
 def attn_kv_forward(q, cache: KvCache, block_table, seqlens_k, cu_seqlens_q, *, scale, mask=MASK_CAUSAL_BOTTOM_RIGHT,
@@ -679,44 +751,52 @@ def attn_kv_forward(q, cache: KvCache, block_table, seqlens_k, cu_seqlens_q, *, 
     allocated here they are undefined.  check_status=True synchronises and
     raises what the kernels found (lengths beyond their bounds, pages outside
     the cache)."""
-    dev, n = cache.device, seqlens_k.shape[0]
-    t, hq = q.shape[0], q.shape[1]
-    _need(q, "q", _F16, (t, hq, cache.d_qk), dev)
-    _need(block_table, "block_table", (torch.int32,), (n, block_table.shape[-1]), dev)
-    if block_table.stride(1) != 1:
-        raise ValueError("block_table rows must be contiguous")
-    L = _Launch(dev, stream)
+    index, qs, dtype = cache.index, q.shape, q.dtype
+    t, hq = qs[0], qs[1]
+    if dtype not in _F16 or q.get_device() != index or len(qs) != 3 or qs[2] != cache.d_qk:
+        _check(q, "q", _F16, (t, hq, cache.d_qk), index)
+    n = seqlens_k.shape[0]
+    cols, row = _table(block_table, n, index)
+    cu_p, len_p = _vector(cu_seqlens_q, "cu_seqlens_q", n + 1, index), _vector(seqlens_k, "seqlens_k", n, index)
+    pad_p = 0
+    if cu_seqlens_q_padded is not None:
+        pad_p = _vector(cu_seqlens_q_padded, "cu_seqlens_q_padded", n + 1, index)
+    raw, ctx = _on(index, stream)
+    dv = cache.d_v
     if out is None:
-        o, lse = L.empty((t, hq, cache.d_v), q.dtype), L.empty((hq, t), torch.float32)
+        device = q.device
+        o, lse = _empty((t, hq, dv), dtype, device, ctx), _empty((hq, t), torch.float32, device, ctx)
+        so = (0, hq * dv, dv)
     else:
         o, lse = out
-        _need(o, "out[0]", (q.dtype,), (t, hq, cache.d_v), dev)
-        _need(lse, "out[1]", (torch.float32,), (hq, t), dev)
+        _check(o, "out[0]", (dtype,), (t, hq, dv), index)
+        _check(lse, "out[1]", (torch.float32,), (hq, t), index)
         if not lse.is_contiguous():
             raise ValueError("out[1] must be contiguous")
-    p = AttnKvFwdParams(
-        _DTYPES[q.dtype], n, hq, t, max_seqlen_q, max_seqlen_k, block_table.shape[1], mask, left, right, scale, 0,
-        _ints(cu_seqlens_q, "cu_seqlens_q", n + 1, dev),
-        None if cu_seqlens_q_padded is None else _ints(cu_seqlens_q_padded, "cu_seqlens_q_padded", n + 1, dev),
-        _ints(seqlens_k, "seqlens_k", n, dev), block_table.data_ptr(),
-        block_table.stride(0) if n > 1 else block_table.shape[1], q.data_ptr(), o.data_ptr(), lse.data_ptr(),
-        _i64x3(*_packed(q)), _i64x3(*_packed(o)), cache.params)
-    st, need = attn_kv_fwd_workspace_size(p)
+        so = _rows3(o, "out[0]")
+    p = _FWD.pack(_DTYPES[dtype], n, hq, t, max_seqlen_q, max_seqlen_k, cols, mask, left, right, scale, 0, cu_p, pad_p,
+                  len_p, block_table.data_ptr(), row, q.data_ptr(), o.data_ptr(), lse.data_ptr(), *_rows3(q, "q"),
+                  *so) + cache.packed
+    need = ctypes.c_size_t(0)
+    st = (_entries.get("attn_kv_fwd_workspace_size") or _entry("attn_kv_fwd_workspace_size", 2))(p, ctypes.addressof(need))
     if st != 0:
         raise AttnError(st, "attn_kv_fwd_workspace_size")
     if workspace is None:
-        workspace = L.empty((need,), torch.uint8)
-    elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
-    st = attn_kv_fwd(p, workspace.data_ptr(), workspace.numel(), L.stream)
+        workspace = _empty((need.value,), torch.uint8, q.device, ctx)
+    elif workspace.get_device() != index or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{index}")
+    ws, nbytes = workspace.data_ptr(), workspace.numel()
+    st = (_entries.get("attn_kv_fwd") or _entry("attn_kv_fwd", 4))(p, ws, nbytes, raw)
     if st != 0:
         raise AttnError(st, "attn_kv_fwd")
     if check_status:
-        st, found = attn_kv_fwd_read_status(p, workspace.data_ptr(), workspace.numel(), L.stream)
+        found = ctypes.c_int(0)
+        f = _entries.get("attn_kv_fwd_read_status") or _entry("attn_kv_fwd_read_status", 5)
+        st = f(p, ws, nbytes, raw, ctypes.addressof(found))
         if st != 0:
             raise AttnError(st, "attn_kv_fwd_read_status")
-        if found != 0:
-            raise AttnError(found, "attn_kv_fwd (device status)")
+        if found.value != 0:
+            raise AttnError(found.value, "attn_kv_fwd (device status)")
     return o, lse
 
 

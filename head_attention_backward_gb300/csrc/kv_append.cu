@@ -2,18 +2,20 @@
 // values under one power-of-two scale per page, kv head and side.
 //
 // Memory bound (2 bytes read and 1 written per value).  The unit of work is a
-// run (the new tokens of one page) of one head and side; a warp owns it,
-// because the scale needs the run's largest magnitude before the first value
-// can be written.  A short run stays in registers between the two passes.
+// run (the new tokens of one page) of one head and side, because the scale
+// needs the run's largest magnitude before the first value can be written.  A
+// group of 1 to 8 warps owns it, enough to hold a full page of values in
+// registers between the two passes (up to 8,192 values; more are read twice).
 #include "common.cuh"
 #include "kv_common.cuh"
+#include "sm100_ptx.cuh"
 
 namespace attn {
 namespace kvappend {
 
 constexpr int NWARPS = 8;
 constexpr int NTHREADS = 32 * NWARPS;
-constexpr int HELD = 8;   // 16-byte pieces of a run that a lane keeps in registers
+constexpr int HELD = 4;   // 16-byte pieces of a run that a lane keeps in registers
 
 struct Args {
   const void* k;
@@ -21,22 +23,37 @@ struct Args {
   Strides sk, sv;
   const int64_t* slots;
   int tokens, tile;
+  int gw;              // warps of a group: 1, 2, 4 or 8
   KvCacheView c;
 };
 
 constexpr int MAX_RUN = 256;   // tokens of a run: the largest page
 
-// The new tokens of one page, and their rows in it (in shared memory).
+// The new tokens of one page, and their rows in it: token t + i in row first +
+// i, or by a list in shared memory where they are not in order.
 struct Run {
+  int t, n, first;   // first: the least row
   const int* tok;
   const uint8_t* at;
-  int n, first;      // tokens; least row among them
 };
 
 __device__ __forceinline__ float2 up2(uint32_t x, __nv_bfloat16*) {
-  return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&x));
+  // a bf16 is the upper half of an fp32
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
 }
 __device__ __forceinline__ float2 up2(uint32_t x, __half*) { return __half22float2(*reinterpret_cast<__half2*>(&x)); }
+
+// Larger magnitudes of two pairs; a NaN is passed over.
+__device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t x, __nv_bfloat16*) {
+  x &= 0x7fff7fffu;
+  const __nv_bfloat162 y = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&m), *reinterpret_cast<__nv_bfloat162*>(&x));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+__device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t x, __half*) {
+  x &= 0x7fff7fffu;
+  const __half2 y = __hmax2(*reinterpret_cast<__half2*>(&m), *reinterpret_cast<__half2*>(&x));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
 
 // Least e with amax <= 448 * 2^e = 1.75 * 2^(e + 8), from amax's exponent and
 // mantissa; limited to the format's range (a subnormal or zero amax is far
@@ -48,14 +65,11 @@ __device__ __forceinline__ int exponent_of(float amax) {
 }
 
 template <typename T>
-__device__ __forceinline__ float amax8(float m, const uint4& x) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = up2(w[i], (T*)nullptr);
-    m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));   // a NaN is passed over
-  }
-  return m;
+__device__ __forceinline__ uint32_t amax8(uint32_t m, const uint4& x) {
+  m = amax2(m, x.x, (T*)nullptr);
+  m = amax2(m, x.y, (T*)nullptr);
+  m = amax2(m, x.z, (T*)nullptr);
+  return amax2(m, x.w, (T*)nullptr);
 }
 
 template <typename T>
@@ -67,69 +81,119 @@ __device__ __forceinline__ uint2 quantise8(const uint4& x, float inv) {
     const float2 f = up2(w[i], (T*)nullptr);
     q[i] = f2_to_e4m3x2(f.x * inv, f.y * inv);
   }
-  return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+  return make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
 }
 
-// One run of one head and side, by one warp.  D: head dim.
+template <int N> struct Dim { static constexpr int value = N; };
+
+// The threads that share a run.
+struct Group {
+  int id, n, tid;      // of the CTA's groups; threads; this thread's place
+  __device__ __forceinline__ void sync() const {
+    if (n == 32) __syncwarp();
+    else ptx::named_bar_sync(1 + id, n);
+  }
+};
+
+// The live rows in front of a run at a larger scale (f: old over new), 16 values
+// at a time.
+template <int D>
+__device__ __noinline__ void round_again(int rows, uint8_t* cache, long long cr, float f, int tid, int n) {
+  for (int i = tid; i < rows * (D / 16); i += n) {
+    uint4* at = reinterpret_cast<uint4*>(cache + (long long)(i / (D / 16)) * cr + (i % (D / 16)) * 16);
+    const uint4 was = *at;
+    const uint32_t w[4] = {was.x, was.y, was.z, was.w};
+    uint32_t q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = e4m3x2_to_h2((uint16_t)w[j]), hi = e4m3x2_to_h2((uint16_t)(w[j] >> 16));
+      const float2 a = up2(lo, (__half*)nullptr), b = up2(hi, (__half*)nullptr);
+      q[j] = f2_to_e4m3x2(a.x * f, a.y * f) | ((uint32_t)f2_to_e4m3x2(b.x * f, b.y * f) << 16);
+    }
+    *at = make_uint4(q[0], q[1], q[2], q[3]);
+  }
+}
+
+// What both forms below do between the passes: the run's scale from the
+// threads' largest magnitudes, and the rows in front of the run.
 template <typename T, int D>
-__device__ __forceinline__ void append_run(const Run& r, const T* x, long long xr, uint8_t* cache, long long cr,
-                                           uint8_t* exp_byte, int lane) {
+__device__ __forceinline__ int settle_scale(const Run& r, uint32_t m, uint8_t* cache, long long cr, uint8_t* exp_byte,
+                                            int old, const Group& G, uint32_t* red) {
+  // magnitudes order like their bits
+  const float2 mm = up2(m, (T*)nullptr);
+  uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(mm.x, mm.y)));
+  if (G.n > 32) {
+    if ((G.tid & 31) == 0) red[G.tid >> 5] = top;
+    G.sync();   // also: every thread has read the old scale
+    for (int w = 0; w < G.n / 32; ++w) top = max(top, red[w]);
+  }
+  const int e = max(old, exponent_of(__uint_as_float(top)));
+  if (r.first > 0 && e > old) round_again<D>(r.first, cache, cr, exp2_int(old - e), G.tid, G.n);
+  if (G.tid == 0) *exp_byte = (uint8_t)(e + KV_EXP_BIAS);
+  return e;
+}
+
+// One run of one head and side, by one group, in order and small enough to be
+// held.  D: head dim; red: a word per warp of the group, not the last item's.
+template <typename T, int D>
+__device__ __forceinline__ void append_held(const Run& r, const T* x, long long xr, uint8_t* cache, long long cr,
+                                            uint8_t* exp_byte, const Group& G, uint32_t* red) {
   constexpr int PER = D / 8;   // pieces of 8 values per row
   const int pieces = r.n * PER;
-  auto load = [&](int i) {
-    return __ldg(reinterpret_cast<const uint4*>(x + (long long)r.tok[i / PER] * xr + (i % PER) * 8));
-  };
   const int old = r.first > 0 ? kv_exp_of(*exp_byte) : KV_EXP_MIN;
   uint4 held[HELD];
-  float m = 0.f;
+  uint32_t m = 0;
 #pragma unroll
-  for (int k = 0; k < HELD; ++k)
-    if (lane + 32 * k < pieces) held[k] = load(lane + 32 * k);
-#pragma unroll
-  for (int k = 0; k < HELD; ++k)
-    if (lane + 32 * k < pieces) m = amax8<T>(m, held[k]);
-  for (int i = lane + 32 * HELD; i < pieces; i += 32) m = amax8<T>(m, load(i));
-  // magnitudes order like their bits
-  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-  const int e = max(old, exponent_of(m));
-  if (r.first > 0 && e > old) {
-    // the live rows in front of the run, 16 values at a time
-    const float f = exp2_int(old - e);
-    for (int i = lane; i < r.first * (D / 16); i += 32) {
-      uint4* at = reinterpret_cast<uint4*>(cache + (long long)(i / (D / 16)) * cr + (i % (D / 16)) * 16);
-      const uint4 was = *at;
-      const uint32_t w[4] = {was.x, was.y, was.z, was.w};
-      uint32_t q[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t lo = e4m3x2_to_h2((uint16_t)w[j]), hi = e4m3x2_to_h2((uint16_t)(w[j] >> 16));
-        const float2 a = up2(lo, (__half*)nullptr), b = up2(hi, (__half*)nullptr);
-        q[j] = f2_to_e4m3x2(a.x * f, a.y * f) | ((uint32_t)f2_to_e4m3x2(b.x * f, b.y * f) << 16);
-      }
-      *at = make_uint4(q[0], q[1], q[2], q[3]);
-    }
+  for (int k = 0; k < HELD; ++k) {
+    const int i = G.tid + G.n * k;
+    if (i < pieces) held[k] = __ldg(reinterpret_cast<const uint4*>(x + (r.t + i / PER) * xr + (i % PER) * 8));
   }
-  const float inv = exp2_int(-e);
-  auto store = [&](int i, const uint4& v) {
-    *reinterpret_cast<uint2*>(cache + (long long)r.at[i / PER] * cr + (i % PER) * 8) = quantise8<T>(v, inv);
-  };
 #pragma unroll
   for (int k = 0; k < HELD; ++k)
-    if (lane + 32 * k < pieces) store(lane + 32 * k, held[k]);
-  for (int i = lane + 32 * HELD; i < pieces; i += 32) store(i, load(i));
-  if (lane == 0) *exp_byte = (uint8_t)(e + KV_EXP_BIAS);
+    if (G.tid + G.n * k < pieces) m = amax8<T>(m, held[k]);
+  const float inv = exp2_int(-settle_scale<T, D>(r, m, cache, cr, exp_byte, old, G, red));
+#pragma unroll
+  for (int k = 0; k < HELD; ++k) {
+    const int i = G.tid + G.n * k;
+    if (i < pieces)
+      *reinterpret_cast<uint2*>(cache + (r.first + i / PER) * cr + (i % PER) * 8) = quantise8<T>(held[k], inv);
+  }
 }
 
-// A CTA takes the runs that start in its tile of tokens (at most 32), all
-// heads and both sides of each, one (run, head, side) per warp at a time.  A
-// run is found by its page: it starts at a token whose page none of the
-// page_size tokens before it has, and ends where page_size tokens in a row have
-// another.
+// Any run, its values read twice.
+template <typename T, int D>
+__device__ __noinline__ void append_any(const Run& r, const T* x, long long xr, uint8_t* cache, long long cr,
+                                        uint8_t* exp_byte, const Group& G, uint32_t* red) {
+  constexpr int PER = D / 8;
+  const int pieces = r.n * PER;
+  auto load = [&](int i) {
+    const int tok = r.tok ? r.tok[i / PER] : r.t + i / PER;
+    return __ldg(reinterpret_cast<const uint4*>(x + tok * xr + (i % PER) * 8));
+  };
+  const int old = r.first > 0 ? kv_exp_of(*exp_byte) : KV_EXP_MIN;
+  uint32_t m = 0;
+#pragma unroll 4
+  for (int i = G.tid; i < pieces; i += G.n) m = amax8<T>(m, load(i));
+  const float inv = exp2_int(-settle_scale<T, D>(r, m, cache, cr, exp_byte, old, G, red));
+#pragma unroll 4
+  for (int i = G.tid; i < pieces; i += G.n) {
+    const int row = r.tok ? r.at[i / PER] : r.first + i / PER;
+    *reinterpret_cast<uint2*>(cache + row * cr + (i % PER) * 8) = quantise8<T>(load(i), inv);
+  }
+}
+
+// A CTA takes the runs that start in its tile of tokens (at most 32), and of
+// each the heads and sides of its share (blockIdx.y), one per group at a time.
+// A run is found by its page: it starts at a token whose page none of the
+// page_size tokens before it has, and ends where page_size tokens in a row
+// have another.
 template <typename T, int DQK, int DV>
-__global__ void __launch_bounds__(NTHREADS) append_kernel(const Args A) {
-  __shared__ int s_tok[NWARPS][MAX_RUN];
+__global__ void __launch_bounds__(NTHREADS, 3) append_kernel(const Args A) {
+  __shared__ int s_tok[NWARPS][MAX_RUN];       // a list per group
   __shared__ uint8_t s_at[NWARPS][MAX_RUN];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ int2 s_run[NWARPS];
+  __shared__ uint32_t s_red[2 * NWARPS];
+  const int lane = threadIdx.x & 31;
   const int t0 = blockIdx.x * A.tile;
   const int shift = A.c.page_shift, size = 1 << shift;
   const long long limit = (long long)A.c.num_pages << shift;
@@ -143,55 +207,87 @@ __global__ void __launch_bounds__(NTHREADS) append_kernel(const Args A) {
   };
   const int mine = lane < A.tile ? page_at(t0 + lane) : -1;
   uint32_t maybe = __ballot_sync(0xffffffffu, mine >= 0 && mine != page_at(t0 + lane - 1));
-  uint32_t starts = 0;
-  for (; maybe; maybe &= maybe - 1) {
-    const int l = __ffs(maybe) - 1, page = __shfl_sync(0xffffffffu, mine, l);
-    bool seen = false;
-    for (int j = 2 + lane; j <= size; j += 32) seen |= page_at(t0 + l - j) == page;
-    if (!__any_sync(0xffffffffu, seen)) starts |= 1u << l;
-  }
+  Group G;
+  G.n = 32 * A.gw;
+  G.id = threadIdx.x / G.n;
+  G.tid = threadIdx.x % G.n;
+  const int groups = NWARPS / A.gw, share = groups * gridDim.y;   // groups at work on one run
   const int per_run = A.c.hkv * 2;
-  const int items = __popc(starts) * per_run;
-  int listed = -1;
-  Run r{s_tok[warp], s_at[warp], 0, 0};
-  int page = 0;
-  for (int i = warp; i < items; i += NWARPS) {
-    const int which = i / per_run, hs = i - which * per_run, h = hs >> 1;
-    if (which != listed) {
-      listed = which;
-      const int t = t0 + (int)__fns(starts, 0, which + 1);
-      page = page_at(t);
-      int n = 0, first = size, last = t;
-      __syncwarp();
-      for (int base = t; n < size && base < A.tokens && base - last <= size; base += 32) {
-        const long long s = slot_at(base + lane);
-        const bool same = s >= 0 && (int)(s >> shift) == page;
-        const uint32_t all = __ballot_sync(0xffffffffu, same);
-        const int at = n + __popc(all & ((1u << lane) - 1));
-        if (same && at < size) {
-          s_tok[warp][at] = base + lane;
-          s_at[warp][at] = (uint8_t)(s & (size - 1));
-          first = min(first, (int)(s & (size - 1)));
-        }
-        if (all) last = base + 31 - __clz(all);
-        n = min(size, n + __popc(all));
+  int turn = 0;
+  for (; maybe; maybe &= maybe - 1) {
+    const int l = __ffs(maybe) - 1, t = t0 + l;
+    const long long slot = slot_at(t);
+    const int page = (int)(slot >> shift), row = (int)(slot & (size - 1));
+    // the tokens before, and those up to 2 page_size on, without a wait between:
+    // whether an earlier one has the page; the run's length if it is in order;
+    // whether the page comes again after that
+    bool earlier = false;
+#pragma unroll 2
+    for (int j = 2 + lane; j <= size; j += 32) earlier |= page_at(t - j) == page;
+    int n = size - row;
+    bool again = false;
+    for (int base = 0; base < 2 * size; base += 128) {
+      long long s[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] = base + 32 * k < 2 * size ? slot_at(t + base + 32 * k + lane) : -1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = base + 32 * k + lane;
+        const uint32_t stop = __ballot_sync(0xffffffffu, i < n && s[k] != slot + i);
+        if (stop) n = base + 32 * k + __ffs(stop) - 1;
+        again |= i >= n && i < n + size && s[k] >= 0 && (int)(s[k] >> shift) == page;
       }
-      r.n = n;
-      r.first = __reduce_min_sync(0xffffffffu, first);
-      __syncwarp();
     }
-    const long long eo = (long long)page * A.c.hkv + h;
-    if ((hs & 1) == 0)
-      append_run<T, DQK>(r, static_cast<const T*>(A.k) + h * A.sk.h, A.sk.r, A.c.k + page * A.c.sk.p + h * A.c.sk.h,
-                         A.c.sk.r, A.c.k_exp + eo, lane);
-    else
-      append_run<T, DV>(r, static_cast<const T*>(A.v) + h * A.sv.h, A.sv.r, A.c.v + page * A.c.sv.p + h * A.c.sv.h,
-                        A.c.sv.r, A.c.v_exp + eo, lane);
+    if (__any_sync(0xffffffffu, earlier)) continue;
+    Run r{t, n, row, nullptr, nullptr};
+    int hs = blockIdx.y * groups + G.id;
+    if (hs >= per_run) continue;
+    const bool list = __any_sync(0xffffffffu, again);
+    if (list) {
+      G.sync();                     // the last list has been used
+      if (G.tid < 32) {
+        int count = 0, first = size, last = t;
+        for (int base = t; count < size && base < A.tokens && base - last <= size; base += 32) {
+          const long long s = slot_at(base + lane);
+          const bool same = s >= 0 && (int)(s >> shift) == page;
+          const uint32_t all = __ballot_sync(0xffffffffu, same);
+          const int at = count + __popc(all & ((1u << lane) - 1));
+          if (same && at < size) {
+            s_tok[G.id][at] = base + lane;
+            s_at[G.id][at] = (uint8_t)(s & (size - 1));
+            first = min(first, (int)(s & (size - 1)));
+          }
+          if (all) last = base + 31 - __clz(all);
+          count = min(size, count + __popc(all));
+        }
+        first = __reduce_min_sync(0xffffffffu, first);
+        if (lane == 0) s_run[G.id] = make_int2(count, first);
+      }
+      G.sync();
+      r = Run{t, s_run[G.id].x, s_run[G.id].y, s_tok[G.id], s_at[G.id]};
+    }
+    for (; hs < per_run; hs += share) {
+      turn ^= NWARPS;
+      const int h = hs >> 1;
+      const bool is_v = hs & 1;
+      uint8_t* exp_byte = (is_v ? A.c.v_exp : A.c.k_exp) + (long long)page * A.c.hkv + h;
+      uint8_t* cache = is_v ? A.c.v + page * A.c.sv.p + h * A.c.sv.h : A.c.k + page * A.c.sk.p + h * A.c.sk.h;
+      const T* x = is_v ? static_cast<const T*>(A.v) + h * A.sv.h : static_cast<const T*>(A.k) + h * A.sk.h;
+      const long long xr = is_v ? A.sv.r : A.sk.r, cr = is_v ? A.c.sv.r : A.c.sk.r;
+      uint32_t* red = s_red + turn + G.id * A.gw;   // two sets in turn: one barrier per item
+      auto go = [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        if (list || r.n * (D / 8) > HELD * G.n) append_any<T, D>(r, x, xr, cache, cr, exp_byte, G, red);
+        else append_held<T, D>(r, x, xr, cache, cr, exp_byte, G, red);
+      };
+      if (DQK == DV || !is_v) go(Dim<DQK>());
+      else go(Dim<DV>());
+    }
   }
 }
 
 template <typename T>
-static void launch(const Args& a, int dqk, int dv, int grid, cudaStream_t st) {
+static void launch(const Args& a, int dqk, int dv, dim3 grid, cudaStream_t st) {
   if (dqk == 64) append_kernel<T, 64, 64><<<grid, NTHREADS, 0, st>>>(a);
   else if (dqk == 128) append_kernel<T, 128, 128><<<grid, NTHREADS, 0, st>>>(a);
   else if (dqk == 192) append_kernel<T, 192, 128><<<grid, NTHREADS, 0, st>>>(a);
@@ -214,8 +310,19 @@ static int run(const attn_kv_append_params* p, cudaStream_t st) {
   a.v = p->v;
   a.slots = p->slots;
   a.tokens = p->tokens;
-  a.tile = p->tokens <= 4096 ? 1 : 16;
-  const int grid = cdiv(p->tokens, a.tile);
+  // a group holds HELD pieces of 8 values per thread
+  const int dim = p->cache.d_qk > p->cache.d_v ? p->cache.d_qk : p->cache.d_v;
+  a.gw = 1;
+  while (a.gw < NWARPS && a.gw * 32 * HELD * 8 < p->cache.page_size * dim) a.gw *= 2;
+  // short calls: a CTA per token and share of the heads; long ones, where most
+  // tokens start no run, up to a warp's width of tokens
+  a.tile = p->tokens / 512;
+  a.tile = a.tile < 1 ? 1 : a.tile > 32 ? 32 : a.tile;
+  // items a group takes one after the other: more where the CTAs' search for
+  // runs would otherwise outweigh them (16,160 tokens: 32.9 us at four, 49.7 at
+  // one; 64 tokens: 4.0 us at one, 6.2 at four)
+  const int rounds = a.tile >= 8 ? 4 : a.tile > 1 ? 2 : 1;
+  const dim3 grid(cdiv(p->tokens, a.tile), cdiv(p->cache.nhead_kv * 2, NWARPS / a.gw * rounds));
   if (p->dtype == ATTN_BF16) launch<__nv_bfloat16>(a, p->cache.d_qk, p->cache.d_v, grid, st);
   else launch<__half>(a, p->cache.d_qk, p->cache.d_v, grid, st);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;

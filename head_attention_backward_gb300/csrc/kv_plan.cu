@@ -3,7 +3,9 @@
 //
 // A few kilobytes move, so the call is its launch and three dependent trips to
 // memory.  One CTA does it all: the sums of a batch of 8192 requests are eight
-// requests per thread, and nothing has to wait for another CTA.
+// requests per thread, and nothing has to wait for another CTA.  Only the slots
+// and positions of many tokens (prompts) are left to a second kernel that spreads
+// them over the GPU, launched early so that it waits in place.
 #include "common.cuh"
 #include "kv_common.cuh"
 
@@ -11,6 +13,8 @@ namespace attn {
 namespace kvplan {
 
 constexpr int NTHREADS = 1024;
+constexpr int FILL_THREADS = 256;
+constexpr int FILL_FROM = 4096;   // tokens
 
 struct Sums {
   long long tok, take, back;
@@ -30,7 +34,7 @@ __device__ __forceinline__ int find(const int* prefix, int n, int x) {
 
 __device__ __forceinline__ int pages_of(int tokens, int shift) { return (int)(((long long)tokens + (1 << shift) - 1) >> shift); }
 
-__global__ void __launch_bounds__(NTHREADS) plan_kernel(const attn_kv_plan_params P, const int shift) {
+__global__ void __launch_bounds__(NTHREADS) plan_kernel(const attn_kv_plan_params P, const int shift, const bool fill) {
   extern __shared__ int sm[];
   const int n = P.batch;
   int* cu = sm;                   // [n + 1] new tokens before request b
@@ -39,6 +43,7 @@ __global__ void __launch_bounds__(NTHREADS) plan_kernel(const attn_kv_plan_param
   int* len0 = back + n + 1;       // [n]     tokens it keeps
   __shared__ Sums part[NTHREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (!fill) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int per = cdiv(n, NTHREADS);
   const int b0 = min(tid * per, n), b1 = min(b0 + per, n);
   const int free_n = *P.free_count;   // the output may be the same word: read by all before the first barrier
@@ -124,7 +129,7 @@ __global__ void __launch_bounds__(NTHREADS) plan_kernel(const attn_kv_plan_param
       P.cu_seqlens[b] = 0;
       if (b < n) P.seqlens_out[b] = P.seqlens[b];
     }
-    for (int t = tid; t < P.max_tokens; t += NTHREADS) {
+    for (int t = tid; fill && t < P.max_tokens; t += NTHREADS) {
       P.positions[t] = 0;
       P.slots[t] = -1;
     }
@@ -148,6 +153,7 @@ __global__ void __launch_bounds__(NTHREADS) plan_kernel(const attn_kv_plan_param
     *P.free_count_out = top - ntake;
     *P.status = ATTN_OK;
   }
+  if (!fill) return;
   __syncthreads();
   const int total_tok = cu[n];
   for (int t = tid; t < P.max_tokens; t += NTHREADS) {
@@ -162,6 +168,27 @@ __global__ void __launch_bounds__(NTHREADS) plan_kernel(const attn_kv_plan_param
     P.positions[t] = pos;
     P.slots[t] = slot;
   }
+}
+
+// Positions and slots from what plan_kernel wrote (no tokens where it refused).
+__global__ void __launch_bounds__(FILL_THREADS) fill_kernel(const attn_kv_plan_params P, const int shift) {
+  extern __shared__ int cu[];     // [batch + 1]
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int n = P.batch;
+  for (int b = threadIdx.x; b <= n; b += FILL_THREADS) cu[b] = __ldcg(P.cu_seqlens + b);
+  __syncthreads();
+  const int t = blockIdx.x * FILL_THREADS + threadIdx.x;
+  if (t >= P.max_tokens) return;
+  int pos = 0;
+  long long slot = -1;
+  if (t < cu[n]) {
+    const int b = find(cu, n, t);
+    pos = __ldcg(P.seqlens_out + b) - cu[b + 1] + t;
+    const int page = __ldcg(P.block_table + b * P.table_stride + (pos >> shift));
+    slot = ((long long)page << shift) + (pos & ((1 << shift) - 1));
+  }
+  P.positions[t] = pos;
+  P.slots[t] = slot;
 }
 
 static int run(const attn_kv_plan_params* p, cudaStream_t st) {
@@ -183,7 +210,21 @@ static int run(const attn_kv_plan_params* p, cudaStream_t st) {
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return ATTN_ERR_CUDA;
-  plan_kernel<<<1, NTHREADS, smem, st>>>(*p, shift);
+  const bool fill = p->max_tokens <= FILL_FROM;
+  plan_kernel<<<1, NTHREADS, smem, st>>>(*p, shift, fill);
+  if (!fill) {
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cdiv(p->max_tokens, FILL_THREADS));
+    cfg.blockDim = dim3(FILL_THREADS);
+    cfg.dynamicSmemBytes = (p->batch + 1) * sizeof(int);
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, fill_kernel, *p, shift) != cudaSuccess) return ATTN_ERR_CUDA;
+  }
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

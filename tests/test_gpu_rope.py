@@ -38,6 +38,10 @@ CASES = [
     (9, 2, 3, 30, 14, 2, torch.float32, False, 1 << 30),
     (40, 2, 2, 20, 20, 2, torch.float32, True, 100),
     (3, 2, 2, 32, 32, 1, torch.float32, True, 100),
+    (70, 3, 2, 7, 4, 2, torch.float32, True, 100),
+    (70, 3, 2, 9, 6, 2, torch.float32, False, 100),
+    (3000, 9, 1, 64, 58, 2, torch.bfloat16, True, 100),
+    (2500, 3, 2, 128, 96, 2, torch.float16, False, 100),
     (9001, 2, 1, 64, 64, 3, torch.bfloat16, False, 9001),
 ]
 
