@@ -5,7 +5,7 @@
 // run (the new tokens of one page) of one head and side, because the scale
 // needs the run's largest magnitude before the first value can be written.  A
 // group of 1 to 8 warps owns it, enough to hold a full page of values in
-// registers between the two passes (up to 8,192 values; more are read twice).
+// registers between the two passes (up to 16,384 values; more are read twice).
 #include "common.cuh"
 #include "kv_common.cuh"
 #include "sm100_ptx.cuh"
@@ -14,8 +14,9 @@ namespace attn {
 namespace kvappend {
 
 constexpr int NWARPS = 8;
+constexpr int RESIDENT = 3;   // CTAs per SM that the registers have to allow
 constexpr int NTHREADS = 32 * NWARPS;
-constexpr int HELD = 4;   // 16-byte pieces of a run that a lane keeps in registers
+constexpr int HELD = 8;   // 16-byte pieces of a run that a lane keeps in registers
 
 struct Args {
   const void* k;
@@ -72,16 +73,40 @@ __device__ __forceinline__ uint32_t amax8(uint32_t m, const uint4& x) {
   return amax2(m, x.w, (T*)nullptr);
 }
 
-template <typename T>
-__device__ __forceinline__ uint2 quantise8(const uint4& x, float inv) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t q[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = up2(w[i], (T*)nullptr);
-    q[i] = f2_to_e4m3x2(f.x * inv, f.y * inv);
+// 8 values over 2^e as e4m3.  bf16: the product with a power of two is exact
+// in bf16 (values that leave its range are 0 in e4m3 anyway).  fp16: likewise
+// while the factor is one of its normal numbers -- what becomes subnormal is
+// below 2^-14, far under half of e4m3's least value -- else in fp32.
+struct Quantiser {
+  uint32_t factor;     // 2^-e twice in the input type, or 0: use inv
+  float inv;           // 2^-e
+};
+__device__ __forceinline__ Quantiser quantiser(int e, __nv_bfloat16*) {
+  const __nv_bfloat162 f = __float2bfloat162_rn(exp2_int(-e));
+  return {*reinterpret_cast<const uint32_t*>(&f), exp2_int(-e)};
+}
+__device__ __forceinline__ Quantiser quantiser(int e, __half*) {
+  const __half2 f = __float2half2_rn(exp2_int(-e));
+  return {e >= -14 && e <= 14 ? *reinterpret_cast<const uint32_t*>(&f) : 0u, exp2_int(-e)};
+}
+__device__ __forceinline__ uint32_t quantise2(uint32_t x, const Quantiser& q, __nv_bfloat16*) {
+  const __nv_bfloat162 y = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&q.factor));
+  const float2 f = up2(*reinterpret_cast<const uint32_t*>(&y), (__nv_bfloat16*)nullptr);
+  return f2_to_e4m3x2(f.x, f.y);
+}
+__device__ __forceinline__ uint32_t quantise2(uint32_t x, const Quantiser& q, __half*) {
+  if (q.factor) {
+    const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<const __half2*>(&q.factor));
+    return h2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&y));
   }
-  return make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
+  const float2 f = up2(x, (__half*)nullptr);
+  return f2_to_e4m3x2(f.x * q.inv, f.y * q.inv);
+}
+template <typename T>
+__device__ __forceinline__ uint2 quantise8(const uint4& x, const Quantiser& q) {
+  T* t = nullptr;
+  return make_uint2(__byte_perm(quantise2(x.x, q, t), quantise2(x.y, q, t), 0x5410),
+                    __byte_perm(quantise2(x.z, q, t), quantise2(x.w, q, t), 0x5410));
 }
 
 template <int N> struct Dim { static constexpr int value = N; };
@@ -133,52 +158,79 @@ __device__ __forceinline__ int settle_scale(const Run& r, uint32_t m, uint8_t* c
   return e;
 }
 
-// One run of one head and side, by one group, in order and small enough to be
-// held.  D: head dim; red: a word per warp of the group, not the last item's.
-template <typename T, int D>
-__device__ __forceinline__ void append_held(const Run& r, const T* x, long long xr, uint8_t* cache, long long cr,
-                                            uint8_t* exp_byte, const Group& G, uint32_t* red) {
-  constexpr int PER = D / 8;   // pieces of 8 values per row
-  const int pieces = r.n * PER;
-  const int old = r.first > 0 ? kv_exp_of(*exp_byte) : KV_EXP_MIN;
-  uint4 held[HELD];
-  uint32_t m = 0;
-#pragma unroll
-  for (int k = 0; k < HELD; ++k) {
-    const int i = G.tid + G.n * k;
-    if (i < pieces) held[k] = __ldg(reinterpret_cast<const uint4*>(x + (r.t + i / PER) * xr + (i % PER) * 8));
+// How a group covers a run: a thread keeps to one piece of 8 columns and takes
+// every step-th row.
+template <int D>
+struct Cover {
+  int row, step, col;
+  __device__ __forceinline__ explicit Cover(const Group& G) {
+    constexpr int PER = D / 8;
+    step = G.n / PER;
+    row = G.tid / PER;
+    col = G.tid % PER * 8;
+    if (row >= step) row = 1 << 16;   // left over where PER is no power of two: no row
   }
+};
+
+// One run of one head and side, by one group, its tokens in order: in blocks of
+// what the group can hold, the last of which (as a rule the only one) stays in
+// registers.  red: a word per warp of the group, not the last item's.
+template <typename T, int D>
+__device__ __forceinline__ void append_in_order(const Run& r, const T* x, long long xr, uint8_t* cache, long long cr,
+                                                uint8_t* exp_byte, const Group& G, uint32_t* red) {
+  const Cover<D> c(G);
+  const int old = r.first > 0 ? kv_exp_of(*exp_byte) : KV_EXP_MIN;
+  const long long sstep = c.step * xr, dstep = c.step * cr;
+  uint4 held[HELD];
+  auto load = [&](int row) {     // rows row, row + step, ...
+    const T* src = x + (r.t + row) * xr + c.col;
 #pragma unroll
-  for (int k = 0; k < HELD; ++k)
-    if (G.tid + G.n * k < pieces) m = amax8<T>(m, held[k]);
-  const float inv = exp2_int(-settle_scale<T, D>(r, m, cache, cr, exp_byte, old, G, red));
+    for (int k = 0; k < HELD; ++k) {
+      held[k] = make_uint4(0, 0, 0, 0);
+      if (row + c.step * k < r.n) held[k] = __ldg(reinterpret_cast<const uint4*>(src));
+      src += sstep;
+    }
+  };
+  uint32_t m = 0;
+  const int last = (r.n - 1) / (HELD * c.step);      // blocks before the last one
+  int row = c.row;
+  for (int i = 0;; ++i) {
+    load(row);
 #pragma unroll
-  for (int k = 0; k < HELD; ++k) {
-    const int i = G.tid + G.n * k;
-    if (i < pieces)
-      *reinterpret_cast<uint2*>(cache + (r.first + i / PER) * cr + (i % PER) * 8) = quantise8<T>(held[k], inv);
+    for (int k = 0; k < HELD; ++k) m = amax8<T>(m, held[k]);
+    if (i == last) break;
+    row += HELD * c.step;
+  }
+  const Quantiser q = quantiser(settle_scale<T, D>(r, m, cache, cr, exp_byte, old, G, red), (T*)nullptr);
+  for (int i = last;; --i) {
+    uint8_t* dst = cache + (r.first + row) * cr + c.col;
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) {
+      if (row + c.step * k < r.n) *reinterpret_cast<uint2*>(dst) = quantise8<T>(held[k], q);
+      dst += dstep;
+    }
+    if (i == 0) break;
+    row -= HELD * c.step;
+    load(row);
   }
 }
 
-// Any run, its values read twice.
+// A run whose tokens are not in order, by its list; the values are read twice.
 template <typename T, int D>
-__device__ __noinline__ void append_any(const Run& r, const T* x, long long xr, uint8_t* cache, long long cr,
+__device__ __noinline__ void append_listed(const Run& r, const T* x, long long xr, uint8_t* cache, long long cr,
                                         uint8_t* exp_byte, const Group& G, uint32_t* red) {
-  constexpr int PER = D / 8;
-  const int pieces = r.n * PER;
-  auto load = [&](int i) {
-    const int tok = r.tok ? r.tok[i / PER] : r.t + i / PER;
-    return __ldg(reinterpret_cast<const uint4*>(x + tok * xr + (i % PER) * 8));
+  const Cover<D> c(G);
+  auto load = [&](int row) {
+    return __ldg(reinterpret_cast<const uint4*>(x + (long long)r.tok[row] * xr + c.col));
   };
   const int old = r.first > 0 ? kv_exp_of(*exp_byte) : KV_EXP_MIN;
   uint32_t m = 0;
-#pragma unroll 4
-  for (int i = G.tid; i < pieces; i += G.n) m = amax8<T>(m, load(i));
-  const float inv = exp2_int(-settle_scale<T, D>(r, m, cache, cr, exp_byte, old, G, red));
-#pragma unroll 4
-  for (int i = G.tid; i < pieces; i += G.n) {
-    const int row = r.tok ? r.at[i / PER] : r.first + i / PER;
-    *reinterpret_cast<uint2*>(cache + row * cr + (i % PER) * 8) = quantise8<T>(load(i), inv);
+#pragma unroll 8
+  for (int row = c.row; row < r.n; row += c.step) m = amax8<T>(m, load(row));
+  const Quantiser q = quantiser(settle_scale<T, D>(r, m, cache, cr, exp_byte, old, G, red), (T*)nullptr);
+#pragma unroll 8
+  for (int row = c.row; row < r.n; row += c.step) {
+    *reinterpret_cast<uint2*>(cache + (long long)r.at[row] * cr + c.col) = quantise8<T>(load(row), q);
   }
 }
 
@@ -188,7 +240,7 @@ __device__ __noinline__ void append_any(const Run& r, const T* x, long long xr, 
 // page_size tokens before it has, and ends where page_size tokens in a row
 // have another.
 template <typename T, int DQK, int DV>
-__global__ void __launch_bounds__(NTHREADS, 3) append_kernel(const Args A) {
+__global__ void __launch_bounds__(NTHREADS, RESIDENT) append_kernel(const Args A) {
   __shared__ int s_tok[NWARPS][MAX_RUN];       // a list per group
   __shared__ uint8_t s_at[NWARPS][MAX_RUN];
   __shared__ int2 s_run[NWARPS];
@@ -277,8 +329,8 @@ __global__ void __launch_bounds__(NTHREADS, 3) append_kernel(const Args A) {
       uint32_t* red = s_red + turn + G.id * A.gw;   // two sets in turn: one barrier per item
       auto go = [&](auto d) {
         constexpr int D = decltype(d)::value;
-        if (list || r.n * (D / 8) > HELD * G.n) append_any<T, D>(r, x, xr, cache, cr, exp_byte, G, red);
-        else append_held<T, D>(r, x, xr, cache, cr, exp_byte, G, red);
+        if (list) append_listed<T, D>(r, x, xr, cache, cr, exp_byte, G, red);
+        else append_in_order<T, D>(r, x, xr, cache, cr, exp_byte, G, red);
       };
       if (DQK == DV || !is_v) go(Dim<DQK>());
       else go(Dim<DV>());
@@ -310,19 +362,23 @@ static int run(const attn_kv_append_params* p, cudaStream_t st) {
   a.v = p->v;
   a.slots = p->slots;
   a.tokens = p->tokens;
-  // a group holds HELD pieces of 8 values per thread
+  // a group holds HELD pieces of 8 values per thread: a whole page, if 8 warps can
   const int dim = p->cache.d_qk > p->cache.d_v ? p->cache.d_qk : p->cache.d_v;
   a.gw = 1;
-  while (a.gw < NWARPS && a.gw * 32 * HELD * 8 < p->cache.page_size * dim) a.gw *= 2;
-  // short calls: a CTA per token and share of the heads; long ones, where most
-  // tokens start no run, up to a warp's width of tokens
-  a.tile = p->tokens / 512;
-  a.tile = a.tile < 1 ? 1 : a.tile > 32 ? 32 : a.tile;
-  // items a group takes one after the other: more where the CTAs' search for
-  // runs would otherwise outweigh them (16,160 tokens: 32.9 us at four, 49.7 at
-  // one; 64 tokens: 4.0 us at one, 6.2 at four)
-  const int rounds = a.tile >= 8 ? 4 : a.tile > 1 ? 2 : 1;
-  const dim3 grid(cdiv(p->tokens, a.tile), cdiv(p->cache.nhead_kv * 2, NWARPS / a.gw * rounds));
+  while (a.gw < NWARPS && HELD * (a.gw * 32 / (dim / 8)) < p->cache.page_size) a.gw *= 2;
+  // Items a group takes one after the other: as many as leave the GPU full, up
+  // to four, beyond which the CTAs' search for runs no longer weighs (16,160
+  // tokens in pages of 64: 22.4 us at four, 29.0 at one; 64 single tokens: 3.8 us
+  // at one, 4.6 at four).
+  const int groups = NWARPS / a.gw, per_run = p->cache.nhead_kv * 2;
+  const long long full = (long long)(p->tokens / p->cache.page_size) * per_run / (groups * 152LL * RESIDENT);
+  const int rounds = full < 1 ? 1 : full > 4 ? 4 : (int)full;
+  const int shares = cdiv(per_run, groups * rounds);
+  // Tokens a CTA searches for runs: one in short calls (where every token may
+  // start one), up to a warp's width as the grid grows.
+  const long long tile = cdiv_ll((long long)p->tokens * shares, 1024);
+  a.tile = tile > 32 ? 32 : (int)tile;
+  const dim3 grid(cdiv(p->tokens, a.tile), shares);
   if (p->dtype == ATTN_BF16) launch<__nv_bfloat16>(a, p->cache.d_qk, p->cache.d_v, grid, st);
   else launch<__half>(a, p->cache.d_qk, p->cache.d_v, grid, st);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;

@@ -111,6 +111,13 @@ __device__ __forceinline__ uint16_t f2_to_e4m3x2(float lo, float hi) {
   return y;
 }
 
+// The same from two packed fp16 values.
+__device__ __forceinline__ uint16_t h2_to_e4m3x2(uint32_t x) {
+  uint16_t y;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(y) : "r"(x));
+  return y;
+}
+
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
 

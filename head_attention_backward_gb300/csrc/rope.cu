@@ -84,9 +84,16 @@ __global__ void __launch_bounds__(NTHREADS) rope_kernel(const Args A, const __gr
   using V = Vec<T, VP>;
   extern __shared__ unsigned long long dyn[];
   unsigned long long* s_step = dyn;                                   // [half]
-  float2* cs = reinterpret_cast<float2*>(dyn + A.half);               // [tok][half]
-  int2* s_row = reinterpret_cast<int2*>(cs + A.tok * A.half);         // [tok]: batch entry, row
+  float2* cs = reinterpret_cast<float2*>(dyn + cdiv(A.half, 2) * 2);  // [tok][chunks of pairs]
+  int2* s_row = reinterpret_cast<int2*>(cs + A.tok * cdiv(A.half, VP) * VP);   // [tok]: batch entry, row
   uint8_t* s_axis = reinterpret_cast<uint8_t*>(s_row + A.tok);        // [half]
+  // Pairs 2k and 2k + 1 of every chunk next to each other, then the next two of
+  // every chunk: neighbouring threads (chunks) read neighbouring 16 bytes.
+  const int full = (A.half + VP - 1) / VP;                            // chunks with a pair
+  const int stride = full * VP;
+  auto place = [&](int pair) {
+    return VP == 1 ? pair : ((pair % VP / 2) * full + pair / VP) * 2 + pair % 2;
+  };
   const int row0 = blockIdx.x * A.tok;
   const int nrow = min(A.tok, A.rows - row0);
   // the table comes from the parameter bank, which serves one address at a time
@@ -105,7 +112,7 @@ __global__ void __launch_bounds__(NTHREADS) rope_kernel(const Args A, const __gr
     const int pos = __ldg(A.pos + s_axis[pair] * A.pa + bs.x * A.pb + bs.y * A.pr);
     float2 x = cos_sin_turns((unsigned long long)(long long)pos * s_step[pair]);
     if (A.inverse) x.y = -x.y;
-    cs[i] = x;
+    cs[rr * stride + place(pair)] = x;
   }
   __syncthreads();
 
@@ -133,7 +140,18 @@ __global__ void __launch_bounds__(NTHREADS) rope_kernel(const Args A, const __gr
     V v0 = *reinterpret_cast<const V*>(in + at0), v1 = v0;
     if (at1 < A.dim) v1 = *reinterpret_cast<const V*>(in + at1);   // an odd last copy is one vector
     if (turns) {
-      const float2* t = cs + r * A.half + c * VP;
+      const float2* row_cs = cs + r * stride;
+      float2 t[VP];
+#pragma unroll
+      for (int p = 0; p < VP; p += 2) {
+        if (VP == 1) {
+          t[0] = row_cs[INTER && c >= A.half ? 0 : c];
+        } else {
+          const float4 x = *reinterpret_cast<const float4*>(row_cs + ((p / 2) * full + (INTER && c >= full ? 0 : c)) * 2);
+          t[p] = make_float2(x.x, x.y);
+          t[p + 1 < VP ? p + 1 : p] = make_float2(x.z, x.w);
+        }
+      }
 #pragma unroll
       for (int p = 0; p < VP; ++p) {
         if (INTER && c * VP + p >= A.half) break;   // copied
@@ -166,7 +184,7 @@ __global__ void __launch_bounds__(NTHREADS) rope_kernel(const Args A, const __gr
 template <typename T, int VP>
 static void launch(const Args& a, const Table& t, bool inter, cudaStream_t st) {
   const int grid = cdiv(a.rows, a.tok);
-  const size_t smem = a.half * 8 + (size_t)a.tok * a.half * sizeof(float2) + a.tok * sizeof(int2) + a.half;
+  const size_t smem = cdiv(a.half, 2) * 16 + (size_t)a.tok * cdiv(a.half, VP) * VP * sizeof(float2) + a.tok * sizeof(int2) + a.half;
   if (inter)
     rope_kernel<T, VP, true><<<grid, NTHREADS, smem, st>>>(a, t);
   else
