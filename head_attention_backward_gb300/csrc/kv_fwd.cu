@@ -30,8 +30,9 @@
 // * The accumulator is held in units of one V scale; a page whose scale is
 //   within 2^4 of it has its ratio put on P (exact), others move the unit.
 //
-// Splits leave (O, max, sum) in the workspace; a second small kernel joins
-// them in a fixed order.
+// In small grids the splits of a row tile form a thread-block cluster and are
+// joined through its shared memory; otherwise they leave (O, max, sum) in the
+// workspace, where a second small kernel joins them.  The order is fixed.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -54,10 +55,16 @@ constexpr int MAX_TILES = 256;      // tiles of a split: its page table fits sha
 // 608: more parts to join and an uneven second wave).  Many jobs: splits short
 // enough to even out ragged lengths (64 requests of up to 8,192 tokens: 108.4 us
 // at 64 tiles, 114.2 at 256, 114.0 at 32).  None so short that its prologue
-// outweighs it (4 requests of 1,000 tokens: 8.8 us at 8 tiles, 9.7 at 16).
+// outweighs it (4 requests of 1,000 tokens: 8.5 us at 12 tiles, 8.8 at 8, 8.9 at
+// 16).
 constexpr int WAVE = 304;
 constexpr int EVEN_TILES = 64;
-constexpr int MIN_TILES = 8;
+constexpr int MIN_TILES = 12;
+// Up to eight splits of a grid of one wave are joined as clusters: no second
+// launch, 8.5 us against 9.2 in that last case.  Not in larger grids, where the
+// CTAs of a cluster hold their SMs for its slowest (158 us against 108 for the 64
+// requests).
+constexpr int MAX_CLUSTER = 8;
 constexpr int EV_SLACK = 4;         // V scales within 2^4 of the accumulator's unit go on P
 constexpr float P_LOG2 = 4.f;       // P = 2^4 at the running maximum
 constexpr float SLACK_LOG2 = 7.f;   // growth of the maximum that is let pass: P <= 2^(4 + 7 + 4)
@@ -73,10 +80,11 @@ struct Cfg {
   static constexpr int OFF_BAR = NWARPS * RING;                        // uint64_t[NWARPS][NST]
   static constexpr int OFF_META = OFF_BAR + NWARPS * NST * 8;          // int2[MAX_TILES + 1]: page, exponents
   static constexpr int OFF_ML = OFF_META + (MAX_TILES + 1) * 8;        // float[2][NWARPS][ROWS]
-  static constexpr int SMEM = OFF_ML + 2 * NWARPS * ROWS * 4 + 8 + 1024;   // + alignment slack
+  static constexpr int SMEM = OFF_ML + 2 * NWARPS * ROWS * 4 + ROWS * 8 + 8 + 1024;   // + alignment slack
   // CTAs per SM that the registers have to allow (shared memory allows them too)
   static constexpr int RESIDENT = NT == 1 ? (DQK == 256 ? 2 : DQK == 192 ? 3 : 4) : (DQK == 256 ? 1 : DQK == 192 ? 2 : 3);
-  static_assert(NWARPS * ROWS * DV * 4 <= NWARPS * RING, "the join of the warps reuses the rings");
+  static constexpr int OFF_JOIN = NWARPS * ROWS * DV * 4;              // float[ROWS][DV], behind the warps' parts
+  static_assert(OFF_JOIN + ROWS * DV * 4 <= NWARPS * RING, "the joins reuse the rings");
 };
 
 struct Maps {
@@ -100,6 +108,7 @@ struct Args {
   int mask, left, right;
   float scale_log2;
   int nsplit, split_tiles, mtiles;
+  int cluster;           // 1: the splits of a job are a cluster
   int job_rows;          // most rows that a row tile can have
   float* part_o;         // [job][nsplit][rows][DV]
   float2* part_ml;       // [job][nsplit][rows]
@@ -175,6 +184,25 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity) {
 }
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity) {
   return ptx::mbar_try_wait(bar, parity) || wait_slow(bar, parity);
+}
+
+// Cluster of the splits: barrier, and reads of another CTA's shared memory.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t in_cta(uint32_t smem_addr, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -261,16 +289,17 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
   int2* meta = reinterpret_cast<int2*>(smem + C::OFF_META);
   float* s_m = reinterpret_cast<float*>(smem + C::OFF_ML);
   float* s_l = s_m + NWARPS * ROWS;
-  int* s_bad = reinterpret_cast<int*>(s_l + NWARPS * ROWS);
+  float2* s_jml = reinterpret_cast<float2*>(s_l + NWARPS * ROWS);   // [ROWS]
+  int* s_bad = reinterpret_cast<int*>(s_jml + ROWS);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
 
-  // block -> (request, kv head, split, row tile), row tiles next to each other
+  // block -> (request, kv head, row tile, split)
   int x = blockIdx.x;
-  const int m = x % A.mtiles;
-  x /= A.mtiles;
   const int split = x % A.nsplit;
   x /= A.nsplit;
+  const int m = x % A.mtiles;
+  x /= A.mtiles;
   const int hk = x % A.c.hkv, b = x / A.c.hkv;
   MaskArgs mk;
   const Job J = make_job<ROWS>(A, b, m, mk);
@@ -286,6 +315,13 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
   const int tile0 = split * A.split_tiles;
   if (J.nrow <= 0 || (split > 0 && tile0 >= J.ntile)) {
     if (reports && tid == 0) A.status[b * A.nsplit + split] = J.bad ? ATTN_ERR_BAD_SEQLENS : ATTN_OK;
+    // a cluster whose rows have splits to join (the same for all of it) meets twice
+    if (A.cluster && J.nrow > 0 && J.ntile > A.split_tiles) {
+      cluster_arrive();
+      cluster_wait();
+      cluster_arrive();
+      cluster_wait();
+    }
     return;
   }
   const int ntile = min(A.split_tiles, J.ntile - tile0);      // may be <= 0 for split 0
@@ -613,7 +649,9 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const bool whole = J.ntile <= A.split_tiles;   // no other split holds keys of these rows
   const long long part = ((long long)(b * A.c.hkv + hk) * A.mtiles + m) * A.nsplit + split;
-  for (int i = tid; i < J.nrow * (DV / 4); i += NTHREADS) {
+  float* s_join = reinterpret_cast<float*>(smem + C::OFF_JOIN);
+  const int pieces = J.nrow * (DV / 4);
+  for (int i = tid; i < pieces; i += NTHREADS) {
     const int row = i / (DV / 4), c = (i % (DV / 4)) * 4;
     float top = s_m[row];
 #pragma unroll
@@ -629,10 +667,44 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
     }
     if (whole) {
       store_row<T>(A, J, hk, row, c, v, top, l);
+    } else if (A.cluster) {
+      *reinterpret_cast<float4*>(s_join + row * DV + c) = v;
+      if (c == 0) s_jml[row] = make_float2(top, l);
     } else {
       *reinterpret_cast<float4*>(A.part_o + (part * ROWS + row) * DV + c) = v;
       if (c == 0) A.part_ml[part * ROWS + row] = make_float2(top, l);
     }
+  }
+  if (A.cluster && !whole) {
+    // each CTA finishes its share of the rows' pieces
+    cluster_arrive();
+    cluster_wait();
+    const int n = cdiv(J.ntile, A.split_tiles);
+    const uint32_t join = ptx::smem_u32(s_join), jml = ptx::smem_u32(s_jml);
+    for (int i = split * NTHREADS + tid; i < pieces; i += n * NTHREADS) {
+      const int row = i / (DV / 4), c = (i % (DV / 4)) * 4;
+      float tops[MAX_CLUSTER], top = -INFINITY;
+#pragma unroll
+      for (int s = 0; s < MAX_CLUSTER; ++s) {
+        tops[s] = s < n ? ld_cluster(in_cta(jml + row * 8, s)) : -INFINITY;
+        top = fmaxf(top, tops[s]);
+      }
+      float l = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int s = 0; s < MAX_CLUSTER; ++s) {
+        if (s >= n) break;
+        const float ls = ld_cluster(in_cta(jml + row * 8 + 4, s));
+        const float4 y = ld_cluster4(in_cta(join + (row * DV + c) * 4, s));
+        // a split that saw no key of the row holds zeros (or NaN, which stays)
+        const float w = tops[s] == -INFINITY ? 1.f : fast_exp2(tops[s] - top);
+        l += w * ls;
+        v.x += w * y.x; v.y += w * y.y; v.z += w * y.z; v.w += w * y.w;
+      }
+      store_row<T>(A, J, hk, row, c, v, top, l);
+    }
+    cluster_arrive();   // no CTA leaves while its memory is read
+    cluster_wait();
   }
   if (reports && tid == 0)
     A.status[b * A.nsplit + split] = *s_bad == 2 ? ATTN_ERR_TIMEOUT : J.bad ? ATTN_ERR_BAD_SEQLENS : *s_bad ? ATTN_ERR_BAD_PAGE : ATTN_OK;
@@ -698,6 +770,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Args A) {
 struct Layout {
   int nt, mtiles, job_rows, nsplit, split_tiles;
   long long jobs;
+  bool cluster;
   size_t off_status, off_ml, off_o, off_long, total;
   KvLong lng;
 };
@@ -724,11 +797,12 @@ static Layout layout(const attn_kv_fwd_params& p) {
   L.split_tiles = cdiv(cdiv(tiles, (int)n), NWARPS) * NWARPS;
   if (L.split_tiles > MAX_TILES) L.split_tiles = MAX_TILES;
   L.nsplit = cdiv(tiles, L.split_tiles);
+  L.cluster = L.nsplit > 1 && L.nsplit <= MAX_CLUSTER && L.jobs * L.nsplit <= WAVE;
   auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
   size_t o = 0;
   L.off_status = o;
   o = up(o + (size_t)p.batch * L.nsplit * sizeof(int));
-  const size_t parts = L.nsplit > 1 ? (size_t)L.jobs * L.nsplit : 0;
+  const size_t parts = L.nsplit > 1 && !L.cluster ? (size_t)L.jobs * L.nsplit : 0;
   L.off_ml = o;
   o = up(o + parts * 8 * L.nt * sizeof(float2));
   L.off_o = o;
@@ -796,6 +870,20 @@ static int launch(const Args& a, long long jobs, cudaStream_t st) {
   auto kern = kv_fwd_kernel<DQK, DV, NT, T>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return ATTN_ERR_CUDA;
+  if (a.cluster) {
+    cudaLaunchAttribute dims;
+    dims.id = cudaLaunchAttributeClusterDimension;
+    dims.val.clusterDim.x = a.nsplit;
+    dims.val.clusterDim.y = dims.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(jobs * a.nsplit));
+    cfg.blockDim = dim3(NTHREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cfg.attrs = &dims;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, maps, a) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  }
   kern<<<(unsigned)(jobs * a.nsplit), NTHREADS, C::SMEM, st>>>(maps, a);
   if (a.nsplit > 1) {
     cudaLaunchAttribute early;
@@ -866,6 +954,7 @@ static int run(const attn_kv_fwd_params* p, void* ws, size_t ws_bytes, cudaStrea
   a.scale_log2 = p->softmax_scale * 1.4426950408889634f;
   a.nsplit = L.nsplit;
   a.split_tiles = L.split_tiles;
+  a.cluster = L.cluster;
   a.mtiles = L.mtiles;
   a.long_from = L.lng.from;
   a.job_rows = L.job_rows;

@@ -14,6 +14,7 @@ namespace rope {
 
 constexpr int MAX_PAIRS = ATTN_ROPE_MAX_DIM / 2;
 constexpr int NTHREADS = 256;
+constexpr int RESIDENT = 5;   // CTAs per SM that the registers have to allow (58.7 us below; 62.3 with no bound, 62.6 at 6)
 
 // Turns per position as a fraction of 2^64: position * step wraps exactly like
 // the angle does, so no reduction error grows with the position.
@@ -80,7 +81,7 @@ struct alignas(sizeof(T) * N) Vec {
 // A CTA takes `tok` rows; its threads walk over (row, head, chunk) in steps of
 // NTHREADS.
 template <typename T, int VP, bool INTER>
-__global__ void __launch_bounds__(NTHREADS) rope_kernel(const Args A, const __grid_constant__ Table table) {
+__global__ void __launch_bounds__(NTHREADS, RESIDENT) rope_kernel(const Args A, const __grid_constant__ Table table) {
   using V = Vec<T, VP>;
   extern __shared__ unsigned long long dyn[];
   unsigned long long* s_step = dyn;                                   // [half]
@@ -266,7 +267,8 @@ static int run(const attn_rope_params* p, cudaStream_t st) {
   a.half = half;
   a.inverse = p->inverse != 0;
   // Rows of a CTA: eight share the table and the wait for their cosines (16,384
-  // rows of 40 heads of 128: 62.7 us, 87.6 at one row, 68.1 at sixteen); one where
+  // rows of 40 heads of 128: 58.7 us; before the register bound 62.7, 87.6 at one
+  // row, 68.1 at sixteen); one where
   // that would leave SMs without a CTA.
   a.tok = a.rows < 2048 ? 1 : 8;
   const int vp = f32 ? 4 : 8;
