@@ -1,8 +1,10 @@
 // Bookkeeping of a serving step (attn_kv_plan): prefix sums over the requests,
 // a stack of free pages, one slot and position per new token.
 //
-// A few kilobytes move, so the call is its launch and three dependent trips to
-// memory.  One CTA does it all: the sums of a batch of 8192 requests are eight
+// A few kilobytes move, so the call is its launch and dependent trips to memory:
+// the lengths, then the stack and tables (first to check them, then, out of L1,
+// to use them).  Slots are worked out from what was read, not from the entries
+// just written, so nothing waits for a store.  One CTA does it all: the sums of a batch of 8192 requests are eight
 // requests per thread, and nothing has to wait for another CTA.  Only the slots
 // and positions of many tokens (prompts) are left to a second kernel that spreads
 // them over the GPU, launched early so that it waits in place.
@@ -12,7 +14,8 @@
 namespace attn {
 namespace kvplan {
 
-constexpr int NTHREADS = 1024;
+constexpr int MAX_THREADS = 1024;
+constexpr int SMALL_THREADS = 256;   // a batch and tokens of at most this many: quicker barriers
 constexpr int FILL_THREADS = 256;
 constexpr int FILL_FROM = 4096;   // tokens
 
@@ -34,17 +37,18 @@ __device__ __forceinline__ int find(const int* prefix, int n, int x) {
 
 __device__ __forceinline__ int pages_of(int tokens, int shift) { return (int)(((long long)tokens + (1 << shift) - 1) >> shift); }
 
-__global__ void __launch_bounds__(NTHREADS) plan_kernel(const attn_kv_plan_params P, const int shift, const bool fill) {
+__global__ void __launch_bounds__(MAX_THREADS) plan_kernel(const attn_kv_plan_params P, const int shift, const bool fill) {
   extern __shared__ int sm[];
   const int n = P.batch;
   int* cu = sm;                   // [n + 1] new tokens before request b
   int* take = cu + n + 1;         // [n + 1] pages popped before it
   int* back = take + n + 1;       // [n + 1] pages given back before it
   int* len0 = back + n + 1;       // [n]     tokens it keeps
-  __shared__ Sums part[NTHREADS / 32];
+  __shared__ Sums part[MAX_THREADS / 32];
+  const int threads = blockDim.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (!fill) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int per = cdiv(n, NTHREADS);
+  const int per = cdiv(n, threads);
   const int b0 = min(tid * per, n), b1 = min(b0 + per, n);
   const int free_n = *P.free_count;   // the output may be the same word: read by all before the first barrier
   const long long cap = (long long)P.max_blocks << shift;
@@ -77,7 +81,7 @@ __global__ void __launch_bounds__(NTHREADS) plan_kernel(const attn_kv_plan_param
   if (lane == 31) part[warp] = s;
   const bool any_bad = __syncthreads_or(bad);
   Sums before{0, 0, 0}, total{0, 0, 0};
-  for (int w = 0; w < NTHREADS / 32; ++w) {
+  for (int w = 0; w < threads / 32; ++w) {
     if (w == warp) before = total;
     total = add(total, part[w]);
   }
@@ -114,22 +118,26 @@ __global__ void __launch_bounds__(NTHREADS) plan_kernel(const attn_kv_plan_param
   // page number i given back / popped i-th (before anything is written)
   auto given = [&](int i) {
     const int b = find(back, n, i);
-    return __ldcg(P.block_table + b * P.table_stride + (i - back[b]));
+    return P.block_table[b * P.table_stride + (i - back[b])];
+  };
+  auto popped = [&](int i) {
+    const int at = top - 1 - i;
+    return at < free_n ? P.free_pages[at] : given(at - free_n);
   };
   auto outside = [&](int page) { return page < 0 || page >= P.num_pages; };
   bool off = false;
-  for (int i = tid; i < nback; i += NTHREADS) off |= outside(given(i));
-  for (int i = tid; i < ntake; i += NTHREADS) {
+  for (int i = tid; i < nback; i += threads) off |= outside(given(i));
+  for (int i = tid; i < ntake; i += threads) {
     const int at = top - 1 - i;
-    if (at < free_n) off |= outside(__ldcg(P.free_pages + at));
+    if (at < free_n) off |= outside(P.free_pages[at]);
   }
   if (__syncthreads_or(off)) why = ATTN_ERR_BAD_PAGE;
   if (why != ATTN_OK) {
-    for (int b = tid; b <= n; b += NTHREADS) {
+    for (int b = tid; b <= n; b += threads) {
       P.cu_seqlens[b] = 0;
       if (b < n) P.seqlens_out[b] = P.seqlens[b];
     }
-    for (int t = tid; fill && t < P.max_tokens; t += NTHREADS) {
+    for (int t = tid; fill && t < P.max_tokens; t += threads) {
       P.positions[t] = 0;
       P.slots[t] = -1;
     }
@@ -139,13 +147,14 @@ __global__ void __launch_bounds__(NTHREADS) plan_kernel(const attn_kv_plan_param
     }
     return;
   }
-  for (int i = tid; i < nback; i += NTHREADS) P.free_pages[free_n + i] = given(i);
-  __syncthreads();
-  for (int i = tid; i < ntake; i += NTHREADS) {
+  // No entry written here is read here: pushes land above free_n, pops in
+  // entries past the pages a request holds.
+  for (int i = tid; i < nback; i += threads) P.free_pages[free_n + i] = given(i);
+  for (int i = tid; i < ntake; i += threads) {
     const int b = find(take, n, i);
-    P.block_table[b * P.table_stride + pages_of(len0[b], shift) + (i - take[b])] = __ldcg(P.free_pages + top - 1 - i);
+    P.block_table[b * P.table_stride + pages_of(len0[b], shift) + (i - take[b])] = popped(i);
   }
-  for (int b = tid; b <= n; b += NTHREADS) {
+  for (int b = tid; b <= n; b += threads) {
     P.cu_seqlens[b] = cu[b];
     if (b < n) P.seqlens_out[b] = len0[b] + cu[b + 1] - cu[b];
   }
@@ -154,15 +163,15 @@ __global__ void __launch_bounds__(NTHREADS) plan_kernel(const attn_kv_plan_param
     *P.status = ATTN_OK;
   }
   if (!fill) return;
-  __syncthreads();
   const int total_tok = cu[n];
-  for (int t = tid; t < P.max_tokens; t += NTHREADS) {
+  for (int t = tid; t < P.max_tokens; t += threads) {
     int pos = 0;
     long long slot = -1;
     if (t < total_tok) {
       const int b = find(cu, n, t);
       pos = len0[b] + t - cu[b];
-      const int page = __ldcg(P.block_table + b * P.table_stride + (pos >> shift));
+      const int block = pos >> shift, held = pages_of(len0[b], shift);
+      const int page = block < held ? P.block_table[b * P.table_stride + block] : popped(take[b] + block - held);
       slot = ((long long)page << shift) + (pos & ((1 << shift) - 1));
     }
     P.positions[t] = pos;
@@ -211,7 +220,8 @@ static int run(const attn_kv_plan_params* p, cudaStream_t st) {
       cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return ATTN_ERR_CUDA;
   const bool fill = p->max_tokens <= FILL_FROM;
-  plan_kernel<<<1, NTHREADS, smem, st>>>(*p, shift, fill);
+  const int threads = p->batch <= SMALL_THREADS && p->max_tokens <= SMALL_THREADS ? SMALL_THREADS : MAX_THREADS;
+  plan_kernel<<<1, threads, smem, st>>>(*p, shift, fill);
   if (!fill) {
     cudaLaunchAttribute early;
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
