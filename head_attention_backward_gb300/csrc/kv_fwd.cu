@@ -49,15 +49,23 @@ namespace kvfwd {
 constexpr int NWARPS = 4;
 constexpr int NTHREADS = 32 * NWARPS;
 constexpr int TILE = 16;            // keys of a warp's step
-constexpr int MAX_TILES = 256;      // tiles of a split: its page table fits shared memory
-// Splits.  Few jobs: as many CTAs as fill one wave of two per SM (one request of
-// 131,072 tokens, 8 kv heads: 50.5 us with 304 CTAs, 55.3 with 152, 56.3 with
-// 608: more parts to join and an uneven second wave).  Many jobs: splits short
-// enough to even out ragged lengths (64 requests of up to 8,192 tokens: 108.4 us
-// at 64 tiles, 114.2 at 256, 114.0 at 32).  None so short that its prologue
-// outweighs it (4 requests of 1,000 tokens: 8.5 us at 12 tiles, 8.8 at 8, 8.9 at
-// 16).
+constexpr int META_TILES = 256;     // tiles whose pages are held in shared memory at a time
+// Splits.  A job is one row tile of one request and kv head.  The host sets how
+// many splits a job has at most, the device how long they are, from the request's
+// own length, so that max_seqlen_k need not be tight.
+// * Few jobs: splits for one wave of two CTAs per SM (one request of 131,072
+//   tokens, 8 kv heads: 50.5 us with 304 CTAs, 55.3 with 152, 56.3 with 608: more
+//   parts to join and an uneven second wave).
+// * Many jobs: splits short enough to even out ragged lengths (64 requests of up to
+//   8,192 tokens: 108.4 us at 64 tiles, 114.2 at 256, 114.0 at 32), as long as the
+//   grid stays within MAX_GRID: CTAs without work cost about 2 ns each.
+// * None so short that its prologue outweighs it (4 requests of 1,000 tokens: 8.5
+//   us at 12 tiles, 8.8 at 8, 8.9 at 16).
+// A list of (job, split) items made on the device by a kernel before this one, and
+// taken by persistent CTAs, was slower throughout (65 us and 119 us in the first two
+// cases): it puts two more trips to memory in front of the first load.
 constexpr int WAVE = 304;
+constexpr int MAX_GRID = 4608;
 constexpr int EVEN_TILES = 64;
 constexpr int MIN_TILES = 12;
 // Up to eight splits of a grid of one wave are joined as clusters: no second
@@ -75,11 +83,11 @@ struct Cfg {
   static constexpr int ROWS = 8 * NT;
   static constexpr int KB = TILE * DQK, VB = TILE * DV;
   static constexpr int STAGE = KB + VB;
-    static constexpr int NST = STAGE <= 2048 ? 6 : 3;
+  static constexpr int NST = STAGE <= 2048 ? 6 : 3;
   static constexpr int RING = NST * STAGE;
   static constexpr int OFF_BAR = NWARPS * RING;                        // uint64_t[NWARPS][NST]
-  static constexpr int OFF_META = OFF_BAR + NWARPS * NST * 8;          // int2[MAX_TILES + 1]: page, exponents
-  static constexpr int OFF_ML = OFF_META + (MAX_TILES + 1) * 8;        // float[2][NWARPS][ROWS]
+  static constexpr int OFF_META = OFF_BAR + NWARPS * NST * 8;          // int2[META_TILES + 1]: page, exponents
+  static constexpr int OFF_ML = OFF_META + (META_TILES + 1) * 8;       // float[2][NWARPS][ROWS]
   static constexpr int SMEM = OFF_ML + 2 * NWARPS * ROWS * 4 + ROWS * 8 + 8 + 1024;   // + alignment slack
   // CTAs per SM that the registers have to allow (shared memory allows them too)
   static constexpr int RESIDENT = NT == 1 ? (DQK == 256 ? 2 : DQK == 192 ? 3 : 4) : (DQK == 256 ? 1 : DQK == 192 ? 2 : 3);
@@ -107,11 +115,11 @@ struct Args {
   int hq, g;             // query heads, per kv head
   int mask, left, right;
   float scale_log2;
-  int nsplit, split_tiles, mtiles;
+  int nsplit, min_tiles, mtiles;   // most splits of a job, least tiles of one; most row tiles of a request
   int cluster;           // 1: the splits of a job are a cluster
   int job_rows;          // most rows that a row tile can have
-  float* part_o;         // [job][nsplit][rows][DV]
-  float2* part_ml;       // [job][nsplit][rows]
+  float* part_o;         // [job][nsplit][job_rows][DV]
+  float2* part_ml;       // [job][nsplit][job_rows]
   int* status;           // [batch][nsplit]
   KvCacheView c;
 };
@@ -152,6 +160,11 @@ __device__ __forceinline__ Job make_job(const Args& A, int b, int m, MaskArgs& m
   j.kbeg = j.klo & ~(TILE - 1);
   j.ntile = j.khi >= j.klo ? (j.khi - j.kbeg) / TILE + 1 : 0;
   return j;
+}
+
+// Tiles of a job's splits: equal shares, whole turns of the warps.
+__device__ __forceinline__ int split_tiles(const Args& A, const Job& j) {
+  return cdiv(max(A.min_tiles, cdiv(j.ntile, A.nsplit)), NWARPS) * NWARPS;
 }
 
 __device__ __forceinline__ bool sees(const MaskArgs& m, int i, int j) {
@@ -304,19 +317,13 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
   MaskArgs mk;
   const Job J = make_job<ROWS>(A, b, m, mk);
   const bool reports = hk == 0 && m == 0;   // one CTA per (request, split) says what it found
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * C::NST;
-  if (tid == 0) *s_bad = 0;
-  if (lane == 0) {
-    for (int i = 0; i < C::NST; ++i) ptx::mbar_init(bars + i, 1);
-    ptx::fence_mbar_init();
-    ptx::tma_prefetch_desc(&maps.k);
-    ptx::tma_prefetch_desc(&maps.v);
-  }
-  const int tile0 = split * A.split_tiles;
+  const int per_split = split_tiles(A, J);
+  const bool whole = J.ntile <= per_split;        // no other split holds keys of these rows
+  const int tile0 = split * per_split;
   if (J.nrow <= 0 || (split > 0 && tile0 >= J.ntile)) {
     if (reports && tid == 0) A.status[b * A.nsplit + split] = J.bad ? ATTN_ERR_BAD_SEQLENS : ATTN_OK;
     // a cluster whose rows have splits to join (the same for all of it) meets twice
-    if (A.cluster && J.nrow > 0 && J.ntile > A.split_tiles) {
+    if (A.cluster && J.nrow > 0 && !whole) {
       cluster_arrive();
       cluster_wait();
       cluster_arrive();
@@ -324,59 +331,57 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
     }
     return;
   }
-  const int ntile = min(A.split_tiles, J.ntile - tile0);      // may be <= 0 for split 0
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * C::NST;
+  if (tid == 0) *s_bad = 0;
+  if (lane == 0) {
+    for (int i = 0; i < C::NST; ++i) ptx::mbar_init(bars + i, 1);
+    ptx::fence_mbar_init();
+  }
+  const int ntile = min(per_split, J.ntile - tile0);      // may be <= 0 for split 0
   const int key0 = J.kbeg + tile0 * TILE;
-  const int page0 = key0 >> A.c.page_shift;
   const int shift = A.c.page_shift, in_page = (1 << shift) - 1;
-  const uint32_t ring = ptx::smem_u32(smem) + warp * C::RING;
+  const int page0 = key0 >> shift;
   const int* table = A.table + b * A.table_stride + page0;
-  // tile i of the split, of this page, into stage `at` (lane 0): every tile
+  const uint32_t ring = ptx::smem_u32(smem) + warp * C::RING;
+  int at_in = 0, at_out = 0;      // stages of the ring to fill and to read next, the latter's phase
+  uint32_t parity = 0;
+  auto advance = [&](int at) { return at + 1 == C::NST ? 0 : at + 1; };
+  // tile i of the split, of this page, into the next stage (lane 0): every tile
   // completes its barrier once
-  auto load = [&](int i, int at, int page) {
+  auto load = [&](int i, int page) {
     const int row = (key0 + i * TILE) & in_page;
-    const uint32_t st = ring + at * C::STAGE;
+    const uint32_t st = ring + at_in * C::STAGE;
     if (page >= 0 && page < A.c.num_pages) {
-      ptx::mbar_arrive_expect_tx(bars + at, C::STAGE);
+      ptx::mbar_arrive_expect_tx(bars + at_in, C::STAGE);
 #pragma unroll
       for (int c = 0; c < Box<DQK>::N; ++c)
-        tma_load_4d(st + c * TILE * Box<DQK>::W, &maps.k, bars + at, c * Box<DQK>::W, hk, row, page);
+        tma_load_4d(st + c * TILE * Box<DQK>::W, &maps.k, bars + at_in, c * Box<DQK>::W, hk, row, page);
 #pragma unroll
       for (int c = 0; c < Box<DV>::N; ++c)
-        tma_load_4d(st + C::KB + c * TILE * Box<DV>::W, &maps.v, bars + at, c * Box<DV>::W, hk, row, page);
+        tma_load_4d(st + C::KB + c * TILE * Box<DV>::W, &maps.v, bars + at_in, c * Box<DV>::W, hk, row, page);
     } else {
-      ptx::mbar_arrive(bars + at);
+      ptx::mbar_arrive(bars + at_in);
     }
   };
-  // the first tiles leave before anything else is known
-  if (lane == 0) {
+  // tiles [from, to) are worked on with their pages in shared memory; the first
+  // ones leave before anything else is known
+  auto start = [&](int from, int to) {
     int first[C::NST - 1];
 #pragma unroll
     for (int s = 0; s < C::NST - 1; ++s) {
-      const int i = warp + s * NWARPS;
-      first[s] = i < ntile ? __ldg(table + (((key0 + i * TILE) >> shift) - page0)) : -1;
+      const int i = from + warp + s * NWARPS;
+      first[s] = lane == 0 && i < to ? __ldg(table + (((key0 + i * TILE) >> shift) - page0)) : -1;
     }
 #pragma unroll
-    for (int s = 0; s < C::NST - 1; ++s)
-      if (warp + s * NWARPS < ntile) load(warp + s * NWARPS, s, first[s]);
-  }
-  __syncthreads();
-
-  // pages and scales of this split
-  if (ntile > 0) {
-    const int npage = ((key0 + ntile * TILE - 1) >> A.c.page_shift) - page0 + 1;
-    for (int i = tid; i < npage; i += NTHREADS) {
-      const int page = __ldg(table + i);
-      int e = 0;
-      if (page >= 0 && page < A.c.num_pages) {
-        const long long at = (long long)page * A.c.hkv + hk;
-        e = (kv_exp_of(__ldg(A.c.k_exp + at)) & 0xffff) | (kv_exp_of(__ldg(A.c.v_exp + at)) << 16);
-        meta[i] = make_int2(page, e);
-      } else {
-        *s_bad = 1;
-        meta[i] = make_int2(-1, 0);
+    for (int s = 0; s < C::NST - 1; ++s) {
+      const int i = from + warp + s * NWARPS;
+      if (i < to) {
+        if (lane == 0) load(i, first[s]);
+        at_in = advance(at_in);
       }
     }
-  }
+  };
+  start(0, min(ntile, META_TILES));
 
   // row g of each row group of q, as fp16 under a power of two; a negative
   // softmax scale goes into its sign, so scores and their factors order alike
@@ -427,7 +432,6 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
       tok[n][r] = min(J.row0 + 8 * n + 2 * t + r, J.row0 + J.nrow - 1) / A.g;
     }
   }
-  __syncthreads();
 
   constexpr int MT = DV / 16;     // tiles of 16 value columns
   float o[NT][MT][4];
@@ -444,167 +448,180 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
   int unit = 0;                   // the accumulator counts in 2^unit
   const int itok0 = J.row0 / A.g, itok1 = (J.row0 + J.nrow - 1) / A.g;
 
-  int at_in = C::NST - 1, at_out = 0;
-  uint32_t parity = 0;
   bool arrived = true;
-  for (int i = warp; i < ntile; i += NWARPS) {
-    const int ahead = i + (C::NST - 1) * NWARPS;
-    if (lane == 0 && ahead < ntile) load(ahead, at_in, meta[((key0 + ahead * TILE) >> shift) - page0].x);
-    at_in = at_in + 1 == C::NST ? 0 : at_in + 1;
-    const int key = key0 + i * TILE;
-    const int2 mt = meta[(key >> shift) - page0];
-    const uint32_t st = ring + at_out * C::STAGE;
-    arrived = __all_sync(0xffffffffu, wait_bar(ptx::smem_u32(bars + at_out), parity));
-    if (!arrived) {
-      // give the copies still in flight as long again before the memory is used
-      for (int j = 0; j < C::NST && i + j * NWARPS < ntile; ++j) {
-        wait_bar(ptx::smem_u32(bars + at_out), parity);
-        if (++at_out == C::NST) {
-          at_out = 0;
-          parity ^= 1;
-        }
+  for (int from = 0; from < ntile; from += META_TILES) {
+    const int to = min(ntile, from + META_TILES), meta0 = (key0 + from * TILE) >> shift;
+    if (from > 0 && arrived) start(from, to);
+    __syncthreads();   // the pages before these have been used
+    for (int i = tid; i <= ((key0 + to * TILE - 1) >> shift) - meta0; i += NTHREADS) {
+      const int page = __ldg(table + (meta0 - page0) + i);
+      if (page >= 0 && page < A.c.num_pages) {
+        const long long at = (long long)page * A.c.hkv + hk;
+        const int ek = kv_exp_of(__ldg(A.c.k_exp + at)), ev = kv_exp_of(__ldg(A.c.v_exp + at));
+        meta[i] = make_int2(page, (ek & 0xffff) | (ev << 16));
+      } else {
+        *s_bad = 1;
+        meta[i] = make_int2(-1, 0);
       }
-      break;
     }
-    if (++at_out == C::NST) {
-      at_out = 0;
-      parity ^= 1;
-    }
-    if (mt.x >= 0) {
-      const bool inside = key >= J.klo && key + TILE - 1 <= J.khi;
-      if (!inside) {
-        // rows that no query sees may hold anything: zero V there (masked
-        // scores make their weights 0, but 0 NaN is NaN)
-        for (int n = lane; n < TILE * (DV / 16); n += 32) {
-          const int r = n / (DV / 16), c = n % (DV / 16);
-          if (key + r < J.klo || key + r > J.khi)
-            *reinterpret_cast<uint4*>(smem + warp * C::RING + (st - ring) + C::KB + off<DV>(r, c)) = make_uint4(0, 0, 0, 0);
-        }
-        ptx::fence_proxy_async_smem();   // before the stage is refilled by TMA
-        __syncwarp();
+    __syncthreads();
+    for (int i = from + warp; arrived && i < to; i += NWARPS) {
+      const int ahead = i + (C::NST - 1) * NWARPS;
+      if (ahead < to) {
+        if (lane == 0) load(ahead, meta[((key0 + ahead * TILE) >> shift) - meta0].x);
+        at_in = advance(at_in);
       }
-      // S^T = K Q^T: keys key_of(g) and 8 more, rows 2t and 2t + 1
-      float s[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
-#pragma unroll
-      for (int c = 0; c < DQK / 64; ++c) {
-        const uint4 w0 = lds128(st + off<DQK>(key_of(g), t + 4 * c)), w1 = lds128(st + off<DQK>(8 + key_of(g), t + 4 * c));
-        const uint32_t a0[4] = {w0.x, w0.y, w0.z, w0.w}, a1[4] = {w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t a[4] = {e4m3x2_to_h2((uint16_t)a0[k]), e4m3x2_to_h2((uint16_t)a1[k]),
-                                 e4m3x2_to_h2((uint16_t)(a0[k] >> 16)), e4m3x2_to_h2((uint16_t)(a1[k] >> 16))};
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816(s[n], a, qb[n][4 * c + k][0], qb[n][4 * c + k][1]);
+      const int key = key0 + i * TILE;
+      const int2 mt = meta[(key >> shift) - meta0];
+      const uint32_t st = ring + at_out * C::STAGE;
+      arrived = __all_sync(0xffffffffu, wait_bar(ptx::smem_u32(bars + at_out), parity));
+      if (!arrived) {
+        // give the copies still in flight as long again before the memory is used
+        for (int j = 0; j < C::NST && i + j * NWARPS < to; ++j) {
+          wait_bar(ptx::smem_u32(bars + at_out), parity);
+          at_out = advance(at_out);
+          parity ^= at_out == 0;
         }
+        break;
       }
-      const float ks = exp2_int((int)(short)(mt.y & 0xffff));
-      const bool full = inside &&
-                        (mk.right < 0 || key + TILE - 1 <= (long long)itok0 + mk.off + mk.right) &&
-                        (mk.left < 0 || key >= (long long)itok1 + mk.off - mk.left);
-      if (!full) {
+      at_out = advance(at_out);
+      parity ^= at_out == 0;
+      if (mt.x >= 0) {
+        const bool inside = key >= J.klo && key + TILE - 1 <= J.khi;
+        if (!inside) {
+          // rows that no query sees may hold anything: zero V there (masked
+          // scores make their weights 0, but 0 NaN is NaN)
+          for (int n = lane; n < TILE * (DV / 16); n += 32) {
+            const int r = n / (DV / 16), c = n % (DV / 16);
+            if (key + r < J.klo || key + r > J.khi)
+              *reinterpret_cast<uint4*>(smem + warp * C::RING + (st - ring) + C::KB + off<DV>(r, c)) = make_uint4(0, 0, 0, 0);
+          }
+          ptx::fence_proxy_async_smem();   // before the stage is refilled by TMA
+          __syncwarp();
+        }
+        // S^T = K Q^T: keys key_of(g) and 8 more, rows 2t and 2t + 1
+        float s[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
+          for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
+#pragma unroll
+        for (int c = 0; c < DQK / 64; ++c) {
+          const uint4 w0 = lds128(st + off<DQK>(key_of(g), t + 4 * c)), w1 = lds128(st + off<DQK>(8 + key_of(g), t + 4 * c));
+          const uint32_t a0[4] = {w0.x, w0.y, w0.z, w0.w}, a1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int kk = key + key_of(g) + 8 * (k >> 1);
-            if (kk < J.klo || kk > J.khi || !sees(mk, tok[n][k & 1], kk)) s[n][k] = -INFINITY;
+            const uint32_t a[4] = {e4m3x2_to_h2((uint16_t)a0[k]), e4m3x2_to_h2((uint16_t)a1[k]),
+                                   e4m3x2_to_h2((uint16_t)(a0[k] >> 16)), e4m3x2_to_h2((uint16_t)(a1[k] >> 16))};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(s[n], a, qb[n][4 * c + k][0], qb[n][4 * c + k][1]);
           }
-      }
-      bool grow = false;
-      float f[NT][2], top[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          f[n][r] = fmaxf(rs[n][r] * ks, 1.17549435e-38f);   // never 0: a masked score stays -inf
-          top[n][r] = fmaxf(s[n][r], s[n][2 + r]) * f[n][r];
-          grow |= top[n][r] > mrow[n][r] + SLACK_LOG2;
         }
-      const int ev = mt.y >> 16;
-      grow = __any_sync(0xffffffffu, grow);
-      if (grow || ev > unit + EV_SLACK || ev < unit - EV_SLACK) {
-        const float de = exp2_int(unit - ev);
-        unit = ev;
+        const float ks = exp2_int((int)(short)(mt.y & 0xffff));
+        const bool full = inside &&
+                          (mk.right < 0 || key + TILE - 1 <= (long long)itok0 + mk.off + mk.right) &&
+                          (mk.left < 0 || key >= (long long)itok1 + mk.off - mk.left);
+        if (!full) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float a[2];
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int kk = key + key_of(g) + 8 * (k >> 1);
+              if (kk < J.klo || kk > J.khi || !sees(mk, tok[n][k & 1], kk)) s[n][k] = -INFINITY;
+            }
+        }
+        bool grow = false;
+        float f[NT][2], top[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            float x = top[n][r];
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            a[r] = 1.f;
-            if (x > mrow[n][r]) {
-              a[r] = fast_exp2(mrow[n][r] - x);   // 0 from -inf
-              mrow[n][r] = x;
-            }
-            lrow[n][r] *= a[r];
-            a[r] *= de;
+            f[n][r] = fmaxf(rs[n][r] * ks, 1.17549435e-38f);   // never 0: a masked score stays -inf
+            top[n][r] = fmaxf(s[n][r], s[n][2 + r]) * f[n][r];
+            grow |= top[n][r] > mrow[n][r] + SLACK_LOG2;
           }
+        const int ev = mt.y >> 16;
+        grow = __any_sync(0xffffffffu, grow);
+        if (grow || ev > unit + EV_SLACK || ev < unit - EV_SLACK) {
+          const float de = exp2_int(unit - ev);
+          unit = ev;
 #pragma unroll
-          for (int j = 0; j < MT; ++j)
+          for (int n = 0; n < NT; ++n) {
+            float a[2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) o[n][j][k] *= a[k & 1];
+            for (int r = 0; r < 2; ++r) {
+              float x = top[n][r];
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+              a[r] = 1.f;
+              if (x > mrow[n][r]) {
+                a[r] = fast_exp2(mrow[n][r] - x);   // 0 from -inf
+                mrow[n][r] = x;
+              }
+              lrow[n][r] *= a[r];
+              a[r] *= de;
+            }
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[n][j][k] *= a[k & 1];
+          }
         }
-      }
-      const __half2 ratio = __float2half2_rn(exp2_int(ev - unit));
-      const uint32_t ratio_bits = *reinterpret_cast<const uint32_t*>(&ratio);
-      uint32_t pb[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float r0 = mrow[n][0] == -INFINITY ? 0.f : P_LOG2 - mrow[n][0];
-        const float r1 = mrow[n][1] == -INFINITY ? 0.f : P_LOG2 - mrow[n][1];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float p0 = fast_exp2(fmaf(s[n][2 * j], f[n][0], r0)), p1 = fast_exp2(fmaf(s[n][2 * j + 1], f[n][1], r1));
-          lrow[n][0] += p0;
-          lrow[n][1] += p1;
-          pb[n][j] = transpose8x8(mul_h2(pack_h2(p0, p1), ratio_bits));
-        }
-      }
-      // O^T += V^T P^T: keys key_of(2t), key_of(2t + 1) and 8 more are this lane's
-      // rows of V; column tile j holds elements 2j (its rows 0-7) and 2j + 1 of each lane
-      // group's consecutive columns
-      const uint32_t vt = st + C::KB;
-      auto columns = [&](int j, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
-        const uint32_t lo0 = __byte_perm(w0, w1, 0x5140), hi0 = __byte_perm(w0, w1, 0x7362);
-        const uint32_t lo1 = __byte_perm(w2, w3, 0x5140), hi1 = __byte_perm(w2, w3, 0x7362);
-        const uint32_t a[4] = {e4m3x2_to_h2((uint16_t)lo0), e4m3x2_to_h2((uint16_t)(lo0 >> 16)),
-                               e4m3x2_to_h2((uint16_t)lo1), e4m3x2_to_h2((uint16_t)(lo1 >> 16))};
-        const uint32_t c[4] = {e4m3x2_to_h2((uint16_t)hi0), e4m3x2_to_h2((uint16_t)(hi0 >> 16)),
-                               e4m3x2_to_h2((uint16_t)hi1), e4m3x2_to_h2((uint16_t)(hi1 >> 16))};
+        const __half2 ratio = __float2half2_rn(exp2_int(ev - unit));
+        const uint32_t ratio_bits = *reinterpret_cast<const uint32_t*>(&ratio);
+        uint32_t pb[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          mma16816(o[n][j], a, pb[n][0], pb[n][1]);
-          mma16816(o[n][j + 1], c, pb[n][0], pb[n][1]);
-        }
-      };
-      const int v0 = key_of(2 * t), v1 = key_of(2 * t + 1);
-      if (DV == 64) {
-        const int c = g >> 1, h8 = (g & 1) * 8;
-        const uint2 w0 = lds64(vt + off<DV>(v0, c) + h8), w1 = lds64(vt + off<DV>(v1, c) + h8);
-        const uint2 w2 = lds64(vt + off<DV>(v0 + 8, c) + h8), w3 = lds64(vt + off<DV>(v1 + 8, c) + h8);
-        columns(0, w0.x, w1.x, w2.x, w3.x);
-        columns(2, w0.y, w1.y, w2.y, w3.y);
-      } else {
+          const float r0 = mrow[n][0] == -INFINITY ? 0.f : P_LOG2 - mrow[n][0];
+          const float r1 = mrow[n][1] == -INFINITY ? 0.f : P_LOG2 - mrow[n][1];
 #pragma unroll
-        for (int half = 0; half < DV / 128; ++half) {
-          const int c = g + 8 * half;
-          const uint4 w0 = lds128(vt + off<DV>(v0, c)), w1 = lds128(vt + off<DV>(v1, c));
-          const uint4 w2 = lds128(vt + off<DV>(v0 + 8, c)), w3 = lds128(vt + off<DV>(v1 + 8, c));
-          columns(8 * half, w0.x, w1.x, w2.x, w3.x);
-          columns(8 * half + 2, w0.y, w1.y, w2.y, w3.y);
-          columns(8 * half + 4, w0.z, w1.z, w2.z, w3.z);
-          columns(8 * half + 6, w0.w, w1.w, w2.w, w3.w);
+          for (int j = 0; j < 2; ++j) {
+            const float p0 = fast_exp2(fmaf(s[n][2 * j], f[n][0], r0)), p1 = fast_exp2(fmaf(s[n][2 * j + 1], f[n][1], r1));
+            lrow[n][0] += p0;
+            lrow[n][1] += p1;
+            pb[n][j] = transpose8x8(mul_h2(pack_h2(p0, p1), ratio_bits));
+          }
+        }
+        // O^T += V^T P^T: keys key_of(2t), key_of(2t + 1) and 8 more are this lane's
+        // rows of V; column tile j holds elements 2j (its rows 0-7) and 2j + 1 of each lane
+        // group's consecutive columns
+        const uint32_t vt = st + C::KB;
+        auto columns = [&](int j, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+          const uint32_t lo0 = __byte_perm(w0, w1, 0x5140), hi0 = __byte_perm(w0, w1, 0x7362);
+          const uint32_t lo1 = __byte_perm(w2, w3, 0x5140), hi1 = __byte_perm(w2, w3, 0x7362);
+          const uint32_t a[4] = {e4m3x2_to_h2((uint16_t)lo0), e4m3x2_to_h2((uint16_t)(lo0 >> 16)),
+                                 e4m3x2_to_h2((uint16_t)lo1), e4m3x2_to_h2((uint16_t)(lo1 >> 16))};
+          const uint32_t c[4] = {e4m3x2_to_h2((uint16_t)hi0), e4m3x2_to_h2((uint16_t)(hi0 >> 16)),
+                                 e4m3x2_to_h2((uint16_t)hi1), e4m3x2_to_h2((uint16_t)(hi1 >> 16))};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma16816(o[n][j], a, pb[n][0], pb[n][1]);
+            mma16816(o[n][j + 1], c, pb[n][0], pb[n][1]);
+          }
+        };
+        const int v0 = key_of(2 * t), v1 = key_of(2 * t + 1);
+        if (DV == 64) {
+          const int c = g >> 1, h8 = (g & 1) * 8;
+          const uint2 w0 = lds64(vt + off<DV>(v0, c) + h8), w1 = lds64(vt + off<DV>(v1, c) + h8);
+          const uint2 w2 = lds64(vt + off<DV>(v0 + 8, c) + h8), w3 = lds64(vt + off<DV>(v1 + 8, c) + h8);
+          columns(0, w0.x, w1.x, w2.x, w3.x);
+          columns(2, w0.y, w1.y, w2.y, w3.y);
+        } else {
+#pragma unroll
+          for (int half = 0; half < DV / 128; ++half) {
+            const int c = g + 8 * half;
+            const uint4 w0 = lds128(vt + off<DV>(v0, c)), w1 = lds128(vt + off<DV>(v1, c));
+            const uint4 w2 = lds128(vt + off<DV>(v0 + 8, c)), w3 = lds128(vt + off<DV>(v1 + 8, c));
+            columns(8 * half, w0.x, w1.x, w2.x, w3.x);
+            columns(8 * half + 2, w0.y, w1.y, w2.y, w3.y);
+            columns(8 * half + 4, w0.z, w1.z, w2.z, w3.z);
+            columns(8 * half + 6, w0.w, w1.w, w2.w, w3.w);
+          }
         }
       }
+      __syncwarp();   // the stage may be refilled
     }
-    __syncwarp();   // the stage may be refilled
   }
   if (!arrived) {   // a load did not arrive: no result instead of a wrong one
     *s_bad = 2;
@@ -647,7 +664,6 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
     }
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const bool whole = J.ntile <= A.split_tiles;   // no other split holds keys of these rows
   const long long part = ((long long)(b * A.c.hkv + hk) * A.mtiles + m) * A.nsplit + split;
   float* s_join = reinterpret_cast<float*>(smem + C::OFF_JOIN);
   const int pieces = J.nrow * (DV / 4);
@@ -671,15 +687,15 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
       *reinterpret_cast<float4*>(s_join + row * DV + c) = v;
       if (c == 0) s_jml[row] = make_float2(top, l);
     } else {
-      *reinterpret_cast<float4*>(A.part_o + (part * ROWS + row) * DV + c) = v;
-      if (c == 0) A.part_ml[part * ROWS + row] = make_float2(top, l);
+      *reinterpret_cast<float4*>(A.part_o + (part * A.job_rows + row) * DV + c) = v;
+      if (c == 0) A.part_ml[part * A.job_rows + row] = make_float2(top, l);
     }
   }
   if (A.cluster && !whole) {
     // each CTA finishes its share of the rows' pieces
     cluster_arrive();
     cluster_wait();
-    const int n = cdiv(J.ntile, A.split_tiles);
+    const int n = cdiv(J.ntile, per_split);
     const uint32_t join = ptx::smem_u32(s_join), jml = ptx::smem_u32(s_jml);
     for (int i = split * NTHREADS + tid; i < pieces; i += n * NTHREADS) {
       const int row = i / (DV / 4), c = (i % (DV / 4)) * 4;
@@ -728,13 +744,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Args A) {
   const int m = job % A.mtiles, bh = job / A.mtiles, hk = bh % A.c.hkv, b = bh / A.c.hkv;
   MaskArgs mk;
   const Job J = make_job<ROWS>(A, b, m, mk);
-  if (row >= J.nrow || J.ntile <= A.split_tiles) return;
-  const int n = cdiv(J.ntile, A.split_tiles);
+  const int n = cdiv(J.ntile, split_tiles(A, J));
+  if (row >= J.nrow || n <= 1) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");   // launched early: the splits' kernel ends here
-  const float2* ml = A.part_ml + (long long)job * A.nsplit * ROWS + row;
-  const float* po = A.part_o + ((long long)job * A.nsplit * ROWS + row) * DV + c;
+  const float2* ml = A.part_ml + (long long)job * A.nsplit * A.job_rows + row;
+  const float* po = A.part_o + ((long long)job * A.nsplit * A.job_rows + row) * DV + c;
   float top = -INFINITY;
-  for (int s = threadIdx.x; s < n; s += blockDim.x) top = fmaxf(top, ml[s * ROWS].x);
+  for (int s = threadIdx.x; s < n; s += blockDim.x) top = fmaxf(top, ml[s * A.job_rows].x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
@@ -744,8 +760,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Args A) {
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int s = grp; s < n; s += groups) {
-    const float2 x = ml[s * ROWS];
-    const float4 y = *reinterpret_cast<const float4*>(po + (long long)s * ROWS * DV);
+    const float2 x = ml[s * A.job_rows];
+    const float4 y = *reinterpret_cast<const float4*>(po + (long long)s * A.job_rows * DV);
     // a split that saw no key of the row holds zeros (or NaN, which stays)
     const float w = x.x == -INFINITY ? 1.f : fast_exp2(x.x - top);
     l += w * x.y;
@@ -768,7 +784,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Args A) {
 // ---------------------------------------------------------------- host side
 
 struct Layout {
-  int nt, mtiles, job_rows, nsplit, split_tiles;
+  int nt, mtiles, job_rows, nsplit, min_tiles;
   long long jobs;
   bool cluster;
   size_t off_status, off_ml, off_o, off_long, total;
@@ -791,22 +807,20 @@ static Layout layout(const attn_kv_fwd_params& p) {
   L.job_rows = (int)(rows < 8 * L.nt ? rows : 8 * L.nt);
   L.jobs = (long long)p.batch * p.cache.nhead_kv * L.mtiles;
   const int tiles = max_keys(p) / TILE + 2;
-  long long n = L.jobs >= WAVE ? cdiv(tiles, EVEN_TILES) : WAVE / L.jobs;
-  if (n > cdiv(tiles, MIN_TILES)) n = cdiv(tiles, MIN_TILES);
-  if (n < cdiv(tiles, MAX_TILES)) n = cdiv(tiles, MAX_TILES);
-  L.split_tiles = cdiv(cdiv(tiles, (int)n), NWARPS) * NWARPS;
-  if (L.split_tiles > MAX_TILES) L.split_tiles = MAX_TILES;
-  L.nsplit = cdiv(tiles, L.split_tiles);
-  L.cluster = L.nsplit > 1 && L.nsplit <= MAX_CLUSTER && L.jobs * L.nsplit <= WAVE;
+  const bool few = L.jobs < WAVE;
+  L.min_tiles = few ? MIN_TILES : EVEN_TILES;
+  const long long n = few ? WAVE / L.jobs : cdiv_ll(MAX_GRID, L.jobs);
+  L.nsplit = n < cdiv(tiles, L.min_tiles) ? (int)n : cdiv(tiles, L.min_tiles);
+  L.cluster = few && L.nsplit > 1 && L.nsplit <= MAX_CLUSTER;
   auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
   size_t o = 0;
   L.off_status = o;
   o = up(o + (size_t)p.batch * L.nsplit * sizeof(int));
   const size_t parts = L.nsplit > 1 && !L.cluster ? (size_t)L.jobs * L.nsplit : 0;
   L.off_ml = o;
-  o = up(o + parts * 8 * L.nt * sizeof(float2));
+  o = up(o + parts * L.job_rows * sizeof(float2));
   L.off_o = o;
-  o = up(o + parts * 8 * L.nt * p.cache.d_v * sizeof(float));
+  o = up(o + parts * L.job_rows * p.cache.d_v * sizeof(float));
   L.off_long = o;
   L.total = o + L.lng.total;
   return L;
@@ -953,7 +967,7 @@ static int run(const attn_kv_fwd_params* p, void* ws, size_t ws_bytes, cudaStrea
   a.right = p->mask == ATTN_MASK_WINDOW ? p->window_right : -1;
   a.scale_log2 = p->softmax_scale * 1.4426950408889634f;
   a.nsplit = L.nsplit;
-  a.split_tiles = L.split_tiles;
+  a.min_tiles = L.min_tiles;
   a.cluster = L.cluster;
   a.mtiles = L.mtiles;
   a.long_from = L.lng.from;

@@ -189,8 +189,10 @@ static int launch(const attn_kv_fwd_params& p, const KvCacheView& c, const Strid
   f.d_qk = p.cache.d_qk;
   f.d_v = p.cache.d_v;
   f.mask = p.mask;
-  f.window_left = p.window_left;
-  f.window_right = p.window_right;
+  // a bound that no key is beyond is none (and keeps the forward's sums in 32 bits)
+  const long long far = (long long)p.max_seqlen_q + max_k;
+  f.window_left = p.window_left >= far ? -1 : p.window_left;
+  f.window_right = p.window_right >= far ? -1 : p.window_right;
   f.softmax_scale = p.softmax_scale;
   f.q = p.q;
   f.k = k16;
