@@ -56,16 +56,18 @@ constexpr int META_TILES = 256;     // tiles whose pages are held in shared memo
 // * Few jobs: splits for one wave of two CTAs per SM (one request of 131,072
 //   tokens, 8 kv heads: 50.5 us with 304 CTAs, 55.3 with 152, 56.3 with 608: more
 //   parts to join and an uneven second wave).
-// * Many jobs: splits short enough to even out ragged lengths (64 requests of up to
-//   8,192 tokens: 108.4 us at 64 tiles, 114.2 at 256, 114.0 at 32), as long as the
-//   grid stays within MAX_GRID: CTAs without work cost about 2 ns each.
+// * Many jobs: at most MAX_GRID CTAs, which still evens out ragged lengths (64
+//   requests of up to 8,192 tokens: 110.2 us, with 4,608 CTAs 108.9, with one or two
+//   splits 114); the CTAs without work behind a loose bound cost little (64
+//   requests of up to 1,000 tokens: 22.4 us under a bound of 1,000, 28.6 under one of
+//   131,072; with 4,608 CTAs 34.7).
 // * None so short that its prologue outweighs it (4 requests of 1,000 tokens: 8.5
 //   us at 12 tiles, 8.8 at 8, 8.9 at 16).
 // A list of (job, split) items made on the device by a kernel before this one, and
-// taken by persistent CTAs, was slower throughout (65 us and 119 us in the first two
+// taken by persistent CTAs, was slower throughout (65 us, 119 us and 32 us in these
 // cases): it puts two more trips to memory in front of the first load.
 constexpr int WAVE = 304;
-constexpr int MAX_GRID = 4608;
+constexpr int MAX_GRID = 2560;
 constexpr int EVEN_TILES = 64;
 constexpr int MIN_TILES = 12;
 // Up to eight splits of a grid of one wave are joined as clusters: no second
@@ -268,7 +270,20 @@ template <> __device__ __forceinline__ uint32_t pack_t2<__nv_bfloat16>(float a, 
 }
 template <> __device__ __forceinline__ uint32_t pack_t2<__half>(float a, float b) { return pack_h2(a, b); }
 
-// Four columns of a finished row: O / l, and with the first ones the LSE.
+// Two columns of a finished row: O / l, and with the first ones the LSE.
+template <typename T>
+__device__ __forceinline__ void store_pair(const Args& A, const Job& J, int hk, int row, int c, float x, float y, float top,
+                                           float l) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int tk = (J.row0 + row) / A.g, h = hk * A.g + J.row0 + row - tk * A.g;
+  T* dst = static_cast<T*>(A.o) + elem_off(A.so, (long long)J.q0 + tk, h) + c;
+  *reinterpret_cast<uint32_t*>(dst) = pack_t2<T>(x * inv, y * inv);
+  if (c == 0)
+    A.lse[(long long)h * A.total_q + J.q0 + tk] =
+        l == 0.f ? -INFINITY : (top - P_LOG2 + log2f(l)) * 0.6931471805599453f;
+}
+
+// Four of them.
 template <typename T>
 __device__ __forceinline__ void store_row(const Args& A, const Job& J, int hk, int row, int c, const float4& v, float top,
                                           float l) {
@@ -726,8 +741,60 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
     A.status[b * A.nsplit + split] = *s_bad == 2 ? ATTN_ERR_TIMEOUT : J.bad ? ATTN_ERR_BAD_SEQLENS : *s_bad ? ATTN_ERR_BAD_PAGE : ATTN_OK;
 }
 
-// Joins the splits of a row in a fixed order: O = sum 2^(m_s - m) O_s / sum
-// 2^(m_s - m) l_s.  A CTA takes one row; DV / 4 threads cover its columns, and
+// The joins: O = sum 2^(m_s - m) O_s / sum 2^(m_s - m) l_s over a row's splits, in
+// a fixed order.  A split that saw no key of the row holds zeros (or NaN, which
+// stays).
+//
+// Many rows of few splits: a warp takes a row, DV / 32 columns to a lane.  Rows
+// with nothing to join cost their lengths' loads (512 jobs of 4 rows: 2 us less
+// than a CTA to each row).
+template <int DV, int NT, typename T>
+__global__ void __launch_bounds__(NTHREADS) join_rows_kernel(const Args A, long long rows) {
+  constexpr int ROWS = 8 * NT, PER = DV / 32 >= 4 ? 4 : 2, REPS = DV / 32 / PER;   // columns in runs of PER
+  const int lane = threadIdx.x & 31;
+  long long x = (long long)blockIdx.x * NWARPS + (threadIdx.x >> 5);
+  if (x >= rows) return;
+  const int row = (int)(x % A.job_rows);
+  const long long job = x / A.job_rows;
+  const int m = (int)(job % A.mtiles), bh = (int)(job / A.mtiles), hk = bh % A.c.hkv, b = bh / A.c.hkv;
+  MaskArgs mk;
+  const Job J = make_job<ROWS>(A, b, m, mk);
+  const int n = cdiv(J.ntile, split_tiles(A, J));
+  if (row >= J.nrow || n <= 1) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // launched early: the splits' kernel ends here
+  const float2* ml = A.part_ml + job * A.nsplit * A.job_rows + row;
+  const float* po = A.part_o + (job * A.nsplit * A.job_rows + row) * DV + lane * PER;
+  float top = -INFINITY;
+  for (int s = lane; s < n; s += 32) top = fmaxf(top, ml[s * A.job_rows].x);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  float l = 0.f, v[REPS][PER];
+#pragma unroll
+  for (int r = 0; r < REPS; ++r)
+#pragma unroll
+    for (int k = 0; k < PER; ++k) v[r][k] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) {
+    const float2 y = ml[s * A.job_rows];
+    const float w = y.x == -INFINITY ? 1.f : fast_exp2(y.x - top);
+    l += w * y.y;
+    const float* src = po + (long long)s * A.job_rows * DV;
+#pragma unroll
+    for (int r = 0; r < REPS; ++r)
+#pragma unroll
+      for (int k = 0; k < PER; k += 2) {
+        const float2 z = *reinterpret_cast<const float2*>(src + r * 32 * PER + k);
+        v[r][k] += w * z.x;
+        v[r][k + 1] += w * z.y;
+      }
+  }
+#pragma unroll
+  for (int r = 0; r < REPS; ++r)
+#pragma unroll
+    for (int k = 0; k < PER; k += 2) store_pair<T>(A, J, hk, row, r * 32 * PER + lane * PER + k, v[r][k], v[r][k + 1], top, l);
+}
+
+// Few rows of many splits: a CTA takes a row; DV / 4 threads cover its columns, and
 // the thread groups take the splits in turn: blockDim.x follows their number.
 constexpr int JOIN_THREADS = 512;   // at most
 
@@ -904,14 +971,21 @@ static int launch(const Args& a, long long jobs, cudaStream_t st) {
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(jobs * a.job_rows));
-    int threads = NTHREADS;   // about four splits to a thread group
-    while (threads < JOIN_THREADS && threads / (DV / 4) * 4 < a.nsplit) threads *= 2;
-    cfg.blockDim = dim3(threads);
     cfg.stream = st;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, join_kernel<DV, NT, T>, a) != cudaSuccess) return ATTN_ERR_CUDA;
+    const long long rows = jobs * a.job_rows;
+    if (jobs >= WAVE) {
+      cfg.gridDim = dim3((unsigned)cdiv_ll(rows, NWARPS));
+      cfg.blockDim = dim3(NTHREADS);
+      if (cudaLaunchKernelEx(&cfg, join_rows_kernel<DV, NT, T>, a, rows) != cudaSuccess) return ATTN_ERR_CUDA;
+    } else {
+      int threads = NTHREADS;   // about four splits to a thread group
+      while (threads < JOIN_THREADS && threads / (DV / 4) * 4 < a.nsplit) threads *= 2;
+      cfg.gridDim = dim3((unsigned)rows);
+      cfg.blockDim = dim3(threads);
+      if (cudaLaunchKernelEx(&cfg, join_kernel<DV, NT, T>, a) != cudaSuccess) return ATTN_ERR_CUDA;
+    }
   }
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
