@@ -53,9 +53,11 @@ constexpr int META_TILES = 256;     // tiles whose pages are held in shared memo
 // Splits.  A job is one row tile of one request and kv head.  The host sets how
 // many splits a job has at most, the device how long they are, from the request's
 // own length, so that max_seqlen_k need not be tight.
-// * Few jobs: splits for one wave of two CTAs per SM (one request of 131,072
-//   tokens, 8 kv heads: 50.5 us with 304 CTAs, 55.3 with 152, 56.3 with 608: more
-//   parts to join and an uneven second wave).
+// * Few jobs: splits for one wave.  Of one request, all equal: two CTAs per SM
+//   (131,072 tokens, 8 kv heads: 50.5 us with 304 CTAs, 55.3 with 152, 56.3 with
+//   608: more parts to join).  Of several, whose lengths differ: four per SM (4
+//   requests of up to 16,384 tokens: 22.2 us with 608 CTAs, 29.6 with 304, 25.9 with
+//   912; 32 of up to 4,096: 40.7, 53.5 and 43.6 us).
 // * Many jobs: at most MAX_GRID CTAs, which still evens out ragged lengths (64
 //   requests of up to 8,192 tokens: 110.2 us, with 4,608 CTAs 108.9, with one or two
 //   splits 114); the CTAs without work behind a loose bound cost little (64
@@ -66,11 +68,12 @@ constexpr int META_TILES = 256;     // tiles whose pages are held in shared memo
 // A list of (job, split) items made on the device by a kernel before this one, and
 // taken by persistent CTAs, was slower throughout (65 us, 119 us and 32 us in these
 // cases): it puts two more trips to memory in front of the first load.
-constexpr int WAVE = 304;
+constexpr int HALF_WAVE = 304;
+constexpr int WAVE = 608;
 constexpr int MAX_GRID = 2560;
 constexpr int EVEN_TILES = 64;
 constexpr int MIN_TILES = 12;
-// Up to eight splits of a grid of one wave are joined as clusters: no second
+// Up to eight splits in a grid of one wave are joined as clusters: no second
 // launch, 8.5 us against 9.2 in that last case.  Not in larger grids, where the
 // CTAs of a cluster hold their SMs for its slowest (158 us against 108 for the 64
 // requests).
@@ -753,15 +756,18 @@ __global__ void __launch_bounds__(NTHREADS) join_rows_kernel(const Args A, long 
   constexpr int ROWS = 8 * NT, PER = DV / 32 >= 4 ? 4 : 2, REPS = DV / 32 / PER;   // columns in runs of PER
   const int lane = threadIdx.x & 31;
   long long x = (long long)blockIdx.x * NWARPS + (threadIdx.x >> 5);
-  if (x >= rows) return;
+  const bool some = x < rows;
+  if (!some) x = 0;
   const int row = (int)(x % A.job_rows);
   const long long job = x / A.job_rows;
   const int m = (int)(job % A.mtiles), bh = (int)(job / A.mtiles), hk = bh % A.c.hkv, b = bh / A.c.hkv;
   MaskArgs mk;
   const Job J = make_job<ROWS>(A, b, m, mk);
   const int n = cdiv(J.ntile, split_tiles(A, J));
-  if (row >= J.nrow || n <= 1) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // launched early: the splits' kernel ends here
+  // launched early: the splits' kernel ends here.  Every thread waits, also where
+  // nothing is to join: what follows on the stream waits for this kernel alone.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!some || row >= J.nrow || n <= 1) return;
   const float2* ml = A.part_ml + job * A.nsplit * A.job_rows + row;
   const float* po = A.part_o + (job * A.nsplit * A.job_rows + row) * DV + lane * PER;
   float top = -INFINITY;
@@ -812,8 +818,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Args A) {
   MaskArgs mk;
   const Job J = make_job<ROWS>(A, b, m, mk);
   const int n = cdiv(J.ntile, split_tiles(A, J));
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // all threads: see join_rows_kernel
   if (row >= J.nrow || n <= 1) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // launched early: the splits' kernel ends here
   const float2* ml = A.part_ml + (long long)job * A.nsplit * A.job_rows + row;
   const float* po = A.part_o + ((long long)job * A.nsplit * A.job_rows + row) * DV + c;
   float top = -INFINITY;
@@ -874,9 +880,9 @@ static Layout layout(const attn_kv_fwd_params& p) {
   L.job_rows = (int)(rows < 8 * L.nt ? rows : 8 * L.nt);
   L.jobs = (long long)p.batch * p.cache.nhead_kv * L.mtiles;
   const int tiles = max_keys(p) / TILE + 2;
-  const bool few = L.jobs < WAVE;
+  const bool few = L.jobs < HALF_WAVE;
   L.min_tiles = few ? MIN_TILES : EVEN_TILES;
-  const long long n = few ? WAVE / L.jobs : cdiv_ll(MAX_GRID, L.jobs);
+  const long long n = few ? (p.batch > 1 ? WAVE : HALF_WAVE) / L.jobs : cdiv_ll(MAX_GRID, L.jobs);
   L.nsplit = n < cdiv(tiles, L.min_tiles) ? (int)n : cdiv(tiles, L.min_tiles);
   L.cluster = few && L.nsplit > 1 && L.nsplit <= MAX_CLUSTER;
   auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
@@ -975,7 +981,7 @@ static int launch(const Args& a, long long jobs, cudaStream_t st) {
     cfg.attrs = &early;
     cfg.numAttrs = 1;
     const long long rows = jobs * a.job_rows;
-    if (jobs >= WAVE) {
+    if (jobs >= HALF_WAVE) {
       cfg.gridDim = dim3((unsigned)cdiv_ll(rows, NWARPS));
       cfg.blockDim = dim3(NTHREADS);
       if (cudaLaunchKernelEx(&cfg, join_rows_kernel<DV, NT, T>, a, rows) != cudaSuccess) return ATTN_ERR_CUDA;

@@ -141,6 +141,19 @@ def test_plan_refused_step_changes_nothing(B, what, status):
     assert p.cu_seqlens.tolist() == [0, 0, 0, 0] and p.slots.tolist() == [-1] * cap
 
 
+def test_plan_refused_step_with_many_tokens(B):
+    """The slots of many tokens are written by a kernel of their own: it sees the
+    refusal too."""
+    cap = 9000
+    td, fd = dev([[0, -1], [-1, -1]]), dev([1, 2, 3, 0])
+    for new, status in (([1, 33], -7), ([1, 0], 0)):
+        p = B.kv_plan(dev(new), dev([3, 0]), td, fd, dev([3]), page_size=16, max_tokens=cap)
+        assert int(p.status) == status
+        n = 0 if status else 1
+        assert p.slots[:n].tolist() == [3] * n and bool((p.slots[n:] == -1).all())
+        assert bool((p.positions[n:] == 0).all()) and p.cu_seqlens.tolist() == [0, n, n]
+
+
 # -------------------------------------------------------------------- append
 
 def runs(spec, page):
@@ -489,6 +502,122 @@ def test_attend_repeats_and_streams(B):
     graph.replay()
     ref = kv_ref.attend(q, cu, [100, 900, 0], table, kc, vc, ke, ve, 0.1, 2)
     check_attend(*out, ref, torch.bfloat16, 128, 900)
+
+
+def test_offsets_past_32_bits(B):
+    """A cache whose pages lie 2 GiB apart: append and attention address it with
+    64 bits, keys and values past the 4 GiB mark."""
+    page, heads, d, pages, gap = 16, 2, 64, 4, 1 << 31
+    raw = torch.empty(pages * gap, dtype=torch.uint8, device="cuda")
+    k, v = (raw.as_strided((pages, page, heads, d), (gap, heads * d, d, 1), off) for off in (0, 1 << 20))
+    for x in (k, v):
+        x.zero_()
+    ke, ve = (torch.full((pages, heads), 127, dtype=torch.uint8, device="cuda") for _ in range(2))
+    f8 = torch.float8_e4m3fn
+    c = B.KvCache(k.view(f8), v.view(f8), ke, ve)
+    g = torch.Generator().manual_seed(2)
+    order, n = [3, 1, 2, 0], 60
+    kn, vn = (torch.randn((n, heads, d), generator=g).to(torch.bfloat16) for _ in range(2))
+    slots = [order[t // page] * page + t % page for t in range(n)]
+    B.kv_append(kn.cuda(), vn.cuda(), dev(slots, torch.int64), c)
+    kc, vc = (torch.zeros((pages, page, heads, d), dtype=torch.uint8) for _ in range(2))
+    ker, ver = (torch.full((pages, heads), 127, dtype=torch.uint8) for _ in range(2))
+    kv_ref.append(kc, ker, kn, slots)
+    kv_ref.append(vc, ver, vn, slots)
+    assert torch.equal(k.cpu(), kc) and torch.equal(v.cpu(), vc) and torch.equal(ke.cpu(), ker)
+    for new in (1, 60):
+        q = torch.randn((new, 4, d), generator=g).to(torch.bfloat16)
+        o, lse = B.attn_kv_forward(q.cuda(), c, dev([order]), dev([n]), dev([0, new]), scale=0.125, max_seqlen_q=new,
+                                   max_seqlen_k=64, check_status=True)
+        check_attend(o, lse, kv_ref.attend(q, [0, new], [n], [order], kc, vc, ker, ver, 0.125, 2), torch.bfloat16, d, n,
+                     weights(torch.bfloat16, new))
+
+
+@pytest.mark.parametrize("heads,group,longest", [(2, 4, 1500), (1, 1, 41000)])
+def test_attend_many_requests_one_long(B, heads, group, longest):
+    """Over 304 jobs: few splits each, most requests with one, a long one with all
+    of them (at 41,000 tokens each of its splits goes through its pages twice)."""
+    g = torch.Generator().manual_seed(longest)
+    batch, page, d = 320, 16, 64
+    lens = torch.randint(0, 40, (batch,), generator=g).tolist()
+    lens[200] = longest
+    new = [1] * batch
+    q, table, kc, vc, ke, ve, cu = attend_case(d, d, torch.float16, page, lens, new, heads, group)
+    o, lse = B.attn_kv_forward(q.cuda(), handle(B, kc, vc, ke, ve), dev(table), dev(lens), dev(cu), scale=0.125,
+                               max_seqlen_q=1, max_seqlen_k=longest, check_status=True)
+    check_attend(o, lse, kv_ref.attend(q, cu, lens, table, kc, vc, ke, ve, 0.125, 2), torch.float16, d, longest)
+
+
+def test_attend_nothing_to_do(B):
+    """No query rows; requests without tokens; a bound of zero."""
+    q, table, kc, vc, ke, ve, cu = attend_case(64, 64, torch.bfloat16, 16, [5, 9], [1, 1], 1, 2)
+    c = handle(B, kc, vc, ke, ve)
+    o, lse = B.attn_kv_forward(q[:0].cuda(), c, dev(table), dev([5, 9]), dev([0, 0, 0]), scale=0.1, max_seqlen_q=1,
+                               max_seqlen_k=16, check_status=True)
+    assert o.shape == (0, 2, 64) and lse.shape == (2, 0)
+    o, lse = B.attn_kv_forward(q.cuda(), c, dev(table), dev([0, 0]), dev(cu), scale=0.1, max_seqlen_q=1, max_seqlen_k=0,
+                               check_status=True)
+    assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+    B.kv_append(torch.empty((0, 1, 64), dtype=torch.bfloat16, device="cuda"),
+                torch.empty((0, 1, 64), dtype=torch.bfloat16, device="cuda"),
+                torch.empty((0,), dtype=torch.int64, device="cuda"), c)
+    assert torch.equal(c.k.view(torch.uint8).cpu(), kc)
+
+
+def test_attend_long_rows_the_fast_forward_does_not_take(B):
+    """Segments of hundreds of tokens with a negative scale: tiles of 16 rows."""
+    lens, new = [260, 150], [200, 150]
+    q, table, kc, vc, ke, ve, cu = attend_case(128, 128, torch.float16, 32, lens, new, 2, 2)
+    o, lse = B.attn_kv_forward(q.cuda(), handle(B, kc, vc, ke, ve), dev(table), dev(lens), dev(cu), scale=-0.1,
+                               max_seqlen_q=200, max_seqlen_k=260, check_status=True)
+    check_attend(o, lse, kv_ref.attend(q, cu, lens, table, kc, vc, ke, ve, -0.1, 2), torch.float16, 128, 260)
+
+
+def test_attend_window_bounds_far_out(B):
+    """Window bounds near 2^31 see everything, in both paths."""
+    lens, new = [90, 300], [1, 150]
+    q, table, kc, vc, ke, ve, cu = attend_case(64, 64, torch.bfloat16, 16, lens, new, 1, 2)
+    far = 2 ** 31 - 1
+    o, lse = B.attn_kv_forward(q.cuda(), handle(B, kc, vc, ke, ve), dev(table), dev(lens), dev(cu), scale=0.1, mask=3,
+                               left=far, right=far, max_seqlen_q=150, max_seqlen_k=300, check_status=True)
+    ref = kv_ref.attend(q, cu, lens, table, kc, vc, ke, ve, 0.1, 0)
+    check_attend(o, lse, ref, torch.bfloat16, 64, 300, torch.bfloat16)
+
+
+def test_what_the_binding_refuses(B):
+    q, table, kc, vc, ke, ve, cu = attend_case(64, 64, torch.bfloat16, 16, [5, 9], [1, 1], 1, 2)
+    c, qd, td, ld, cud = handle(B, kc, vc, ke, ve), q.cuda(), dev(table), dev([5, 9]), dev(cu)
+    kw = dict(scale=0.1, max_seqlen_q=1, max_seqlen_k=16)
+    bad = [(q, c, td, ld, cud), (qd.float(), c, td, ld, cud), (qd[..., :32], c, td, ld, cud),
+           (qd, c, td.long(), ld, cud), (qd, c, td.T, ld, cud), (qd, c, td, ld.long(), cud), (qd, c, td, ld, cud[:2]),
+           (qd, c, td, ld, dev([[0, 1, 2]])), (qd, c, td, ld.cpu(), cud), (qd.transpose(1, 2), c, td, ld, cud)]
+    for args in bad:
+        with pytest.raises(ValueError):
+            B.attn_kv_forward(*args, **kw)
+    with pytest.raises(ValueError):
+        B.attn_kv_forward(qd, c, td, ld, cud, workspace=torch.empty(10, device="cuda"), **kw)
+    with pytest.raises(B.AttnError):
+        B.attn_kv_forward(qd, c, td, ld, cud, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"), **kw)
+    k = torch.zeros((2, 1, 64), dtype=torch.bfloat16, device="cuda")
+    sl = dev([0, 1], torch.int64)
+    for args in ((k, k, sl.int(), c), (k, k[:1], sl, c), (k.half(), k, sl, c), (k.float(), k.float(), sl, c),
+                 (k, k.cpu(), sl, c), (k, k, sl[:1], c)):
+        with pytest.raises(ValueError):
+            B.kv_append(*args)
+    one = dev([1, 1])
+    plan = dict(page_size=16, max_tokens=4)
+    for args in ((one, ld.long(), td, dev([0, 1]), dev([0])), (one, ld[:1], td, dev([0, 1]), dev([0])),
+                 (one, ld, td.T, dev([0, 1]), dev([0])), (one, ld, td, dev([0, 1]), dev([0, 0])),
+                 (one, ld, td, dev([0, 1]).cpu(), dev([0]))):
+        with pytest.raises(ValueError):
+            B.kv_plan(*args, **plan)
+    f = B.rope_frequencies(64)
+    pos = dev([1, 2])
+    for args in ((qd, None, pos.long(), f), (qd, None, pos[:1], f), (qd, None, pos.cpu(), f), (qd, None, pos, f.float()),
+                 (qd, None, pos, f.cuda()), (qd, qd[..., :32], pos, f), (qd, qd.half(), pos, f),
+                 (qd.transpose(1, 2), None, pos, f), (qd[0], None, pos, f)):
+        with pytest.raises((ValueError, B.AttnError)):
+            B.rope(*args)
 
 
 # ------------------------------------------------------- the step they make up

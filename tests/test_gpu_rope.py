@@ -95,6 +95,25 @@ def test_layouts(B, dtype, layout):
         check(got, x, ref)
 
 
+def test_many_rows_in_batches(B):
+    """Enough rows for eight to a CTA, heads outside the rows, a ragged last CTA,
+    negative and zero frequencies."""
+    b, s, hq, hkv, d = 3, 701, 3, 1, 64
+    g = torch.Generator().manual_seed(8)
+    q, k = torch.randn((b, s, hq, d), generator=g), torch.randn((b, s, hkv, d), generator=g)
+    f = B.rope_frequencies(d)
+    f[3], f[5] = -0.37, 0.0
+    for dtype in (torch.bfloat16, torch.float32):
+        pos = torch.randint(0, 9000, (2, b, s), generator=g, dtype=torch.int32)
+        axis = (torch.arange(d // 2) % 2).to(torch.uint8)
+        qq, kk = q.to(dtype), k.to(dtype)
+        qd = qq.cuda().transpose(1, 2).contiguous().transpose(1, 2)
+        qo, ko = B.rope(qd, kk.cuda(), pos.cuda(), f, pair_axis=axis)
+        flat = pos.reshape(2, -1)
+        for x, got in ((qq, qo), (kk, ko)):
+            check(got, x, kv_ref.rope(x.reshape(b * s, -1, d), flat, f, axis).view(x.shape))
+
+
 def test_copied_columns_keep_their_bits(B):
     """Columns past rot_dim: NaN payloads, infinities and negative zero come through."""
     x = torch.tensor([0x7fc1, 0xff80, 0x8000, 0x7f80, 1, 0xffff, 0, 0x3f80] * 8, dtype=torch.int32).to(torch.int16)
