@@ -9,9 +9,9 @@ not been built: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
-import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -451,92 +451,39 @@ def attn_backward(q, k, v, o, do, lse, *, scale, mask=MASK_NONE, left=-1, right=
 # ------------------------------------------- rotary positions and the cache
 #
 # These run once per layer or step of a serving loop, often for a few
-# microseconds of device time, so the marshalling is kept short: each tensor's
-# attributes are read once, the whole argument struct is packed in one go (the
-# layouts below are those of the ctypes mirrors above), and what is wrong is
-# only worked out once something is.
+# microseconds of device time.  Their marshalling (checks of types, shapes,
+# strides and devices, outputs, the struct, the call on the current stream) is
+# compiled: csrc/marshal.cpp.  What is refused before a launch raises ValueError
+# (tensors) or AttnError (the library's status).
 
-_F16 = (torch.bfloat16, torch.float16)
-_FLOATS = tuple(_DTYPES)
-_BYTES = (torch.float8_e4m3fn, torch.uint8)
-_I32, _I64 = torch.int32, torch.int64
-_current_device = torch._C._cuda_getDevice
-_current_raw_stream = torch._C._cuda_getCurrentRawStream
-
-_ROPE = struct.Struct("<10i Q 3q 2Q 4Q 12q")
-_CACHE = struct.Struct("<6i 4Q 6q")
-_PLAN = struct.Struct("<6i 4Q q 7Q")
-_APPEND = struct.Struct("<2i 2Q 6q Q")
-_FWD = struct.Struct("<10i f i 4Q q 3Q 6q")
-for _s, _c, _tail in ((_ROPE, AttnRopeParams, 0), (_CACHE, AttnKvCache, 0), (_PLAN, AttnKvPlanParams, 0),
-                      (_APPEND, AttnKvAppendParams, 1), (_FWD, AttnKvFwdParams, 1)):
-    assert _s.size + (_tail and _CACHE.size) == ctypes.sizeof(_c), _c
+_marshal = None
 
 
-def _entry(name: str, nargs: int):
-    """The library's function `name` for packed structs (bytes)."""
-    global _entries
-    f = load()[name]
-    f.argtypes = [_vp] * nargs
-    f.restype = ctypes.c_int
-    _entries[name] = f
-    return f
+def _load_marshal():
+    """The compiled marshalling, bound to the library that load() holds."""
+    global _marshal
+    if _marshal is None:
+        lib = load()
+        path = os.path.join(_PKG, "_marshal.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it first (head_attention_backward_gb300.build.build_marshal)")
+        spec = importlib.util.spec_from_file_location("_marshal", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.bind(*(ctypes.cast(getattr(lib, n), _vp).value for n in (
+            "attn_rope", "attn_kv_plan", "attn_kv_append", "attn_kv_fwd_workspace_size", "attn_kv_fwd",
+            "attn_kv_fwd_read_status")))
+        _marshal = m
+    return _marshal
 
 
-_entries = {}
-
-
-def _check(t: torch.Tensor, what: str, dtypes, shape=None, device=None):
-    """Raises ValueError if t is not of these types, shape and device."""
-    if t.dtype not in dtypes:
-        raise ValueError(f"{what}: dtype {t.dtype} is not one of {tuple(dtypes)}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_cuda or (device is not None and t.get_device() != device):
-        raise ValueError(f"{what} must be on cuda:{device if device is not None else '?'}, not on {t.device}")
-
-
-def _vector(t: torch.Tensor, what: str, n: int, index: int, dtype=_I32) -> int:
-    """Address of a contiguous vector of n whole numbers on device `index`."""
-    if t.dtype is not dtype or t.get_device() != index or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{what} must be a contiguous {dtype} vector of {n} on cuda:{index}; "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _rows3(t: torch.Tensor, what: str):
-    """{0, row, head} strides of a [T, H, D] tensor; a dimension of one entry
-    may carry any stride, so it is given the contiguous one."""
-    row, head, one = t.stride()
-    n, h, d = t.shape
-    if one != 1 and d > 1:
-        raise ValueError(f"{what}: the head dimension must be contiguous (stride 1)")
-    if h == 1:
-        head = d
-    return 0, (row if n > 1 else h * head), head
-
-
-def _on(index: int, stream):
-    """(raw stream, context for allocations) of a call on device `index`.  With
-    an explicit stream the outputs are allocated on it, so that the allocator
-    does not hand their memory to other work while the kernels may still write
-    it."""
-    if index != _current_device():
-        raise ValueError(f"tensors on device {index}, but the current device is {_current_device()}")
-    raw = _current_raw_stream(index)
-    if stream is None:
-        return raw, None
-    want = _stream(stream)
-    if want == raw:
-        return raw, None
-    return want, torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(want))
-
-
-def _empty(shape, dtype, device, ctx):
-    if ctx is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with ctx:
-        return torch.empty(shape, dtype=dtype, device=device)
+def _on_stream(stream):
+    """Context in which `stream` (a torch stream or a raw handle) is current:
+    outputs are then allocated on it, so that the allocator does not hand their
+    memory to other work while the kernels may still write it."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0) -> torch.Tensor:
@@ -554,73 +501,14 @@ def rope(q, k, positions, inv_freq, *, pair_axis=None, interleaved=False, invers
     axes; inv_freq and pair_axis are host tensors (float64 and uint8,
     rot_dim / 2 entries).  inverse=True is the gradient: rope(dq, dk, ...,
     inverse=True) after attn_backward."""
-    dtype, index, qs = q.dtype, q.get_device(), q.shape
-    code, packed = _DTYPES.get(dtype), len(qs) == 3
-    if code is None or index < 0 or not (packed or len(qs) == 4):
-        _check(q, "q", _FLOATS)
-        raise ValueError("q must be [T, H, D] or [B, S, H, D]")
-    if packed:
-        batch, (seqlen, heads, dim) = 1, qs
-    else:
-        batch, seqlen, heads, dim = qs
-    if (inv_freq.dtype is not torch.float64 or inv_freq.get_device() >= 0 or inv_freq.dim() != 1
-            or not inv_freq.is_contiguous()):
-        raise ValueError("inv_freq must be a contiguous float64 vector on the host")
-    half = inv_freq.shape[0]
-    axis_ptr = 0
-    if pair_axis is not None:
-        if (pair_axis.dtype is not torch.uint8 or pair_axis.get_device() >= 0 or pair_axis.shape != (half,)
-                or not pair_axis.is_contiguous()):
-            raise ValueError("pair_axis must be a contiguous uint8 vector on the host, as long as inv_freq")
-        axis_ptr = pair_axis.data_ptr()
-    # strides {axis, batch entry, row}
-    ps, sp = positions.shape, positions.stride()
-    n_axes = 1
-    if ps == qs[:-2]:
-        sp = (0, 0, *sp) if packed else (0, *sp)
-    elif ps[1:] == qs[:-2]:
-        n_axes = ps[0]
-        if packed:
-            sp = (sp[0], 0, sp[1])
-    else:
-        raise ValueError(f"positions {tuple(ps)} do not fit rows {tuple(qs[:-2])}")
-    if positions.dtype is not _I32 or positions.get_device() != index:
-        _check(positions, "positions", (_I32,), None, index)
-    raw, ctx = _on(index, stream)
-    if out is not None:
-        qo, ko = out
-        _check(qo, "out[0]", (dtype,), qs, index)
-        if k is not None:
-            _check(ko, "out[1]", (dtype,), k.shape, index)
-    elif ctx is None:
-        qo, ko = torch.empty_like(q), None if k is None else torch.empty_like(k)
-    else:
-        with ctx:
-            qo, ko = torch.empty_like(q), None if k is None else torch.empty_like(k)
-    sq, so = q.stride(), qo.stride()
-    if sq[-1] != 1 or so[-1] != 1:
-        raise ValueError("the head dimension must be contiguous (stride 1)")
-    nk, kp, kop, sk, sko = 0, 0, 0, (0, 0, 0, 1), (0, 0, 0, 1)
-    if k is not None:
-        ks = k.shape
-        nk = ks[-2]
-        if k.dtype is not dtype or k.get_device() != index or ks[-1] != dim or ks[:-2] != qs[:-2]:
-            _check(k, "k", (dtype,), (*qs[:-2], nk, dim), index)
-        kp, kop, sk, sko = k.data_ptr(), ko.data_ptr(), k.stride(), ko.stride()
-        if sk[-1] != 1 or sko[-1] != 1:
-            raise ValueError("the head dimension must be contiguous (stride 1)")
-        if packed:
-            sk, sko = (0, *sk), (0, *sko)
-    if packed:
-        sq, so = (0, *sq), (0, *so)
-    p = _ROPE.pack(code, batch, seqlen, heads, nk, dim, 2 * half, n_axes, 1 if interleaved else 0,
-                   1 if inverse else 0, positions.data_ptr(), *sp, inv_freq.data_ptr(), axis_ptr, q.data_ptr(), kp,
-                   qo.data_ptr(), kop, sq[0], sq[1], sq[2], sk[0], sk[1], sk[2], so[0], so[1], so[2], sko[0], sko[1],
-                   sko[2])
-    st = (_entries.get("attn_rope") or _entry("attn_rope", 2))(p, raw)
+    if stream is not None:
+        with _on_stream(stream):
+            return rope(q, k, positions, inv_freq, pair_axis=pair_axis, interleaved=interleaved, inverse=inverse, out=out)
+    qo, ko = (None, None) if out is None else out
+    st, qo, ko = (_marshal or _load_marshal()).rope(q, k, positions, inv_freq, pair_axis, interleaved, inverse, qo, ko)
     if st != 0:
         raise AttnError(st, "attn_rope")
-    return qo, (None if k is None else ko)
+    return qo, ko
 
 
 class KvCache:
@@ -633,24 +521,9 @@ class KvCache:
     __slots__ = ("k", "v", "k_exp", "v_exp", "num_pages", "page_size", "nhead_kv", "d_qk", "d_v", "index", "packed")
 
     def __init__(self, k, v, k_exp, v_exp):
-        index, ks, vs = k.get_device(), k.shape, v.shape
-        pages, size, heads, dqk = ks
-        dv = vs[3]
-        sk, sv = k.stride(), v.stride()
-        if (index < 0 or k.dtype not in _BYTES or v.dtype is not k.dtype or vs != (pages, size, heads, dv)
-                or v.get_device() != index or sk[3] != 1 or sv[3] != 1):
-            _check(k, "k", _BYTES)
-            _check(v, "v", (k.dtype,), (pages, size, heads, dv), index)
-            raise ValueError("the head dimension must be contiguous (stride 1)")
-        es = (pages, heads)
-        for name, e in (("k_exp", k_exp), ("v_exp", v_exp)):
-            if e.dtype is not torch.uint8 or e.get_device() != index or e.shape != es or not e.is_contiguous():
-                _check(e, name, (torch.uint8,), es, index)
-                raise ValueError(f"{name} must be contiguous")
+        (self.packed, self.index, self.num_pages, self.page_size, self.nhead_kv, self.d_qk,
+         self.d_v) = (_marshal or _load_marshal()).cache(k, v, k_exp, v_exp)
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
-        self.num_pages, self.page_size, self.nhead_kv, self.d_qk, self.d_v, self.index = pages, size, heads, dqk, dv, index
-        self.packed = _CACHE.pack(pages, size, heads, dqk, dv, 0, k.data_ptr(), v.data_ptr(), k_exp.data_ptr(),
-                                  v_exp.data_ptr(), sk[0], sk[1], sk[2], sv[0], sv[1], sv[2])
 
     @classmethod
     def empty(cls, num_pages, page_size, nhead_kv, d_qk, d_v, device="cuda"):
@@ -679,15 +552,6 @@ class KvPlan(NamedTuple):
             raise AttnError(s, "attn_kv_plan (device status)")
 
 
-def _table(t: torch.Tensor, n: int, index: int):
-    """(columns, row stride) of an int32 [n, columns] block table."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype is not _I32 or t.get_device() != index or len(shape) != 2 or shape[0] != n or stride[1] != 1:
-        _check(t, "block_table", (_I32,), (n, shape[-1]), index)
-        raise ValueError("block_table rows must be contiguous")
-    return shape[1], (stride[0] if n > 1 else shape[1])
-
-
 def kv_plan(new_lens, seqlens, block_table, free_pages, free_count, *, page_size, max_tokens, out=None, stream=None):
     """Pages, positions and slots for one step (attn_kv_plan).  new_lens and
     seqlens int32 [B] (KV_RELEASE ends a request), block_table int32
@@ -695,50 +559,30 @@ def kv_plan(new_lens, seqlens, block_table, free_pages, free_count, *, page_size
     free_count int32 [1].  Returns a KvPlan, `out` itself when given: its
     seqlens and free_count may be the inputs', so that a captured call
     advances its state at every replay."""
-    index, n = new_lens.get_device(), new_lens.shape[0]
-    pages = free_pages.shape[0]
-    cols, row = _table(block_table, n, index)
-    new_p, len_p = _vector(new_lens, "new_lens", n, index), _vector(seqlens, "seqlens", n, index)
-    free_p, count_p = _vector(free_pages, "free_pages", pages, index), _vector(free_count, "free_count", 1, index)
-    raw, ctx = _on(index, stream)
-    if out is None:
-        # two blocks for six vectors: the words, the slots
-        device = new_lens.device
-        words, slots = _empty((2 * n + 3 + max_tokens,), _I32, device, ctx), _empty((max_tokens,), _I64, device, ctx)
-        cu, lens, count, status, pos = words.split((n + 1, n, 1, 1, max_tokens))
-        out = KvPlan(cu, lens, pos, slots, count, status)
-        w = words.data_ptr()
-        cu_p, out_p, left_p, status_p, pos_p = w, w + 4 * (n + 1), w + 4 * (2 * n + 1), w + 4 * (2 * n + 2), w + 4 * (2 * n + 3)
-        slots_p = slots.data_ptr()
-    else:
-        cu_p, out_p = _vector(out.cu_seqlens, "out.cu_seqlens", n + 1, index), _vector(out.seqlens, "out.seqlens", n, index)
-        left_p, status_p = _vector(out.free_count, "out.free_count", 1, index), _vector(out.status, "out.status", 1, index)
-        pos_p = _vector(out.positions, "out.positions", max_tokens, index)
-        slots_p = _vector(out.slots, "out.slots", max_tokens, index, _I64)
-    p = _PLAN.pack(n, page_size, pages, cols, max_tokens, 0, new_p, len_p, out_p, block_table.data_ptr(), row, free_p,
-                   count_p, left_p, cu_p, pos_p, slots_p, status_p)
-    st = (_entries.get("attn_kv_plan") or _entry("attn_kv_plan", 2))(p, raw)
+    if stream is not None:
+        with _on_stream(stream):
+            return kv_plan(new_lens, seqlens, block_table, free_pages, free_count, page_size=page_size,
+                           max_tokens=max_tokens, out=out)
+    st, made = (_marshal or _load_marshal()).plan(new_lens, seqlens, block_table, free_pages, free_count, page_size,
+                                                  max_tokens, out)
     if st != 0:
         raise AttnError(st, "attn_kv_plan")
-    return out
+    return KvPlan(*made) if out is None else out
 
 
 def kv_append(k, v, slots, cache: KvCache, *, stream=None):
     """New keys and values into the cache (attn_kv_append): k [T, kv heads,
     d_qk] and v [T, kv heads, d_v] in bf16 or fp16, slots int64 [T] as from
     kv_plan (-1: skipped)."""
-    index, ks, dtype = cache.index, k.shape, k.dtype
-    n, heads = ks[0], cache.nhead_kv
-    if (dtype not in _F16 or v.dtype is not dtype or ks != (n, heads, cache.d_qk) or v.shape != (n, heads, cache.d_v)
-            or k.get_device() != index or v.get_device() != index):
-        _check(k, "k", _F16, (n, heads, cache.d_qk), index)
-        _check(v, "v", (dtype,), (n, heads, cache.d_v), index)
-    raw, _ = _on(index, stream)
-    p = _APPEND.pack(_DTYPES[dtype], n, k.data_ptr(), v.data_ptr(), *_rows3(k, "k"), *_rows3(v, "v"),
-                     _vector(slots, "slots", n, index, _I64)) + cache.packed
-    st = (_entries.get("attn_kv_append") or _entry("attn_kv_append", 2))(p, raw)
+    if stream is not None:
+        with _on_stream(stream):
+            return kv_append(k, v, slots, cache)
+    st = (_marshal or _load_marshal()).append(k, v, slots, cache.packed, cache.index)
     if st != 0:
         raise AttnError(st, "attn_kv_append")
+
+
+_FWD_STEPS = ("attn_kv_fwd_workspace_size", "attn_kv_fwd", "attn_kv_fwd_read_status", "attn_kv_fwd (device status)")
 
 
 def attn_kv_forward(q, cache: KvCache, block_table, seqlens_k, cu_seqlens_q, *, scale, mask=MASK_CAUSAL_BOTTOM_RIGHT,
@@ -751,52 +595,18 @@ def attn_kv_forward(q, cache: KvCache, block_table, seqlens_k, cu_seqlens_q, *, 
     allocated here they are undefined.  check_status=True synchronises and
     raises what the kernels found (lengths beyond their bounds, pages outside
     the cache)."""
-    index, qs, dtype = cache.index, q.shape, q.dtype
-    t, hq = qs[0], qs[1]
-    if dtype not in _F16 or q.get_device() != index or len(qs) != 3 or qs[2] != cache.d_qk:
-        _check(q, "q", _F16, (t, hq, cache.d_qk), index)
-    n = seqlens_k.shape[0]
-    cols, row = _table(block_table, n, index)
-    cu_p, len_p = _vector(cu_seqlens_q, "cu_seqlens_q", n + 1, index), _vector(seqlens_k, "seqlens_k", n, index)
-    pad_p = 0
-    if cu_seqlens_q_padded is not None:
-        pad_p = _vector(cu_seqlens_q_padded, "cu_seqlens_q_padded", n + 1, index)
-    raw, ctx = _on(index, stream)
-    dv = cache.d_v
-    if out is None:
-        device = q.device
-        o, lse = _empty((t, hq, dv), dtype, device, ctx), _empty((hq, t), torch.float32, device, ctx)
-        so = (0, hq * dv, dv)
-    else:
-        o, lse = out
-        _check(o, "out[0]", (dtype,), (t, hq, dv), index)
-        _check(lse, "out[1]", (torch.float32,), (hq, t), index)
-        if not lse.is_contiguous():
-            raise ValueError("out[1] must be contiguous")
-        so = _rows3(o, "out[0]")
-    p = _FWD.pack(_DTYPES[dtype], n, hq, t, max_seqlen_q, max_seqlen_k, cols, mask, left, right, scale, 0, cu_p, pad_p,
-                  len_p, block_table.data_ptr(), row, q.data_ptr(), o.data_ptr(), lse.data_ptr(), *_rows3(q, "q"),
-                  *so) + cache.packed
-    need = ctypes.c_size_t(0)
-    st = (_entries.get("attn_kv_fwd_workspace_size") or _entry("attn_kv_fwd_workspace_size", 2))(p, ctypes.addressof(need))
+    if stream is not None:
+        with _on_stream(stream):
+            return attn_kv_forward(q, cache, block_table, seqlens_k, cu_seqlens_q, scale=scale, mask=mask, left=left,
+                                   right=right, max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k,
+                                   cu_seqlens_q_padded=cu_seqlens_q_padded, out=out, workspace=workspace,
+                                   check_status=check_status)
+    o, lse = (None, None) if out is None else out
+    st, step, o, lse = (_marshal or _load_marshal()).attend(
+        q, cache.packed, cache.index, block_table, seqlens_k, cu_seqlens_q, cu_seqlens_q_padded, scale, mask, left, right,
+        max_seqlen_q, max_seqlen_k, o, lse, workspace, check_status)
     if st != 0:
-        raise AttnError(st, "attn_kv_fwd_workspace_size")
-    if workspace is None:
-        workspace = _empty((need.value,), torch.uint8, q.device, ctx)
-    elif workspace.get_device() != index or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{index}")
-    ws, nbytes = workspace.data_ptr(), workspace.numel()
-    st = (_entries.get("attn_kv_fwd") or _entry("attn_kv_fwd", 4))(p, ws, nbytes, raw)
-    if st != 0:
-        raise AttnError(st, "attn_kv_fwd")
-    if check_status:
-        found = ctypes.c_int(0)
-        f = _entries.get("attn_kv_fwd_read_status") or _entry("attn_kv_fwd_read_status", 5)
-        st = f(p, ws, nbytes, raw, ctypes.addressof(found))
-        if st != 0:
-            raise AttnError(st, "attn_kv_fwd_read_status")
-        if found.value != 0:
-            raise AttnError(found.value, "attn_kv_fwd (device status)")
+        raise AttnError(st, _FWD_STEPS[step])
     return o, lse
 
 

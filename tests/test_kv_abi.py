@@ -215,10 +215,30 @@ def test_new_status_codes_have_names(lib):
         assert B.attn_status_string(code) != "unknown status"
 
 
-def test_binding_checks_before_it_calls():
-    """Wrong types, shapes, layouts and devices are errors in Python already."""
+@pytest.fixture(scope="module")
+def marshal(lib):
+    from head_attention_backward_gb300 import build
+    build.build_marshal()
+    return B._load_marshal()
+
+
+def test_marshalling_refuses_before_it_calls(marshal):
+    """Wrong types, shapes, layouts and devices are Python errors; no argument
+    ends the process."""
     q = torch.zeros((4, 2, 64))
     f = B.rope_frequencies(64)
+    for args in ((), (1,), (None,) * 9, (q,) * 9, (q, None, q, f, None, 0, 0, None, None), ("x",) * 9):
+        with pytest.raises((TypeError, ValueError)):
+            marshal.rope(*args)
+    for fn, n in ((marshal.cache, 4), (marshal.plan, 8), (marshal.append, 5), (marshal.attend, 17), (marshal.bind, 6)):
+        for x in (None, 3.5, "x", q, torch.zeros(0), torch.zeros((), dtype=torch.int32)):
+            with pytest.raises((TypeError, ValueError)):
+                fn(*(x,) * n)
+        with pytest.raises(TypeError):
+            fn()
+    i = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        B.kv_plan(i, i, torch.zeros((3, 2), dtype=torch.int32), i, i[:1], page_size=16, max_tokens=4)
     with pytest.raises(ValueError):
         B.rope(q, None, torch.zeros(4, dtype=torch.int32), f)      # not on a GPU
     with pytest.raises(ValueError):
