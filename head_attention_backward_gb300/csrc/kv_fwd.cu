@@ -125,7 +125,7 @@ struct Args {
   int job_rows;          // most rows that a row tile can have
   float* part_o;         // [job][nsplit][job_rows][DV]
   float2* part_ml;       // [job][nsplit][job_rows]
-  int* status;           // [batch][nsplit]
+  int* status;           // one per CTA: what its lengths, pages and loads gave
   KvCacheView c;
 };
 
@@ -334,12 +334,11 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
   const int hk = x % A.c.hkv, b = x / A.c.hkv;
   MaskArgs mk;
   const Job J = make_job<ROWS>(A, b, m, mk);
-  const bool reports = hk == 0 && m == 0;   // one CTA per (request, split) says what it found
   const int per_split = split_tiles(A, J);
   const bool whole = J.ntile <= per_split;        // no other split holds keys of these rows
   const int tile0 = split * per_split;
   if (J.nrow <= 0 || (split > 0 && tile0 >= J.ntile)) {
-    if (reports && tid == 0) A.status[b * A.nsplit + split] = J.bad ? ATTN_ERR_BAD_SEQLENS : ATTN_OK;
+    if (tid == 0) A.status[blockIdx.x] = J.bad ? ATTN_ERR_BAD_SEQLENS : ATTN_OK;
     // a cluster whose rows have splits to join (the same for all of it) meets twice
     if (A.cluster && J.nrow > 0 && !whole) {
       cluster_arrive();
@@ -740,8 +739,11 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
     cluster_arrive();   // no CTA leaves while its memory is read
     cluster_wait();
   }
-  if (reports && tid == 0)
-    A.status[b * A.nsplit + split] = *s_bad == 2 ? ATTN_ERR_TIMEOUT : J.bad ? ATTN_ERR_BAD_SEQLENS : *s_bad ? ATTN_ERR_BAD_PAGE : ATTN_OK;
+  if (tid == 0)
+    A.status[blockIdx.x] = *s_bad == 2 ? ATTN_ERR_TIMEOUT
+                           : J.bad     ? ATTN_ERR_BAD_SEQLENS
+                           : *s_bad    ? ATTN_ERR_BAD_PAGE
+                                       : ATTN_OK;
 }
 
 // The joins: O = sum 2^(m_s - m) O_s / sum 2^(m_s - m) l_s over a row's splits, in
@@ -888,7 +890,7 @@ static Layout layout(const attn_kv_fwd_params& p) {
   auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
   size_t o = 0;
   L.off_status = o;
-  o = up(o + (size_t)p.batch * L.nsplit * sizeof(int));
+  o = up(o + (size_t)L.jobs * L.nsplit * sizeof(int));
   const size_t parts = L.nsplit > 1 && !L.cluster ? (size_t)L.jobs * L.nsplit : 0;
   L.off_ml = o;
   o = up(o + parts * L.job_rows * sizeof(float2));
@@ -1091,7 +1093,7 @@ extern "C" int attn_kv_fwd_read_status(const attn_kv_fwd_params* p, const void* 
   int part[1024];
   const char* words[2] = {static_cast<const char*>(workspace) + L.off_status,
                           static_cast<const char*>(workspace) + L.off_long + kv_long_status_offset(L.lng)};
-  const long long count[2] = {(long long)p->batch * L.nsplit, L.lng.slots};
+  const long long count[2] = {L.jobs * L.nsplit, L.lng.slots};
   for (int a = 0; a < 2; ++a)
     for (long long i = 0; i < count[a]; i += 1024) {
       const size_t k = (size_t)(count[a] - i < 1024 ? count[a] - i : 1024);

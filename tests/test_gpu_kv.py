@@ -436,6 +436,14 @@ def test_attend_reports_bad_lengths_and_pages(B):
     ref = kv_ref.attend(q, cu, [0, 30], table, k2, v2, ke, ve, 0.1, 2)
     check_attend(o[1:], lse[:, 1:], tuple(x[1:] if i in (0, 2) else x[:, 1:] for i, x in enumerate(ref)),
                  torch.bfloat16, 64, 90)
+    # reported wherever it is seen: here only by the last of 40 causal queries
+    q2 = q[:1].expand(41, -1, -1).contiguous()
+    late = [list(r) for r in table]
+    late[0][5] = -1
+    with pytest.raises(B.AttnError) as e:
+        B.attn_kv_forward(q2.cuda(), c, dev(late), dev([90, 30]), dev([0, 40, 41]), scale=0.1, max_seqlen_q=40,
+                          max_seqlen_k=96, check_status=True)
+    assert e.value.status == B.ATTN_ERR_BAD_PAGE
     short = [table[0][:2] + table[0][3:], table[1]]
     ref = kv_ref.attend(q, cu, [74, 30], short, kc, vc, ke, ve, 0.1, 2)
     check_attend(o, lse, ref, torch.bfloat16, 64, 90)
