@@ -523,7 +523,13 @@ class KvCache:
     def __init__(self, k, v, k_exp, v_exp):
         (self.packed, self.index, self.num_pages, self.page_size, self.nhead_kv, self.d_qk,
          self.d_v) = (_marshal or _load_marshal()).cache(k, v, k_exp, v_exp)
-        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        self.k, self.v, self.k_exp = k, v, k_exp
+        self.v_exp = v_exp
+
+    def __setattr__(self, name, value):
+        if hasattr(self, "v_exp"):   # the last one to be set
+            raise AttributeError("a KvCache describes the tensors it was made from; make another for others")
+        object.__setattr__(self, name, value)
 
     @classmethod
     def empty(cls, num_pages, page_size, nhead_kv, d_qk, d_v, device="cuda"):

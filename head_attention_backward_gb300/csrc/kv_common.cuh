@@ -30,6 +30,9 @@ inline bool kv_headdims(int dqk, int dv) {
          (dqk == 256 && dv == 256);
 }
 
+// Grids carry twice this many (head, side) pairs in their second dimension.
+constexpr int KV_MAX_HEADS = 16384;
+
 inline int kv_page_shift(int page_size) {
   for (int s = 4; s <= 8; ++s)
     if (page_size == 1 << s) return s;
@@ -52,7 +55,7 @@ inline bool kv_strides(const int64_t in[3], long long pages, long long rows, lon
 }
 
 inline int kv_resolve(const attn_kv_cache& c, KvCacheView* out) {
-  if (c.num_pages < 1 || c.nhead_kv < 1 || c.reserved != 0) return ATTN_ERR_INVALID_ARG;
+  if (c.num_pages < 1 || c.nhead_kv < 1 || c.nhead_kv > KV_MAX_HEADS || c.reserved != 0) return ATTN_ERR_INVALID_ARG;
   const int shift = kv_page_shift(c.page_size);
   if (shift < 0) return ATTN_ERR_INVALID_ARG;
   if (!kv_headdims(c.d_qk, c.d_v)) return ATTN_ERR_UNSUPPORTED_HEADDIM;

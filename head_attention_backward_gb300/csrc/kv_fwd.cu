@@ -905,7 +905,8 @@ static Layout layout(const attn_kv_fwd_params& p) {
 static int validate_sizes(const attn_kv_fwd_params* p) {
   if (!p || p->reserved != 0 || (p->dtype != ATTN_BF16 && p->dtype != ATTN_FP16)) return ATTN_ERR_INVALID_ARG;
   const attn_kv_cache& c = p->cache;
-  if (c.num_pages < 1 || c.nhead_kv < 1 || c.reserved != 0 || kv_page_shift(c.page_size) < 0) return ATTN_ERR_INVALID_ARG;
+  if (c.num_pages < 1 || c.nhead_kv < 1 || c.nhead_kv > KV_MAX_HEADS || c.reserved != 0 || kv_page_shift(c.page_size) < 0)
+    return ATTN_ERR_INVALID_ARG;
   if (!kv_headdims(c.d_qk, c.d_v)) return ATTN_ERR_UNSUPPORTED_HEADDIM;
   if (p->batch < 1 || p->batch > (1 << 20) || p->nhead_q < 1 || p->nhead_q > (1 << 16) || p->nhead_q % c.nhead_kv)
     return ATTN_ERR_INVALID_ARG;

@@ -204,7 +204,7 @@ static int run(const attn_kv_plan_params* p, cudaStream_t st) {
   if (!p || p->reserved != 0) return ATTN_ERR_INVALID_ARG;
   const int shift = kv_page_shift(p->page_size);
   if (shift < 0 || p->batch < 1 || p->batch > ATTN_KV_MAX_BATCH || p->num_pages < 1 || p->max_blocks < 1 ||
-      p->max_tokens < 0)
+      p->max_tokens < 0 || p->max_tokens > (1 << 30))
     return ATTN_ERR_INVALID_ARG;
   if (((long long)p->max_blocks << shift) > (1LL << 30) || p->table_stride < p->max_blocks ||
       p->table_stride >= (1LL << 36))

@@ -83,11 +83,19 @@ T* vector(PyObject* o, const char* what, int64_t n, int index) {
   return pointer<T>(t);
 }
 
+// Three zero strides mean contiguous to the library, so an expanded tensor must
+// not reach it: its first element stands for all of them.
+void spread(const at::Tensor& t, const char* what) {
+  for (int64_t i = 0; i < t.dim(); ++i)
+    if (t.size(i) > 1 && t.stride(i) == 0) refuse(what, "a tensor that is not expanded", t);
+}
+
 // {0, row, head} strides of [T, H, D]; a dimension of one entry may carry any
 // stride and is given the contiguous one.
 void rows3(const at::Tensor& t, const char* what, int64_t out[3]) {
   const int64_t n = t.size(0), h = t.size(1), d = t.size(2);
   if (d > 1 && t.stride(2) != 1) refuse(what, "contiguous in the head dimension", t);
+  spread(t, what);
   out[0] = 0;
   out[2] = h > 1 ? t.stride(1) : d;
   out[1] = n > 1 ? t.stride(0) : h * out[2];
@@ -213,7 +221,8 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.stride_pos[1] = dims == 4 ? pos.stride(axes) : 0;
     p.stride_pos[2] = pos.stride(axes + rows_dims - 1);
     p.positions = pointer<const int32_t>(pos);
-    auto strides = [&](const at::Tensor& t, int64_t out[3]) {
+    auto strides = [&](const at::Tensor& t, const char* what, int64_t out[3]) {
+      spread(t, what);
       out[0] = dims == 4 ? t.stride(0) : 0;
       out[1] = t.stride(rows_dims - 1);
       out[2] = t.stride(rows_dims);
@@ -230,8 +239,8 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor qo = output(a[7], q, "out[0]");
     p.q = q.data_ptr();
     p.q_out = qo.data_ptr();
-    strides(q, p.stride_q);
-    strides(qo, p.stride_q_out);
+    strides(q, "q", p.stride_q);
+    strides(qo, "out[0]", p.stride_q_out);
     at::Tensor ko;
     if (has_k) {
       const at::Tensor& k = tensor(a[1], "k");
@@ -243,8 +252,8 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       p.nhead_kv = (int32_t)k.size(-2);
       p.k = k.data_ptr();
       p.k_out = ko.data_ptr();
-      strides(k, p.stride_k);
-      strides(ko, p.stride_k_out);
+      strides(k, "k", p.stride_k);
+      strides(ko, "out[1]", p.stride_k_out);
     }
     const int st = call([&] { return entries.rope(&p, stream); });
     return Py_BuildValue("iNN", st, THPVariable_Wrap(qo), has_k ? THPVariable_Wrap(ko) : Py_NewRef(Py_None));
@@ -262,6 +271,8 @@ PyObject* py_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (v.scalar_type() != k.scalar_type() || v.dim() != 4 || v.size(0) != k.size(0) || v.size(1) != k.size(1) ||
         v.size(2) != k.size(2) || !on(v, index) || v.stride(3) != 1)
       refuse("v", "like k but for d_v", v);
+    spread(k, "k");
+    spread(v, "v");
     attn_kv_cache c{};
     for (int i = 0; i < 2; ++i) {
       const at::Tensor& e = tensor(a[2 + i], i ? "v_exp" : "k_exp");

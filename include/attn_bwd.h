@@ -458,7 +458,7 @@ int attn_rope(const attn_rope_params* p, cudaStream_t stream);
 typedef struct {
   int32_t num_pages;      /* >= 1                                                  */
   int32_t page_size;      /* 16, 32, 64, 128 or 256                                */
-  int32_t nhead_kv;
+  int32_t nhead_kv;       /* 1 .. 16384                                            */
   int32_t d_qk;           /* (64, 64), (128, 128), (192, 128) or (256, 256)        */
   int32_t d_v;
   int32_t reserved;       /* 0                                                     */
@@ -500,7 +500,7 @@ typedef struct {
   int32_t page_size;      /* as in attn_kv_cache                                   */
   int32_t num_pages;
   int32_t max_blocks;     /* columns of block_table, max_blocks * page_size <= 2^30 */
-  int32_t max_tokens;     /* entries of positions and slots                        */
+  int32_t max_tokens;     /* entries of positions and slots, 0 .. 2^30             */
   int32_t reserved;       /* 0                                                     */
   const int32_t* new_lens;   /* device, [batch]                                    */
   const int32_t* seqlens;    /* device, [batch], tokens in the cache               */
@@ -611,7 +611,8 @@ int attn_kv_fwd(const attn_kv_fwd_params* p, void* workspace, size_t workspace_b
 
 /* Synchronise `stream` and return what the last attn_kv_fwd of *p on
  * `workspace` found on the device (ATTN_OK, ATTN_ERR_BAD_SEQLENS,
- * ATTN_ERR_BAD_PAGE) in *status. */
+ * ATTN_ERR_BAD_PAGE; ATTN_ERR_TIMEOUT if a load inside a kernel never arrived,
+ * whose rows are then NaN) in *status. */
 int attn_kv_fwd_read_status(const attn_kv_fwd_params* p, const void* workspace, size_t workspace_bytes,
                             cudaStream_t stream, int* status);
 

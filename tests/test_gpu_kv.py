@@ -628,6 +628,48 @@ def test_what_the_binding_refuses(B):
             B.rope(*args)
 
 
+def test_expanded_tensors_are_refused(B):
+    """Strides of zero in a tensor with more than one entry: the library would
+    take three of them for contiguous and read past the tensor."""
+    def e(*shape, dtype=torch.bfloat16):
+        return torch.zeros(shape[-1], dtype=dtype, device="cuda").expand(shape)
+
+    q, table, kc, vc, ke, ve, cu = attend_case(64, 64, torch.bfloat16, 16, [5, 9], [1, 1], 1, 2)
+    c, qd, td, ld, cud = handle(B, kc, vc, ke, ve), q.cuda(), dev(table), dev([5, 9]), dev(cu)
+    kw = dict(scale=0.1, max_seqlen_q=1, max_seqlen_k=16)
+    flat = torch.zeros_like(qd)
+    lse = torch.zeros((qd.shape[1], qd.shape[0]), device="cuda")
+    for x in (e(*qd.shape), qd[:1].expand(qd.shape), qd[:, :1].expand(qd.shape)):
+        with pytest.raises(ValueError, match="expanded"):
+            B.attn_kv_forward(x, c, td, ld, cud, **kw)
+        with pytest.raises(ValueError, match="expanded"):
+            B.attn_kv_forward(qd, c, td, ld, cud, out=(x, lse), **kw)
+        with pytest.raises(ValueError, match="expanded"):
+            B.rope(x, None, dev([1, 2]), B.rope_frequencies(64))
+        with pytest.raises(ValueError, match="expanded"):
+            B.rope(flat, x, dev([1, 2]), B.rope_frequencies(64))
+        with pytest.raises(ValueError, match="expanded"):
+            B.rope(flat, None, dev([1, 2]), B.rope_frequencies(64), out=(x, None))
+    k, sl = torch.zeros((2, c.nhead_kv, 64), dtype=torch.bfloat16, device="cuda"), dev([0, 1], torch.int64)
+    for args in ((e(2, c.nhead_kv, 64), k), (k, e(2, c.nhead_kv, 64))):
+        with pytest.raises(ValueError, match="expanded"):
+            B.kv_append(*args, sl, c)
+    page, byte = e(4, 16, 2, 64, dtype=torch.uint8), torch.zeros((4, 16, 2, 64), dtype=torch.uint8, device="cuda")
+    s = torch.full((4, 2), 127, dtype=torch.uint8, device="cuda")
+    for args in ((page, byte), (byte, page)):
+        with pytest.raises(ValueError, match="expanded"):
+            B.KvCache(*args, s, s.clone())
+    # one entry may carry any stride
+    assert torch.equal(B.rope(flat[:1, :1].expand(1, 1, 64), None, dev([1]), B.rope_frequencies(64))[0], flat[:1, :1])
+
+
+def test_a_cache_handle_keeps_its_tensors(B):
+    c = B.KvCache.empty(4, 16, 2, 64, 64)
+    for name in ("k", "v", "k_exp", "v_exp", "packed", "page_size"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, getattr(c, name))
+
+
 # ------------------------------------------------------- the step they make up
 
 @pytest.mark.parametrize("graph", [False, True])

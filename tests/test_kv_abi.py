@@ -93,7 +93,8 @@ def cache(**kw):
 
 
 BAD_CACHES = [
-    (dict(num_pages=0), -1), (dict(nhead_kv=0), -1), (dict(page_size=8), -1), (dict(page_size=48), -1),
+    (dict(num_pages=0), -1), (dict(nhead_kv=0), -1), (dict(nhead_kv=16385), -1),
+    (dict(page_size=8), -1), (dict(page_size=48), -1),
     (dict(page_size=512), -1), (dict(d_qk=96), -2), (dict(d_qk=64), -2), (dict(d_v=64), -2), (dict(reserved=1), -1),
 ]
 BAD_CACHE_POINTERS = [
@@ -116,6 +117,7 @@ def plan_params(**kw):
 
 @pytest.mark.parametrize("kw", [
     dict(batch=0), dict(batch=8193), dict(page_size=24), dict(num_pages=0), dict(max_blocks=0), dict(max_tokens=-1),
+    dict(max_tokens=2 ** 30 + 1),
     dict(max_blocks=2 ** 27, table_stride=2 ** 27), dict(table_stride=3), dict(reserved=7), dict(new_lens=None),
     dict(seqlens=None), dict(seqlens_out=None), dict(block_table=None), dict(free_pages=None), dict(free_count=None),
     dict(free_count_out=None), dict(cu_seqlens=None), dict(positions=None), dict(slots=None), dict(status=None),
