@@ -53,11 +53,13 @@ constexpr int META_TILES = 256;     // tiles whose pages are held in shared memo
 // Splits.  A job is one row tile of one request and kv head.  The host sets how
 // many splits a job has at most, the device how long they are, from the request's
 // own length, so that max_seqlen_k need not be tight.
-// * Few jobs: splits for one wave.  Of one request, all equal: two CTAs per SM
-//   (131,072 tokens, 8 kv heads: 50.5 us with 304 CTAs, 55.3 with 152, 56.3 with
-//   608: more parts to join).  Of several, whose lengths differ: four per SM (4
-//   requests of up to 16,384 tokens: 22.2 us with 608 CTAs, 29.6 with 304, 25.9 with
-//   912; 32 of up to 4,096: 40.7, 53.5 and 43.6 us).
+// * Few jobs (at most half a wave): splits for one wave.  Of one request, all
+//   equal: two CTAs per SM (131,072 tokens, 8 kv heads: 50.5 us with 304 CTAs, 55.3
+//   with 152, 56.3 with 608: more parts to join).  Of several, whose lengths differ:
+//   as many as are resident (head dim 128, four per SM: 4 requests of up to 16,384
+//   tokens: 21.2 us with 608 CTAs, 29.1 with 304, 24.5 with 912; 16 of up to 2,000:
+//   14.6, 17.8 and 20.5.  Head dim 192, three: 29.8 us with 456 CTAs, 30.7 with 608;
+//   16.4 and 20.2.  Head dim 256, two: 8 of up to 1,000 11.4 us with 304, 19.0 with 608).
 // * Many jobs: at most MAX_GRID CTAs, which still evens out ragged lengths (64
 //   requests of up to 8,192 tokens: 110.2 us, with 4,608 CTAs 108.9, with one or two
 //   splits 114); the CTAs without work behind a loose bound cost little (64
@@ -69,7 +71,6 @@ constexpr int META_TILES = 256;     // tiles whose pages are held in shared memo
 // taken by persistent CTAs, was slower throughout (65 us, 119 us and 32 us in these
 // cases): it puts two more trips to memory in front of the first load.
 constexpr int HALF_WAVE = 304;
-constexpr int WAVE = 608;
 constexpr int MAX_GRID = 2560;
 constexpr int EVEN_TILES = 64;
 constexpr int MIN_TILES = 12;
@@ -81,6 +82,9 @@ constexpr int MAX_CLUSTER = 8;
 constexpr int EV_SLACK = 4;         // V scales within 2^4 of the accumulator's unit go on P
 constexpr float P_LOG2 = 4.f;       // P = 2^4 at the running maximum
 constexpr float SLACK_LOG2 = 7.f;   // growth of the maximum that is let pass: P <= 2^(4 + 7 + 4)
+
+// CTAs per SM that the registers have to allow (shared memory allows them too).
+constexpr int resident(int dqk, int nt) { return (dqk == 256 ? 3 : dqk == 192 ? 4 : 5) - nt; }
 
 // NT: query rows of a CTA in units of 8.
 template <int DQK, int DV, int NT>
@@ -94,8 +98,7 @@ struct Cfg {
   static constexpr int OFF_META = OFF_BAR + NWARPS * NST * 8;          // int2[META_TILES + 1]: page, exponents
   static constexpr int OFF_ML = OFF_META + (META_TILES + 1) * 8;       // float[2][NWARPS][ROWS]
   static constexpr int SMEM = OFF_ML + 2 * NWARPS * ROWS * 4 + ROWS * 8 + 8 + 1024;   // + alignment slack
-  // CTAs per SM that the registers have to allow (shared memory allows them too)
-  static constexpr int RESIDENT = NT == 1 ? (DQK == 256 ? 2 : DQK == 192 ? 3 : 4) : (DQK == 256 ? 1 : DQK == 192 ? 2 : 3);
+  static constexpr int RESIDENT = resident(DQK, NT);
   static constexpr int OFF_JOIN = NWARPS * ROWS * DV * 4;              // float[ROWS][DV], behind the warps' parts
   static_assert(OFF_JOIN + ROWS * DV * 4 <= NWARPS * RING, "the joins reuse the rings");
 };
@@ -881,10 +884,18 @@ static Layout layout(const attn_kv_fwd_params& p) {
   L.mtiles = (int)cdiv_ll(rows, 8 * L.nt);
   L.job_rows = (int)(rows < 8 * L.nt ? rows : 8 * L.nt);
   L.jobs = (long long)p.batch * p.cache.nhead_kv * L.mtiles;
-  const int tiles = max_keys(p) / TILE + 2;
-  const bool few = L.jobs < HALF_WAVE;
+  // Keys that the rows of a job see at most (8 requests of up to 1,183 tokens under
+  // a window of 190, head dim 256: 8.8 us, 18.1 with splits for all of them).
+  long long keys = max_keys(p);
+  if (p.mask == ATTN_MASK_WINDOW && p.window_left >= 0 && p.window_right >= 0) {
+    const long long span = (long long)p.window_left + p.window_right + 1 + cdiv(8 * L.nt, g);
+    keys = span < keys ? span : keys;
+  }
+  const int tiles = (int)(keys / TILE) + 2;
+  const int wave = 152 * resident(p.cache.d_qk, L.nt);
+  const bool few = 2 * L.jobs <= wave;
   L.min_tiles = few ? MIN_TILES : EVEN_TILES;
-  const long long n = few ? (p.batch > 1 ? WAVE : HALF_WAVE) / L.jobs : cdiv_ll(MAX_GRID, L.jobs);
+  const long long n = few ? (p.batch > 1 ? wave : HALF_WAVE) / L.jobs : cdiv_ll(MAX_GRID, L.jobs);
   L.nsplit = n < cdiv(tiles, L.min_tiles) ? (int)n : cdiv(tiles, L.min_tiles);
   L.cluster = few && L.nsplit > 1 && L.nsplit <= MAX_CLUSTER;
   auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
