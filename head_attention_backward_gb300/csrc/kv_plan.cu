@@ -4,20 +4,26 @@
 // A few kilobytes move, so the call is its launch and dependent trips to memory:
 // the lengths, then the stack and tables (first to check them, then, out of L1,
 // to use them).  Slots are worked out from what was read, not from the entries
-// just written, so nothing waits for a store.  One CTA does it all: the sums of a batch of 8192 requests are eight
-// requests per thread, and nothing has to wait for another CTA.  Only the slots
-// and positions of many tokens (prompts) are left to a second kernel that spreads
-// them over the GPU, launched early so that it waits in place.
+// just written, so nothing waits for a store.  One CTA does it all: the sums of a
+// batch of 8192 requests are 17 requests per thread, and nothing has to wait for
+// another CTA.  Only the slots and positions of many tokens (prompts) are left to
+// a second kernel that spreads them over the GPU, launched early so that it waits
+// in place.
 #include "common.cuh"
 #include "kv_common.cuh"
 
 namespace attn {
 namespace kvplan {
 
-constexpr int MAX_THREADS = 1024;
-constexpr int SMALL_THREADS = 256;   // a batch and tokens of at most this many: quicker barriers
+// One request per thread up to 256; more threads make every barrier slower than
+// they make the loops shorter (256 requests of a token each: 4.3 us with 256, 4.7 with 512, 6.5 with
+// 1,024; 512: 5.3, 4.8, 6.6; 8,000: 18.9, 14.2, 13.7).
+constexpr int MAX_THREADS = 512;
+constexpr int SMALL_THREADS = 256;
 constexpr int FILL_THREADS = 256;
-constexpr int FILL_FROM = 4096;   // tokens
+// Tokens from which a second kernel writes them (2,000: 7.8 us with it, 8.9 without; 4,000:
+// 8.0 and 14.0; 700: 4.8 and 3.8).
+constexpr int FILL_FROM = 1024;
 
 struct Sums {
   long long tok, take, back;
@@ -48,7 +54,7 @@ __global__ void __launch_bounds__(MAX_THREADS) plan_kernel(const attn_kv_plan_pa
   const int threads = blockDim.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (!fill) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int per = cdiv(n, threads);
+  const int per = cdiv(n, threads) | 1;   // odd: the threads' entries lie in different banks
   const int b0 = min(tid * per, n), b1 = min(b0 + per, n);
   const int free_n = *P.free_count;   // the output may be the same word: read by all before the first barrier
   const long long cap = (long long)P.max_blocks << shift;
@@ -220,7 +226,7 @@ static int run(const attn_kv_plan_params* p, cudaStream_t st) {
       cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return ATTN_ERR_CUDA;
   const bool fill = p->max_tokens <= FILL_FROM;
-  const int threads = p->batch <= SMALL_THREADS && p->max_tokens <= SMALL_THREADS ? SMALL_THREADS : MAX_THREADS;
+  const int threads = p->batch <= SMALL_THREADS ? SMALL_THREADS : MAX_THREADS;
   plan_kernel<<<1, threads, smem, st>>>(*p, shift, fill);
   if (!fill) {
     cudaLaunchAttribute early;
