@@ -31,12 +31,15 @@ struct Sums {
 
 __device__ __forceinline__ Sums add(Sums a, Sums b) { return {a.tok + b.tok, a.take + b.take, a.back + b.back}; }
 
-// Largest b with prefix[b] <= x, for prefix[0] = 0 <= x < prefix[n].
+// Largest b with prefix[b] <= x, for prefix[0] = 0 <= x < prefix[n]; three
+// probes at a time, since each step waits for shared memory.
 __device__ __forceinline__ int find(const int* prefix, int n, int x) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (prefix[mid] <= x) lo = mid; else hi = mid;
+    const int step = (hi - lo + 3) >> 2, a = lo + step, b = min(a + step, hi), c = min(b + step, hi);
+    const bool pa = prefix[a] <= x, pb = prefix[b] <= x, pc = prefix[c] <= x;
+    lo = pc ? c : pb ? b : pa ? a : lo;
+    hi = pc ? hi : pb ? c : pa ? b : a;
   }
   return lo;
 }
