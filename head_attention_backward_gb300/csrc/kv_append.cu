@@ -249,9 +249,12 @@ __global__ void __launch_bounds__(NTHREADS, RESIDENT) append_kernel(const Args A
   const int t0 = blockIdx.x * A.tile;
   const int shift = A.c.page_shift, size = 1 << shift;
   const long long limit = (long long)A.c.num_pages << shift;
+  // a load without a branch, so that many are on their way together (pages of 128:
+  // 8.2 us against 9.4)
   auto slot_at = [&](int t) -> long long {
-    const long long s = t >= 0 && t < A.tokens ? (long long)__ldg(A.slots + t) : -1;
-    return s < limit ? s : -1;
+    const bool in = t >= 0 && t < A.tokens;
+    const long long s = (long long)__ldg(A.slots + (in ? t : t0));
+    return in && s < limit ? s : -1;
   };
   auto page_at = [&](int t) {   // -1: none
     const long long s = slot_at(t);
@@ -368,8 +371,8 @@ static int run(const attn_kv_append_params* p, cudaStream_t st) {
   while (a.gw < NWARPS && HELD * (a.gw * 32 / (dim / 8)) < p->cache.page_size) a.gw *= 2;
   // Items a group takes one after the other: as many as leave the GPU full, up
   // to four, beyond which the CTAs' search for runs no longer weighs (16,160
-  // tokens in pages of 64: 22.4 us at four, 29.0 at one; 64 single tokens: 3.8 us
-  // at one, 4.6 at four).
+  // tokens in pages of 64: 24.4 us at four, 27.9 at one, 32.6 at eight; 64 single
+  // tokens: 4.0 us at one, 4.6 at four).
   const int groups = NWARPS / a.gw, per_run = p->cache.nhead_kv * 2;
   const long long full = (long long)(p->tokens / p->cache.page_size) * per_run / (groups * 152LL * RESIDENT);
   const int rounds = full < 1 ? 1 : full > 4 ? 4 : (int)full;
