@@ -392,14 +392,21 @@ struct FwdLayout {
 };
 void launch_fwd(const attn_fwd_params& p, const FwdLayout& L, cudaStream_t st);
 // Segments given by first row and length instead of offsets (group mode): row
-// arrays of `batch` entries on the device.
+// arrays of `batch` entries on the device.  Their query tiles pack the heads of a
+// group (rows = token x head), at most 128 of them, and the keys of a tile may be
+// split over CTAs, whose parts a second kernel joins.
 struct FwdSegments {
   const int* zeros;
   const int* len_q;
   const int* start_q;
   const int* len_k;
   const int* start_k;
+  int nsplit;              // most splits of a tile's keys
+  float* part_o;           // [nsplit][total_q][nhead_q][d_v], used where nsplit > 1
+  float2* part_ml;         // [nsplit][total_q][nhead_q]: running maximum (log2 units) and sum
 };
+constexpr int FWD_TILE_ROWS = 128;   // query rows of a tile of the tensor-core forward, and keys
+constexpr int FWD_MIN_SPLIT = 8;     // key tiles of a split at least
 // Tensor-core forward (fwd_tc.cu); ATTN_ERR_UNSUPPORTED_HEADDIM for the
 // dtypes, head dims and scales it is not built for.  `seg` replaces the cu_seqlens of p.
 int launch_fwd_tc(const attn_fwd_params& p, const FwdLayout& L, cudaStream_t st, const FwdSegments* seg = nullptr);

@@ -113,7 +113,27 @@ struct Args {
   Strides so;
   float* lse;
   int tq;                  // group mode: LSE row stride (rows of q)
+  // packed segments only
+  int tok;                 // query tokens of a tile, each with the g heads of its group
+  int nsplit;
+  float* part_o;
+  float2* part_ml;
 };
+
+// Packed segments: the key tiles of query tokens [qs, qe], and what split `split`
+// of them takes.
+struct KeyTiles {
+  int first, n;            // of this split; n may be 0 in split 0 alone
+  int splits;              // that hold tiles
+};
+__device__ __forceinline__ KeyTiles key_tiles(const MaskArgs& m, int lk, int qs, int qe, int nsplit, int split) {
+  int klo = 0, khi = lk - 1;
+  if (m.left >= 0) klo = max(klo, qs + m.off - m.left);
+  if (m.right >= 0) khi = min(khi, qe + m.off + m.right);
+  const int kt0 = klo / FN, all = (lk > 0 && khi >= klo) ? khi / FN - kt0 + 1 : 0;
+  const int per = max(cdiv(all, nsplit), FWD_MIN_SPLIT), begin = split * per;
+  return {kt0 + begin, min(per, all - begin), cdiv(all, per)};
+}
 
 struct Ctx {
   uint64_t* bar;
@@ -156,12 +176,15 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __half*) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-template <int DQK, int DV, typename T>
+// PACKED: segments with packed query tiles and split keys (FwdSegments).
+template <int DQK, int DV, typename T, bool PACKED>
 __global__ void __launch_bounds__(NTHREADS, 1) fwd_tc_kernel(const __grid_constant__ Maps maps, const Args A) {
   using C = FCfg<DQK, DV>;
   static_assert(C::KST <= 3 && B_END <= C::NBAR, "barrier slots");
-  const int qt = gridDim.x - 1 - blockIdx.x;   // the longest causal tiles first
-  const int h = blockIdx.y, b = blockIdx.z, hk = h / A.g;
+  const int xt = gridDim.x - 1 - blockIdx.x;   // the longest causal tiles first
+  const int qt = PACKED ? xt / A.nsplit : xt, split = PACKED ? xt - qt * A.nsplit : 0;
+  const int b = blockIdx.z, hk = PACKED ? blockIdx.y : blockIdx.y / A.g;
+  const int h = PACKED ? hk * A.g : blockIdx.y;   // (first) head
   int q0, lq, k0, lk;
   if (A.group) {
     lq = __ldg(A.cu_q_end + b) - __ldg(A.cu_q + b);
@@ -171,16 +194,24 @@ __global__ void __launch_bounds__(NTHREADS, 1) fwd_tc_kernel(const __grid_consta
   } else {
     q0 = b * A.sq; lq = A.sq; k0 = b * A.sk; lk = A.sk;
   }
-  const int qs = qt * FM;
+  const int qs = qt * (PACKED ? A.tok : FM);
   if (qs >= lq) return;
   // KV tiles any row of this query tile can see
   const MaskArgs m = mask_args(A.mask, A.left, A.right, lq, lk);
-  const int qe = min(qs + FM, lq) - 1;
+  const int qe = min(qs + (PACKED ? A.tok : FM), lq) - 1;
   int klo = 0, khi = lk - 1;
   if (m.left >= 0) klo = max(klo, qs + m.off - m.left);
   if (m.right >= 0) khi = min(khi, qe + m.off + m.right);
-  const int kt0 = klo / FN;
-  const int nkv = (lk > 0 && khi >= klo) ? khi / FN - kt0 + 1 : 0;
+  int kt0 = klo / FN;
+  int nkv = (lk > 0 && khi >= klo) ? khi / FN - kt0 + 1 : 0;
+  bool whole = true;
+  if (PACKED) {
+    const KeyTiles kt = key_tiles(m, lk, qs, qe, A.nsplit, split);
+    if (split > 0 && kt.n <= 0) return;
+    kt0 = kt.first;
+    nkv = kt.n;
+    whole = kt.splits <= 1;
+  }
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -229,7 +260,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fwd_tc_kernel(const __grid_consta
       tma_prefetch_desc(&maps.q);
       tma_prefetch_desc(&maps.k);
       tma_prefetch_desc(&maps.v);
-      mbar_arrive_expect_tx(bar + B_Q_FULL, C::Q_BYTES);
+      mbar_arrive_expect_tx(bar + B_Q_FULL, PACKED ? C::NCK * 128 * A.g * A.tok : C::Q_BYTES);
       for (int c = 0; c < C::NCK; ++c)
         tma_load_3d(smem + C::OFF_Q + c * C::CH, &maps.q, bar + B_Q_FULL, c * 64, h, q0 + qs);
       // K tile i and V tile i - (KST - 1) in turn: K runs ahead
@@ -319,8 +350,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) fwd_tc_kernel(const __grid_consta
     const int quarter = warp & 3;
     const int half = (warp - FIRST_SM_WARP) >> 2;
     const int r = quarter * 32 + lane;                 // query row = TMEM lane
-    const int qi = qs + r;
-    const bool row_ok = qi < lq;
+    // packed: row = token x head; rows past the last whole token hold anything
+    // and are not stored
+    const int qi = qs + (PACKED ? r / A.g : r), hr = PACKED ? h + r - r / A.g * A.g : h;
+    const bool row_ok = qi < lq && (!PACKED || r < A.g * A.tok);
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
     float* red = reinterpret_cast<float*>(smem + C::OFF_RED);   // [slot][half][row]
     // this warp's value of row r for the partner warp: write, arrive, wait
@@ -446,8 +479,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) fwd_tc_kernel(const __grid_consta
     float lo_other = 0.f;
     if (ok) ok = exchange(l, 2, B_EPI + quarter, 0, lo_other);
     l += lo_other;
-    const long long li = A.group ? (long long)h * A.tq + q0 + qi : ((long long)b * A.hq + h) * A.sq + qi;
-    T* orow = static_cast<T*>(A.o) + elem_off(A.so, (long long)q0 + qi, h) + half * OC;
+    const long long li = A.group ? (long long)hr * A.tq + q0 + qi : ((long long)b * A.hq + hr) * A.sq + qi;
+    T* orow = static_cast<T*>(A.o) + elem_off(A.so, (long long)q0 + qi, hr) + half * OC;
+    // a part: O and the sum as they are, fp32
+    const long long part = PACKED ? ((long long)split * A.tq + q0 + qi) * A.hq + hr : 0;
     const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
     for (int c = 0; c < OC / 32; ++c) {
@@ -459,7 +494,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) fwd_tc_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = 0u;
       }
-      if (row_ok && ok) {
+      if (PACKED && !whole) {
+        if (row_ok && ok) {
+          float4* dst = reinterpret_cast<float4*>(A.part_o + part * DV + half * OC + c * 32);
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            dst[v] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]), __uint_as_float(o[4 * v + 2]),
+                                 __uint_as_float(o[4 * v + 3]));
+        }
+      } else if (row_ok && ok) {
         uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
@@ -472,7 +515,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) fwd_tc_kernel(const __grid_consta
         }
       }
     }
-    if (row_ok && half == 0)
+    if (PACKED && !whole) {
+      if (row_ok && half == 0)
+        A.part_ml[part] = ok ? make_float2(mx, l) : make_float2(0.f, __int_as_float(0x7fc00000));
+    } else if (row_ok && half == 0)
       A.lse[li] = !ok ? __int_as_float(0x7fc00000) : l > 0.f ? (mx + log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
 
@@ -482,6 +528,60 @@ __global__ void __launch_bounds__(NTHREADS, 1) fwd_tc_kernel(const __grid_consta
     tc_fence_after();
     __syncwarp();
     tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// Joins the parts of packed tiles whose keys were split, in the order of the
+// splits: O = sum 2^(m_s - m) O_s / sum 2^(m_s - m) l_s.  A warp takes a row at a
+// time, its lanes first a split's maximum and sum each, then the columns.
+constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_GRID = 2048;      // CTAs at most, unless segments x kv heads are more
+constexpr int MAX_SPLITS = 32;       // lanes
+
+template <int DV, typename T>
+__global__ void __launch_bounds__(32 * JOIN_WARPS) join_parts_kernel(const Args A) {
+  constexpr int PER = DV / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hk = blockIdx.y, b = blockIdx.z;
+  const int lq = __ldg(A.cu_q_end + b), lk = __ldg(A.cu_k_end + b), q0 = __ldg(A.st_q + b);
+  const MaskArgs m = mask_args(A.mask, A.left, A.right, lq, lk);
+  const long long step = (long long)A.tq * A.hq;   // rows of a split
+  for (long long i = (long long)blockIdx.x * JOIN_WARPS + warp; i < (long long)lq * A.g;
+       i += (long long)gridDim.x * JOIN_WARPS) {
+    const int tk = (int)(i / A.g), h = hk * A.g + (int)(i - (long long)tk * A.g);
+    const int qs = tk / A.tok * A.tok;
+    const int n = key_tiles(m, lk, qs, min(qs + A.tok, lq) - 1, A.nsplit, 0).splits;
+    if (n <= 1) continue;
+    const long long row = (long long)(q0 + tk) * A.hq + h;
+    const float2 ml = lane < n ? A.part_ml[row + lane * step] : make_float2(-INFINITY, 0.f);
+    float top = ml.x;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    // a split that saw no key of the row holds zeros
+    const float weight = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top);
+    const float part = weight * ml.y;
+    float l = 0.f, v[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) v[k] = 0.f;
+    const float* src = A.part_o + row * DV + lane * PER;
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float w = __shfl_sync(0xffffffffu, weight, s);
+      l += __shfl_sync(0xffffffffu, part, s);
+#pragma unroll
+      for (int k = 0; k < PER; k += 2) {
+        const float2 x = *reinterpret_cast<const float2*>(src + s * step * DV + k);
+        v[k] += w * x.x;
+        v[k + 1] += w * x.y;
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    T* dst = static_cast<T*>(A.o) + elem_off(A.so, (long long)q0 + tk, h) + lane * PER;
+#pragma unroll
+    for (int k = 0; k < PER; k += 2)
+      *reinterpret_cast<uint32_t*>(dst + k) = pack2(v[k] * inv, v[k + 1] * inv, (T*)nullptr);
+    if (lane == 0)
+      A.lse[(long long)h * A.tq + q0 + tk] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
   }
 }
 
@@ -502,14 +602,14 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // 3-D view (dim, heads, rows) of a 16-bit tensor with element strides x;
-// boxes of 64 x 1 x 128 rows with 128-byte swizzle.
+// boxes of 64 x box_heads x box_rows (at most 128 rows of 64) with 128-byte swizzle.
 static bool make_map(CUtensorMap* m, const void* base, bool fp16, int dim, int heads, long long rows,
-                     const Strides& x) {
+                     const Strides& x, int box_heads = 1, int box_rows = 128) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)(rows > 0 ? rows : 1)};
   cuuint64_t strides[2] = {(cuuint64_t)x.h * 2, (cuuint64_t)x.r * 2};
-  cuuint32_t box[3] = {64, 1, 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -524,14 +624,16 @@ static int launch_typed(const attn_fwd_params& p, const FwdLayout& L, cudaStream
   const bool fp16 = IsHalf<T>::value;
   const long long rq = group ? p.total_q : (long long)p.batch * p.seqlen_q;
   const long long rk = group ? p.total_k : (long long)p.batch * p.seqlen_k;
+  const int g = p.nhead_q / p.nhead_kv, tok = seg ? FM / g : 0;
+  if (seg && (tok < 1 || seg->nsplit < 1 || seg->nsplit > MAX_SPLITS)) return ATTN_ERR_INVALID_ARG;
   Maps maps;
-  if (!make_map(&maps.q, p.q, fp16, DQK, p.nhead_q, rq, L.q) || !make_map(&maps.k, p.k, fp16, DQK, p.nhead_kv, rk, L.k) ||
+  if (!make_map(&maps.q, p.q, fp16, DQK, p.nhead_q, rq, L.q, seg ? g : 1, seg ? tok : FM) || !make_map(&maps.k, p.k, fp16, DQK, p.nhead_kv, rk, L.k) ||
       !make_map(&maps.v, p.v, fp16, DV, p.nhead_kv, rk, L.v))
     return ATTN_ERR_CUDA;
   Args a;
   a.group = group ? 1 : 0;
   a.hq = p.nhead_q;
-  a.g = p.nhead_q / p.nhead_kv;
+  a.g = g;
   a.sq = p.seqlen_q;
   a.sk = p.seqlen_k;
   a.cu_q = seg ? seg->zeros : p.cu_seqlens_q;
@@ -548,14 +650,27 @@ static int launch_typed(const attn_fwd_params& p, const FwdLayout& L, cudaStream
   a.so = L.o;
   a.lse = p.lse;
   a.tq = group ? p.total_q : 0;
-  const int ntq = cdiv(p.seqlen_q > 0 ? p.seqlen_q : 1, FM);
-  auto kern = fwd_tc_kernel<DQK, DV, T>;
+  a.tok = tok;
+  a.nsplit = seg ? seg->nsplit : 1;
+  a.part_o = seg ? seg->part_o : nullptr;
+  a.part_ml = seg ? seg->part_ml : nullptr;
+  const int ntq = cdiv(p.seqlen_q > 0 ? p.seqlen_q : 1, seg ? tok : FM);
+  auto kern = seg ? fwd_tc_kernel<DQK, DV, T, true> : fwd_tc_kernel<DQK, DV, T, false>;
   // more than half the shared memory, so that two CTAs (each holding all
   // TMEM columns) never share an SM
   const int smem = C::SMEM_BYTES > 120 * 1024 ? C::SMEM_BYTES : 120 * 1024;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return ATTN_ERR_CUDA;
-  kern<<<dim3(ntq, p.nhead_q, p.batch), NTHREADS, smem, st>>>(maps, a);
+  if (seg) {
+    kern<<<dim3(ntq * a.nsplit, p.nhead_kv, p.batch), NTHREADS, smem, st>>>(maps, a);
+    if (a.nsplit > 1) {
+      const long long rows = (long long)p.seqlen_q * g, heads = (long long)p.nhead_kv * p.batch;
+      const long long each = heads < JOIN_GRID ? JOIN_GRID / heads : 1, need = cdiv_ll(rows, JOIN_WARPS);
+      join_parts_kernel<DV, T><<<dim3((unsigned)(need < each ? need : each), p.nhead_kv, p.batch), 32 * JOIN_WARPS, 0, st>>>(a);
+    }
+  } else {
+    kern<<<dim3(ntq, p.nhead_q, p.batch), NTHREADS, smem, st>>>(maps, a);
+  }
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -90,7 +90,8 @@ struct KvLong {
   int slots;              // most of them that q can hold; 0: the path is not used
   int group, groups;      // slots whose keys are expanded at a time, and times
   long long kpad;         // rows of a slot's keys and values
-  size_t off_list, off_k, off_v, total;   // workspace; total is 0 without slots
+  int nsplit;             // CTAs that a query tile's keys are split over at most
+  size_t off_list, off_k, off_v, off_po, off_pml, total;   // workspace; total is 0 without slots
 };
 KvLong kv_long_layout(const attn_kv_fwd_params& p, int max_k);
 int launch_kv_long(const attn_kv_fwd_params& p, const KvCacheView& c, const Strides& sq, const Strides& so, int max_k,

@@ -77,7 +77,8 @@ constexpr int MIN_TILES = 12;
 // Up to eight splits in a grid of one wave are joined as clusters: no second
 // launch, 8.5 us against 9.2 in that last case.  Not in larger grids, where the
 // CTAs of a cluster hold their SMs for its slowest (158 us against 108 for the 64
-// requests).
+// requests), nor where the clusters that fit next to each other are fewer than the
+// jobs (54 of eight splits, three CTAs per SM: 16.8 us, 10.6 without).
 constexpr int MAX_CLUSTER = 8;
 constexpr int EV_SLACK = 4;         // V scales within 2^4 of the accumulator's unit go on P
 constexpr float P_LOG2 = 4.f;       // P = 2^4 at the running maximum
@@ -897,7 +898,8 @@ static Layout layout(const attn_kv_fwd_params& p) {
   L.min_tiles = few ? MIN_TILES : EVEN_TILES;
   const long long n = few ? (p.batch > 1 ? wave : HALF_WAVE) / L.jobs : cdiv_ll(MAX_GRID, L.jobs);
   L.nsplit = n < cdiv(tiles, L.min_tiles) ? (int)n : cdiv(tiles, L.min_tiles);
-  L.cluster = few && L.nsplit > 1 && L.nsplit <= MAX_CLUSTER;
+  // clusters of one wave: a cluster stays within eighteen SMs or so
+  L.cluster = few && L.nsplit > 1 && L.nsplit <= MAX_CLUSTER && L.jobs <= 8 * (wave * 18 / 152 / L.nsplit);
   auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
   size_t o = 0;
   L.off_status = o;

@@ -8,8 +8,17 @@
 // The expansion reads each cache byte once and writes two; the forward reads
 // them back.
 //
+// The forward's query tiles hold tokens x heads of a group, so that a short
+// segment fills its 128 rows (34 tokens of 8 heads: 3 tiles instead of 8;
+// 4 prompt pieces of 1,024 tokens of 4 heads, whose causal edge is then only
+// 32 tokens wide: 333 to 325 us), and where the tiles leave SMs idle their keys are
+// split over CTAs (109 tokens over 5,841 keys, 4 kv heads, 3 requests: 37.7 us in
+// all, 59.3 with one CTA per tile).
+//
 // The segments are found on the device: a setup kernel lists them in slots, so
 // one call may mix long segments with the short ones of kv_fwd.cu.
+#include <cmath>
+
 #include "common.cuh"
 #include "kv_common.cuh"
 
@@ -18,19 +27,54 @@ namespace kvlong {
 
 constexpr int PAD = 128;                        // keys of a tile of the forward
 constexpr size_t EXPANDED_BYTES = size_t(1) << 30;   // expanded keys and values at a time (a slot at least)
+constexpr int MAX_SPLITS = 16;
 constexpr int NTHREADS = 256;
-constexpr int SETUP_THREADS = 1024;
+constexpr int SETUP_THREADS = 256;
 
-// Query tokens from which a segment is long.  The other path's time grows with
+// Query tokens above which a segment is long.  The other path's time grows with
 // tokens x group (rows of 16 that each pass over the cache), this one's hardly
-// up to 128 tokens.  Device time in us, this path / the other, of batch x kv
-// heads x group over 4,096 cached tokens:
-//   4 x 8 x 4:  17 tokens 57 / 49,  33: 58 / 52,  49: 58 / 93,  129:  93 / 241
-//   8 x 4 x 8:  17 tokens 88 / 53,  33: 89 / 106, 49: 89 / 162, 129: 124 / 388
-//   4 x 8 x 1:  49 tokens 58 / 42,  97: 58 / 52, 129: 60 / 80
-//   1 x 8 x 4:  49 tokens 46 / 41,  65: 46 / 43,  97: 46 / 52
-// (600 and 16,384 cached tokens cross at about the same places).
-static int long_from(int group) { return 24 + 96 / group; }
+// up to 128 rows, but it starts some 17 us later.  Per row and cached token of a
+// kv head of 128 + 128 columns the other takes about 3.5 ps, this one per cached
+// token what the other takes for some 72 rows.  Device time in us, this path / the
+// other, of batch x kv heads x group, up to so many cached tokens:
+//   4 x 8 x 4,  4,096:  17 tokens  47 /  42,  33:  59 /  60,  49:  55 /  82,  97:  59 / 157
+//   8 x 4 x 8,  4,096:   9 tokens  42 /  41,  17:  52 /  57,  33:  51 /  85,  97:  72 / 231
+//   4 x 8 x 1,  4,096:  33 tokens  45 /  26,  49:  45 /  32,  97:  45 /  43
+//   1 x 8 x 4,  4,096:  33 tokens  36 /  25,  49:  36 /  41,  97:  34 /  71
+//   1 x 8 x 4, 32,768:   9 tokens  90 /  51,  17:  91 /  93,  33:  92 / 136,  97: 108 / 510
+//   4 x 2 x 4,  1,000:  33 tokens  27 /  13,  97:  28 /  18
+// The bounds keep the rule (and with it the rounding of the weights) within sight
+// of the tokens: 24 at least, 24 + 96 / group at most.
+static int long_from(const attn_kv_fwd_params& p, int max_k) {
+  const attn_kv_cache& c = p.cache;
+  const int group = p.nhead_q / c.nhead_kv;
+  const long long segments = p.total_q / 32 + 1 < p.batch ? p.total_q / 32 + 1 : p.batch;
+  double keys = max_k;
+  if (p.mask == ATTN_MASK_WINDOW && p.window_left >= 0 && p.window_right >= 0)
+    keys = std::fmin(keys, (double)p.window_left + p.window_right + 64);
+  const double work = segments * c.nhead_kv * std::fmax(keys, 1.) * (c.d_qk + c.d_v) / 256.;
+  const double tokens = (72 + 17e-6 / 3.5e-12 / work) / group;
+  return (int)std::fmin(std::fmax(tokens, 24.), 24 + 96 / group);
+}
+
+// Splits of a query tile's keys: the number whose waves over the SMs take the
+// least time, where the tiles alone (at most: q can hold no more) would not fill
+// them once.
+static int splits(const attn_kv_fwd_params& p, const KvLong& L, int tok) {
+  const long long by_rows = p.total_q / tok + L.slots, by_slots = (long long)L.group * cdiv(p.max_seqlen_q, tok);
+  const long long ctas = p.cache.nhead_kv * (by_rows < by_slots ? by_rows : by_slots);
+  if (ctas >= 152) return 1;
+  int best = 1;
+  float least = 0.85f;   // a split has to gain more than the join costs
+  for (int n = 2; n <= MAX_SPLITS && (n - 1) * FWD_MIN_SPLIT * FWD_TILE_ROWS < L.kpad; ++n) {
+    const float cost = (float)cdiv_ll(ctas * n, 152) / n + 0.02f * n;
+    if (cost < least) {
+      least = cost;
+      best = n;
+    }
+  }
+  return best;
+}
 
 // Per slot; every array has `slots` entries.
 struct Lists {
@@ -130,17 +174,21 @@ __device__ __forceinline__ void expand16(const uint4& x, float f, uint4* dst) {
 }
 
 // Rows [16 blockIdx.x, + 16) of a slot's keys and values (blockIdx.y: the slot
-// of the group); rows past the length, up to a tile of the forward, become 0.
-// A page outside the cache empties the segment's keys.
+// of the group), of the forward's tiles that the segment sees; rows that it does
+// not see become 0, whatever they or their pages hold.  A page outside the cache empties the segment's keys.
 template <typename T>
 __global__ void __launch_bounds__(NTHREADS)
     expand_kernel(const Lists L, int slot0, const KvCacheView c, int dqk, int dv, const int* table,
-                  long long table_stride, T* k16, T* v16, long long kpad) {
+                  long long table_stride, T* k16, T* v16, long long kpad, int mask, int left, int right) {
   const int slot = slot0 + blockIdx.y;
-  const int lk = L.len_k[slot], row0 = blockIdx.x * 16;
-  if (row0 >= (lk + PAD - 1) / PAD * PAD) return;
+  const int lk = L.len_k[slot], lq = L.len_q[slot], row0 = blockIdx.x * 16;
+  const MaskArgs m = mask_args(mask, left, right, lq, lk);
+  const int klo = m.left >= 0 ? max(0, m.off - m.left) : 0;
+  const int khi = m.right >= 0 ? min(lk - 1, lq - 1 + m.off + m.right) : lk - 1;
+  if (row0 < klo / PAD * PAD || khi < 0 || row0 >= (khi / PAD + 1) * PAD) return;
+  const bool any = row0 + 16 > klo && row0 <= khi;   // 16 rows lie in one page
   int page = 0;
-  if (row0 < lk) {
+  if (any) {
     page = __ldg(table + L.request[slot] * table_stride + (row0 >> c.page_shift));
     if (page < 0 || page >= c.num_pages) {
       if (threadIdx.x == 0) {
@@ -153,14 +201,14 @@ __global__ void __launch_bounds__(NTHREADS)
   const int in0 = row0 & ((1 << c.page_shift) - 1);
   const int pk = dqk / 16, pv = dv / 16, per = pk + pv;    // 16-byte pieces of a head's row, K then V
   const long long out0 = (long long)blockIdx.y * kpad + row0;
-  for (int i = threadIdx.x; i < 16 * c.hkv * per; i += NTHREADS) {
+  for (int i = blockIdx.z * NTHREADS + threadIdx.x; i < 16 * c.hkv * per; i += NTHREADS * gridDim.z) {
     const int r = i / (c.hkv * per), x = i - r * (c.hkv * per);
     const bool is_v = x >= c.hkv * pk;
     const int y = is_v ? x - c.hkv * pk : x, n = is_v ? pv : pk;
     const int h = y / n, p = y - h * n;
     uint4 raw = make_uint4(0, 0, 0, 0);
     float f = 1.f;
-    if (row0 + r < lk) {
+    if (any && row0 + r >= klo && row0 + r <= khi) {
       const KvStrides& s = is_v ? c.sv : c.sk;
       raw = __ldg(reinterpret_cast<const uint4*>((is_v ? c.v : c.k) + page * s.p + (in0 + r) * s.r + h * s.h + p * 16));
       f = exp2_int(kv_exp_of(__ldg((is_v ? c.v_exp : c.k_exp) + (long long)page * c.hkv + h)));
@@ -190,9 +238,9 @@ static int launch(const attn_kv_fwd_params& p, const KvCacheView& c, const Strid
   f.d_v = p.cache.d_v;
   f.mask = p.mask;
   // a bound that no key is beyond is none (and keeps the forward's sums in 32 bits)
-  const long long far = (long long)p.max_seqlen_q + max_k;
-  f.window_left = p.window_left >= far ? -1 : p.window_left;
-  f.window_right = p.window_right >= far ? -1 : p.window_right;
+  f.window_left = p.window_left >= max_k ? -1 : p.window_left;
+  f.window_right = p.window_right >= p.max_seqlen_q || p.window_right >= p.total_q ? -1 : p.window_right;
+  const int left = p.mask == ATTN_MASK_WINDOW ? f.window_left : -1, right = p.mask == ATTN_MASK_WINDOW ? f.window_right : -1;
   f.softmax_scale = p.softmax_scale;
   f.q = p.q;
   f.k = k16;
@@ -207,12 +255,19 @@ static int launch(const attn_kv_fwd_params& p, const KvCacheView& c, const Strid
   lay.hq0 = p.nhead_q;
   for (int g = 0; g < L.groups; ++g) {
     const int s0 = g * L.group, n = s0 + L.group <= L.slots ? L.group : L.slots - s0;
+    // few rows: their pieces over more CTAs (3 segments of 600
+    // tokens, 8 heads: 6.0 us against 9.7)
+    const long long ctas = L.kpad / 16 * n;
+    const int rounds = cdiv(16 * f.nhead_kv * (f.d_qk + f.d_v) / 16, NTHREADS);
+    const int share = ctas >= 1216 ? 1 : (int)(1216 / ctas < rounds ? 1216 / ctas : rounds);
     if (max_k > 0)
-      expand_kernel<T><<<dim3((unsigned)(L.kpad / 16), n), NTHREADS, 0, st>>>(T_, s0, c, f.d_qk, f.d_v, p.block_table,
-                                                                             p.table_stride, k16, v16, L.kpad);
+      expand_kernel<T><<<dim3((unsigned)(L.kpad / 16), n, share), NTHREADS, 0, st>>>(T_, s0, c, f.d_qk, f.d_v, p.block_table,
+                                                                             p.table_stride, k16, v16, L.kpad, f.mask,
+                                                                             left, right);
     f.batch = n;
     f.total_k = (int)(n * L.kpad);
-    const FwdSegments seg{T_.zeros + s0, T_.len_q + s0, T_.start_q + s0, T_.len_k + s0, T_.start_k + s0};
+    const FwdSegments seg{T_.zeros + s0, T_.len_q + s0, T_.start_q + s0, T_.len_k + s0, T_.start_k + s0, L.nsplit,
+                          reinterpret_cast<float*>(ws + L.off_po), reinterpret_cast<float2*>(ws + L.off_pml)};
     const int r = launch_fwd_tc(f, lay, st, &seg);
     if (r != ATTN_OK) return r;
   }
@@ -225,8 +280,9 @@ KvLong kv_long_layout(const attn_kv_fwd_params& p, int max_k) {
   KvLong L{};
   L.from = 0x7fffffff;
   const attn_kv_cache& c = p.cache;
-  const bool built = c.d_qk <= 192 && p.softmax_scale > 0.f && p.nhead_q <= 65535;
-  const int from = kvlong::long_from(p.nhead_q / c.nhead_kv);
+  const int group = p.nhead_q / c.nhead_kv;
+  const bool built = c.d_qk <= 192 && p.softmax_scale > 0.f && group <= FWD_TILE_ROWS;
+  const int from = kvlong::long_from(p, max_k);
   if (!built || p.max_seqlen_q <= from) return L;
   L.from = from;
   // segments of more than `from` rows that do not overlap
@@ -240,6 +296,7 @@ KvLong kv_long_layout(const attn_kv_fwd_params& p, int max_k) {
   g = g * L.kpad > (1LL << 30) ? (1LL << 30) / L.kpad : g;   // rows stay 32-bit coordinates
   L.group = (int)(g < 1 ? 1 : g > 65535 ? 65535 : g);
   L.groups = cdiv(L.slots, L.group);
+  L.nsplit = kvlong::splits(p, L, FWD_TILE_ROWS / group);
   auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
   size_t o = 0;
   L.off_list = o;
@@ -248,6 +305,11 @@ KvLong kv_long_layout(const attn_kv_fwd_params& p, int max_k) {
   o = up(o + (size_t)L.group * L.kpad * c.nhead_kv * c.d_qk * 2);
   L.off_v = o;
   o = up(o + (size_t)L.group * L.kpad * c.nhead_kv * c.d_v * 2);
+  const size_t parts = L.nsplit > 1 ? (size_t)L.nsplit * p.total_q * p.nhead_q : 0;
+  L.off_po = o;
+  o = up(o + parts * c.d_v * sizeof(float));
+  L.off_pml = o;
+  o = up(o + parts * sizeof(float2));
   L.total = o;
   return L;
 }

@@ -563,13 +563,15 @@ int attn_kv_append(const attn_kv_append_params* p, cudaStream_t stream);
  * Lengths and pages are checked on the device: a segment outside q counts as
  * empty, seqlens_k is limited to 0 .. min(max_seqlen_k, max_blocks pages), the
  * tokens of a page outside the cache are masked (in a long segment, below, all
- * tokens are), and attn_kv_fwd_read_status reports it.  Cache rows past
- * seqlens_k (or, for single-token segments, outside the mask) never reach a
- * result, whatever they hold; other masked values must be finite.
- * Segments of more than 24 + 96 / (nhead_q / nhead_kv) query tokens (d_qk below
- * 256, positive softmax_scale) are long: their keys and values are expanded to
- * the type of q in the workspace and attn_fwd's tensor-core kernel runs on
- * them, its softmax weights rounded to that type (with FP16, cache values past
+ * tokens are), and attn_kv_fwd_read_status reports it.  Cache rows that no
+ * query of a segment sees (past seqlens_k, outside the window) never reach a
+ * result, whatever they hold, and a page of such rows alone is not looked up:
+ * its block_table entry may be anything.  Other masked values must be finite.
+ * Segments of more than 24 + 96 / G query tokens (G = nhead_q / nhead_kv <= 128,
+ * d_qk below 256, positive softmax_scale), where there is much to do (many kv
+ * heads, a large max_seqlen_k) of fewer, but more than 24, are long: their keys
+ * and values are expanded to the type of q in the workspace and attn_fwd's
+ * tensor-core kernel runs on them, its softmax weights rounded to that type (with FP16, cache values past
  * 65504 are clamped to it); other weights are rounded to 11 bits.  One call may
  * mix both kinds.  Long segments must not overlap one another in q. */
 typedef struct {

@@ -472,6 +472,44 @@ def test_attend_long_segments_in_groups(B):
     check_attend(o, lse, ref, torch.bfloat16, d, 333, torch.bfloat16)
 
 
+SPLIT = [
+    # page, lens, new, heads (kv, per kv), mask, left, right: few query tiles over
+    # thousands of keys, so that CTAs share a tile's keys
+    (16, [5000], [130], 1, 1, 2, -1, -1),
+    (64, [4100, 300, 2200], [64, 130, 1], 1, 3, 2, -1, -1),     # groups that do not divide 128, one tile unsplit
+    (32, [3000, 2100], [121, 50], 2, 5, 0, -1, -1),
+    (16, [2500, 5000], [90, 600], 1, 2, 3, 1500, 40),           # windows that end inside the splits
+    (16, [4000], [200], 1, 4, 1, -1, -1),                       # top-left: one tile of keys
+    (128, [2600, 100], [2600, 140], 1, 1, 2, -1, -1),           # from one key tile to all of them
+    (16, [3000], [30], 1, 64, 2, -1, -1),
+    (16, [2200], [26], 1, 128, 2, -1, -1),                      # one token fills a tile
+    (16, [2200], [26], 1, 129, 2, -1, -1),                      # more heads than a tile: never long
+]
+
+
+@pytest.mark.parametrize("dqk,dv,dtype", [(64, 64, torch.float16), (128, 128, torch.bfloat16), (192, 128, torch.bfloat16)])
+@pytest.mark.parametrize("page,lens,new,hkv,group,mask,left,right", SPLIT)
+def test_attend_long_segments_split(B, dqk, dv, dtype, page, lens, new, hkv, group, mask, left, right):
+    """Also the same bits when run again, and NaN in the cache rows that no query
+    sees, whose pages are not looked up."""
+    q, table, kc, vc, ke, ve, cu = attend_case(dqk, dv, dtype, page, lens, new, hkv, group)
+    ref = kv_ref.attend(q, cu, lens, table, kc, vc, ke, ve, 0.1, mask, left, right)
+    for b, n in enumerate(lens):
+        seen = [(max(0, n - new[b] - left), n) if mask == 3 else (0, min(n, new[b])) if mask == 1 else (0, n)][0]
+        for i in range((n + page - 1) // page):
+            rows = [r for r in range(page) if not seen[0] <= i * page + r < seen[1]]
+            if rows:
+                kc[table[b][i], rows], vc[table[b][i], rows] = 127, 255
+            if len(rows) == page:
+                table[b][i] = -7
+    args = (q.cuda(), handle(B, kc, vc, ke, ve), dev(table), dev(lens), dev(cu))
+    kw = dict(scale=0.1, mask=mask, left=left, right=right, max_seqlen_q=max(new), max_seqlen_k=max(lens))
+    o, lse = B.attn_kv_forward(*args, check_status=True, **kw)
+    check_attend(o, lse, ref, dtype, dqk, max(lens), weights(dtype, max(new)), what=f"{page} {lens} {new}")
+    again = B.attn_kv_forward(*args, **kw)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
 def test_attend_long_segments_overlapping(B):
     """Padded starts that make long segments overlap: reported, nothing outside
     the declared rows touched."""
