@@ -511,25 +511,32 @@ def rope(q, k, positions, inv_freq, *, pair_axis=None, interleaved=False, invers
     return qo, ko
 
 
-class KvCache:
+class _KvCacheFields(NamedTuple):
+    k: torch.Tensor
+    v: torch.Tensor
+    k_exp: torch.Tensor
+    v_exp: torch.Tensor
+    packed: bytes
+    index: int
+    num_pages: int
+    page_size: int
+    nhead_kv: int
+    d_qk: int
+    d_v: int
+
+
+class KvCache(_KvCacheFields):
     """Handle of a paged 8-bit cache (attn_kv_cache): k [pages, page_size,
     kv heads, d_qk] and v [..., d_v] as torch.float8_e4m3fn (or uint8), any
     strides with a contiguous head dimension, and the scale exponents k_exp,
     v_exp uint8 [pages, kv heads].  It keeps the tensors and their packed
-    description; make it once per cache."""
+    description, and stays with them: its attributes cannot be replaced."""
 
-    __slots__ = ("k", "v", "k_exp", "v_exp", "num_pages", "page_size", "nhead_kv", "d_qk", "d_v", "index", "packed")
+    __slots__ = ()
+    __eq__, __ne__, __hash__ = object.__eq__, object.__ne__, object.__hash__
 
-    def __init__(self, k, v, k_exp, v_exp):
-        (self.packed, self.index, self.num_pages, self.page_size, self.nhead_kv, self.d_qk,
-         self.d_v) = (_marshal or _load_marshal()).cache(k, v, k_exp, v_exp)
-        self.k, self.v, self.k_exp = k, v, k_exp
-        self.v_exp = v_exp
-
-    def __setattr__(self, name, value):
-        if hasattr(self, "v_exp"):   # the last one to be set
-            raise AttributeError("a KvCache describes the tensors it was made from; make another for others")
-        object.__setattr__(self, name, value)
+    def __new__(cls, k, v, k_exp, v_exp):
+        return tuple.__new__(cls, (k, v, k_exp, v_exp) + (_marshal or _load_marshal()).cache(k, v, k_exp, v_exp))
 
     @classmethod
     def empty(cls, num_pages, page_size, nhead_kv, d_qk, d_v, device="cuda"):
