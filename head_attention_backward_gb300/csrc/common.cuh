@@ -402,8 +402,11 @@ struct FwdSegments {
   const int* len_k;
   const int* start_k;
   int nsplit;              // most splits of a tile's keys
-  float* part_o;           // [nsplit][total_q][nhead_q][d_v], used where nsplit > 1
-  float2* part_ml;         // [nsplit][total_q][nhead_q]: running maximum (log2 units) and sum
+  // where nsplit > 1: per split and part row, which is a row of q, or where slot_rows
+  // is not 0 token + slot_rows x segment
+  long long part_rows, slot_rows;
+  float* part_o;           // [nsplit][part_rows][nhead_q][d_v]
+  float2* part_ml;         // [nsplit][part_rows][nhead_q]: running maximum (log2 units) and sum
 };
 constexpr int FWD_TILE_ROWS = 128;   // query rows of a tile of the tensor-core forward, and keys
 constexpr int FWD_MIN_SPLIT = 8;     // key tiles of a split at least

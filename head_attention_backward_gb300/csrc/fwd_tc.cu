@@ -116,9 +116,15 @@ struct Args {
   // packed segments only
   int tok;                 // query tokens of a tile, each with the g heads of its group
   int nsplit;
+  long long part_rows, slot_rows;
   float* part_o;
   float2* part_ml;
 };
+
+// Part row of token i of segment b (whose tokens start at row q0) and of a head.
+__device__ __forceinline__ long long part_row(const Args& A, int b, int q0, int i, int h) {
+  return ((A.slot_rows ? A.slot_rows * b : q0) + i) * A.hq + h;
+}
 
 // Packed segments: the key tiles of query tokens [qs, qe], and what split `split`
 // of them takes.
@@ -482,7 +488,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fwd_tc_kernel(const __grid_consta
     const long long li = A.group ? (long long)hr * A.tq + q0 + qi : ((long long)b * A.hq + hr) * A.sq + qi;
     T* orow = static_cast<T*>(A.o) + elem_off(A.so, (long long)q0 + qi, hr) + half * OC;
     // a part: O and the sum as they are, fp32
-    const long long part = PACKED ? ((long long)split * A.tq + q0 + qi) * A.hq + hr : 0;
+    const long long part = PACKED ? split * A.part_rows * A.hq + part_row(A, b, q0, qi, hr) : 0;
     const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
     for (int c = 0; c < OC / 32; ++c) {
@@ -545,14 +551,14 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_parts_kernel(const Args 
   const int hk = blockIdx.y, b = blockIdx.z;
   const int lq = __ldg(A.cu_q_end + b), lk = __ldg(A.cu_k_end + b), q0 = __ldg(A.st_q + b);
   const MaskArgs m = mask_args(A.mask, A.left, A.right, lq, lk);
-  const long long step = (long long)A.tq * A.hq;   // rows of a split
+  const long long step = A.part_rows * A.hq;
   for (long long i = (long long)blockIdx.x * JOIN_WARPS + warp; i < (long long)lq * A.g;
        i += (long long)gridDim.x * JOIN_WARPS) {
     const int tk = (int)(i / A.g), h = hk * A.g + (int)(i - (long long)tk * A.g);
     const int qs = tk / A.tok * A.tok;
     const int n = key_tiles(m, lk, qs, min(qs + A.tok, lq) - 1, A.nsplit, 0).splits;
     if (n <= 1) continue;
-    const long long row = (long long)(q0 + tk) * A.hq + h;
+    const long long row = part_row(A, b, q0, tk, h);
     const float2 ml = lane < n ? A.part_ml[row + lane * step] : make_float2(-INFINITY, 0.f);
     float top = ml.x;
 #pragma unroll
@@ -652,6 +658,8 @@ static int launch_typed(const attn_fwd_params& p, const FwdLayout& L, cudaStream
   a.tq = group ? p.total_q : 0;
   a.tok = tok;
   a.nsplit = seg ? seg->nsplit : 1;
+  a.part_rows = seg ? seg->part_rows : 0;
+  a.slot_rows = seg ? seg->slot_rows : 0;
   a.part_o = seg ? seg->part_o : nullptr;
   a.part_ml = seg ? seg->part_ml : nullptr;
   const int ntq = cdiv(p.seqlen_q > 0 ? p.seqlen_q : 1, seg ? tok : FM);

@@ -91,6 +91,7 @@ struct KvLong {
   int group, groups;      // slots whose keys are expanded at a time, and times
   long long kpad;         // rows of a slot's keys and values
   int nsplit;             // CTAs that a query tile's keys are split over at most
+  long long part_rows, slot_rows;   // of their parts: see FwdSegments
   size_t off_list, off_k, off_v, off_po, off_pml, total;   // workspace; total is 0 without slots
 };
 KvLong kv_long_layout(const attn_kv_fwd_params& p, int max_k);

@@ -231,7 +231,7 @@ static int launch(const attn_kv_fwd_params& p, const KvCacheView& c, const Strid
   f.dtype = p.dtype;
   f.nhead_q = p.nhead_q;
   f.nhead_kv = p.cache.nhead_kv;
-  f.seqlen_q = p.max_seqlen_q;
+  f.seqlen_q = p.max_seqlen_q < p.total_q ? p.max_seqlen_q : p.total_q;
   f.seqlen_k = max_k;
   f.total_q = p.total_q;
   f.d_qk = p.cache.d_qk;
@@ -267,7 +267,7 @@ static int launch(const attn_kv_fwd_params& p, const KvCacheView& c, const Strid
     f.batch = n;
     f.total_k = (int)(n * L.kpad);
     const FwdSegments seg{T_.zeros + s0, T_.len_q + s0, T_.start_q + s0, T_.len_k + s0, T_.start_k + s0, L.nsplit,
-                          reinterpret_cast<float*>(ws + L.off_po), reinterpret_cast<float2*>(ws + L.off_pml)};
+                          L.part_rows, L.slot_rows, reinterpret_cast<float*>(ws + L.off_po), reinterpret_cast<float2*>(ws + L.off_pml)};
     const int r = launch_fwd_tc(f, lay, st, &seg);
     if (r != ATTN_OK) return r;
   }
@@ -305,7 +305,10 @@ KvLong kv_long_layout(const attn_kv_fwd_params& p, int max_k) {
   o = up(o + (size_t)L.group * L.kpad * c.nhead_kv * c.d_qk * 2);
   L.off_v = o;
   o = up(o + (size_t)L.group * L.kpad * c.nhead_kv * c.d_v * 2);
-  const size_t parts = L.nsplit > 1 ? (size_t)L.nsplit * p.total_q * p.nhead_q : 0;
+  L.slot_rows = p.max_seqlen_q < p.total_q ? p.max_seqlen_q : p.total_q;
+  if (L.slot_rows * L.group >= p.total_q) L.slot_rows = 0;
+  L.part_rows = L.slot_rows ? L.slot_rows * L.group : p.total_q;
+  const size_t parts = L.nsplit > 1 ? (size_t)L.nsplit * L.part_rows * p.nhead_q : 0;
   L.off_po = o;
   o = up(o + parts * c.d_v * sizeof(float));
   L.off_pml = o;

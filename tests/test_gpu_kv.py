@@ -510,6 +510,31 @@ def test_attend_long_segments_split(B, dqk, dv, dtype, page, lens, new, hkv, gro
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
 
 
+def test_attend_long_segments_in_a_wide_buffer(B):
+    """Split long segments in a q of far more rows than they have: the parts
+    follow the segments, not the buffer."""
+    lens, new, d, total = [3000, 2600, 40], [60, 130, 3], 64, 40000
+    q, table, kc, vc, ke, ve, cu = attend_case(d, d, torch.bfloat16, 16, lens, new, 1, 2)
+    starts = [39000, 20, 30000, 39900]
+    wide, out = (torch.zeros((total, 2, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lse = torch.full((2, total), 9.0, device="cuda")
+    rows = [starts[b] + i for b in range(3) for i in range(new[b])]
+    wide[rows] = q.cuda()
+    p = B.AttnKvFwdParams(dtype=B.ATTN_BF16, batch=3, nhead_q=2, total_q=total, max_seqlen_q=130, max_seqlen_k=3000,
+                          max_blocks=len(table[0]), mask=2, softmax_scale=0.1,
+                          cache=B.AttnKvCache(num_pages=400, page_size=16, nhead_kv=1, d_qk=d, d_v=d))
+    st, size = B.attn_kv_fwd_workspace_size(p)
+    assert st == 0 and size < 32 << 20
+    B.attn_kv_forward(wide, handle(B, kc, vc, ke, ve), dev(table), dev(lens), dev(cu), scale=0.1, max_seqlen_q=130,
+                      max_seqlen_k=3000, cu_seqlens_q_padded=dev(starts), out=(out, lse), check_status=True,
+                      workspace=torch.empty(size, dtype=torch.uint8, device="cuda"))
+    ref = kv_ref.attend(q, cu, lens, table, kc, vc, ke, ve, 0.1, 2)
+    check_attend(out[rows], lse[:, rows], ref, torch.bfloat16, d, 3000, torch.bfloat16)
+    others = torch.ones(total, dtype=torch.bool)
+    others[rows] = False
+    assert bool((out[others.cuda()] == 0).all()) and bool((lse[:, others.cuda()] == 9).all())
+
+
 def test_attend_long_segments_overlapping(B):
     """Padded starts that make long segments overlap: reported, nothing outside
     the declared rows touched."""
