@@ -119,12 +119,13 @@ struct Args {
   const int* table;
   long long table_stride;
   int max_k;             // min(max_seqlen_k, max_blocks pages)
-  int total_q, max_q;
+  int total_q, max_q, batch;
   int long_from;         // segments of more tokens are left to the long path
   int hq, g;             // query heads, per kv head
   int mask, left, right;
   float scale_log2;
-  int nsplit, min_tiles, mtiles;   // most splits of a job, least tiles of one; most row tiles of a request
+  int nsplit, min_tiles, mtiles;   // most splits of a job, least tiles of one; most row tiles of a request: see slot_of
+  int direct;            // 1: slots are request x row tile
   int cluster;           // 1: the splits of a job are a cluster
   int job_rows;          // most rows that a row tile can have
   float* part_o;         // [job][nsplit][job_rows][DV]
@@ -169,6 +170,40 @@ __device__ __forceinline__ Job make_job(const Args& A, int b, int m, MaskArgs& m
   j.kbeg = j.klo & ~(TILE - 1);
   j.ntile = j.khi >= j.klo ? (j.khi - j.kbeg) / TILE + 1 : 0;
   return j;
+}
+
+// Request and row tile of a slot.  Where requests may have many more row tiles than
+// q has rows, the grid follows the packed rows (64 single tokens of 4 heads per kv
+// head under a max_seqlen_q of 32: 640 jobs, not 4,096; 132 us, not 181): request
+// b's tiles start at slot cu_q[b] g / ROWS + b, which leaves room for them.  A warp
+// searches 32 requests at a time.
+struct Slot {
+  int b, m;
+};
+template <int ROWS>
+__device__ __forceinline__ Slot slot_of(const Args& A, int slot) {
+  if (A.direct) return {slot / A.mtiles, slot % A.mtiles};
+  const int lane = threadIdx.x & 31;
+  const long long c0 = __ldg(A.cu_q);
+  auto first = [&](int i) { return (__ldg(A.cu_q + i) - c0) * A.g / ROWS + i; };
+  int lo = 0, hi = A.batch;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step;
+    const uint32_t at = __ballot_sync(0xffffffffu, i < hi && first(i) <= slot);
+    const int n = at == 0xffffffffu ? 32 : __ffs(~at) - 1;   // probes up to the first beyond the slot
+    hi = min(hi, lo + (n + 1) * step);
+    lo += n * step;
+  }
+  const long long m = slot - first(lo);
+  return {lo, m >= 0 && m < (1 << 26) ? (int)m : 1 << 26};   // past any row
+}
+// Whether a request's lengths are wrong that no slot may lead to: a search over
+// offsets that go back misses some.
+template <int ROWS>
+__device__ __forceinline__ bool misses(const Args& A, int slot) {
+  MaskArgs mk;
+  return !A.direct && slot < A.batch &&
+         (make_job<ROWS>(A, slot, 0, mk).bad || (long long)__ldg(A.cu_q + A.batch) - __ldg(A.cu_q) > A.total_q);
 }
 
 // Tiles of a job's splits: equal shares, whole turns of the warps.
@@ -329,15 +364,14 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
 
-  // block -> (request, kv head, row tile, split)
-  int x = blockIdx.x;
-  const int split = x % A.nsplit;
-  x /= A.nsplit;
-  const int m = x % A.mtiles;
-  x /= A.mtiles;
-  const int hk = x % A.c.hkv, b = x / A.c.hkv;
+  // block -> (slot, kv head, split) -> (request, row tile)
+  const int job = blockIdx.x / A.nsplit, split = blockIdx.x - job * A.nsplit;
+  const int slot = job / A.c.hkv, hk = job - slot * A.c.hkv;
+  const Slot at = slot_of<ROWS>(A, slot);
+  const int b = at.b;
   MaskArgs mk;
-  const Job J = make_job<ROWS>(A, b, m, mk);
+  Job J = make_job<ROWS>(A, b, at.m, mk);
+  if (split == 0 && hk == 0 && misses<ROWS>(A, slot)) J.bad = true;   // reported
   const int per_split = split_tiles(A, J);
   const bool whole = J.ntile <= per_split;        // no other split holds keys of these rows
   const int tile0 = split * per_split;
@@ -685,7 +719,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
     }
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const long long part = ((long long)(b * A.c.hkv + hk) * A.mtiles + m) * A.nsplit + split;
+  const long long part = blockIdx.x;
   float* s_join = reinterpret_cast<float*>(smem + C::OFF_JOIN);
   const int pieces = J.nrow * (DV / 4);
   for (int i = tid; i < pieces; i += NTHREADS) {
@@ -766,9 +800,10 @@ __global__ void __launch_bounds__(NTHREADS) join_rows_kernel(const Args A, long 
   if (!some) x = 0;
   const int row = (int)(x % A.job_rows);
   const long long job = x / A.job_rows;
-  const int m = (int)(job % A.mtiles), bh = (int)(job / A.mtiles), hk = bh % A.c.hkv, b = bh / A.c.hkv;
+  const int slot = (int)(job / A.c.hkv), hk = (int)(job - (long long)slot * A.c.hkv);
+  const Slot at = slot_of<ROWS>(A, slot);
   MaskArgs mk;
-  const Job J = make_job<ROWS>(A, b, m, mk);
+  const Job J = make_job<ROWS>(A, at.b, at.m, mk);
   const int n = cdiv(J.ntile, split_tiles(A, J));
   // launched early: the splits' kernel ends here.  Every thread waits, also where
   // nothing is to join: what follows on the stream waits for this kernel alone.
@@ -820,9 +855,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Args A) {
   const int groups = blockDim.x / COLS, nw = blockDim.x / 32;
   const int job = blockIdx.x / A.job_rows, row = blockIdx.x % A.job_rows;
   const int grp = threadIdx.x / COLS, col = threadIdx.x % COLS, c = col * 4;
-  const int m = job % A.mtiles, bh = job / A.mtiles, hk = bh % A.c.hkv, b = bh / A.c.hkv;
+  const int slot = job / A.c.hkv, hk = job - slot * A.c.hkv;
+  const Slot at = slot_of<ROWS>(A, slot);
   MaskArgs mk;
-  const Job J = make_job<ROWS>(A, b, m, mk);
+  const Job J = make_job<ROWS>(A, at.b, at.m, mk);
   const int n = cdiv(J.ntile, split_tiles(A, J));
   asm volatile("griddepcontrol.wait;" ::: "memory");   // all threads: see join_rows_kernel
   if (row >= J.nrow || n <= 1) return;
@@ -865,7 +901,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Args A) {
 struct Layout {
   int nt, mtiles, job_rows, nsplit, min_tiles;
   long long jobs;
-  bool cluster;
+  bool cluster, direct;
   size_t off_status, off_ml, off_o, off_long, total;
   KvLong lng;
 };
@@ -879,12 +915,16 @@ static Layout layout(const attn_kv_fwd_params& p) {
   Layout L{};
   const int g = p.nhead_q / p.cache.nhead_kv;
   L.lng = kv_long_layout(p, max_keys(p));
-  const int most = p.max_seqlen_q < L.lng.from ? p.max_seqlen_q : L.lng.from;   // query tokens of this path
-  const long long rows = (long long)(most > 0 ? most : 1) * g;
-  L.nt = rows <= 8 ? 1 : 2;
+  int most = p.max_seqlen_q < L.lng.from ? p.max_seqlen_q : L.lng.from;   // query tokens of this path
+  most = most < p.total_q ? most : p.total_q;
+  const long long rows = (long long)(most > 0 ? most : 1) * g, all_rows = (long long)p.total_q * g;
+  // tiles of 8 rows where a request has no more, at least on average
+  L.nt = rows <= 8 || all_rows <= 8LL * p.batch ? 1 : 2;
   L.mtiles = (int)cdiv_ll(rows, 8 * L.nt);
   L.job_rows = (int)(rows < 8 * L.nt ? rows : 8 * L.nt);
-  L.jobs = (long long)p.batch * p.cache.nhead_kv * L.mtiles;
+  const long long packed = all_rows / (8 * L.nt) + p.batch, each = (long long)p.batch * L.mtiles;
+  L.direct = each <= packed;
+  L.jobs = p.cache.nhead_kv * (L.direct ? each : packed);
   // Keys that the rows of a job see at most (8 requests of up to 1,183 tokens under
   // a window of 190, head dim 256: 8.8 us, 18.1 with splits for all of them).
   long long keys = max_keys(p);
@@ -1056,6 +1096,7 @@ static int run(const attn_kv_fwd_params* p, void* ws, size_t ws_bytes, cudaStrea
   a.max_k = max_keys(*p);
   a.total_q = p->total_q;
   a.max_q = p->max_seqlen_q;
+  a.batch = p->batch;
   a.hq = p->nhead_q;
   a.g = p->nhead_q / p->cache.nhead_kv;
   a.mask = p->mask;
@@ -1065,6 +1106,7 @@ static int run(const attn_kv_fwd_params* p, void* ws, size_t ws_bytes, cudaStrea
   a.nsplit = L.nsplit;
   a.min_tiles = L.min_tiles;
   a.cluster = L.cluster;
+  a.direct = L.direct;
   a.mtiles = L.mtiles;
   a.long_from = L.lng.from;
   a.job_rows = L.job_rows;

@@ -573,7 +573,7 @@ int attn_kv_append(const attn_kv_append_params* p, cudaStream_t stream);
  * and values are expanded to the type of q in the workspace and attn_fwd's
  * tensor-core kernel runs on them, its softmax weights rounded to that type (with FP16, cache values past
  * 65504 are clamped to it); other weights are rounded to 11 bits.  One call may
- * mix both kinds.  Long segments must not overlap one another in q. */
+ * mix both kinds.  Segments must not overlap one another in q. */
 typedef struct {
   int32_t dtype;          /* ATTN_BF16 or ATTN_FP16: type of q and o               */
   int32_t batch;          /* segments, >= 1                                        */

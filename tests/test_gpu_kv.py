@@ -535,6 +535,29 @@ def test_attend_long_segments_in_a_wide_buffer(B):
     assert bool((out[others.cuda()] == 0).all()) and bool((lse[:, others.cuda()] == 9).all())
 
 
+@pytest.mark.parametrize("batch,group,longest,scale", [(70, 4, 7, 0.1), (300, 1, 20, 0.1), (5, 8, 24, 0.1), (1100, 2, 6, 0.1),
+                                                       (40, 4, 130, -0.1)])
+def test_attend_few_rows_under_a_loose_bound(B, batch, group, longest, scale):
+    """max_seqlen_q far above most lengths: the grid follows the rows that q has.
+    Empty segments first, last and in between; lengths that go back and more rows
+    than q has are reported."""
+    g = torch.Generator().manual_seed(batch)
+    new = torch.randint(0, 3, (batch,), generator=g).tolist()
+    new[0], new[batch // 2], new[-1] = 0, longest, 0
+    lens = torch.randint(0, 60, (batch,), generator=g).tolist()
+    lens[batch // 2] = 900
+    q, table, kc, vc, ke, ve, cu = attend_case(64, 64, torch.bfloat16, 16, lens, new, 2, group)
+    c, qd = handle(B, kc, vc, ke, ve), q.cuda()
+    kw = dict(scale=scale, max_seqlen_q=200, max_seqlen_k=900, check_status=True)
+    o, lse = B.attn_kv_forward(qd, c, dev(table), dev(lens), dev(cu), **kw)
+    ref = kv_ref.attend(q, cu, lens, table, kc, vc, ke, ve, scale, 2)
+    check_attend(o, lse, ref, torch.bfloat16, 64, 900)
+    for bad in (cu[:2] + [-1] + cu[3:], [x - 1 for x in cu[:-1]] + [cu[-1] + 1], cu[:-2] + [cu[-1] + 5, cu[-1]]):
+        with pytest.raises(B.AttnError) as e:
+            B.attn_kv_forward(qd, c, dev(table), dev(lens), dev(bad), **kw)
+        assert e.value.status == B.ATTN_ERR_BAD_SEQLENS
+
+
 def test_attend_long_segments_overlapping(B):
     """Padded starts that make long segments overlap: reported, nothing outside
     the declared rows touched."""
