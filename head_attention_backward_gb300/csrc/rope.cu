@@ -75,8 +75,9 @@ struct alignas(sizeof(T) * N) Vec {
 // elements of either rotated half, VP pairs; the columns past the rotated ones
 // follow in chunks of two vectors that are copied.  Interleaved: 2 VP
 // consecutive elements, pairs past the rotated ones copied.  VP = 8 (16-bit) or
-// 4 (fp32) makes a vector one 16-byte access; VP = 1 takes any rot_dim and any
-// fp32 alignment.
+// 4 (fp32) makes a vector one 16-byte access; VP = 1 takes fp32 rows of any
+// alignment and size.  What else does not divide into such chunks is the staged
+// kernel's below.
 //
 // A CTA takes `tok` rows; its threads walk over (row, head, chunk) in steps of
 // NTHREADS.
@@ -182,6 +183,110 @@ __global__ void __launch_bounds__(NTHREADS, RESIDENT) rope_kernel(const Args A, 
   }
 }
 
+// Halves that start inside a 16-byte vector (half split, rot_dim no multiple of 16,
+// or 8 for fp32), and interleaved rows that are an odd number of vectors.  A thread
+// takes one vector of columns; a row's threads are in one warp, which passes the
+// partners on through shared memory (five words per vector, nine cosines for eight:
+// no bank conflicts), so rows still move in 16-byte pieces and may be rotated in
+// place.  8,098 rows of 10 heads of 256, 250 rotated, fp16: 31.1 us, element by
+// element 51.9.
+template <typename T, bool INTER>
+__global__ void __launch_bounds__(NTHREADS) rope_staged_kernel(const Args A, const __grid_constant__ Table table) {
+  constexpr int E = 16 / sizeof(T);                      // elements of a vector
+  constexpr int WARPS = NTHREADS / 32, MOST = ATTN_ROPE_MAX_DIM / E > 32 ? 2 : 1;   // vectors of a thread
+  using V = Vec<T, E>;
+  __shared__ uint32_t s_part[WARPS][32 * MOST * 5];
+  __shared__ unsigned long long s_step[MAX_PAIRS];       // from the parameter bank, which serves one address at a time
+  __shared__ uint8_t s_axis[MAX_PAIRS];
+  extern __shared__ unsigned long long dyn[];
+  float2* cs = reinterpret_cast<float2*>(dyn);
+  const int stride = A.half + A.half / 8 + 1;
+  if (threadIdx.x < A.half) {
+    s_step[threadIdx.x] = table.step[threadIdx.x];
+    s_axis[threadIdx.x] = table.axis[threadIdx.x];
+  }
+  __syncthreads();
+  const int row0 = blockIdx.x * A.tok, nrow = min(A.tok, A.rows - row0);
+  for (int i = threadIdx.x; i < nrow * A.half; i += NTHREADS) {
+    const int rr = i / A.half, pair = i - rr * A.half, row = row0 + rr, b = row / A.seqlen;
+    const int pos = __ldg(A.pos + s_axis[pair] * A.pa + b * A.pb + (row - b * A.seqlen) * A.pr);
+    float2 x = cos_sin_turns((unsigned long long)(long long)pos * s_step[pair]);
+    if (A.inverse) x.y = -x.y;
+    cs[rr * stride + pair + pair / 8] = x;
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int vecs = A.dim / E, mine = cdiv(vecs, 32);     // vectors of a head's row, of a thread
+  const int rows = mine > 1 ? 1 : 32 / vecs;             // heads' rows that a warp takes at a time
+  const int sub = mine > 1 ? 0 : lane / vecs, c0 = mine > 1 ? lane : lane - sub * vecs;
+  uint32_t* part = s_part[warp] + sub * vecs * 5;
+  // a row's heads one after the other, its cosines in registers
+  const int share = max(1, WARPS / nrow);                // warps of a row
+  for (int r = warp / share; r < nrow; r += WARPS / share) {
+    const int row = row0 + r, b = row / A.seqlen, s = row - b * A.seqlen;
+    float2 t[MOST][E];                                   // cos, and sin as it multiplies the partner
+#pragma unroll
+    for (int k = 0; k < MOST; ++k)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int col = (c0 + 32 * k) * E + e;
+        const bool first = INTER ? e % 2 == 0 : col < A.half;
+        const int pair = min(INTER ? col / 2 : first ? col : col - A.half, A.half - 1);
+        t[k][e] = cs[r * stride + pair + pair / 8];
+        if (first) t[k][e].y = -t[k][e].y;
+      }
+    for (int h0 = warp % share * rows; h0 < A.heads; h0 += share * rows) {
+      const int h = h0 + sub;
+      const bool live = sub < rows && h < A.heads;
+      const Side& x = h < A.hq ? A.q : A.k;
+      const int hh = h < A.hq ? h : h - A.hq;
+      const T* in = static_cast<const T*>(x.in) + b * x.ib + s * x.ir + hh * x.ih;
+      T* out = static_cast<T*>(x.out) + b * x.ob + s * x.orow + hh * x.oh;
+      V v[MOST];
+#pragma unroll
+      for (int k = 0; k < MOST; ++k) {
+        const int c = c0 + 32 * k;
+        if (!live || c >= vecs) continue;
+        v[k] = *reinterpret_cast<const V*>(in + c * E);
+        if (!INTER) {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(&v[k]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) part[c * 5 + i] = w[i];
+        }
+      }
+      if (!INTER) __syncwarp();
+#pragma unroll
+      for (int k = 0; k < MOST; ++k) {
+        const int c = c0 + 32 * k;
+        if (!live || c >= vecs) continue;
+        V y = v[k];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int col = c * E + e;
+          const int other = col < A.half ? col + A.half : col - A.half;
+          const float own = TypeOps<T>::to_f(v[k].v[e]);
+          const float partner =
+              TypeOps<T>::to_f(INTER ? v[k].v[e ^ 1] : reinterpret_cast<const T*>(part + other / E * 5)[other % E]);
+          const T turned = TypeOps<T>::from_f(own * t[k][e].x + partner * t[k][e].y);
+          if (col < 2 * A.half) y.v[e] = turned;         // the others are copied
+        }
+        *reinterpret_cast<V*>(out + c * E) = y;
+      }
+      if (!INTER) __syncwarp();                          // the parts may be overwritten
+    }
+  }
+}
+
+template <typename T>
+static void launch_staged(const Args& a, const Table& t, bool inter, cudaStream_t st) {
+  const int grid = cdiv(a.rows, a.tok);
+  const size_t smem = (size_t)a.tok * (a.half + a.half / 8 + 1) * sizeof(float2);
+  if (inter)
+    rope_staged_kernel<T, true><<<grid, NTHREADS, smem, st>>>(a, t);
+  else
+    rope_staged_kernel<T, false><<<grid, NTHREADS, smem, st>>>(a, t);
+}
+
 template <typename T, int VP>
 static void launch(const Args& a, const Table& t, bool inter, cudaStream_t st) {
   const int grid = cdiv(a.rows, a.tok);
@@ -266,25 +371,25 @@ static int run(const attn_rope_params* p, cudaStream_t st) {
   a.dim = p->head_dim;
   a.half = half;
   a.inverse = p->inverse != 0;
-  // Rows of a CTA: eight share the table and the wait for their cosines (16,384
-  // rows of 40 heads of 128: 58.7 us; before the register bound 62.7, 87.6 at one
-  // row, 68.1 at sixteen); one where
-  // that would leave SMs without a CTA.
-  a.tok = a.rows < 2048 ? 1 : 8;
+  // Rows of a CTA share the table and the wait for their cosines; fewer where eight
+  // would leave SMs idle (16,384 rows of 40 heads of 128: 58.7 us at eight, 60.2 at
+  // four, 87 at one; 3,000: 12.9, 11.3 and 15.3; 800: two 5.4, one 6.4; 64: 3.3 at one,
+  // 3.7 at two).
+  a.tok = a.rows < 600 ? 1 : a.rows < 1500 ? 2 : a.rows < 8000 ? 4 : 8;
   const int vp = f32 ? 4 : 8;
-  bool vec = p->interleaved ? p->head_dim % (2 * vp) == 0 : half % vp == 0 && p->head_dim % vp == 0;
+  const bool pairs = p->interleaved ? p->head_dim % (2 * vp) == 0 : half % vp == 0 && p->head_dim % vp == 0;
+  bool wide = p->head_dim % vp == 0;   // rows of whole vectors
   if (f32)
     for (const Side* x : {&a.q, &a.k}) {
       if (x == &a.k && !has_k) continue;
-      vec = vec && aligned_to(x->in, 16) && aligned_to(x->out, 16) && x->ib % 4 == 0 && x->ir % 4 == 0 &&
-            x->ih % 4 == 0 && x->ob % 4 == 0 && x->orow % 4 == 0 && x->oh % 4 == 0;
+      wide = wide && aligned_to(x->in, 16) && aligned_to(x->out, 16) && x->ib % 4 == 0 && x->ir % 4 == 0 &&
+             x->ih % 4 == 0 && x->ob % 4 == 0 && x->orow % 4 == 0 && x->oh % 4 == 0;
     }
   const bool inter = p->interleaved != 0;
-  switch (p->dtype) {
-    case ATTN_BF16: vec ? launch<__nv_bfloat16, 8>(a, t, inter, st) : launch<__nv_bfloat16, 1>(a, t, inter, st); break;
-    case ATTN_FP16: vec ? launch<__half, 8>(a, t, inter, st) : launch<__half, 1>(a, t, inter, st); break;
-    default: vec ? launch<float, 4>(a, t, inter, st) : launch<float, 1>(a, t, inter, st); break;
-  }
+  if (!wide) launch<float, 1>(a, t, inter, st);   // 16-bit rows always are
+  else if (p->dtype == ATTN_BF16) pairs ? launch<__nv_bfloat16, 8>(a, t, inter, st) : launch_staged<__nv_bfloat16>(a, t, inter, st);
+  else if (p->dtype == ATTN_FP16) pairs ? launch<__half, 8>(a, t, inter, st) : launch_staged<__half>(a, t, inter, st);
+  else pairs ? launch<float, 4>(a, t, inter, st) : launch_staged<float>(a, t, inter, st);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

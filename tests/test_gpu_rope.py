@@ -43,6 +43,14 @@ CASES = [
     (3000, 9, 1, 64, 58, 2, torch.bfloat16, True, 100),
     (2500, 3, 2, 128, 96, 2, torch.float16, False, 100),
     (9001, 2, 1, 64, 64, 3, torch.bfloat16, False, 9001),
+    # halves that start inside a 16-byte vector, rows of an odd number of vectors
+    (700, 5, 2, 256, 250, 2, torch.float32, False, 5000),
+    (1600, 3, 1, 256, 254, 1, torch.float16, False, 5000),
+    (5, 1, 0, 200, 122, 3, torch.bfloat16, False, 1 << 20),
+    (8100, 1, 1, 8, 2, 1, torch.bfloat16, False, 100),
+    (611, 7, 3, 72, 20, 2, torch.float16, True, 100),
+    (2100, 11, 2, 132, 132, 1, torch.float32, True, 100),
+    (13, 4, 4, 4, 2, 1, torch.float32, False, 100),
 ]
 
 
@@ -182,3 +190,24 @@ def test_around_attention(B):
         rep["tensor"] = n
         reps.append(rep)
     assert_all_ok(reps, "rope around attention")
+
+
+@pytest.mark.parametrize("dtype,d,rot,inter", [(torch.bfloat16, 128, 126, False), (torch.float32, 256, 36, False),
+                                               (torch.float16, 40, 10, True), (torch.float32, 68, 68, True)])
+def test_rope_staged_in_place(B, dtype, d, rot, inter):
+    """Slices of a packed projection with halves that start inside a vector, rotated
+    where they are: the same bits as out of place, and the rest untouched."""
+    g = torch.Generator().manual_seed(d)
+    qkv = torch.randn((2, 333, 9, d), generator=g).to(dtype).cuda()
+    was = qkv.clone()
+    pos = torch.randint(0, 9000, (2, 333), generator=g, dtype=torch.int32).cuda()
+    q, k = qkv[:, :, :5], qkv[:, :, 5:7]
+    f = B.rope_frequencies(rot)
+    want = B.rope(q, k, pos, f, interleaved=inter)
+    B.rope(q, k, pos, f, interleaved=inter, out=(q, k))
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(qkv[:, :, 7:], was[:, :, 7:])
+    assert not torch.equal(q, was[:, :, :5])
+    back = B.rope(q, k, pos, f, interleaved=inter, inverse=True)
+    # |x| < 5.5, turned below 8: half a step of each component, turned back (8 eps), the
+    # last rounding (3 eps), and cos^2 + sin^2 within 3 eps of 1 (17 eps)
+    assert float((back[0].double() - was[:, :, :5].double()).abs().max()) <= 28 * torch.finfo(dtype).eps
