@@ -571,9 +571,11 @@ int attn_kv_append(const attn_kv_append_params* p, cudaStream_t stream);
  * d_qk below 256, positive softmax_scale), where there is much to do (many kv
  * heads, a large max_seqlen_k) of fewer, but more than 24, are long: their keys
  * and values are expanded to the type of q in the workspace and attn_fwd's
- * tensor-core kernel runs on them, its softmax weights rounded to that type (with FP16, cache values past
- * 65504 are clamped to it); other weights are rounded to 11 bits.  One call may
- * mix both kinds.  Segments must not overlap one another in q. */
+ * tensor-core kernel runs on them, its softmax weights rounded to that type (with
+ * FP16 to no finer steps than 2^-24 of the row's largest, and cache values past
+ * 65504 are clamped to it); other weights are rounded to 11 bits, to no finer
+ * steps than 2^-28 of the row's largest.  One call may mix both kinds.  Segments
+ * must not overlap one another in q. */
 typedef struct {
   int32_t dtype;          /* ATTN_BF16 or ATTN_FP16: type of q and o               */
   int32_t batch;          /* segments, >= 1                                        */
