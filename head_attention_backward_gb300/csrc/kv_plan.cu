@@ -209,6 +209,9 @@ __global__ void __launch_bounds__(FILL_THREADS) fill_kernel(const attn_kv_plan_p
   P.slots[t] = slot;
 }
 
+// Shared memory of plan_kernel's four arrays.
+static size_t plan_smem(int batch) { return (4 * (size_t)batch + 3) * sizeof(int); }
+
 static int run(const attn_kv_plan_params* p, cudaStream_t st) {
   if (!p || p->reserved != 0) return ATTN_ERR_INVALID_ARG;
   const int shift = kv_page_shift(p->page_size);
@@ -224,9 +227,12 @@ static int run(const attn_kv_plan_params* p, cudaStream_t st) {
     if (!x || !aligned_to(x, 4)) return ATTN_ERR_INVALID_ARG;
   if (p->max_tokens > 0 && (!p->positions || !p->slots)) return ATTN_ERR_INVALID_ARG;
   if (!aligned_to(p->positions, 4) || !aligned_to(p->slots, 8)) return ATTN_ERR_INVALID_ARG;
-  const size_t smem = (4 * (size_t)p->batch + 3) * sizeof(int);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  // The default limit is 48 KB less the static shared memory.  The limit is the
+  // kernel's, not the call's: always the same one, so that a call on another thread
+  // cannot lower it before the launch.
+  const size_t smem = plan_smem(p->batch);
+  if (smem > 32 * 1024 && cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)plan_smem(ATTN_KV_MAX_BATCH)) != cudaSuccess)
     return ATTN_ERR_CUDA;
   const bool fill = p->max_tokens <= FILL_FROM;
   const int threads = p->batch <= SMALL_THREADS ? SMALL_THREADS : MAX_THREADS;

@@ -1,0 +1,88 @@
+"""Serving operators at the edges of what their calls allow: overflowed keys,
+pages that a request keeps filling, handles whose tensors moved, weights and
+caches at the end of the 16-bit ranges, calls from two threads."""
+import math
+import subprocess
+import sys
+import threading
+
+import pytest
+import torch
+
+from oracle import kv_ref
+from tests.kv_cases import F64, block_table, check_attend, half_step, random_cache
+from tests.test_gpu_kv import attend_case, dev, handle, runs
+from tests.test_gpu_parity import B  # noqa: F401  (fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------- plan
+
+def plan_problem(batch, seed, most_new=4, room=100):
+    g = torch.Generator().manual_seed(seed)
+    lens = torch.randint(0, 60, (batch,), generator=g).tolist()
+    new = torch.randint(-1, most_new + 1, (batch,), generator=g).tolist()
+    table, pool = block_table(lens, 16, g, extra_pages=batch, extra_cols=2)
+    used = {p for row in table for p in row if p >= 0}
+    free = [p for p in range(pool) if p not in used]
+    count = len(free)
+    free += [0] * (pool - count)
+    return new, lens, table, free, count, sum(max(n, 0) for n in new) + room
+
+
+FIRST_PLAN = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+from head_attention_backward_gb300 import binding as B
+batch, new = int(sys.argv[1]), int(sys.argv[2])
+i = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+lens = i(batch)
+lens[:new] = 1
+p = B.kv_plan(lens, i(batch), i(batch, 2), torch.arange(2 * batch, dtype=torch.int32, device="cuda"), i(1) + 2 * batch,
+              page_size=16, max_tokens=new)
+p.check()
+assert p.cu_seqlens.tolist() == [min(b, new) for b in range(batch + 1)]
+assert p.slots.tolist() == [16 * (2 * batch - 1 - t) for t in range(new)]
+"""
+
+
+@pytest.mark.parametrize("batch", [3047, 3048, 3071, 3072])
+@pytest.mark.parametrize("tokens", [100, 3000])
+def test_first_plan_of_a_process(B, batch, tokens):
+    """No larger call before it has widened what the kernel may use."""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_PLAN.format(root=root), str(batch), str(tokens)], capture_output=True,
+                       text=True, cwd=root, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_plans_from_two_threads(B):
+    """Batches of different sizes at the same time, on a stream each."""
+    sizes, errors = (3100, 8192), []
+
+    def work(batch):
+        try:
+            s = torch.cuda.Stream()
+            new, lens, table, free, count, cap = plan_problem(batch, batch)
+            want = kv_ref.plan(new, lens, [list(r) for r in table], list(free), count, 16, cap)
+            with torch.cuda.stream(s):
+                nd, ld, cd = dev(new), dev(lens), dev([count])
+                td, fd = dev(table), dev(free)
+                for _ in range(40):
+                    p = B.kv_plan(nd, ld, td.clone(), fd.clone(), cd, page_size=16, max_tokens=cap)
+                    p.check()
+                    got = (p.cu_seqlens.tolist(), p.seqlens.tolist(), p.positions.tolist(), p.slots.tolist(),
+                           p.free_count.tolist()[0])
+                    assert got == tuple(want)
+        except BaseException as e:   # noqa: BLE001  (reported below)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in sizes]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
