@@ -671,6 +671,7 @@ static int launch_typed(const attn_fwd_params& p, const FwdLayout& L, cudaStream
     return ATTN_ERR_CUDA;
   if (seg) {
     kern<<<dim3(ntq * a.nsplit, p.nhead_kv, p.batch), NTHREADS, smem, st>>>(maps, a);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;   // no parts to join
     if (a.nsplit > 1) {
       const long long rows = (long long)p.seqlen_q * g, heads = (long long)p.nhead_kv * p.batch;
       const long long each = heads < JOIN_GRID ? JOIN_GRID / heads : 1, need = cdiv_ll(rows, JOIN_WARPS);

@@ -1028,6 +1028,7 @@ static int launch(const Args& a, long long jobs, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kern, maps, a) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
   }
   kern<<<(unsigned)(jobs * a.nsplit), NTHREADS, C::SMEM, st>>>(maps, a);
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;   // no parts to join
   if (a.nsplit > 1) {
     cudaLaunchAttribute early;
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1049,7 +1050,7 @@ static int launch(const Args& a, long long jobs, cudaStream_t st) {
       if (cudaLaunchKernelEx(&cfg, join_kernel<DV, NT, T>, a) != cudaSuccess) return ATTN_ERR_CUDA;
     }
   }
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return ATTN_OK;
 }
 
 template <int DQK, int DV, typename T>

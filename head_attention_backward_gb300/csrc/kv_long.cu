@@ -225,6 +225,8 @@ static int launch(const attn_kv_fwd_params& p, const KvCacheView& c, const Strid
   const int* st_q = p.cu_seqlens_q_padded ? p.cu_seqlens_q_padded : p.cu_seqlens_q;
   setup_kernel<<<1, SETUP_THREADS, 0, st>>>(p.cu_seqlens_q, st_q, p.seqlens_k, p.batch, p.total_q, p.max_seqlen_q, max_k,
                                             L.from, L.slots, L.group, (int)L.kpad, T_);
+  // what follows reads the lists, and each forward the keys expanded for it
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   T* k16 = reinterpret_cast<T*>(ws + L.off_k);
   T* v16 = reinterpret_cast<T*>(ws + L.off_v);
   attn_fwd_params f{};
@@ -264,6 +266,7 @@ static int launch(const attn_kv_fwd_params& p, const KvCacheView& c, const Strid
       expand_kernel<T><<<dim3((unsigned)(L.kpad / 16), n, share), NTHREADS, 0, st>>>(T_, s0, c, f.d_qk, f.d_v, p.block_table,
                                                                              p.table_stride, k16, v16, L.kpad, f.mask,
                                                                              left, right);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
     f.batch = n;
     f.total_k = (int)(n * L.kpad);
     const FwdSegments seg{T_.zeros + s0, T_.len_q + s0, T_.start_q + s0, T_.len_k + s0, T_.start_k + s0, L.nsplit,
@@ -271,7 +274,7 @@ static int launch(const attn_kv_fwd_params& p, const KvCacheView& c, const Strid
     const int r = launch_fwd_tc(f, lay, st, &seg);
     if (r != ATTN_OK) return r;
   }
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return ATTN_OK;
 }
 
 }  // namespace kvlong

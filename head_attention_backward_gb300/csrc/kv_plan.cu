@@ -237,6 +237,8 @@ static int run(const attn_kv_plan_params* p, cudaStream_t st) {
   const bool fill = p->max_tokens <= FILL_FROM;
   const int threads = p->batch <= SMALL_THREADS ? SMALL_THREADS : MAX_THREADS;
   plan_kernel<<<1, threads, smem, st>>>(*p, shift, fill);
+  // the second kernel reads what the first wrote: never without it
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   if (!fill) {
     cudaLaunchAttribute early;
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -250,7 +252,7 @@ static int run(const attn_kv_plan_params* p, cudaStream_t st) {
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, fill_kernel, *p, shift) != cudaSuccess) return ATTN_ERR_CUDA;
   }
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return ATTN_OK;
 }
 
 }  // namespace kvplan

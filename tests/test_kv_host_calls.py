@@ -140,3 +140,50 @@ def test_a_plan_never_lowers_the_limit_of_another(fake):
     for batch in (3072, 3100, 5000, 8192):
         assert plan(fake, batch) == 0
         assert fake.fake_limit(b"plan_kernel") == high
+
+
+DECODE = dict(cache_kw=dict(num_pages=10000), max_blocks=8192, table_stride=8192)
+CALLS = {
+    # call, its kernels in order
+    "rope": (lambda: ("attn_rope", rope_params()), ["rope_kernel"]),
+    "plan, few tokens": (lambda: ("attn_kv_plan", plan_params()), ["plan_kernel"]),
+    "plan, many tokens": (lambda: ("attn_kv_plan", plan_params(max_tokens=5000)), ["plan_kernel", "fill_kernel"]),
+    "plan, many requests": (lambda: ("attn_kv_plan", plan_params(batch=8192, max_tokens=5000)), ["plan_kernel", "fill_kernel"]),
+    "append": (lambda: ("attn_kv_append", append_params()), ["append_kernel"]),
+    "attend, one split": (lambda: ("attn_kv_fwd", fwd_params()), ["kv_fwd_kernel"]),
+    "attend, a cluster": (lambda: ("attn_kv_fwd", fwd_params(max_seqlen_k=1000, **DECODE)), ["kv_fwd_kernel"]),
+    "attend, few rows": (lambda: ("attn_kv_fwd", fwd_params(max_seqlen_k=131072, **DECODE)), ["kv_fwd_kernel", "join_kernel"]),
+    "attend, many rows": (lambda: ("attn_kv_fwd", fwd_params(batch=400, total_q=400, max_seqlen_k=131072, **DECODE)),
+                          ["kv_fwd_kernel", "join_rows_kernel"]),
+    "attend, a prompt": (lambda: ("attn_kv_fwd", fwd_params(batch=2, total_q=700, max_seqlen_q=600, max_seqlen_k=640, max_blocks=40,
+                                                            table_stride=40)),
+                         ["setup_kernel", "expand_kernel", "fwd_tc_kernel", "kv_fwd_kernel"]),
+    "attend, a short prompt over many keys": (
+        lambda: ("attn_kv_fwd", fwd_params(batch=1, nhead_q=2, total_q=130, max_seqlen_q=130, max_seqlen_k=5000, **DECODE)),
+        ["setup_kernel", "expand_kernel", "fwd_tc_kernel", "join_parts_kernel", "kv_fwd_kernel", "join_kernel"]),
+    "attend, prompts in groups": (
+        lambda: ("attn_kv_fwd", fwd_params(cache_kw=dict(num_pages=10000, nhead_kv=8), batch=2, total_q=2000, max_seqlen_q=1000,
+                                           max_seqlen_k=2 ** 18, max_blocks=2 ** 14, table_stride=2 ** 14)),
+        ["setup_kernel"] + 2 * ["expand_kernel", "fwd_tc_kernel", "join_parts_kernel"] + ["kv_fwd_kernel"]),
+}
+
+
+@pytest.mark.parametrize("what", CALLS)
+def test_no_kernel_follows_one_that_was_not_launched(fake, what):
+    """The kernels of a call read what those before them wrote: where a launch
+    fails, the call ends there with its error."""
+    make, kernels = CALLS[what]
+
+    def run(fail):
+        fake.fake_reset(fail)
+        name, p = make()
+        more = (A[10], 1 << 40, None) if name == "attn_kv_fwd" else (None,)
+        st = getattr(fake, name)(ctypes.byref(p), *more)
+        return st, [fake.fake_name(i).decode() for i in range(fake.fake_count())]
+
+    st, names = run(-1)
+    assert st == 0 and len(names) == len(kernels) and all(k in n for k, n in zip(kernels, names)), names
+    for i in range(len(kernels)):
+        st, ran = run(i)
+        assert st == B.ATTN_ERR_CUDA and ran == names[:i + 1], (i, ran)
+        assert fake.fake_done() == i
