@@ -44,15 +44,18 @@ __device__ __forceinline__ float2 up2(uint32_t x, __nv_bfloat16*) {
 }
 __device__ __forceinline__ float2 up2(uint32_t x, __half*) { return __half22float2(*reinterpret_cast<__half2*>(&x)); }
 
-// Larger magnitudes of two pairs; a NaN is passed over.
+// Larger finite magnitudes of two pairs.  |x| + 0 |x| is |x| where x is finite and
+// NaN elsewhere, which the maximum passes over.
 __device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t x, __nv_bfloat16*) {
   x &= 0x7fff7fffu;
-  const __nv_bfloat162 y = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&m), *reinterpret_cast<__nv_bfloat162*>(&x));
+  const __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162*>(&x);
+  const __nv_bfloat162 y = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&m), __hfma2(v, __float2bfloat162_rn(0.f), v));
   return *reinterpret_cast<const uint32_t*>(&y);
 }
 __device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t x, __half*) {
   x &= 0x7fff7fffu;
-  const __half2 y = __hmax2(*reinterpret_cast<__half2*>(&m), *reinterpret_cast<__half2*>(&x));
+  const __half2 v = *reinterpret_cast<__half2*>(&x);
+  const __half2 y = __hmax2(*reinterpret_cast<__half2*>(&m), __hfma2(v, __float2half2_rn(0.f), v));
   return *reinterpret_cast<const uint32_t*>(&y);
 }
 

@@ -525,14 +525,14 @@ int attn_kv_plan(const attn_kv_plan_params* p, cudaStream_t stream);
  * (-1) are skipped.  The tokens of a call that go to one page form a run; the
  * page's rows in front of the run's first row are live, other rows that the
  * run does not name are not (their values become unspecified).  For each run,
- * head and side, with amax = the largest |x| of the run and e(amax) the least
- * e with amax <= 448 * 2^e, limited to [-30, 30]:
+ * head and side, with amax = the largest finite |x| of the run (0 if it has
+ * none) and e(amax) the least e with amax <= 448 * 2^e, limited to [-30, 30]:
  *   - the run holds row 0: the scale becomes 2^e(amax);
  *   - otherwise it becomes the larger of that and the old scale, and if it
  *     grew the live rows are rounded again to it;
  *   - the new values are rounded (to nearest even) to e4m3 multiples of it;
- *     beyond 448 scales they are clamped, NaN stays NaN (and is ignored by
- *     amax).
+ *     beyond 448 scales, and where they are infinite, they are clamped; NaN
+ *     stays NaN.
  * A run is found as long as fewer than page_size tokens of other pages (or
  * skipped ones) lie between two of its tokens.  A page named again farther
  * off, or a slot named twice, leaves that page's values unspecified, and

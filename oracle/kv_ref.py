@@ -9,7 +9,7 @@ it, and it shares no code with the CUDA path.  Definitions:
 * cache: e4m3 values (sign, 4 exponent bits with bias 7, 3 mantissa bits, no
   infinities, largest 448) times 2^(byte - 127) per page and head.  Appending a
   run of tokens to a page sets or raises the scale to the least power of two
-  that holds the run's largest magnitude, and rounds the rows in front of the
+  that holds the run's largest finite magnitude, and rounds the rows in front of the
   run again when it grew.
 * plan: the page stack and block tables of the C header, one page at a time.
 * attention over the cache: attn_ref's forward on each request's gathered,
@@ -101,7 +101,7 @@ def append(cache, exps, x, slots):
         r = min(rows)
         for h in range(x.shape[1]):
             part = x[toks, h]
-            mags = part.abs()[~torch.isnan(part)]
+            mags = part.abs()[torch.isfinite(part)]
             e = exponent_for(float(mags.max()) if mags.numel() else 0.0)
             if r > 0:
                 old = clamp_exp(exps[p, h])

@@ -86,3 +86,40 @@ def test_plans_from_two_threads(B):
     for t in threads:
         t.join()
     assert not errors, errors
+
+
+# -------------------------------------------------------------------- append
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dqk,dv,page", [(64, 64, 16), (192, 128, 32), (256, 256, 256)])
+@pytest.mark.parametrize("order", ["run", "list"])
+def test_append_one_infinity_leaves_the_page(B, dtype, dqk, dv, page, order):
+    """An overflowed value is clamped to the largest of the scale that the finite
+    ones ask for: the rows before it and its neighbours keep their values."""
+    heads, pages = 2, 5
+    g = torch.Generator().manual_seed(dqk)
+    kc, ke = random_cache(pages, page, heads, dqk, g)
+    vc, ve = random_cache(pages, page, heads, dv, g)
+    slots = runs([(3, 5, 7), (0, 0, page), (2, page - 1, 1), (4, 0, 2), (1, 1, 1)], page)
+    if order == "list":
+        slots[1], slots[4] = slots[4], slots[1]
+        slots[8], slots[9] = slots[9], slots[8]
+    n = len(slots)
+    k = torch.randn((n, heads, dqk), generator=g).to(dtype)
+    v = torch.randn((n, heads, dv), generator=g).to(dtype)
+    k[2, 0, 7], k[3, 1, dqk - 1] = math.inf, -math.inf
+    v[7 + page // 2, 1, :9] = torch.tensor([math.inf, -math.inf, math.nan] * 3)
+    v[7 + page, :, 3] = -math.inf
+    k[7 + page + 1:7 + page + 3, 0] = math.inf           # a run of nothing finite: the least scale
+    v[n - 1, 0, 1:] = 0.0
+    v[n - 1, 0, 0] = math.inf
+    c = handle(B, kc, vc, ke, ve)
+    B.kv_append(k.cuda(), v.cuda(), dev(slots, torch.int64), c)
+    kv_ref.append(kc, ke, k, slots)
+    kv_ref.append(vc, ve, v, slots)
+    assert int(ke[0].max()) < 127 + 5 and int(ke[3].max()) < 127 + 5
+    nan = lambda x: (x & 127) == 127   # noqa: E731
+    for name, got, ref in (("k", c.k, kc), ("v", c.v, vc)):
+        got = got.view(torch.uint8).cpu()
+        assert torch.equal(nan(got), nan(ref)) and torch.equal(got[~nan(ref)], ref[~nan(ref)]), name
+    assert torch.equal(c.k_exp.cpu(), ke) and torch.equal(c.v_exp.cpu(), ve)
