@@ -61,7 +61,9 @@ __global__ void __launch_bounds__(MAX_THREADS) plan_kernel(const attn_kv_plan_pa
   const int b0 = min(tid * per, n), b1 = min(b0 + per, n);
   const int free_n = *P.free_count;   // the output may be the same word: read by all before the first barrier
   const long long cap = (long long)P.max_blocks << shift;
-  bool bad = free_n < 0 || free_n > P.num_pages;
+  auto outside = [&](int page) { return page < 0 || page >= P.num_pages; };
+  bool bad = free_n < 0 || free_n > P.num_pages, off = false;
+  int filled = 0;
   Sums mine{0, 0, 0};
   for (int b = b0; b < b1; ++b) {
     const int add_n = P.new_lens[b], len = P.seqlens[b];
@@ -75,6 +77,11 @@ __global__ void __launch_bounds__(MAX_THREADS) plan_kernel(const attn_kv_plan_pa
     } else {
       mine.tok += add_n;
       mine.take += pages_of(len + add_n, shift) - held;
+      // the page that the new tokens fill up first; looked at below, where it has arrived
+      if (add_n > 0 && (len & ((1 << shift) - 1))) {
+        off |= outside(filled);
+        filled = P.block_table[b * P.table_stride + held - 1];
+      }
     }
   }
   // exclusive prefix over the threads
@@ -133,8 +140,7 @@ __global__ void __launch_bounds__(MAX_THREADS) plan_kernel(const attn_kv_plan_pa
     const int at = top - 1 - i;
     return at < free_n ? P.free_pages[at] : given(at - free_n);
   };
-  auto outside = [&](int page) { return page < 0 || page >= P.num_pages; };
-  bool off = false;
+  off |= outside(filled);
   for (int i = tid; i < nback; i += threads) off |= outside(given(i));
   for (int i = tid; i < ntake; i += threads) {
     const int at = top - 1 - i;

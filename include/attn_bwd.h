@@ -494,7 +494,8 @@ typedef struct {
  * ATTN_ERR_BAD_SEQLENS (a length below 0, past max_blocks pages or with
  * more new tokens than max_tokens in all; a free_count outside 0..num_pages,
  * or more pages given back than the stack holds), ATTN_ERR_OUT_OF_PAGES, or
- * ATTN_ERR_BAD_PAGE (a page to be pushed or popped outside 0..num_pages - 1). */
+ * ATTN_ERR_BAD_PAGE (a page to be pushed, popped or filled further outside
+ * 0..num_pages - 1; other entries of block_table are not looked at). */
 typedef struct {
   int32_t batch;          /* 1 .. ATTN_KV_MAX_BATCH                                */
   int32_t page_size;      /* as in attn_kv_cache                                   */

@@ -88,6 +88,34 @@ def test_plans_from_two_threads(B):
     assert not errors, errors
 
 
+@pytest.mark.parametrize("page", [-1, 12, 2 ** 31 - 1])
+@pytest.mark.parametrize("room", [0, 3000])
+def test_plan_checks_the_page_that_a_request_fills(B, page, room):
+    """New tokens in the partly filled last page: its entry has to name a page, as
+    those that are pushed and popped.  A full last page, or one of a request
+    without new tokens, is not written and not looked at."""
+    table = [[0, 1, -1], [2, -1, -1], [3, -1, -1]]
+    lens, free, count = [20, 16, 7], [4, 5, 6, 7, 8, 9, 10, 11, 0, 0, 0, 0], 8
+
+    def run(new, rows):
+        cap = sum(new) + room
+        td, fd = dev(rows), dev(free)
+        p = B.kv_plan(dev(new), dev(lens), td, fd, dev([count]), page_size=16, max_tokens=cap)
+        return p, td, fd, cap
+
+    bad = [list(r) for r in table]
+    bad[0][1] = page
+    p, td, fd, cap = run([3, 1, 0], bad)
+    assert int(p.status) == B.ATTN_ERR_BAD_PAGE
+    assert td.tolist() == bad and fd.tolist() == free and p.seqlens.tolist() == lens
+    assert p.free_count.tolist() == [count] and p.cu_seqlens.tolist() == [0] * 4 and p.slots.tolist() == [-1] * cap
+    # entries that this step has no use for
+    bad[0][0], bad[1][0], bad[2][0] = page, page, page
+    p, td, fd, cap = run([0, 2, 0], bad)
+    p.check()
+    assert p.slots.tolist() == [11 * 16, 11 * 16 + 1] + [-1] * room
+
+
 # -------------------------------------------------------------------- append
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
