@@ -530,7 +530,8 @@ class KvCache(_KvCacheFields):
     kv heads, d_qk] and v [..., d_v] as torch.float8_e4m3fn (or uint8), any
     strides with a contiguous head dimension, and the scale exponents k_exp,
     v_exp uint8 [pages, kv heads].  It keeps the tensors and their packed
-    description, and stays with them: its attributes cannot be replaced."""
+    description, addresses among them, and stays with them: its attributes
+    cannot be replaced, and calls refuse it once a tensor has other memory."""
 
     __slots__ = ()
     __eq__, __ne__, __hash__ = object.__eq__, object.__ne__, object.__hash__
@@ -590,7 +591,7 @@ def kv_append(k, v, slots, cache: KvCache, *, stream=None):
     if stream is not None:
         with _on_stream(stream):
             return kv_append(k, v, slots, cache)
-    st = (_marshal or _load_marshal()).append(k, v, slots, cache.packed, cache.index)
+    st = (_marshal or _load_marshal()).append(k, v, slots, cache, cache.index)
     if st != 0:
         raise AttnError(st, "attn_kv_append")
 
@@ -616,7 +617,7 @@ def attn_kv_forward(q, cache: KvCache, block_table, seqlens_k, cu_seqlens_q, *, 
                                    check_status=check_status)
     o, lse = (None, None) if out is None else out
     st, step, o, lse = (_marshal or _load_marshal()).attend(
-        q, cache.packed, cache.index, block_table, seqlens_k, cu_seqlens_q, cu_seqlens_q_padded, scale, mask, left, right,
+        q, cache, cache.index, block_table, seqlens_k, cu_seqlens_q, cu_seqlens_q_padded, scale, mask, left, right,
         max_seqlen_q, max_seqlen_k, o, lse, workspace, check_status)
     if st != 0:
         raise AttnError(st, _FWD_STEPS[step])

@@ -298,9 +298,18 @@ PyObject* py_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The description that a KvCache, a tuple (k, v, k_exp, v_exp, packed, ...), keeps of
+// its tensors.  Their memory may have been replaced since (set_, .data, a resized
+// storage): the addresses have to be those that were packed.
 void read_cache(PyObject* o, attn_kv_cache* c) {
-  if (!PyBytes_Check(o) || PyBytes_GET_SIZE(o) != sizeof(*c)) throw Refused{"not a packed cache"};
-  std::memcpy(c, PyBytes_AS_STRING(o), sizeof(*c));
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) < 5) throw Refused{"cache must be a KvCache"};
+  PyObject* packed = PyTuple_GET_ITEM(o, 4);
+  if (!PyBytes_Check(packed) || PyBytes_GET_SIZE(packed) != sizeof(*c)) throw Refused{"cache must be a KvCache"};
+  std::memcpy(c, PyBytes_AS_STRING(packed), sizeof(*c));
+  const void* at[4] = {c->k, c->v, c->k_exp, c->v_exp};
+  for (int i = 0; i < 4; ++i)
+    if (tensor(PyTuple_GET_ITEM(o, i), "a tensor of the cache").data_ptr() != at[i])
+      throw Refused{"a tensor of the cache has moved since its KvCache was made: make a new one"};
 }
 
 const at::Tensor& table(PyObject* o, int64_t batch, int index, int32_t* cols, int64_t* stride) {
@@ -380,7 +389,7 @@ PyObject* py_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 bool is16(const at::Tensor& t) { return t.scalar_type() == at::kBFloat16 || t.scalar_type() == at::kHalf; }
 
-// append(k, v, slots, packed cache, device) -> status
+// append(k, v, slots, KvCache, device) -> status
 PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 5, [&]() -> PyObject* {
     const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
@@ -405,7 +414,7 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// attend(q, packed cache, device, block_table, seqlens_k, cu_seqlens_q, cu_seqlens_q_padded or None, scale, mask,
+// attend(q, KvCache, device, block_table, seqlens_k, cu_seqlens_q, cu_seqlens_q_padded or None, scale, mask,
 // left, right, max_seqlen_q, max_seqlen_k, o or None, lse or None, workspace or None, check)
 // -> (status, step that gave it, o, lse); steps: 0 size, 1 launch, 2 reading the device's status, 3 that status
 PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {

@@ -151,3 +151,37 @@ def test_append_one_infinity_leaves_the_page(B, dtype, dqk, dv, page, order):
         got = got.view(torch.uint8).cpu()
         assert torch.equal(nan(got), nan(ref)) and torch.equal(got[~nan(ref)], ref[~nan(ref)]), name
     assert torch.equal(c.k_exp.cpu(), ke) and torch.equal(c.v_exp.cpu(), ve)
+
+
+# ------------------------------------------------------------ tensors that move
+
+def test_a_handle_whose_tensors_moved_is_refused(B):
+    """The handle holds addresses: a tensor that was given other memory since must
+    not be written through the old one."""
+    def make():
+        return [torch.zeros((4, 16, 2, 64), dtype=torch.uint8, device="cuda") for _ in range(2)] + [
+            torch.full((4, 2), 127, dtype=torch.uint8, device="cuda") for _ in range(2)]
+
+    k, sl = torch.ones((2, 2, 64), dtype=torch.bfloat16, device="cuda"), dev([0, 1], torch.int64)
+    q, td = torch.ones((1, 2, 64), dtype=torch.bfloat16, device="cuda"), dev([[0]])
+    kw = dict(scale=0.1, max_seqlen_q=1, max_seqlen_k=16)
+    for i in range(4):
+        t = make()
+        c = B.KvCache(*t)
+        B.kv_append(k, k, sl, c)
+        B.attn_kv_forward(q, c, td, dev([2]), dev([0, 1]), **kw)
+        kept = t[i].detach()                             # the old memory stays alive
+        was = kept.clone()
+        t[i].data = torch.zeros_like(kept)
+        for _ in range(2):
+            with pytest.raises(ValueError, match="moved"):
+                B.kv_append(k * 3, k * 3, sl, c)
+            with pytest.raises(ValueError, match="moved"):
+                B.attn_kv_forward(q, c, td, dev([2]), dev([0, 1]), **kw)
+            assert torch.equal(kept, was) and not bool(t[i].any())
+            t[i].data = kept                             # back: the handle holds again
+            B.kv_append(k, k, sl, c)
+            t[i].data = torch.zeros_like(kept)
+    t = make()
+    with pytest.raises(ValueError, match="moved"):       # a tuple's replacement of a field
+        B.kv_append(k, k, sl, B.KvCache(*t)._replace(k=torch.zeros_like(t[0])))
