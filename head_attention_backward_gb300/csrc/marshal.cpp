@@ -100,6 +100,12 @@ void rows3(const at::Tensor& t, const char* what, int64_t out[3]) {
   out[1] = n > 1 ? t.stride(0) : h * out[2];
 }
 
+// The library writes this tensor of the caller's: what autograd saved of it before
+// no longer holds.
+void changed(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();   // those have no version
+}
+
 cudaStream_t stream_of(int index) {
   if (!bound) throw Refused{"the library has not been loaded"};
   const int current = c10::cuda::current_device();
@@ -254,6 +260,8 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       strides(k, "k", p.stride_k);
       strides(ko, "out[1]", p.stride_k_out);
     }
+    if (a[7] != Py_None) changed(qo);
+    if (has_k && a[8] != Py_None) changed(ko);
     const int st = call([&] { return entries.rope(&p, stream); });
     return Py_BuildValue("iNN", st, THPVariable_Wrap(qo), has_k ? THPVariable_Wrap(ko) : Py_NewRef(Py_None));
   });
@@ -348,7 +356,8 @@ PyObject* py_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.max_tokens = whole32(a[6], "max_tokens");
     p.new_lens = vector<int32_t>(a[0], "new_lens", batch, index);
     p.seqlens = vector<int32_t>(a[1], "seqlens", batch, index);
-    p.block_table = pointer<int32_t>(table(a[2], batch, index, &p.max_blocks, &p.table_stride));
+    const at::Tensor& blocks = table(a[2], batch, index, &p.max_blocks, &p.table_stride);
+    p.block_table = pointer<int32_t>(blocks);
     p.free_pages = vector<int32_t>(a[3], "free_pages", pages, index);
     p.free_count = vector<int32_t>(a[4], "free_count", 1, index);
     if (p.max_tokens < 0) throw Refused{"max_tokens must not be negative"};
@@ -380,6 +389,10 @@ PyObject* py_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
       p.free_count_out = vector<int32_t>(o[4], "out.free_count", 1, index);
       p.status = vector<int32_t>(o[5], "out.status", 1, index);
     }
+    changed(blocks);
+    changed(free);
+    if (out != Py_None)
+      for (int i = 0; i < 6; ++i) changed(THPVariable_Unpack(PyTuple_GET_ITEM(out, i)));
     const int st = call([&] { return entries.plan(&p, stream); });
     if (out != Py_None) return Py_BuildValue("iO", st, out);
     return Py_BuildValue("i(NNNNNN)", st, THPVariable_Wrap(view[0]), THPVariable_Wrap(view[1]), THPVariable_Wrap(view[2]),
@@ -410,6 +423,7 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     rows3(v, "v", p.stride_v);
     p.slots = vector<int64_t>(a[2], "slots", k.size(0), index);
     cudaStream_t stream = stream_of(index);
+    for (int i = 0; i < 4; ++i) changed(THPVariable_Unpack(PyTuple_GET_ITEM(a[3], i)));
     return PyLong_FromLong(call([&] { return entries.append(&p, stream); }));
   });
 }
@@ -482,6 +496,10 @@ PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         refuse("workspace", "a contiguous uint8 tensor next to q", ws);
     }
     const size_t bytes = (size_t)ws.numel();
+    if (a[13] != Py_None) {
+      changed(o);
+      changed(lse);
+    }
     st = call([&] { return entries.fwd(&p, ws.data_ptr(), bytes, stream); });
     if (st != ATTN_OK || !check) return result(st, 1);
     int found = ATTN_OK;

@@ -185,3 +185,46 @@ def test_a_handle_whose_tensors_moved_is_refused(B):
     t = make()
     with pytest.raises(ValueError, match="moved"):       # a tuple's replacement of a field
         B.kv_append(k, k, sl, B.KvCache(*t)._replace(k=torch.zeros_like(t[0])))
+
+
+def test_outputs_given_by_the_caller_count_as_changed(B):
+    """Autograd refuses a backward pass over a saved tensor that was overwritten
+    since; it learns of it by the tensor's version."""
+    pos, f = dev([1, 2]), B.rope_frequencies(64)
+    x = torch.randn((2, 3, 64), device="cuda", requires_grad=True)
+    y = x.exp()                                          # saves its result
+    z, _ = B.rope(y, None, pos, f)
+    B.rope(y, None, pos, f, out=(y.detach(), None))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+    q, k = torch.randn((2, 3, 64), device="cuda"), torch.randn((2, 1, 64), device="cuda")
+    was = q._version, k._version
+    B.rope(q, k, pos, f)
+    assert (q._version, k._version) == was
+    B.rope(q, k, pos, f, out=(q, k))
+    assert q._version > was[0] and k._version > was[1]
+    # the other calls: outputs, and what they update
+    qq, table, kc, vc, ke, ve, cu = attend_case(64, 64, torch.bfloat16, 16, [5, 9], [1, 1], 1, 2)
+    c, qd, td, ld, cud = handle(B, kc, vc, ke, ve), qq.cuda(), dev(table), dev([5, 9]), dev(cu)
+    o, lse = torch.empty_like(qd), torch.empty((2, 2), device="cuda")
+
+    def change(call, *tensors):
+        was = [t._version for t in tensors]
+        call()
+        return [t._version > w for t, w in zip(tensors, was)]
+
+    kw = dict(scale=0.1, max_seqlen_q=1, max_seqlen_k=16)
+    assert change(lambda: B.attn_kv_forward(qd, c, td, ld, cud, out=(o, lse), **kw), o, lse, qd, td) == [True, True, False,
+                                                                                                        False]
+    kn = torch.ones((1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    assert change(lambda: B.kv_append(kn, kn, dev([0], torch.int64), c), c.k, c.v, c.k_exp, c.v_exp, kn) == [True] * 4 + [False]
+    fd, cd, nd = dev([0, 1, 2]), dev([3]), dev([1, 1])
+    out = B.KvPlan(dev([0] * 3), ld, dev([0] * 2), dev([0] * 2, torch.int64), cd, dev([0]))
+    td = dev([[3, -1], [4, -1]])
+    assert change(lambda: B.kv_plan(nd, ld, td, fd, cd, page_size=16, max_tokens=2, out=out), td, fd, *out, nd) == [True] * 8 + [
+        False]
+    with torch.inference_mode():                         # tensors without a version
+        i = torch.randn((2, 3, 64), device="cuda")
+    want, _ = B.rope(i, None, pos, f)
+    B.rope(i, None, pos, f, out=(i, None))
+    assert torch.equal(i, want)
