@@ -28,7 +28,9 @@
 //   to 2^-18 of the row's maximum, 2^-28 reached.  Scores, maxima, sums and O
 //   are fp32.
 // * The accumulator is held in units of one V scale; a page whose scale is
-//   within 2^4 of it has its ratio put on P (exact), others move the unit.
+//   within 2^4 of it has their ratio r put on P before its one rounding, others
+//   move the unit.  Such a P has 11 bits down to 2^-18 / r and reaches 2^-28 / r
+//   of the row's maximum: r = 2^-4 at worst, 2^-14 and 2^-24.
 //
 // In small grids the splits of a row tile form a thread-block cluster and are
 // joined through its shared memory; otherwise they leave (O, max, sum) in the
@@ -345,11 +347,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
-  const __half2 h = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 template <int DQK, int DV, int NT, typename T>
 __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_kernel(const __grid_constant__ Maps maps, const Args A) {
   using C = Cfg<DQK, DV, NT>;
@@ -623,8 +620,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
               for (int k = 0; k < 4; ++k) o[n][j][k] *= a[k & 1];
           }
         }
-        const __half2 ratio = __float2half2_rn(exp2_int(ev - unit));
-        const uint32_t ratio_bits = *reinterpret_cast<const uint32_t*>(&ratio);
+        const float ratio = exp2_int(ev - unit);
         uint32_t pb[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -635,7 +631,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK, DV, NT>::RESIDENT) kv_fwd_k
             const float p0 = fast_exp2(fmaf(s[n][2 * j], f[n][0], r0)), p1 = fast_exp2(fmaf(s[n][2 * j + 1], f[n][1], r1));
             lrow[n][0] += p0;
             lrow[n][1] += p1;
-            pb[n][j] = transpose8x8(mul_h2(pack_h2(p0, p1), ratio_bits));
+            pb[n][j] = transpose8x8(pack_h2(p0 * ratio, p1 * ratio));
           }
         }
         // O^T += V^T P^T: keys key_of(2t), key_of(2t + 1) and 8 more are this lane's

@@ -575,8 +575,9 @@ int attn_kv_append(const attn_kv_append_params* p, cudaStream_t stream);
  * tensor-core kernel runs on them, its softmax weights rounded to that type (with
  * FP16 to no finer steps than 2^-24 of the row's largest, and cache values past
  * 65504 are clamped to it); other weights are rounded to 11 bits, to no finer
- * steps than 2^-28 of the row's largest.  One call may mix both kinds.  Segments
- * must not overlap one another in q. */
+ * steps than 2^-28 of the row's largest (2^-24 where the V scale of their page is
+ * 2^-4 of one before it, in proportion between).  One call may mix both kinds.
+ * Segments must not overlap one another in q. */
 typedef struct {
   int32_t dtype;          /* ATTN_BF16 or ATTN_FP16: type of q and o               */
   int32_t batch;          /* segments, >= 1                                        */

@@ -228,3 +228,46 @@ def test_outputs_given_by_the_caller_count_as_changed(B):
     want, _ = B.rope(i, None, pos, f)
     B.rope(i, None, pos, f, out=(i, None))
     assert torch.equal(i, want)
+
+
+# ------------------------------------------------------------ attention's numerics
+
+def test_weights_under_a_smaller_scale_are_rounded_once(B):
+    """A light key whose page has V scales 2^4 below the accumulator's: its weight
+    w in [2^-15, 2^-14) meets fp16's steps of 2^-24 and is rounded to them once,
+    from fp32.  Key 0 has weight 1 and V = 0, key 64 (the same warp's next tile)
+    weight w and V = 448 2^2 against 2^6; all others have none.
+
+    The kernel's w is off by 2^-18 of itself at most (score in log2 units below
+    2^4 at 2^-24, its exponential 2^-22); weights within 2^-6 of a step of a tie
+    are left out (2^-6 2^-24 / 2^-15 = 2^-15).  What is left of O l / (448 2^2 2^4)
+    is the rounded weight, off by half a step of O and the same 2^-18 of l."""
+    n, d, page = 512, 64, 16
+    g = torch.Generator().manual_seed(5)
+    kc, vc = (torch.zeros((5, page, 1, d)) for _ in range(2))
+    kc[:, :, :, 1] = -448.0
+    kc[0, 0, 0, 1] = kc[4, 0, 0, 1] = 0.0
+    kc[4, 0, 0, 0] = kc[4, 0, 0, 2] = 1.0
+    vc[4, 0, 0] = 448.0
+    ke = torch.full((5, 1), 127, dtype=torch.uint8)
+    ve = torch.full((5, 1), 127 + 6, dtype=torch.uint8)
+    ve[4] = 127 + 2
+    q = torch.zeros((n, 1, d))
+    q[:, 0, 0] = -(9.72 + 0.65 * torch.rand(n, generator=g))
+    q[:, 0, 1] = 1.0
+    q[:, 0, 2] = 0.01 * torch.rand(n, generator=g)
+    q = q.half()
+    f8 = torch.float8_e4m3fn
+    o, _ = B.attn_kv_forward(q.cuda(), B.KvCache(kc.to(f8).cuda(), vc.to(f8).cuda(), ke.cuda(), ve.cuda()),
+                             dev([[0, 1, 2, 3, 4]] * n), dev([80] * n), dev(list(range(n + 1))), scale=1.0, mask=0,
+                             max_seqlen_q=1, max_seqlen_k=80, check_status=True)
+    w = torch.exp(q[:, 0, 0].to(F64) + q[:, 0, 2].to(F64))
+    assert bool(((w > 2.0 ** -15) & (w < 2.0 ** -14)).all())
+    steps = w * 2.0 ** 24
+    clear = ((steps % 1) - 0.5).abs() > 2.0 ** -6
+    assert int(clear.sum()) > n // 2
+    got = o[:, 0].cpu().to(F64) * (1 + w)[:, None] / (448 * 2.0 ** 2) * 2.0 ** 24
+    want = torch.round(steps)
+    err = (got - want[:, None]).abs().amax(1)
+    lim = want * (half_step(torch.float16) + 2.0 ** -17)
+    assert bool((err <= lim)[clear].all()), f"{int((err > lim)[clear].sum())} of {int(clear.sum())} rounded otherwise"
