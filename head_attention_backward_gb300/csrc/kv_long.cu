@@ -3,10 +3,11 @@
 // Hundreds of query rows per key make the products the bound (4 Hq d flops per
 // query and key against two cache bytes per key, head and column), so they
 // belong on tcgen05.  The cache's pages are first expanded to 16-bit rows in
-// the workspace (every e4m3 value times a power of two is exact in bf16, and in
-// fp16 within its range), and the tensor-core forward of attn_fwd runs on them.
-// The expansion reads each cache byte once and writes two; the forward reads
-// them back.
+// the workspace (every e4m3 value times a power of two is exact in bf16; in fp16 it
+// is rounded to multiples of 2^-24, which changes values below 2^-21 under scales
+// below 2^-15, and clamped at 65504), and the tensor-core forward of attn_fwd runs
+// on them.  The expansion reads each cache byte once and writes two; the forward
+// reads them back.
 //
 // The forward's query tiles hold tokens x heads of a group, so that a short
 // segment fills its 128 rows (34 tokens of 8 heads: 3 tiles instead of 8;

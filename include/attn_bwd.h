@@ -570,13 +570,19 @@ int attn_kv_append(const attn_kv_append_params* p, cudaStream_t stream);
  * its block_table entry may be anything.  Other masked values must be finite.
  * Segments of more than 24 + 96 / G query tokens (G = nhead_q / nhead_kv <= 128,
  * d_qk below 256, positive softmax_scale), where there is much to do (many kv
- * heads, a large max_seqlen_k) of fewer, but more than 24, are long: their keys
- * and values are expanded to the type of q in the workspace and attn_fwd's
- * tensor-core kernel runs on them, its softmax weights rounded to that type (with
- * FP16 to no finer steps than 2^-24 of the row's largest, and cache values past
- * 65504 are clamped to it); other weights are rounded to 11 bits, to no finer
- * steps than 2^-28 of the row's largest (2^-24 where the V scale of their page is
- * 2^-4 of one before it, in proportion between).  One call may mix both kinds.
+ * heads, a large max_seqlen_k, a total_q for many segments) of fewer, but more
+ * than 24, are long: their keys and values are expanded to the type of q in the
+ * workspace and attn_fwd's tensor-core kernel runs on them.  Softmax weights are
+ * rounded
+ *   - in long segments to the type of q (FP16: to no finer steps than 2^-24 of the
+ *     row's largest); with FP16 the cache's values too, to multiples of 2^-24 and
+ *     not past 65504 (exact for what was appended from FP16 below 63488);
+ *   - in the others to 11 bits, to no finer steps than 2^-28 of the row's largest
+ *     (2^-24 where the V scale of their page is 2^-4 of one before it, in
+ *     proportion between).
+ * Which of the two a segment of 25 tokens or more gets follows the sizes and
+ * bounds of the whole call, the same for all its segments: the same tokens may be
+ * rounded otherwise in another batch.  One call may mix both kinds.
  * Segments must not overlap one another in q. */
 typedef struct {
   int32_t dtype;          /* ATTN_BF16 or ATTN_FP16: type of q and o               */

@@ -271,3 +271,31 @@ def test_weights_under_a_smaller_scale_are_rounded_once(B):
     err = (got - want[:, None]).abs().amax(1)
     lim = want * (half_step(torch.float16) + 2.0 ** -17)
     assert bool((err <= lim)[clear].all()), f"{int((err > lim)[clear].sum())} of {int(clear.sum())} rounded otherwise"
+
+
+def rows_of(ref, rows):
+    return tuple(x[rows] if i in (0, 2) else x[:, rows] for i, x in enumerate(ref))
+
+
+def test_fp16_segments_over_tiny_scales(B):
+    """Cache values below fp16's steps (scales near 2^-25).  A short segment takes
+    them exactly; a long one has them rounded to multiples of 2^-24: every key and
+    value is off by 2^-25 at most, a score by 2^-25 sum |q| scale =: ds."""
+    lens, new, d, scale = [300, 300], [150, 4], 64, 300.0
+    q, table, kc, vc, ke, ve, cu = attend_case(d, d, torch.float16, 16, lens, new, 1, 1, q_scale=30.0)
+    g = torch.Generator().manual_seed(1)
+    for e in (ke, ve):
+        e[:] = torch.randint(127 - 30, 127 - 20, e.shape, generator=g).to(torch.uint8)
+    o, lse = B.attn_kv_forward(q.cuda(), handle(B, kc, vc, ke, ve), dev(table), dev(lens), dev(cu), scale=scale,
+                               max_seqlen_q=150, max_seqlen_k=300, check_status=True)
+    ref = kv_ref.attend(q, cu, lens, table, kc, vc, ke, ve, scale, 2)
+    short = list(range(150, 154))
+    check_attend(o[short], lse[:, short], rows_of(ref, short), torch.float16, d, 300)
+    rows = list(range(150))
+    ro, rl, mag, size = rows_of(ref, rows)
+    ds = 2.0 ** -25 * q[rows].to(F64).abs().sum(-1).T * scale + d * 2.0 ** -23 * size     # [1, T]
+    rel = 2 * ds + half_step(torch.float16) + 2.0 ** -16 + 40 * 2.0 ** -24
+    # weights of less than 2^-24 of the row's largest may be lost: 300 of them
+    lim = rel.T[..., None] * mag + 2 * 2.0 ** -25 + half_step(torch.float16) * ro.abs() + 300 * 2.0 ** -24 * 448 * 2.0 ** -20
+    assert bool(((o[rows].cpu().to(F64) - ro).abs() <= lim).all())
+    assert bool(((lse[:, rows].cpu().to(F64) - rl).abs() <= ds + 2.0 ** -15 + 2.0 ** -22 * rl.abs()).all())
