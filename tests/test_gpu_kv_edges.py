@@ -277,6 +277,26 @@ def rows_of(ref, rows):
     return tuple(x[rows] if i in (0, 2) else x[:, rows] for i, x in enumerate(ref))
 
 
+@pytest.mark.parametrize("name,d,lens,new,hkv,group,scale,short", [
+    ("beside a long one", 128, [30, 200, 40, 25], [1, 150, 5, 20], 2, 4, 0.01, (0, 2, 3)),
+    ("head dim 256", 256, [100, 40], [90, 30], 1, 2, 0.002, (0, 1)),
+    ("little work", 64, [60, 48], [48, 30], 1, 4, 0.01, (0, 1)),
+    ("one head to a group", 64, [130], [120], 1, 1, 0.01, (0,)),
+    ("negative scale", 64, [140], [130], 1, 2, -0.01, (0,)),
+])
+def test_short_segments_keep_11_bits_of_their_weights(B, name, d, lens, new, hkv, group, scale, short):
+    """Segments that the tensor-core forward does not take, by the header's rule: up
+    to 24 tokens, 24 + 96 / G where there is little to do, and all at head dim 256
+    or a negative scale.  Many keys of like weight make O small beside sum p |v|, so
+    that weights of 8 bits would leave the bounds (at 70 to 770 elements)."""
+    q, table, kc, vc, ke, ve, cu = attend_case(d, d, torch.bfloat16, 16, lens, new, hkv, group, q_scale=2.0)
+    o, lse = B.attn_kv_forward(q.cuda(), handle(B, kc, vc, ke, ve), dev(table), dev(lens), dev(cu), scale=scale,
+                               max_seqlen_q=max(new), max_seqlen_k=max(lens), check_status=True)
+    ref = kv_ref.attend(q, cu, lens, table, kc, vc, ke, ve, scale, 2)
+    rows = [r for b in short for r in range(cu[b], cu[b + 1])]
+    check_attend(o[rows], lse[:, rows], rows_of(ref, rows), torch.bfloat16, d, max(lens), torch.float16, what=name)
+
+
 def test_fp16_segments_over_tiny_scales(B):
     """Cache values below fp16's steps (scales near 2^-25).  A short segment takes
     them exactly; a long one has them rounded to multiples of 2^-24: every key and
