@@ -489,7 +489,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) fwd_tc_kernel(const __grid_consta
     T* orow = static_cast<T*>(A.o) + elem_off(A.so, (long long)q0 + qi, hr) + half * OC;
     // a part: O and the sum as they are, fp32
     const long long part = PACKED ? split * A.part_rows * A.hq + part_row(A, b, q0, qi, hr) : 0;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    // packed: a row whose scores are NaN has the sum NaN, and is not one that saw no key
+    const bool seen = PACKED ? l != 0.f : l > 0.f;
+    const float inv = seen ? 1.f / l : 0.f;
 #pragma unroll 1
     for (int c = 0; c < OC / 32; ++c) {
       uint32_t o[32];
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fwd_tc_kernel(const __grid_consta
       if (row_ok && half == 0)
         A.part_ml[part] = ok ? make_float2(mx, l) : make_float2(0.f, __int_as_float(0x7fc00000));
     } else if (row_ok && half == 0)
-      A.lse[li] = !ok ? __int_as_float(0x7fc00000) : l > 0.f ? (mx + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      A.lse[li] = !ok ? __int_as_float(0x7fc00000) : seen ? (mx + log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
 
   tc_fence_before();

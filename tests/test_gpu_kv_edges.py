@@ -319,3 +319,19 @@ def test_fp16_segments_over_tiny_scales(B):
     lim = rel.T[..., None] * mag + 2 * 2.0 ** -25 + half_step(torch.float16) * ro.abs() + 300 * 2.0 ** -24 * 448 * 2.0 ** -20
     assert bool(((o[rows].cpu().to(F64) - ro).abs() <= lim).all())
     assert bool(((lse[:, rows].cpu().to(F64) - rl).abs() <= ds + 2.0 ** -15 + 2.0 ** -22 * rl.abs()).all())
+
+
+@pytest.mark.parametrize("keys,new", [(300, 150), (5000, 130), (90, 3)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_nan_scores_give_nan_in_every_path(B, keys, new, dtype):
+    """A row of q with a NaN: O and LSE are NaN, not the -inf of a row that sees no
+    key; its neighbours are what they were.  Long, long with split keys, short."""
+    q, table, kc, vc, ke, ve, cu = attend_case(64, 64, dtype, 16, [keys], [new], 1, 1)
+    args = (handle(B, kc, vc, ke, ve), dev(table), dev([keys]), dev(cu))
+    kw = dict(scale=0.1, max_seqlen_q=new, max_seqlen_k=keys)
+    want = B.attn_kv_forward(q.cuda(), *args, **kw)
+    q[1, 0, 3] = math.nan
+    o, lse = B.attn_kv_forward(q.cuda(), *args, **kw)
+    assert bool(torch.isnan(o[1]).all()) and bool(torch.isnan(lse[:, 1]).all())
+    others = [0] + list(range(2, new))
+    assert torch.equal(o[others], want[0][others]) and torch.equal(lse[:, others], want[1][:, others])
