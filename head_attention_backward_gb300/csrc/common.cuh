@@ -407,6 +407,7 @@ struct FwdSegments {
   long long part_rows, slot_rows;
   float* part_o;           // [nsplit][part_rows][nhead_q][d_v]
   float2* part_ml;         // [nsplit][part_rows][nhead_q]: running maximum (log2 units) and sum
+  int* status;             // ATTN_ERR_TIMEOUT where a wait ran out (its rows are NaN)
 };
 constexpr int FWD_TILE_ROWS = 128;   // query rows of a tile of the tensor-core forward, and keys
 constexpr int FWD_MIN_SPLIT = 8;     // key tiles of a split at least

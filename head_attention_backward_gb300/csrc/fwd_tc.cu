@@ -119,6 +119,7 @@ struct Args {
   long long part_rows, slot_rows;
   float* part_o;
   float2* part_ml;
+  int* status;             // per segment: set where a wait ran out
 };
 
 // Part row of token i of segment b (whose tokens start at row q0) and of a head.
@@ -491,7 +492,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) fwd_tc_kernel(const __grid_consta
     const long long part = PACKED ? split * A.part_rows * A.hq + part_row(A, b, q0, qi, hr) : 0;
     // packed: a row whose scores are NaN has the sum NaN, and is not one that saw no key
     const bool seen = PACKED ? l != 0.f : l > 0.f;
-    const float inv = seen ? 1.f / l : 0.f;
+    // ... and a wait that ran out leaves NaN and says so
+    if (PACKED && !ok && lane == 0) A.status[b] = ATTN_ERR_TIMEOUT;
+    const float inv = PACKED && !ok ? __int_as_float(0x7fc00000) : seen ? 1.f / l : 0.f;
 #pragma unroll 1
     for (int c = 0; c < OC / 32; ++c) {
       uint32_t o[32];
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) fwd_tc_kernel(const __grid_consta
             dst[v] = make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]), __uint_as_float(o[4 * v + 2]),
                                  __uint_as_float(o[4 * v + 3]));
         }
-      } else if (row_ok && ok) {
+      } else if (row_ok && (ok || PACKED)) {
         uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
@@ -664,6 +667,7 @@ static int launch_typed(const attn_fwd_params& p, const FwdLayout& L, cudaStream
   a.slot_rows = seg ? seg->slot_rows : 0;
   a.part_o = seg ? seg->part_o : nullptr;
   a.part_ml = seg ? seg->part_ml : nullptr;
+  a.status = seg ? seg->status : nullptr;
   const int ntq = cdiv(p.seqlen_q > 0 ? p.seqlen_q : 1, seg ? tok : FM);
   auto kern = seg ? fwd_tc_kernel<DQK, DV, T, true> : fwd_tc_kernel<DQK, DV, T, false>;
   // more than half the shared memory, so that two CTAs (each holding all

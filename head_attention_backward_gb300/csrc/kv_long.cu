@@ -271,7 +271,8 @@ static int launch(const attn_kv_fwd_params& p, const KvCacheView& c, const Strid
     f.batch = n;
     f.total_k = (int)(n * L.kpad);
     const FwdSegments seg{T_.zeros + s0, T_.len_q + s0, T_.start_q + s0, T_.len_k + s0, T_.start_k + s0, L.nsplit,
-                          L.part_rows, L.slot_rows, reinterpret_cast<float*>(ws + L.off_po), reinterpret_cast<float2*>(ws + L.off_pml)};
+                          L.part_rows, L.slot_rows, reinterpret_cast<float*>(ws + L.off_po), reinterpret_cast<float2*>(ws + L.off_pml),
+                          T_.status + s0};
     const int r = launch_fwd_tc(f, lay, st, &seg);
     if (r != ATTN_OK) return r;
   }
