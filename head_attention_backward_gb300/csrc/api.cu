@@ -10,6 +10,7 @@
 #include <cstdlib>
 
 #include "common.cuh"
+#include "fwd_tc.cuh"
 
 namespace attn {
 

@@ -30,6 +30,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "fwd_tc.cuh"
 #include "sm100_ptx.cuh"
 
 namespace attn {

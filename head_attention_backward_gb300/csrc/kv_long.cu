@@ -21,6 +21,7 @@
 #include <cmath>
 
 #include "common.cuh"
+#include "fwd_tc.cuh"
 #include "kv_common.cuh"
 
 namespace attn {
