@@ -345,7 +345,8 @@ at::Tensor piece(const at::Tensor& base, int64_t at, int64_t n) {
 PyObject* py_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 8, [&]() -> PyObject* {
     const at::Tensor &lens = tensor(a[0], "new_lens"), &free = tensor(a[3], "free_pages");
-    if (!lens.is_cuda() || lens.dim() != 1 || free.dim() != 1) refuse("new_lens", "an int32 vector on a GPU", lens);
+    if (!lens.is_cuda() || lens.dim() != 1) refuse("new_lens", "an int32 vector on a GPU", lens);
+    if (free.dim() != 1) refuse("free_pages", "an int32 vector next to new_lens", free);
     const int index = lens.get_device();
     const int64_t batch = lens.size(0), pages = free.size(0);
     if (batch > INT32_MAX || pages > INT32_MAX) throw Refused{"sizes past 32 bits"};

@@ -116,6 +116,15 @@ def test_plan_checks_the_page_that_a_request_fills(B, page, room):
     assert p.slots.tolist() == [11 * 16, 11 * 16 + 1] + [-1] * room
 
 
+def test_plan_names_the_tensor_it_refuses(B):
+    i = dev([1, 1])
+    td = dev([[0, -1], [1, -1]])
+    with pytest.raises(ValueError, match="free_pages"):
+        B.kv_plan(i, i, td, dev([[2, 3]]), dev([2]), page_size=16, max_tokens=2)
+    with pytest.raises(ValueError, match="new_lens"):
+        B.kv_plan(dev([[1, 1]]), i, td, dev([2, 3]), dev([2]), page_size=16, max_tokens=2)
+
+
 # -------------------------------------------------------------------- append
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
