@@ -298,19 +298,16 @@ static void launch(const Args& a, const Table& t, bool inter, cudaStream_t st) {
 }
 
 // {batch, row, head} strides: contiguous when all are zero, otherwise positive
-// wherever the dimension has more than one entry and, for 16-bit types, whole
-// 16-byte units.
+// wherever the dimension has more than one entry (0 where it has not) and, for
+// 16-bit types, whole 16-byte units.
 static bool strides3(const int64_t in[3], int batch, int seqlen, int heads, int dim, bool vec16, long long out[3]) {
-  if (in[0] == 0 && in[1] == 0 && in[2] == 0) {
-    out[2] = dim;
-    out[1] = (long long)heads * dim;
-    out[0] = (long long)seqlen * out[1];
-    return true;
-  }
+  const bool contiguous = in[0] == 0 && in[1] == 0 && in[2] == 0;
   const int n[3] = {batch, seqlen, heads};
-  for (int i = 0; i < 3; ++i) {
-    out[i] = n[i] > 1 ? in[i] : 0;
-    if (n[i] > 1 && (in[i] <= 0 || in[i] >= (1LL << 36) || (vec16 && in[i] % 8))) return false;
+  long long step = dim;
+  for (int i = 2; i >= 0; --i) {
+    out[i] = n[i] <= 1 ? 0 : contiguous ? step : in[i];
+    if (n[i] > 1 && !contiguous && (in[i] <= 0 || in[i] >= (1LL << 36) || (vec16 && in[i] % 8))) return false;
+    step *= n[i];
   }
   return true;
 }

@@ -187,3 +187,15 @@ def test_no_kernel_follows_one_that_was_not_launched(fake, what):
         st, ran = run(i)
         assert st == B.ATTN_ERR_CUDA and ran == names[:i + 1], (i, ran)
         assert fake.fake_done() == i
+
+
+@pytest.mark.parametrize("batch,seqlen,heads", [(1, 10, 4), (3, 1, 4), (2, 5, 1), (1, 1, 1)])
+def test_rope_in_place_whichever_way_its_strides_are_written(fake, batch, seqlen, heads):
+    """Contiguous rows may be written as three zeros or in numbers, and a dimension
+    with one entry may carry any stride: the output is q itself all the same."""
+    numbers = [seqlen * heads * 64 if batch > 1 else 7, heads * 64 if seqlen > 1 else 7, 64 if heads > 1 else 7]
+    for si, so in ((numbers, (0, 0, 0)), ((0, 0, 0), numbers), (numbers, numbers)):
+        fake.fake_reset(-1)
+        p = rope_params(batch=batch, seqlen=seqlen, nhead_q=heads, nhead_kv=0, q=A[1], q_out=A[1], stride_q=si, stride_q_out=so)
+        assert fake.attn_rope(ctypes.byref(p), None) == 0, (si, so)
+        assert fake.fake_done() == 1
