@@ -377,7 +377,7 @@ static int run(const attn_kv_append_params* p, cudaStream_t st) {
   // tokens in pages of 64: 24.4 us at four, 27.9 at one, 32.6 at eight; 64 single
   // tokens: 4.0 us at one, 4.6 at four).
   const int groups = NWARPS / a.gw, per_run = p->cache.nhead_kv * 2;
-  const long long full = (long long)(p->tokens / p->cache.page_size) * per_run / (groups * 152LL * RESIDENT);
+  const long long full = (long long)(p->tokens / p->cache.page_size) * per_run / ((long long)groups * SMS * RESIDENT);
   const int rounds = full < 1 ? 1 : full > 4 ? 4 : (int)full;
   const int shares = cdiv(per_run, groups * rounds);
   // Tokens a CTA searches for runs: one in short calls (where every token may

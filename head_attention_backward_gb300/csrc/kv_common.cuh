@@ -30,6 +30,8 @@ inline bool kv_headdims(int dqk, int dv) {
          (dqk == 256 && dv == 256);
 }
 
+constexpr int SMS = 152;   // of a GB300; splits and shares are made for them
+
 // Grids carry twice this many (head, side) pairs in their second dimension.
 constexpr int KV_MAX_HEADS = 16384;
 

@@ -72,7 +72,7 @@ constexpr int META_TILES = 256;     // tiles whose pages are held in shared memo
 // A list of (job, split) items made on the device by a kernel before this one, and
 // taken by persistent CTAs, was slower throughout (65 us, 119 us and 32 us in these
 // cases): it puts two more trips to memory in front of the first load.
-constexpr int HALF_WAVE = 304;
+constexpr int HALF_WAVE = 2 * SMS;
 constexpr int MAX_GRID = 2560;
 constexpr int EVEN_TILES = 64;
 constexpr int MIN_TILES = 12;
@@ -929,13 +929,13 @@ static Layout layout(const attn_kv_fwd_params& p) {
     keys = span < keys ? span : keys;
   }
   const int tiles = (int)(keys / TILE) + 2;
-  const int wave = 152 * resident(p.cache.d_qk, L.nt);
+  const int wave = SMS * resident(p.cache.d_qk, L.nt);
   const bool few = 2 * L.jobs <= wave;
   L.min_tiles = few ? MIN_TILES : EVEN_TILES;
   const long long n = few ? (p.batch > 1 ? wave : HALF_WAVE) / L.jobs : cdiv_ll(MAX_GRID, L.jobs);
   L.nsplit = n < cdiv(tiles, L.min_tiles) ? (int)n : cdiv(tiles, L.min_tiles);
   // clusters of one wave: a cluster stays within eighteen SMs or so
-  L.cluster = few && L.nsplit > 1 && L.nsplit <= MAX_CLUSTER && L.jobs <= 8 * (wave * 18 / 152 / L.nsplit);
+  L.cluster = few && L.nsplit > 1 && L.nsplit <= MAX_CLUSTER && L.jobs <= 8 * (wave * 18 / SMS / L.nsplit);
   auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
   size_t o = 0;
   L.off_status = o;

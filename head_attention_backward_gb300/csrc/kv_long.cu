@@ -65,11 +65,11 @@ static int long_from(const attn_kv_fwd_params& p, int max_k) {
 static int splits(const attn_kv_fwd_params& p, const KvLong& L, int tok) {
   const long long by_rows = p.total_q / tok + L.slots, by_slots = (long long)L.group * cdiv(p.max_seqlen_q, tok);
   const long long ctas = p.cache.nhead_kv * (by_rows < by_slots ? by_rows : by_slots);
-  if (ctas >= 152) return 1;
+  if (ctas >= SMS) return 1;
   int best = 1;
   float least = 0.85f;   // a split has to gain more than the join costs
   for (int n = 2; n <= MAX_SPLITS && (n - 1) * FWD_MIN_SPLIT * FWD_TILE_ROWS < L.kpad; ++n) {
-    const float cost = (float)cdiv_ll(ctas * n, 152) / n + 0.02f * n;
+    const float cost = (float)cdiv_ll(ctas * n, SMS) / n + 0.02f * n;
     if (cost < least) {
       least = cost;
       best = n;
@@ -263,7 +263,8 @@ static int launch(const attn_kv_fwd_params& p, const KvCacheView& c, const Strid
     // tokens, 8 heads: 6.0 us against 9.7)
     const long long ctas = L.kpad / 16 * n;
     const int rounds = cdiv(16 * f.nhead_kv * (f.d_qk + f.d_v) / 16, NTHREADS);
-    const int share = ctas >= 1216 ? 1 : (int)(1216 / ctas < rounds ? 1216 / ctas : rounds);
+    const int full = 8 * SMS;   // CTAs that an SM holds
+    const int share = ctas >= full ? 1 : (int)(full / ctas < rounds ? full / ctas : rounds);
     if (max_k > 0)
       expand_kernel<T><<<dim3((unsigned)(L.kpad / 16), n, share), NTHREADS, 0, st>>>(T_, s0, c, f.d_qk, f.d_v, p.block_table,
                                                                              p.table_stride, k16, v16, L.kpad, f.mask,
