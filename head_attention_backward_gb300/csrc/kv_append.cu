@@ -373,7 +373,7 @@ static int run(const attn_kv_append_params* p, cudaStream_t st) {
   a.gw = 1;
   while (a.gw < NWARPS && HELD * (a.gw * 32 / (dim / 8)) < p->cache.page_size) a.gw *= 2;
   // Items a group takes one after the other: as many as leave the GPU full, up
-  // to four, beyond which the CTAs' search for runs no longer weighs (16,160
+  // to four, beyond which the CTAs' search for runs no longer weighs (15,295
   // tokens in pages of 64: 24.4 us at four, 27.9 at one, 32.6 at eight; 64 single
   // tokens: 4.0 us at one, 4.6 at four).
   const int groups = NWARPS / a.gw, per_run = p->cache.nhead_kv * 2;

@@ -614,7 +614,9 @@ typedef struct {
 } attn_kv_fwd_params;
 
 /* Workspace bytes attn_kv_fwd needs for *p: host arithmetic on the scalar
- * fields alone, as attn_bwd_workspace_size. */
+ * fields alone, as attn_bwd_workspace_size.  Where q can hold long segments they
+ * include room for expanded keys: up to 1 GiB, or one segment's of max_seqlen_k
+ * tokens if that is more. */
 int attn_kv_fwd_workspace_size(const attn_kv_fwd_params* p, size_t* bytes);
 
 /* Enqueue the attention on `stream`.  `workspace`: device, 256-byte aligned,
