@@ -41,6 +41,14 @@ inline int kv_page_shift(int page_size) {
   return -1;
 }
 
+// Whether a call of the runtime succeeded.  It remembers a failure until it is asked
+// for: it is asked here, so that the next call's check does not find this one's.
+inline bool succeeded(cudaError_t e) {
+  if (e == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
 inline bool aligned_to(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 // A dimension with one entry never uses its stride; it gets a valid one.

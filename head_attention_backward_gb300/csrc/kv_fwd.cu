@@ -1007,7 +1007,7 @@ static int launch(const Args& a, long long jobs, cudaStream_t st) {
   Maps maps;
   if (!make_map<DQK>(&maps.k, a.c.k, a.c, a.c.sk) || !make_map<DV>(&maps.v, a.c.v, a.c, a.c.sv)) return ATTN_ERR_CUDA;
   auto kern = kv_fwd_kernel<DQK, DV, NT, T>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+  if (!succeeded(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)))
     return ATTN_ERR_CUDA;
   if (a.cluster) {
     cudaLaunchAttribute dims;
@@ -1021,7 +1021,7 @@ static int launch(const Args& a, long long jobs, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = &dims;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, maps, a) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    return succeeded(cudaLaunchKernelEx(&cfg, kern, maps, a)) ? ATTN_OK : ATTN_ERR_CUDA;
   }
   kern<<<(unsigned)(jobs * a.nsplit), NTHREADS, C::SMEM, st>>>(maps, a);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;   // no parts to join
@@ -1037,13 +1037,13 @@ static int launch(const Args& a, long long jobs, cudaStream_t st) {
     if (jobs >= HALF_WAVE) {
       cfg.gridDim = dim3((unsigned)cdiv_ll(rows, NWARPS));
       cfg.blockDim = dim3(NTHREADS);
-      if (cudaLaunchKernelEx(&cfg, join_rows_kernel<DV, NT, T>, a, rows) != cudaSuccess) return ATTN_ERR_CUDA;
+      if (!succeeded(cudaLaunchKernelEx(&cfg, join_rows_kernel<DV, NT, T>, a, rows))) return ATTN_ERR_CUDA;
     } else {
       int threads = NTHREADS;   // about four splits to a thread group
       while (threads < JOIN_THREADS && threads / (DV / 4) * 4 < a.nsplit) threads *= 2;
       cfg.gridDim = dim3((unsigned)rows);
       cfg.blockDim = dim3(threads);
-      if (cudaLaunchKernelEx(&cfg, join_kernel<DV, NT, T>, a) != cudaSuccess) return ATTN_ERR_CUDA;
+      if (!succeeded(cudaLaunchKernelEx(&cfg, join_kernel<DV, NT, T>, a))) return ATTN_ERR_CUDA;
     }
   }
   return ATTN_OK;

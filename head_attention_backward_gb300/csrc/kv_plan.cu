@@ -237,8 +237,8 @@ static int run(const attn_kv_plan_params* p, cudaStream_t st) {
   // kernel's, not the call's: always the same one, so that a call on another thread
   // cannot lower it before the launch.
   const size_t smem = plan_smem(p->batch);
-  if (smem > 32 * 1024 && cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)plan_smem(ATTN_KV_MAX_BATCH)) != cudaSuccess)
+  if (smem > 32 * 1024 && !succeeded(cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                          (int)plan_smem(ATTN_KV_MAX_BATCH))))
     return ATTN_ERR_CUDA;
   const bool fill = p->max_tokens <= FILL_FROM;
   const int threads = p->batch <= SMALL_THREADS ? SMALL_THREADS : MAX_THREADS;
@@ -256,7 +256,7 @@ static int run(const attn_kv_plan_params* p, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, fill_kernel, *p, shift) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (!succeeded(cudaLaunchKernelEx(&cfg, fill_kernel, *p, shift))) return ATTN_ERR_CUDA;
   }
   return ATTN_OK;
 }

@@ -189,6 +189,19 @@ def test_no_kernel_follows_one_that_was_not_launched(fake, what):
         assert fake.fake_done() == i
 
 
+@pytest.mark.parametrize("what", CALLS)
+def test_a_failed_launch_is_not_held_against_the_next_call(fake, what):
+    """The runtime remembers an error until it is asked for: a call that failed
+    leaves none behind."""
+    make, kernels = CALLS[what]
+    for i in range(len(kernels)):
+        fake.fake_reset(i)
+        name, p = make()
+        more = (A[10], 1 << 40, None) if name == "attn_kv_fwd" else (None,)
+        assert getattr(fake, name)(ctypes.byref(p), *more) == B.ATTN_ERR_CUDA
+        assert fake.cudaGetLastError() == 0, i
+
+
 @pytest.mark.parametrize("batch,seqlen,heads", [(1, 10, 4), (3, 1, 4), (2, 5, 1), (1, 1, 1)])
 def test_rope_in_place_whichever_way_its_strides_are_written(fake, batch, seqlen, heads):
     """Contiguous rows may be written as three zeros or in numbers, and a dimension
