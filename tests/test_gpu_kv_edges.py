@@ -344,3 +344,42 @@ def test_nan_scores_give_nan_in_every_path(B, keys, new, dtype):
     assert bool(torch.isnan(o[1]).all()) and bool(torch.isnan(lse[:, 1]).all())
     others = [0] + list(range(2, new))
     assert torch.equal(o[others], want[0][others]) and torch.equal(lse[:, others], want[1][:, others])
+
+
+def test_steps_from_two_threads(B):
+    """Rotation, append and attention (short and long segments) of two caches at the
+    same time, on a stream each: the bits of the calls made one after the other."""
+    errors, jobs = [], []
+    for d, lens, new in ((64, [300, 20, 90], [130, 1, 2]), (128, [2000, 5], [1, 1])):
+        q, table, kc, vc, ke, ve, cu = attend_case(d, d, torch.bfloat16, 16, lens, new, 2, 4)
+        slots = [table[b][i // 16] * 16 + i % 16 for b, n in enumerate(lens) for i in range(n - new[b], n)]
+        pos = [i for b, n in enumerate(lens) for i in range(n - new[b], n)]
+        k, v = torch.randn_like(q[:, :2]).cuda(), torch.randn_like(q[:, :2]).cuda()
+        jobs.append((B.rope_frequencies(d), q.cuda(), k, v, dev(pos), dev(slots, torch.int64), dev(table), dev(lens), dev(cu),
+                     (kc, vc, ke, ve), dict(scale=0.1, max_seqlen_q=max(new), max_seqlen_k=max(lens))))
+
+    def step(job):
+        f, q, k, v, pos, slots, table, lens, cu, cache, kw = job
+        c = handle(B, *cache)
+        rq, rk = B.rope(q, k, pos, f)
+        B.kv_append(rk, v, slots, c)
+        o, lse = B.attn_kv_forward(rq, c, table, lens, cu, **kw)
+        return [x.cpu() for x in (o, lse, c.k.view(torch.uint8), c.v.view(torch.uint8), c.k_exp, c.v_exp)]
+
+    def work(job, want):
+        try:
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.default_stream())
+            with torch.cuda.stream(s):
+                for _ in range(30):
+                    for a, b in zip(step(job), want):
+                        assert torch.equal(a, b)
+        except BaseException as e:   # noqa: BLE001  (reported below)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(j, step(j))) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
