@@ -48,7 +48,7 @@ assert p.slots.tolist() == [16 * (2 * batch - 1 - t) for t in range(new)]
 """
 
 
-@pytest.mark.parametrize("batch", [3047, 3048, 3071, 3072])
+@pytest.mark.parametrize("batch", [3047, 3048, 3071, 3073])
 @pytest.mark.parametrize("tokens", [100, 3000])
 def test_first_plan_of_a_process(B, batch, tokens):
     """No larger call before it has widened what the kernel may use."""

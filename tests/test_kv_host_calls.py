@@ -121,7 +121,7 @@ def plan(fake, batch, max_tokens=8):
     return fake.attn_kv_plan(ctypes.byref(plan_params(batch=batch, max_tokens=max_tokens)), None)
 
 
-@pytest.mark.parametrize("batch", [1, 256, 2047, 3000, 3047, 3048, 3060, 3071, 3072, 8191, 8192])
+@pytest.mark.parametrize("batch", [1, 256, 2047, 3000, 3047, 3048, 3060, 3071, 3073, 8191, 8192])
 def test_plan_is_launched_at_every_batch(fake, batch):
     """As the first call of a process: whatever shared memory it needs has to be
     asked for."""
@@ -137,7 +137,7 @@ def test_a_plan_never_lowers_the_limit_of_another(fake):
     assert plan(fake, 8192) == 0
     high = fake.fake_limit(b"plan_kernel")
     assert high >= (4 * 8192 + 3) * 4
-    for batch in (3072, 3100, 5000, 8192):
+    for batch in (3073, 3100, 5000, 8192):
         assert plan(fake, batch) == 0
         assert fake.fake_limit(b"plan_kernel") == high
 
