@@ -100,10 +100,23 @@ class AttnKvFwdParams(ctypes.Structure):
                 ("stride_o", _i64x3), ("cache", AttnKvCache)]
 
 
+class AttnCheckpointTensors(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("o", _vp), ("q_exp", _vp), ("k_exp", _vp), ("v_exp", _vp),
+                ("o_exp", _vp), ("stride_q", _i64x3), ("stride_k", _i64x3), ("stride_v", _i64x3), ("stride_o", _i64x3)]
+
+
+class AttnCheckpointParams(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("batch", _i32), ("nhead_q", _i32), ("nhead_kv", _i32), ("seqlen_q", _i32),
+                ("seqlen_k", _i32), ("d_qk", _i32), ("d_v", _i32), ("q", _vp), ("k", _vp), ("v", _vp), ("o", _vp),
+                ("stride_q", _i64x3), ("stride_k", _i64x3), ("stride_v", _i64x3), ("stride_o", _i64x3),
+                ("ckpt", AttnCheckpointTensors)]
+
+
 EXPORTS = ["attn_bwd_workspace_size", "attn_bwd", "attn_bwd_timed", "attn_bwd_read_status",
            "attn_fwd", "attn_status_string", "attn_bwd_static_ws", "attn_selftest_waits", "attn_bwd_host",
            "attn_rope", "attn_kv_plan", "attn_kv_append", "attn_kv_fwd_workspace_size", "attn_kv_fwd",
-           "attn_kv_fwd_read_status"]
+           "attn_kv_fwd_read_status", "attn_checkpoint_save", "attn_bwd_checkpoint_workspace_size",
+           "attn_bwd_checkpoint"]
 
 _lib = None
 
@@ -139,6 +152,12 @@ def load(path: str = LIB_PATH):
     lib.attn_kv_fwd.restype = ctypes.c_int
     lib.attn_kv_fwd_read_status.argtypes = [P(AttnKvFwdParams), _vp, ctypes.c_size_t, _vp, P(ctypes.c_int)]
     lib.attn_kv_fwd_read_status.restype = ctypes.c_int
+    lib.attn_checkpoint_save.argtypes = [P(AttnCheckpointParams), _vp]
+    lib.attn_checkpoint_save.restype = ctypes.c_int
+    lib.attn_bwd_checkpoint_workspace_size.argtypes = [P(AttnBwdParams), P(AttnCheckpointTensors), P(ctypes.c_size_t)]
+    lib.attn_bwd_checkpoint_workspace_size.restype = ctypes.c_int
+    lib.attn_bwd_checkpoint.argtypes = [P(AttnBwdParams), P(AttnCheckpointTensors), _vp, ctypes.c_size_t, _vp]
+    lib.attn_bwd_checkpoint.restype = ctypes.c_int
     lib.attn_status_string.argtypes = [ctypes.c_int]
     lib.attn_status_string.restype = ctypes.c_char_p
     lib.attn_bwd_host.argtypes = [P(AttnBwdParams), P(AttnHostTensors), _vp, ctypes.c_size_t, _vp, _vp, _vp,
@@ -208,6 +227,21 @@ def attn_kv_fwd_read_status(p: AttnKvFwdParams, workspace: int, workspace_bytes:
     s = ctypes.c_int(0)
     st = load().attn_kv_fwd_read_status(ctypes.byref(p), workspace, workspace_bytes, stream, ctypes.byref(s))
     return st, s.value
+
+
+def attn_checkpoint_save(p: AttnCheckpointParams, stream: int = 0) -> int:
+    return load().attn_checkpoint_save(ctypes.byref(p), stream)
+
+
+def attn_bwd_checkpoint_workspace_size(p: AttnBwdParams, c: AttnCheckpointTensors):
+    n = ctypes.c_size_t(0)
+    st = load().attn_bwd_checkpoint_workspace_size(ctypes.byref(p), ctypes.byref(c), ctypes.byref(n))
+    return st, n.value
+
+
+def attn_bwd_checkpoint(p: AttnBwdParams, c: AttnCheckpointTensors, workspace: int, workspace_bytes: int,
+                        stream: int = 0) -> int:
+    return load().attn_bwd_checkpoint(ctypes.byref(p), ctypes.byref(c), workspace, workspace_bytes, stream)
 
 
 def attn_bwd_host(p: AttnBwdParams, host: AttnHostTensors, workspace: int, workspace_bytes: int, stream: int,
@@ -472,7 +506,8 @@ def _load_marshal():
         spec.loader.exec_module(m)
         m.bind(*(ctypes.cast(getattr(lib, n), _vp).value for n in (
             "attn_rope", "attn_kv_plan", "attn_kv_append", "attn_kv_fwd_workspace_size", "attn_kv_fwd",
-            "attn_kv_fwd_read_status")))
+            "attn_kv_fwd_read_status", "attn_checkpoint_save", "attn_bwd_checkpoint_workspace_size",
+            "attn_bwd_checkpoint", "attn_bwd_read_status")))
         _marshal = m
     return _marshal
 
@@ -622,6 +657,70 @@ def attn_kv_forward(q, cache: KvCache, block_table, seqlens_k, cu_seqlens_q, *, 
     if st != 0:
         raise AttnError(st, _FWD_STEPS[step])
     return o, lse
+
+
+# ------------------------------------------------------- 8-bit checkpoints
+
+CKPT_GROUP = 32   # ATTN_CKPT_GROUP
+
+
+class AttnCheckpoint(NamedTuple):
+    """What a backward pass needs of q, k, v and o in 8 bits (attn_checkpoint): int8
+    numbers shaped like the tensors they stand for, dense in any order of batch,
+    rows and heads, and uint8 exponents, one per 32 columns.  A value is
+    number * 2^(exponent - 127); 255 marks a group with an infinity or a NaN."""
+    q: torch.Tensor
+    k: torch.Tensor
+    v: torch.Tensor
+    o: torch.Tensor
+    q_exp: torch.Tensor
+    k_exp: torch.Tensor
+    v_exp: torch.Tensor
+    o_exp: torch.Tensor
+
+
+def checkpoint(q, k, v, o, *, out=None, stream=None):
+    """An AttnCheckpoint of a forward pass's q, k, v and o (attn_checkpoint_save),
+    new or written into `out`: [B, S, H, D] or [T, H, D] in bf16, fp16 or fp32,
+    head dims multiples of 32.  Once it is made, those tensors need not be kept."""
+    if stream is not None:
+        with _on_stream(stream):
+            return checkpoint(q, k, v, o, out=out)
+    st, made = (_marshal or _load_marshal()).checkpoint(q, k, v, o, out)
+    if st != 0:
+        raise AttnError(st, "attn_checkpoint_save")
+    return AttnCheckpoint(*made) if out is None else out
+
+
+_CKPT_STEPS = ("attn_bwd_checkpoint_workspace_size", "attn_bwd_checkpoint", "attn_bwd_read_status",
+               "attn_bwd_checkpoint (device status)")
+
+
+def attn_backward_checkpoint(ckpt: AttnCheckpoint, do, lse, *, scale, mask=MASK_NONE, left=-1, right=-1,
+                             deterministic=False, cu_seqlens_q=None, cu_seqlens_k=None, max_seqlen_q=0, max_seqlen_k=0,
+                             cu_seqlens_q_padded=None, cu_seqlens_k_padded=None, workspace=None, out=None, stream=None,
+                             check_status=True, bias=None, return_dbias=False, dropout_p=0.0, philox_seed=None,
+                             philox_offset=None):
+    """attn_backward at a checkpoint's q, k, v and o (attn_bwd_checkpoint): dQ, dK,
+    dV (and dbias) in the type of `do`, laid out like the checkpoint unless `out`
+    is given.  lse is the forward's; the other arguments are attn_backward's."""
+    if stream is not None:
+        with _on_stream(stream):
+            return attn_backward_checkpoint(
+                ckpt, do, lse, scale=scale, mask=mask, left=left, right=right, deterministic=deterministic,
+                cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k,
+                cu_seqlens_q_padded=cu_seqlens_q_padded, cu_seqlens_k_padded=cu_seqlens_k_padded, workspace=workspace,
+                out=out, check_status=check_status, bias=bias, return_dbias=return_dbias, dropout_p=dropout_p,
+                philox_seed=philox_seed, philox_offset=philox_offset)
+    kind = BIAS_NONE if bias is None else bias_type_of(bias, ckpt.q.shape[0], ckpt.q.shape[2])
+    dq, dk, dv = (None, None, None) if out is None else out
+    st, step, dq, dk, dv, dbias = (_marshal or _load_marshal()).backward(
+        ckpt, do, lse, scale, mask, left, right, int(deterministic), cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+        max_seqlen_k, cu_seqlens_q_padded, cu_seqlens_k_padded, workspace, dq, dk, dv, check_status, bias, kind,
+        return_dbias, dropout_p, philox_seed, philox_offset)
+    if st != 0:
+        raise AttnError(st, _CKPT_STEPS[step])
+    return (dq, dk, dv, dbias) if return_dbias else (dq, dk, dv)
 
 
 KV_RELEASE = -1   # ATTN_KV_RELEASE

@@ -9,6 +9,7 @@
 #include <cstdio>
 #include <cstdlib>
 
+#include "ckpt_common.cuh"
 #include "common.cuh"
 #include "fwd_tc.cuh"
 
@@ -311,7 +312,7 @@ static void log_config(const attn_bwd_params& p, const WsLayout& L) {
 // Schedule and preprocess launches of one call, or of one part of a call
 // split into parts (attn_bwd_host: parts after the first keep the status the
 // earlier parts left).
-void launch_schedule_preprocess(const Problem& P, cudaStream_t st, bool keep_status);
+void launch_schedule_preprocess(const Problem& P, cudaStream_t st, bool keep_status, const CkO& ck = {});
 
 // The validated problem the kernels of one call (or of one part of a call) run.
 static int prepare(const attn_bwd_params* p, void* ws, size_t ws_bytes, Problem* P) {
@@ -342,8 +343,9 @@ static int launch_main(const Problem& P, cudaStream_t s) {
 // zero and no attention kernel runs.
 static bool empty_problem(const Problem& P) { return rows_q(P) == 0 || rows_k(P) == 0; }
 
+// ck: an 8-bit checkpoint's o, which p->o and its strides then stand for.
 static int run(const attn_bwd_params* p, void* ws, size_t ws_bytes, cudaStream_t s,
-               cudaEvent_t* ev /* 4 events or null */, bool keep_status = false) {
+               cudaEvent_t* ev /* 4 events or null */, bool keep_status = false, const CkO& ck = {}) {
   Problem P;
   int st = prepare(p, ws, ws_bytes, &P);
   if (st != ATTN_OK) return st;
@@ -353,7 +355,7 @@ static int run(const attn_bwd_params* p, void* ws, size_t ws_bytes, cudaStream_t
     for (int i = 1; ev && i < 4; ++i) cudaEventRecord(ev[i], s);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
   }
-  launch_schedule_preprocess(P, s, keep_status);
+  launch_schedule_preprocess(P, s, keep_status, ck);
   if (ev) cudaEventRecord(ev[1], s);
   if ((st = launch_main(P, s)) != ATTN_OK) return st;
   if (ev) cudaEventRecord(ev[2], s);
@@ -365,6 +367,83 @@ static int run(const attn_bwd_params* p, void* ws, size_t ws_bytes, cudaStream_t
 static bool all_zero(const int64_t x[3]) { return x[0] == 0 && x[1] == 0 && x[2] == 0; }
 
 static size_t dtype_bytes(int dtype) { return dtype == ATTN_FP32 ? 4 : 2; }
+
+// The backward of an 8-bit checkpoint: attn_bwd's problem with q, k and v (fp32: o
+// too) in the workspace behind its own part, in the checkpoint's memory order.
+struct CkProblem {
+  attn_bwd_params p;        // of attn_bwd; tensors in the workspace not set yet
+  size_t off[4], total;     // q, k, v, o in the workspace
+  long long values[4];      // to expand
+};
+
+static int ck_problem(const attn_bwd_params* p, const attn_checkpoint* c, CkProblem* out) {
+  if (!p || !c) return ATTN_ERR_INVALID_ARG;
+  int st = validate_common(p);
+  if (st != ATTN_OK) return st;
+  if (p->deterministic < ATTN_DET_ATOMIC || p->deterministic > ATTN_DET_SPLIT) return ATTN_ERR_INVALID_ARG;
+  if (p->q || p->k || p->v || p->o || !all_zero(p->stride_q) || !all_zero(p->stride_k) || !all_zero(p->stride_v) ||
+      !all_zero(p->stride_o))
+    return ATTN_ERR_INVALID_ARG;
+  if (!ck_headdim(p->d_qk) || !ck_headdim(p->d_v)) return ATTN_ERR_UNSUPPORTED_HEADDIM;
+  out->p = *p;
+  const bool group = p->cu_seqlens_q != nullptr;
+  const int64_t* in[4] = {c->stride_q, c->stride_k, c->stride_v, c->stride_o};
+  int64_t* to[4] = {out->p.stride_q, out->p.stride_k, out->p.stride_v, out->p.stride_o};
+  for (int i = 0; i < 4; ++i) {
+    const bool q_side = i == 0 || i == 3;
+    const long long size[3] = {group ? 1 : p->batch, group ? (q_side ? p->total_q : p->total_k) : (q_side ? p->seqlen_q : p->seqlen_k),
+                               q_side ? p->nhead_q : p->nhead_kv};
+    const int d = i < 2 ? p->d_qk : p->d_v;
+    long long own[3];
+    int order[3];
+    if (size[0] * size[1] * size[2] > (1LL << 33) / d || !ck_dense(in[i], size, d, own, order)) return ATTN_ERR_INVALID_ARG;
+    for (int k = 0; k < 3; ++k) to[i][k] = own[k];
+    out->values[i] = size[0] * size[1] * size[2] * d;
+  }
+  if (p->dtype != ATTN_FP32) out->values[3] = 0;
+  attn_bwd_params e;
+  Strides sx[8];
+  if ((st = effective_bwd(out->p, &e, sx)) != ATTN_OK) return st;
+  out->total = ws_layout(e).total;
+  for (int i = 0; i < 4; ++i) {
+    out->off[i] = out->total;
+    out->total += ((size_t)out->values[i] * dtype_bytes(p->dtype) + 255) & ~size_t(255);
+  }
+  return ATTN_OK;
+}
+
+static int run_checkpoint(const attn_bwd_params* p, const attn_checkpoint* c, void* ws, size_t ws_bytes, cudaStream_t s) {
+  CkProblem k;
+  int st = ck_problem(p, c, &k);
+  if (st != ATTN_OK) return st;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return ATTN_ERR_INVALID_ARG;
+  if (ws_bytes < k.total) return ATTN_ERR_WORKSPACE_TOO_SMALL;
+  const bool group = p->cu_seqlens_q != nullptr;
+  const bool no_q = (group ? (long long)p->total_q : (long long)p->batch * p->seqlen_q) == 0;
+  const bool no_k = (group ? (long long)p->total_k : (long long)p->batch * p->seqlen_k) == 0;
+  const int8_t* n[4] = {c->q, c->k, c->v, c->o};
+  const uint8_t* exp[4] = {c->q_exp, c->k_exp, c->v_exp, c->o_exp};
+  const bool may_be_null[4] = {no_q, no_k, no_k, no_q};
+  void* wide[4];
+  for (int i = 0; i < 4; ++i) {
+    if ((!n[i] || !exp[i]) && !may_be_null[i]) return ATTN_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(n[i]) & 15u) != 0) return ATTN_ERR_INVALID_ARG;
+    wide[i] = static_cast<char*>(ws) + k.off[i];
+  }
+  k.p.q = wide[0];
+  k.p.k = wide[1];
+  k.p.v = wide[2];
+  const bool fp32 = p->dtype == ATTN_FP32;
+  k.p.o = fp32 ? wide[3] : static_cast<const void*>(n[3]);
+  // every refusal comes before the first launch
+  Problem P;
+  if ((st = prepare(&k.p, ws, ws_bytes, &P)) != ATTN_OK) return st;
+  if (!empty_problem(P)) {
+    launch_ck_expand(p->dtype, n, exp, wide, k.values, s);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  }
+  return run(&k.p, ws, ws_bytes, s, nullptr, false, fp32 ? CkO{} : CkO{n[3], exp[3]});
+}
 
 // One tensor of attn_bwd_host: rows per batch entry (all rows in group mode),
 // heads, head dim, element bytes.
@@ -567,6 +646,20 @@ extern "C" int attn_bwd_workspace_size(const attn_bwd_params* p, size_t* bytes) 
 extern "C" int attn_bwd(const attn_bwd_params* p, void* workspace, size_t workspace_bytes,
                         cudaStream_t stream) {
   return run(p, workspace, workspace_bytes, stream, nullptr);
+}
+
+extern "C" int attn_bwd_checkpoint_workspace_size(const attn_bwd_params* p, const attn_checkpoint* c, size_t* bytes) {
+  if (!bytes) return ATTN_ERR_INVALID_ARG;
+  *bytes = 0;
+  CkProblem k;
+  const int st = ck_problem(p, c, &k);
+  if (st == ATTN_OK) *bytes = k.total;
+  return st;
+}
+
+extern "C" int attn_bwd_checkpoint(const attn_bwd_params* p, const attn_checkpoint* c, void* workspace,
+                                   size_t workspace_bytes, cudaStream_t stream) {
+  return run_checkpoint(p, c, workspace, workspace_bytes, stream);
 }
 
 extern "C" int attn_bwd_timed(const attn_bwd_params* p, void* workspace, size_t workspace_bytes,

@@ -12,6 +12,7 @@
 //   ascending slice order, cast to the output dtype (the "dq_convert"
 //   post-kernel of TransformerEngine PR #671, Summary, and the split
 //   accumulation "converted back to final gradients" of aiter PR #2216).
+#include "ckpt_common.cuh"
 #include "common.cuh"
 
 namespace attn {
@@ -239,6 +240,29 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b, __half*) {
   return s;
 }
 
+__device__ __forceinline__ float2 pair_to_float2(uint32_t x, __nv_bfloat16*) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x));
+}
+__device__ __forceinline__ float2 pair_to_float2(uint32_t x, __half*) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+
+// Eight numbers of an 8-bit checkpoint (a.x, a.y, scale exponent a.z) times 8 values.
+template <typename T>
+__device__ __forceinline__ float dot8_ck(uint4 a, uint4 b) {
+  float o[8], s = 0.f;
+  ck_values8<T>(make_uint2(a.x, a.y), ck_scale(a.z), o);
+  const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 d = pair_to_float2(w[i], (T*)nullptr);
+    s = fmaf(o[2 * i], d.x, s);
+    s = fmaf(o[2 * i + 1], d.y, s);
+  }
+  return s;
+}
+
+
 // Padded group layout: gradient rows that belong to no segment are zero.
 // Gap g in [0, nseg] holds the rows from the end of segment g-1 (row 0 for
 // g = 0) up to the start of segment g (the row total for g = nseg); the
@@ -324,8 +348,10 @@ __device__ __forceinline__ void batch_schedule(const Problem& P, int sched, long
 }
 
 // VW: 16-byte vectors per lane and row (1 for d_v <= 128, 2 for d_v = 256).
-template <typename T, int VW>
-__global__ void __launch_bounds__(256, PRE_BLOCKS_PER_SM) preprocess_kernel(Problem P, long long ntok, int sched) {
+// CK: O is an 8-bit checkpoint's (16-bit types; 8 bytes and a scale per lane and row
+// instead of 16 bytes).
+template <typename T, int VW, bool CK = false>
+__global__ void __launch_bounds__(256, PRE_BLOCKS_PER_SM) preprocess_kernel(Problem P, long long ntok, int sched, CkO ck) {
   const int lane = threadIdx.x & 31;
   const long long tid = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const long long nthreads = (long long)gridDim.x * blockDim.x;
@@ -343,6 +369,19 @@ __global__ void __launch_bounds__(256, PRE_BLOCKS_PER_SM) preprocess_kernel(Prob
     const uint4* dO = static_cast<const uint4*>(P.dout);
     const int nv = P.dv / 8;
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    // 8 values of O; of a checkpoint: its numbers and their scale's exponent
+    auto load_o = [&](long long oo, int piece) -> uint4 {
+      if constexpr (CK) {
+        const uint2 n = __ldcs(reinterpret_cast<const uint2*>(ck.n + oo) + piece);
+        return make_uint4(n.x, n.y, __ldg(ck.exp + ((oo >> 5) + (piece >> 2))), 0u);
+      } else {
+        return __ldcs(O + (oo >> 3) + piece);
+      }
+    };
+    auto dot = [&](const uint4& o, const uint4& d) {
+      if constexpr (CK) return dot8_ck<T>(o, d);
+      else return dot8(o, d, (T*)nullptr);
+    };
     // the trip count is warp-uniform (the shuffles below take the full mask)
     for (long long w0 = (hw >> 1) * 2 * RPH; w0 < nrows; w0 += nhw * RPH) {
       const long long r0 = w0 + (hw & 1) * RPH;
@@ -361,11 +400,11 @@ __global__ void __launch_bounds__(256, PRE_BLOCKS_PER_SM) preprocess_kernel(Prob
       for (int i = 0; i < RPH; ++i) {
         const long long r = r0 + i;
         const bool ok = r < nrows && sub < nv;
-        a[i] = ok ? __ldcs(O + (oo >> 3) + sub) : z;
+        a[i] = ok ? load_o(oo, sub) : z;
         b[i] = ok ? __ldcs(dO + (od >> 3) + sub) : z;
         if constexpr (VW == 2) {   // d_v = 256: the second half of the row
           const bool ok2 = r < nrows && sub + 16 < nv;
-          a2[i] = ok2 ? __ldcs(O + (oo >> 3) + sub + 16) : z;
+          a2[i] = ok2 ? load_o(oo, sub + 16) : z;
           b2[i] = ok2 ? __ldcs(dO + (od >> 3) + sub + 16) : z;
         }
         li[i] = P.group ? (long long)h * P.tq + tok : (bq * P.hq + h) * P.sq + q;
@@ -383,8 +422,8 @@ __global__ void __launch_bounds__(256, PRE_BLOCKS_PER_SM) preprocess_kernel(Prob
       }
 #pragma unroll
       for (int i = 0; i < RPH; ++i) {
-        float acc = dot8(a[i], b[i], (T*)nullptr);
-        if constexpr (VW == 2) acc += dot8(a2[i], b2[i], (T*)nullptr);
+        float acc = dot(a[i], b[i]);
+        if constexpr (VW == 2) acc += dot(a2[i], b2[i]);
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
         if (sub == 0 && r0 + i < nrows && li[i] >= 0 && li[i] < P.n_lse) store_row_stats(P, li[i], l[i], acc);
@@ -470,31 +509,41 @@ __global__ void __launch_bounds__(256) dbias_fill_kernel(Problem P) {
 
 // sched: 0 = the scheduler kernel ran before; 1 / 2 = batch mode, this
 // kernel schedules (2: keep an earlier part's status).
-static void launch_preprocess_sched(const Problem& P, cudaStream_t st, int sched) {
+static void launch_preprocess_sched(const Problem& P, cudaStream_t st, int sched, const CkO& ck) {
   const long long ntok = P.group ? (long long)P.tq : (long long)P.nseg * P.sq;
   const int grid = num_sms() * PRE_BLOCKS_PER_SM;   // one resident wave
   const bool wide = P.dv > 128;
+  if (ck.n && P.dtype != ATTN_FP32) {   // fp32 checkpoints are expanded whole
+    if (P.dtype == ATTN_BF16) {
+      if (wide) preprocess_kernel<__nv_bfloat16, 2, true><<<grid, 256, 0, st>>>(P, ntok, sched, ck);
+      else preprocess_kernel<__nv_bfloat16, 1, true><<<grid, 256, 0, st>>>(P, ntok, sched, ck);
+    } else {
+      if (wide) preprocess_kernel<__half, 2, true><<<grid, 256, 0, st>>>(P, ntok, sched, ck);
+      else preprocess_kernel<__half, 1, true><<<grid, 256, 0, st>>>(P, ntok, sched, ck);
+    }
+    return;
+  }
   switch (P.dtype) {
     case ATTN_BF16:
-      if (wide) preprocess_kernel<__nv_bfloat16, 2><<<grid, 256, 0, st>>>(P, ntok, sched);
-      else preprocess_kernel<__nv_bfloat16, 1><<<grid, 256, 0, st>>>(P, ntok, sched);
+      if (wide) preprocess_kernel<__nv_bfloat16, 2><<<grid, 256, 0, st>>>(P, ntok, sched, ck);
+      else preprocess_kernel<__nv_bfloat16, 1><<<grid, 256, 0, st>>>(P, ntok, sched, ck);
       break;
     case ATTN_FP16:
-      if (wide) preprocess_kernel<__half, 2><<<grid, 256, 0, st>>>(P, ntok, sched);
-      else preprocess_kernel<__half, 1><<<grid, 256, 0, st>>>(P, ntok, sched);
+      if (wide) preprocess_kernel<__half, 2><<<grid, 256, 0, st>>>(P, ntok, sched, ck);
+      else preprocess_kernel<__half, 1><<<grid, 256, 0, st>>>(P, ntok, sched, ck);
       break;
-    default: preprocess_kernel<float, 1><<<grid, 256, 0, st>>>(P, ntok, sched); break;
+    default: preprocess_kernel<float, 1><<<grid, 256, 0, st>>>(P, ntok, sched, ck); break;
   }
 }
 
-void launch_preprocess(const Problem& P, cudaStream_t st) { launch_preprocess_sched(P, st, 0); }
+void launch_preprocess(const Problem& P, cudaStream_t st) { launch_preprocess_sched(P, st, 0, {}); }
 
 // Schedule + preprocess of one call (or one part of a call split into parts,
 // keep_status: the earlier parts' status stays).  Group mode validates
 // cu_seqlens in the scheduler kernel first; batch mode folds the schedule into
 // the preprocess kernel (debug builds keep the separate scheduler, whose
 // header reset then precedes every index check of the preprocess).
-void launch_schedule_preprocess(const Problem& P, cudaStream_t st, bool keep_status) {
+void launch_schedule_preprocess(const Problem& P, cudaStream_t st, bool keep_status, const CkO& ck) {
   if (P.dbias != nullptr) {
     const int grid = num_sms() * 4;
     if (P.dtype == ATTN_FP16) dbias_fill_kernel<__half><<<grid, 256, 0, st>>>(P);
@@ -502,12 +551,12 @@ void launch_schedule_preprocess(const Problem& P, cudaStream_t st, bool keep_sta
   }
 #ifndef ATTN_DEBUG
   if (!P.group) {
-    launch_preprocess_sched(P, st, keep_status ? 2 : 1);
+    launch_preprocess_sched(P, st, keep_status ? 2 : 1, ck);
     return;
   }
 #endif
   schedule_kernel<<<1, 256, 0, st>>>(P, keep_status ? 1 : 0);
-  launch_preprocess_sched(P, st, 0);
+  launch_preprocess_sched(P, st, 0, ck);
 }
 
 // ----------------------------------------------------------- reduce/convert

@@ -1,5 +1,6 @@
 // Argument marshalling of the serving entry points (attn_rope, attn_kv_plan,
-// attn_kv_append, attn_kv_fwd) from torch tensors: checks, outputs, the
+// attn_kv_append, attn_kv_fwd) and of the 8-bit checkpoints (attn_checkpoint_save,
+// attn_bwd_checkpoint) from torch tensors: checks, outputs, the
 // parameter struct and the call, in one compiled step.  These calls take a few
 // microseconds of device time; done in Python, reading some forty tensor
 // attributes and allocating through the Python API took 16 to 35 us of host time.
@@ -12,10 +13,12 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
+#include <ATen/ops/empty_strided.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstring>
 #include <string>
 
@@ -31,7 +34,12 @@ struct Entries {
   int (*fwd_size)(const attn_kv_fwd_params*, size_t*);
   int (*fwd)(const attn_kv_fwd_params*, void*, size_t, cudaStream_t);
   int (*fwd_status)(const attn_kv_fwd_params*, const void*, size_t, cudaStream_t, int*);
+  int (*ck_save)(const attn_checkpoint_params*, cudaStream_t);
+  int (*ck_bwd_size)(const attn_bwd_params*, const attn_checkpoint*, size_t*);
+  int (*ck_bwd)(const attn_bwd_params*, const attn_checkpoint*, void*, size_t, cudaStream_t);
+  int (*bwd_status)(const void*, cudaStream_t, int*);
 } entries;
+constexpr int N_ENTRIES = sizeof(entries) / sizeof(void*);
 bool bound = false;
 
 struct Refused {
@@ -166,11 +174,11 @@ bool truth(PyObject* o, const char* what) {
   return t == 1;
 }
 
-// bind(addresses of the six entries)
+// bind(addresses of the entries, in their order)
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 6, [&]() -> PyObject* {
-    void* p[6];
-    for (int i = 0; i < 6; ++i) {
+  return guarded(n, N_ENTRIES, [&]() -> PyObject* {
+    void* p[N_ENTRIES];
+    for (int i = 0; i < N_ENTRIES; ++i) {
       p[i] = reinterpret_cast<void*>(whole(a[i], "an address"));
       if (!p[i]) throw Refused{"a null address"};
     }
@@ -509,10 +517,277 @@ PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ------------------------------------------------------------ checkpoints
+
+// Dimensions of a [B, S, H, D] or [T, H, D] tensor in the order of its memory, the
+// last one apart, outermost first.
+void memory_order(const at::Tensor& t, int order[3]) {
+  const int n = (int)t.dim() - 1;
+  for (int i = 0; i < n; ++i) order[i] = i;
+  for (int i = 1; i < n; ++i)
+    for (int j = i; j > 0 && t.stride(order[j - 1]) < t.stride(order[j]); --j) std::swap(order[j - 1], order[j]);
+}
+
+// {batch, row, head} strides of a [B, S, H, D] or [T, H, D] tensor with contiguous heads.
+void strides3(const at::Tensor& t, const char* what, int64_t out[3]) {
+  if (t.size(-1) > 1 && t.stride(-1) != 1) refuse(what, "contiguous in the head dimension", t);
+  spread(t, what);
+  out[0] = t.dim() == 4 ? t.stride(0) : 0;
+  out[1] = t.stride(-3);
+  out[2] = t.stride(-2);
+}
+
+// {batch, rows, heads} of one, as 32-bit sizes.
+void sizes3(const at::Tensor& t, int32_t* batch, int32_t* rows, int32_t* heads) {
+  for (int64_t i = 0; i < t.dim(); ++i)
+    if (t.size(i) > INT32_MAX) throw Refused{"sizes past 32 bits"};
+  *batch = t.dim() == 4 ? (int32_t)t.size(0) : 1;
+  *rows = (int32_t)t.size(-3);
+  *heads = (int32_t)t.size(-2);
+}
+
+const char* const CK_NAMES[4] = {"q", "k", "v", "o"};
+
+// q, k, v and o of one problem: the same number of dimensions and device, k's rows v's,
+// q's o's.  type: of all four, or undefined for whatever q has.
+void ck_shapes(const at::Tensor* const x[4], at::ScalarType type, int index) {
+  const at::Tensor& q = *x[0];
+  for (int i = 0; i < 4; ++i) {
+    const at::Tensor& t = *x[i];
+    const at::Tensor& rows = *x[i == 2 ? 1 : 0];
+    bool fits = t.scalar_type() == type && t.dim() == q.dim() && on(t, index) && (q.dim() == 3 || q.dim() == 4) &&
+                t.size(-1) == x[i < 2 ? 0 : 2]->size(-1) && (q.dim() == 3 || t.size(0) == q.size(0));
+    if (fits && i >= 2) fits = t.size(-3) == rows.size(-3) && t.size(-2) == rows.size(-2);
+    if (!fits) refuse(CK_NAMES[i], "[B, S, H, D] or [T, H, D] of one problem, one type and one device", t);
+  }
+}
+
+// The tensors of an AttnCheckpoint.
+void read_checkpoint(PyObject* o, const at::Tensor* n[4], const at::Tensor* exp[4], attn_checkpoint* c) {
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 8) throw Refused{"the checkpoint must be an AttnCheckpoint"};
+  for (int i = 0; i < 8; ++i) (i < 4 ? n[i] : exp[i - 4]) = &tensor(PyTuple_GET_ITEM(o, i), "a tensor of the checkpoint");
+  if (!n[0]->is_cuda()) refuse("q of the checkpoint", "on a GPU", *n[0]);
+  const int index = n[0]->get_device();
+  ck_shapes(n, at::kChar, index);
+  int64_t* strides[4] = {c->stride_q, c->stride_k, c->stride_v, c->stride_o};
+  int8_t** to[4] = {&c->q, &c->k, &c->v, &c->o};
+  uint8_t** exps[4] = {&c->q_exp, &c->k_exp, &c->v_exp, &c->o_exp};
+  for (int i = 0; i < 4; ++i) {
+    const at::Tensor &x = *n[i], &e = *exp[i];
+    strides3(x, CK_NAMES[i], strides[i]);
+    *to[i] = pointer<int8_t>(x);
+    bool fits = e.scalar_type() == at::kByte && e.dim() == x.dim() && on(e, index) &&
+                e.size(-1) * ATTN_CKPT_GROUP == x.size(-1) && (e.size(-1) <= 1 || e.stride(-1) == 1);
+    for (int64_t d = 0; fits && d + 1 < x.dim(); ++d)
+      fits = e.size(d) == x.size(d) && (x.size(d) <= 1 || e.stride(d) * ATTN_CKPT_GROUP == x.stride(d));
+    if (!fits) refuse(std::string(CK_NAMES[i]) + "_exp", "uint8, an entry per 32 numbers in their order", e);
+    *exps[i] = pointer<uint8_t>(e);
+  }
+}
+
+// checkpoint(q, k, v, o, AttnCheckpoint or None) -> (status, (its eight tensors))
+PyObject* py_checkpoint(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  return guarded(nargs, 5, [&]() -> PyObject* {
+    const at::Tensor* x[4];
+    for (int i = 0; i < 4; ++i) x[i] = &tensor(a[i], CK_NAMES[i]);
+    attn_checkpoint_params p{};
+    p.dtype = dtype_code(*x[0]);
+    if (p.dtype < 0 || !x[0]->is_cuda()) refuse("q", "bf16, fp16 or fp32 on a GPU", *x[0]);
+    const int index = x[0]->get_device();
+    ck_shapes(x, x[0]->scalar_type(), index);
+    int32_t rows_o, heads_o;
+    sizes3(*x[0], &p.batch, &p.seqlen_q, &p.nhead_q);
+    sizes3(*x[1], &p.batch, &p.seqlen_k, &p.nhead_kv);
+    sizes3(*x[3], &p.batch, &rows_o, &heads_o);
+    for (int i = 0; i < 4; i += 2) {
+      const int64_t d = x[i]->size(-1);
+      if (d > 256) return Py_BuildValue("iO", (int)ATTN_ERR_UNSUPPORTED_HEADDIM, Py_None);
+      (i ? p.d_v : p.d_qk) = (int32_t)d;
+    }
+    int64_t* from[4] = {p.stride_q, p.stride_k, p.stride_v, p.stride_o};
+    const void** at_[4] = {&p.q, &p.k, &p.v, &p.o};
+    for (int i = 0; i < 4; ++i) {
+      strides3(*x[i], CK_NAMES[i], from[i]);
+      *at_[i] = x[i]->data_ptr();
+    }
+    if (p.d_qk % ATTN_CKPT_GROUP || p.d_v % ATTN_CKPT_GROUP || p.d_qk < 1 || p.d_v < 1)
+      return Py_BuildValue("iO", (int)ATTN_ERR_UNSUPPORTED_HEADDIM, Py_None);
+    cudaStream_t stream = stream_of(index);
+    PyObject* out = a[4];
+    if (out == Py_None) {
+      // one block for the eight tensors, which live and die together
+      int64_t begin[8], total = 0;
+      for (int i = 0; i < 8; ++i) {
+        begin[i] = total;
+        total += (x[i & 3]->numel() / (i < 4 ? 1 : ATTN_CKPT_GROUP) + 255) & ~255LL;
+      }
+      const at::Tensor block = at::empty({total}, x[0]->options().dtype(at::kByte));
+      out = PyTuple_New(8);
+      for (int i = 0; i < 8; ++i) {
+        const at::Tensor& s = *x[i & 3];
+        int order[3];
+        memory_order(s, order);
+        const int64_t last = s.size(-1) / (i < 4 ? 1 : ATTN_CKPT_GROUP), dims = s.dim();
+        int64_t size[4], stride[4], next = last;
+        size[dims - 1] = last;
+        stride[dims - 1] = 1;
+        for (int64_t k = dims - 2; k >= 0; --k) {
+          size[order[k]] = s.size(order[k]);
+          stride[order[k]] = next;
+          next *= std::max<int64_t>(1, s.size(order[k]));
+        }
+        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+            c10::Storage(block.storage()), block.key_set(), caffe2::TypeMeta::fromScalarType(i < 4 ? at::kChar : at::kByte));
+        t.unsafeGetTensorImpl()->set_storage_offset(begin[i]);
+        t.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef(size, dims), at::IntArrayRef(stride, dims));
+        PyTuple_SET_ITEM(out, i, THPVariable_Wrap(t));
+      }
+    } else {
+      Py_INCREF(out);
+    }
+    struct Release {
+      PyObject* o;
+      ~Release() { Py_XDECREF(o); }
+    } held{out};
+    const at::Tensor *n[4], *exp[4];
+    read_checkpoint(out, n, exp, &p.ckpt);
+    for (int i = 0; i < 4; ++i) {
+      if (n[i]->sizes() != x[i]->sizes() || !on(*n[i], index)) refuse(std::string("out.") + CK_NAMES[i], "of its input's shape, next to it", *n[i]);
+      if (a[4] != Py_None) {
+        changed(*n[i]);
+        changed(*exp[i]);
+      }
+    }
+    const int st = call([&] { return entries.ck_save(&p, stream); });
+    return Py_BuildValue("iO", st, out);
+  });
+}
+
+// backward(AttnCheckpoint, do, lse, scale, mask, left, right, deterministic, cu_seqlens_q or None, cu_seqlens_k,
+// max_seqlen_q, max_seqlen_k, cu_seqlens_q_padded or None, cu_seqlens_k_padded or None, workspace or None,
+// dq or None, dk, dv, check, bias or None, bias type, return_dbias, dropout_p, seed or None, offset or None)
+// -> (status, step that gave it, dq, dk, dv, dbias or None); steps as attend's
+PyObject* py_backward(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  return guarded(nargs, 25, [&]() -> PyObject* {
+    const at::Tensor *n[4], *exp[4];
+    attn_checkpoint c{};
+    read_checkpoint(a[0], n, exp, &c);
+    const int index = n[0]->get_device();
+    attn_bwd_params p{};
+    int32_t batch, rows_q, rows_k;
+    sizes3(*n[0], &batch, &rows_q, &p.nhead_q);
+    sizes3(*n[1], &batch, &rows_k, &p.nhead_kv);
+    if (n[0]->size(-1) > INT32_MAX || n[2]->size(-1) > INT32_MAX) throw Refused{"sizes past 32 bits"};
+    p.d_qk = (int32_t)n[0]->size(-1);
+    p.d_v = (int32_t)n[2]->size(-1);
+    const bool group = a[8] != Py_None;
+    if ((n[0]->dim() == 3) != group) throw Refused{"cu_seqlens_q and cu_seqlens_k go with [T, H, D] tensors"};
+    if (group) {
+      const at::Tensor& cu = tensor(a[8], "cu_seqlens_q");
+      if (cu.dim() != 1 || cu.size(0) < 1 || cu.size(0) > INT32_MAX) refuse("cu_seqlens_q", "an int32 vector", cu);
+      p.batch = (int32_t)cu.size(0) - 1;
+      p.seqlen_q = whole32(a[10], "max_seqlen_q");
+      p.seqlen_k = whole32(a[11], "max_seqlen_k");
+      p.total_q = rows_q;
+      p.total_k = rows_k;
+      p.cu_seqlens_q = vector<int32_t>(a[8], "cu_seqlens_q", cu.size(0), index);
+      p.cu_seqlens_k = vector<int32_t>(a[9], "cu_seqlens_k", cu.size(0), index);
+      if (a[12] != Py_None) p.cu_seqlens_q_padded = vector<int32_t>(a[12], "cu_seqlens_q_padded", cu.size(0), index);
+      if (a[13] != Py_None) p.cu_seqlens_k_padded = vector<int32_t>(a[13], "cu_seqlens_k_padded", cu.size(0), index);
+    } else {
+      if (a[9] != Py_None || a[12] != Py_None || a[13] != Py_None) throw Refused{"segment offsets need cu_seqlens_q"};
+      p.batch = batch;
+      p.seqlen_q = rows_q;
+      p.seqlen_k = rows_k;
+    }
+    const at::Tensor &dout = tensor(a[1], "do"), &lse = tensor(a[2], "lse");
+    p.dtype = dtype_code(dout);
+    if (p.dtype < 0 || dout.sizes() != n[3]->sizes() || !on(dout, index))
+      refuse("do", "bf16, fp16 or fp32, shaped like the checkpoint's o and next to it", dout);
+    const bool lse_fits = lse.scalar_type() == at::kFloat && on(lse, index) && lse.is_contiguous() &&
+                          (group ? lse.dim() == 2 && lse.size(0) == p.nhead_q && lse.size(1) == rows_q
+                                 : lse.dim() == 3 && lse.size(0) == batch && lse.size(1) == p.nhead_q && lse.size(2) == rows_q);
+    if (!lse_fits) refuse("lse", "contiguous float32 [B, Hq, S] or [Hq, T], as the forward gives it", lse);
+    auto number = [&](PyObject* o, const char* what) {
+      const double v = PyFloat_AsDouble(o);
+      if (v == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        throw Refused{std::string(what) + " must be a number"};
+      }
+      return (float)v;
+    };
+    p.softmax_scale = number(a[3], "scale");
+    p.mask = whole32(a[4], "mask");
+    p.window_left = whole32(a[5], "left");
+    p.window_right = whole32(a[6], "right");
+    p.deterministic = whole32(a[7], "deterministic");
+    p.dout = dout.data_ptr();
+    p.lse = pointer<const float>(lse);
+    strides3(dout, "do", p.stride_dout);
+    p.dropout_p = number(a[22], "dropout_p");
+    if (a[23] != Py_None) p.philox_seed = reinterpret_cast<const uint64_t*>(vector<int64_t>(a[23], "philox_seed", 1, index));
+    if (a[24] != Py_None) p.philox_offset = reinterpret_cast<const uint64_t*>(vector<int64_t>(a[24], "philox_offset", 1, index));
+    if (a[19] != Py_None) {
+      const at::Tensor& bias = tensor(a[19], "bias");
+      if (bias.scalar_type() != dout.scalar_type() || bias.dim() != 4 || bias.size(2) != rows_q || bias.size(3) != rows_k ||
+          !on(bias, index) || !bias.is_contiguous())
+        refuse("bias", "contiguous [1 or B, 1 or Hq, Sq, Sk] in do's type next to it", bias);
+      p.bias_type = whole32(a[20], "bias type");
+      p.bias = bias.data_ptr();
+    }
+    cudaStream_t stream = stream_of(index);
+    at::Tensor g[3], dbias;
+    void** to[3] = {&p.dq, &p.dk, &p.dv};
+    int64_t* strides[3] = {p.stride_dq, p.stride_dk, p.stride_dv};
+    static const char* const names[3] = {"out[0]", "out[1]", "out[2]"};
+    for (int i = 0; i < 3; ++i) {
+      if (a[15] == Py_None) {
+        g[i] = at::empty_strided(n[i]->sizes(), n[i]->strides(), dout.options());
+      } else {
+        g[i] = tensor(a[15 + i], names[i]);
+        if (g[i].scalar_type() != dout.scalar_type() || g[i].sizes() != n[i]->sizes() || !on(g[i], index))
+          refuse(names[i], "in do's type, shaped like the tensor whose gradient it is", g[i]);
+      }
+      strides3(g[i], names[i], strides[i]);
+      *to[i] = g[i].data_ptr();
+    }
+    if (truth(a[21], "return_dbias")) {
+      dbias = at::empty({p.batch, p.nhead_q, rows_q, rows_k}, dout.options());
+      p.dbias = dbias.data_ptr();
+    }
+    auto result = [&](int st, int step) {
+      return Py_BuildValue("iiNNNN", st, step, THPVariable_Wrap(g[0]), THPVariable_Wrap(g[1]), THPVariable_Wrap(g[2]),
+                           dbias.defined() ? THPVariable_Wrap(dbias) : Py_NewRef(Py_None));
+    };
+    size_t need = 0;
+    int st = entries.ck_bwd_size(&p, &c, &need);
+    if (st != ATTN_OK) return result(st, 0);
+    at::Tensor ws;
+    if (a[14] == Py_None) {
+      ws = at::empty({(int64_t)need}, dout.options().dtype(at::kByte));
+    } else {
+      ws = tensor(a[14], "workspace");
+      if (ws.scalar_type() != at::kByte || !on(ws, index) || !ws.is_contiguous())
+        refuse("workspace", "a contiguous uint8 tensor next to do", ws);
+    }
+    if (a[15] != Py_None)
+      for (const at::Tensor& x : g) changed(x);
+    const bool check = truth(a[18], "check_status");
+    const size_t bytes = (size_t)ws.numel();
+    st = call([&] { return entries.ck_bwd(&p, &c, ws.data_ptr(), bytes, stream); });
+    if (st != ATTN_OK || !check) return result(st, 1);
+    int found = ATTN_OK;
+    st = call([&] { return entries.bwd_status(ws.data_ptr(), stream, &found); });
+    return st != ATTN_OK ? result(st, 2) : result(found, 3);
+  });
+}
+
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f))
 PyMethodDef methods[] = {{"bind", FAST(py_bind), METH_FASTCALL, nullptr},     {"rope", FAST(py_rope), METH_FASTCALL, nullptr},
                          {"cache", FAST(py_cache), METH_FASTCALL, nullptr},   {"plan", FAST(py_plan), METH_FASTCALL, nullptr},
                          {"append", FAST(py_append), METH_FASTCALL, nullptr}, {"attend", FAST(py_attend), METH_FASTCALL, nullptr},
+                         {"checkpoint", FAST(py_checkpoint), METH_FASTCALL, nullptr},
+                         {"backward", FAST(py_backward), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -389,6 +389,83 @@ int attn_bwd_static_ws(const attn_bwd_params* p, cudaStream_t stream);
 int attn_selftest_waits(void* scratch, size_t scratch_bytes, cudaStream_t stream, int status[3]);
 
 /* ===================================================================== *
+ * Activation checkpoints in 8 bits: what attn_bwd needs of the forward pass
+ * (q, k, v, o) kept in half the memory until the backward pass, and the
+ * backward pass that reads it.  The pages cited above have no counterpart:
+ * an addition of this library, under its conventions.
+ * ===================================================================== */
+
+#define ATTN_CKPT_GROUP 32   /* consecutive columns of a row and head that share a scale */
+
+/* q, k, v and o in 8 bits.  Element x of a tensor (an element offset) is
+ * n[x] * 2^(exp[x / 32] - 127), limited to the type's largest finite value: a
+ * whole number of -127 .. 127 times the power of two of its group of 32
+ * columns.  Such a value is exact in bf16 and fp32 (and in fp16, as far down
+ * as 2^-24).  An exponent byte of 255 makes the group NaN.
+ * The tensors are dense: any order of batch, rows and heads, without gaps,
+ * the head dimension innermost, so exp has one byte per 32 numbers. */
+typedef struct {
+  int8_t* q;              /* device, 16-byte aligned                               */
+  int8_t* k;
+  int8_t* v;
+  int8_t* o;
+  uint8_t* q_exp;         /* device, an entry per group                            */
+  uint8_t* k_exp;
+  uint8_t* v_exp;
+  uint8_t* o_exp;
+  int64_t stride_q[3];    /* {batch, row, head} strides of the numbers, in elements
+                             (all three 0: contiguous [batch, row, head, d])     */
+  int64_t stride_k[3];
+  int64_t stride_v[3];
+  int64_t stride_o[3];
+} attn_checkpoint;
+
+/* Arguments of attn_checkpoint_save. */
+typedef struct {
+  int32_t dtype;          /* attn_dtype_t of q, k, v and o                         */
+  int32_t batch;          /* rows are [batch, seqlen]; packed tokens: batch = 1    */
+  int32_t nhead_q;
+  int32_t nhead_kv;
+  int32_t seqlen_q;
+  int32_t seqlen_k;
+  int32_t d_qk;           /* multiples of 32 up to 256                             */
+  int32_t d_v;
+  const void* q;          /* device, 16-byte aligned                               */
+  const void* k;
+  const void* v;
+  const void* o;
+  int64_t stride_q[3];    /* {batch, row, head} element strides, multiples of 8 (all
+                             three 0: contiguous); any batch stride              */
+  int64_t stride_k[3];
+  int64_t stride_v[3];
+  int64_t stride_o[3];
+  attn_checkpoint ckpt;   /* written                                               */
+} attn_checkpoint_params;
+
+/* Write the checkpoint of q, k, v and o on `stream` (one kernel).  With amax =
+ * the largest |x| of a group, its scale 2^e is the least with amax <= 127 *
+ * 2^e, e >= -126, and its numbers are x / 2^e rounded to nearest even: no
+ * value moves by more than amax / 127 (half a step of 2^e), but for those of
+ * fp32 groups below 127 * 2^-126.  A group that holds an infinity or a NaN
+ * gets byte 255 and zeros.  Tensors of a side without rows may be null. */
+int attn_checkpoint_save(const attn_checkpoint_params* p, cudaStream_t stream);
+
+/* Workspace bytes attn_bwd_checkpoint needs for *p and *c: those of attn_bwd,
+ * and q, k and v in 16 (FP32: 32, with o) bits.  Host arithmetic alone; of *c
+ * only the strides are looked at. */
+int attn_bwd_checkpoint_workspace_size(const attn_bwd_params* p, const attn_checkpoint* c, size_t* bytes);
+
+/* attn_bwd at the checkpoint's q, k, v and o: *p with its q, k, v and o null and
+ * their strides zero, everything else as in attn_bwd (dtype is that of dout and
+ * of the gradients, lse the forward's, which saw the tensors before they were
+ * rounded; head dims multiples of 32).  Batch order and heads of *c follow the
+ * layout rules of attn_bwd_params, together with dout's and the gradients'.
+ * q, k and v are expanded into the workspace, o is read as it is.  The status
+ * is read with attn_bwd_read_status, as attn_bwd's. */
+int attn_bwd_checkpoint(const attn_bwd_params* p, const attn_checkpoint* c, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream);
+
+/* ===================================================================== *
  * Serving operators: rotary positions, a paged 8-bit key / value cache,
  * its bookkeeping, and attention over it.  One serving step runs
  *   attn_kv_plan -> attn_rope -> attn_kv_append -> attn_kv_fwd
