@@ -83,7 +83,8 @@ class AttnKvPlanParams(ctypes.Structure):
     _fields_ = [("batch", _i32), ("page_size", _i32), ("num_pages", _i32), ("max_blocks", _i32),
                 ("max_tokens", _i32), ("reserved", _i32), ("new_lens", _vp), ("seqlens", _vp), ("seqlens_out", _vp),
                 ("block_table", _vp), ("table_stride", ctypes.c_int64), ("free_pages", _vp), ("free_count", _vp),
-                ("free_count_out", _vp), ("cu_seqlens", _vp), ("positions", _vp), ("slots", _vp), ("status", _vp)]
+                ("free_count_out", _vp), ("cu_seqlens", _vp), ("positions", _vp), ("slots", _vp), ("status", _vp),
+                ("position_offsets", _vp)]
 
 
 class AttnKvAppendParams(ctypes.Structure):
@@ -98,6 +99,27 @@ class AttnKvFwdParams(ctypes.Structure):
                 ("cu_seqlens_q_padded", _vp), ("seqlens_k", _vp), ("block_table", _vp),
                 ("table_stride", ctypes.c_int64), ("q", _vp), ("o", _vp), ("lse", _vp), ("stride_q", _i64x3),
                 ("stride_o", _i64x3), ("cache", AttnKvCache)]
+
+
+class AttnKvWeights(ctypes.Structure):
+    _fields_ = [("weight", _vp), ("position", _vp), ("status", _vp)]
+
+
+class AttnKvWeighParams(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("batch", _i32), ("nhead_q", _i32), ("total_q", _i32), ("max_seqlen_q", _i32),
+                ("max_seqlen_k", _i32), ("max_blocks", _i32), ("mask", _i32), ("window_left", _i32),
+                ("window_right", _i32), ("softmax_scale", _f32), ("decay", _f32), ("cu_seqlens_q", _vp),
+                ("cu_seqlens_q_padded", _vp), ("seqlens_k", _vp), ("block_table", _vp),
+                ("table_stride", ctypes.c_int64), ("position_offsets", _vp), ("q", _vp), ("lse", _vp),
+                ("stride_q", _i64x3), ("weights", AttnKvWeights), ("cache", AttnKvCache)]
+
+
+class AttnKvEvictParams(ctypes.Structure):
+    _fields_ = [("batch", _i32), ("max_seqlen_k", _i32), ("max_blocks", _i32), ("sink", _i32), ("recent", _i32),
+                ("slack", _i32), ("reserved", _i32), ("keep", _vp), ("seqlens", _vp), ("seqlens_out", _vp),
+                ("position_offsets", _vp), ("position_offsets_out", _vp), ("block_table", _vp),
+                ("table_stride", ctypes.c_int64), ("free_pages", _vp), ("free_count", _vp), ("free_count_out", _vp),
+                ("status", _vp), ("weights", AttnKvWeights), ("cache", AttnKvCache)]
 
 
 class AttnCheckpointTensors(ctypes.Structure):
@@ -116,7 +138,7 @@ EXPORTS = ["attn_bwd_workspace_size", "attn_bwd", "attn_bwd_timed", "attn_bwd_re
            "attn_fwd", "attn_status_string", "attn_bwd_static_ws", "attn_selftest_waits", "attn_bwd_host",
            "attn_rope", "attn_kv_plan", "attn_kv_append", "attn_kv_fwd_workspace_size", "attn_kv_fwd",
            "attn_kv_fwd_read_status", "attn_checkpoint_save", "attn_bwd_checkpoint_workspace_size",
-           "attn_bwd_checkpoint"]
+           "attn_bwd_checkpoint", "attn_kv_weigh", "attn_kv_evict_workspace_size", "attn_kv_evict"]
 
 _lib = None
 
@@ -152,6 +174,12 @@ def load(path: str = LIB_PATH):
     lib.attn_kv_fwd.restype = ctypes.c_int
     lib.attn_kv_fwd_read_status.argtypes = [P(AttnKvFwdParams), _vp, ctypes.c_size_t, _vp, P(ctypes.c_int)]
     lib.attn_kv_fwd_read_status.restype = ctypes.c_int
+    lib.attn_kv_weigh.argtypes = [P(AttnKvWeighParams), _vp]
+    lib.attn_kv_weigh.restype = ctypes.c_int
+    lib.attn_kv_evict_workspace_size.argtypes = [P(AttnKvEvictParams), P(ctypes.c_size_t)]
+    lib.attn_kv_evict_workspace_size.restype = ctypes.c_int
+    lib.attn_kv_evict.argtypes = [P(AttnKvEvictParams), _vp, ctypes.c_size_t, _vp]
+    lib.attn_kv_evict.restype = ctypes.c_int
     lib.attn_checkpoint_save.argtypes = [P(AttnCheckpointParams), _vp]
     lib.attn_checkpoint_save.restype = ctypes.c_int
     lib.attn_bwd_checkpoint_workspace_size.argtypes = [P(AttnBwdParams), P(AttnCheckpointTensors), P(ctypes.c_size_t)]
@@ -227,6 +255,20 @@ def attn_kv_fwd_read_status(p: AttnKvFwdParams, workspace: int, workspace_bytes:
     s = ctypes.c_int(0)
     st = load().attn_kv_fwd_read_status(ctypes.byref(p), workspace, workspace_bytes, stream, ctypes.byref(s))
     return st, s.value
+
+
+def attn_kv_weigh(p: AttnKvWeighParams, stream: int = 0) -> int:
+    return load().attn_kv_weigh(ctypes.byref(p), stream)
+
+
+def attn_kv_evict_workspace_size(p: AttnKvEvictParams):
+    n = ctypes.c_size_t(0)
+    st = load().attn_kv_evict_workspace_size(ctypes.byref(p), ctypes.byref(n))
+    return st, n.value
+
+
+def attn_kv_evict(p: AttnKvEvictParams, workspace: int, workspace_bytes: int, stream: int = 0) -> int:
+    return load().attn_kv_evict(ctypes.byref(p), workspace, workspace_bytes, stream)
 
 
 def attn_checkpoint_save(p: AttnCheckpointParams, stream: int = 0) -> int:
@@ -507,7 +549,8 @@ def _load_marshal():
         m.bind(*(ctypes.cast(getattr(lib, n), _vp).value for n in (
             "attn_rope", "attn_kv_plan", "attn_kv_append", "attn_kv_fwd_workspace_size", "attn_kv_fwd",
             "attn_kv_fwd_read_status", "attn_checkpoint_save", "attn_bwd_checkpoint_workspace_size",
-            "attn_bwd_checkpoint", "attn_bwd_read_status")))
+            "attn_bwd_checkpoint", "attn_bwd_read_status", "attn_kv_weigh", "attn_kv_evict_workspace_size",
+            "attn_kv_evict")))
         _marshal = m
     return _marshal
 
@@ -601,19 +644,22 @@ class KvPlan(NamedTuple):
             raise AttnError(s, "attn_kv_plan (device status)")
 
 
-def kv_plan(new_lens, seqlens, block_table, free_pages, free_count, *, page_size, max_tokens, out=None, stream=None):
+def kv_plan(new_lens, seqlens, block_table, free_pages, free_count, *, page_size, max_tokens, position_offsets=None,
+            out=None, stream=None):
     """Pages, positions and slots for one step (attn_kv_plan).  new_lens and
     seqlens int32 [B] (KV_RELEASE ends a request), block_table int32
     [B, max_blocks] and free_pages int32 [num_pages] are updated in place,
     free_count int32 [1].  Returns a KvPlan, `out` itself when given: its
     seqlens and free_count may be the inputs', so that a captured call
-    advances its state at every replay."""
+    advances its state at every replay.  position_offsets int32 [B], for caches
+    that kv_evict shrinks: tokens forgotten so far, added to the positions and
+    set to 0 for requests that end."""
     if stream is not None:
         with _on_stream(stream):
             return kv_plan(new_lens, seqlens, block_table, free_pages, free_count, page_size=page_size,
-                           max_tokens=max_tokens, out=out)
+                           max_tokens=max_tokens, position_offsets=position_offsets, out=out)
     st, made = (_marshal or _load_marshal()).plan(new_lens, seqlens, block_table, free_pages, free_count, page_size,
-                                                  max_tokens, out)
+                                                  max_tokens, out, position_offsets)
     if st != 0:
         raise AttnError(st, "attn_kv_plan")
     return KvPlan(*made) if out is None else out
@@ -657,6 +703,94 @@ def attn_kv_forward(q, cache: KvCache, block_table, seqlens_k, cu_seqlens_q, *, 
     if st != 0:
         raise AttnError(st, _FWD_STEPS[step])
     return o, lse
+
+
+# ---------------------------------------------------------------- eviction
+
+
+class KvWeights(NamedTuple):
+    """Accumulated attention weight of every cached token next to a KvCache
+    (attn_kv_weights): weight float32 and position int32, both [pages, kv heads,
+    page_size], and the word that keeps the first error of a kv_weigh call."""
+    weight: torch.Tensor
+    position: torch.Tensor
+    status: torch.Tensor
+
+    @classmethod
+    def empty(cls, cache: KvCache):
+        """Weights for a cache, zero everywhere."""
+        shape = (cache.num_pages, cache.nhead_kv, cache.page_size)
+        make = lambda s, t: torch.zeros(s, dtype=t, device=cache.k.device)   # noqa: E731
+        return cls(make(shape, torch.float32), make(shape, torch.int32), make(1, torch.int32))
+
+    def check(self):
+        """Synchronises; raises AttnError if a kv_weigh call since the word was zero
+        found lengths beyond their bounds or pages outside the cache."""
+        s = int(self.status)
+        if s != 0:
+            raise AttnError(s, "attn_kv_weigh (device status)")
+
+
+def kv_weigh(q, lse, cache: KvCache, weights: KvWeights, block_table, seqlens_k, cu_seqlens_q, *, scale,
+             mask=MASK_CAUSAL_BOTTOM_RIGHT, left=-1, right=-1, decay=1.0, position_offsets=None, max_seqlen_q,
+             max_seqlen_k, cu_seqlens_q_padded=None, stream=None):
+    """Add to `weights` what the cached tokens get of the attention of packed
+    queries q (attn_kv_weigh): after attn_kv_forward, with its arguments and its
+    LSE.  The segments' new tokens start from 0 and get their positions, the other
+    tokens' weights are multiplied by `decay` first.  position_offsets int32 [B] as
+    in kv_plan."""
+    if stream is not None:
+        with _on_stream(stream):
+            return kv_weigh(q, lse, cache, weights, block_table, seqlens_k, cu_seqlens_q, scale=scale, mask=mask,
+                            left=left, right=right, decay=decay, position_offsets=position_offsets,
+                            max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k,
+                            cu_seqlens_q_padded=cu_seqlens_q_padded)
+    st = (_marshal or _load_marshal()).weigh(q, lse, cache, cache.index, weights, block_table, seqlens_k, cu_seqlens_q,
+                                             cu_seqlens_q_padded, position_offsets, scale, mask, left, right, decay,
+                                             max_seqlen_q, max_seqlen_k)
+    if st != 0:
+        raise AttnError(st, "attn_kv_weigh")
+
+
+class KvEviction(NamedTuple):
+    """What attn_kv_evict computes: the requests' new lengths, the tokens they have
+    forgotten so far, the free pages, the status word (0 = ATTN_OK), all on the
+    device."""
+    seqlens: torch.Tensor
+    position_offsets: torch.Tensor
+    free_count: torch.Tensor
+    status: torch.Tensor
+
+    def check(self):
+        """Synchronises; raises AttnError if the call was refused."""
+        s = int(self.status)
+        if s != 0:
+            raise AttnError(s, "attn_kv_evict (device status)")
+
+
+_EVICT_STEPS = ("attn_kv_evict_workspace_size", "attn_kv_evict")
+
+
+def kv_evict(cache: KvCache, weights: KvWeights, keep, seqlens, position_offsets, block_table, free_pages, free_count, *,
+             sink=0, recent=0, slack=0, max_seqlen_k, out=None, workspace=None, stream=None):
+    """Shrink requests of more than keep[b] + slack tokens (keep int32 [B], -1:
+    never) to keep[b], kv head by kv head those of the largest accumulated weight
+    (attn_kv_evict); tokens at positions below `sink` and among the last `recent` go
+    last.  cache, weights and free_pages are updated in place.  Returns a
+    KvEviction, `out` itself when given: its seqlens, position_offsets and
+    free_count may be the inputs', so that a captured call advances its state at
+    every replay."""
+    if stream is not None:
+        with _on_stream(stream):
+            return kv_evict(cache, weights, keep, seqlens, position_offsets, block_table, free_pages, free_count,
+                            sink=sink, recent=recent, slack=slack, max_seqlen_k=max_seqlen_k, out=out,
+                            workspace=workspace)
+    st, step, made = (_marshal or _load_marshal()).evict(cache, cache.index, weights, keep, seqlens, position_offsets,
+                                                         block_table, free_pages, free_count, sink, recent, slack,
+                                                         max_seqlen_k, out, workspace)
+    if st != 0:
+        raise AttnError(st, _EVICT_STEPS[step])
+    return KvEviction(*made) if out is None else out
 
 
 # ------------------------------------------------------- 8-bit checkpoints

@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(MAX_THREADS) plan_kernel(const attn_kv_plan_pa
     P.block_table[b * P.table_stride + pages_of(len0[b], shift) + (i - take[b])] = popped(i);
   }
   for (int b = tid; b <= n; b += threads) {
+    if (b < n && P.position_offsets && P.new_lens[b] == ATTN_KV_RELEASE) P.position_offsets[b] = 0;
     P.cu_seqlens[b] = cu[b];
     if (b < n) P.seqlens_out[b] = len0[b] + cu[b + 1] - cu[b];
   }
@@ -180,16 +181,17 @@ __global__ void __launch_bounds__(MAX_THREADS) plan_kernel(const attn_kv_plan_pa
   if (!fill) return;
   const int total_tok = cu[n];
   for (int t = tid; t < P.max_tokens; t += threads) {
-    int pos = 0;
+    int pos = 0, shift_by = 0;
     long long slot = -1;
     if (t < total_tok) {
       const int b = find(cu, n, t);
+      if (P.position_offsets) shift_by = P.position_offsets[b];
       pos = len0[b] + t - cu[b];
       const int block = pos >> shift, held = pages_of(len0[b], shift);
       const int page = block < held ? P.block_table[b * P.table_stride + block] : popped(take[b] + block - held);
       slot = ((long long)page << shift) + (pos & ((1 << shift) - 1));
     }
-    P.positions[t] = pos;
+    P.positions[t] = pos + shift_by;
     P.slots[t] = slot;
   }
 }
@@ -203,15 +205,16 @@ __global__ void __launch_bounds__(FILL_THREADS) fill_kernel(const attn_kv_plan_p
   __syncthreads();
   const int t = blockIdx.x * FILL_THREADS + threadIdx.x;
   if (t >= P.max_tokens) return;
-  int pos = 0;
+  int pos = 0, shift_by = 0;
   long long slot = -1;
   if (t < cu[n]) {
     const int b = find(cu, n, t);
+    if (P.position_offsets) shift_by = __ldcg(P.position_offsets + b);
     pos = __ldcg(P.seqlens_out + b) - cu[b + 1] + t;
     const int page = __ldcg(P.block_table + b * P.table_stride + (pos >> shift));
     slot = ((long long)page << shift) + (pos & ((1 << shift) - 1));
   }
-  P.positions[t] = pos;
+  P.positions[t] = pos + shift_by;
   P.slots[t] = slot;
 }
 
@@ -232,7 +235,7 @@ static int run(const attn_kv_plan_params* p, cudaStream_t st) {
   for (const void* x : need)
     if (!x || !aligned_to(x, 4)) return ATTN_ERR_INVALID_ARG;
   if (p->max_tokens > 0 && (!p->positions || !p->slots)) return ATTN_ERR_INVALID_ARG;
-  if (!aligned_to(p->positions, 4) || !aligned_to(p->slots, 8)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned_to(p->positions, 4) || !aligned_to(p->slots, 8) || !aligned_to(p->position_offsets, 4)) return ATTN_ERR_INVALID_ARG;
   // The default limit is 48 KB less the static shared memory.  The limit is the
   // kernel's, not the call's: always the same one, so that a call on another thread
   // cannot lower it before the launch.

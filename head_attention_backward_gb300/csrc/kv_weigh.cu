@@ -1,0 +1,315 @@
+// Attention weights of cached tokens (attn_kv_weigh):
+//
+//   w[page, head, row] <- decay w + sum over query rows and heads of the group of
+//                         exp(s q k - LSE),   K = 2^ek Kq per page and kv head.
+//
+// The softmax is not computed again: the LSE of the attention call is its
+// normaliser, so one pass over K is enough, V is not read, and every key's sum is
+// its own: no maximum, no rescaling, nothing to join between CTAs and no atomics.
+// Decoding is bound by memory (1 byte a K value, a quarter of attention's flops a
+// byte), long segments by the products and the exponentials: kv_weigh_tc.cu.
+//
+// * A CTA owns one request, kv head and split of the keys.  The query rows (token x
+//   head of the group) lie in shared memory as fp16 fragments under a power-of-two
+//   scale per row, which is exact unless an element is 2^-28 of its row's largest.
+// * A warp takes tiles of 16 keys in turn, straight from global memory into
+//   registers, the next tile on its way while one is worked on.  S^T = K Q^T in
+//   m16n8k16 products: the 16-row side holds the keys, so a key's sum over query rows
+//   is in four lanes of one warp.  The contraction's order is free, so a lane takes
+//   16 consecutive bytes of a K row as its share of four k-steps: one wide load,
+//   e4m3 to fp16 in one conversion per two values, exactly.
+// * Scores, exponentials, sums and weights are fp32.
+#include <cmath>
+
+#include "kv_weigh.cuh"
+#include "sm100_ptx.cuh"
+
+namespace attn {
+namespace kvweigh {
+
+constexpr int NWARPS = 8;
+constexpr int NTHREADS = 32 * NWARPS;
+constexpr int TILE = 16;
+constexpr int CHUNK = 128;          // query rows in shared memory at a time
+constexpr int MIN_TILES = 2 * NWARPS;
+
+template <typename T> __device__ __forceinline__ float2 up2(uint32_t x);
+template <> __device__ __forceinline__ float2 up2<__nv_bfloat16>(uint32_t x) {
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+template <> __device__ __forceinline__ float2 up2<__half>(uint32_t x) {
+  return __half22float2(*reinterpret_cast<__half2*>(&x));
+}
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int DQK, typename T>
+__global__ void __launch_bounds__(NTHREADS, DQK <= 64 ? 3 : 2) weigh_kernel(const Args A) {
+  constexpr int PIECES = DQK / 64;           // 16-byte pieces of a K row in a lane
+  constexpr int FRAGS = DQK / 32;            // 16-byte pieces of a row group's fragments in a lane
+  extern __shared__ uint4 s_q[];             // [row group][FRAGS][lane]
+  __shared__ float2 s_row[CHUNK];            // log2 units per raw score, log2-scaled LSE (infinite: adds nothing)
+  __shared__ int s_tok[CHUNK];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int job = blockIdx.x / A.nsplit, split = blockIdx.x - job * A.nsplit;
+  const int b = job / A.c.hkv, hk = job - b * A.c.hkv;
+  const Segment J = segment_of(A, b);
+  if (J.bad && tid == 0 && split == 0 && hk == 0) report(A, ATTN_ERR_BAD_SEQLENS);
+  if (J.lq <= 0 || J.lq > A.long_from) return;
+  const MaskArgs mk = mask_args(A.mask, A.left, A.right, J.lq, J.lk);
+  // keys whose weights change: those that a query sees, or all if the old ones decay
+  int kfrom, kto;
+  seen_by(mk, J.lk, 0, J.lq - 1, kfrom, kto);
+  if (A.decay != 1.f) kfrom = 0, kto = J.lk - 1;
+  const int fresh = A.fresh ? J.lk - J.lq : J.lk;           // keys from here on start from 0
+  const int k0 = kfrom & ~(TILE - 1), ntile_all = kto >= kfrom ? (kto - k0) / TILE + 1 : 0;
+  const int per = cdiv(max(MIN_TILES, cdiv(ntile_all, A.nsplit)), NWARPS) * NWARPS;
+  const int tile0 = split * per, ntile = min(per, ntile_all - tile0);
+  if (ntile <= 0) return;
+  const int key0 = k0 + tile0 * TILE;
+  const int shift = A.c.page_shift, in_page = (1 << shift) - 1;
+  const int* table = A.table + b * A.table_stride;
+  const int offset = A.offsets ? __ldg(A.offsets + b) : 0;
+  const uint8_t* kbase = A.c.k + hk * A.c.sk.h + (long long)g * A.c.sk.r + t * 16;
+  const int nrow = J.lq * A.g;
+
+  for (int r0 = 0; r0 < nrow; r0 += CHUNK) {
+    const int rows = min(CHUNK, nrow - r0), groups = cdiv(rows, 8);
+    // rows of this chunk, a row group per warp: row g's share of lane t are the 16
+    // elements at pieces t + 4 c
+    if (r0 > 0) __syncthreads();
+    for (int n = warp; n < groups; n += NWARPS) {
+      const int row = r0 + min(8 * n + g, rows - 1);
+      const int i = row / A.g;
+      const int h = hk * A.g + row - i * A.g;
+      const T* qp = static_cast<const T*>(A.q) + elem_off(A.sq, (long long)J.q0 + i, h);
+      uint4 raw[FRAGS];
+      float mx = 0.f;
+#pragma unroll
+      for (int c = 0; c < PIECES; ++c) {
+        const uint4* p = reinterpret_cast<const uint4*>(qp + (t + 4 * c) * 16);
+        raw[2 * c] = __ldg(p);
+        raw[2 * c + 1] = __ldg(p + 1);
+      }
+#pragma unroll
+      for (int x = 0; x < FRAGS; ++x) {
+        const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = up2<T>(w[k]);
+          mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      int e = (int)(__float_as_uint(mx) >> 23) - 127;
+      e = e == 128 ? 14 : max(e, -100);      // infinities stay what they are
+      const float up = exp2_int(14 - e);
+#pragma unroll
+      for (int x = 0; x < FRAGS; ++x) {
+        const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+        uint32_t y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = up2<T>(w[k]);
+          y[k] = pack_h2(f.x * up, f.y * up);
+        }
+        s_q[(n * FRAGS + x) * 32 + lane] = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+      if (t == 0) {
+        const float l = __ldg(A.lse + (long long)h * A.total_q + J.q0 + i);
+        const bool adds = 8 * n + g < rows && fabsf(l) < INFINITY;
+        s_row[8 * n + g] = make_float2(A.scale_log2 * exp2_int(e - 14), adds ? l * 1.4426950408889634f : INFINITY);
+        s_tok[8 * n + g] = i;
+      }
+    }
+    __syncthreads();
+    const int i0 = r0 / A.g, i1 = (r0 + rows - 1) / A.g;
+    int vlo, vhi;                            // keys that any row of the chunk sees
+    seen_by(mk, J.lk, i0, i1, vlo, vhi);
+    const bool first = r0 == 0;
+
+    for (int base = 0; base * NWARPS + warp < ntile; base += 32) {
+      // pages and scales of this warp's next 32 tiles
+      int page = -1, ek = 0;
+      {
+        const int i = (base + lane) * NWARPS + warp;
+        if (i < ntile) {
+          page = __ldg(table + ((key0 + i * TILE) >> shift));
+          if (page < 0 || page >= A.c.num_pages) {
+            page = -1;
+            report(A, ATTN_ERR_BAD_PAGE);
+          } else {
+            ek = kv_exp_of(__ldg(A.c.k_exp + (long long)page * A.c.hkv + hk));
+          }
+        }
+      }
+      const int count = min(32, cdiv(ntile - warp, NWARPS) - base);
+      auto key_at = [&](int j) { return key0 + ((base + j) * NWARPS + warp) * TILE; };
+      auto seen = [&](int j) { return key_at(j) <= vhi && key_at(j) + TILE - 1 >= vlo; };
+      uint4 ka[PIECES][2], kb[PIECES][2];
+      auto load = [&](int j, uint4 (&k)[PIECES][2]) {
+        const int pg = __shfl_sync(0xffffffffu, page, j);
+        if (pg < 0 || !seen(j)) return;
+        const uint8_t* p = kbase + pg * A.c.sk.p + (long long)(key_at(j) & in_page) * A.c.sk.r;
+#pragma unroll
+        for (int c = 0; c < PIECES; ++c) {
+          k[c][0] = __ldg(reinterpret_cast<const uint4*>(p + c * 64));
+          k[c][1] = __ldg(reinterpret_cast<const uint4*>(p + 8 * A.c.sk.r + c * 64));
+        }
+      };
+      auto work = [&](int j, const uint4 (&k)[PIECES][2]) {
+        const int pg = __shfl_sync(0xffffffffu, page, j);
+        const float scale = exp2_int(__shfl_sync(0xffffffffu, ek, j));
+        const int key = key_at(j);
+        if (pg < 0 || (!first && !seen(j))) return;
+        // the old weights: lane t = 0 has key g, t = 1 key g + 8
+        const int mine = key + g + 8 * t;
+        const bool owns = t < 2 && mine >= kfrom && mine <= kto;
+        const long long at = ((long long)pg * A.c.hkv + hk) * (in_page + 1) + (mine & in_page);
+        float old = 0.f;
+        const bool is_fresh = mine >= fresh;
+        if (owns && (!first || !(is_fresh || A.decay == 0.f))) old = A.weight[at];
+        if (first) old *= A.decay;
+        float sum[2] = {0.f, 0.f};
+        if (seen(j)) {
+          const bool full = whole(mk, J.lk, i0, i1, key, key + TILE - 1);
+          for (int n = 0; n < groups; ++n) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < FRAGS; ++x) {
+              const uint4 q = s_q[(n * FRAGS + x) * 32 + lane];
+              const uint4 &r = k[x >> 1][0], &r8 = k[x >> 1][1];
+              const uint32_t w0[4] = {r.x, r.y, r.z, r.w}, w8[4] = {r8.x, r8.y, r8.z, r8.w};
+#pragma unroll
+              for (int s = 0; s < 2; ++s) {
+                const int word = (x & 1) * 2 + s;
+                const uint32_t a[4] = {e4m3x2_to_h2((uint16_t)w0[word]), e4m3x2_to_h2((uint16_t)w8[word]),
+                                       e4m3x2_to_h2((uint16_t)(w0[word] >> 16)), e4m3x2_to_h2((uint16_t)(w8[word] >> 16))};
+                mma16816(c, a, s ? q.z : q.x, s ? q.w : q.y);
+              }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float2 u = s_row[8 * n + 2 * t + r];
+              const int tok = s_tok[8 * n + 2 * t + r];
+#pragma unroll
+              for (int kk = 0; kk < 2; ++kk) {
+                const bool adds = u.y < INFINITY && (full || sees(mk, tok, key + g + 8 * kk));
+                const float p = fast_exp2(fmaf(c[2 * kk + r], u.x * scale, -u.y));
+                sum[kk] += adds ? p : 0.f;
+              }
+            }
+          }
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk) {
+            sum[kk] += __shfl_xor_sync(0xffffffffu, sum[kk], 1);
+            sum[kk] += __shfl_xor_sync(0xffffffffu, sum[kk], 2);
+          }
+        }
+        if (owns) {
+          A.weight[at] = old + (t == 0 ? sum[0] : sum[1]);
+          if (first && is_fresh) A.position[at] = (int)((unsigned)mine + (unsigned)offset);
+        }
+      };
+      load(0, ka);
+      for (int j = 0; j < count; j += 2) {
+        if (j + 1 < count) load(j + 1, kb);
+        work(j, ka);
+        if (j + 2 < count) load(j + 2, ka);
+        if (j + 1 < count) work(j + 1, kb);
+      }
+    }
+  }
+}
+
+template <int DQK, typename T>
+static int launch(const Args& a, int grid, int groups, cudaStream_t st) {
+  const size_t smem = (size_t)groups * (DQK / 32) * 32 * 16, most = (size_t)(CHUNK / 8) * (DQK / 32) * 32 * 16;
+  // the limit is the kernel's, always the same one
+  if (smem > 32 * 1024 &&
+      !succeeded(cudaFuncSetAttribute(weigh_kernel<DQK, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most)))
+    return ATTN_ERR_CUDA;
+  weigh_kernel<DQK, T><<<grid, NTHREADS, smem, st>>>(a);
+  return succeeded(cudaGetLastError()) ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+template <typename T>
+static int launch(const Args& a, int dqk, int grid, int groups, cudaStream_t st) {
+  if (dqk == 64) return launch<64, T>(a, grid, groups, st);
+  if (dqk == 128) return launch<128, T>(a, grid, groups, st);
+  if (dqk == 192) return launch<192, T>(a, grid, groups, st);
+  return launch<256, T>(a, grid, groups, st);
+}
+
+static int run(const attn_kv_weigh_params* p, cudaStream_t st) {
+  if (!p || (p->dtype != ATTN_BF16 && p->dtype != ATTN_FP16)) return ATTN_ERR_INVALID_ARG;
+  Args a{};
+  const int s = kv_resolve(p->cache, &a.c);
+  if (s != ATTN_OK) return s;
+  if (p->batch < 1 || p->nhead_q < 1 || p->nhead_q % p->cache.nhead_kv != 0 || p->total_q < 0 || p->max_seqlen_q < 0 ||
+      p->max_seqlen_k < 0 || p->max_blocks < 1 || p->table_stride < p->max_blocks || p->table_stride >= (1LL << 36))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->total_q > (1 << 30) || ((long long)p->max_blocks << a.c.page_shift) > (1LL << 30) ||
+      (long long)p->batch * p->cache.nhead_kv > (1 << 24) || p->nhead_q > (1 << 20))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->mask < ATTN_MASK_NONE || p->mask > ATTN_MASK_WINDOW) return ATTN_ERR_INVALID_ARG;
+  if (p->mask == ATTN_MASK_WINDOW && (p->window_left < -1 || p->window_right < -1)) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(p->softmax_scale) || p->softmax_scale == 0.f || !std::isfinite(p->decay) || p->decay < 0.f)
+    return ATTN_ERR_INVALID_ARG;
+  const void* words[] = {p->cu_seqlens_q, p->seqlens_k, p->block_table, p->weights.weight, p->weights.position, p->weights.status};
+  for (const void* x : words)
+    if (!x || !aligned_to(x, 4)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned_to(p->cu_seqlens_q_padded, 4) || !aligned_to(p->position_offsets, 4) || !aligned_to(p->lse, 4) ||
+      !aligned_to(p->q, 16) || !packed_strides(p->stride_q, p->nhead_q, p->cache.d_qk, &a.sq))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->total_q == 0) return ATTN_OK;
+  if (!p->q || !p->lse) return ATTN_ERR_INVALID_ARG;
+  a.q = p->q;
+  a.lse = p->lse;
+  a.cu_q = p->cu_seqlens_q;
+  a.st_q = p->cu_seqlens_q_padded ? p->cu_seqlens_q_padded : p->cu_seqlens_q;
+  a.len_k = p->seqlens_k;
+  a.table = p->block_table;
+  a.table_stride = p->table_stride;
+  a.offsets = p->position_offsets;
+  const long long cap = (long long)p->max_blocks << a.c.page_shift;
+  a.max_k = p->max_seqlen_k < cap ? p->max_seqlen_k : (int)cap;
+  a.total_q = p->total_q;
+  a.max_q = p->max_seqlen_q;
+  a.hq = p->nhead_q;
+  a.g = p->nhead_q / p->cache.nhead_kv;
+  a.mask = p->mask;
+  a.left = p->mask == ATTN_MASK_WINDOW ? p->window_left : -1;
+  a.right = p->mask == ATTN_MASK_WINDOW ? p->window_right : -1;
+  a.fresh = p->mask == ATTN_MASK_CAUSAL_BOTTOM_RIGHT || p->mask == ATTN_MASK_WINDOW;
+  a.scale_log2 = p->softmax_scale * 1.4426950408889634f;
+  a.decay = p->decay;
+  a.weight = p->weights.weight;
+  a.position = p->weights.position;
+  a.status = p->weights.status;
+  a.long_from = 1 << 30;
+  const int jobs = p->batch * p->cache.nhead_kv;
+  const int tiles = cdiv(a.max_k, TILE);
+  int nsplit = 2560 / jobs;
+  nsplit = nsplit < cdiv(tiles, MIN_TILES) ? nsplit : cdiv(tiles, MIN_TILES);
+  a.nsplit = nsplit < 1 ? 1 : nsplit;
+  const long long most = (long long)(p->max_seqlen_q < p->total_q ? p->max_seqlen_q : p->total_q) * a.g;
+  const int groups = cdiv(most < CHUNK ? (int)most : CHUNK, 8);
+  return p->dtype == ATTN_BF16 ? launch<__nv_bfloat16>(a, p->cache.d_qk, jobs * a.nsplit, groups, st)
+                               : launch<__half>(a, p->cache.d_qk, jobs * a.nsplit, groups, st);
+}
+
+}  // namespace kvweigh
+}  // namespace attn
+
+extern "C" int attn_kv_weigh(const attn_kv_weigh_params* p, cudaStream_t stream) { return attn::kvweigh::run(p, stream); }

@@ -1,0 +1,71 @@
+// What the two kernels of attn_kv_weigh share.
+#pragma once
+
+#include "common.cuh"
+#include "kv_common.cuh"
+
+namespace attn {
+namespace kvweigh {
+
+struct Args {
+  const void* q;
+  const float* lse;
+  Strides sq;
+  const int* cu_q;
+  const int* st_q;
+  const int* len_k;
+  const int* table;
+  long long table_stride;
+  const int* offsets;      // of positions, per request, or null
+  int max_k;               // min(max_seqlen_k, max_blocks pages)
+  int total_q, max_q;
+  int long_from;           // segments of more tokens are the other kernel's
+  int hq, g;               // query heads, per kv head
+  int mask, left, right;
+  int fresh;               // 1: the last tokens of a segment's keys are its new ones
+  float scale_log2, decay;
+  int nsplit;              // most splits of a request's keys
+  float* weight;           // [page][kv head][row]
+  int* position;
+  int* status;
+  KvCacheView c;
+};
+
+struct Segment {
+  int lq, lk, q0;
+  bool bad;                // lengths outside the declared bounds: left alone
+};
+__device__ __forceinline__ Segment segment_of(const Args& A, int b) {
+  Segment s;
+  s.lq = __ldg(A.cu_q + b + 1) - __ldg(A.cu_q + b);
+  s.q0 = __ldg(A.st_q + b);
+  s.lk = __ldg(A.len_k + b);
+  s.bad = s.lq < 0 || s.lq > A.max_q || s.q0 < 0 || (long long)s.q0 + s.lq > A.total_q || s.lk < 0 || s.lk > A.max_k;
+  if (s.bad) s.lq = 0;
+  return s;
+}
+
+__device__ __forceinline__ void report(const Args& A, int code) { atomicCAS(A.status, 0, code); }
+
+// Keys that any of the query tokens i0 .. i1 sees, lo > hi: none.
+__device__ __forceinline__ void seen_by(const MaskArgs& m, int lk, int i0, int i1, int& lo, int& hi) {
+  lo = 0;
+  hi = lk - 1;
+  if (m.left >= 0) lo = (int)max(0ll, (long long)i0 + m.off - m.left);
+  if (m.right >= 0) hi = (int)min((long long)hi, (long long)i1 + m.off + m.right);
+}
+
+// Whether all of them see all of the keys j0 .. j1.
+__device__ __forceinline__ bool whole(const MaskArgs& m, int lk, int i0, int i1, int j0, int j1) {
+  return j1 < lk && (m.left < 0 || j0 >= (long long)i1 + m.off - m.left) &&
+         (m.right < 0 || j1 <= (long long)i0 + m.off + m.right);
+}
+
+// Whether token i sees key j.
+__device__ __forceinline__ bool sees(const MaskArgs& m, int i, int j) {
+  const long long c = (long long)i + m.off;
+  return (m.left < 0 || j >= c - m.left) && (m.right < 0 || j <= c + m.right);
+}
+
+}  // namespace kvweigh
+}  // namespace attn

@@ -1,5 +1,5 @@
 // Argument marshalling of the serving entry points (attn_rope, attn_kv_plan,
-// attn_kv_append, attn_kv_fwd) and of the 8-bit checkpoints (attn_checkpoint_save,
+// attn_kv_append, attn_kv_fwd, attn_kv_weigh, attn_kv_evict) and of the 8-bit checkpoints (attn_checkpoint_save,
 // attn_bwd_checkpoint) from torch tensors: checks, outputs, the
 // parameter struct and the call, in one compiled step.  These calls take a few
 // microseconds of device time; done in Python, reading some forty tensor
@@ -38,6 +38,9 @@ struct Entries {
   int (*ck_bwd_size)(const attn_bwd_params*, const attn_checkpoint*, size_t*);
   int (*ck_bwd)(const attn_bwd_params*, const attn_checkpoint*, void*, size_t, cudaStream_t);
   int (*bwd_status)(const void*, cudaStream_t, int*);
+  int (*weigh)(const attn_kv_weigh_params*, cudaStream_t);
+  int (*evict_size)(const attn_kv_evict_params*, size_t*);
+  int (*evict)(const attn_kv_evict_params*, void*, size_t, cudaStream_t);
 } entries;
 constexpr int N_ENTRIES = sizeof(entries) / sizeof(void*);
 bool bound = false;
@@ -348,10 +351,11 @@ at::Tensor piece(const at::Tensor& base, int64_t at, int64_t n) {
   return t;
 }
 
-// plan(new_lens, seqlens, block_table, free_pages, free_count, page_size, max_tokens, out or None)
+// plan(new_lens, seqlens, block_table, free_pages, free_count, page_size, max_tokens, out or None,
+// position_offsets or None)
 // -> (status, (cu_seqlens, seqlens, positions, slots, free_count, status word))
 PyObject* py_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 8, [&]() -> PyObject* {
+  return guarded(n, 9, [&]() -> PyObject* {
     const at::Tensor &lens = tensor(a[0], "new_lens"), &free = tensor(a[3], "free_pages");
     if (!lens.is_cuda() || lens.dim() != 1) refuse("new_lens", "an int32 vector on a GPU", lens);
     if (free.dim() != 1) refuse("free_pages", "an int32 vector next to new_lens", free);
@@ -370,6 +374,7 @@ PyObject* py_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.free_pages = vector<int32_t>(a[3], "free_pages", pages, index);
     p.free_count = vector<int32_t>(a[4], "free_count", 1, index);
     if (p.max_tokens < 0) throw Refused{"max_tokens must not be negative"};
+    if (a[8] != Py_None) p.position_offsets = vector<int32_t>(a[8], "position_offsets", batch, index);
     cudaStream_t stream = stream_of(index);
     PyObject* out = a[7];
     at::Tensor view[6];
@@ -400,6 +405,7 @@ PyObject* py_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     changed(blocks);
     changed(free);
+    if (a[8] != Py_None) changed(THPVariable_Unpack(a[8]));
     if (out != Py_None)
       for (int i = 0; i < 6; ++i) changed(THPVariable_Unpack(PyTuple_GET_ITEM(out, i)));
     const int st = call([&] { return entries.plan(&p, stream); });
@@ -514,6 +520,141 @@ PyObject* py_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int found = ATTN_OK;
     st = call([&] { return entries.fwd_status(&p, ws.data_ptr(), bytes, stream, &found); });
     return st != ATTN_OK ? result(st, 2) : result(found, 3);
+  });
+}
+
+// KvWeights (weight, position, status) next to a cache.
+void read_weights(PyObject* o, const attn_kv_cache& c, int index, attn_kv_weights* w) {
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 3) throw Refused{"weights must be a KvWeights"};
+  for (int i = 0; i < 2; ++i) {
+    const at::Tensor& t = tensor(PyTuple_GET_ITEM(o, i), i ? "weights.position" : "weights.weight");
+    if (t.scalar_type() != (i ? at::kInt : at::kFloat) || t.dim() != 3 || t.size(0) != c.num_pages ||
+        t.size(1) != c.nhead_kv || t.size(2) != c.page_size || !on(t, index) || !t.is_contiguous())
+      refuse(i ? "weights.position" : "weights.weight",
+             i ? "contiguous int32 [pages, kv heads, page_size] next to the cache"
+               : "contiguous float32 [pages, kv heads, page_size] next to the cache", t);
+    (i ? *reinterpret_cast<void**>(&w->position) : *reinterpret_cast<void**>(&w->weight)) = t.data_ptr();
+  }
+  w->status = vector<int32_t>(PyTuple_GET_ITEM(o, 2), "weights.status", 1, index);
+}
+
+float number(PyObject* o, const char* what) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    throw Refused{std::string(what) + " must be a number"};
+  }
+  return (float)v;
+}
+
+// weigh(q, lse, KvCache, device, KvWeights, block_table, seqlens_k, cu_seqlens_q, cu_seqlens_q_padded or None,
+// position_offsets or None, scale, mask, left, right, decay, max_seqlen_q, max_seqlen_k) -> status
+PyObject* py_weigh(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 17, [&]() -> PyObject* {
+    const at::Tensor &q = tensor(a[0], "q"), &lse = tensor(a[1], "lse"), &lens = tensor(a[6], "seqlens_k");
+    const int index = whole32(a[3], "device");
+    attn_kv_weigh_params p{};
+    read_cache(a[2], &p.cache);
+    read_weights(a[4], p.cache, index, &p.weights);
+    if (!is16(q) || q.dim() != 3 || q.size(0) > INT32_MAX || q.size(1) > INT32_MAX || q.size(2) != p.cache.d_qk ||
+        !on(q, index))
+      refuse("q", "bf16 or fp16 [T, Hq, d_qk] next to the cache", q);
+    if (lens.dim() != 1 || lens.size(0) >= INT32_MAX) refuse("seqlens_k", "an int32 vector", lens);
+    const int64_t t = q.size(0), hq = q.size(1), batch = lens.size(0);
+    if (lse.scalar_type() != at::kFloat || lse.dim() != 2 || lse.size(0) != hq || lse.size(1) != t || !on(lse, index) ||
+        !lse.is_contiguous())
+      refuse("lse", "contiguous float32 [Hq, T] next to q", lse);
+    p.dtype = dtype_code(q);
+    p.batch = (int32_t)batch;
+    p.nhead_q = (int32_t)hq;
+    p.total_q = (int32_t)t;
+    p.block_table = pointer<const int32_t>(table(a[5], batch, index, &p.max_blocks, &p.table_stride));
+    p.seqlens_k = vector<int32_t>(a[6], "seqlens_k", batch, index);
+    p.cu_seqlens_q = vector<int32_t>(a[7], "cu_seqlens_q", batch + 1, index);
+    if (a[8] != Py_None) p.cu_seqlens_q_padded = vector<int32_t>(a[8], "cu_seqlens_q_padded", batch + 1, index);
+    if (a[9] != Py_None) p.position_offsets = vector<int32_t>(a[9], "position_offsets", batch, index);
+    p.softmax_scale = number(a[10], "scale");
+    p.mask = whole32(a[11], "mask");
+    p.window_left = whole32(a[12], "left");
+    p.window_right = whole32(a[13], "right");
+    p.decay = number(a[14], "decay");
+    p.max_seqlen_q = whole32(a[15], "max_seqlen_q");
+    p.max_seqlen_k = whole32(a[16], "max_seqlen_k");
+    p.q = q.data_ptr();
+    p.lse = pointer<const float>(lse);
+    rows3(q, "q", p.stride_q);
+    cudaStream_t stream = stream_of(index);
+    for (int i = 0; i < 3; ++i) changed(THPVariable_Unpack(PyTuple_GET_ITEM(a[4], i)));
+    return PyLong_FromLong(call([&] { return entries.weigh(&p, stream); }));
+  });
+}
+
+// evict(KvCache, device, KvWeights, keep, seqlens, position_offsets, block_table, free_pages, free_count, sink, recent,
+// slack, max_seqlen_k, out or None, workspace or None)
+// -> (status, step that gave it, (seqlens, position_offsets, free_count, status word)); steps: 0 size, 1 launch
+PyObject* py_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 15, [&]() -> PyObject* {
+    const at::Tensor &lens = tensor(a[4], "seqlens"), &free = tensor(a[7], "free_pages");
+    const int index = whole32(a[1], "device");
+    attn_kv_evict_params p{};
+    read_cache(a[0], &p.cache);
+    read_weights(a[2], p.cache, index, &p.weights);
+    if (lens.dim() != 1 || lens.size(0) > INT32_MAX) refuse("seqlens", "an int32 vector", lens);
+    const int64_t batch = lens.size(0);
+    p.batch = (int32_t)batch;
+    p.keep = vector<int32_t>(a[3], "keep", batch, index);
+    p.seqlens = vector<int32_t>(a[4], "seqlens", batch, index);
+    p.position_offsets = vector<int32_t>(a[5], "position_offsets", batch, index);
+    p.block_table = pointer<const int32_t>(table(a[6], batch, index, &p.max_blocks, &p.table_stride));
+    p.free_pages = vector<int32_t>(a[7], "free_pages", p.cache.num_pages, index);
+    p.free_count = vector<int32_t>(a[8], "free_count", 1, index);
+    p.sink = whole32(a[9], "sink");
+    p.recent = whole32(a[10], "recent");
+    p.slack = whole32(a[11], "slack");
+    p.max_seqlen_k = whole32(a[12], "max_seqlen_k");
+    cudaStream_t stream = stream_of(index);
+    PyObject* out = a[13];
+    at::Tensor view[4];
+    if (out == Py_None) {
+      const int64_t at[] = {0, batch, 2 * batch, 2 * batch + 1}, len[] = {batch, batch, 1, 1};
+      const at::Tensor words = at::empty({2 * batch + 2}, lens.options());
+      for (int i = 0; i < 4; ++i) view[i] = piece(words, at[i], len[i]);
+      int32_t* w = pointer<int32_t>(words);
+      p.seqlens_out = w;
+      p.position_offsets_out = w + at[1];
+      p.free_count_out = w + at[2];
+      p.status = w + at[3];
+    } else {
+      if (!PyTuple_Check(out) || PyTuple_GET_SIZE(out) != 4) throw Refused{"out must be a KvEviction"};
+      PyObject** o = &PyTuple_GET_ITEM(out, 0);
+      p.seqlens_out = vector<int32_t>(o[0], "out.seqlens", batch, index);
+      p.position_offsets_out = vector<int32_t>(o[1], "out.position_offsets", batch, index);
+      p.free_count_out = vector<int32_t>(o[2], "out.free_count", 1, index);
+      p.status = vector<int32_t>(o[3], "out.status", 1, index);
+    }
+    auto result = [&](int st, int step) {
+      if (out != Py_None) return Py_BuildValue("iiO", st, step, out);
+      return Py_BuildValue("ii(NNNN)", st, step, THPVariable_Wrap(view[0]), THPVariable_Wrap(view[1]),
+                           THPVariable_Wrap(view[2]), THPVariable_Wrap(view[3]));
+    };
+    size_t need = 0;
+    const int st = entries.evict_size(&p, &need);
+    if (st != ATTN_OK) return result(st, 0);
+    at::Tensor ws;
+    if (a[14] == Py_None) {
+      ws = at::empty({(int64_t)need}, lens.options().dtype(at::kByte));
+    } else {
+      ws = tensor(a[14], "workspace");
+      if (ws.scalar_type() != at::kByte || !on(ws, index) || !ws.is_contiguous())
+        refuse("workspace", "a contiguous uint8 tensor next to the cache", ws);
+    }
+    for (int i = 0; i < 4; ++i) changed(THPVariable_Unpack(PyTuple_GET_ITEM(a[0], i)));
+    for (int i = 0; i < 2; ++i) changed(THPVariable_Unpack(PyTuple_GET_ITEM(a[2], i)));
+    changed(free);
+    if (out != Py_None)
+      for (int i = 0; i < 4; ++i) changed(THPVariable_Unpack(PyTuple_GET_ITEM(out, i)));
+    const size_t bytes = (size_t)ws.numel();
+    return result(call([&] { return entries.evict(&p, ws.data_ptr(), bytes, stream); }), 1);
   });
 }
 
@@ -708,14 +849,6 @@ PyObject* py_backward(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                           (group ? lse.dim() == 2 && lse.size(0) == p.nhead_q && lse.size(1) == rows_q
                                  : lse.dim() == 3 && lse.size(0) == batch && lse.size(1) == p.nhead_q && lse.size(2) == rows_q);
     if (!lse_fits) refuse("lse", "contiguous float32 [B, Hq, S] or [Hq, T], as the forward gives it", lse);
-    auto number = [&](PyObject* o, const char* what) {
-      const double v = PyFloat_AsDouble(o);
-      if (v == -1.0 && PyErr_Occurred()) {
-        PyErr_Clear();
-        throw Refused{std::string(what) + " must be a number"};
-      }
-      return (float)v;
-    };
     p.softmax_scale = number(a[3], "scale");
     p.mask = whole32(a[4], "mask");
     p.window_left = whole32(a[5], "left");
@@ -786,6 +919,7 @@ PyObject* py_backward(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
 PyMethodDef methods[] = {{"bind", FAST(py_bind), METH_FASTCALL, nullptr},     {"rope", FAST(py_rope), METH_FASTCALL, nullptr},
                          {"cache", FAST(py_cache), METH_FASTCALL, nullptr},   {"plan", FAST(py_plan), METH_FASTCALL, nullptr},
                          {"append", FAST(py_append), METH_FASTCALL, nullptr}, {"attend", FAST(py_attend), METH_FASTCALL, nullptr},
+                         {"weigh", FAST(py_weigh), METH_FASTCALL, nullptr},   {"evict", FAST(py_evict), METH_FASTCALL, nullptr},
                          {"checkpoint", FAST(py_checkpoint), METH_FASTCALL, nullptr},
                          {"backward", FAST(py_backward), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

@@ -593,6 +593,10 @@ typedef struct {
   int64_t* slots;            /* device output, [max_tokens], 8-byte aligned, -1
                                 past the last token                              */
   int32_t* status;           /* device output, [1], attn_status_t                  */
+  int32_t* position_offsets; /* device, [batch], or NULL: tokens that a request has
+                                forgotten (attn_kv_evict).  positions[t] is then
+                                x + position_offsets[b]; entries of requests that
+                                end become 0                                     */
 } attn_kv_plan_params;
 
 /* Enqueue the bookkeeping on `stream`. */
@@ -706,6 +710,112 @@ int attn_kv_fwd(const attn_kv_fwd_params* p, void* workspace, size_t workspace_b
  * whose rows are then NaN) in *status. */
 int attn_kv_fwd_read_status(const attn_kv_fwd_params* p, const void* workspace, size_t workspace_bytes,
                             cudaStream_t stream, int* status);
+
+/* Accumulated attention weight of every cached token, next to a cache: entry
+ * (page, head, row) is that of the token in that row of the page, for that kv
+ * head.  The tokens of one row may differ from head to head after an eviction. */
+typedef struct {
+  float* weight;          /* device, [num_pages, nhead_kv, page_size]              */
+  int32_t* position;      /* device, the same: where in its sequence the token was */
+  int32_t* status;        /* device, [1]: the first attn_status_t that an
+                             attn_kv_weigh call found; kept until it is zeroed   */
+} attn_kv_weights;
+
+/* What the cached tokens got of the attention of new ones.  Segments, masks,
+ * pages, q and LSE are those of the attn_kv_fwd call before it (LSE its output).
+ * For each segment b with query tokens, key j < seqlens_k[b] and kv head:
+ *   weight <- old + sum of exp(softmax_scale * q_i k_j - LSE_i)
+ * over the query rows i that see j and the query heads of the group.  old is
+ * decay * weight, but 0 for the segment's own new tokens: with
+ * ATTN_MASK_CAUSAL_BOTTOM_RIGHT and ATTN_MASK_WINDOW the last Lq of its keys,
+ * whose position becomes j + position_offsets[b] (with the other masks no key
+ * is new).  With decay = 0 the old weights are not read.  Rows whose LSE is not
+ * finite add nothing; a key that holds NaN has weight NaN.
+ * Sums and weights are fp32, scores are sums of exact products; the order of
+ * the additions is fixed by the call's sizes, so a call repeats bit for bit.
+ * A page belongs to one request of a call: where several name it, its weights
+ * are unspecified.  A segment outside its bounds (as in attn_kv_fwd; seqlens_k
+ * outside 0 .. min(max_seqlen_k, max_blocks pages) too) is left alone, the
+ * tokens of a page outside the cache are skipped, and *weights.status has it. */
+typedef struct {
+  int32_t dtype;          /* ATTN_BF16 or ATTN_FP16: type of q                     */
+  int32_t batch;          /* segments, >= 1                                        */
+  int32_t nhead_q;        /* a multiple of cache.nhead_kv                          */
+  int32_t total_q;        /* rows of q                                             */
+  int32_t max_seqlen_q;   /* upper bounds, as in attn_kv_fwd                       */
+  int32_t max_seqlen_k;
+  int32_t max_blocks;     /* columns of block_table                                */
+  int32_t mask;           /* attn_mask_t                                           */
+  int32_t window_left;    /* ATTN_MASK_WINDOW only; -1 = unbounded                 */
+  int32_t window_right;
+  float softmax_scale;    /* finite, not 0                                         */
+  float decay;            /* finite, >= 0; 1 accumulates                           */
+  const int32_t* cu_seqlens_q; /* device, [batch + 1]                              */
+  const int32_t* cu_seqlens_q_padded; /* device, [batch + 1], or NULL              */
+  const int32_t* seqlens_k;    /* device, [batch]                                  */
+  const int32_t* block_table;  /* device, [batch] rows of max_blocks               */
+  int64_t table_stride;        /* elements from row to row, >= max_blocks          */
+  const int32_t* position_offsets; /* device, [batch], or NULL: 0                  */
+  const void* q;          /* device, [total_q, nhead_q, d_qk], 16-byte aligned     */
+  const float* lse;       /* device, [nhead_q, total_q], fp32 natural log          */
+  int64_t stride_q[3];    /* as in attn_kv_fwd_params                              */
+  attn_kv_weights weights;
+  attn_kv_cache cache;    /* only k and k_exp are read                             */
+} attn_kv_weigh_params;
+
+/* Enqueue it on `stream`. */
+int attn_kv_weigh(const attn_kv_weigh_params* p, cudaStream_t stream);
+
+/* Let requests forget tokens.  Request b shrinks to keep[b] tokens if keep[b]
+ * >= 0 and seqlens[b] > keep[b] + slack; others stay as they are.  Each kv head
+ * chooses for itself among rows 0 .. seqlens[b] - 1: the protected ones before
+ * the others (those whose position is below sink, or at least seqlens[b] +
+ * position_offsets[b] - recent: the last `recent` tokens seen), then those of
+ * larger weight (NaN below every number), of equals the lower row.  The rows below keep[b]
+ * that go are filled, in order, by the rows from keep[b] on that stay; no other
+ * row moves.  A row takes its K, V, weight and position along.  The page it comes
+ * to has from then on the larger of its own scale and of those that come in (K
+ * and V apart); where that is more than a row's scale was, the row is rounded
+ * again to it.  seqlens becomes keep[b], position_offsets grows by what went, and
+ * the pages behind the last one needed go back to free_pages, request by
+ * request, in block-table order (their entries in block_table stay).
+ * Attention with ATTN_MASK_CAUSAL_BOTTOM_RIGHT does not depend on the old
+ * tokens' order.  With a window it would: the window counts rows.
+ * If anything is wrong, nothing changes: the outputs repeat the inputs, and
+ * *status is ATTN_ERR_BAD_SEQLENS (a length outside 0 .. min(max_seqlen_k,
+ * max_blocks pages), keep below -1, a free_count outside 0 .. num_pages, or
+ * more pages given back than the stack holds) or ATTN_ERR_BAD_PAGE (a page of a
+ * request that shrinks outside the cache).  A page belongs to one request. */
+typedef struct {
+  int32_t batch;          /* 1 .. ATTN_KV_MAX_BATCH                                */
+  int32_t max_seqlen_k;   /* upper bound on seqlens; workspace follows it          */
+  int32_t max_blocks;     /* columns of block_table, max_blocks * page_size <= 2^30 */
+  int32_t sink;           /* >= 0                                                  */
+  int32_t recent;         /* >= 0                                                  */
+  int32_t slack;          /* >= 0                                                  */
+  int32_t reserved;       /* 0                                                     */
+  const int32_t* keep;       /* device, [batch]; -1: never shrinks                 */
+  const int32_t* seqlens;    /* device, [batch]                                    */
+  int32_t* seqlens_out;      /* device, [batch]; may be seqlens                    */
+  const int32_t* position_offsets; /* device, [batch]                              */
+  int32_t* position_offsets_out;   /* device, [batch]; may be position_offsets     */
+  const int32_t* block_table; /* device, [batch] rows of max_blocks                */
+  int64_t table_stride;      /* elements from row to row, >= max_blocks            */
+  int32_t* free_pages;       /* device, [num_pages], updated                       */
+  const int32_t* free_count; /* device, [1]                                        */
+  int32_t* free_count_out;   /* device, [1]; may be free_count                     */
+  int32_t* status;           /* device output, [1], attn_status_t                  */
+  attn_kv_weights weights;   /* status is not used                                 */
+  attn_kv_cache cache;
+} attn_kv_evict_params;
+
+/* Workspace bytes attn_kv_evict needs for *p: host arithmetic on the scalar
+ * fields alone, about 4 bytes per batch entry, kv head and token of max_seqlen_k. */
+int attn_kv_evict_workspace_size(const attn_kv_evict_params* p, size_t* bytes);
+
+/* Enqueue it on `stream` (two kernels).  `workspace`: device, 256-byte aligned,
+ * contents irrelevant on entry, not shared with another call in flight. */
+int attn_kv_evict(const attn_kv_evict_params* p, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
