@@ -32,6 +32,7 @@ constexpr int NTHREADS = 32 * NWARPS;
 constexpr int TILE = 16;
 constexpr int CHUNK = 128;          // query rows in shared memory at a time
 constexpr int MIN_TILES = 2 * NWARPS;
+constexpr int LONG_ROWS = 64;
 
 template <typename T> __device__ __forceinline__ float2 up2(uint32_t x);
 template <> __device__ __forceinline__ float2 up2<__nv_bfloat16>(uint32_t x) {
@@ -297,7 +298,8 @@ static int run(const attn_kv_weigh_params* p, cudaStream_t st) {
   a.weight = p->weights.weight;
   a.position = p->weights.position;
   a.status = p->weights.status;
-  a.long_from = 1 << 30;
+  // Segments of more query rows than LONG_ROWS go to the tensor cores.
+  a.long_from = a.g <= long_group(p->cache.d_qk) ? LONG_ROWS / a.g : 1 << 30;
   const int jobs = p->batch * p->cache.nhead_kv;
   const int tiles = cdiv(a.max_k, TILE);
   int nsplit = 2560 / jobs;
@@ -305,8 +307,11 @@ static int run(const attn_kv_weigh_params* p, cudaStream_t st) {
   a.nsplit = nsplit < 1 ? 1 : nsplit;
   const long long most = (long long)(p->max_seqlen_q < p->total_q ? p->max_seqlen_q : p->total_q) * a.g;
   const int groups = cdiv(most < CHUNK ? (int)most : CHUNK, 8);
-  return p->dtype == ATTN_BF16 ? launch<__nv_bfloat16>(a, p->cache.d_qk, jobs * a.nsplit, groups, st)
-                               : launch<__half>(a, p->cache.d_qk, jobs * a.nsplit, groups, st);
+  const bool bf16 = p->dtype == ATTN_BF16;
+  const int s2 = bf16 ? launch<__nv_bfloat16>(a, p->cache.d_qk, jobs * a.nsplit, groups, st)
+                      : launch<__half>(a, p->cache.d_qk, jobs * a.nsplit, groups, st);
+  if (s2 != ATTN_OK || most <= (long long)a.long_from * a.g) return s2;
+  return launch_long(a, bf16, p->cache.d_qk, p->batch, st);
 }
 
 }  // namespace kvweigh

@@ -67,5 +67,10 @@ __device__ __forceinline__ bool sees(const MaskArgs& m, int i, int j) {
   return (m.left < 0 || j >= c - m.left) && (m.right < 0 || j <= c + m.right);
 }
 
+// Segments of more than a.long_from tokens, on the tensor cores (kv_weigh_tc.cu), and
+// the most query heads per kv head that it takes.
+int long_group(int dqk);
+int launch_long(const Args& a, bool bf16, int dqk, int batch, cudaStream_t st);
+
 }  // namespace kvweigh
 }  // namespace attn

@@ -94,6 +94,60 @@ def test_weigh_masks_and_decay(B, mask, left, right, decay):
     weigh_case(B, torch.bfloat16, [130, 70, 33], [5, 1, 33], 16, 2, 2, 64, 64, mask, left, right, decay)
 
 
+LONG_WEIGHS = [
+    # lens, new, page, kv heads, group, d, d_v, mask, left, right
+    ([1500, 130], [700, 129], 16, 1, 4, 128, 128, 2, -1, -1), ([260], [260], 64, 2, 3, 64, 64, 2, -1, -1),
+    ([300, 1000, 77], [200, 1, 30], 32, 2, 5, 192, 128, 2, -1, -1), ([129, 600], [128, 140], 256, 1, 2, 256, 256, 2, -1, -1),
+    ([700], [300], 16, 2, 1, 128, 128, 3, 100, 0), ([700, 300], [90, 300], 16, 1, 2, 64, 64, 3, 33, 17),
+    ([400], [200], 16, 1, 128, 64, 64, 2, -1, -1), ([140], [30], 16, 1, 70, 192, 128, 2, -1, -1), ([130, 500], [90, 260], 128, 2, 2, 128, 128, 0, -1, -1),
+    ([90, 40], [200, 100], 16, 1, 2, 128, 128, 2, -1, -1), ([330], [140], 16, 1, 2, 128, 128, 1, -1, -1),
+]
+
+
+@pytest.mark.parametrize("lens,new,page,hkv,group,d,dv,mask,left,right", LONG_WEIGHS)
+@pytest.mark.parametrize("dtype,decay", [(torch.bfloat16, 1.0), (torch.float16, 0.5)])
+def test_weigh_long_segments(B, lens, new, page, hkv, group, d, dv, mask, left, right, dtype, decay):
+    weigh_case(B, dtype, lens, new, page, hkv, group, d, dv, mask, left, right, decay, padded=decay != 1.0)
+
+
+def test_weigh_long_segment_rows_without_a_finite_lse(B):
+    """A query row of NaN in a long segment, and padding rows of NaN behind the last one."""
+    g, table, pool, kc, ke, vc, ve = small(B, lens=(200, 20), d=128)
+    q = torch.randn((150, 4, 128), generator=g).bfloat16()
+    lse = torch.full((4, 150), 3.0)
+    q[7, 1], lse[1, 7] = math.nan, math.nan
+    q[141:], lse[:, 141:] = math.nan, math.nan
+    lse[2, 30] = -math.inf
+    weight, position = random_weights(pool, 2, 16, g)
+    w = weights_of(B, weight, position)
+    B.kv_weigh(q.cuda(), lse.cuda(), handle(B, kc, vc, ke, ve), w, dev(table), dev([200, 20]), dev([0, 140, 141]), scale=0.08,
+               max_seqlen_q=140, max_seqlen_k=208)
+    w.check()
+    q[7, 1] = 0
+    want, where, slack = evict_ref.weigh(q, lse, [0, 140, 141], [200, 20], table, kc, ke, weight, position, [0, 0], 0.08)
+    assert bool(((w.weight.cpu().double() - want).abs() <= slack).all()) and torch.equal(w.position.cpu(), where)
+
+
+def test_weigh_long_segment_reports_pages(B):
+    g, table, pool, kc, ke, vc, ve = small(B, lens=(200, 20), d=64)
+    c = handle(B, kc, vc, ke, ve)
+    q, lse = torch.randn((120, 4, 64), generator=g).bfloat16().cuda(), torch.full((4, 120), 3.0, device="cuda")
+    weight, position = random_weights(pool, 2, 16, g)
+    good, w = weights_of(B, weight, position), weights_of(B, weight, position)
+    kw = dict(scale=0.08, max_seqlen_q=120, max_seqlen_k=208)
+    B.kv_weigh(q, lse, c, good, dev(table), dev([200, 20]), dev([0, 119, 120]), **kw)
+    good.check()
+    broken = [list(r) for r in table]
+    broken[0][5] = pool
+    B.kv_weigh(q, lse, c, w, dev(broken), dev([200, 20]), dev([0, 119, 120]), **kw)
+    with pytest.raises(B.AttnError) as e:
+        w.check()
+    assert e.value.status == B.ATTN_ERR_BAD_PAGE
+    same = [p for p in range(pool) if p != table[0][5]]
+    assert torch.equal(w.weight[same], good.weight[same])
+    assert torch.equal(w.weight[table[0][5]].cpu(), weight[table[0][5]])
+
+
 def test_weigh_more_queries_than_keys(B):
     """Rows that see nothing have LSE = -inf and add nothing."""
     weigh_case(B, torch.bfloat16, [10, 200], [30, 210], 16, 2, 2, 64)
