@@ -12,8 +12,8 @@
 // * A CTA owns one request, kv head and split of the keys.  The query rows (token x
 //   head of the group) lie in shared memory as fp16 fragments under a power-of-two
 //   scale per row, which is exact unless an element is 2^-28 of its row's largest.
-// * A warp takes tiles of 16 keys in turn, straight from global memory into
-//   registers, the next tile on its way while one is worked on.  S^T = K Q^T in
+// * A warp takes tiles of 16 keys in turn, through a ring of its own in shared memory
+//   that each lane fills for itself with asynchronous copies.  S^T = K Q^T in
 //   m16n8k16 products: the 16-row side holds the keys, so a key's sum over query rows
 //   is in four lanes of one warp.  The contraction's order is free, so a lane takes
 //   16 consecutive bytes of a K row as its share of four k-steps: one wide load,
@@ -52,12 +52,45 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int DQK, typename T>
-__global__ void __launch_bounds__(NTHREADS, DQK <= 64 ? 3 : 2) weigh_kernel(const Args A) {
-  constexpr int PIECES = DQK / 64;           // 16-byte pieces of a K row in a lane
-  constexpr int FRAGS = DQK / 32;            // 16-byte pieces of a row group's fragments in a lane
-  extern __shared__ uint4 s_q[];             // [row group][FRAGS][lane]
-  __shared__ float2 s_row[CHUNK];            // log2 units per raw score, log2-scaled LSE (infinite: adds nothing)
+// Copies of a lane's own, read back by that lane alone: no barrier joins the lanes.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+template <int DQK>
+struct Cfg {
+  static constexpr int PIECES = DQK / 64;    // 16-byte pieces of a K row in a lane
+  static constexpr int FRAGS = DQK / 32;     // 16-byte pieces of a row group's fragments in a lane
+  static constexpr int RESIDENT = DQK <= 128 ? 3 : 2;
+  static constexpr int DEPTH = DQK == 64 ? 6 : DQK == 256 ? 3 : 4;   // tiles of a warp's ring
+  static constexpr int STAGE = TILE * DQK + 128;                     // and 16 old weights
+  static constexpr int RING = NWARPS * DEPTH * STAGE;
+  static constexpr int GROUP = FRAGS * 32 * 16;                      // a row group's fragments
+};
+
+// ONE: at most eight query rows, whose fragments stay in registers.
+template <int DQK, typename T, bool ONE>
+__global__ void __launch_bounds__(NTHREADS, Cfg<DQK>::RESIDENT) weigh_kernel(const Args A) {
+  using C = Cfg<DQK>;
+  constexpr int PIECES = C::PIECES, FRAGS = C::FRAGS, DEPTH = C::DEPTH;
+  extern __shared__ uint4 s_all[];           // the warps' rings, then the fragments: [row group][FRAGS][lane]
+  uint4* s_q = s_all + C::RING / 16;
+  __shared__ float2 s_row[CHUNK];            // log2 units per raw score, negated log2-scaled LSE
   __shared__ int s_tok[CHUNK];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -76,172 +109,223 @@ __global__ void __launch_bounds__(NTHREADS, DQK <= 64 ? 3 : 2) weigh_kernel(cons
   const int per = cdiv(max(MIN_TILES, cdiv(ntile_all, A.nsplit)), NWARPS) * NWARPS;
   const int tile0 = split * per, ntile = min(per, ntile_all - tile0);
   if (ntile <= 0) return;
-  const int key0 = k0 + tile0 * TILE;
+  const int key0 = k0 + (tile0 + warp) * TILE;              // this warp's first tile, then every NWARPS-th
+  constexpr int STEP = NWARPS * TILE;
+  const int mine = cdiv(ntile - warp, NWARPS);
   const int shift = A.c.page_shift, in_page = (1 << shift) - 1;
   const int* table = A.table + b * A.table_stride;
   const int offset = A.offsets ? __ldg(A.offsets + b) : 0;
   const uint8_t* kbase = A.c.k + hk * A.c.sk.h + (long long)g * A.c.sk.r + t * 16;
+  const long long krow8 = 8 * A.c.sk.r;
+  const int own = g + 8 * t;                                // the key of a tile that lane t < 2 writes
+  const uint32_t ring = ptx::smem_u32(s_all) + warp * DEPTH * C::STAGE + lane * 16;
+  const uint32_t wring = ptx::smem_u32(s_all) + warp * DEPTH * C::STAGE + TILE * DQK + lane * 4;
   const int nrow = J.lq * A.g;
 
   for (int r0 = 0; r0 < nrow; r0 += CHUNK) {
-    const int rows = min(CHUNK, nrow - r0), groups = cdiv(rows, 8);
-    // rows of this chunk, a row group per warp: row g's share of lane t are the 16
-    // elements at pieces t + 4 c
-    if (r0 > 0) __syncthreads();
-    for (int n = warp; n < groups; n += NWARPS) {
-      const int row = r0 + min(8 * n + g, rows - 1);
-      const int i = row / A.g;
-      const int h = hk * A.g + row - i * A.g;
-      const T* qp = static_cast<const T*>(A.q) + elem_off(A.sq, (long long)J.q0 + i, h);
-      uint4 raw[FRAGS];
-      float mx = 0.f;
-#pragma unroll
-      for (int c = 0; c < PIECES; ++c) {
-        const uint4* p = reinterpret_cast<const uint4*>(qp + (t + 4 * c) * 16);
-        raw[2 * c] = __ldg(p);
-        raw[2 * c + 1] = __ldg(p + 1);
-      }
-#pragma unroll
-      for (int x = 0; x < FRAGS; ++x) {
-        const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = up2<T>(w[k]);
-          mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-      }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      int e = (int)(__float_as_uint(mx) >> 23) - 127;
-      e = e == 128 ? 14 : max(e, -100);      // infinities stay what they are
-      const float up = exp2_int(14 - e);
-#pragma unroll
-      for (int x = 0; x < FRAGS; ++x) {
-        const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
-        uint32_t y[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = up2<T>(w[k]);
-          y[k] = pack_h2(f.x * up, f.y * up);
-        }
-        s_q[(n * FRAGS + x) * 32 + lane] = make_uint4(y[0], y[1], y[2], y[3]);
-      }
-      if (t == 0) {
-        const float l = __ldg(A.lse + (long long)h * A.total_q + J.q0 + i);
-        const bool adds = 8 * n + g < rows && fabsf(l) < INFINITY;
-        s_row[8 * n + g] = make_float2(A.scale_log2 * exp2_int(e - 14), adds ? l * 1.4426950408889634f : INFINITY);
-        s_tok[8 * n + g] = i;
-      }
-    }
-    __syncthreads();
+    const int rows = min(CHUNK, nrow - r0), groups = ONE ? 1 : cdiv(rows, 8);
     const int i0 = r0 / A.g, i1 = (r0 + rows - 1) / A.g;
+    const bool first = r0 == 0;
     int vlo, vhi;                            // keys that any row of the chunk sees
     seen_by(mk, J.lk, i0, i1, vlo, vhi);
-    const bool first = r0 == 0;
+    // keys that all of them see (keys past the last one are never written)
+    const int flo = mk.left >= 0 ? (int)max(0ll, (long long)i1 + mk.off - mk.left) : 0;
+    const int fhi = mk.right >= 0 ? (int)max(-1ll, min((long long)INT32_MAX, (long long)i0 + mk.off + mk.right)) : INT32_MAX;
+    bool staged = false;
+    float2 row[2];
+    uint4 qf[ONE ? FRAGS : 1];
 
-    for (int base = 0; base * NWARPS + warp < ntile; base += 32) {
+    for (int base = 0; base < mine || !staged; base += 32) {
       // pages and scales of this warp's next 32 tiles
+      const int count = min(32, mine - base), key_base = key0 + base * STEP;
       int page = -1, ek = 0;
-      {
-        const int i = (base + lane) * NWARPS + warp;
-        if (i < ntile) {
-          page = __ldg(table + ((key0 + i * TILE) >> shift));
-          if (page < 0 || page >= A.c.num_pages) {
-            page = -1;
-            report(A, ATTN_ERR_BAD_PAGE);
-          } else {
-            ek = kv_exp_of(__ldg(A.c.k_exp + (long long)page * A.c.hkv + hk));
-          }
+      if (lane < count) {
+        page = __ldg(table + ((key_base + lane * STEP) >> shift));
+        if (page < 0 || page >= A.c.num_pages) {
+          page = -1;
+          report(A, ATTN_ERR_BAD_PAGE);
+        } else {
+          ek = kv_exp_of(__ldg(A.c.k_exp + (long long)page * A.c.hkv + hk));
         }
       }
-      const int count = min(32, cdiv(ntile - warp, NWARPS) - base);
-      auto key_at = [&](int j) { return key0 + ((base + j) * NWARPS + warp) * TILE; };
-      auto seen = [&](int j) { return key_at(j) <= vhi && key_at(j) + TILE - 1 >= vlo; };
-      uint4 ka[PIECES][2], kb[PIECES][2];
-      auto load = [&](int j, uint4 (&k)[PIECES][2]) {
-        const int pg = __shfl_sync(0xffffffffu, page, j);
-        if (pg < 0 || !seen(j)) return;
-        const uint8_t* p = kbase + pg * A.c.sk.p + (long long)(key_at(j) & in_page) * A.c.sk.r;
-#pragma unroll
-        for (int c = 0; c < PIECES; ++c) {
-          k[c][0] = __ldg(reinterpret_cast<const uint4*>(p + c * 64));
-          k[c][1] = __ldg(reinterpret_cast<const uint4*>(p + 8 * A.c.sk.r + c * 64));
-        }
+      auto seen = [&](int key) { return key <= vhi && key + TILE - 1 >= vlo; };
+      auto weight_at = [&](int pg, int key) {
+        return (((long long)pg * A.c.hkv + hk) << shift) + ((key + own) & in_page);
       };
-      auto work = [&](int j, const uint4 (&k)[PIECES][2]) {
-        const int pg = __shfl_sync(0xffffffffu, page, j);
+      // tile j into its stage; a group per tile, empty ones too
+      auto load = [&](int j, int stage) {
+        if (j < count) {
+          const int pg = __shfl_sync(0xffffffffu, page, j), key = key_base + j * STEP;
+          if (pg >= 0) {
+            if (seen(key)) {
+              const uint8_t* p = kbase + pg * A.c.sk.p + (long long)(key & in_page) * A.c.sk.r;
+              const uint32_t dst = ring + stage * C::STAGE;
+#pragma unroll
+              for (int c = 0; c < PIECES; ++c) {
+                cp16(dst + c * 1024, p + c * 64);
+                cp16(dst + c * 1024 + 512, p + krow8 + c * 64);
+              }
+            }
+            if (t < 2) cp4(wring + stage * C::STAGE, A.weight + weight_at(pg, key));
+          }
+        }
+        cp_commit();
+      };
+#pragma unroll
+      for (int j = 0; j < DEPTH - 1; ++j) load(j, j);
+
+      if (!staged) {
+        // rows of this chunk, a row group per warp: row g's share of lane t are the 16
+        // elements at pieces t + 4 c; rows that add nothing are zero
+        if (!first) __syncthreads();
+        for (int n = warp; n < groups; n += NWARPS) {
+          const int rr = 8 * n + g;
+          const int rl = r0 + min(rr, rows - 1);
+          const int i = rl / A.g;
+          const int h = hk * A.g + rl - i * A.g;
+          const T* qp = static_cast<const T*>(A.q) + elem_off(A.sq, (long long)J.q0 + i, h);
+          const float l = __ldg(A.lse + (long long)h * A.total_q + J.q0 + i);
+          const bool adds = rr < rows && fabsf(l) < INFINITY;
+          uint4 raw[FRAGS];
+          float mx = 0.f;
+#pragma unroll
+          for (int c = 0; c < PIECES; ++c) {
+            const uint4* p = reinterpret_cast<const uint4*>(qp + (t + 4 * c) * 16);
+            raw[2 * c] = __ldg(p);
+            raw[2 * c + 1] = __ldg(p + 1);
+          }
+#pragma unroll
+          for (int x = 0; x < FRAGS; ++x) {
+            if (!adds) raw[x] = make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = up2<T>(w[k]);
+              mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+          }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          int e = (int)(__float_as_uint(mx) >> 23) - 127;
+          e = e == 128 ? 14 : max(e, -100);      // infinities stay what they are
+          const float up = exp2_int(14 - e);
+#pragma unroll
+          for (int x = 0; x < FRAGS; ++x) {
+            const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+            uint32_t y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = up2<T>(w[k]);
+              y[k] = pack_h2(f.x * up, f.y * up);
+            }
+            s_q[(n * FRAGS + x) * 32 + lane] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+          if (t == 0) {
+            s_row[rr] = make_float2(A.scale_log2 * exp2_int(e - 14), adds ? -l * 1.4426950408889634f : -INFINITY);
+            s_tok[rr] = i;
+          }
+        }
+        __syncthreads();
+        staged = true;
+        if (ONE) {
+#pragma unroll
+          for (int x = 0; x < FRAGS; ++x) qf[ONE ? x : 0] = s_q[x * 32 + lane];
+          row[0] = s_row[2 * t];
+          row[1] = s_row[2 * t + 1];
+        }
+      }
+
+      int stage = 0;
+      for (int j = 0; j < count; ++j) {
+        const int ahead = stage == 0 ? DEPTH - 1 : stage - 1;
+        load(j + DEPTH - 1, ahead);
+        cp_wait<DEPTH - 1>();
+        const int pg = __shfl_sync(0xffffffffu, page, j), key = key_base + j * STEP;
         const float scale = exp2_int(__shfl_sync(0xffffffffu, ek, j));
-        const int key = key_at(j);
-        if (pg < 0 || (!first && !seen(j))) return;
-        // the old weights: lane t = 0 has key g, t = 1 key g + 8
-        const int mine = key + g + 8 * t;
-        const bool owns = t < 2 && mine >= kfrom && mine <= kto;
-        const long long at = ((long long)pg * A.c.hkv + hk) * (in_page + 1) + (mine & in_page);
-        float old = 0.f;
-        const bool is_fresh = mine >= fresh;
-        if (owns && (!first || !(is_fresh || A.decay == 0.f))) old = A.weight[at];
-        if (first) old *= A.decay;
+        const uint32_t src = ring + stage * C::STAGE, old_at = wring + stage * C::STAGE;
+        stage = stage + 1 == DEPTH ? 0 : stage + 1;
+        if (pg < 0) continue;
+        const bool in_view = seen(key);
+        if (!first && !in_view) continue;
         float sum[2] = {0.f, 0.f};
-        if (seen(j)) {
-          const bool full = whole(mk, J.lk, i0, i1, key, key + TILE - 1);
+        if (in_view) {
+          const bool full = key >= flo && key + TILE - 1 <= fhi;
+          uint4 k[PIECES][2];
+#pragma unroll
+          for (int c = 0; c < PIECES; ++c) {
+            k[c][0] = lds128(src + c * 1024);
+            k[c][1] = lds128(src + c * 1024 + 512);
+          }
           for (int n = 0; n < groups; ++n) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int x = 0; x < FRAGS; ++x) {
-              const uint4 q = s_q[(n * FRAGS + x) * 32 + lane];
-              const uint4 &r = k[x >> 1][0], &r8 = k[x >> 1][1];
-              const uint32_t w0[4] = {r.x, r.y, r.z, r.w}, w8[4] = {r8.x, r8.y, r8.z, r8.w};
+              const uint4 q = ONE ? qf[ONE ? x : 0] : s_q[(n * FRAGS + x) * 32 + lane];
+              const uint4 &ra = k[x >> 1][0], &rb = k[x >> 1][1];
+              const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
               for (int s = 0; s < 2; ++s) {
                 const int word = (x & 1) * 2 + s;
-                const uint32_t a[4] = {e4m3x2_to_h2((uint16_t)w0[word]), e4m3x2_to_h2((uint16_t)w8[word]),
-                                       e4m3x2_to_h2((uint16_t)(w0[word] >> 16)), e4m3x2_to_h2((uint16_t)(w8[word] >> 16))};
-                mma16816(c, a, s ? q.z : q.x, s ? q.w : q.y);
+                const uint32_t a[4] = {e4m3x2_to_h2((uint16_t)wa[word]), e4m3x2_to_h2((uint16_t)wb[word]),
+                                       e4m3x2_to_h2((uint16_t)(wa[word] >> 16)), e4m3x2_to_h2((uint16_t)(wb[word] >> 16))};
+                mma16816(acc, a, s ? q.z : q.x, s ? q.w : q.y);
               }
             }
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const float2 u = s_row[8 * n + 2 * t + r];
-              const int tok = s_tok[8 * n + 2 * t + r];
-#pragma unroll
-              for (int kk = 0; kk < 2; ++kk) {
-                const bool adds = u.y < INFINITY && (full || sees(mk, tok, key + g + 8 * kk));
-                const float p = fast_exp2(fmaf(c[2 * kk + r], u.x * scale, -u.y));
-                sum[kk] += adds ? p : 0.f;
-              }
+            if (!ONE) {
+              row[0] = s_row[8 * n + 2 * t];
+              row[1] = s_row[8 * n + 2 * t + 1];
             }
-          }
+            float p[2][2];
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk) {
-            sum[kk] += __shfl_xor_sync(0xffffffffu, sum[kk], 1);
-            sum[kk] += __shfl_xor_sync(0xffffffffu, sum[kk], 2);
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+              for (int kk = 0; kk < 2; ++kk) p[r][kk] = fast_exp2(fmaf(acc[2 * kk + r], row[r].x * scale, row[r].y));
+            if (!full) {
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+                  if (!sees(mk, s_tok[8 * n + 2 * t + r], key + g + 8 * kk)) p[r][kk] = 0.f;
+            }
+            sum[0] += p[0][0] + p[1][0];
+            sum[1] += p[0][1] + p[1][1];
           }
+          // over the four lanes; even lanes end with key g, odd ones with key g + 8
+          const bool odd = t & 1;
+          const float other = __shfl_xor_sync(0xffffffffu, odd ? sum[0] : sum[1], 1);
+          sum[0] = (odd ? sum[1] : sum[0]) + other;
+          sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 2);
         }
-        if (owns) {
-          A.weight[at] = old + (t == 0 ? sum[0] : sum[1]);
-          if (first && is_fresh) A.position[at] = (int)((unsigned)mine + (unsigned)offset);
+        const int at_key = key + own;
+        if (t < 2 && at_key >= kfrom && at_key <= kto) {
+          const long long at = weight_at(pg, key);
+          // (a later chunk adds to what this lane wrote before)
+          float old = first ? lds32(old_at) * A.decay : A.weight[at];
+          const bool is_fresh = at_key >= fresh;
+          if (first && (is_fresh || A.decay == 0.f)) old = 0.f;
+          A.weight[at] = old + sum[0];
+          if (first && is_fresh) A.position[at] = (int)((unsigned)at_key + (unsigned)offset);
         }
-      };
-      load(0, ka);
-      for (int j = 0; j < count; j += 2) {
-        if (j + 1 < count) load(j + 1, kb);
-        work(j, ka);
-        if (j + 2 < count) load(j + 2, ka);
-        if (j + 1 < count) work(j + 1, kb);
       }
+      cp_wait<0>();
     }
   }
 }
 
+template <int DQK, typename T, bool ONE>
+static int launch_rows(const Args& a, int grid, int groups, cudaStream_t st) {
+  using C = Cfg<DQK>;
+  // the limit is the kernel's, always the same one
+  constexpr int MOST = C::RING + (ONE ? 1 : CHUNK / 8) * C::GROUP;
+  if (!succeeded(cudaFuncSetAttribute(weigh_kernel<DQK, T, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST)))
+    return ATTN_ERR_CUDA;
+  weigh_kernel<DQK, T, ONE><<<grid, NTHREADS, C::RING + groups * C::GROUP, st>>>(a);
+  return succeeded(cudaGetLastError()) ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 template <int DQK, typename T>
 static int launch(const Args& a, int grid, int groups, cudaStream_t st) {
-  const size_t smem = (size_t)groups * (DQK / 32) * 32 * 16, most = (size_t)(CHUNK / 8) * (DQK / 32) * 32 * 16;
-  // the limit is the kernel's, always the same one
-  if (smem > 32 * 1024 &&
-      !succeeded(cudaFuncSetAttribute(weigh_kernel<DQK, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most)))
-    return ATTN_ERR_CUDA;
-  weigh_kernel<DQK, T><<<grid, NTHREADS, smem, st>>>(a);
-  return succeeded(cudaGetLastError()) ? ATTN_OK : ATTN_ERR_CUDA;
+  return groups <= 1 ? launch_rows<DQK, T, true>(a, grid, 1, st) : launch_rows<DQK, T, false>(a, grid, groups, st);
 }
 
 template <typename T>
