@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK>::RESIDENT) weigh_kernel(con
   uint4* s_q = s_all + C::RING / 16;
   __shared__ float2 s_row[CHUNK];            // log2 units per raw score, negated log2-scaled LSE
   __shared__ int s_tok[CHUNK];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the long segments' kernel
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int job = blockIdx.x / A.nsplit, split = blockIdx.x - job * A.nsplit;

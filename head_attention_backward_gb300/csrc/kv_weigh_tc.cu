@@ -16,9 +16,9 @@
 // Where there are few key tiles, a cluster of CTAs shares one: each takes every S-th
 // query tile, and the sums are added in the order of the ranks.
 //
-// Warps: 0-3 the exponentials (one per 32 keys), 4 lane 0 loads query tiles (TMA), 5
-// owns TMEM and lane 0 issues the products, 6 keeps the query rows' LSE a few tiles
-// ahead.  Every wait is bounded; where one runs out the keys' weights are NaN and the
+// Warps: 0-7 the exponentials (two per 32 keys, half of the columns each), 8 lane 0 loads
+// query tiles (TMA), 9 owns TMEM and lane 0 issues the products, 10 keeps the query rows'
+// LSE a few tiles ahead.  Every wait is bounded; where one runs out the keys' weights are NaN and the
 // status says so.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -35,9 +35,9 @@ namespace kvweigh {
 using namespace ptx;
 
 constexpr int KM = 128;                 // keys of a CTA
-constexpr int EXP_WARPS = 4;
-constexpr int LOAD_WARP = 4, MMA_WARP = 5, LSE_WARP = 6;
-constexpr int TC_THREADS = 32 * 7;
+constexpr int EXP_WARPS = 8;            // two per 32 keys, half of the query rows each
+constexpr int LOAD_WARP = 8, MMA_WARP = 9, LSE_WARP = 10;
+constexpr int TC_THREADS = 32 * 11;
 constexpr int COL_RING = 4;             // query tiles whose LSE are held
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 
@@ -50,8 +50,8 @@ struct TcCfg {
   static constexpr int OFF_Q = NCH * KCH;
   static constexpr int OFF_NL = OFF_Q + ST * NCH * QCH;      // float[COL_RING][N]: -LSE in log2 units
   static constexpr int OFF_TOK = OFF_NL + COL_RING * N * 4;  // int[N]: token of a row in its tile
-  static constexpr int OFF_SUM = OFF_TOK + N * 4;            // float[KM]: for the cluster
-  static constexpr int OFF_ODD = OFF_SUM + KM * 4;           // int[COL_RING]: a row adds nothing
+  static constexpr int OFF_SUM = OFF_TOK + N * 4;            // float[2][KM]: halves of the sums
+  static constexpr int OFF_ODD = OFF_SUM + 2 * KM * 4;           // int[COL_RING]: a row adds nothing
   static constexpr int NBAR = 2 * ST + 4 + 2 * COL_RING + 1;
   static constexpr int OFF_BAR = OFF_ODD + COL_RING * 4;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
@@ -102,6 +102,14 @@ __device__ __forceinline__ uint32_t widen2(uint16_t x, __nv_bfloat16*) {
   return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);   // their upper halves
 }
 
+// The float at p of CTA `rank`'s shared memory.
+__device__ __forceinline__ float peek(const float* p, int rank) {
+  float x;
+  asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+               : "=f"(x) : "r"(smem_u32(p)), "r"(rank) : "memory");
+  return x;
+}
+
 template <int DQK, typename T>
 __global__ void __launch_bounds__(TC_THREADS, 2) weigh_tc_kernel(const __grid_constant__ CUtensorMap q_map, const TcArgs X) {
   using C = TcCfg<DQK>;
@@ -112,13 +120,16 @@ __global__ void __launch_bounds__(TC_THREADS, 2) weigh_tc_kernel(const __grid_co
   const int jobs = gridDim.x / X.share / X.tiles, kt = item / jobs, job = item - kt * jobs;
   const int b = job / A.c.hkv, hk = job - b * A.c.hkv;
   const Segment J = segment_of(A, b);
-  if (J.lq <= A.long_from) return;            // the other kernel's, or none; the same for the whole cluster
+  // All returns below are the same for the whole cluster, and wait for the short
+  // segments' kernel: this one is not complete before it.
+  auto done = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
+  if (J.lq <= A.long_from) return done();     // the other kernel's, or none
   const MaskArgs mk = mask_args(A.mask, A.left, A.right, J.lq, J.lk);
   int kfrom, kto;
   seen_by(mk, J.lk, 0, J.lq - 1, kfrom, kto);
   if (A.decay != 1.f) kfrom = 0, kto = J.lk - 1;
   const int key0 = (kfrom / KM + kt) * KM;
-  if (kfrom > kto || key0 > kto) return;
+  if (kfrom > kto || key0 > kto) return done();
   const int key1 = min(key0 + KM - 1, J.lk - 1);
   // query tiles with a row that sees one of the keys
   long long i_lo = 0, i_hi = J.lq - 1;
@@ -263,21 +274,37 @@ __global__ void __launch_bounds__(TC_THREADS, 2) weigh_tc_kernel(const __grid_co
       tc_wait(own, C::DRAIN, 0);
     }
   } else if (warp == LSE_WARP) {
+    // rows lane, lane + 32, ... of a tile; all loads of a tile are under way together,
+    // a tile ahead of their use
+    int tok[C::N / 32];
+    const float* head[C::N / 32];
+#pragma unroll
+    for (int k = 0; k < C::N / 32; ++k) {
+      const int r = k * 32 + lane;
+      tok[k] = s_tok[r];
+      head[k] = A.lse + (long long)(hk * A.g + r - tok[k] * A.g) * A.total_q + J.q0;
+    }
+    float l[C::N / 32];
+    auto load = [&](int j) {
+      const int i0 = (qt0 + rank + j * X.share) * X.tok;
+#pragma unroll
+      for (int k = 0; k < C::N / 32; ++k) {
+        const bool in = k * 32 + lane < used && i0 + tok[k] < J.lq;
+        const float v = __ldg(in ? head[k] + i0 + tok[k] : A.lse);
+        l[k] = in ? v : INFINITY;
+      }
+    };
+    if (n > 0) load(0);
     for (int j = 0; j < n; ++j) {
       const int s = j % COL_RING;
-      const int i0 = (qt0 + rank + j * X.share) * X.tok;
       float nl[C::N / 32];
       bool odd = false;
 #pragma unroll
       for (int k = 0; k < C::N / 32; ++k) {
-        const int r = k * 32 + lane, t = r / A.g, i = i0 + t;
-        nl[k] = -INFINITY;
-        if (r < used && i < J.lq) {
-          const float l = __ldg(A.lse + (long long)(hk * A.g + r - t * A.g) * A.total_q + J.q0 + i);
-          if (fabsf(l) < INFINITY) nl[k] = -l * 1.4426950408889634f;
-        }
-        odd |= r < used && nl[k] == -INFINITY;
+        nl[k] = fabsf(l[k]) < INFINITY ? -l[k] * 1.4426950408889634f : -INFINITY;
+        odd |= k * 32 + lane < used && nl[k] == -INFINITY;
       }
+      if (j + 1 < n) load(j + 1);
       if (!tc_wait_warp(ctx, C::C_EMPTY + s, ((j / COL_RING) & 1) ^ 1)) break;
 #pragma unroll
       for (int k = 0; k < C::N / 32; ++k) s_nl[s * C::N + k * 32 + lane] = nl[k];
@@ -287,51 +314,61 @@ __global__ void __launch_bounds__(TC_THREADS, 2) weigh_tc_kernel(const __grid_co
     }
   } else {
     // ------------------------------------------------------- exponentials
-    const int r = warp * 32 + lane, key = key0 + r;
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-    const int page = key <= key1 ? page_of(key) : -1;
-    if (key <= key1 && page < 0) report(A, ATTN_ERR_BAD_PAGE);
+    const int half = warp >> 2, r = (warp & 3) * 32 + lane, key = key0 + r;
+    constexpr int COLS = C::N / 2;
+    const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * COLS;
+    int page = -1;                            // of this thread's key, if its weight changes
+    if (key >= kfrom && key <= kto) {
+      page = page_of(key);
+      if (page < 0) report(A, ATTN_ERR_BAD_PAGE);
+    }
     const float u = page >= 0 ? A.scale_log2 * exp2_int(kv_exp_of(__ldg(A.c.k_exp + (long long)page * A.c.hkv + hk))) : 0.f;
+    // tiles whose first token is at least need0 and whose last one is at most need1 see all keys
+    const int need0 = mk.right >= 0 ? (int)max(0ll, (long long)key1 - mk.off - mk.right) : 0;
+    const int need1 = mk.left >= 0 ? (int)min((long long)INT32_MAX, (long long)key0 - mk.off + mk.left) : INT32_MAX;
+    // tokens that see this thread's key
+    const long long see0 = mk.right >= 0 ? (long long)key - mk.off - mk.right : INT32_MIN;
+    const long long see1 = mk.left >= 0 ? (long long)key - mk.off + mk.left : INT32_MAX;
     const float2 u2 = make_float2(u, u), one2 = make_float2(1.f, 1.f);
-    float2 sum[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) sum[k] = make_float2(0.f, 0.f);
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
+    int i0 = (qt0 + rank) * X.tok;
+    for (int j = 0; j < n; ++j, i0 += X.share * X.tok) {
       const int sb = j & 1, s = j % COL_RING;
       if (!(ok = tc_wait_warp(ctx, C::C_FULL + s, (j / COL_RING) & 1))) break;
       if (!(ok = tc_wait_warp(ctx, C::S_FULL + sb, (j >> 1) & 1))) break;
       tc_fence_after();
-      const int i0 = (qt0 + rank + j * X.share) * X.tok, i1 = min(i0 + X.tok, J.lq) - 1;
-      const bool plain = !s_odd[s] && whole(mk, INT32_MAX, i0, i1, key0, key1);
-      const float4* nl = reinterpret_cast<const float4*>(s_nl + s * C::N);
+      // columns of this warp whose tokens see this thread's key (tokens ascend with the column)
+      const int from = (int)min((long long)C::N, max(0ll, see0 - i0) * A.g) - half * COLS;
+      const int to = (int)min((long long)C::N, max(0ll, see1 - i0 + 1) * A.g) - half * COLS;
+      const bool plain = !s_odd[s] && i0 >= need0 && min(i0 + X.tok, J.lq) - 1 <= need1;
+      const float* nl = s_nl + s * C::N + half * COLS;
 #pragma unroll
-      for (int c = 0; c < C::N; c += 64) {
-        uint32_t v[64];
-        tmem_ld32(lanes + sb * C::N + c, *reinterpret_cast<uint32_t(*)[32]>(v));
-        tmem_ld32(lanes + sb * C::N + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+      for (int c = 0; c < COLS; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(mine + sb * C::N + c, v);
         tmem_wait_ld();
-        if (c + 64 == C::N) {
+        if (c + 32 == COLS) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar + C::S_EMPTY + sb);
         }
         if (plain) {
 #pragma unroll
-          for (int k = 0; k < 64; k += 4) {
-            const float4 l = nl[(c + k) >> 2];
+          for (int k = 0; k < 32; k += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(nl + c + k);
             const float2 x = fma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), u2, make_float2(l.x, l.y));
             const float2 y = fma2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), u2, make_float2(l.z, l.w));
-            sum[(k >> 1) & 3] = fma2(make_float2(fast_exp2(x.x), fast_exp2(x.y)), one2, sum[(k >> 1) & 3]);
-            sum[((k >> 1) + 1) & 3] = fma2(make_float2(fast_exp2(y.x), fast_exp2(y.y)), one2, sum[((k >> 1) + 1) & 3]);
+            sum[0] = fma2(make_float2(fast_exp2(x.x), fast_exp2(x.y)), one2, sum[0]);
+            sum[1] = fma2(make_float2(fast_exp2(y.x), fast_exp2(y.y)), one2, sum[1]);
           }
         } else {
 #pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            const float l = s_nl[s * C::N + c + k];
-            const bool adds = l > -INFINITY && sees(mk, i0 + s_tok[c + k], key);
+          for (int k = 0; k < 32; ++k) {
+            const float l = nl[c + k];
+            const bool adds = l > -INFINITY && c + k >= from && c + k < to;
             const float p = fast_exp2(fmaf(__uint_as_float(v[k]), u, l));
-            (k & 1 ? sum[(k >> 1) & 3].y : sum[(k >> 1) & 3].x) += adds ? p : 0.f;
+            (k & 1 ? sum[(k >> 1) & 1].y : sum[(k >> 1) & 1].x) += adds ? p : 0.f;
           }
         }
       }
@@ -339,12 +376,12 @@ __global__ void __launch_bounds__(TC_THREADS, 2) weigh_tc_kernel(const __grid_co
       if (lane == 0) mbar_arrive(bar + C::C_EMPTY + s);
     }
     ok = __all_sync(0xffffffffu, ok);
-    float w = ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
+    float w = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     if (!ok) {
       w = __int_as_float(0x7fc00000);
       if (lane == 0) report(A, ATTN_ERR_TIMEOUT);
     }
-    s_sum[r] = w;
+    s_sum[half * KM + r] = w;
   }
   tc_fence_before();
   __syncthreads();
@@ -356,13 +393,8 @@ __global__ void __launch_bounds__(TC_THREADS, 2) weigh_tc_kernel(const __grid_co
   if (X.share > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (rank == 0 && tid < KM) {
     const int key = key0 + tid;
-    float w = s_sum[tid];
-    for (int s = 1; s < X.share; ++s) {
-      float x;
-      asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
-                   : "=f"(x) : "r"(smem_u32(s_sum + tid)), "r"(s) : "memory");
-      w += x;
-    }
+    float w = s_sum[tid] + s_sum[KM + tid];
+    for (int s = 1; s < X.share; ++s) w += peek(s_sum + tid, s) + peek(s_sum + KM + tid, s);
     const int page = key >= kfrom && key <= kto ? page_of(key) : -1;
     if (page >= 0) {
       const long long at = ((long long)page * A.c.hkv + hk) * (in_page + 1) + (key & in_page);
@@ -373,6 +405,7 @@ __global__ void __launch_bounds__(TC_THREADS, 2) weigh_tc_kernel(const __grid_co
   }
   // no CTA leaves while another reads its shared memory
   if (X.share > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  done();
 }
 
 // -------------------------------------------------------------------- host
@@ -413,17 +446,21 @@ static int launch_tc(const Args& a, int batch, cudaStream_t st) {
     return ATTN_ERR_CUDA;
   const auto kern = weigh_tc_kernel<DQK, T>;
   if (!succeeded(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM))) return ATTN_ERR_CUDA;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = x.share;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  // It starts beside the short segments' kernel: neither touches what the other does, and
+  // that one began after all earlier work.
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = x.share;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * x.share));
   cfg.blockDim = dim3(TC_THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
   return succeeded(cudaLaunchKernelEx(&cfg, kern, map, x)) ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
