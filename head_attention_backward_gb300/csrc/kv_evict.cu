@@ -7,15 +7,15 @@
 // >= keep and every write to a row < keep, so nothing has to wait for anything, and
 // no more than min(keep, n - keep) rows move.
 //
-// * select_kernel: a cluster of 1 to 8 CTAs owns a request and head.  Its rows' keys
-//   go to shared memory once (8 bytes a row read: weight and position); the least key
-//   that stays is found digit by digit (11, 11 and 10 bits) from histograms that the
-//   CTAs add up through each other's shared memory; two prefix sums over the rows
-//   number the holes and those that fill them.  One more cluster checks the call and
-//   counts the pages that go back.
-// * move_kernel: a warp owns a page that has holes: the larger of its scale and of
-//   those that come in, the rows that stay rounded again if it grew, then the rows.
-//   One more CTA writes the lengths and the stack.
+// * select_kernel: a cluster of 1 to 16 CTAs owns a request and head.  Its rows' keys
+//   go to shared memory once (8 bytes a row read: weight and position), several rows of
+//   a thread on their way together; the least key that stays is found digit by digit
+//   (11, 11 and 10 bits) from histograms that the CTAs add up through each other's
+//   shared memory; two prefix sums over the rows number the holes and those that fill
+//   them.  A few more CTAs check the call and count the pages that go back.
+// * move_kernel: a CTA owns a stretch of a request's and head's pages: the larger of a
+//   page's scale and of those that come in, the rows that stay rounded again where it
+//   grew, then the rows.  One more CTA writes the lengths and the stack.
 //
 // Bound by memory where much goes (8 bytes a row, 2 (d_qk + d_v) a row that moves),
 // by the dependent trips to memory and the barriers of the selection elsewhere.
@@ -29,8 +29,12 @@ constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int BINS = 2048;
 constexpr int HELD = 40 * 1024;         // keys of a CTA's share that fit shared memory
+constexpr int MAX_CLUSTER = 16;
+constexpr int SHARE = 4096;             // rows of a CTA that its cluster grows for
 constexpr int MOVE_THREADS = 256;
 constexpr int MOVE_WARPS = MOVE_THREADS / 32;
+constexpr int CHUNK = 1024;             // rows that a CTA of move_kernel works on at a time
+constexpr int CHUNK_PAGES = CHUNK / 16;
 constexpr uint32_t FIRST = 0xffffffffu; // key of a protected row
 
 struct Args {
@@ -42,7 +46,9 @@ struct Args {
   int pages;             // of max_k tokens
   int half;              // most rows that move
   int spread;            // CTAs that share a request's and head's pages
-  int* verdict;          // status of the call
+  int checks;            // CTAs that check the call, at most MOVE_THREADS
+  int* verdict;          // status of the call, but for its pages
+  int* off;              // [checks]: pages outside the cache
   int4* plan;            // [batch]: length, length after, pages given back before it, unused
   int2* edge;            // [batch][kv head]: exponent bytes of the page that row `keep` is in
   int* holes;            // [batch][kv head][pages + 1]: holes before a page
@@ -66,8 +72,11 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+// A barrier of the CTAs that own a request and head (a cluster's costs a microsecond).
+template <bool ONE>
+__device__ __forceinline__ void owners_sync() {
+  if (ONE) __syncthreads();
+  else asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ int rank_of() {
   uint32_t r;
@@ -80,6 +89,14 @@ __device__ __forceinline__ int peek(const void* p, int rank) {
   int v;
   asm volatile("{\n\t.reg .u32 x;\n\tmapa.shared::cluster.u32 x, %1, %2;\n\tld.shared::cluster.u32 %0, [x];\n\t}"
                : "=r"(v) : "r"(a), "r"(rank) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ int4 peek4(const void* p, int rank) {
+  const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+  int4 v;
+  asm volatile("{\n\t.reg .u32 x;\n\tmapa.shared::cluster.u32 x, %4, %5;\n\tld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [x];\n\t}"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a), "r"(rank) : "memory");
   return v;
 }
 
@@ -111,79 +128,105 @@ __device__ __forceinline__ int block_before(int v, int* scratch, int* total) {
   return before + s - v;
 }
 
-// The checks of the whole call, and where each request's pages go on the stack.
-__device__ void check_call(const Args& A, int* scratch) {
+// The checks of the whole call by A.checks CTAs, and (the first of them) where each
+// request's pages go on the stack.
+__device__ void check_call(const Args& A, int part, int* scratch) {
   const attn_kv_evict_params& P = A.p;
   const int shift = A.c.page_shift, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int free_n = *P.free_count;
-  bool bad = free_n < 0 || free_n > A.c.num_pages, off = false;
-  long long given = 0;
-  for (int b0 = 0; b0 < P.batch; b0 += THREADS) {
-    const int b = b0 + threadIdx.x;
-    int n = 0, after = 0, back = 0, total;
-    if (b < P.batch) {
-      const int keep = P.keep[b];
-      n = after = P.seqlens[b];
-      bad |= n < 0 || n > A.max_k || keep < -1;
-      if (evicts(A, n, keep)) {
-        after = keep;
-        back = pages_of(n, shift) - pages_of(keep, shift);
+  if (part == 0) {
+    const int free_n = *P.free_count;
+    bool bad = free_n < 0 || free_n > A.c.num_pages;
+    long long given = 0;
+    for (int b0 = 0; b0 < P.batch; b0 += THREADS) {
+      const int b = b0 + threadIdx.x;
+      int n = 0, after = 0, back = 0, total;
+      if (b < P.batch) {
+        const int keep = P.keep[b];
+        n = after = P.seqlens[b];
+        bad |= n < 0 || n > A.max_k || keep < -1;
+        if (evicts(A, n, keep)) {
+          after = keep;
+          back = pages_of(n, shift) - pages_of(keep, shift);
+        }
       }
+      const int before = block_before(back, scratch, &total);
+      if (b < P.batch) A.plan[b] = make_int4(n, after, (int)min(given + before, (long long)INT32_MAX), 0);
+      given += total;
+      __syncthreads();
     }
-    const int before = block_before(back, scratch, &total);
-    if (b < P.batch) A.plan[b] = make_int4(n, after, (int)min(given + before, (long long)INT32_MAX), 0);
-    given += total;
-    __syncthreads();
+    bad |= given > A.c.num_pages - free_n;
+    const bool any_bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *A.verdict = any_bad ? ATTN_ERR_BAD_SEQLENS : ATTN_OK;
   }
-  bad |= given > A.c.num_pages - free_n;
-  const bool any_bad = __syncthreads_or(bad);
-  if (!any_bad) {
-    for (int b = warp; b < P.batch; b += WARPS) {
-      const int4 r = A.plan[b];
-      if (r.x == r.y) continue;
-      for (int i = lane; i < pages_of(r.x, shift); i += 32) {
-        const int page = P.block_table[b * P.table_stride + i];
-        off |= page < 0 || page >= A.c.num_pages;
-      }
+  // pages of the requests that shrink: several warps a request if there are few
+  const int mine = cdiv(P.batch - part, A.checks), team = max(1, WARPS / max(1, mine)), teams = WARPS / team;
+  bool off = false;
+  for (int i = warp / team; i < mine && warp < team * teams; i += teams) {
+    const int b = part + i * A.checks, n = P.seqlens[b];
+    if (!evicts(A, n, P.keep[b])) continue;
+    const int held = pages_of(n, shift);
+    const int* table = P.block_table + b * P.table_stride;
+    constexpr int U = 8;
+    for (int j0 = (warp % team) * 32 + lane; j0 < held; j0 += team * 32 * U) {
+      int page[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) page[k] = j0 + k * team * 32 < held ? __ldg(table + j0 + k * team * 32) : 0;
+#pragma unroll
+      for (int k = 0; k < U; ++k) off |= page[k] < 0 || page[k] >= A.c.num_pages;
     }
   }
   const bool any_off = __syncthreads_or(off);
-  if (threadIdx.x == 0) *A.verdict = any_bad ? ATTN_ERR_BAD_SEQLENS : any_off ? ATTN_ERR_BAD_PAGE : ATTN_OK;
+  if (threadIdx.x == 0) A.off[part] = any_off;
 }
 
-__global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__ Args A) {
+// ONE: clusters of one CTA.
+template <bool ONE>
+__global__ void __launch_bounds__(THREADS, 2) select_kernel(const __grid_constant__ Args A) {
   extern __shared__ uint32_t s_keys[];
-  __shared__ int s_hist[BINS];
+  __shared__ __align__(16) int s_hist[BINS];
   __shared__ int s_scratch[2][WARPS];
   __shared__ int s_found[2], s_sum[3];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const attn_kv_evict_params& P = A.p;
-  const int tid = threadIdx.x, rank = rank_of(), heads = A.c.hkv;
-  const int job = blockIdx.x / A.cluster;
-  if (job == P.batch * heads) {
-    if (rank == 0) check_call(A, s_scratch[0]);
+  const int tid = threadIdx.x, rank = ONE ? 0 : rank_of(), heads = A.c.hkv;
+  const int cluster = ONE ? 1 : A.cluster, job = blockIdx.x / cluster;
+  if (job >= P.batch * heads) {
+    const int part = blockIdx.x - P.batch * heads * cluster;
+    if (part < A.checks) check_call(A, part, s_scratch[0]);
     return;
   }
   const int b = job / heads, h = job - b * heads;
   const int n = P.seqlens[b], keep = P.keep[b];
   if (!evicts(A, n, keep) || keep == 0) return;         // the same for the whole cluster
   const int shift = A.c.page_shift, in_page = (1 << shift) - 1;
-  const int per = cdiv(n, A.cluster), lo = min(rank * per, n), mine = min(per, n - lo);
+  const int per = cdiv(n, cluster), lo = min(rank * per, n), mine = min(per, n - lo);
   uint32_t* keys = A.keys ? A.keys + (long long)job * A.max_k + lo : s_keys;
   const int* table = P.block_table + b * P.table_stride;
   const long long recent = (long long)n + P.position_offsets[b] - P.recent;
   auto fill = [&](bool protected_only) {
-    for (int i = tid; i < mine; i += THREADS) {
-      const int row = lo + i, page = table[row >> shift];
-      uint32_t k = 0;
-      if (page >= 0 && page < A.c.num_pages) {
-        const long long at = (((long long)page * heads + h) << shift) + (row & in_page);
-        const int pos = __ldg(P.weights.position + at);
-        const uint32_t by_weight = key_of(__ldg(P.weights.weight + at));
-        const bool first = pos < P.sink || pos >= recent;
-        k = protected_only ? (first ? by_weight : 0) : first ? FIRST : by_weight;
+    constexpr int U = 8;                                 // rows of a thread on their way together
+    for (int i0 = tid; i0 < mine; i0 += THREADS * U) {
+      int page[U], pos[U];
+      float w[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int i = i0 + k * THREADS;
+        page[k] = i < mine ? __ldg(table + ((lo + i) >> shift)) : -1;
       }
-      keys[i] = k;
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const bool in = page[k] >= 0 && page[k] < A.c.num_pages;
+        const long long at = (((long long)page[k] * heads + h) << shift) + ((lo + i0 + k * THREADS) & in_page);
+        pos[k] = in ? __ldg(P.weights.position + at) : 0;
+        w[k] = in ? __ldg(P.weights.weight + at) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int i = i0 + k * THREADS;
+        const bool first = pos[k] < P.sink || pos[k] >= recent;
+        const uint32_t by_weight = key_of(w[k]);
+        if (i < mine) keys[i] = protected_only ? (first ? by_weight : 0) : first ? FIRST : by_weight;
+      }
     }
   };
   fill(false);
@@ -211,19 +254,23 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
         atomicAdd(&s_hist[digit], 1);
       }
     }
-    cluster_sync();
+    owners_sync<ONE>();
     // bins from the top: thread t has four, the last threads the lowest
     constexpr int PER = BINS / THREADS;
-    int bin[PER], sum = 0, total;
+    static_assert(PER == 4, "a vector per thread");
+    int sum, total;
     const int top = BINS - 1 - tid * PER;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) bin[j] = 0;
-    for (int r = 0; r < A.cluster; ++r) {
-#pragma unroll
-      for (int j = 0; j < PER; ++j) bin[j] += A.cluster == 1 ? s_hist[top - j] : peek(&s_hist[top - j], r);
+    int4 v = *reinterpret_cast<const int4*>(&s_hist[top - 3]);
+    if (!ONE) {
+      v = make_int4(0, 0, 0, 0);
+#pragma unroll 4
+      for (int r = 0; r < cluster; ++r) {
+        const int4 x = peek4(&s_hist[top - 3], r);
+        v = make_int4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+      }
     }
-#pragma unroll
-    for (int j = 0; j < PER; ++j) sum += bin[j];
+    const int bin[PER] = {v.w, v.z, v.y, v.x};
+    sum = v.x + v.y + v.z + v.w;
     int before = block_before(sum, s_scratch[pass & 1], &total);
     if (before < left && left <= before + sum) {
 #pragma unroll
@@ -235,7 +282,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
         before += bin[j];
       }
     }
-    cluster_sync();                                      // also: the histograms have been read
+    owners_sync<ONE>();                                      // also: the histograms have been read
     if (pass == 0 && s_found[0] == BINS - 1) {           // `keep` protected rows or more: among themselves
       fill(true);
       pass = -1;
@@ -252,8 +299,9 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
   for (int i = a; i < z; ++i) equal += keys[i] == found;
   int ties = block_before(equal, s_scratch[1], &total);
   if (tid == 0) s_sum[0] = total;
-  cluster_sync();
-  for (int r = 0; r < rank; ++r) ties += peek(&s_sum[0], r);
+  owners_sync<ONE>();
+  if (!ONE)
+    for (int r = 0; r < rank; ++r) ties += peek(&s_sum[0], r);
   int holes = 0, fills = 0;
   {
     int t = ties;
@@ -273,10 +321,10 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
     s_sum[1] = total_holes;
     s_sum[2] = total_fills;
   }
-  cluster_sync();
+  owners_sync<ONE>();
   holes = holes0;
   fills = fills0;
-  for (int r = 0; r < rank; ++r) {
+  for (int r = 0; !ONE && r < rank; ++r) {
     holes += peek(&s_sum[1], r);
     fills += peek(&s_sum[2], r);
   }
@@ -300,7 +348,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
       A.edge[job] = make_int2(A.c.k_exp[at], A.c.v_exp[at]);
     }
   }
-  cluster_sync();                                        // no CTA leaves while others read its shared memory
+  if (!ONE) owners_sync<ONE>();                          // no CTA leaves while others read its shared memory
 }
 
 // 16 e4m3 values times f, rounded again.
@@ -317,70 +365,39 @@ __device__ __forceinline__ uint4 times(const uint4& x, float f) {
   return make_uint4(q[0], q[1], q[2], q[3]);
 }
 
-struct Side {
-  uint8_t* x;            // of the head
-  uint8_t* exp;
-  long long page, row;   // strides
-  int edge;              // exponent byte of the page that row `keep` is in, before the call
-};
-
-// The holes [h0, h1) of one page, on one side, by one warp.
+// Rows [0, rows) of a page's head, one side of the cache, at a larger scale (f: old over
+// new), by one warp.  Holes among them are filled after this.
 template <int D>
-__device__ __forceinline__ void fill_page(const Side& S, const int* table, const int* to, const int* from, int h0, int h1,
-                                          int first, int rows, int edge_block, int shift, int heads) {
-  constexpr int PER = D / 16;
-  const int lane = threadIdx.x & 31, in_page = (1 << shift) - 1;
-  const int page = table[first >> shift];
-  uint8_t* exp_at = S.exp + (long long)page * heads;
-  auto exp_of = [&](int row) {
-    const int block = row >> shift;
-    return kv_exp_of(block == edge_block ? (uint8_t)S.edge : S.exp[(long long)table[block] * heads]);
-  };
-  const int old = kv_exp_of(*exp_at);
-  int e = old;
-  for (int i = h0 + lane; i < h1; i += 32) e = max(e, exp_of(from[i]));
-  e = __reduce_max_sync(0xffffffffu, e);
-  uint8_t* dst = S.x + page * S.page;
-  if (e > old) {
-    // every row below `keep`, holes too: they are written after this
-    const float f = exp2_int(old - e);
-    for (int i = lane; i < rows * PER; i += 32) {
-      uint4* at = reinterpret_cast<uint4*>(dst + (i / PER) * S.row + (i % PER) * 16);
-      *at = times(*at, f);
-    }
-    if (lane == 0) *exp_at = (uint8_t)(e + KV_EXP_BIAS);
-    __syncwarp();
-  }
-  constexpr int N = 4;   // pieces in flight
-  const int all = (h1 - h0) * PER;
-  for (int i0 = lane; i0 < all; i0 += 32 * N) {
+__device__ __forceinline__ void round_again(uint8_t* page, long long stride, int rows, float f) {
+  constexpr int PER = D / 16, N = 4;
+  for (int i0 = threadIdx.x & 31; i0 < rows * PER; i0 += 32 * N) {
     uint4 x[N];
-    int ex[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const int i = i0 + 32 * k;
-      if (i < all) {
-        const int row = from[h0 + i / PER];
-        x[k] = *reinterpret_cast<const uint4*>(S.x + table[row >> shift] * S.page + (row & in_page) * S.row + (i % PER) * 16);
-        ex[k] = exp_of(row);
-      }
+      if (i < rows * PER) x[k] = *reinterpret_cast<const uint4*>(page + (i / PER) * stride + (i % PER) * 16);
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const int i = i0 + 32 * k;
-      if (i < all)
-        *reinterpret_cast<uint4*>(dst + (to[h0 + i / PER] & in_page) * S.row + (i % PER) * 16) =
-            ex[k] == e ? x[k] : times(x[k], exp2_int(ex[k] - e));
+      if (i < rows * PER) *reinterpret_cast<uint4*>(page + (i / PER) * stride + (i % PER) * 16) = times(x[k], f);
     }
   }
 }
 
 template <int DQK, int DV>
-__global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const __grid_constant__ Args A) {
+__global__ void __launch_bounds__(MOVE_THREADS, 3) move_kernel(const __grid_constant__ Args A) {
+  __shared__ int s_page[CHUNK];              // of what fills a hole
+  __shared__ int s_rows[CHUNK];              // its row in the page, the hole's in the chunk, exponents of its page
+  __shared__ int s_dst[CHUNK_PAGES];         // pages of the chunk
+  __shared__ int s_old[2][CHUNK_PAGES], s_new[2][CHUNK_PAGES];   // their exponents: K, V
+  __shared__ int s_back[MOVE_WARPS];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const attn_kv_evict_params& P = A.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, shift = A.c.page_shift, in_page = (1 << shift) - 1;
-  const int heads = A.c.hkv, verdict = *A.verdict;
+  const int heads = A.c.hkv;
+  const bool off = __syncthreads_or(tid < A.checks && A.off[tid]);
+  const int verdict = *A.verdict != ATTN_OK ? *A.verdict : off ? ATTN_ERR_BAD_PAGE : ATTN_OK;
   if (blockIdx.x == P.batch * heads * A.spread) {
     // lengths, offsets, the stack
     const int free_n = *P.free_count;
@@ -401,7 +418,6 @@ __global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const __grid_constan
         P.free_pages[free_n + r.z + i] = P.block_table[b * P.table_stride + need + i];
       back = max(back, r.z + held - need);
     }
-    __shared__ int s_back[MOVE_WARPS];
     if (lane == 0) s_back[warp] = back;
     __syncthreads();
     if (tid == 0) {
@@ -415,32 +431,92 @@ __global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const __grid_constan
   const int b = job / heads, h = job - b * heads;
   const int4 r = A.plan[b];
   if (verdict != ATTN_OK || r.y >= r.x) return;
-  const int keep = r.y, pages = pages_of(keep, shift);
+  const int keep = r.y, pages = pages_of(keep, shift), each = cdiv(pages, A.spread);
+  const int end = min(pages, (share + 1) * each), step = CHUNK >> shift;
   const int* table = P.block_table + b * P.table_stride;
   const int* to = A.to + (long long)job * A.half;
   const int* from = A.from + (long long)job * A.half;
   const int* starts = A.holes + (long long)job * (A.pages + 1);
-  const int2 edge = A.edge[job];
-  const Side K{A.c.k + h * A.c.sk.h, A.c.k_exp + h, A.c.sk.p, A.c.sk.r, edge.x};
-  const Side V{A.c.v + h * A.c.sv.h, A.c.v_exp + h, A.c.sv.p, A.c.sv.r, edge.y};
-  for (int p = share * MOVE_WARPS + warp; p < pages; p += A.spread * MOVE_WARPS) {
-    const int h0 = starts[p], h1 = starts[p + 1], first = p << shift, rows = min(1 << shift, keep - first);
-    if (h0 == h1) continue;
-    fill_page<DQK>(K, table, to, from, h0, h1, first, rows, keep >> shift, shift, heads);
-    fill_page<DV>(V, table, to, from, h0, h1, first, rows, keep >> shift, shift, heads);
-    const long long own = ((long long)table[p] * heads + h) << shift;
-    for (int i = h0 + lane; i < h1; i += 32) {
-      const int row = from[i];
-      const long long src = (((long long)table[row >> shift] * heads + h) << shift) + (row & in_page);
-      const long long dst = own + (to[i] & in_page);
-      P.weights.weight[dst] = P.weights.weight[src];
-      P.weights.position[dst] = P.weights.position[src];
+  uint8_t* kh = A.c.k + h * A.c.sk.h;
+  uint8_t* vh = A.c.v + h * A.c.sv.h;
+  for (int p0 = share * each; p0 < end; p0 += step) {
+    const int np = min(step, end - p0), h0 = starts[p0], count = starts[p0 + np] - h0;
+    if (count == 0) continue;
+    __syncthreads();                                     // the last chunk's rows have moved
+    if (tid < np) {
+      const int page = table[p0 + tid];
+      const long long at = (long long)page * heads + h;
+      s_dst[tid] = page;
+      s_old[0][tid] = s_new[0][tid] = kv_exp_of(A.c.k_exp[at]);
+      s_old[1][tid] = s_new[1][tid] = kv_exp_of(A.c.v_exp[at]);
+    }
+    __syncthreads();
+    for (int i = tid; i < count; i += MOVE_THREADS) {
+      const int row = to[h0 + i] - (p0 << shift), src = from[h0 + i], page = table[src >> shift];
+      const long long at = (long long)page * heads + h;
+      // the page that row `keep` is in may be getting new exponents from another CTA
+      int ek, ev;
+      if (src >> shift == keep >> shift) {
+        const int2 e = A.edge[job];
+        ek = e.x, ev = e.y;
+      } else {
+        ek = A.c.k_exp[at], ev = A.c.v_exp[at];
+      }
+      ek = kv_exp_of((uint8_t)ek), ev = kv_exp_of((uint8_t)ev);
+      const long long w_src = (at << shift) + (src & in_page);
+      const long long w_dst = (((long long)s_dst[row >> shift] * heads + h) << shift) + (row & in_page);
+      const float w = P.weights.weight[w_src];
+      const int pos = P.weights.position[w_src];
+      atomicMax(&s_new[0][row >> shift], ek);
+      atomicMax(&s_new[1][row >> shift], ev);
+      s_page[i] = page;
+      s_rows[i] = (src & in_page) | row << 8 | (ek - KV_EXP_MIN) << 18 | (ev - KV_EXP_MIN) << 24;
+      P.weights.weight[w_dst] = w;
+      P.weights.position[w_dst] = pos;
+    }
+    __syncthreads();
+    // pages whose scale grew
+    for (int q = warp; q < 2 * np; q += MOVE_WARPS) {
+      const int p = q >> 1, v = q & 1, old = s_old[v][p], now = s_new[v][p];
+      if (now == old) continue;
+      const int page = s_dst[p], rows = min(1 << shift, keep - ((p0 + p) << shift));
+      if (v) round_again<DV>(vh + page * A.c.sv.p, A.c.sv.r, rows, exp2_int(old - now));
+      else round_again<DQK>(kh + page * A.c.sk.p, A.c.sk.r, rows, exp2_int(old - now));
+      if (lane == 0) (v ? A.c.v_exp : A.c.k_exp)[(long long)page * heads + h] = (uint8_t)(now + KV_EXP_BIAS);
+    }
+    __syncthreads();
+    // the rows, 16 bytes of K or V at a time
+    constexpr int PK = DQK / 16, PER = PK + DV / 16, N = 4;
+    for (int i0 = tid; i0 < count * PER; i0 += MOVE_THREADS * N) {
+      uint4 x[N];
+      uint8_t* dst[N];
+      int shrink[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int i = i0 + k * MOVE_THREADS;
+        dst[k] = nullptr;
+        if (i < count * PER) {
+          const int hole = i / PER, c = i - hole * PER, info = s_rows[hole];
+          const int row = info >> 8 & (CHUNK - 1), p = row >> shift;
+          const bool v = c >= PK;
+          const int col = (v ? c - PK : c) * 16;
+          const uint8_t* src = v ? vh + s_page[hole] * A.c.sv.p + (info & 255) * A.c.sv.r
+                                 : kh + s_page[hole] * A.c.sk.p + (info & 255) * A.c.sk.r;
+          x[k] = *reinterpret_cast<const uint4*>(src + col);
+          dst[k] = (v ? vh + s_dst[p] * A.c.sv.p + (row & in_page) * A.c.sv.r
+                      : kh + s_dst[p] * A.c.sk.p + (row & in_page) * A.c.sk.r) + col;
+          shrink[k] = (info >> (v ? 24 : 18) & 63) + KV_EXP_MIN - s_new[v][p];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (dst[k]) *reinterpret_cast<uint4*>(dst[k]) = shrink[k] == 0 ? x[k] : times(x[k], exp2_int(shrink[k]));
     }
   }
 }
 
 struct Layout {
-  size_t off_plan, off_edge, off_holes, off_to, off_from, off_keys, total;
+  size_t off_off, off_plan, off_edge, off_holes, off_to, off_from, off_keys, total;
   int cluster, pages, half, max_k;
   bool held;
 };
@@ -458,13 +534,14 @@ static int layout(const attn_kv_evict_params* p, Layout* L) {
   L->max_k = p->max_seqlen_k < cap ? p->max_seqlen_k : (int)cap;
   // Rows of a CTA: enough for its threads, few enough for its shared memory.
   L->cluster = 1;
-  while (L->cluster < 8 && cdiv(L->max_k, L->cluster) > 8192) L->cluster *= 2;
+  while (L->cluster < MAX_CLUSTER && cdiv(L->max_k, L->cluster) > SHARE) L->cluster *= 2;
   L->held = cdiv(L->max_k, L->cluster) <= HELD;
   L->pages = cdiv(L->max_k, c.page_size);
   L->half = L->max_k / 2 + 1;
   const size_t jobs = (size_t)p->batch * c.nhead_kv;
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   size_t o = 256;
+  L->off_off = o;   o = up(o + MOVE_THREADS * sizeof(int));
   L->off_plan = o;  o = up(o + (size_t)p->batch * sizeof(int4));
   L->off_edge = o;  o = up(o + jobs * sizeof(int2));
   L->off_holes = o; o = up(o + jobs * (L->pages + 1) * sizeof(int));
@@ -501,6 +578,8 @@ static int run(const attn_kv_evict_params* p, void* ws, size_t bytes, cudaStream
   a.pages = L.pages;
   a.half = L.half;
   a.verdict = reinterpret_cast<int*>(w);
+  a.off = reinterpret_cast<int*>(w + L.off_off);
+  a.checks = cdiv(p->batch, WARPS) < MOVE_THREADS ? cdiv(p->batch, WARPS) : MOVE_THREADS;
   a.plan = reinterpret_cast<int4*>(w + L.off_plan);
   a.edge = reinterpret_cast<int2*>(w + L.off_edge);
   a.holes = reinterpret_cast<int*>(w + L.off_holes);
@@ -508,24 +587,28 @@ static int run(const attn_kv_evict_params* p, void* ws, size_t bytes, cudaStream
   a.from = reinterpret_cast<int*>(w + L.off_from);
   a.keys = L.held ? nullptr : reinterpret_cast<uint32_t*>(w + L.off_keys);
   const int jobs = p->batch * p->cache.nhead_kv;
-  const int share = 8 * SMS / jobs, whole = cdiv(L.pages, MOVE_WARPS);
-  a.spread = share < 1 || whole < 1 ? 1 : share < whole ? share : whole;
+  // about two CTAs per SM, each of a page at least
+  const int share = cdiv(2 * SMS, jobs);
+  a.spread = L.pages < 1 ? 1 : share < L.pages ? share : L.pages;
   const size_t smem = L.held ? (size_t)cdiv(L.max_k, L.cluster) * sizeof(uint32_t) : 0;
-  if (smem > 32 * 1024 && !succeeded(cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const auto select = L.cluster == 1 ? select_kernel<true> : select_kernel<false>;
+  if (smem > 32 * 1024 && !succeeded(cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                           (int)(HELD * sizeof(uint32_t)))))
+    return ATTN_ERR_CUDA;
+  if (L.cluster > 8 && !succeeded(cudaFuncSetAttribute(select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)))
     return ATTN_ERR_CUDA;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim.x = L.cluster;
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((jobs + 1) * L.cluster);
+  cfg.gridDim = dim3((jobs + cdiv(a.checks, L.cluster)) * L.cluster);
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  if (!succeeded(cudaLaunchKernelEx(&cfg, select_kernel, a))) return ATTN_ERR_CUDA;
+  if (!succeeded(cudaLaunchKernelEx(&cfg, select, a))) return ATTN_ERR_CUDA;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(jobs * a.spread + 1);
