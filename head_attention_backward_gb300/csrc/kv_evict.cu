@@ -7,7 +7,7 @@
 // >= keep and every write to a row < keep, so nothing has to wait for anything, and
 // no more than min(keep, n - keep) rows move.
 //
-// * select_kernel: a cluster of 1 to 16 CTAs owns a request and head.  Its rows' keys
+// * select_kernel: a cluster of 1 to 8 CTAs owns a request and head.  Its rows' keys
 //   go to shared memory once (8 bytes a row read: weight and position), several rows of
 //   a thread on their way together; the least key that stays is found digit by digit
 //   (11, 11 and 10 bits) from histograms that the CTAs add up through each other's
@@ -25,12 +25,16 @@
 namespace attn {
 namespace kvevict {
 
-constexpr int THREADS = 512;
-constexpr int WARPS = THREADS / 32;
+// Threads of a CTA of select_kernel: two CTAs per SM where one owns a request and head,
+// more threads per row where several do (131,072 rows, 8 heads: PLACEHOLDER).
+constexpr int ONE_THREADS = 512, MANY_THREADS = 1024;
+constexpr int MAX_WARPS = MANY_THREADS / 32;
 constexpr int BINS = 2048;
 constexpr int HELD = 40 * 1024;         // keys of a CTA's share that fit shared memory
-constexpr int MAX_CLUSTER = 16;
-constexpr int SHARE = 4096;             // rows of a CTA that its cluster grows for
+// Clusters of 16 are no help: their CTAs need 16 SMs of a GPC at a time, and eight heads'
+// clusters ran in two turns (131,072 rows: 61 us against 38 with eight CTAs).
+constexpr int MAX_CLUSTER = 8;
+constexpr int SHARE = 8192;             // rows of a CTA that its cluster grows for
 constexpr int MOVE_THREADS = 256;
 constexpr int MOVE_WARPS = MOVE_THREADS / 32;
 constexpr int CHUNK = 1024;             // rows that a CTA of move_kernel works on at a time
@@ -110,8 +114,9 @@ __device__ __forceinline__ int warp_scan(int v) {
   return v;
 }
 
-// Sum over the threads before this one; *total over all.  scratch: WARPS words, free
+// Sum over the threads before this one; *total over all.  scratch: MAX_WARPS words, free
 // for the next use after a barrier.
+template <int THREADS>
 __device__ __forceinline__ int block_before(int v, int* scratch, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int s = warp_scan(v);
@@ -119,7 +124,7 @@ __device__ __forceinline__ int block_before(int v, int* scratch, int* total) {
   __syncthreads();
   int before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
+  for (int w = 0; w < THREADS / 32; ++w) {
     const int x = scratch[w];
     if (w < warp) before += x;
     all += x;
@@ -130,7 +135,9 @@ __device__ __forceinline__ int block_before(int v, int* scratch, int* total) {
 
 // The checks of the whole call by A.checks CTAs, and (the first of them) where each
 // request's pages go on the stack.
+template <int THREADS>
 __device__ void check_call(const Args& A, int part, int* scratch) {
+  constexpr int WARPS = THREADS / 32;
   const attn_kv_evict_params& P = A.p;
   const int shift = A.c.page_shift, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (part == 0) {
@@ -149,7 +156,7 @@ __device__ void check_call(const Args& A, int part, int* scratch) {
           back = pages_of(n, shift) - pages_of(keep, shift);
         }
       }
-      const int before = block_before(back, scratch, &total);
+      const int before = block_before<THREADS>(back, scratch, &total);
       if (b < P.batch) A.plan[b] = make_int4(n, after, (int)min(given + before, (long long)INT32_MAX), 0);
       given += total;
       __syncthreads();
@@ -181,10 +188,11 @@ __device__ void check_call(const Args& A, int part, int* scratch) {
 
 // ONE: clusters of one CTA.
 template <bool ONE>
-__global__ void __launch_bounds__(THREADS, 2) select_kernel(const __grid_constant__ Args A) {
+__global__ void __launch_bounds__(ONE ? ONE_THREADS : MANY_THREADS, ONE ? 2 : 1) select_kernel(const __grid_constant__ Args A) {
+  constexpr int THREADS = ONE ? ONE_THREADS : MANY_THREADS;
   extern __shared__ uint32_t s_keys[];
   __shared__ __align__(16) int s_hist[BINS];
-  __shared__ int s_scratch[2][WARPS];
+  __shared__ int s_scratch[2][MAX_WARPS];
   __shared__ int s_found[2], s_sum[3];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const attn_kv_evict_params& P = A.p;
@@ -192,7 +200,7 @@ __global__ void __launch_bounds__(THREADS, 2) select_kernel(const __grid_constan
   const int cluster = ONE ? 1 : A.cluster, job = blockIdx.x / cluster;
   if (job >= P.batch * heads) {
     const int part = blockIdx.x - P.batch * heads * cluster;
-    if (part < A.checks) check_call(A, part, s_scratch[0]);
+    if (part < A.checks) check_call<THREADS>(A, part, s_scratch[0]);
     return;
   }
   const int b = job / heads, h = job - b * heads;
@@ -255,23 +263,27 @@ __global__ void __launch_bounds__(THREADS, 2) select_kernel(const __grid_constan
       }
     }
     owners_sync<ONE>();
-    // bins from the top: thread t has four, the last threads the lowest
-    constexpr int PER = BINS / THREADS;
-    static_assert(PER == 4, "a vector per thread");
+    // bins from the top: of the first BINS / 4 threads, thread t has four
+    constexpr int PER = 4;
+    static_assert(BINS / PER <= THREADS, "a vector per thread");
     int sum, total;
-    const int top = BINS - 1 - tid * PER;
-    int4 v = *reinterpret_cast<const int4*>(&s_hist[top - 3]);
-    if (!ONE) {
-      v = make_int4(0, 0, 0, 0);
-#pragma unroll 4
-      for (int r = 0; r < cluster; ++r) {
-        const int4 x = peek4(&s_hist[top - 3], r);
-        v = make_int4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+    const int top = max(PER - 1, BINS - 1 - tid * PER);
+    int4 v = make_int4(0, 0, 0, 0);
+    if (ONE) {
+      if (tid < BINS / PER) v = *reinterpret_cast<const int4*>(&s_hist[top - 3]);
+    } else if (tid < BINS / PER) {
+      // eight ranks' words on their way together (another CTA's memory is a microsecond away)
+      for (int r0 = 0; r0 < cluster; r0 += 8) {
+        int4 x[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) x[r] = r0 + r < cluster ? peek4(&s_hist[top - 3], r0 + r) : make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v = make_int4(v.x + x[r].x, v.y + x[r].y, v.z + x[r].z, v.w + x[r].w);
       }
     }
     const int bin[PER] = {v.w, v.z, v.y, v.x};
     sum = v.x + v.y + v.z + v.w;
-    int before = block_before(sum, s_scratch[pass & 1], &total);
+    int before = block_before<THREADS>(sum, s_scratch[pass & 1], &total);
     if (before < left && left <= before + sum) {
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
@@ -297,11 +309,17 @@ __global__ void __launch_bounds__(THREADS, 2) select_kernel(const __grid_constan
   const int walk = cdiv(mine, THREADS) | 1, a = min(tid * walk, mine), z = min(a + walk, mine);
   int equal = 0, total;
   for (int i = a; i < z; ++i) equal += keys[i] == found;
-  int ties = block_before(equal, s_scratch[1], &total);
-  if (tid == 0) s_sum[0] = total;
-  owners_sync<ONE>();
-  if (!ONE)
-    for (int r = 0; r < rank; ++r) ties += peek(&s_sum[0], r);
+  int ties = block_before<THREADS>(equal, s_scratch[1], &total);
+  // sums of the CTAs before this one: a lane reads one CTA's
+  auto ranks_before = [&](int which) {
+    const int x = (tid & 31) < rank ? peek(&s_sum[which], tid & 31) : 0;
+    return __reduce_add_sync(0xffffffffu, x);
+  };
+  if (!ONE) {
+    if (tid == 0) s_sum[0] = total;
+    owners_sync<ONE>();
+    ties += ranks_before(0);
+  }
   int holes = 0, fills = 0;
   {
     int t = ties;
@@ -314,19 +332,19 @@ __global__ void __launch_bounds__(THREADS, 2) select_kernel(const __grid_constan
     }
   }
   int total_holes, total_fills;
-  const int holes0 = block_before(holes, s_scratch[0], &total_holes);
+  const int holes0 = block_before<THREADS>(holes, s_scratch[0], &total_holes);
   __syncthreads();
-  const int fills0 = block_before(fills, s_scratch[1], &total_fills);
-  if (tid == 0) {
-    s_sum[1] = total_holes;
-    s_sum[2] = total_fills;
-  }
-  owners_sync<ONE>();
+  const int fills0 = block_before<THREADS>(fills, s_scratch[1], &total_fills);
   holes = holes0;
   fills = fills0;
-  for (int r = 0; !ONE && r < rank; ++r) {
-    holes += peek(&s_sum[1], r);
-    fills += peek(&s_sum[2], r);
+  if (!ONE) {
+    if (tid == 0) {
+      s_sum[1] = total_holes;
+      s_sum[2] = total_fills;
+    }
+    owners_sync<ONE>();
+    holes += ranks_before(1);
+    fills += ranks_before(2);
   }
   int* to = A.to + (long long)job * A.half;
   int* from = A.from + (long long)job * A.half;
@@ -351,24 +369,27 @@ __global__ void __launch_bounds__(THREADS, 2) select_kernel(const __grid_constan
   if (!ONE) owners_sync<ONE>();                          // no CTA leaves while others read its shared memory
 }
 
-// 16 e4m3 values times f, rounded again.
-__device__ __forceinline__ uint4 times(const uint4& x, float f) {
+// 16 e4m3 values times 2^shift, shift < 0, rounded again.  In fp16: the product is exact
+// as far as 2^-24, far below half of e4m3's least value, 2^-10; a factor below fp16's
+// least number is 0, and so are its products in e4m3.
+__device__ __forceinline__ uint4 times(const uint4& x, int shift) {
+  const __half2 f = __float2half2_rn(exp2_int(shift));
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t q[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t lo = e4m3x2_to_h2((uint16_t)w[j]), hi = e4m3x2_to_h2((uint16_t)(w[j] >> 16));
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    q[j] = f2_to_e4m3x2(a.x * f, a.y * f) | ((uint32_t)f2_to_e4m3x2(b.x * f, b.y * f) << 16);
+    uint32_t lo = e4m3x2_to_h2((uint16_t)w[j]), hi = e4m3x2_to_h2((uint16_t)(w[j] >> 16));
+    *reinterpret_cast<__half2*>(&lo) = __hmul2(*reinterpret_cast<__half2*>(&lo), f);
+    *reinterpret_cast<__half2*>(&hi) = __hmul2(*reinterpret_cast<__half2*>(&hi), f);
+    q[j] = __byte_perm(h2_to_e4m3x2(lo), h2_to_e4m3x2(hi), 0x5410);
   }
   return make_uint4(q[0], q[1], q[2], q[3]);
 }
 
-// Rows [0, rows) of a page's head, one side of the cache, at a larger scale (f: old over
-// new), by one warp.  Holes among them are filled after this.
+// Rows [0, rows) of a page's head, one side of the cache, at a scale 2^-shift times as
+// large, by one warp.  Holes among them are filled after this.
 template <int D>
-__device__ __forceinline__ void round_again(uint8_t* page, long long stride, int rows, float f) {
+__device__ __forceinline__ void round_again(uint8_t* page, long long stride, int rows, int shift) {
   constexpr int PER = D / 16, N = 4;
   for (int i0 = threadIdx.x & 31; i0 < rows * PER; i0 += 32 * N) {
     uint4 x[N];
@@ -380,7 +401,7 @@ __device__ __forceinline__ void round_again(uint8_t* page, long long stride, int
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const int i = i0 + 32 * k;
-      if (i < rows * PER) *reinterpret_cast<uint4*>(page + (i / PER) * stride + (i % PER) * 16) = times(x[k], f);
+      if (i < rows * PER) *reinterpret_cast<uint4*>(page + (i / PER) * stride + (i % PER) * 16) = times(x[k], shift);
     }
   }
 }
@@ -480,37 +501,35 @@ __global__ void __launch_bounds__(MOVE_THREADS, 3) move_kernel(const __grid_cons
       const int p = q >> 1, v = q & 1, old = s_old[v][p], now = s_new[v][p];
       if (now == old) continue;
       const int page = s_dst[p], rows = min(1 << shift, keep - ((p0 + p) << shift));
-      if (v) round_again<DV>(vh + page * A.c.sv.p, A.c.sv.r, rows, exp2_int(old - now));
-      else round_again<DQK>(kh + page * A.c.sk.p, A.c.sk.r, rows, exp2_int(old - now));
+      if (v) round_again<DV>(vh + page * A.c.sv.p, A.c.sv.r, rows, old - now);
+      else round_again<DQK>(kh + page * A.c.sk.p, A.c.sk.r, rows, old - now);
       if (lane == 0) (v ? A.c.v_exp : A.c.k_exp)[(long long)page * heads + h] = (uint8_t)(now + KV_EXP_BIAS);
     }
     __syncthreads();
-    // the rows, 16 bytes of K or V at a time
-    constexpr int PK = DQK / 16, PER = PK + DV / 16, N = 4;
-    for (int i0 = tid; i0 < count * PER; i0 += MOVE_THREADS * N) {
+    // the rows: a thread keeps to 16 bytes of K or V and takes every LANES-th hole
+    constexpr int PK = DQK / 16, PER = PK + DV / 16, LANES = MOVE_THREADS / PER, N = 4;
+    const int c = tid % PER;
+    const bool v = c >= PK;
+    const KvStrides& st = v ? A.c.sv : A.c.sk;
+    uint8_t* base = v ? vh + (c - PK) * 16 : kh + c * 16;
+    const int* now = s_new[v];
+    for (int i0 = tid / PER; i0 < (tid < LANES * PER ? count : 0); i0 += LANES * N) {
       uint4 x[N];
       uint8_t* dst[N];
       int shrink[N];
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        const int i = i0 + k * MOVE_THREADS;
-        dst[k] = nullptr;
-        if (i < count * PER) {
-          const int hole = i / PER, c = i - hole * PER, info = s_rows[hole];
-          const int row = info >> 8 & (CHUNK - 1), p = row >> shift;
-          const bool v = c >= PK;
-          const int col = (v ? c - PK : c) * 16;
-          const uint8_t* src = v ? vh + s_page[hole] * A.c.sv.p + (info & 255) * A.c.sv.r
-                                 : kh + s_page[hole] * A.c.sk.p + (info & 255) * A.c.sk.r;
-          x[k] = *reinterpret_cast<const uint4*>(src + col);
-          dst[k] = (v ? vh + s_dst[p] * A.c.sv.p + (row & in_page) * A.c.sv.r
-                      : kh + s_dst[p] * A.c.sk.p + (row & in_page) * A.c.sk.r) + col;
-          shrink[k] = (info >> (v ? 24 : 18) & 63) + KV_EXP_MIN - s_new[v][p];
+        const int i = i0 + k * LANES;
+        if (i < count) {
+          const int info = s_rows[i], row = info >> 8 & (CHUNK - 1), p = row >> shift;
+          x[k] = *reinterpret_cast<const uint4*>(base + s_page[i] * st.p + (info & 255) * st.r);
+          dst[k] = base + s_dst[p] * st.p + (row & in_page) * st.r;
+          shrink[k] = (info >> (v ? 24 : 18) & 63) + KV_EXP_MIN - now[p];
         }
       }
 #pragma unroll
       for (int k = 0; k < N; ++k)
-        if (dst[k]) *reinterpret_cast<uint4*>(dst[k]) = shrink[k] == 0 ? x[k] : times(x[k], exp2_int(shrink[k]));
+        if (i0 + k * LANES < count) *reinterpret_cast<uint4*>(dst[k]) = shrink[k] == 0 ? x[k] : times(x[k], shrink[k]);
     }
   }
 }
@@ -579,7 +598,7 @@ static int run(const attn_kv_evict_params* p, void* ws, size_t bytes, cudaStream
   a.half = L.half;
   a.verdict = reinterpret_cast<int*>(w);
   a.off = reinterpret_cast<int*>(w + L.off_off);
-  a.checks = cdiv(p->batch, WARPS) < MOVE_THREADS ? cdiv(p->batch, WARPS) : MOVE_THREADS;
+  a.checks = cdiv(p->batch, ONE_THREADS / 32) < MOVE_THREADS ? cdiv(p->batch, ONE_THREADS / 32) : MOVE_THREADS;
   a.plan = reinterpret_cast<int4*>(w + L.off_plan);
   a.edge = reinterpret_cast<int2*>(w + L.off_edge);
   a.holes = reinterpret_cast<int*>(w + L.off_holes);
@@ -595,15 +614,13 @@ static int run(const attn_kv_evict_params* p, void* ws, size_t bytes, cudaStream
   if (smem > 32 * 1024 && !succeeded(cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                           (int)(HELD * sizeof(uint32_t)))))
     return ATTN_ERR_CUDA;
-  if (L.cluster > 8 && !succeeded(cudaFuncSetAttribute(select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)))
-    return ATTN_ERR_CUDA;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim.x = L.cluster;
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((jobs + cdiv(a.checks, L.cluster)) * L.cluster);
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(L.cluster == 1 ? ONE_THREADS : MANY_THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = &at;

@@ -137,38 +137,47 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK>::RESIDENT) weigh_kernel(con
     uint4 qf[ONE ? FRAGS : 1];
 
     for (int base = 0; base < mine || !staged; base += 32) {
-      // pages and scales of this warp's next 32 tiles
+      // This warp's next 32 tiles, a lane each: addresses, scale, and what the others ask
+      // of them as bits.  Worked out per tile by all lanes, they were half of the
+      // instructions, which bound the kernel.
       const int count = min(32, mine - base), key_base = key0 + base * STEP;
-      int page = -1, ek = 0;
-      if (lane < count) {
-        page = __ldg(table + ((key_base + lane * STEP) >> shift));
-        if (page < 0 || page >= A.c.num_pages) {
-          page = -1;
-          report(A, ATTN_ERR_BAD_PAGE);
-        } else {
-          ek = kv_exp_of(__ldg(A.c.k_exp + (long long)page * A.c.hkv + hk));
+      long long k_at = 0, w_at = 0;
+      float scale = 0.f;
+      uint32_t has, views, wholes;           // tiles with a page; that a row sees; that all rows see
+      {
+        const int key = key_base + lane * STEP;
+        bool ok = false;
+        if (lane < count) {
+          const int page = __ldg(table + (key >> shift));
+          ok = page >= 0 && page < A.c.num_pages;
+          if (ok) {
+            const long long at = (long long)page * A.c.hkv + hk;
+            scale = exp2_int(kv_exp_of(__ldg(A.c.k_exp + at)));
+            k_at = page * A.c.sk.p + (long long)(key & in_page) * A.c.sk.r;
+            w_at = (at << shift) + (key & in_page);
+          } else {
+            report(A, ATTN_ERR_BAD_PAGE);
+          }
         }
+        has = __ballot_sync(0xffffffffu, ok);
+        views = __ballot_sync(0xffffffffu, ok && key <= vhi && key + TILE - 1 >= vlo);
+        wholes = __ballot_sync(0xffffffffu, key >= flo && key + TILE - 1 <= fhi);
       }
-      auto seen = [&](int key) { return key <= vhi && key + TILE - 1 >= vlo; };
-      auto weight_at = [&](int pg, int key) {
-        return (((long long)pg * A.c.hkv + hk) << shift) + ((key + own) & in_page);
-      };
       // tile j into its stage; a group per tile, empty ones too
       auto load = [&](int j, int stage) {
         if (j < count) {
-          const int pg = __shfl_sync(0xffffffffu, page, j), key = key_base + j * STEP;
-          if (pg >= 0) {
-            if (seen(key)) {
-              const uint8_t* p = kbase + pg * A.c.sk.p + (long long)(key & in_page) * A.c.sk.r;
-              const uint32_t dst = ring + stage * C::STAGE;
+          const long long ka = __shfl_sync(0xffffffffu, k_at, j), wa = __shfl_sync(0xffffffffu, w_at, j);
+          if (views >> j & 1) {
+            const uint8_t* p = kbase + ka;
+            const uint8_t* p8 = p + krow8;
+            const uint32_t dst = ring + stage * C::STAGE;
 #pragma unroll
-              for (int c = 0; c < PIECES; ++c) {
-                cp16(dst + c * 1024, p + c * 64);
-                cp16(dst + c * 1024 + 512, p + krow8 + c * 64);
-              }
+            for (int c = 0; c < PIECES; ++c) {
+              cp16(dst + c * 1024, p + c * 64);
+              cp16(dst + c * 1024 + 512, p8 + c * 64);
             }
-            if (t < 2) cp4(wring + stage * C::STAGE, A.weight + weight_at(pg, key));
           }
+          if (t < 2 && first && (has >> j & 1)) cp4(wring + stage * C::STAGE, A.weight + wa + own);
         }
         cp_commit();
       };
@@ -236,21 +245,21 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK>::RESIDENT) weigh_kernel(con
         }
       }
 
-      int stage = 0;
-      for (int j = 0; j < count; ++j) {
-        const int ahead = stage == 0 ? DEPTH - 1 : stage - 1;
-        load(j + DEPTH - 1, ahead);
+      for (int j0 = 0; j0 < count; j0 += DEPTH) {
+#pragma unroll
+      for (int stage = 0; stage < DEPTH; ++stage) {      // tile j is in stage j % DEPTH
+        const int j = j0 + stage;
+        if (j >= count) break;
+        load(j + DEPTH - 1, (stage + DEPTH - 1) % DEPTH);
         cp_wait<DEPTH - 1>();
-        const int pg = __shfl_sync(0xffffffffu, page, j), key = key_base + j * STEP;
-        const float scale = exp2_int(__shfl_sync(0xffffffffu, ek, j));
+        const int key = key_base + j * STEP;
+        const float u = __shfl_sync(0xffffffffu, scale, j);
+        const long long wa = __shfl_sync(0xffffffffu, w_at, j);
         const uint32_t src = ring + stage * C::STAGE, old_at = wring + stage * C::STAGE;
-        stage = stage + 1 == DEPTH ? 0 : stage + 1;
-        if (pg < 0) continue;
-        const bool in_view = seen(key);
-        if (!first && !in_view) continue;
+        const bool in_view = views >> j & 1;
+        if (!(has >> j & 1) || (!first && !in_view)) continue;
         float sum[2] = {0.f, 0.f};
         if (in_view) {
-          const bool full = key >= flo && key + TILE - 1 <= fhi;
           uint4 k[PIECES][2];
 #pragma unroll
           for (int c = 0; c < PIECES; ++c) {
@@ -280,8 +289,8 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK>::RESIDENT) weigh_kernel(con
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
-              for (int kk = 0; kk < 2; ++kk) p[r][kk] = fast_exp2(fmaf(acc[2 * kk + r], row[r].x * scale, row[r].y));
-            if (!full) {
+              for (int kk = 0; kk < 2; ++kk) p[r][kk] = fast_exp2(fmaf(acc[2 * kk + r], row[r].x * u, row[r].y));
+            if (!(wholes >> j & 1)) {
 #pragma unroll
               for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -299,14 +308,15 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK>::RESIDENT) weigh_kernel(con
         }
         const int at_key = key + own;
         if (t < 2 && at_key >= kfrom && at_key <= kto) {
-          const long long at = weight_at(pg, key);
+          float* w = A.weight + wa + own;
           // (a later chunk adds to what this lane wrote before)
-          float old = first ? lds32(old_at) * A.decay : A.weight[at];
+          float old = first ? lds32(old_at) * A.decay : *w;
           const bool is_fresh = at_key >= fresh;
           if (first && (is_fresh || A.decay == 0.f)) old = 0.f;
-          A.weight[at] = old + sum[0];
-          if (first && is_fresh) A.position[at] = (int)((unsigned)at_key + (unsigned)offset);
+          *w = old + sum[0];
+          if (first && is_fresh) A.position[wa + own] = (int)((unsigned)at_key + (unsigned)offset);
         }
+      }
       }
       cp_wait<0>();
     }
