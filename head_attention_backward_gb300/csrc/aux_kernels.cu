@@ -352,6 +352,7 @@ __device__ __forceinline__ void batch_schedule(const Problem& P, int sched, long
 // instead of 16 bytes).
 template <typename T, int VW, bool CK = false>
 __global__ void __launch_bounds__(256, PRE_BLOCKS_PER_SM) preprocess_kernel(Problem P, long long ntok, int sched, CkO ck) {
+  if constexpr (CK) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the expansion of q, k and v
   const int lane = threadIdx.x & 31;
   const long long tid = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   const long long nthreads = (long long)gridDim.x * blockDim.x;

@@ -229,6 +229,8 @@ __global__ void __launch_bounds__(THREADS) expand_kernel(const __grid_constant__
       y[v] = make_uint4(pack2t<T>(f[0], f[1]), pack2t<T>(f[2], f[3]), pack2t<T>(f[4], f[5]), pack2t<T>(f[6], f[7]));
     }
   }
+  // complete only after the kernel that it ran beside
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // -------------------------------------------------------------------- host
@@ -320,18 +322,27 @@ bool ck_dense(const int64_t in[3], const long long size[3], int d, long long own
   return true;
 }
 
-void launch_ck_expand(int dtype, const int8_t* const n[4], const uint8_t* const exp[4], void* const y[4],
-                      const long long values[4], cudaStream_t st) {
+bool launch_ck_expand(const CkExpand& x, bool beside, cudaStream_t st) {
   ckpt::ExpandArgs a{};
   uint32_t ctas = 0;
   for (int i = 0; i < 4; ++i) {
-    a.t[i] = {n[i], exp[i], y[i], (uint32_t)(values[i] / 8), ctas};
-    ctas += (uint32_t)cdiv_ll(values[i] / 8, ckpt::PER_CTA);
+    a.t[i] = {x.n[i], x.exp[i], x.y[i], (uint32_t)(x.values[i] / 8), ctas};
+    ctas += (uint32_t)cdiv_ll(x.values[i] / 8, ckpt::PER_CTA);
   }
-  if (ctas == 0) return;
-  if (dtype == ATTN_BF16) ckpt::expand_kernel<__nv_bfloat16><<<ctas, ckpt::THREADS, 0, st>>>(a);
-  else if (dtype == ATTN_FP16) ckpt::expand_kernel<__half><<<ctas, ckpt::THREADS, 0, st>>>(a);
-  else ckpt::expand_kernel<float><<<ctas, ckpt::THREADS, 0, st>>>(a);
+  if (ctas == 0) return true;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(ckpt::THREADS);
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = beside ? 1 : 0;
+  const cudaError_t e = x.dtype == ATTN_BF16   ? cudaLaunchKernelEx(&cfg, ckpt::expand_kernel<__nv_bfloat16>, a)
+                        : x.dtype == ATTN_FP16 ? cudaLaunchKernelEx(&cfg, ckpt::expand_kernel<__half>, a)
+                                               : cudaLaunchKernelEx(&cfg, ckpt::expand_kernel<float>, a);
+  return e == cudaSuccess;
 }
 
 }  // namespace attn

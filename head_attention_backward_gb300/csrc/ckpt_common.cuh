@@ -15,13 +15,22 @@ struct CkO {
   const int8_t* n;
   const uint8_t* exp;
 };
+// What a backward pass expands of a checkpoint: q, k, v (fp32: and o).
+struct CkExpand {
+  CkO o;
+  int dtype;
+  const int8_t* n[4];
+  const uint8_t* exp[4];
+  void* y[4];
+  long long values[4];
+};
 
 // checkpoint.cu: supported head dims; the strides and dimension order (outermost
 // first) of a tensor without gaps; expansion of up to four tensors.
 bool ck_headdim(int d);
 bool ck_dense(const int64_t in[3], const long long size[3], int d, long long own[3], int order[3]);
-void launch_ck_expand(int dtype, const int8_t* const n[4], const uint8_t* const exp[4], void* const y[4],
-                      const long long values[4], cudaStream_t st);
+// beside: it may run beside the preprocess kernel launched just before it.
+bool launch_ck_expand(const CkExpand& x, bool beside, cudaStream_t st);
 
 inline bool ck_aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

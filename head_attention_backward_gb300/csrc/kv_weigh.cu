@@ -32,7 +32,14 @@ constexpr int NTHREADS = 32 * NWARPS;
 constexpr int TILE = 16;
 constexpr int CHUNK = 128;          // query rows in shared memory at a time
 constexpr int MIN_TILES = 2 * NWARPS;
-constexpr int LONG_ROWS = 64;
+// Query rows (tokens x heads of the group) of a segment beyond which it goes to the
+// tensor cores.  8 requests of 4,000 tokens, 8 kv heads of 128: 128 rows 38 us here,
+// 47 us there; 256 rows 74 and 54.  4 requests, 4 heads of 192: 96 rows 21 and 21, 128
+// rows 25 and 19; of 256: 27 and 29, 32 and 28.
+constexpr int LONG_ROWS = 128;
+// CTAs at most, unless requests x kv heads are more (64 requests of up to 8,192 tokens:
+// 65 us with 1,536, 66 with 2,560, 71 with 4,096).
+constexpr int MAX_GRID = 1536;
 
 template <typename T> __device__ __forceinline__ float2 up2(uint32_t x);
 template <> __device__ __forceinline__ float2 up2<__nv_bfloat16>(uint32_t x) {
@@ -397,7 +404,7 @@ static int run(const attn_kv_weigh_params* p, cudaStream_t st) {
   a.long_from = a.g <= long_group(p->cache.d_qk) ? LONG_ROWS / a.g : 1 << 30;
   const int jobs = p->batch * p->cache.nhead_kv;
   const int tiles = cdiv(a.max_k, TILE);
-  int nsplit = 2560 / jobs;
+  int nsplit = MAX_GRID / jobs;
   nsplit = nsplit < cdiv(tiles, MIN_TILES) ? nsplit : cdiv(tiles, MIN_TILES);
   a.nsplit = nsplit < 1 ? 1 : nsplit;
   const long long most = (long long)(p->max_seqlen_q < p->total_q ? p->max_seqlen_q : p->total_q) * a.g;
