@@ -590,3 +590,38 @@ def test_offsets_past_32_bits(B):
     evict_ref.evict([300], [700], [0], [near], [0] * 3, 0, {"k": kc, "v": vc}, exps, got, where)
     for i, p in enumerate(table[0]):
         assert torch.equal(k[p].cpu(), kc[i]) and torch.equal(v[p].cpu(), vc[i])
+
+
+@pytest.mark.parametrize("lens,new,bound", [
+    ([150] * 3 + [900] + [40] * 300 + [333], [1] * 3 + [300] + [1] * 300 + [200], 1 << 17),   # two lists, few long segments
+    ([700, 260, 500], [600, 250, 140], 1 << 16),                                             # a list, several items a CTA
+])
+def test_weigh_loose_bounds(B, lens, new, bound):
+    """Long segments among short ones under a bound that leaves room for many: they are
+    listed on the device, and their weights are those of a tight bound, but for the order
+    of the additions, which the bounds decide: a rounding per query row and side."""
+    g = torch.Generator().manual_seed(len(lens))
+    page, hkv, group, d = 16, 2, 2, 64
+    table, pool = block_table(lens, page, g)
+    kc, ke = random_cache(pool, page, hkv, d, g)
+    c = handle(B, kc, kc.clone(), ke, ke.clone())
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    q = torch.randn((cu[-1], hkv * group, d), generator=g).bfloat16()
+    lse = torch.full((hkv * group, cu[-1]), 4.0)
+    weight, position = random_weights(pool, hkv, page, g)
+    wide = torch.zeros((len(lens), bound // page), dtype=I32)
+    wide[:, :len(table[0])] = torch.tensor(table)
+    results = []
+    for td, most in ((dev(table), max(lens)), (wide.cuda(), bound)):
+        w = weights_of(B, weight, position)
+        B.kv_weigh(q.cuda(), lse.cuda(), c, w, td, dev(lens), dev(cu), scale=0.1, max_seqlen_q=max(new), max_seqlen_k=most)
+        w.check()
+        results.append(w)
+    a, b = (w.weight.double() for w in results)
+    assert bool(((a - b).abs() <= 2 * 2.0 ** -24 * (max(new) * group + 8) * b.abs()).all())
+    assert torch.equal(results[0].position, results[1].position)
+    if len(lens) < 10:
+        want, where, slack = evict_ref.weigh(q, lse, cu, lens, table, kc, ke, weight, position, [0] * len(lens), 0.1)
+        assert bool(((results[1].weight.cpu().double() - want).abs() <= slack).all())
