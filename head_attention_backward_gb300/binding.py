@@ -110,7 +110,7 @@ class AttnKvWeighParams(ctypes.Structure):
                 ("max_seqlen_k", _i32), ("max_blocks", _i32), ("mask", _i32), ("window_left", _i32),
                 ("window_right", _i32), ("softmax_scale", _f32), ("decay", _f32), ("cu_seqlens_q", _vp),
                 ("cu_seqlens_q_padded", _vp), ("seqlens_k", _vp), ("block_table", _vp),
-                ("table_stride", ctypes.c_int64), ("position_offsets", _vp), ("q", _vp), ("lse", _vp),
+                ("table_stride", ctypes.c_int64), ("position_offsets", _vp), ("new_lens", _vp), ("q", _vp), ("lse", _vp),
                 ("stride_q", _i64x3), ("weights", AttnKvWeights), ("cache", AttnKvCache)]
 
 
@@ -732,22 +732,24 @@ class KvWeights(NamedTuple):
 
 
 def kv_weigh(q, lse, cache: KvCache, weights: KvWeights, block_table, seqlens_k, cu_seqlens_q, *, scale,
-             mask=MASK_CAUSAL_BOTTOM_RIGHT, left=-1, right=-1, decay=1.0, position_offsets=None, max_seqlen_q,
-             max_seqlen_k, cu_seqlens_q_padded=None, stream=None):
+             mask=MASK_CAUSAL_BOTTOM_RIGHT, left=-1, right=-1, decay=1.0, position_offsets=None, new_lens=None,
+             max_seqlen_q, max_seqlen_k, cu_seqlens_q_padded=None, stream=None):
     """Add to `weights` what the cached tokens get of the attention of packed
     queries q (attn_kv_weigh): after attn_kv_forward, with its arguments and its
-    LSE.  The segments' new tokens start from 0 and get their positions, the other
-    tokens' weights are multiplied by `decay` first.  position_offsets int32 [B] as
-    in kv_plan."""
+    LSE.  The segments' new tokens (those of q, or the last new_lens[b], int32 [B])
+    start from 0 and get their positions, the other tokens' weights are multiplied
+    by `decay` first.  position_offsets int32 [B] as in kv_plan.  Every appended
+    token has to be new in one call; where only the last queries of a prompt are to
+    weigh it, pass those (with their LSE) and new_lens = the prompt's length."""
     if stream is not None:
         with _on_stream(stream):
             return kv_weigh(q, lse, cache, weights, block_table, seqlens_k, cu_seqlens_q, scale=scale, mask=mask,
                             left=left, right=right, decay=decay, position_offsets=position_offsets,
-                            max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k,
+                            new_lens=new_lens, max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k,
                             cu_seqlens_q_padded=cu_seqlens_q_padded)
     st = (_marshal or _load_marshal()).weigh(q, lse, cache, cache.index, weights, block_table, seqlens_k, cu_seqlens_q,
-                                             cu_seqlens_q_padded, position_offsets, scale, mask, left, right, decay,
-                                             max_seqlen_q, max_seqlen_k)
+                                             cu_seqlens_q_padded, position_offsets, new_lens, scale, mask, left, right,
+                                             decay, max_seqlen_q, max_seqlen_k)
     if st != 0:
         raise AttnError(st, "attn_kv_weigh")
 

@@ -108,11 +108,8 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK>::RESIDENT) weigh_kernel(con
   if (J.bad && tid == 0 && split == 0 && hk == 0) report(A, ATTN_ERR_BAD_SEQLENS);
   if (J.lq <= 0 || J.lq > A.long_from) return;
   const MaskArgs mk = mask_args(A.mask, A.left, A.right, J.lq, J.lk);
-  // keys whose weights change: those that a query sees, or all if the old ones decay
   int kfrom, kto;
-  seen_by(mk, J.lk, 0, J.lq - 1, kfrom, kto);
-  if (A.decay != 1.f) kfrom = 0, kto = J.lk - 1;
-  const int fresh = A.fresh ? J.lk - J.lq : J.lk;           // keys from here on start from 0
+  changing(A, J, mk, kfrom, kto);
   const int k0 = kfrom & ~(TILE - 1), ntile_all = kto >= kfrom ? (kto - k0) / TILE + 1 : 0;
   const int per = cdiv(max(MIN_TILES, cdiv(ntile_all, A.nsplit)), NWARPS) * NWARPS;
   const int tile0 = split * per, ntile = min(per, ntile_all - tile0);
@@ -318,7 +315,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK>::RESIDENT) weigh_kernel(con
           float* w = A.weight + wa + own;
           // (a later chunk adds to what this lane wrote before)
           float old = first ? lds32(old_at) * A.decay : *w;
-          const bool is_fresh = at_key >= fresh;
+          const bool is_fresh = at_key >= J.fresh;
           if (first && (is_fresh || A.decay == 0.f)) old = 0.f;
           *w = old + sum[0];
           if (first && is_fresh) A.position[wa + own] = (int)((unsigned)at_key + (unsigned)offset);
@@ -372,7 +369,7 @@ static int run(const attn_kv_weigh_params* p, cudaStream_t st) {
   const void* words[] = {p->cu_seqlens_q, p->seqlens_k, p->block_table, p->weights.weight, p->weights.position, p->weights.status};
   for (const void* x : words)
     if (!x || !aligned_to(x, 4)) return ATTN_ERR_INVALID_ARG;
-  if (!aligned_to(p->cu_seqlens_q_padded, 4) || !aligned_to(p->position_offsets, 4) || !aligned_to(p->lse, 4) ||
+  if (!aligned_to(p->cu_seqlens_q_padded, 4) || !aligned_to(p->position_offsets, 4) || !aligned_to(p->new_lens, 4) || !aligned_to(p->lse, 4) ||
       !aligned_to(p->q, 16) || !packed_strides(p->stride_q, p->nhead_q, p->cache.d_qk, &a.sq))
     return ATTN_ERR_INVALID_ARG;
   if (p->total_q == 0) return ATTN_OK;
@@ -385,6 +382,7 @@ static int run(const attn_kv_weigh_params* p, cudaStream_t st) {
   a.table = p->block_table;
   a.table_stride = p->table_stride;
   a.offsets = p->position_offsets;
+  a.new_lens = p->new_lens;
   const long long cap = (long long)p->max_blocks << a.c.page_shift;
   a.max_k = p->max_seqlen_k < cap ? p->max_seqlen_k : (int)cap;
   a.total_q = p->total_q;

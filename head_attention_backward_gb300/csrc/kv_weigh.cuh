@@ -17,12 +17,13 @@ struct Args {
   const int* table;
   long long table_stride;
   const int* offsets;      // of positions, per request, or null
+  const int* new_lens;     // keys new to the weights, per request, or null: see fresh
   int max_k;               // min(max_seqlen_k, max_blocks pages)
   int total_q, max_q;
   int long_from;           // segments of more tokens are the other kernel's
   int hq, g;               // query heads, per kv head
   int mask, left, right;
-  int fresh;               // 1: the last tokens of a segment's keys are its new ones
+  int fresh;               // without new_lens: 1: the last keys of a segment are its query tokens
   float scale_log2, decay;
   int nsplit;              // most splits of a request's keys
   float* weight;           // [page][kv head][row]
@@ -33,6 +34,7 @@ struct Args {
 
 struct Segment {
   int lq, lk, q0;
+  int fresh;               // keys from here on start from 0
   bool bad;                // lengths outside the declared bounds: left alone
 };
 __device__ __forceinline__ Segment segment_of(const Args& A, int b) {
@@ -40,7 +42,10 @@ __device__ __forceinline__ Segment segment_of(const Args& A, int b) {
   s.lq = __ldg(A.cu_q + b + 1) - __ldg(A.cu_q + b);
   s.q0 = __ldg(A.st_q + b);
   s.lk = __ldg(A.len_k + b);
-  s.bad = s.lq < 0 || s.lq > A.max_q || s.q0 < 0 || (long long)s.q0 + s.lq > A.total_q || s.lk < 0 || s.lk > A.max_k;
+  const int added = A.new_lens ? __ldg(A.new_lens + b) : A.fresh ? min(s.lq, s.lk) : 0;
+  s.fresh = s.lk - added;
+  s.bad = s.lq < 0 || s.lq > A.max_q || s.q0 < 0 || (long long)s.q0 + s.lq > A.total_q || s.lk < 0 || s.lk > A.max_k ||
+          (s.lq > 0 && (added < 0 || added > s.lk));
   if (s.bad) s.lq = 0;
   return s;
 }
@@ -59,6 +64,15 @@ __device__ __forceinline__ void seen_by(const MaskArgs& m, int lk, int i0, int i
 __device__ __forceinline__ bool whole(const MaskArgs& m, int lk, int i0, int i1, int j0, int j1) {
   return j1 < lk && (m.left < 0 || j0 >= (long long)i1 + m.off - m.left) &&
          (m.right < 0 || j1 <= (long long)i0 + m.off + m.right);
+}
+
+// Keys of a segment whose weights change, lo > hi: none.  Those that a query sees and the
+// new ones, or all if the old ones decay.
+__device__ __forceinline__ void changing(const Args& A, const Segment& s, const MaskArgs& m, int& lo, int& hi) {
+  seen_by(m, s.lk, 0, s.lq - 1, lo, hi);
+  if (lo > hi) lo = s.lk, hi = s.lk - 1;
+  if (s.fresh < s.lk) lo = min(lo, s.fresh), hi = s.lk - 1;
+  if (A.decay != 1.f) lo = 0, hi = s.lk - 1;
 }
 
 // Whether token i sees key j.

@@ -135,21 +135,20 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// A long segment, and the keys of it whose weights change: those that a query sees, or
-// all if the old ones decay.  kfrom > kto: none, or not a long segment.
+// A long segment, and the keys of it whose weights change; kfrom > kto: none, or not a
+// long segment.
 struct Long {
-  int q0, lq, lk, kfrom, kto;
+  int q0, lq, lk, fresh, kfrom, kto;
   MaskArgs mk;
 };
 __device__ __forceinline__ Long long_at(const Args& A, int b) {
   Long L{};
   const Segment J = segment_of(A, b);
-  L.q0 = J.q0, L.lq = J.lq, L.lk = J.lk;
+  L.q0 = J.q0, L.lq = J.lq, L.lk = J.lk, L.fresh = J.fresh;
   L.kfrom = 0, L.kto = -1;
   if (J.lq <= A.long_from) return L;
   L.mk = mask_args(A.mask, A.left, A.right, J.lq, J.lk);
-  seen_by(L.mk, J.lk, 0, J.lq - 1, L.kfrom, L.kto);
-  if (A.decay != 1.f) L.kfrom = 0, L.kto = J.lk - 1;
+  changing(A, J, L.mk, L.kfrom, L.kto);
   return L;
 }
 
@@ -203,11 +202,10 @@ __device__ __forceinline__ long long weight_at(const Args& A, const Item& I, int
   const int shift = A.c.page_shift;
   return (((long long)page * A.c.hkv + I.hk) << shift) + (key & ((1 << shift) - 1));
 }
-__device__ __forceinline__ bool is_fresh(const Args& A, const Item& I, int key) { return A.fresh && key >= I.s.lk - I.s.lq; }
 // The new weight of a key that got w, and a new key's position.
 __device__ __forceinline__ void settle(const Args& A, const Item& I, int key, int page, float old, float w) {
   const long long at = weight_at(A, I, key, page);
-  const bool fresh = is_fresh(A, I, key);
+  const bool fresh = key >= I.s.fresh;
   A.weight[at] = (fresh || A.decay == 0.f ? 0.f : A.decay * old) + w;
   if (fresh) A.position[at] = (int)((unsigned)key + (A.offsets ? (unsigned)__ldg(A.offsets + I.b) : 0u));
 }

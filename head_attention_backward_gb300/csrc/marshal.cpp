@@ -548,9 +548,9 @@ float number(PyObject* o, const char* what) {
 }
 
 // weigh(q, lse, KvCache, device, KvWeights, block_table, seqlens_k, cu_seqlens_q, cu_seqlens_q_padded or None,
-// position_offsets or None, scale, mask, left, right, decay, max_seqlen_q, max_seqlen_k) -> status
+// position_offsets or None, new_lens or None, scale, mask, left, right, decay, max_seqlen_q, max_seqlen_k) -> status
 PyObject* py_weigh(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 17, [&]() -> PyObject* {
+  return guarded(n, 18, [&]() -> PyObject* {
     const at::Tensor &q = tensor(a[0], "q"), &lse = tensor(a[1], "lse"), &lens = tensor(a[6], "seqlens_k");
     const int index = whole32(a[3], "device");
     attn_kv_weigh_params p{};
@@ -573,13 +573,14 @@ PyObject* py_weigh(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.cu_seqlens_q = vector<int32_t>(a[7], "cu_seqlens_q", batch + 1, index);
     if (a[8] != Py_None) p.cu_seqlens_q_padded = vector<int32_t>(a[8], "cu_seqlens_q_padded", batch + 1, index);
     if (a[9] != Py_None) p.position_offsets = vector<int32_t>(a[9], "position_offsets", batch, index);
-    p.softmax_scale = number(a[10], "scale");
-    p.mask = whole32(a[11], "mask");
-    p.window_left = whole32(a[12], "left");
-    p.window_right = whole32(a[13], "right");
-    p.decay = number(a[14], "decay");
-    p.max_seqlen_q = whole32(a[15], "max_seqlen_q");
-    p.max_seqlen_k = whole32(a[16], "max_seqlen_k");
+    if (a[10] != Py_None) p.new_lens = vector<int32_t>(a[10], "new_lens", batch, index);
+    p.softmax_scale = number(a[11], "scale");
+    p.mask = whole32(a[12], "mask");
+    p.window_left = whole32(a[13], "left");
+    p.window_right = whole32(a[14], "right");
+    p.decay = number(a[15], "decay");
+    p.max_seqlen_q = whole32(a[16], "max_seqlen_q");
+    p.max_seqlen_k = whole32(a[17], "max_seqlen_k");
     p.q = q.data_ptr();
     p.lse = pointer<const float>(lse);
     rows3(q, "q", p.stride_q);

@@ -726,17 +726,21 @@ typedef struct {
  * For each segment b with query tokens, key j < seqlens_k[b] and kv head:
  *   weight <- old + sum of exp(softmax_scale * q_i k_j - LSE_i)
  * over the query rows i that see j and the query heads of the group.  old is
- * decay * weight, but 0 for the segment's own new tokens: with
- * ATTN_MASK_CAUSAL_BOTTOM_RIGHT and ATTN_MASK_WINDOW the last Lq of its keys,
- * whose position becomes j + position_offsets[b] (with the other masks no key
- * is new).  With decay = 0 the old weights are not read.  Rows whose LSE is not
- * finite add nothing; a key that holds NaN has weight NaN.
+ * decay * weight, but 0 for keys that are new to the weights, whose position
+ * becomes j + position_offsets[b]: the last new_lens[b] keys of the segment, or,
+ * where new_lens is null, its last Lq with ATTN_MASK_CAUSAL_BOTTOM_RIGHT and
+ * ATTN_MASK_WINDOW and none with the other masks.  Every appended token has to
+ * be new in one call: until then its weight and position are what its row held
+ * before.  (Where only the last queries of a prompt weigh it, new_lens is the
+ * prompt's length.)  With decay = 0 the old weights are not read.  Rows whose
+ * LSE is not finite add nothing; a key that holds NaN has weight NaN.
  * Sums and weights are fp32, scores are sums of exact products; the order of
  * the additions is fixed by the call's sizes, so a call repeats bit for bit.
  * A page belongs to one request of a call: where several name it, its weights
- * are unspecified.  A segment outside its bounds (as in attn_kv_fwd; seqlens_k
- * outside 0 .. min(max_seqlen_k, max_blocks pages) too) is left alone, the
- * tokens of a page outside the cache are skipped, and *weights.status has it. */
+ * are unspecified.  A segment without query tokens is left alone, so is one
+ * outside its bounds (as in attn_kv_fwd; seqlens_k outside 0 ..
+ * min(max_seqlen_k, max_blocks pages) and new_lens outside 0 .. seqlens_k too);
+ * the tokens of a page outside the cache are skipped; *weights.status has it. */
 typedef struct {
   int32_t dtype;          /* ATTN_BF16 or ATTN_FP16: type of q                     */
   int32_t batch;          /* segments, >= 1                                        */
@@ -756,6 +760,7 @@ typedef struct {
   const int32_t* block_table;  /* device, [batch] rows of max_blocks               */
   int64_t table_stride;        /* elements from row to row, >= max_blocks          */
   const int32_t* position_offsets; /* device, [batch], or NULL: 0                  */
+  const int32_t* new_lens;     /* device, [batch], or NULL, see above              */
   const void* q;          /* device, [total_q, nhead_q, d_qk], 16-byte aligned     */
   const float* lse;       /* device, [nhead_q, total_q], fp32 natural log          */
   int64_t stride_q[3];    /* as in attn_kv_fwd_params                              */

@@ -18,7 +18,8 @@ from oracle import attn_ref, kv_ref
 F64 = torch.float64
 
 
-def weigh(q, lse, cu, lens, table, kc, ke, weight, position, offsets, scale, mask=2, left=-1, right=-1, decay=1.0):
+def weigh(q, lse, cu, lens, table, kc, ke, weight, position, offsets, scale, mask=2, left=-1, right=-1, decay=1.0,
+          new_lens=None):
     """New weights (fp64) and positions, and for tolerances the sum over the rows of
     p (ds + |s| + |LSE| + 1) units: see the tests.  weight and position [pages,
     heads, page] are not changed."""
@@ -31,7 +32,8 @@ def weigh(q, lse, cu, lens, table, kc, ke, weight, position, offsets, scale, mas
             continue
         pages = table[b][: (n + page - 1) // page]
         see = attn_ref.visible(hi - lo, n, mask, left, right)
-        touched = see.any(0) if decay == 1.0 else torch.ones(n, dtype=torch.bool)
+        added = new_lens[b] if new_lens is not None else min(hi - lo, n) if mask in (2, 3) else 0
+        touched = see.any(0) | (torch.arange(n) >= n - added) if decay == 1.0 else torch.ones(n, dtype=torch.bool)
         k = kv_ref.gather(kc, ke, [max(p, 0) for p in pages], n)
         for h in range(kc.shape[2]):
             got, err = torch.zeros(n, dtype=F64), torch.zeros(n, dtype=F64)
@@ -47,7 +49,7 @@ def weigh(q, lse, cu, lens, table, kc, ke, weight, position, offsets, scale, mas
                 pg = pages[j // page]
                 if pg < 0 or pg >= kc.shape[0] or not bool(touched[j]):
                     continue
-                fresh = mask in (2, 3) and j >= n - (hi - lo)
+                fresh = j >= n - added
                 old = 0.0 if fresh or decay == 0.0 else decay * float(weight[pg, h, j % page])
                 out[pg, h, j % page] = old + got[j]
                 slack[pg, h, j % page] = err[j] + (2.0 ** -23 * ((hi - lo) * group + 8)) * (abs(old) + float(got[j]))

@@ -71,7 +71,7 @@ def weigh_params(cache_kw=None, weights_kw=None, **kw):
     (dict(decay=-0.5), -1), (dict(decay=float("inf")), -1), (dict(decay=float("nan")), -1), (dict(batch=2 ** 24), -1),
     (dict(cu_seqlens_q=None), -1), (dict(seqlens_k=None), -1), (dict(block_table=None), -1), (dict(q=None), -1),
     (dict(lse=None), -1), (dict(q=A[3] + 8), -1), (dict(lse=A[4] + 2), -1), (dict(position_offsets=A[8] + 1), -1),
-    (dict(cu_seqlens_q_padded=A[0] + 2), -1), (dict(stride_q=(0, 1004, 128)), -1),
+    (dict(cu_seqlens_q_padded=A[0] + 2), -1), (dict(new_lens=A[8] + 2), -1), (dict(stride_q=(0, 1004, 128)), -1),
     (dict(weights_kw=dict(weight=None)), -1), (dict(weights_kw=dict(position=None)), -1),
     (dict(weights_kw=dict(status=None)), -1), (dict(weights_kw=dict(weight=A[9] + 2)), -1)]
     + [(dict(cache_kw=c), s) for c, s in BAD_CACHES + BAD_CACHE_POINTERS])
@@ -134,7 +134,7 @@ def test_marshalling_refuses_before_it_calls(lib):
     build.build_marshal()
     m = B._load_marshal()
     q = torch.zeros((4, 2, 64))
-    for fn, n in ((m.weigh, 17), (m.evict, 15), (m.checkpoint, 5), (m.backward, 25), (m.plan, 9)):
+    for fn, n in ((m.weigh, 18), (m.evict, 15), (m.checkpoint, 5), (m.backward, 25), (m.plan, 9)):
         for x in (None, 3.5, "x", q, torch.zeros(0), torch.zeros((), dtype=torch.int32), (1, 2, 3), (q,) * 8):
             with pytest.raises((TypeError, ValueError)):
                 fn(*(x,) * n)

@@ -26,7 +26,7 @@ def random_weights(pages, heads, page, g):
 # --------------------------------------------------------------------- weigh
 
 def weigh_case(B, dtype, lens, new, page, hkv, group, d, dv=None, mask=2, left=-1, right=-1, decay=1.0, seed=0, scale=None,
-               padded=False, offsets=True, tight=True):
+               padded=False, offsets=True, tight=True, fresh=None):
     """Runs one call and compares; the kernel's error per weight is at most the sum of
     p (score error + exponent's argument and ex2, 2^-22 (|s| + |LSE| + 1)) over its rows,
     plus one rounding per addition (the oracle returns that bound)."""
@@ -55,12 +55,12 @@ def weigh_case(B, dtype, lens, new, page, hkv, group, d, dv=None, mask=2, left=-
     weight, position = random_weights(pool, hkv, page, g)
     off = [7 * b + 1 for b in range(len(lens))] if offsets else [0] * len(lens)
     want, where, slack = evict_ref.weigh(q[rows], lse[:, rows], cu, lens, table, kc, ke, weight, position, off, scale, mask, left,
-                                         right, decay)
+                                         right, decay, fresh)
     c = handle(B, kc, vc, ke, ve)
     w = weights_of(B, weight, position)
     kw = dict(scale=scale, mask=mask, left=left, right=right, decay=decay, max_seqlen_q=max(new) if tight else 1000,
               max_seqlen_k=max(lens) if tight else len(table[0]) * page,
-              position_offsets=dev(off) if offsets else None,
+              position_offsets=dev(off) if offsets else None, new_lens=dev(fresh) if fresh else None,
               cu_seqlens_q_padded=dev(starts + [total]) if padded else None)
     B.kv_weigh(q.cuda(), lse.cuda(), c, w, dev(table), dev(lens), dev(cu), **kw)
     w.check()
@@ -92,6 +92,32 @@ def test_weigh(B, lens, new, page, hkv, group, d, dv, dtype):
 @pytest.mark.parametrize("decay", [1.0, 0.75, 0.0])
 def test_weigh_masks_and_decay(B, mask, left, right, decay):
     weigh_case(B, torch.bfloat16, [130, 70, 33], [5, 1, 33], 16, 2, 2, 64, 64, mask, left, right, decay)
+
+
+@pytest.mark.parametrize("mask,left", [(0, -1), (1, -1), (2, -1), (3, 20)])
+@pytest.mark.parametrize("new", [[1, 4, 0, 2], [70, 4, 0, 90]])
+@pytest.mark.parametrize("decay", [1.0, 0.5])
+def test_weigh_new_lens(B, mask, left, new, decay):
+    """Fewer or more tokens are new than query: whole prompts that their last queries
+    weigh, tokens weighed before, none.  Both kernels."""
+    weigh_case(B, torch.bfloat16, [150, 70, 33, 300], new, 16, 2, 2, 64, 64, mask, left, 0 if mask == 3 else -1, decay,
+               fresh=[150, 0, 33, 217])
+
+
+def test_weigh_reports_new_lens(B):
+    g, table, pool, kc, ke, vc, ve = small(B)
+    q, lse = torch.randn((2, 4, 64), generator=g).bfloat16().cuda(), torch.full((4, 2), 3.0, device="cuda")
+    weight, position = random_weights(pool, 2, 16, g)
+    for bad in ([-1, 1], [51, 1]):
+        w = weights_of(B, weight, position)
+        B.kv_weigh(q, lse, handle(B, kc, vc, ke, ve), w, dev(table), dev([50, 20]), dev([0, 1, 2]), scale=0.1, new_lens=dev(bad),
+                   max_seqlen_q=1, max_seqlen_k=64)
+        with pytest.raises(B.AttnError) as e:
+            w.check()
+        assert e.value.status == B.ATTN_ERR_BAD_SEQLENS
+        for j in range(50):
+            assert torch.equal(w.weight[table[0][j // 16], :, j % 16].cpu(), weight[table[0][j // 16], :, j % 16])
+        assert not torch.equal(w.weight[table[1][0]].cpu(), weight[table[1][0]])
 
 
 LONG_WEIGHS = [
