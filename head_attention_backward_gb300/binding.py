@@ -825,7 +825,7 @@ def checkpoint(q, k, v, o, *, out=None, stream=None):
     st, made = (_marshal or _load_marshal()).checkpoint(q, k, v, o, out)
     if st != 0:
         raise AttnError(st, "attn_checkpoint_save")
-    return AttnCheckpoint(*made) if out is None else out
+    return AttnCheckpoint._make(made) if out is None else out
 
 
 _CKPT_STEPS = ("attn_bwd_checkpoint_workspace_size", "attn_bwd_checkpoint", "attn_bwd_read_status",

@@ -755,53 +755,58 @@ PyObject* py_checkpoint(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (p.d_qk % ATTN_CKPT_GROUP || p.d_v % ATTN_CKPT_GROUP || p.d_qk < 1 || p.d_v < 1)
       return Py_BuildValue("iO", (int)ATTN_ERR_UNSUPPORTED_HEADDIM, Py_None);
     cudaStream_t stream = stream_of(index);
-    PyObject* out = a[4];
-    if (out == Py_None) {
-      // one block for the eight tensors, which live and die together
-      int64_t begin[8], total = 0;
-      for (int i = 0; i < 8; ++i) {
-        begin[i] = total;
-        total += (x[i & 3]->numel() / (i < 4 ? 1 : ATTN_CKPT_GROUP) + 255) & ~255LL;
-      }
-      const at::Tensor block = at::empty({total}, x[0]->options().dtype(at::kByte));
-      out = PyTuple_New(8);
-      for (int i = 0; i < 8; ++i) {
-        const at::Tensor& s = *x[i & 3];
-        int order[3];
-        memory_order(s, order);
-        const int64_t last = s.size(-1) / (i < 4 ? 1 : ATTN_CKPT_GROUP), dims = s.dim();
-        int64_t size[4], stride[4], next = last;
-        size[dims - 1] = last;
-        stride[dims - 1] = 1;
-        for (int64_t k = dims - 2; k >= 0; --k) {
-          size[order[k]] = s.size(order[k]);
-          stride[order[k]] = next;
-          next *= std::max<int64_t>(1, s.size(order[k]));
-        }
-        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
-            c10::Storage(block.storage()), block.key_set(), caffe2::TypeMeta::fromScalarType(i < 4 ? at::kChar : at::kByte));
-        t.unsafeGetTensorImpl()->set_storage_offset(begin[i]);
-        t.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef(size, dims), at::IntArrayRef(stride, dims));
-        PyTuple_SET_ITEM(out, i, THPVariable_Wrap(t));
-      }
-    } else {
-      Py_INCREF(out);
-    }
-    struct Release {
-      PyObject* o;
-      ~Release() { Py_XDECREF(o); }
-    } held{out};
-    const at::Tensor *n[4], *exp[4];
-    read_checkpoint(out, n, exp, &p.ckpt);
-    for (int i = 0; i < 4; ++i) {
-      if (n[i]->sizes() != x[i]->sizes() || !on(*n[i], index)) refuse(std::string("out.") + CK_NAMES[i], "of its input's shape, next to it", *n[i]);
-      if (a[4] != Py_None) {
+    if (a[4] != Py_None) {
+      const at::Tensor *n[4], *exp[4];
+      read_checkpoint(a[4], n, exp, &p.ckpt);
+      for (int i = 0; i < 4; ++i) {
+        if (n[i]->sizes() != x[i]->sizes() || !on(*n[i], index)) refuse(std::string("out.") + CK_NAMES[i], "of its input's shape, next to it", *n[i]);
         changed(*n[i]);
         changed(*exp[i]);
       }
+      return Py_BuildValue("iO", call([&] { return entries.ck_save(&p, stream); }), a[4]);
     }
-    const int st = call([&] { return entries.ck_save(&p, stream); });
-    return Py_BuildValue("iO", st, out);
+    // one block for the eight tensors, which live and die together
+    int64_t begin[8], total = 0;
+    for (int i = 0; i < 8; ++i) {
+      begin[i] = total;
+      total += (x[i & 3]->numel() / (i < 4 ? 1 : ATTN_CKPT_GROUP) + 255) & ~255LL;
+    }
+    const at::Tensor block = at::empty({total}, x[0]->options().dtype(at::kByte));
+    uint8_t* bytes = pointer<uint8_t>(block);
+    int8_t** numbers[4] = {&p.ckpt.q, &p.ckpt.k, &p.ckpt.v, &p.ckpt.o};
+    uint8_t** exps[4] = {&p.ckpt.q_exp, &p.ckpt.k_exp, &p.ckpt.v_exp, &p.ckpt.o_exp};
+    int64_t* strides[4] = {p.ckpt.stride_q, p.ckpt.stride_k, p.ckpt.stride_v, p.ckpt.stride_o};
+    at::Tensor made[8];
+    for (int i = 0; i < 8; ++i) {
+      const at::Tensor& s = *x[i & 3];
+      int order[3];
+      memory_order(s, order);
+      const int64_t last = s.size(-1) / (i < 4 ? 1 : ATTN_CKPT_GROUP), dims = s.dim();
+      int64_t size[4], stride[4], next = last;
+      size[dims - 1] = last;
+      stride[dims - 1] = 1;
+      for (int64_t k = dims - 2; k >= 0; --k) {
+        size[order[k]] = s.size(order[k]);
+        stride[order[k]] = next;
+        next *= std::max<int64_t>(1, s.size(order[k]));
+      }
+      made[i] = at::detail::make_tensor<c10::TensorImpl>(
+          c10::Storage(block.storage()), block.key_set(), caffe2::TypeMeta::fromScalarType(i < 4 ? at::kChar : at::kByte));
+      made[i].unsafeGetTensorImpl()->set_storage_offset(begin[i]);
+      made[i].unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef(size, dims), at::IntArrayRef(stride, dims));
+      if (i < 4) {
+        *numbers[i] = reinterpret_cast<int8_t*>(bytes + begin[i]);
+        strides[i][0] = dims == 4 ? stride[0] : 0;
+        strides[i][1] = stride[dims - 3];
+        strides[i][2] = stride[dims - 2];
+      } else {
+        *exps[i - 4] = bytes + begin[i];
+      }
+    }
+    const int status = call([&] { return entries.ck_save(&p, stream); });
+    PyObject* out = PyTuple_New(8);
+    for (int i = 0; i < 8; ++i) PyTuple_SET_ITEM(out, i, THPVariable_Wrap(made[i]));
+    return Py_BuildValue("iN", status, out);
   });
 }
 
