@@ -208,6 +208,33 @@ def test_backward_of_packed_segments(B, segments, dtype, dqk, dv):
         assert torch.equal(a, x)
 
 
+@pytest.mark.parametrize("det", [0, 1])
+def test_backward_of_padded_segments(B, det):
+    """Segments with padding behind them: their rows' gradients, zeros elsewhere."""
+    g = torch.Generator().manual_seed(6)
+    lens, starts, rows = [50, 0, 129, 7], [0, 60, 64, 200, 230], 240
+    q, k, v, do = (torch.zeros((rows, h, 64)).bfloat16() for h in (4, 2, 2, 4))
+    for x in (q, k, v, do):
+        for n, s in zip(lens, starts):
+            x[s:s + n] = torch.randn((n, *x.shape[1:]), generator=g).bfloat16()
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    pad = torch.tensor(starts, dtype=torch.int32).cuda()
+    kw = dict(scale=0.125, mask=2, cu_seqlens_q=cu, cu_seqlens_k=cu, cu_seqlens_q_padded=pad, cu_seqlens_k_padded=pad,
+              max_seqlen_q=129, max_seqlen_k=129)
+    dev = [x.cuda() for x in (q, k, v)]
+    o, lse = B.attn_forward(*dev, **kw)
+    c = B.checkpoint(*dev, o)
+    wide = [ckpt_ref.values(getattr(c, n).cpu(), getattr(c, n + "_exp").cpu(), torch.bfloat16).bfloat16().cuda() for n in NAMES]
+    got = B.attn_backward_checkpoint(c, do.cuda(), lse, deterministic=det, **kw)
+    same = B.attn_backward(*wide, do.cuda(), lse, deterministic=1, **kw)
+    for a, x in zip(got, same):
+        if det:
+            assert torch.equal(a, x)
+        else:      # atomics: at most two fp32 partials a query tile here, so a rounding of bf16
+            assert float((a.float() - x.float()).abs().max()) <= 2.0 ** -7 * float(x.float().abs().max())
+    assert float(got[0][50:64].float().abs().max()) == 0 and float(got[1][207:].float().abs().max()) == 0
+
+
 @pytest.mark.parametrize("layout", ["BHSD", "SBHD"])
 def test_backward_of_other_layouts(B, layout):
     q, k, v, o, do, lse, kw = problem(torch.bfloat16, 2, 100, 100, 4, 2, 64, 64, 9, mask=1)

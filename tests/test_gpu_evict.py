@@ -186,6 +186,7 @@ def test_weigh_padded_segments_and_loose_bounds(B):
 
 def test_weigh_negative_scale(B):
     weigh_case(B, torch.bfloat16, [90], [2], 16, 1, 2, 64, scale=-0.1)
+    weigh_case(B, torch.bfloat16, [190], [100], 16, 1, 2, 64, scale=-0.1)
 
 
 def small(B, seed=1, lens=(50, 20), page=16, hkv=2, d=64):
@@ -355,6 +356,18 @@ def test_evict_scales_and_outputs(B, in_place, spread):
 
 def test_evict_slack(B):
     evict_case(B, [70, 71, 75], [60, 60, 60], 16, 1, 64, 64, slack=10)
+
+
+@pytest.mark.parametrize("steps", [1, 3, 50])
+def test_evict_few_distinct_weights(B, steps):
+    """Ties at every digit: all of a key's rows stay, some, or the first alone."""
+    def few(weight, position, table):
+        weight.copy_((torch.randint(0, steps, weight.shape, generator=torch.Generator().manual_seed(steps)) + 1) * 2.0 ** -11 + 1)
+        position.fill_(1 << 20)
+        position[::2] = -5
+    for keep in (1, 40, 99, 149):
+        evict_case(B, [150, 60], [keep, 30], 16, 2, 64, 64, change=few)
+        evict_case(B, [150, 60], [keep, 30], 16, 2, 64, 64, sink=1, change=few)
 
 
 def test_evict_equal_weights_and_odd_ones(B):
