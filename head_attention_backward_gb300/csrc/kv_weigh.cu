@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK>::RESIDENT) weigh_kernel(con
     // keys that all of them see (keys past the last one are never written)
     const int flo = mk.left >= 0 ? (int)max(0ll, (long long)i1 + mk.off - mk.left) : 0;
     const int fhi = mk.right >= 0 ? (int)max(-1ll, min((long long)INT32_MAX, (long long)i0 + mk.off + mk.right)) : INT32_MAX;
-    bool staged = false;
+    bool staged = false, odd = false;        // odd: a row of the chunk adds nothing, not even NaN
     float2 row[2];
     uint4 qf[ONE ? FRAGS : 1];
 
@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK>::RESIDENT) weigh_kernel(con
         // rows of this chunk, a row group per warp: row g's share of lane t are the 16
         // elements at pieces t + 4 c; rows that add nothing are zero
         if (!first) __syncthreads();
+        bool without = false;
         for (int n = warp; n < groups; n += NWARPS) {
           const int rr = 8 * n + g;
           const int rl = r0 + min(rr, rows - 1);
@@ -200,6 +201,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK>::RESIDENT) weigh_kernel(con
           const T* qp = static_cast<const T*>(A.q) + elem_off(A.sq, (long long)J.q0 + i, h);
           const float l = __ldg(A.lse + (long long)h * A.total_q + J.q0 + i);
           const bool adds = rr < rows && fabsf(l) < INFINITY;
+          without |= rr < rows && !adds;
           uint4 raw[FRAGS];
           float mx = 0.f;
 #pragma unroll
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK>::RESIDENT) weigh_kernel(con
             s_tok[rr] = i;
           }
         }
-        __syncthreads();
+        odd = __syncthreads_or(without);
         staged = true;
         if (ONE) {
 #pragma unroll
@@ -249,6 +251,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK>::RESIDENT) weigh_kernel(con
         }
       }
 
+      if (odd) wholes = 0;
       for (int j0 = 0; j0 < count; j0 += DEPTH) {
 #pragma unroll
       for (int stage = 0; stage < DEPTH; ++stage) {      // tile j is in stage j % DEPTH
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK>::RESIDENT) weigh_kernel(con
               for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk)
-                  if (!sees(mk, s_tok[8 * n + 2 * t + r], key + g + 8 * kk)) p[r][kk] = 0.f;
+                  if (row[r].y == -INFINITY || !sees(mk, s_tok[8 * n + 2 * t + r], key + g + 8 * kk)) p[r][kk] = 0.f;
             }
             sum[0] += p[0][0] + p[1][0];
             sum[1] += p[0][1] + p[1][1];

@@ -733,7 +733,8 @@ typedef struct {
  * be new in one call: until then its weight and position are what its row held
  * before.  (Where only the last queries of a prompt weigh it, new_lens is the
  * prompt's length.)  With decay = 0 the old weights are not read.  Rows whose
- * LSE is not finite add nothing; a key that holds NaN has weight NaN.
+ * LSE is not finite add nothing; a key that holds NaN gets NaN from the others
+ * (after attn_kv_fwd, whose LSE is NaN for every row that sees it: nothing).
  * Sums and weights are fp32, scores are sums of exact products; the order of
  * the additions is fixed by the call's sizes, so a call repeats bit for bit.
  * A page belongs to one request of a call: where several name it, its weights

@@ -221,6 +221,27 @@ def test_weigh_rows_without_a_finite_lse_and_nan_keys(B):
     assert bool(((got.double() - want).abs() <= slack + 1e-30).all()) and torch.equal(w.position.cpu(), where)
 
 
+@pytest.mark.parametrize("lq,window", [(1, 0), (3, 0), (30, 0), (140, 0), (30, 20), (140, 60)])
+def test_weigh_nan_key_after_a_forward(B, lq, window):
+    """A NaN in a key makes the LSE of every row that sees it NaN, in its kv head: those
+    rows add nothing, to that key neither, whichever kernel the segment's length takes."""
+    g, table, pool, kc, ke, vc, ve = small(B, lens=(200, 20))
+    kc[table[0][10], 3, 0] = 127                     # key 163
+    q = torch.randn((lq + 1, 4, 64), generator=g).bfloat16()
+    c, cu, kw = handle(B, kc, vc, ke, ve), [0, lq, lq + 1], dict(scale=0.125, max_seqlen_q=lq, max_seqlen_k=208)
+    kw.update(mask=3, left=window, right=0) if window else kw.update(mask=2)
+    lse = B.attn_kv_forward(q.cuda(), c, dev(table), dev([200, 20]), dev(cu), **kw)[1]
+    weight, position = random_weights(pool, 2, 16, g)
+    w = weights_of(B, weight, position)
+    B.kv_weigh(q.cuda(), lse, c, w, dev(table), dev([200, 20]), dev(cu), **kw)
+    w.check()
+    assert bool(torch.isnan(lse[:2, :lq]).any()) and bool(torch.isfinite(lse[2:]).all())
+    kc[table[0][10], 3, 0] = 0
+    want, where, slack = evict_ref.weigh(q, lse.cpu(), cu, [200, 20], table, kc, ke, weight, position, [0, 0], 0.125,
+                                         mask=kw["mask"], left=window or -1, right=0 if window else -1)
+    assert bool(((w.weight.cpu().double() - want).abs() <= slack + 1e-30).all()) and torch.equal(w.position.cpu(), where)
+
+
 def test_weigh_decay_zero_does_not_read(B):
     g, table, pool, kc, ke, vc, ve = small(B)
     q = torch.randn((2, 4, 64), generator=g).bfloat16().cuda()
