@@ -221,6 +221,37 @@ def test_weigh_rows_without_a_finite_lse_and_nan_keys(B):
     assert bool(((got.double() - want).abs() <= slack + 1e-30).all()) and torch.equal(w.position.cpu(), where)
 
 
+@pytest.mark.parametrize("lq", [1, 30, 140])
+@pytest.mark.parametrize("layout", ["heads outside rows", "a part of wider rows"])
+def test_weigh_strided_queries_and_streams(B, lq, layout):
+    """The bits of the contiguous call, on a stream that is given or current."""
+    g, table, pool, kc, ke, vc, ve = small(B, lens=(200, 20), d=128)
+    q = torch.randn((lq + 1, 4, 128), generator=g).bfloat16().cuda()
+    lse = torch.full((4, lq + 1), 5.0, device="cuda")
+    c = handle(B, kc, vc, ke, ve)
+    if layout == "heads outside rows":
+        strided = q.transpose(0, 1).contiguous().transpose(0, 1)
+    else:
+        strided = torch.full((lq + 1, 8, 128), math.nan, device="cuda").bfloat16()[:, 2:6]
+        strided.copy_(q)
+    assert not strided.is_contiguous() or lq == 0
+    td, ld, cu = dev(table), dev([200, 20]), dev([0, lq, lq + 1])
+    weight, position = random_weights(pool, 2, 16, g)
+    kw = dict(scale=0.08, max_seqlen_q=lq, max_seqlen_k=208)
+    a, b, d = weights_of(B, weight, position), weights_of(B, weight, position), weights_of(B, weight, position)
+    B.kv_weigh(q, lse, c, a, td, ld, cu, **kw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    B.kv_weigh(strided, lse, c, b, td, ld, cu, stream=side, **kw)
+    with torch.cuda.stream(side):
+        B.kv_weigh(strided, lse, c, d, td, ld, cu, **kw)
+    side.synchronize()
+    for w in (a, b, d):
+        w.check()
+        assert torch.equal(w.weight, a.weight) and torch.equal(w.position, a.position)
+    assert not torch.equal(a.weight.cpu(), weight)
+
+
 @pytest.mark.parametrize("lq,window", [(1, 0), (3, 0), (30, 0), (140, 0), (30, 20), (140, 60)])
 def test_weigh_nan_key_after_a_forward(B, lq, window):
     """A NaN in a key makes the LSE of every row that sees it NaN, in its kv head: those
