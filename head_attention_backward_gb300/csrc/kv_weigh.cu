@@ -27,19 +27,13 @@
 namespace attn {
 namespace kvweigh {
 
-constexpr int NWARPS = 8;
-constexpr int NTHREADS = 32 * NWARPS;
 constexpr int TILE = 16;
 constexpr int CHUNK = 128;          // query rows in shared memory at a time
-constexpr int MIN_TILES = 2 * NWARPS;
 // Query rows (tokens x heads of the group) of a segment beyond which it goes to the
 // tensor cores.  8 requests of 4,000 tokens, 8 kv heads of 128: 128 rows 38 us here,
 // 47 us there; 256 rows 74 and 54.  4 requests, 4 heads of 192: 96 rows 21 and 21, 128
 // rows 25 and 19; of 256: 27 and 29, 32 and 28.
 constexpr int LONG_ROWS = 128;
-// CTAs at most, unless requests x kv heads are more (64 requests of up to 8,192 tokens:
-// 65 us with 1,536, 66 with 2,560, 71 with 4,096).
-constexpr int MAX_GRID = 1536;
 
 template <typename T> __device__ __forceinline__ float2 up2(uint32_t x);
 template <> __device__ __forceinline__ float2 up2<__nv_bfloat16>(uint32_t x) {
@@ -79,21 +73,30 @@ __device__ __forceinline__ float lds32(uint32_t a) {
   return v;
 }
 
-template <int DQK>
+// ONE: at most eight query rows, whose fragments stay in registers.
+template <int DQK, bool ONE>
 struct Cfg {
+  // More, smaller CTAs where their shared memory is the rings alone: one's beginning hides
+  // under more others (64 requests of up to 8,192 tokens, 8 heads of 128: 62 us; 65 with 8
+  // warps, three CTAs per SM and a tile more in each ring; 63 with 2 warps).
+  static constexpr int NWARPS = ONE ? 4 : 8;
+  static constexpr int MIN_TILES = 2 * NWARPS;   // of a split
+  // CTAs at most, unless requests x kv heads are more (the same call: 62 us, 64 with 2,560;
+  // with 8 warps 65 with 1,536, 66 with 2,560, 71 with 4,096).
+  static constexpr int MAX_GRID = ONE ? 3072 : 1536;
   static constexpr int PIECES = DQK / 64;    // 16-byte pieces of a K row in a lane
   static constexpr int FRAGS = DQK / 32;     // 16-byte pieces of a row group's fragments in a lane
-  static constexpr int RESIDENT = DQK <= 128 ? 3 : 2;
-  static constexpr int DEPTH = DQK == 64 ? 6 : DQK == 256 ? 3 : 4;   // tiles of a warp's ring
+  static constexpr int RESIDENT = ONE ? (DQK <= 128 ? 7 : 4) : DQK <= 128 ? 3 : 2;
+  static constexpr int DEPTH = DQK == 64 ? (ONE ? 5 : 6) : DQK == 256 ? 3 : ONE && DQK == 128 ? 3 : 4;   // tiles of a warp's ring
   static constexpr int STAGE = TILE * DQK + 128;                     // and 16 old weights
   static constexpr int RING = NWARPS * DEPTH * STAGE;
   static constexpr int GROUP = FRAGS * 32 * 16;                      // a row group's fragments
 };
 
-// ONE: at most eight query rows, whose fragments stay in registers.
 template <int DQK, typename T, bool ONE>
-__global__ void __launch_bounds__(NTHREADS, Cfg<DQK>::RESIDENT) weigh_kernel(const Args A) {
-  using C = Cfg<DQK>;
+__global__ void __launch_bounds__(32 * Cfg<DQK, ONE>::NWARPS, Cfg<DQK, ONE>::RESIDENT) weigh_kernel(const Args A) {
+  using C = Cfg<DQK, ONE>;
+  constexpr int NWARPS = C::NWARPS;
   constexpr int PIECES = C::PIECES, FRAGS = C::FRAGS, DEPTH = C::DEPTH;
   extern __shared__ uint4 s_all[];           // the warps' rings, then the fragments: [row group][FRAGS][lane]
   uint4* s_q = s_all + C::RING / 16;
@@ -111,7 +114,7 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK>::RESIDENT) weigh_kernel(con
   int kfrom, kto;
   changing(A, J, mk, kfrom, kto);
   const int k0 = kfrom & ~(TILE - 1), ntile_all = kto >= kfrom ? (kto - k0) / TILE + 1 : 0;
-  const int per = cdiv(max(MIN_TILES, cdiv(ntile_all, A.nsplit)), NWARPS) * NWARPS;
+  const int per = cdiv(max(C::MIN_TILES, cdiv(ntile_all, A.nsplit)), NWARPS) * NWARPS;
   const int tile0 = split * per, ntile = min(per, ntile_all - tile0);
   if (ntile <= 0) return;
   const int key0 = k0 + (tile0 + warp) * TILE;              // this warp's first tile, then every NWARPS-th
@@ -331,27 +334,30 @@ __global__ void __launch_bounds__(NTHREADS, Cfg<DQK>::RESIDENT) weigh_kernel(con
 }
 
 template <int DQK, typename T, bool ONE>
-static int launch_rows(const Args& a, int grid, int groups, cudaStream_t st) {
-  using C = Cfg<DQK>;
+static int launch_rows(Args a, int jobs, int groups, cudaStream_t st) {
+  using C = Cfg<DQK, ONE>;
+  const int most = cdiv(cdiv(a.max_k, TILE), C::MIN_TILES);
+  const int nsplit = C::MAX_GRID / jobs < most ? C::MAX_GRID / jobs : most;
+  a.nsplit = nsplit < 1 ? 1 : nsplit;
   // the limit is the kernel's, always the same one
   constexpr int MOST = C::RING + (ONE ? 1 : CHUNK / 8) * C::GROUP;
   if (!succeeded(cudaFuncSetAttribute(weigh_kernel<DQK, T, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST)))
     return ATTN_ERR_CUDA;
-  weigh_kernel<DQK, T, ONE><<<grid, NTHREADS, C::RING + groups * C::GROUP, st>>>(a);
+  weigh_kernel<DQK, T, ONE><<<jobs * a.nsplit, 32 * C::NWARPS, C::RING + groups * C::GROUP, st>>>(a);
   return succeeded(cudaGetLastError()) ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 template <int DQK, typename T>
-static int launch(const Args& a, int grid, int groups, cudaStream_t st) {
-  return groups <= 1 ? launch_rows<DQK, T, true>(a, grid, 1, st) : launch_rows<DQK, T, false>(a, grid, groups, st);
+static int launch(const Args& a, int jobs, int groups, cudaStream_t st) {
+  return groups <= 1 ? launch_rows<DQK, T, true>(a, jobs, 1, st) : launch_rows<DQK, T, false>(a, jobs, groups, st);
 }
 
 template <typename T>
-static int launch(const Args& a, int dqk, int grid, int groups, cudaStream_t st) {
-  if (dqk == 64) return launch<64, T>(a, grid, groups, st);
-  if (dqk == 128) return launch<128, T>(a, grid, groups, st);
-  if (dqk == 192) return launch<192, T>(a, grid, groups, st);
-  return launch<256, T>(a, grid, groups, st);
+static int launch(const Args& a, int dqk, int jobs, int groups, cudaStream_t st) {
+  if (dqk == 64) return launch<64, T>(a, jobs, groups, st);
+  if (dqk == 128) return launch<128, T>(a, jobs, groups, st);
+  if (dqk == 192) return launch<192, T>(a, jobs, groups, st);
+  return launch<256, T>(a, jobs, groups, st);
 }
 
 static int run(const attn_kv_weigh_params* p, cudaStream_t st) {
@@ -404,15 +410,11 @@ static int run(const attn_kv_weigh_params* p, cudaStream_t st) {
   // Segments of more query rows than LONG_ROWS go to the tensor cores.
   a.long_from = a.g <= long_group(p->cache.d_qk) ? LONG_ROWS / a.g : 1 << 30;
   const int jobs = p->batch * p->cache.nhead_kv;
-  const int tiles = cdiv(a.max_k, TILE);
-  int nsplit = MAX_GRID / jobs;
-  nsplit = nsplit < cdiv(tiles, MIN_TILES) ? nsplit : cdiv(tiles, MIN_TILES);
-  a.nsplit = nsplit < 1 ? 1 : nsplit;
   const long long most = (long long)(p->max_seqlen_q < p->total_q ? p->max_seqlen_q : p->total_q) * a.g;
   const int groups = cdiv(most < CHUNK ? (int)most : CHUNK, 8);
   const bool bf16 = p->dtype == ATTN_BF16;
-  const int s2 = bf16 ? launch<__nv_bfloat16>(a, p->cache.d_qk, jobs * a.nsplit, groups, st)
-                      : launch<__half>(a, p->cache.d_qk, jobs * a.nsplit, groups, st);
+  const int s2 = bf16 ? launch<__nv_bfloat16>(a, p->cache.d_qk, jobs, groups, st)
+                      : launch<__half>(a, p->cache.d_qk, jobs, groups, st);
   if (s2 != ATTN_OK || most <= (long long)a.long_from * a.g) return s2;
   return launch_long(a, bf16, p->cache.d_qk, p->batch, st);
 }
