@@ -81,9 +81,11 @@ struct Cfg {
   // warps, three CTAs per SM and a tile more in each ring; 63 with 2 warps).
   static constexpr int NWARPS = ONE ? 4 : 8;
   static constexpr int MIN_TILES = 2 * NWARPS;   // of a split
-  // CTAs at most, unless requests x kv heads are more (the same call: 62 us, 64 with 2,560;
-  // with 8 warps 65 with 1,536, 66 with 2,560, 71 with 4,096).
-  static constexpr int MAX_GRID = ONE ? 3072 : 1536;
+  // More CTAs than reside even out ragged requests, as long as a warp's share stays FULL_TILES
+  // / NWARPS tiles: MAX_GRID of them at most (the same call: 62 us, 64 with 2,128, 71 with
+  // one wave; 16 requests of up to 2,000: 9.4 with all of MIN_TILES, one wave 7.9).
+  static constexpr int FULL_TILES = ONE ? 8 * NWARPS : MIN_TILES;
+  static constexpr int MAX_GRID = ONE ? 3600 : 1536;
   static constexpr int PIECES = DQK / 64;    // 16-byte pieces of a K row in a lane
   static constexpr int FRAGS = DQK / 32;     // 16-byte pieces of a row group's fragments in a lane
   static constexpr int RESIDENT = ONE ? (DQK <= 128 ? 7 : 4) : DQK <= 128 ? 3 : 2;
@@ -336,9 +338,11 @@ __global__ void __launch_bounds__(32 * Cfg<DQK, ONE>::NWARPS, Cfg<DQK, ONE>::RES
 template <int DQK, typename T, bool ONE>
 static int launch_rows(Args a, int jobs, int groups, cudaStream_t st) {
   using C = Cfg<DQK, ONE>;
-  const int most = cdiv(cdiv(a.max_k, TILE), C::MIN_TILES);
-  const int nsplit = C::MAX_GRID / jobs < most ? C::MAX_GRID / jobs : most;
-  a.nsplit = nsplit < 1 ? 1 : nsplit;
+  const int tiles = cdiv(a.max_k, TILE), wave = C::RESIDENT * SMS / jobs, many = C::MAX_GRID / jobs;
+  const int full = cdiv(tiles, C::FULL_TILES), least = cdiv(tiles, C::MIN_TILES);
+  a.nsplit = full < many ? full : many;
+  if (a.nsplit < wave) a.nsplit = wave < least ? wave : least;
+  if (a.nsplit < 1) a.nsplit = 1;
   // the limit is the kernel's, always the same one
   constexpr int MOST = C::RING + (ONE ? 1 : CHUNK / 8) * C::GROUP;
   if (!succeeded(cudaFuncSetAttribute(weigh_kernel<DQK, T, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST)))
