@@ -235,6 +235,23 @@ def test_backward_of_padded_segments(B, det):
     assert float(got[0][50:64].float().abs().max()) == 0 and float(got[1][207:].float().abs().max()) == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_backward_of_rows_that_see_one_key(B, dtype):
+    """o is v, and so are their checkpoints: dQ and dK are 0 but for the order of two equal
+    fp32 sums of d products, each off by at most d 2^-24 of the products' magnitudes; P is
+    below 2, and a rounding of dS and of the result adds less than that again."""
+    q, k, v, o, do, lse, kw = problem(dtype, 5, 1, 1, 4, 2, 128, 128, 3)
+    c = B.checkpoint(*(x.cuda() for x in (q, k, v, o)))
+    dq, dk, dv = (x.cpu().to(F64) for x in B.attn_backward_checkpoint(c, do.cuda(), lse.cuda(), scale=128 ** -0.5))
+    wide = {n: ckpt_ref.values(getattr(c, n).cpu(), getattr(c, n + "_exp").cpu(), dtype).to(F64) for n in NAMES}
+    kk, vv = (wide[n].repeat_interleave(2, 2) for n in ("k", "v"))
+    assert torch.equal(wide["o"], vv)
+    ds = 4 * 2 * 128 * 2.0 ** -24 * (do.to(F64) * vv).abs().sum(-1, keepdim=True) * 128 ** -0.5
+    assert bool((dq.abs() <= ds * kk.abs() + 2.0 ** -24).all())
+    assert bool((dk.abs() <= (ds * wide["q"].abs()).unflatten(2, (2, 2)).sum(3) + 2.0 ** -24).all())
+    assert float(dv.abs().max()) > 0
+
+
 @pytest.mark.parametrize("layout", ["BHSD", "SBHD"])
 def test_backward_of_other_layouts(B, layout):
     q, k, v, o, do, lse, kw = problem(torch.bfloat16, 2, 100, 100, 4, 2, 64, 64, 9, mask=1)
