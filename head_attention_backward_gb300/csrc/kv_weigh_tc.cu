@@ -71,7 +71,7 @@ struct TcCfg {
   static constexpr int OFF_LIST = OFF_ODD + COL_RING * 4;    // int[LIST + 12]: key tiles before a segment of the list; of a warp's
   static constexpr int OFF_BAR = OFF_LIST + (LIST + 12) * 4;
   enum { Q_FULL = 0, Q_EMPTY = ST, S_FULL = 2 * ST, S_EMPTY = S_FULL + 2, C_FULL = S_EMPTY + 2, C_EMPTY = C_FULL + COL_RING,
-         DRAIN = C_EMPTY + COL_RING, NBAR };
+         NBAR = C_EMPTY + COL_RING };
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int BYTES = OFF_MISC + 16 + 1024;         // + alignment slack
   // two CTAs per SM at most: more would wait for TMEM
@@ -287,7 +287,6 @@ __global__ void __launch_bounds__(TC_THREADS, TcCfg<DQK>::RESIDENT) weigh_tc_ker
           mbar_init(bar + C::C_FULL + i, 32);
           mbar_init(bar + C::C_EMPTY + i, EXP_WARPS);
         }
-        mbar_init(bar + C::DRAIN, 1);
         fence_mbar_init();
       }
       if (!begun) {
@@ -381,7 +380,8 @@ __global__ void __launch_bounds__(TC_THREADS, TcCfg<DQK>::RESIDENT) weigh_tc_ker
           constexpr uint32_t ID = idesc_f16(KM, C::N, false, false, std::is_same<T, __half>::value);
           const uint64_t dk = sdesc_sw128(smem_u32(smem), 16, 1024);
           const uint64_t dq = sdesc_sw128(smem_u32(smem + C::OFF_Q), 16, 1024);
-          for (int j = 0; j < n; ++j) {
+          int j = 0;
+          for (; j < n; ++j) {
             const int s = j % C::ST, sb = j & 1;
             if (!tc_wait(ctx, C::Q_FULL + s, (j / C::ST) & 1)) break;
             if (!tc_wait(ctx, C::S_EMPTY + sb, ((j >> 1) & 1) ^ 1)) break;
@@ -395,9 +395,11 @@ __global__ void __launch_bounds__(TC_THREADS, TcCfg<DQK>::RESIDENT) weigh_tc_ker
             umma_commit(bar + C::S_FULL + sb);
             umma_commit(bar + C::Q_EMPTY + s);
           }
-          // no product may be in flight when TMEM is released
-          umma_commit(bar + C::DRAIN);
-          tc_wait(own, C::DRAIN, 0);
+          // No product may be in flight when TMEM is released, and no commit may still signal a
+          // barrier when the next item begins it anew.  Each signals its own, in no order that a
+          // later one would tell of: all that nobody has to have waited for are waited for here.
+          for (int i = max(0, j - C::ST); i < j; ++i) tc_wait(own, C::Q_EMPTY + i % C::ST, (i / C::ST) & 1);
+          for (int i = max(0, j - 2); i < j; ++i) tc_wait(own, C::S_FULL + (i & 1), (i >> 1) & 1);
         }
       } else if (warp == LSE_WARP) {
         // rows lane, lane + 32, ... of a tile; all loads of a tile are under way together,
