@@ -314,6 +314,10 @@ static void log_config(const attn_bwd_params& p, const WsLayout& L) {
 // earlier parts left).
 void launch_schedule_preprocess(const Problem& P, cudaStream_t st, bool keep_status, const CkO& ck = {});
 
+namespace kvweigh {
+int launch_selftest(int* out, cudaStream_t st);   // kv_weigh_tc.cu
+}
+
 // The validated problem the kernels of one call (or of one part of a call) run.
 static int prepare(const attn_bwd_params* p, void* ws, size_t ws_bytes, Problem* P) {
   int st = validate_bwd(p);
@@ -728,5 +732,16 @@ extern "C" const char* attn_status_string(int status) {
 
 extern "C" int attn_selftest_waits(void* scratch, size_t scratch_bytes, cudaStream_t stream, int status[3]) {
   if (!status) return ATTN_ERR_INVALID_ARG;
-  return selftest_waits(scratch, scratch_bytes, stream, status);
+  int st = selftest_waits(scratch, scratch_bytes, stream, status);
+  if (st != ATTN_OK) return st;
+  // attn_kv_weigh's wait, into two of the words behind the turn counter
+  int* words = static_cast<int*>(scratch) + 3 * HDR_WORDS + 1;
+  int weigh[2];
+  if ((st = kvweigh::launch_selftest(words, stream)) != ATTN_OK) return st;
+  if (cudaMemcpyAsync(weigh, words, sizeof(weigh), cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+      cudaStreamSynchronize(stream) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  if (weigh[0] != ATTN_ERR_TIMEOUT) status[0] = ATTN_ERR_DEVICE_FLAG;
+  if (weigh[1] != 1) status[2] = ATTN_ERR_DEVICE_FLAG;
+  return ATTN_OK;
 }

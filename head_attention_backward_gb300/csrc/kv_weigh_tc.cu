@@ -97,20 +97,22 @@ struct TcCtx {
   uint64_t* bar;
   volatile int* stop;
 };
+template <uint64_t LIMIT>
 __device__ __noinline__ bool tc_wait_slow(const TcCtx& c, uint32_t a, uint32_t parity) {
   const uint64_t t0 = globaltimer();
   while (!mbar_try_wait_sleep(a, parity, 20000)) {
     if (*c.stop) return false;
-    if (globaltimer() - t0 > WAIT_LIMIT_NS) {
+    if (globaltimer() - t0 > LIMIT) {
       *c.stop = 1;
       return false;
     }
   }
   return true;
 }
+template <uint64_t LIMIT = WAIT_LIMIT_NS>
 __device__ __forceinline__ bool tc_wait(const TcCtx& c, int i, uint32_t parity) {
   const uint32_t a = smem_u32(c.bar + i);
-  return mbar_test_wait(a, parity) || tc_wait_slow(c, a, parity);
+  return mbar_test_wait(a, parity) || tc_wait_slow<LIMIT>(c, a, parity);
 }
 __device__ __forceinline__ bool tc_wait_warp(const TcCtx& c, int i, uint32_t parity) {
   return __all_sync(0xffffffffu, tc_wait(c, i, parity));
@@ -531,6 +533,25 @@ __global__ void __launch_bounds__(TC_THREADS, TcCfg<DQK>::RESIDENT) weigh_tc_ker
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// The bounded wait on a barrier that nobody completes, and again where another warp has
+// given up before: out[0] = ATTN_ERR_TIMEOUT if the first ran out and said so, out[1] = 1
+// if the second did not wait.
+__global__ void __launch_bounds__(32) selftest_kernel(int* out) {
+  constexpr uint64_t LIMIT = 1000000ull;   // 1 ms
+  __shared__ __align__(8) uint64_t bar[1];
+  __shared__ int stop[2];
+  if (threadIdx.x != 0) return;
+  stop[0] = 0, stop[1] = 1;
+  mbar_init(bar, 1);
+  fence_mbar_init();
+  const TcCtx alone{bar, stop}, late{bar, stop + 1};
+  const bool first = tc_wait<LIMIT>(alone, 0, 0);
+  out[0] = !first && *alone.stop == 1 ? ATTN_ERR_TIMEOUT : ATTN_OK;
+  const uint64_t t0 = globaltimer();
+  const bool second = tc_wait<LIMIT>(late, 0, 0);
+  out[1] = !second && globaltimer() - t0 < LIMIT / 2;
+}
+
 // -------------------------------------------------------------------- host
 
 static PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -601,6 +622,11 @@ static int launch_tc(const Args& a, int dqk, int batch, cudaStream_t st) {
   if (dqk == 128) return launch_tc<128, T>(a, batch, st);
   if (dqk == 192) return launch_tc<192, T>(a, batch, st);
   return launch_tc<256, T>(a, batch, st);
+}
+
+int launch_selftest(int* out, cudaStream_t st) {
+  selftest_kernel<<<1, 32, 0, st>>>(out);
+  return succeeded(cudaGetLastError()) ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 int long_group(int dqk) { return dqk <= 128 ? 128 : 64; }

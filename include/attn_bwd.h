@@ -376,15 +376,18 @@ int attn_bwd_static_ws(const attn_bwd_params* p, cudaStream_t stream);
 
 /* Self-test of the bounded waits the backward kernels rely on (the pages ask
  * for loud failure instead of silent corruption: aiter PR #2216's launcher
- * returns an error, TE PR #671's check aborts).  One CTA runs, each bounded
- * at 1 ms:
- *   status[0]: an mbarrier wait whose phase never completes -> ATTN_ERR_TIMEOUT;
+ * returns an error, TE PR #671's check aborts), and of the one of attn_kv_weigh's
+ * long segments.  One thread runs at a time, each wait bounded at 1 ms:
+ *   status[0]: mbarrier waits whose phase never completes, attn_bwd's and
+ *              attn_kv_weigh's -> ATTN_ERR_TIMEOUT when both gave it;
  *   status[1]: a wait for a turn counter that nobody advances -> ATTN_ERR_TIMEOUT;
- *   status[2]: the same wait entered after another CTA recorded an error,
- *              which must give up at once -> ATTN_OK when it did.
+ *   status[2]: the same wait entered after another CTA recorded an error, and
+ *              attn_kv_weigh's after another warp gave up, which must give up at
+ *              once -> ATTN_OK when they did.
  * No GPU fault, trap or unbounded wait is involved.  `scratch` is a device
  * buffer of at least 3 * 128 * 4 + 16 bytes, 16-byte aligned, owned by the
- * caller; its contents are overwritten.  Synchronises `stream`.  Returns
+ * caller; its contents are overwritten (attn_kv_weigh's results are the int32
+ * words 385, ATTN_ERR_TIMEOUT, and 386, 1).  Synchronises `stream`.  Returns
  * ATTN_OK when the test ran (the results are in status), an error otherwise. */
 int attn_selftest_waits(void* scratch, size_t scratch_bytes, cudaStream_t stream, int status[3]);
 

@@ -116,3 +116,13 @@ def test_plain_form_is_the_oracles():
         assert torch.equal(a[1], b[1])
         assert bool(((a[0] - b[0]).abs() <= 1e-12 * (1 + b[0].abs())).all())
         assert bool(((a[2] - b[2]).abs() <= 1e-12 * (1 + b[2])).all()) and math.isfinite(float(a[2].sum()))
+
+
+@pytest.mark.gpu
+def test_long_segments_wait_is_bounded(B):
+    """The wait of the long segments' kernel on a barrier that nobody completes gives up
+    within its bound, and at once where another warp has given up before."""
+    scratch = torch.zeros(B.SELFTEST_SCRATCH_BYTES, dtype=torch.uint8, device="cuda")
+    rc, status = B.attn_selftest_waits(scratch.data_ptr(), scratch.numel(), torch.cuda.current_stream().cuda_stream)
+    assert (rc, status) == (0, [B.ATTN_ERR_TIMEOUT, B.ATTN_ERR_TIMEOUT, 0])
+    assert scratch.view(I32)[385:387].tolist() == [B.ATTN_ERR_TIMEOUT, 1]
