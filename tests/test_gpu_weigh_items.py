@@ -8,7 +8,7 @@ import torch
 
 from oracle import attn_ref, kv_ref
 from tests.kv_cases import block_table, random_cache
-from tests.test_gpu_evict import random_weights, weights_of
+from tests.test_gpu_evict import random_weights, weigh_case, weights_of
 from tests.test_gpu_kv import dev, handle
 from tests.test_gpu_parity import B  # noqa: F401  (fixture)
 
@@ -126,3 +126,12 @@ def test_long_segments_wait_is_bounded(B):
     rc, status = B.attn_selftest_waits(scratch.data_ptr(), scratch.numel(), torch.cuda.current_stream().cuda_stream)
     assert (rc, status) == (0, [B.ATTN_ERR_TIMEOUT, B.ATTN_ERR_TIMEOUT, 0])
     assert scratch.view(I32)[385:387].tolist() == [B.ATTN_ERR_TIMEOUT, 1]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,new,hkv,group,d,dv", [([150, 40], [60, 5], 1, 130, 64, 64), ([90], [33], 2, 65, 192, 128),
+                                                     ([200], [20], 1, 256, 128, 128), ([50, 20], [40, 20], 1, 80, 256, 256)])
+@pytest.mark.parametrize("dtype,decay", [(torch.bfloat16, 1.0), (torch.float16, 0.5)])
+def test_weigh_prompts_of_large_groups(B, lens, new, hkv, group, d, dv, dtype, decay):
+    """More query heads per kv head than the long segments' kernel takes: 128 rows at a time."""
+    weigh_case(B, dtype, lens, new, 16, hkv, group, d, dv, decay=decay)
