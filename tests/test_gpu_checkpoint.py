@@ -382,3 +382,21 @@ def test_offsets_past_32_bits(B):
     want, byte = ckpt_ref.quantise(tail)
     for n in ("q", "o"):
         assert torch.equal(getattr(c, n)[-5:].cpu(), want) and torch.equal(getattr(c, n + "_exp")[-5:].cpu(), byte)
+
+
+def test_backward_in_another_type(B):
+    """fp16 gradients from a checkpoint of bf16 tensors: those at the values that fp16 has,
+    past 65504 limited and below 2^-24 rounded."""
+    g = torch.Generator().manual_seed(8)
+    q, k, v, o, do = (torch.randn((2, 70, h, 64), generator=g).bfloat16() for h in (4, 2, 2, 4, 4))
+    v[0, 3, 0, 5], v[1, 60, 1, 40], k[0, 7, 1, 32:] = 1e5, -3e38, 3e-8
+    lse = 4 + torch.randn((2, 4, 70), generator=g)
+    c = B.checkpoint(*(x.cuda() for x in (q, k, v, o)))
+    at = [ckpt_ref.values(getattr(c, n).cpu(), getattr(c, n + "_exp").cpu(), torch.float16).half() for n in NAMES]
+    assert float(at[2][0, 3, 0, 5]) == 65504 and float(at[2][1, 60, 1, 40]) == -65504
+    kw = dict(scale=0.125, mask=1, deterministic=1)
+    small = (do.float() * 1e-4).half().cuda()
+    got = B.attn_backward_checkpoint(c, small, lse.cuda(), **kw)
+    same = B.attn_backward(*(x.cuda() for x in at), small, lse.cuda(), **kw)
+    for a, x in zip(got, same):
+        assert a.dtype == torch.float16 and bool(torch.isfinite(x).all()) and torch.equal(a, x)
