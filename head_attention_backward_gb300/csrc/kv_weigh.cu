@@ -313,9 +313,9 @@ __global__ void __launch_bounds__(32 * Cfg<DQK, ONE>::NWARPS, Cfg<DQK, ONE>::RES
             sum[1] += p[0][1] + p[1][1];
           }
           // over the four lanes; even lanes end with key g, odd ones with key g + 8
-          const bool odd = t & 1;
-          const float other = __shfl_xor_sync(0xffffffffu, odd ? sum[0] : sum[1], 1);
-          sum[0] = (odd ? sum[1] : sum[0]) + other;
+          const bool right = t & 1;
+          const float other = __shfl_xor_sync(0xffffffffu, right ? sum[0] : sum[1], 1);
+          sum[0] = (right ? sum[1] : sum[0]) + other;
           sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 2);
         }
         const int at_key = key + own;

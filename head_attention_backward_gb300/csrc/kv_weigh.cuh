@@ -60,12 +60,6 @@ __device__ __forceinline__ void seen_by(const MaskArgs& m, int lk, int i0, int i
   if (m.right >= 0) hi = (int)min((long long)hi, (long long)i1 + m.off + m.right);
 }
 
-// Whether all of them see all of the keys j0 .. j1.
-__device__ __forceinline__ bool whole(const MaskArgs& m, int lk, int i0, int i1, int j0, int j1) {
-  return j1 < lk && (m.left < 0 || j0 >= (long long)i1 + m.off - m.left) &&
-         (m.right < 0 || j1 <= (long long)i0 + m.off + m.right);
-}
-
 // Keys of a segment whose weights change, lo > hi: none.  Those that a query sees and the
 // new ones, or all if the old ones decay.
 __device__ __forceinline__ void changing(const Args& A, const Segment& s, const MaskArgs& m, int& lo, int& hi) {
