@@ -838,7 +838,8 @@ def attn_backward_checkpoint(ckpt: AttnCheckpoint, do, lse, *, scale, mask=MASK_
                              check_status=True, bias=None, return_dbias=False, dropout_p=0.0, philox_seed=None,
                              philox_offset=None):
     """attn_backward at a checkpoint's q, k, v and o (attn_bwd_checkpoint): dQ, dK,
-    dV (and dbias) in the type of `do`, laid out like the checkpoint unless `out`
+    dV (and dbias) in the type of `do`, which should be that of the tensors that went
+    in (a checkpoint does not hold it), laid out like the checkpoint unless `out`
     is given.  lse is the forward's; the other arguments are attn_backward's."""
     if stream is not None:
         with _on_stream(stream):

@@ -195,7 +195,8 @@ template <> __device__ __forceinline__ uint32_t pack2t<__half>(float a, float b)
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Every value is exact in T: no rounding happens here.
+// Every value is exact in T if the checkpoint's tensors were of that type.  In fp16 those
+// of a wider type's are limited to 65504 and rounded below 2^-14.
 template <typename T>
 __global__ void __launch_bounds__(THREADS) expand_kernel(const __grid_constant__ ExpandArgs A) {
   int i = 0;

@@ -461,7 +461,10 @@ int attn_bwd_checkpoint_workspace_size(const attn_bwd_params* p, const attn_chec
 /* attn_bwd at the checkpoint's q, k, v and o: *p with its q, k, v and o null and
  * their strides zero, everything else as in attn_bwd (dtype is that of dout and
  * of the gradients, lse the forward's, which saw the tensors before they were
- * rounded; head dims multiples of 32).  Batch order and heads of *c follow the
+ * rounded; head dims multiples of 32).  A checkpoint does not hold the type of its
+ * tensors: dtype should be that type.  With ATTN_FP16 and a checkpoint of wider
+ * tensors, values past 65504 are limited to it, and those of q, k and v below
+ * 2^-14 are rounded to multiples of 2^-24.  Batch order and heads of *c follow the
  * layout rules of attn_bwd_params, together with dout's and the gradients'.
  * q, k and v are expanded into the workspace, o is read as it is.  The status
  * is read with attn_bwd_read_status, as attn_bwd's. */
@@ -599,7 +602,9 @@ typedef struct {
   int32_t* position_offsets; /* device, [batch], or NULL: tokens that a request has
                                 forgotten (attn_kv_evict).  positions[t] is then
                                 x + position_offsets[b]; entries of requests that
-                                end become 0                                     */
+                                end become 0.  Read of every caller's struct: code
+                                compiled against a header without this member has
+                                to be compiled again                             */
 } attn_kv_plan_params;
 
 /* Enqueue the bookkeeping on `stream`. */
@@ -735,11 +740,15 @@ typedef struct {
  * ATTN_MASK_WINDOW and none with the other masks.  Every appended token has to
  * be new in one call: until then its weight and position are what its row held
  * before.  (Where only the last queries of a prompt weigh it, new_lens is the
- * prompt's length.)  With decay = 0 the old weights are not read.  Rows whose
- * LSE is not finite add nothing; a key that holds NaN gets NaN from the others
- * (after attn_kv_fwd, whose LSE is NaN for every row that sees it: nothing).
+ * prompt's length.)  With decay = 0 it does not matter what the old weights are,
+ * NaN among them.  Rows whose LSE is not finite add nothing; a key that holds NaN
+ * gets NaN from the others (after attn_kv_fwd, whose LSE is NaN for every row that
+ * sees it: nothing).
  * Sums and weights are fp32, scores are sums of exact products; the order of
  * the additions is fixed by the call's sizes, so a call repeats bit for bit.
+ * Segments of more than 128 / G query tokens (G = nhead_q / nhead_kv) run on the
+ * tensor cores where G <= 128 (d_qk above 128: 64); of larger groups, 128 query
+ * rows at a time pass over the request's keys.
  * A page belongs to one request of a call: where several name it, its weights
  * are unspecified.  A segment without query tokens is left alone, so is one
  * outside its bounds (as in attn_kv_fwd; seqlens_k outside 0 ..
@@ -819,7 +828,8 @@ typedef struct {
 } attn_kv_evict_params;
 
 /* Workspace bytes attn_kv_evict needs for *p: host arithmetic on the scalar
- * fields alone, about 4 bytes per batch entry, kv head and token of max_seqlen_k. */
+ * fields alone, about 4 bytes per batch entry, kv head and token of max_seqlen_k
+ * (8 where max_seqlen_k is above 327,680). */
 int attn_kv_evict_workspace_size(const attn_kv_evict_params* p, size_t* bytes);
 
 /* Enqueue it on `stream` (two kernels).  `workspace`: device, 256-byte aligned,
