@@ -135,3 +135,40 @@ def test_long_segments_wait_is_bounded(B):
 def test_weigh_prompts_of_large_groups(B, lens, new, hkv, group, d, dv, dtype, decay):
     """More query heads per kv head than the long segments' kernel takes: 128 rows at a time."""
     weigh_case(B, dtype, lens, new, 16, hkv, group, d, dv, decay=decay)
+
+
+@pytest.mark.gpu
+def test_weigh_beside_other_calls(B):
+    """Long segments of two requests at a time on two streams, a forward pass on a third:
+    all of them hold TMEM; the weights are those of the calls alone."""
+    g = torch.Generator().manual_seed(9)
+    page, hkv, group, d, lens, new = 16, 4, 4, 128, [1500, 700], [300, 200]
+    table, pool = block_table(lens, page, g)
+    kc, ke = random_cache(pool, page, hkv, d, g)
+    c = handle(B, kc, kc.clone(), ke, ke.clone())
+    q = torch.randn((sum(new), hkv * group, d), generator=g).bfloat16().cuda()
+    lse = (5 + torch.randn((hkv * group, sum(new)), generator=g)).cuda()
+    weight, position = random_weights(pool, hkv, page, g)
+    td, ld, cu = dev(table), dev(lens), dev([0, 300, 500])
+    x, k = (torch.randn((2, 1024, h, d), generator=g).bfloat16().cuda() for h in (16, 4))
+    weigh = lambda w: B.kv_weigh(q, lse, c, w, td, ld, cu, scale=0.08, max_seqlen_q=300, max_seqlen_k=1500)   # noqa: E731
+    forward = lambda: B.attn_forward(x, k, k, scale=0.08, mask=1)   # noqa: E731
+    one = weights_of(B, weight, position)
+    weigh(one)
+    o, l = forward()
+    both = [[weights_of(B, weight, position) for _ in range(8)] for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(8):
+        for s, ws in zip(streams, both):
+            with torch.cuda.stream(s):
+                weigh(ws[i])
+        with torch.cuda.stream(streams[2]):
+            outs.append(forward())
+    torch.cuda.synchronize()
+    for w in both[0] + both[1]:
+        w.check()
+        assert torch.equal(w.weight, one.weight) and torch.equal(w.position, one.position)
+    for a, b in outs:
+        assert torch.equal(a, o) and torch.equal(b, l)
