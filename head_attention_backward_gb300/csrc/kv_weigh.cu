@@ -31,7 +31,7 @@ constexpr int TILE = 16;
 constexpr int CHUNK = 128;          // query rows in shared memory at a time
 // Query rows (tokens x heads of the group) of a segment beyond which it goes to the
 // tensor cores.  8 requests of 4,000 tokens, 8 kv heads of 128: 128 rows 38 us here,
-// 47 us there; 256 rows 74 and 54.  4 requests, 4 heads of 192: 96 rows 21 and 21, 128
+// 47 us there; 256 rows 74 and 55.  4 requests, 4 heads of 192: 96 rows 21 and 21, 128
 // rows 25 and 19; of 256: 27 and 29, 32 and 28.
 constexpr int LONG_ROWS = 128;
 

@@ -11,12 +11,13 @@
 // sum never leaves the thread, and there is neither a maximum nor a second product.
 // Per 128 x 128 tile of depth 128 the products take 512 clocks of the tensor cores and
 // the exponentials as long (32 a clock and SM); S^T is double-buffered in TMEM, and two
-// CTAs share an SM, so that one's waits run under the other's tiles.  Two forms that
-// were slower (4 x 1,024 tokens over 5,120, this one 154 us, 890 TFLOP/s): 256 keys per
-// item, kept in TMEM, one CTA per SM (198), which halves the query tiles' way through L2
-// and shared memory, but that bounds nothing; and 304 persistent CTAs that fetch the next
-// item's keys while they work (186): the registers for it cost the inner loop more than
-// an item's beginning (TMEM 2.4 us, keys 1.4) costs beside another CTA's tiles.
+// CTAs share an SM, so that one's waits run under the other's tiles: an SM takes 1,075
+// clocks a tile while both are at theirs, 1,577 while one is.  Two forms that were slower
+// (4 x 1,024 tokens over 5,120, this one 154 us, 890 TFLOP/s): 256 keys per item, kept in
+// TMEM, one CTA per SM (198), which halves the query tiles' way through L2 and shared
+// memory, but that bounds nothing; and 304 persistent CTAs that fetch the next item's keys
+// while they work (186): the registers for it cost the inner loop more than an item's
+// beginning (TMEM 2.4 us, keys 1.4) costs beside another CTA's tiles.
 //
 // The items are those of the long segments alone.  Where the bounds leave room for many,
 // each CTA lists them for itself, so that a loose max_seqlen_k, or many short segments,
@@ -53,7 +54,7 @@ constexpr int LIST = 256;               // segments whose items are listed at a 
 constexpr int MAX_PLACES = 4096;
 // CTAs for a list at most.  Those beyond the 304 that reside begin as others end, which
 // evens out ragged items, and pay for TMEM again, 2.4 us (8 requests of 4,000 tokens, 64
-// new: 54 us with 608, 60 with 2,048).
+// new: 55 us with 608, 60 with 2,048).
 constexpr int MAX_TC_GRID = 608;
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;
 

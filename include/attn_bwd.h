@@ -461,7 +461,9 @@ int attn_bwd_checkpoint_workspace_size(const attn_bwd_params* p, const attn_chec
 /* attn_bwd at the checkpoint's q, k, v and o: *p with its q, k, v and o null and
  * their strides zero, everything else as in attn_bwd (dtype is that of dout and
  * of the gradients, lse the forward's, which saw the tensors before they were
- * rounded; head dims multiples of 32).  A checkpoint does not hold the type of its
+ * rounded; head dims multiples of 32).  Gradients move with the rounding: for
+ * normal q, k and v by 1 to 2 % of their norms, for twice as large scores by 2.5 to
+ * 3 %.  A checkpoint does not hold the type of its
  * tensors: dtype should be that type.  With ATTN_FP16 and a checkpoint of wider
  * tensors, values past 65504 are limited to it, and those of q, k and v below
  * 2^-14 are rounded to multiples of 2^-24.  Batch order and heads of *c follow the
